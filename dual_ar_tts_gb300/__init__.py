@@ -22,7 +22,10 @@ EXPORTS = ("s2_weight_count", "s2_weight_info", "s2_frame_workspace_bytes", "s2_
            "s2_decode_frames", "s2_fast_logits", "s2_sync_status", "s2_set_spin_limit", "s2_set_trace",
            "s2_phase_count", "s2_frame_free", "s2_last_error", "s2_fast_logits_static", "s2_stream_import",
            "s2_stop_stream", "s2_stream_progress", "s2_codec_latent", "s2_quantize_e4m3", "s2_set_barrier_base",
-           "s2_draw")
+           "s2_draw", "s2_quantize_q4", "s2_q4_matmul", "s2_kv4_page_bytes", "s2_kv4_append", "s2_kv4_read",
+           "s2_kv4_attention_workspace", "s2_kv4_attention", "s2_adjust_logits")
+
+S2_KV4_PAGE = 64
 
 
 class s2_dims(ctypes.Structure):
@@ -43,6 +46,13 @@ class s2_sampling(ctypes.Structure):
 class s2_debug_taps(ctypes.Structure):
     _fields_ = [("main_logits", ctypes.c_void_p), ("fast_logits", ctypes.c_void_p), ("hidden", ctypes.c_void_p),
                 ("draws", ctypes.c_void_p)]
+
+
+class s2_kv4(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("n_kv_head", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("table", ctypes.c_void_p), ("table_cols", ctypes.c_int),
+                ("n_seq", ctypes.c_int), ("q_start", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int), ("status", ctypes.c_void_p)]
 
 
 class S2Error(RuntimeError):
@@ -86,6 +96,14 @@ def load(path: str = LIB_PATH):
         "s2_quantize_e4m3": (i32, [vp, ctypes.c_longlong, i32, vp, vp, vp]),
         "s2_stream_progress": (i32, [vp, i32, P(i32), vp, vp]),
         "s2_draw": (i32, [i32, vp, i32, i32, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp]),
+        "s2_quantize_q4": (i32, [vp, i32, i64, i32, i32, vp, vp, vp]),
+        "s2_q4_matmul": (i32, [i32, vp, i32, i64, vp, vp, i32, i32, i32, vp, vp]),
+        "s2_kv4_page_bytes": (i64, [i32, i32]),
+        "s2_kv4_append": (i32, [P(s2_kv4), vp, i32, i64, i32, vp, i32, vp, vp, ctypes.c_float, vp, vp]),
+        "s2_kv4_read": (i32, [P(s2_kv4), vp, vp, vp]),
+        "s2_kv4_attention_workspace": (sz, [i32, i32, i32, i32, i32, i32]),
+        "s2_kv4_attention": (i32, [P(s2_kv4), vp, i32, i32, ctypes.c_float, i32, vp, vp, sz, vp]),
+        "s2_adjust_logits": (i32, [i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, vp, i64, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -206,6 +224,253 @@ def quantize_e4m3(w):
     s2_quantize_e4m3(w.data_ptr(), w.shape[0], w.shape[1], codes.data_ptr(), scales.data_ptr(),
                      torch.cuda.current_stream().cuda_stream)
     return codes, scales
+
+
+# ------------------------------------- 4-bit weights, 4-bit cache, adjusted logits
+
+def _dtype_code(t, what):
+    import torch
+    code = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be fp32, bf16 or fp16")
+    return code
+
+
+def _need(ok, msg):
+    if not ok:
+        raise ValueError(msg)
+
+
+def _on(dev, *tensors):
+    """All given tensors are on the CUDA device `dev`."""
+    _need(dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
+          "tensors must be on one CUDA device")
+
+
+def _launch(name, dev, *args):
+    """Call an entry point on dev's current stream, with dev the current device while it launches."""
+    import torch
+    fn = getattr(_lib or load(), name)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != S2_OK:
+        raise S2Error(name, rc, "see include/s2frame.h for what the call takes")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def quantize_q4(w, group: int = 32):
+    """Device matrix [rows][cols] (fp32, bf16 or fp16) -> (uint8 codes [rows][ceil(cols/128)*64], bf16 scales
+    [rows][ceil(cols/128)*(128/group)]): 4-bit codes with a scale per `group` (32, 64 or 128) columns; layout in
+    s2frame.h."""
+    import torch
+    dt = _dtype_code(w, "w")
+    _need(w.dim() == 2 and w.is_cuda and w.numel() > 0, "quantize_q4 takes a 2-D CUDA tensor")
+    _need(group in (32, 64, 128) and w.shape[1] % group == 0, "columns must be a multiple of group: 32, 64 or 128")
+    w = w.contiguous()
+    rows, cols = w.shape
+    blocks = -(-cols // 128)
+    codes = torch.empty((rows, blocks * 64), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((rows, blocks * (128 // group)), dtype=torch.bfloat16, device=w.device)
+    _launch("s2_quantize_q4", w.device, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def q4_matmul(x, codes, scales, group: int = 32, out=None):
+    """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type."""
+    import torch
+    dt = _dtype_code(x, "x")
+    dev = x.device
+    _need(x.dim() == 2 and codes.dim() == 2 and scales.dim() == 2 and x.numel() > 0, "q4_matmul takes 2-D tensors")
+    _on(dev, x, codes, scales, out)
+    n, k = x.shape
+    m, blocks = codes.shape[0], -(-k // 128)
+    _need(group in (32, 64, 128) and k % group == 0, "columns must be a multiple of group: 32, 64 or 128")
+    _need(codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape[1] == blocks * 64,
+          "codes must be contiguous uint8 [rows][ceil(k/128)*64]")
+    _need(scales.dtype == torch.bfloat16 and scales.is_contiguous() and
+          tuple(scales.shape) == (m, blocks * (128 // group)),
+          "scales must be contiguous bf16 [rows][ceil(k/128)*(128/group)]")
+    if x.stride(1) != 1 or x.stride(0) < k or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16:
+        x = x.contiguous()
+        if x.data_ptr() % 16:
+            x = x.clone()
+    if out is None:
+        out = torch.empty((n, m), dtype=x.dtype, device=dev)
+    else:
+        _need(out.dtype == x.dtype and tuple(out.shape) == (n, m) and out.is_contiguous(),
+              "out must be contiguous [n][rows] of x's type")
+    _launch("s2_q4_matmul", dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k, group,
+            out.data_ptr())
+    return out
+
+
+def rope_table(n_pos: int, head_dim: int, base: float = 1e6, bf16: bool = True, device="cuda"):
+    """fp32 [n_pos][head_dim/2][2] of (cos, sin) of position * base^(-2i/head_dim), angles in fp64, the values
+    rounded to bf16 precision as the decode's own table (bf16=False: to fp32)."""
+    import torch
+    theta = base ** (-2.0 * torch.arange(head_dim // 2, dtype=torch.float64, device=device) / head_dim)
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * theta
+    t = torch.stack([a.cos(), a.sin()], -1).float()
+    return (t.bfloat16().float() if bf16 else t).contiguous()
+
+
+def kv4_pages(n_pages: int, n_kv_head: int, head_dim: int, device="cuda"):
+    """The pages of one layer's 4-bit cache: uint8 [n_pages][n_kv_head][80*head_dim], zeroed."""
+    import torch
+    nbytes = load().s2_kv4_page_bytes(n_kv_head, head_dim)
+    _need(nbytes > 0 and n_pages > 0, "kv4_pages takes head_dim 64 or 128 and positive counts")
+    return torch.zeros((n_pages, n_kv_head, nbytes // n_kv_head), dtype=torch.uint8, device=device)
+
+
+def _kv4(pages, table, q_start, lengths, n_rows, status):
+    import torch
+    _need(pages.dtype == torch.uint8 and pages.dim() == 3 and pages.is_contiguous() and
+          pages.shape[2] in (80 * 64, 80 * 128), "pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim]")
+    i32 = torch.int32
+    _need(table.dtype == i32 and table.dim() == 2 and table.is_contiguous(), "table must be contiguous int32 [n_seq][cols]")
+    n_seq = table.shape[0]
+    _need(q_start.dtype == i32 and q_start.shape == (n_seq + 1,) and q_start.is_contiguous(), "q_start must be int32 [n_seq+1]")
+    _need(lengths.dtype == i32 and lengths.shape == (n_seq,) and lengths.is_contiguous(), "lengths must be int32 [n_seq]")
+    _need(status is None or (status.dtype == i32 and status.numel() == 1), "status must be one int32")
+    _on(pages.device, table, q_start, lengths, status)
+    return s2_kv4(pages.data_ptr(), pages.shape[0], pages.shape[1], pages.shape[2] // 80, table.data_ptr(),
+                  table.shape[1], n_seq, q_start.data_ptr(), lengths.data_ptr(), n_rows, _ptr(status))
+
+
+def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=None, k_norm=None, eps: float = 1e-6,
+               q_out=None, status=None):
+    """Append rows to a paged 4-bit cache (kv4_pages): qkv [n_rows][(n_head + 2 n_kv_head)*head_dim] (fp32, bf16 or
+    fp16; q | k | v, head-major).  Queries and keys are normed per head where q_norm / k_norm (fp32 [head_dim]) are
+    given and rotated by rope's (rope_table) row of their position; keys and values are quantised.  table int32
+    [n_seq][cols], q_start int32 [n_seq + 1] and lengths int32 [n_seq] place the rows (see s2_kv4 in s2frame.h).
+    Returns the rotated queries [n_rows][n_head][head_dim]; rows behind the last sequence are left as they were."""
+    import torch
+    dt = _dtype_code(qkv, "qkv")
+    _need(qkv.dim() == 2 and qkv.shape[0] > 0, "qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
+    n_rows = qkv.shape[0]
+    c = _kv4(pages, table, q_start, lengths, n_rows, status)
+    hd = c.head_dim
+    _on(pages.device, qkv, rope, q_norm, k_norm, q_out)
+    _need(qkv.shape[1] == (n_head + 2 * c.n_kv_head) * hd and n_head >= 0,
+          "qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
+    _need(rope.dtype == torch.float32 and rope.dim() == 3 and tuple(rope.shape[1:]) == (hd // 2, 2) and
+          rope.is_contiguous(), "rope must be contiguous fp32 [n_pos][head_dim/2][2]")
+    for w in (q_norm, k_norm):
+        _need(w is None or (w.dtype == torch.float32 and w.shape == (hd,) and w.is_contiguous()),
+              "norm weights must be fp32 [head_dim]")
+    if qkv.stride(1) != 1 or qkv.stride(0) < qkv.shape[1] or qkv.stride(0) * qkv.element_size() % 16 or \
+            qkv.data_ptr() % 16:
+        qkv = qkv.contiguous()
+        if qkv.data_ptr() % 16:
+            qkv = qkv.clone()
+    if q_out is None:
+        q_out = torch.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
+    else:
+        _need(q_out.dtype == qkv.dtype and tuple(q_out.shape) == (n_rows, n_head, hd) and q_out.is_contiguous(),
+              "q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type")
+    _launch("s2_kv4_append", qkv.device, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
+            rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr() or None)
+    return q_out
+
+
+def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None, status=None):
+    """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]."""
+    import torch
+    _need(n_rows > 0, "n_rows must be positive")
+    c = _kv4(pages, table, q_start, lengths, n_rows, status)
+    shape = (c.n_kv_head, n_rows, c.head_dim)
+    out = []
+    for t in (k_out, v_out):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.float16, device=pages.device)
+        _need(t.dtype == torch.float16 and tuple(t.shape) == shape and t.is_contiguous(),
+              "outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim]")
+        out.append(t)
+    _on(pages.device, *out)
+    _launch("s2_kv4_read", pages.device, ctypes.byref(c), out[0].data_ptr(), out[1].data_ptr())
+    return out[0], out[1]
+
+
+def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None, max_len: int = 0, workspace=None,
+                  out=None, status=None):
+    """Causal attention of q [n_rows][n_head][head_dim] (fp32, bf16 or fp16) over a paged 4-bit cache that holds
+    the rows' own keys and values already (kv4_append).  scale defaults to 1/sqrt(head_dim); max_len (the largest
+    length expected, 0: what the table can hold) only sets how the work is split; workspace, a uint8 tensor of
+    s2_kv4_attention_workspace bytes, is allocated where none is given."""
+    import torch
+    dt = _dtype_code(q, "q")
+    _need(q.dim() == 3 and q.numel() > 0, "q must be [n_rows][n_head][head_dim]")
+    n_rows, n_head, hd = q.shape
+    c = _kv4(pages, table, q_start, lengths, n_rows, status)
+    _need(hd == c.head_dim and n_head % c.n_kv_head == 0 and max_len >= 0,
+          "q's heads must be a multiple of the cache's, of the same head_dim")
+    _on(pages.device, q, out, workspace)
+    q = q.contiguous()
+    if q.data_ptr() % 16:
+        q = q.clone()
+    if out is None:
+        out = torch.empty((n_rows, n_head, hd), dtype=q.dtype, device=q.device)
+    else:
+        _need(out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous(),
+              "out must be contiguous, of q's shape and type")
+    max_len = max_len or table.shape[1] * S2_KV4_PAGE
+    if workspace is None:
+        nbytes = (_lib or load()).s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, c.n_kv_head, hd, max_len)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _launch("s2_kv4_attention", q.device, ctypes.byref(c), q.data_ptr(), dt, n_head,
+            hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None, mask=None, sem_begin: int = -1,
+                  im_end: int = 0, out=None):
+    """Logits [rows][n] (fp32, bf16 or fp16) adjusted for a draw -> fp32 [rows][n] (see s2_adjust_logits).
+    history int32 [rows][cols] with hist_len int32 [rows] and penalties fp32 [rows][3] of (repetition, frequency,
+    presence); bias fp32 [rows or 1][n]; mask int32 or uint32 bits [rows or 1][ceil(n/32)].  Entry ids as in draw."""
+    import torch
+    dt = _dtype_code(logits, "logits")
+    dev = logits.device
+    _need(logits.dim() == 2 and logits.numel() > 0, "logits must be [rows][n]")
+    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
+    rows, n = logits.shape
+    cols = 0
+    _need((history is None) == (penalties is None), "history and penalties go together")
+    _need(hist_len is None or (history is not None and hist_len.dtype == torch.int32 and
+                               hist_len.shape == (rows,) and hist_len.is_contiguous()), "hist_len must be int32 [rows]")
+    if history is not None:
+        _need(history.dtype == torch.int32 and history.dim() == 2 and history.shape[0] == rows and
+              history.is_contiguous(), "history must be contiguous int32 [rows][cols]")
+        _need(penalties.dtype == torch.float32 and tuple(penalties.shape) == (rows, 3) and penalties.is_contiguous(),
+              "penalties must be contiguous fp32 [rows][3]")
+        cols = history.shape[1]
+        if cols == 0:
+            history = penalties = hist_len = None
+    strides = []
+    for t, width, kinds, what in ((bias, n, (torch.float32,), "bias must be fp32 [rows or 1][n]"),
+                                  (mask, -(-n // 32), (torch.int32, torch.uint32),
+                                   "mask must be 32-bit [rows or 1][ceil(n/32)]")):
+        if t is not None:
+            _need(t.dtype in kinds and t.dim() == 2 and t.shape[0] in (1, rows) and t.shape[1] == width and
+                  t.is_contiguous(), what)
+        strides.append(0 if t is None or t.shape[0] == 1 else width)
+    logits = logits.contiguous()
+    if out is None:
+        out = torch.empty((rows, n), dtype=torch.float32, device=dev)
+    else:
+        _need(out.dtype == torch.float32 and tuple(out.shape) == (rows, n) and out.is_contiguous(),
+              "out must be contiguous fp32 [rows][n]")
+    _launch("s2_adjust_logits", dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt, _ptr(history), _ptr(hist_len),
+            cols, _ptr(penalties), _ptr(bias), strides[0], _ptr(mask), strides[1], out.data_ptr())
+    return out
 
 
 def s2_decode_frames(ctx, stream_ids, n_frames: int, params, expo_ptr: int, forced_ptr: int | None, codes_ptr: int,

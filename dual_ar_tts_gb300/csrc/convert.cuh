@@ -1,0 +1,34 @@
+// Element types of the stateless operators: a value of S2_F32 / S2_BF16 / S2_F16 as fp32 and back.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/s2frame.h"
+
+namespace s2 {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+inline int dtype_bytes(int dtype) { return dtype == S2_F32 ? 4 : dtype == S2_BF16 || dtype == S2_F16 ? 2 : 0; }
+
+// f(T{}) with T the C++ type of `dtype` (checked by the caller with dtype_bytes)
+template <typename F>
+inline auto with_dtype(int dtype, F f) {
+  if (dtype == S2_F32) return f(float{});
+  if (dtype == S2_BF16) return f(__nv_bfloat16{});
+  return f(__half{});
+}
+
+}  // namespace s2

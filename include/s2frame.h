@@ -325,6 +325,131 @@ int s2_quantize_e4m3(const void* w, long long rows, int cols, uint8_t* codes, fl
 int s2_draw(int rows, const float* logits, int n, int sem_begin, int im_end, int block_end, float temperature,
             float top_p, const float* expo, int32_t* out, struct CUstream_st* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * 4-bit weights, a 4-bit paged key/value cache and adjusted logits: stateless calls on caller
+ * buffers, for a decode step whose projections and cache are held in 4 bits.  (The precedent on
+ * the pages is s2.cpp's K-quantised GGUF tensors, s2.cpp analysis ch.02 §5 and ch.04 §4; the
+ * formats are this library's choice.)  One such step is: s2_q4_matmul (wqkv), s2_kv4_append,
+ * s2_kv4_attention, s2_q4_matmul (wo, then the feed-forward and the logits), s2_adjust_logits,
+ * s2_draw.  All of them allocate nothing, keep nothing between calls, are asynchronous on
+ * `stream`, may be captured into a CUDA graph, and give the same bits for the same inputs.
+ * dtype is S2_F32, S2_BF16 or S2_F16; sums are held in fp32 whatever the type, and a result is
+ * rounded to it once.  Outputs may not overlap inputs unless a call says so.
+ * Errors (nothing launched): S2_EINVAL bad count, size, type, pointer or alignment; S2_ECUDA
+ * launch failed. */
+
+/* 4-bit codes of weight rows, with one scale per group of 32, 64 or 128 columns:
+ *   scales[r][g] = bf16(w_m / -8), w_m the group's entry of the largest magnitude (first of equals)
+ *   code[r][k]   = clamp(rint(w[r][k] / scale) + 8, 0, 15)     (fp32 division, ties to even)
+ * standing for scale * (code - 8).  A group of zeros gets scale 0 and codes 8; a group with an
+ * entry that is not finite gets scale NaN and codes 8, so that products with it are NaN.
+ * Layout: a row is ceil(cols / 128) blocks of 128 columns; a block is 64 bytes, and its 32-bit word
+ * 4c + j holds columns 32j + 8c .. 32j + 8c + 7, lowest nibble first.  Columns past `cols` in the
+ * last block have code 8 and scale 0.
+ *   w       device [rows][cols] of dtype; cols a multiple of group
+ *   codes   device uint8 [rows][ceil(cols / 128) * 64], 16-byte aligned
+ *   scales  device bf16 [rows][ceil(cols / 128) * (128 / group)], 2-byte aligned */
+int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group, uint8_t* codes, void* scales,
+                   struct CUstream_st* stream);
+
+/* y[i][r] = Σ_k x[i][k] · scale[r][k / group] · (code[r][k] - 8) for n activation rows and m weight
+ * rows quantised as above.  Activations keep their precision: fp32 rows enter the products in full.
+ *   x       device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times the
+ *           element size a multiple of 16
+ *   codes, scales  as s2_quantize_q4 writes them, both 16-byte aligned; k a multiple of group
+ *   y       device [n][m] of dtype, aligned to its element size */
+int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride, const uint8_t* codes, const void* scales,
+                 int m, int k, int group, void* y, struct CUstream_st* stream);
+
+/* The paged 4-bit cache of one layer, and the rows of a call.
+ *   pages   device [n_pages][n_kv_head][block], 16-byte aligned.  A page holds S2_KV4_PAGE positions;
+ *           a block (80 * head_dim bytes) is one head of it: key codes [64][head_dim / 2] bytes (low
+ *           nibble = even element), key parameters [64][head_dim / 32] of {fp16 scale, fp16 zero},
+ *           then the same of the values.  An element stands for fp16(scale * (code - zero)).
+ *   table   device int32 [n_seq][table_cols]: the pages of each sequence in order of position
+ *   q_start device int32 [n_seq + 1], ascending from q_start[0] = 0: sequence s has the call's rows
+ *           q_start[s] .. q_start[s + 1] - 1 (none, where equal)
+ *   lengths device int32 [n_seq]: positions of each sequence in the cache, the call's rows included:
+ *           they are its last ones, so row i of sequence s is position
+ *           lengths[s] - (q_start[s + 1] - i)
+ *   n_rows  rows of the call's buffers; those from q_start[n_seq] on are left as they were
+ *   status  device int32 or NULL: S2_EINVAL is written there when a position or a page is out of
+ *           range (each call says what it does then)
+ * These arrays are read on the device, so a captured call follows their values.  A page may belong
+ * to several sequences as long as no call appends to it. */
+#define S2_KV4_PAGE 64
+typedef struct s2_kv4 {
+  void* pages;
+  int n_pages, n_kv_head, head_dim; /* head_dim 64 or 128 */
+  const int32_t* table;
+  int table_cols, n_seq;
+  const int32_t* q_start;
+  const int32_t* lengths;
+  int n_rows;
+  int32_t* status;
+} s2_kv4;
+
+/* Bytes of one page (n_kv_head * 80 * head_dim), or -1 for a shape that is not supported. */
+long long s2_kv4_page_bytes(int n_kv_head, int head_dim);
+
+/* Append the rows' keys and values, and rotate their queries.  Per row and head of [q | k | v]:
+ *   q, k:  x <- x * (1 / sqrt(mean(x^2) + eps)) * norm weight      (where that weight is given)
+ *          pairs (2i, 2i + 1) <- (x0 cos - x1 sin, x1 cos + x0 sin), the table's row of the position
+ *   k, v:  quantised in groups of 32, lo and hi the group's least and largest element:
+ *          scale = fp16(max((hi - lo) / 15, max|x| / 127)), zero = clamp(rint(-lo / scale), -127, 127),
+ *          code = clamp(rint(x / scale) + zero, 0, 15); elements beyond ±57344 count as that, a
+ *          group with a NaN gets scale NaN, and where the scale rounds to 0 so are zero and codes
+ * all in fp32, each operation rounded by itself.
+ *   qkv     device [n_rows][n_head + 2 n_kv_head][head_dim] of dtype, rows qkv_stride elements apart
+ *           (16-byte aligned, as is the stride)
+ *   n_head  query heads (0: keys and values alone; q_out may then be NULL)
+ *   rope    device fp32 [n_pos][head_dim / 2][2] of (cos, sin), 16-byte aligned
+ *   q_norm, k_norm  device fp32 [head_dim], 16-byte aligned, or NULL
+ *   q_out   device [n_rows][n_head][head_dim] of dtype, 16-byte aligned
+ * A row whose position is not in 0..n_pos - 1, or whose page is out of range, is left out whole.
+ * No two rows of a call may fall on the same slot of the same page (its contents would be neither's). */
+int s2_kv4_append(const s2_kv4* cache, const void* qkv, int dtype, long long qkv_stride, int n_head,
+                  const float* rope, int n_pos, const float* q_norm, const float* k_norm, float eps, void* q_out,
+                  struct CUstream_st* stream);
+
+/* The keys and values that the rows' positions stand for, fp16 [n_kv_head][n_rows][head_dim] each,
+ * 16-byte aligned (with one sequence and as many rows as positions: a layer of what
+ * s2_stream_import takes).  A row whose position or page is out of range is written as zeros. */
+int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* stream);
+
+/* Causal attention of the rows' queries over their sequences: query head h reads KV head
+ * h / (n_head / n_kv_head) at positions 0 .. its own, scores scaled by `scale`.  A row that sees no
+ * position (lengths[s] short of the sequence's rows) gets zeros; what a page holds past a
+ * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
+ * are not attended.
+ *   q, out    device [n_rows][n_head][head_dim] of dtype, 16-byte aligned
+ *   max_len   the largest length expected, by which the work is split (0: table_cols pages); a
+ *             longer sequence is still right
+ *   workspace device, 16-byte aligned, of at least s2_kv4_attention_workspace bytes for the same
+ *             sizes (NULL where that is 0).  Calls that may run at the same time need one each. */
+size_t s2_kv4_attention_workspace(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len);
+int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, int n_head, float scale, int max_len, void* out,
+                     void* workspace, size_t ws_bytes, struct CUstream_st* stream);
+
+/* Logits adjusted for a draw (s2_draw takes the result).  For entry e of row r, c the number of
+ * times its token is in the row's history:
+ *   l = logits[r][e];  if c > 0: l = (l > 0 ? l / rep : l * rep) - freq * c - pres
+ *   l = l + bias[r][e];  -inf where the mask's bit is 0;  out[r][e] = l (fp32)
+ * Ids of entries are those of s2_draw: the entry index (sem_begin < 0), or sem_begin + e for
+ * e < n - 1 and im_end for e = n - 1.  Ids in the history that no entry has do not count.
+ *   logits    device [rows][n] of dtype, aligned to its element size; rows 1..65535
+ *   history   device int32 [rows][hist_cols] with hist_len device int32 [rows] (NULL: hist_cols
+ *             each; clamped to 0..hist_cols), or NULL
+ *   penalties device fp32 [rows][3] of (rep, freq, pres); given with a history and only then
+ *   bias      device fp32, rows bias_stride elements apart (0: one row for all), or NULL
+ *   mask      device uint32, bit e % 32 of word e / 32, rows mask_stride words apart (0: one for
+ *             all), or NULL
+ *   out       device fp32 [rows][n]; may be logits itself where that is fp32 */
+int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* logits, int dtype,
+                     const int32_t* history, const int32_t* hist_len, int hist_cols, const float* penalties,
+                     const float* bias, long long bias_stride, const uint32_t* mask, long long mask_stride,
+                     float* out, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

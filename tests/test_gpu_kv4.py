@@ -1,0 +1,364 @@
+"""The paged 4-bit cache (s2_kv4_append, s2_kv4_read, s2_kv4_attention) against its definition.
+
+Appended codes and parameters are compared with a plain form that rounds every fp32 operation by
+itself (as the kernel does); with the norm, the plain form's mean square comes from 64 bits and the
+kernel's from pairs of fp32, both rounded to fp32 once, so that bits can differ only where a sum lies
+on a rounding border of the last place: a few elements in a million may then take the neighbouring
+code.  Rotated queries: six fp32 roundings and the type's own.  Attention: tests/four_bit.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import four_bit as fb
+
+pytestmark = pytest.mark.gpu
+
+
+def _layout(spans, rng, extra=3, cols=0):
+    """table, q_start, lengths, pages in the pool for spans of (new rows, length)."""
+    need = [-(-length // fb.PAGE) for _, length in spans]
+    pool = sum(need) + extra
+    order = rng.permutation(pool).astype(np.int32)
+    table = np.full((len(spans), max(need + [1, cols])), -7, np.int32)     # entries past a length are never read
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    q_start = np.cumsum([0] + [n for n, _ in spans]).astype(np.int32)
+    lengths = np.asarray([length for _, length in spans], np.int32)
+    return table, q_start, lengths, pool
+
+
+def _gpu(*arrays):
+    return [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in arrays]
+
+
+SPANS = {
+    "one": [(1, 1)],
+    "page_end": [(1, 64), (1, 65), (2, 128)],
+    "ragged": [(3, 17), (0, 9), (70, 70), (1, 200), (0, 0), (5, 133)],
+    "decode": [(1, n) for n in (1, 63, 64, 65, 700, 2, 33, 129)],
+    "prompt": [(150, 150), (64, 640)],
+}
+HEADS = [(4, 2, 64), (32, 8, 128), (3, 3, 64), (16, 1, 128), (6, 2, 128)]
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("hq,hkv,hd", HEADS)
+@pytest.mark.parametrize("spans", ["one", "page_end", "ragged", "prompt"])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append_and_read(spans, hq, hkv, hd, dtype, norm):
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(hq * hd + len(spans))
+    table, q_start, lengths, pool = _layout(SPANS[spans], rng)
+    rows = int(q_start[-1])
+    dt = fb.TYPES[dtype]
+    heads = hq + 2 * hkv
+    x = rng.standard_normal((rows, heads, hd)) * np.exp(rng.standard_normal((heads, hd)))
+    x[..., 3] += 5.0                                                    # a biased channel
+    qkv = torch.from_numpy(x.astype(np.float32)).to(dt)
+    qkv[0, hq, :32] = 0                                                 # a group of zeros
+    qkv[0, hq + hkv, :32] = 0.75                                        # a constant group
+    n_pos = int(lengths.max()) + 2
+    rope = pkg.rope_table(n_pos, hd)
+    qw, kw = [torch.from_numpy((1 + 0.1 * rng.standard_normal(hd)).astype(np.float32)) if norm else None for _ in "qk"]
+    pages = torch.full((pool, hkv, 80 * hd), 0xA5, dtype=torch.uint8)
+    want = pages.clone()
+    gp = pages.cuda()
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = torch.full((rows + 2, hq, hd), 9.0, dtype=dt, device="cuda")
+    more = torch.cat([qkv.flatten(1), torch.full((2, heads * hd), math.nan, dtype=dt)]).cuda()  # rows behind the last
+    got = pkg.kv4_append(more, gp, gt, gs, gl, rope, hq, q_norm=None if qw is None else qw.cuda(),
+                         k_norm=None if kw is None else kw.cuda(), eps=1e-6, q_out=q_out, status=status)
+    seq = np.repeat(np.arange(len(lengths)), np.diff(q_start))
+    pos = lengths[seq] - (q_start[seq + 1] - np.arange(rows))
+    cs = rope.cpu()[torch.from_numpy(pos).long()][:, None]
+    f = qkv.float()
+    q64 = f[:, :hq].double()
+    if norm:
+        q64 = q64 * (q64.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * qw.double()
+    a, b, c, s = q64[..., 0::2], q64[..., 1::2], cs[..., 0].double(), cs[..., 1].double()
+    q64, mag = [torch.stack(t, -1).flatten(-2) for t in
+                ((a * c - b * s, b * c + a * s), ((a * c).abs() + (b * s).abs(), (b * c).abs() + (a * s).abs()))]
+    err = (got[:rows].cpu().double() - q64).abs()
+    assert (err <= 10 * 2.0 ** -24 * mag + fb.rounding(q64, dt)).all()
+    assert (got[rows:] == 9).all() and int(status) == 0
+    k = fb.norm_rotate(f[:, hq:hq + hkv], kw, 1e-6, cs)
+    for i in range(rows):
+        fb.put(want, int(table[seq[i], pos[i] // 64]), int(pos[i] % 64), k[i], f[i, hq + hkv:])
+    if norm:
+        off = (gp.cpu() != want).float().mean().item()
+        assert off <= max(1e-5, 2.0 / want.numel()), off
+    else:
+        assert torch.equal(gp.cpu(), want)                              # every other byte as it was
+    rk, rv = pkg.kv4_read(gp, gt, gs, gl, rows + 2, k_out=torch.full((hkv, rows + 2, hd), 9, dtype=torch.float16, device="cuda"))
+    kept = gp.cpu()
+    for part, r in enumerate((rk, rv)):
+        for i in range(rows):
+            full = fb.get(kept, part, [int(table[seq[i], pos[i] // 64])])[:, pos[i] % 64]
+            assert torch.equal(r[:, i].cpu(), full)
+    assert (rk[:, rows:] == 9).all()
+    # half a step of the group's scale from what went in (one step where the range was clipped by the zero point)
+    vs = fb.kv_quantise(f[:, hq + hkv:])[1].float().repeat_interleave(32, -1)
+    assert ((rv[:, :rows].transpose(0, 1).cpu().float() - f[:, hq + hkv:]).abs() <= vs * 1.02 + 1e-6).all()
+
+
+def test_append_non_finite_and_large_values():
+    import dual_ar_tts_gb300 as pkg
+    hkv, hd = 2, 128
+    qkv = torch.randn((1, 2 * hkv, hd), generator=torch.Generator().manual_seed(0))
+    qkv[0, 0, 5] = math.nan
+    qkv[0, 1, 40] = math.inf
+    qkv[0, 2, 70] = -3e38
+    qkv[0, 3, :32] = 1e-9                                               # the scale rounds to zero
+    qkv[0, 3, 32:64] = torch.linspace(100.0, 100.5, 32)                 # narrow and far from zero
+    rope = torch.zeros((1, hd // 2, 2))
+    rope[..., 0] = 1
+    pages = pkg.kv4_pages(1, hkv, hd)
+    one = _gpu(np.zeros((1, 1), np.int32), np.asarray([0, 1], np.int32), np.asarray([1], np.int32))
+    pkg.kv4_append(qkv.flatten(1).cuda(), pages, *one, rope.cuda(), 0)
+    k, v = [t[:, 0].cpu() for t in pkg.kv4_read(pages, *one, 1)]
+    assert torch.isnan(k[0, :32]).all() and torch.isfinite(k[0, 32:]).all()
+    # a key is rotated before it is quantised: inf * sin(0) is NaN in the pair, so the group's scale is
+    assert torch.isnan(k[1, 32:64]).all() and torch.isfinite(k[1, :32]).all() and torch.isfinite(k[1, 64:]).all()
+    assert torch.isfinite(v).all() and v[0, 70] < -5e4 and (v[1, :32] == 0).all()
+    assert ((v[1, 32:64].float() - qkv[0, 3, 32:64]).abs() <= 100.5 / 127 * 1.01).all()
+
+
+def test_append_leaves_out_bad_rows():
+    """A page out of range, a position below zero, behind the rotation table or behind the page table."""
+    import dual_ar_tts_gb300 as pkg
+    hq, hkv, hd = 4, 2, 64
+    spans = [(2, 70), (1, 1), (3, 2), (1, 65), (1, 130)]
+    table = np.asarray([[0, 9], [1, -1], [2, -1], [3, -1], [4, 5]], np.int32)   # 9 and -1 do not exist
+    q_start = np.cumsum([0] + [n for n, _ in spans]).astype(np.int32)
+    lengths = np.asarray([n for _, n in spans], np.int32)
+    rows = int(q_start[-1])
+    qkv = torch.randn((rows, (hq + 2 * hkv) * hd), generator=torch.Generator().manual_seed(1)).cuda()
+    pages = pkg.kv4_pages(6, hkv, hd)
+    before = pages.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = torch.full((rows, hq, hd), 9.0, device="cuda")
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    pkg.kv4_append(qkv, pages, gt, gs, gl, pkg.rope_table(100, hd), hq, q_out=q_out, status=status)
+    assert int(status) == pkg.S2_EINVAL
+    skipped = torch.tensor([True, True, False, True, False, False, True, True])
+    assert torch.equal((q_out.cpu() == 9).flatten(1).all(1), skipped)
+    changed = (pages != before).flatten(1).any(1).cpu()
+    assert changed.tolist() == [False, True, True, False, False, False]
+    status.zero_()
+    k, v = pkg.kv4_read(pages, gt, gs, gl, rows, status=status)
+    assert int(status) == pkg.S2_EINVAL
+    for i in range(rows):
+        bad = i in (0, 1, 3, 6)
+        assert bool((k[:, i] == 0).all()) == (bad or i == 7)            # row 7: its (empty) page can be read
+
+
+def _attend(pkg, q, pages, table, q_start, lengths, **kw):
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    return pkg.kv4_attention(q.cuda(), pages.cuda(), gt, gs, gl, **kw)
+
+
+def _check_attention(got, q, pages, table, q_start, lengths, scale, dt, live=None):
+    hq, hkv = q.shape[1], pages.shape[1]
+    worst = 0.0
+    for s in range(len(lengths)):
+        a, b = int(q_start[s]), int(q_start[s + 1])
+        if a == b:
+            continue
+        n = b - a
+        L = int(lengths[s])
+        ids = [int(p) for p in table[s, :-(-L // 64)]] if L > 0 else []
+        seen = [max(0, L - n + i + 1) for i in range(n)]
+        for h in range(hq):
+            kv = [(fb.get(pages[:, h // (hq // hkv)][:, None], part, ids)[0, :L] if ids else torch.zeros((0, q.shape[2])))
+                  for part in range(2)]
+            o, rel, wv, tiny = fb.attention(q[a:b, h], kv[0], kv[1], seen, scale) if L > 0 else \
+                (torch.zeros((n, q.shape[2])), 0, torch.zeros((n, q.shape[2])), 0)
+            tol = fb.attention_tol(o, rel, wv, tiny, dt) if L > 0 else torch.zeros_like(o)
+            err = (got[a:b, h].cpu().double() - o).abs()
+            assert (err <= tol).all(), (s, h, float((err - tol).max()))
+            worst = max(worst, float((err / tol.clamp(min=1e-30)).max()))
+    return worst
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("hq,hkv,hd", HEADS + [(40, 2, 64), (7, 1, 128)])
+@pytest.mark.parametrize("spans", ["one", "page_end", "ragged", "decode", "prompt"])
+def test_attention(spans, hq, hkv, hd, dtype):
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(hq + hd + len(spans))
+    table, q_start, lengths, pool = _layout(SPANS[spans], rng, cols=6)
+    rows = int(q_start[-1])
+    dt = fb.TYPES[dtype]
+    pages = torch.zeros((pool, hkv, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((rows + 1, hq, hd)).astype(np.float32) * 1.5).to(dt)
+    out = torch.full((rows + 1, hq, hd), 9.0, dtype=dt, device="cuda")
+    got = _attend(pkg, q, pages, table, q_start, lengths, out=out)
+    assert (got[rows:] == 9).all()
+    _check_attention(got, q, pages, table, q_start, lengths, hd ** -0.5, dt)
+    again = _attend(pkg, q, pages, table, q_start, lengths, max_len=int(lengths.max()))
+    _check_attention(again, q, pages, table, q_start, lengths, hd ** -0.5, dt)
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_attention_long_and_split(dtype):
+    """Lengths that are split over blocks; the hint below, at and above the length; the same bits again."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(11)
+    spans = [(1, 5003), (2, 3000), (1, 1), (1, 64)]
+    table, q_start, lengths, pool = _layout(spans, rng, cols=200)
+    dt = fb.TYPES[dtype]
+    pages = torch.zeros((pool, 2, 80 * 128), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((5, 8, 128)).astype(np.float32) * 3).to(dt)
+    for hint in (0, 64, 2000, 5003, 12800):
+        got = _attend(pkg, q, pages, table, q_start, lengths, max_len=hint)
+        _check_attention(got, q, pages, table, q_start, lengths, 128 ** -0.5, dt)
+        assert torch.equal(got, _attend(pkg, q, pages, table, q_start, lengths, max_len=hint))
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_attention_ignores_what_is_masked(dtype):
+    """Slots past a length and in the future of a row hold NaN and infinities; a row that sees nothing gets zeros."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(3)
+    spans = [(4, 70), (5, 3), (2, 128), (3, 0), (2, 1)]
+    table, q_start, lengths, pool = _layout(spans, rng)
+    dt = fb.TYPES[dtype]
+    hq, hkv, hd = 8, 2, 128
+    pages = torch.zeros((pool, hkv, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    for s, (_, L) in enumerate(spans):
+        if L % 64:
+            for part in range(2):
+                codes, par = fb._parts(pages, part)
+                par[int(table[s, L // 64]), :, L % 64:] = torch.tensor([math.nan, math.inf]).half()
+                codes[int(table[s, L // 64]), :, L % 64:] = 255
+    q = torch.from_numpy(rng.standard_normal((16, hq, hd)).astype(np.float32)).to(dt)
+    got = _attend(pkg, q, pages, table, q_start, lengths)
+    assert torch.isfinite(got).all()
+    assert (got[4:6] == 0).all() and (got[11:14] == 0).all() and (got[14] == 0).all()
+    _check_attention(got, q, pages, table, q_start, lengths, hd ** -0.5, dt)
+    # a key in a row's future: NaN there, rows before it are as they were
+    codes, par = fb._parts(pages, 0)
+    par[int(table[2, 1]), :, 63] = math.nan
+    later = _attend(pkg, q, pages, table, q_start, lengths)
+    assert torch.equal(later[9], got[9]) and torch.isnan(later[10]).all()
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_attention_magnitudes(dtype):
+    """Scores far apart (one position takes all; 10 nats below it thousands share the rest), queries of 1e-6 and
+    1e4, tiny value scales."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(5)
+    dt = fb.TYPES[dtype]
+    spans = [(1, 4000), (1, 4000), (1, 333), (3, 3)]
+    table, q_start, lengths, pool = _layout(spans, rng)
+    pages = torch.zeros((pool, 1, 80 * 64), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    codes, par = fb._parts(pages, 1)
+    par[..., 0] *= 1e-3
+    par[..., 1] = 7
+    q = torch.from_numpy(rng.standard_normal((6, 4, 64)).astype(np.float32))
+    q[0] *= 8
+    q[1] *= 1e-6 if dtype != "fp16" else 1e-4
+    q[2] *= 1e4 if dtype != "fp16" else 50
+    # one key that matches q[0] head 0, about 10 nats over the others' mass
+    k = fb.get(pages, 0, [int(table[0, 0])])
+    q = q.to(dt)
+    got = _attend(pkg, q, pages, table, q_start, lengths)
+    assert k.shape[1] == 64
+    _check_attention(got, q, pages, table, q_start, lengths, 0.125, dt)
+
+
+def test_attention_bad_pages_are_not_attended():
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(9)
+    table, q_start, lengths, pool = _layout([(1, 200), (2, 64), (1, 300)], rng)
+    pages = torch.zeros((pool, 2, 80 * 64), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((4, 4, 64)).astype(np.float32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _attend(pkg, q, pages, table, q_start, lengths, status=status)
+    assert int(status) == 0
+    bad = table.copy()
+    bad[0, 1], bad[1, 0], bad[2, 0] = pool, -1, 2 ** 31 - 1
+    got = _attend(pkg, q, pages, bad, q_start, lengths, status=status)
+    assert int(status) == pkg.S2_EINVAL
+    assert (got[1:3] == 0).all()
+    # sequence 0 without its second page: the same as its other pages alone, where no causal limit cuts in
+    cut = np.asarray([[table[0, 0], table[0, 2], table[0, 3]]], np.int32)
+    want = _attend(pkg, q[:1], pages, cut, np.asarray([0, 1], np.int32), np.asarray([136], np.int32))
+    assert (got[0] - want[0]).abs().max() <= 1e-5 * want[0].abs().max()
+    # a length past the page table
+    status.zero_()
+    got = _attend(pkg, q[:1], pages, table[:1, :2], np.asarray([0, 1], np.int32), np.asarray([1000], np.int32), status=status)
+    assert int(status) == pkg.S2_EINVAL
+    want = _attend(pkg, q[:1], pages, table[:1, :2], np.asarray([0, 1], np.int32), np.asarray([128], np.int32))
+    assert (got - want).abs().max() <= 1e-5 * want.abs().max()
+
+
+def test_shared_pages_and_a_pool_past_32_bits():
+    """Two sequences read the same prefix pages; the pool is larger than 4 GiB and its last pages are in use."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(21)
+    n_pages = (1 << 32) // (80 * 128) + 50
+    small = torch.zeros((5, 1, 80 * 128), dtype=torch.uint8)
+    fb.fill_random(small, rng)
+    pages = torch.empty((n_pages, 1, 80 * 128), dtype=torch.uint8, device="cuda")
+    first = n_pages - 5
+    pages[first:] = small.cuda()
+    local = np.asarray([[0, 1, 2], [0, 1, 3], [4, -1, -1]], np.int32)
+    table = np.where(local >= 0, local + first, -1).astype(np.int32)
+    q_start, lengths = np.asarray([0, 1, 3, 4], np.int32), np.asarray([170, 190, 20], np.int32)
+    q = torch.from_numpy(rng.standard_normal((4, 4, 128)).astype(np.float32)).bfloat16()
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    got = pkg.kv4_attention(q.cuda(), pages, gt, gs, gl)
+    _check_attention(got, q, small, local, q_start, lengths, 128 ** -0.5, torch.bfloat16)
+    qkv = torch.randn((4, 3 * 128), device="cuda")
+    own = _gpu(np.asarray([[first + 4]], np.int32), np.asarray([0, 4], np.int32), np.asarray([64], np.int32))
+    pkg.kv4_append(qkv, pages, *own, pkg.rope_table(64, 128), 1)
+    k, v = pkg.kv4_read(pages, *own, 4)
+    assert torch.equal(v.cpu(), fb.get(pages[first:].cpu(), 1, [4])[:, 60:])
+    del pages
+    torch.cuda.empty_cache()
+
+
+def test_attention_captured_and_replayed_with_other_lengths():
+    """One graph; lengths, tables and queries change between replays.  A second graph has its own workspace, and
+    the two run on two streams at the same time."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(2)
+    table, q_start, lengths, pool = _layout([(1, 3000), (1, 1500)], rng)
+    pages = torch.zeros((pool, 2, 80 * 128), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    gp = pages.cuda()
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    q = torch.randn((2, 8, 128), device="cuda").half()
+    nbytes = pkg.load().s2_kv4_attention_workspace(2, 2, 8, 2, 128, 3000)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    torch.cuda.synchronize()
+    for s in side:
+        ws = torch.empty(max(16, nbytes), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            pkg.kv4_attention(q, gp, gt, gs, gl, max_len=3000, workspace=ws, out=out)
+        graphs.append((g, ws, out))
+    for new in ((3000, 1500), (1, 1472), (2900, 64)):
+        gl.copy_(torch.tensor(new, dtype=torch.int32))
+        q.copy_(torch.randn((2, 8, 128)).half())
+        torch.cuda.synchronize()
+        for (g, _, _), s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[0][2], graphs[1][2])
+        _check_attention(graphs[0][2], q.cpu(), pages, table, q_start, np.asarray(new), 128 ** -0.5, torch.float16)
