@@ -423,8 +423,8 @@ int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* strea
  * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
  * are not attended.
  *   q, out    device [n_rows][n_head][head_dim] of dtype, 16-byte aligned
- *   max_len   the largest length expected, by which the work is split (0: table_cols pages); a
- *             longer sequence is still right
+ *   max_len   the largest length expected, by which the work is split (0, or more than table_cols
+ *             pages hold: those); a longer sequence is still right
  *   workspace device, 16-byte aligned, of at least s2_kv4_attention_workspace bytes for the same
  *             sizes (NULL where that is 0).  Calls that may run at the same time need one each. */
 size_t s2_kv4_attention_workspace(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len);
