@@ -228,11 +228,20 @@ def quantize_e4m3(w):
 
 # ------------------------------------- 4-bit weights, 4-bit cache, adjusted logits
 
-def _dtype_code(t, what):
-    import torch
-    code = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}.get(t.dtype)
+# A call of a few microseconds is soon outweighed by what Python does around it, so the checks below
+# read each property of a tensor once and compare plain values.
+
+_kinds = None    # torch element type -> S2_* code
+
+
+def _code(t):
+    global _kinds
+    if _kinds is None:
+        import torch
+        _kinds = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}
+    code = _kinds.get(t.dtype)
     if code is None:
-        raise ValueError(f"{what} must be fp32, bf16 or fp16")
+        raise ValueError("the element type must be fp32, bf16 or fp16")
     return code
 
 
@@ -242,17 +251,20 @@ def _need(ok, msg):
 
 
 def _on(dev, *tensors):
-    """All given tensors are on the CUDA device `dev`."""
-    _need(dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
-          "tensors must be on one CUDA device")
+    """All given tensors are on CUDA device number `dev`."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError("tensors must be on one CUDA device")
 
 
 def _launch(name, dev, *args):
-    """Call an entry point on dev's current stream, with dev the current device while it launches."""
+    """Call an entry point on the current stream of device number `dev`, with that device current meanwhile."""
     import torch
     fn = getattr(_lib or load(), name)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -265,12 +277,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _rows16(x):
+    """x [n][k], as rows that start on 16 bytes (a copy where they do not)."""
+    s0, s1 = x.stride()
+    if s1 == 1 and s0 >= x.shape[1] and s0 * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
+        return x
+    pad = -x.shape[1] % 8
+    if pad:
+        import torch
+        y = torch.empty((x.shape[0], x.shape[1] + pad), dtype=x.dtype, device=x.device)[:, :x.shape[1]]
+        return y.copy_(x)
+    x = x.contiguous()
+    return x.clone() if x.data_ptr() % 16 else x
+
+
 def quantize_q4(w, group: int = 32):
     """Device matrix [rows][cols] (fp32, bf16 or fp16) -> (uint8 codes [rows][ceil(cols/128)*64], bf16 scales
     [rows][ceil(cols/128)*(128/group)]): 4-bit codes with a scale per `group` (32, 64 or 128) columns; layout in
     s2frame.h."""
     import torch
-    dt = _dtype_code(w, "w")
+    dt = _code(w)
     _need(w.dim() == 2 and w.is_cuda and w.numel() > 0, "quantize_q4 takes a 2-D CUDA tensor")
     _need(group in (32, 64, 128) and w.shape[1] % group == 0, "columns must be a multiple of group: 32, 64 or 128")
     w = w.contiguous()
@@ -278,33 +304,28 @@ def quantize_q4(w, group: int = 32):
     blocks = -(-cols // 128)
     codes = torch.empty((rows, blocks * 64), dtype=torch.uint8, device=w.device)
     scales = torch.empty((rows, blocks * (128 // group)), dtype=torch.bfloat16, device=w.device)
-    _launch("s2_quantize_q4", w.device, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
+    _launch("s2_quantize_q4", w.get_device(), w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def q4_matmul(x, codes, scales, group: int = 32, out=None):
     """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type."""
     import torch
-    dt = _dtype_code(x, "x")
-    dev = x.device
-    _need(x.dim() == 2 and codes.dim() == 2 and scales.dim() == 2 and x.numel() > 0, "q4_matmul takes 2-D tensors")
-    _on(dev, x, codes, scales, out)
+    dt, dev = _code(x), x.get_device()
+    _need(x.dim() == 2 and codes.dim() == 2 and scales.dim() == 2, "q4_matmul takes 2-D tensors")
     n, k = x.shape
-    m, blocks = codes.shape[0], -(-k // 128)
+    m, width = codes.shape
+    _on(dev, codes, scales, out)
     _need(group in (32, 64, 128) and k % group == 0, "columns must be a multiple of group: 32, 64 or 128")
-    _need(codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape[1] == blocks * 64,
+    _need(codes.dtype is torch.uint8 and codes.is_contiguous() and width == -(-k // 128) * 64,
           "codes must be contiguous uint8 [rows][ceil(k/128)*64]")
-    _need(scales.dtype == torch.bfloat16 and scales.is_contiguous() and
-          tuple(scales.shape) == (m, blocks * (128 // group)),
-          "scales must be contiguous bf16 [rows][ceil(k/128)*(128/group)]")
-    if x.stride(1) != 1 or x.stride(0) < k or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16:
-        x = x.contiguous()
-        if x.data_ptr() % 16:
-            x = x.clone()
+    _need(scales.dtype is torch.bfloat16 and scales.is_contiguous() and
+          scales.shape == (m, width * 2 // group), "scales must be contiguous bf16 [rows][ceil(k/128)*(128/group)]")
+    x = _rows16(x)
     if out is None:
-        out = torch.empty((n, m), dtype=x.dtype, device=dev)
+        out = torch.empty((n, m), dtype=x.dtype, device=x.device)
     else:
-        _need(out.dtype == x.dtype and tuple(out.shape) == (n, m) and out.is_contiguous(),
+        _need(out.dtype is x.dtype and out.shape == (n, m) and out.is_contiguous(),
               "out must be contiguous [n][rows] of x's type")
     _launch("s2_q4_matmul", dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k, group,
             out.data_ptr())
@@ -329,19 +350,21 @@ def kv4_pages(n_pages: int, n_kv_head: int, head_dim: int, device="cuda"):
     return torch.zeros((n_pages, n_kv_head, nbytes // n_kv_head), dtype=torch.uint8, device=device)
 
 
-def _kv4(pages, table, q_start, lengths, n_rows, status):
+def _kv4(dev, pages, table, q_start, lengths, n_rows, status):
     import torch
-    _need(pages.dtype == torch.uint8 and pages.dim() == 3 and pages.is_contiguous() and
-          pages.shape[2] in (80 * 64, 80 * 128), "pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim]")
     i32 = torch.int32
-    _need(table.dtype == i32 and table.dim() == 2 and table.is_contiguous(), "table must be contiguous int32 [n_seq][cols]")
-    n_seq = table.shape[0]
-    _need(q_start.dtype == i32 and q_start.shape == (n_seq + 1,) and q_start.is_contiguous(), "q_start must be int32 [n_seq+1]")
-    _need(lengths.dtype == i32 and lengths.shape == (n_seq,) and lengths.is_contiguous(), "lengths must be int32 [n_seq]")
-    _need(status is None or (status.dtype == i32 and status.numel() == 1), "status must be one int32")
-    _on(pages.device, table, q_start, lengths, status)
-    return s2_kv4(pages.data_ptr(), pages.shape[0], pages.shape[1], pages.shape[2] // 80, table.data_ptr(),
-                  table.shape[1], n_seq, q_start.data_ptr(), lengths.data_ptr(), n_rows, _ptr(status))
+    n_pages, n_kv_head, block = pages.shape
+    n_seq, cols = table.shape
+    _on(dev, pages, table, q_start, lengths, status)
+    _need(pages.dtype is torch.uint8 and pages.is_contiguous() and block in (80 * 64, 80 * 128),
+          "pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim]")
+    _need(table.dtype is i32 and table.is_contiguous(), "table must be contiguous int32 [n_seq][cols]")
+    _need(q_start.dtype is i32 and q_start.shape == (n_seq + 1,) and q_start.is_contiguous(),
+          "q_start must be int32 [n_seq+1]")
+    _need(lengths.dtype is i32 and lengths.shape == (n_seq,) and lengths.is_contiguous(), "lengths must be int32 [n_seq]")
+    _need(status is None or (status.dtype is i32 and status.numel() == 1), "status must be one int32")
+    return s2_kv4(pages.data_ptr(), n_pages, n_kv_head, block // 80, table.data_ptr(), cols, n_seq, q_start.data_ptr(),
+                  lengths.data_ptr(), n_rows, _ptr(status))
 
 
 def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=None, k_norm=None, eps: float = 1e-6,
@@ -352,50 +375,50 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
     [n_seq][cols], q_start int32 [n_seq + 1] and lengths int32 [n_seq] place the rows (see s2_kv4 in s2frame.h).
     Returns the rotated queries [n_rows][n_head][head_dim]; rows behind the last sequence are left as they were."""
     import torch
-    dt = _dtype_code(qkv, "qkv")
-    _need(qkv.dim() == 2 and qkv.shape[0] > 0, "qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
-    n_rows = qkv.shape[0]
-    c = _kv4(pages, table, q_start, lengths, n_rows, status)
+    dt, dev = _code(qkv), qkv.get_device()
+    _need(qkv.dim() == 2 and pages.dim() == 3 and table.dim() == 2,
+          "qkv and table must be 2-D, pages 3-D")
+    n_rows, width = qkv.shape
+    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
     hd = c.head_dim
-    _on(pages.device, qkv, rope, q_norm, k_norm, q_out)
-    _need(qkv.shape[1] == (n_head + 2 * c.n_kv_head) * hd and n_head >= 0,
+    _on(dev, rope, q_norm, k_norm, q_out)
+    _need(n_head >= 0 and width == (n_head + 2 * c.n_kv_head) * hd,
           "qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
-    _need(rope.dtype == torch.float32 and rope.dim() == 3 and tuple(rope.shape[1:]) == (hd // 2, 2) and
-          rope.is_contiguous(), "rope must be contiguous fp32 [n_pos][head_dim/2][2]")
+    f32 = torch.float32
+    _need(rope.dtype is f32 and rope.dim() == 3 and rope.shape[1:] == (hd // 2, 2) and rope.is_contiguous(),
+          "rope must be contiguous fp32 [n_pos][head_dim/2][2]")
     for w in (q_norm, k_norm):
-        _need(w is None or (w.dtype == torch.float32 and w.shape == (hd,) and w.is_contiguous()),
+        _need(w is None or (w.dtype is f32 and w.shape == (hd,) and w.is_contiguous()),
               "norm weights must be fp32 [head_dim]")
-    if qkv.stride(1) != 1 or qkv.stride(0) < qkv.shape[1] or qkv.stride(0) * qkv.element_size() % 16 or \
-            qkv.data_ptr() % 16:
-        qkv = qkv.contiguous()
-        if qkv.data_ptr() % 16:
-            qkv = qkv.clone()
+    qkv = _rows16(qkv)
     if q_out is None:
         q_out = torch.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
     else:
-        _need(q_out.dtype == qkv.dtype and tuple(q_out.shape) == (n_rows, n_head, hd) and q_out.is_contiguous(),
+        _need(q_out.dtype is qkv.dtype and q_out.shape == (n_rows, n_head, hd) and q_out.is_contiguous(),
               "q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type")
-    _launch("s2_kv4_append", qkv.device, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
-            rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr() or None)
+    _launch("s2_kv4_append", dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
+            rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr())
     return q_out
 
 
 def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None, status=None):
     """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]."""
     import torch
-    _need(n_rows > 0, "n_rows must be positive")
-    c = _kv4(pages, table, q_start, lengths, n_rows, status)
+    _need(pages.dim() == 3 and table.dim() == 2, "pages must be 3-D and table 2-D")
+    dev = pages.get_device()
+    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
     shape = (c.n_kv_head, n_rows, c.head_dim)
-    out = []
+    f16 = torch.float16
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=f16, device=pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=f16, device=pages.device)
     for t in (k_out, v_out):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.float16, device=pages.device)
-        _need(t.dtype == torch.float16 and tuple(t.shape) == shape and t.is_contiguous(),
+        _need(t.dtype is f16 and t.shape == shape and t.is_contiguous(),
               "outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim]")
-        out.append(t)
-    _on(pages.device, *out)
-    _launch("s2_kv4_read", pages.device, ctypes.byref(c), out[0].data_ptr(), out[1].data_ptr())
-    return out[0], out[1]
+    _on(dev, k_out, v_out)
+    _launch("s2_kv4_read", dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
+    return k_out, v_out
 
 
 def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None, max_len: int = 0, workspace=None,
@@ -405,27 +428,28 @@ def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None,
     length expected, 0: what the table can hold) only sets how the work is split; workspace, a uint8 tensor of
     s2_kv4_attention_workspace bytes, is allocated where none is given."""
     import torch
-    dt = _dtype_code(q, "q")
-    _need(q.dim() == 3 and q.numel() > 0, "q must be [n_rows][n_head][head_dim]")
+    dt, dev = _code(q), q.get_device()
+    _need(q.dim() == 3 and pages.dim() == 3 and table.dim() == 2, "q and pages must be 3-D and table 2-D")
     n_rows, n_head, hd = q.shape
-    c = _kv4(pages, table, q_start, lengths, n_rows, status)
-    _need(hd == c.head_dim and n_head % c.n_kv_head == 0 and max_len >= 0,
+    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
+    n_kv = c.n_kv_head
+    _on(dev, out, workspace)
+    _need(hd == c.head_dim and n_head % n_kv == 0 and max_len >= 0,
           "q's heads must be a multiple of the cache's, of the same head_dim")
-    _on(pages.device, q, out, workspace)
-    q = q.contiguous()
-    if q.data_ptr() % 16:
-        q = q.clone()
+    if not q.is_contiguous() or q.data_ptr() % 16:
+        q = q.clone(memory_format=torch.contiguous_format)
     if out is None:
-        out = torch.empty((n_rows, n_head, hd), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     else:
-        _need(out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous(),
+        _need(out.dtype is q.dtype and out.shape == q.shape and out.is_contiguous(),
               "out must be contiguous, of q's shape and type")
-    max_len = max_len or table.shape[1] * S2_KV4_PAGE
     if workspace is None:
-        nbytes = (_lib or load()).s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, c.n_kv_head, hd, max_len)
+        held = c.table_cols * S2_KV4_PAGE
+        nbytes = (_lib or load()).s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd,
+                                                             min(max_len or held, held))
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _launch("s2_kv4_attention", q.device, ctypes.byref(c), q.data_ptr(), dt, n_head,
+    _launch("s2_kv4_attention", dev, ctypes.byref(c), q.data_ptr(), dt, n_head,
             hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _ptr(workspace),
             0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
@@ -437,39 +461,41 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
     history int32 [rows][cols] with hist_len int32 [rows] and penalties fp32 [rows][3] of (repetition, frequency,
     presence); bias fp32 [rows or 1][n]; mask int32 or uint32 bits [rows or 1][ceil(n/32)].  Entry ids as in draw."""
     import torch
-    dt = _dtype_code(logits, "logits")
-    dev = logits.device
-    _need(logits.dim() == 2 and logits.numel() > 0, "logits must be [rows][n]")
-    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
+    dt, dev = _code(logits), logits.get_device()
+    _need(logits.dim() == 2, "logits must be [rows][n]")
     rows, n = logits.shape
-    cols = 0
-    _need((history is None) == (penalties is None), "history and penalties go together")
-    _need(hist_len is None or (history is not None and hist_len.dtype == torch.int32 and
-                               hist_len.shape == (rows,) and hist_len.is_contiguous()), "hist_len must be int32 [rows]")
+    i32, f32 = torch.int32, torch.float32
+    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
+    cols = bias_stride = mask_stride = 0
+    _need((history is None) == (penalties is None) and (hist_len is None or history is not None),
+          "history and penalties go together, hist_len with them")
     if history is not None:
-        _need(history.dtype == torch.int32 and history.dim() == 2 and history.shape[0] == rows and
-              history.is_contiguous(), "history must be contiguous int32 [rows][cols]")
-        _need(penalties.dtype == torch.float32 and tuple(penalties.shape) == (rows, 3) and penalties.is_contiguous(),
+        _need(history.dtype is i32 and history.dim() == 2 and history.shape[0] == rows and history.is_contiguous(),
+              "history must be contiguous int32 [rows][cols]")
+        _need(penalties.dtype is f32 and penalties.shape == (rows, 3) and penalties.is_contiguous(),
               "penalties must be contiguous fp32 [rows][3]")
+        _need(hist_len is None or (hist_len.dtype is i32 and hist_len.shape == (rows,) and hist_len.is_contiguous()),
+              "hist_len must be int32 [rows]")
         cols = history.shape[1]
         if cols == 0:
             history = penalties = hist_len = None
-    strides = []
-    for t, width, kinds, what in ((bias, n, (torch.float32,), "bias must be fp32 [rows or 1][n]"),
-                                  (mask, -(-n // 32), (torch.int32, torch.uint32),
-                                   "mask must be 32-bit [rows or 1][ceil(n/32)]")):
-        if t is not None:
-            _need(t.dtype in kinds and t.dim() == 2 and t.shape[0] in (1, rows) and t.shape[1] == width and
-                  t.is_contiguous(), what)
-        strides.append(0 if t is None or t.shape[0] == 1 else width)
-    logits = logits.contiguous()
+    if bias is not None:
+        _need(bias.dtype is f32 and bias.shape in ((1, n), (rows, n)) and bias.is_contiguous(),
+              "bias must be contiguous fp32 [rows or 1][n]")
+        bias_stride = n if bias.shape[0] > 1 else 0
+    if mask is not None:
+        words = -(-n // 32)
+        _need(mask.dtype in (i32, torch.uint32) and mask.shape in ((1, words), (rows, words)) and mask.is_contiguous(),
+              "mask must be contiguous 32-bit [rows or 1][ceil(n/32)]")
+        mask_stride = words if mask.shape[0] > 1 else 0
+    if not logits.is_contiguous():
+        logits = logits.contiguous()
     if out is None:
-        out = torch.empty((rows, n), dtype=torch.float32, device=dev)
+        out = torch.empty((rows, n), dtype=f32, device=logits.device)
     else:
-        _need(out.dtype == torch.float32 and tuple(out.shape) == (rows, n) and out.is_contiguous(),
-              "out must be contiguous fp32 [rows][n]")
+        _need(out.dtype is f32 and out.shape == (rows, n) and out.is_contiguous(), "out must be contiguous fp32 [rows][n]")
     _launch("s2_adjust_logits", dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt, _ptr(history), _ptr(hist_len),
-            cols, _ptr(penalties), _ptr(bias), strides[0], _ptr(mask), strides[1], out.data_ptr())
+            cols, _ptr(penalties), _ptr(bias), bias_stride, _ptr(mask), mask_stride, out.data_ptr())
     return out
 
 
