@@ -22,7 +22,8 @@ EXPORTS = ("s2_weight_count", "s2_weight_info", "s2_frame_workspace_bytes", "s2_
            "s2_decode_frames", "s2_fast_logits", "s2_sync_status", "s2_set_spin_limit", "s2_set_trace",
            "s2_phase_count", "s2_frame_free", "s2_last_error", "s2_fast_logits_static", "s2_stream_import",
            "s2_stop_stream", "s2_stream_progress", "s2_codec_latent", "s2_quantize_e4m3", "s2_set_barrier_base",
-           "s2_draw", "s2_quantize_q4", "s2_q4_matmul", "s2_kv4_page_bytes", "s2_kv4_append", "s2_kv4_read",
+           "s2_draw", "s2_quantize_q4", "s2_q4_matmul_workspace", "s2_q4_matmul",
+           "s2_kv4_page_bytes", "s2_kv4_append", "s2_kv4_read",
            "s2_kv4_attention_workspace", "s2_kv4_attention", "s2_adjust_logits")
 
 S2_KV4_PAGE = 64
@@ -97,7 +98,8 @@ def load(path: str = LIB_PATH):
         "s2_stream_progress": (i32, [vp, i32, P(i32), vp, vp]),
         "s2_draw": (i32, [i32, vp, i32, i32, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp]),
         "s2_quantize_q4": (i32, [vp, i32, i64, i32, i32, vp, vp, vp]),
-        "s2_q4_matmul": (i32, [i32, vp, i32, i64, vp, vp, i32, i32, i32, vp, vp]),
+        "s2_q4_matmul_workspace": (sz, [i32, i32, i32]),
+        "s2_q4_matmul": (i32, [i32, vp, i32, i64, vp, vp, i32, i32, i32, vp, vp, sz, vp]),
         "s2_kv4_page_bytes": (i64, [i32, i32]),
         "s2_kv4_append": (i32, [P(s2_kv4), vp, i32, i64, i32, vp, i32, vp, vp, ctypes.c_float, vp, vp]),
         "s2_kv4_read": (i32, [P(s2_kv4), vp, vp, vp]),
@@ -308,14 +310,15 @@ def quantize_q4(w, group: int = 32):
     return codes, scales
 
 
-def q4_matmul(x, codes, scales, group: int = 32, out=None):
-    """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type."""
+def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
+    """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type.
+    workspace, a uint8 tensor of s2_q4_matmul_workspace bytes, is allocated where none is given."""
     import torch
     dt, dev = _code(x), x.get_device()
     _need(x.dim() == 2 and codes.dim() == 2 and scales.dim() == 2, "q4_matmul takes 2-D tensors")
     n, k = x.shape
     m, width = codes.shape
-    _on(dev, codes, scales, out)
+    _on(dev, codes, scales, out, workspace)
     _need(group in (32, 64, 128) and k % group == 0, "columns must be a multiple of group: 32, 64 or 128")
     _need(codes.dtype is torch.uint8 and codes.is_contiguous() and width == -(-k // 128) * 64,
           "codes must be contiguous uint8 [rows][ceil(k/128)*64]")
@@ -327,8 +330,12 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None):
     else:
         _need(out.dtype is x.dtype and out.shape == (n, m) and out.is_contiguous(),
               "out must be contiguous [n][rows] of x's type")
+    if workspace is None:
+        nbytes = (_lib or load()).s2_q4_matmul_workspace(n, k, dt)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     _launch("s2_q4_matmul", dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k, group,
-            out.data_ptr())
+            out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
 
 

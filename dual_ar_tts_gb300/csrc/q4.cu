@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "convert.cuh"
 #include "ptx.cuh"
@@ -68,86 +69,77 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 
 // ---------------------------------------------------------------- products
 //
-// y = x W^T on mma.sync.m16n8k16 (bf16 operands, fp32 sums): 16 weight rows are the A operand, expanded
-// from their codes in registers (0x4300 | code is 128 + code in bf16, less 136 exactly), 8 activation
-// columns the B operand.  tcgen05 would want the expanded weights in tensor or shared memory first; a
-// decode step has 1 to 32 columns, and what bounds it is the reading of the codes.  A 32-bit word of codes
-// feeds the k positions of two instructions in the order (0,4)(1,5) | (2,6)(3,7) of its nibbles; the
-// activations are staged in that order.
+// y = x W^T on mma.sync.m16n8k16 (fp16 operands, fp32 sums): 16 weight rows are the A operand, expanded from
+// their codes in registers, 8 activation columns the B operand.  tcgen05 would want the expanded weights in
+// tensor or shared memory first and their group sums read back for every scale; a decode step has 1 to 32
+// columns, and what bounds it is the reading and expanding of the codes.
 //
-// Activations enter in full: an fp16 value is two bf16 terms and an fp32 value three (truncations of what
-// is left), each a column of its own, added at the end.  Codes are whole numbers, so products are exact;
-// a group's scale multiplies its fp32 sum.
+// Expanding is masking: a nibble in the low bits of an fp16 is the subnormal code * 2^-24, and four bits up it
+// is 16 times that.  The activations of those positions are staged as x / 16, the products are exact, and the
+// 8 that each code is off by goes into the sum's start, -8 * 2^-24 * sum x.  A 32-bit word of codes feeds the
+// k positions of two instructions in the order (0,4)(1,5) | (2,6)(3,7) of its nibbles; activations are staged
+// in that order.  A group's scale multiplies its fp32 sum.
 //
-// A block takes 128 rows (a warp 16) and a range of the columns of W; the blocks of a cluster split W's
-// columns and add their sums through distributed shared memory in rank order.
+// Activations are scaled by a power of two so that the largest of a row (of a staged chunk of it) lies in
+// 2^13 .. 2^14.  fp16 and bf16 values are then exact in fp16, but for elements 2^-24 below the largest and less,
+// which keep 2^-34 of it; an fp32 value is two fp16 terms (22 bits), each a column of its own, added at the end.
+//
+// A warp copies its codes ahead of their use (cp.async, its own ring).  Few activations are staged by each
+// block itself (k_q4_few); more of them once, by a kernel in front (k_q4_planes, k_q4_many).
 
-constexpr int kRows = 128;        // weight rows of a block
-constexpr int kChunk = 8;         // code blocks of activations in shared memory at a time
-constexpr int kAhead = 4;         // code blocks of weights that a warp has in flight (a chunk is whole turns of them)
+constexpr int kWarps = 8;
 
 template <typename T>
-struct Terms;
-template <>
-struct Terms<__nv_bfloat16> {
-  static constexpr int n = 1;
-};
-template <>
-struct Terms<__half> {
-  static constexpr int n = 2;
-};
-template <>
-struct Terms<float> {
-  static constexpr int n = 3;
-};
+constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
 
-// the next bf16 term of v (its leading 8 bits; what is not finite whole), which is taken off v
-__device__ __forceinline__ uint32_t next_term(float& v) {
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7f800000u) == 0x7f800000u) {
-    v = 0.f;
-    return (u & 0x7fffffu) ? 0x7fffu : u >> 16;
-  }
-  v -= __uint_as_float(u & 0xffff0000u);
-  return u >> 16;
-}
-
-// eight consecutive activations
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+// eight consecutive activations as loaded
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const T* h = reinterpret_cast<const T*>(&a);
+struct Eight {
+  uint4 raw[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f(h[i]);
-}
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = (&raw[0].x)[sizeof(T) == 4 ? i : i / 2];
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<uint16_t>(i % 2 ? w >> 16 : w)));
+    else return i % 2 ? bf16hi(w) : bf16lo(w);
+  }
+};
 
-__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
+// The power of two that takes a largest magnitude (its bits) to 2^13 .. 2^14, by its exponent; what is not
+// finite, and zero, stays as it is.
+__device__ __forceinline__ int scale_exponent(uint32_t top) {
+  const int e = static_cast<int>(top >> 23);
+  return top == 0 || e == 255 ? 0 : min(13 + 127 - e, 126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// d = A b + init, and d += A b
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, float2 init) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %10, %11};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(init.x), "f"(init.y));
+}
+__device__ __forceinline__ void mma_more(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// nibbles i and i + 4 of w as bf16 code - 8
-__device__ __forceinline__ uint32_t expand_q4(uint32_t w, int i) {
-  const uint32_t u = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(136.f));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
-               : "r"(addr), "r"(rank));
-  return v;
+template <int kSize>
+__device__ __forceinline__ void cp_async_small(void* smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(kSize), "r"(bytes)
+               : "memory");
 }
 
 struct MatmulArgs {
@@ -157,180 +149,476 @@ struct MatmulArgs {
   const uint8_t* codes;
   const __nv_bfloat16* scales;
   void* y;
+  int tiles;  // R
 };
 
-// a warp's part of one code block: 16 bytes of rows g and g + 8 each, and the rows' scales
-template <int G>
-struct WeightBlock {
-  uint4 w[2];
-  uint32_t s[2][G == 32 ? 2 : 1];
+// One 8-element item of an activation row (columns 8c .. 8c + 7 of a 32-column part, the four lanes c of a part
+// side by side in the warp), scaled by `up`: the B operand's 16 bytes of each term, and what the part's sum of
+// codes starts with (for all four lanes).
+template <typename T>
+struct Staged {
+  uint4 b[kTerms<T>];
+  float init[kTerms<T>];
+  __device__ __forceinline__ Staged(const Eight<T>& v, float up) {
+    float rest[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rest[e] = v[e] * up;
+#pragma unroll
+    for (int t = 0; t < kTerms<T>; ++t) {
+      uint32_t h[4];  // pairs (0,4) (1,5) (2,6) (3,7), the odd ones sixteen times too small
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = e % 2 ? 0.0625f : 1.f, back = e % 2 ? 16.f : 1.f;
+        const __half2 p = __floats2half2_rn(rest[e] * f, rest[e + 4] * f);
+        const float2 r = __half22float2(p);
+        h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        sum += (r.x + r.y) * back;
+        rest[e] -= r.x * back;
+        rest[e + 4] -= r.y * back;
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      b[t] = make_uint4(h[0], h[1], h[2], h[3]);
+      init[t] = sum * (-8.f / 16777216.f);
+    }
+  }
 };
+
+template <typename T>
+__device__ __forceinline__ uint32_t largest(const Eight<T>& v) {  // bits of the magnitude; NaN counts as the largest
+  uint32_t t = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t = max(t, __float_as_uint(v[e]) & 0x7fffffffu);
+  return t;
+}
+
+constexpr int kRing = 1024 + 128;  // a code block of 16 rows and its scales
+
+// A warp's codes: entry j of its sequence is block first + j * step of its 16 rows, kAhead in flight.
+template <int G, int kAhead>
+struct Codes {
+  static constexpr int SB = kBlock / G;  // scales of a block
+  uint8_t* ring;
+  const uint8_t *wa, *wb;
+  const __nv_bfloat16* scales;
+  size_t sat, send;
+  uint32_t par0, par1;  // parities of the rows' first scales (G = 128)
+  int issued = 0, count, step;
+
+  __device__ __forceinline__ Codes(uint8_t* r, const MatmulArgs& a, int row0, int blocks, int first, int n, int st)
+      : ring(r), scales(a.scales), count(n), step(st) {
+    const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
+    const int ra = min(row0 + g, a.m - 1), rb = min(row0 + g + 8, a.m - 1);
+    wa = a.codes + (static_cast<size_t>(ra) * blocks + first) * 64 + c * 16;
+    wb = a.codes + (static_cast<size_t>(rb) * blocks + first) * 64 + c * 16;
+    sat = (static_cast<size_t>(c ? rb : ra) * blocks + first) * SB;  // lanes c = 0, 1 copy the scales
+    send = static_cast<size_t>(a.m) * blocks;
+    par0 = static_cast<uint32_t>(ra) * blocks + first;
+    par1 = static_cast<uint32_t>(rb) * blocks + first;
+  }
+  __device__ __forceinline__ void issue() {  // does not commit
+    if (issued < count) {
+      const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
+      uint8_t* dst = ring + issued % kAhead * kRing;
+      cp_async16(dst + lane * 16, wa);
+      cp_async16(dst + 512 + lane * 16, wb);
+      wa += step * 64;
+      wb += step * 64;
+      if (c < 2) {
+        uint8_t* to = dst + 1024 + (g + 8 * c) * 8;
+        if constexpr (G == 128)  // two bytes wanted: the aligned four around them, less what lies past the last scale
+          cp_async_small<4>(to, scales + (sat & ~size_t{1}), (sat | 1) < send ? 4 : 2);
+        else
+          cp_async_small<2 * SB>(to, scales + sat, 2 * SB);
+        sat += step * SB;
+      }
+    }
+    ++issued;
+  }
+};
+
+// One code block (entry j of a ring) times the staged activations: z += W x, in units of 2^-24.  xq: this lane's
+// B operands, part p of tile t at xq[p * part_stride + t * 32]; iq: its sums' starts, at iq[(p * NT + t) * 4].
+template <int NT, int G>
+__device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t par1, const uint4* xq, int part_stride,
+                                         const float2* iq, float (&z)[NT][4]) {
+  const int lane = threadIdx.x % 32, g = lane / 4;
+  const uint4 w0 = lds128(at + lane * 16), w1 = lds128(at + 512 + lane * 16);
+  float s0[4], s1[4];
+  const uint32_t sa = at + 1024 + g * 8;
+  const uint32_t u = lds32(sa), v = lds32(sa + 64);
+  if constexpr (G == 32) {
+    const uint32_t u1 = lds32(sa + 4), v1 = lds32(sa + 68);
+    s0[0] = bf16lo(u), s0[1] = bf16hi(u), s0[2] = bf16lo(u1), s0[3] = bf16hi(u1);
+    s1[0] = bf16lo(v), s1[1] = bf16hi(v), s1[2] = bf16lo(v1), s1[3] = bf16hi(v1);
+  } else if constexpr (G == 64) {
+    s0[1] = bf16lo(u), s0[3] = bf16hi(u);
+    s1[1] = bf16lo(v), s1[3] = bf16hi(v);
+  } else {
+    s0[3] = par0 & 1 ? bf16hi(u) : bf16lo(u);
+    s1[3] = par1 & 1 ? bf16hi(v) : bf16lo(v);
+  }
+  const uint32_t wv[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
+  float d[NT][4];
+#pragma unroll
+  for (int part = 0; part < 4; ++part) {
+    const uint32_t p = wv[0][part], q = wv[1][part], p8 = p >> 8, q8 = q >> 8;
+    constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+    const bool first = part * 32 % G == 0, last = (part + 1) * 32 % G == 0;  // of a group
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint4 x = xq[part * part_stride + t * 32];
+      const float2 i0 = iq[(part * NT + t) * 4];
+      if (first) {
+        mma_first(d[t], p & lo, q & lo, p & hi, q & hi, x.x, x.y, i0);
+      } else {
+        d[t][0] += i0.x, d[t][1] += i0.y, d[t][2] += i0.x, d[t][3] += i0.y;
+        mma_more(d[t], p & lo, q & lo, p & hi, q & hi, x.x, x.y);
+      }
+      mma_more(d[t], p8 & lo, q8 & lo, p8 & hi, q8 & hi, x.z, x.w);
+      if (last) {
+        z[t][0] += s0[part] * d[t][0];
+        z[t][1] += s0[part] * d[t][1];
+        z[t][2] += s1[part] * d[t][2];
+        z[t][3] += s1[part] * d[t][3];
+      }
+    }
+  }
+}
+
+// a row's sum with its scaling taken back (the power itself may be out of fp32's range)
+__device__ __forceinline__ float unscale(float z, uint32_t top) {
+  const int e = 24 - scale_exponent(top);
+  return z * pow2(e / 2) * pow2(e - e / 2);
+}
+
+// ---- few activations: one tile of columns, staged whole by every block.  A block is 8 warps: R tiles of 16 rows
+// times 8 / R parts of W's columns (blocks of 128, taken in turn), whose sums are added in order at the end.
+constexpr int kFewAhead = 8;
+template <typename T>
+constexpr int kFewItems = sizeof(T) == 4 ? 4 : 8;  // loads of 8 activations that a thread has in flight
+
+template <typename T, int G>
+__global__ void __launch_bounds__(32 * kWarps, 2) k_q4_few(const MatmulArgs a) {
+  constexpr int TN = kTerms<T>, kItems = kFewItems<T>, kOut = 9;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint32_t top[8];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
+  const int parts = kWarps / a.tiles, tile = warp % a.tiles, part_k = warp / a.tiles;
+  const int blocks = (a.k + kBlock - 1) / kBlock, nn = a.n, live = nn * TN;
+  uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kFewAhead * kRing);  // [block, part][live column][lane c]
+  float* inits = reinterpret_cast<float*>(xs + blocks * 16 * live);         // [block, part][8]
+  const int row0 = (blockIdx.x * a.tiles + tile) * 16;
+
+  Codes<G, kFewAhead> codes(smem + warp * kFewAhead * kRing, a, row0, blocks, part_k,
+                            (blocks - part_k + parts - 1) / parts, parts);
+#pragma unroll
+  for (int i = 0; i < kFewAhead - 1; ++i) {
+    codes.issue();
+    cp_async_commit();
+  }
+  Eight<T> held[kItems];
+  const int items = blocks * 16 * nn;
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    const int i = threadIdx.x + u * 32 * kWarps, pc = i / 4, row = pc % nn, p = pc / nn;
+    const int k = p * 32 + i % 4 * 8;
+    if (i < items && k < a.k)
+      held[u].load(static_cast<const T*>(a.x) + row * a.x_stride + k);
+    else
+      held[u].zero();
+  }
+  if (threadIdx.x < 8) top[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    if (u * 32 * kWarps >= items) break;
+    uint32_t t = largest(held[u]);
+    if (nn == 1) {
+      t = __reduce_max_sync(0xffffffffu, t);
+      if (lane == 0) atomicMax(top, t);
+    } else {
+      t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      if (c == 0) atomicMax(top + (threadIdx.x + u * 32 * kWarps) / 4 % nn, t);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    if (u * 32 * kWarps >= items) break;
+    const int i = threadIdx.x + u * 32 * kWarps, pc = i / 4, row = pc % nn, p = pc / nn;
+    const Staged<T> st(held[u], pow2(scale_exponent(top[row])));
+    if (i < items)
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+        xs[(p * live + row * TN + t) * 4 + c] = st.b[t];
+        if (c == 0) inits[p * 8 + row * TN + t] = st.init[t];
+      }
+  }
+  __syncthreads();
+
+  float z[1][4] = {};
+  const uint4* xl = xs + (g < live ? lane : 0);  // the other columns' sums are not used
+  int j = 0;
+  for (int b = part_k; b < blocks; b += parts, ++j) {
+    codes.issue();
+    cp_async_commit();
+    cp_async_wait_group<kFewAhead - 1>();
+    __syncwarp();
+    multiply<1, G>(smem_u32(codes.ring + j % kFewAhead * kRing), codes.par0 + j * parts, codes.par1 + j * parts,
+                   xl + b * 16 * live, 4 * live, reinterpret_cast<const float2*>(inits + b * 32) + c, z);
+    __syncwarp();
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem);
+  const int rows = a.tiles * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[(part_k * rows + tile * 16 + g + i / 2 * 8) * kOut + 2 * c + i % 2] = z[0][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * nn; i += 32 * kWarps) {
+    const int r = i % rows, col = i / rows, row = blockIdx.x * rows + r;
+    if (row >= a.m) continue;
+    float v = 0.f;
+    for (int q = 0; q < parts; ++q)
+#pragma unroll
+      for (int t = TN - 1; t >= 0; --t) v += out[(q * rows + r) * kOut + col * TN + t];
+    static_cast<T*>(a.y)[static_cast<size_t>(col) * a.m + row] = from_f<T>(unscale(v, top[col]));
+  }
+}
+
+template <typename T>
+bool few(int n, int blocks) {
+  return static_cast<long long>(n) * kTerms<T> <= 8 &&
+         static_cast<long long>(n) * blocks * 16 <= kFewItems<T> * 32 * kWarps;
+}
+
+template <typename T, int G>
+int launch_few(MatmulArgs a, cudaStream_t st) {
+  const int all = (a.m + 15) / 16, blocks = (a.k + kBlock - 1) / kBlock;
+  a.tiles = kWarps;  // R: the most row tiles in a block that leave two blocks an SM
+  while (a.tiles > 1 && (all + a.tiles - 1) / a.tiles < 304) a.tiles /= 2;
+  const int smem = kWarps * kFewAhead * kRing + blocks * (256 * a.n * kTerms<T> + 128);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(k_q4_few<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+                              cudaSuccess)
+    return S2_ECUDA;
+  k_q4_few<T, G><<<(all + a.tiles - 1) / a.tiles, 32 * kWarps, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
+}
+
+// ---- more activations: staged once, as planes in the workspace that every block then copies.
+
+// What the workspace holds for `tiles` tiles of 8 columns.
+struct Planes {
+  uint4* b;       // [block, part][tile][lane]
+  float* inits;   // [block, part][8 tiles]
+  uint32_t* top;  // [row]
+  int tiles;
+  size_t bytes;
+};
+Planes planes(int n, int k, int terms, void* ws) {
+  Planes p{};
+  const long long cols = static_cast<long long>(n) * terms;
+  // passes of one, two or four tiles
+  p.tiles = static_cast<int>(cols <= 8 ? 1 : cols <= 16 ? 2 : (cols + 31) / 32 * 4);
+  const size_t parts = (static_cast<size_t>(k) + kBlock - 1) / kBlock * 4;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  p.b = reinterpret_cast<uint4*>(at);
+  p.inits = reinterpret_cast<float*>(at + parts * p.tiles * 512);
+  p.top = reinterpret_cast<uint32_t*>(at + parts * p.tiles * (512 + 32));
+  p.bytes = parts * p.tiles * (512 + 32) + static_cast<size_t>(p.tiles) * 8 * 4;
+  return p;
+}
+
+// One block per activation row (and per row of zeros that fills the last tile).
+template <typename T>
+__global__ void __launch_bounds__(512) k_q4_planes(const MatmulArgs a, const Planes p) {
+  constexpr int TN = kTerms<T>;
+  __shared__ uint32_t top;
+  const int row = blockIdx.x, lane = threadIdx.x % 32;
+  const bool live = row < a.n;
+  const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(live ? row : 0) * a.x_stride;
+  const int items = (a.k + kBlock - 1) / kBlock * 16;
+  auto load = [&](int i) {
+    Eight<T> v;
+    if (live && i < items && i * 8 < a.k)
+      v.load(x + i * 8);
+    else
+      v.zero();
+    return v;
+  };
+  if (threadIdx.x == 0) top = 0;
+  __syncthreads();
+  uint32_t t = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < items; i += blockDim.x) t = max(t, largest(load(i)));
+  t = __reduce_max_sync(0xffffffffu, t);
+  if (lane == 0) atomicMax(&top, t);
+  __syncthreads();
+  const float up = pow2(scale_exponent(top));
+  if (threadIdx.x == 0) p.top[row] = top;
+#pragma unroll 2
+  for (int i0 = 0; i0 < items; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x, part = i / 4;
+    const Staged<T> st(load(i), up);
+    if (i < items)
+#pragma unroll
+      for (int u = 0; u < TN; ++u) {
+        const int col = row * TN + u;
+        p.b[(static_cast<size_t>(part) * p.tiles + col / 8) * 32 + col % 8 * 4 + i % 4] = st.b[u];
+        if (i % 4 == 0) p.inits[static_cast<size_t>(part) * p.tiles * 8 + col] = st.init[u];
+      }
+  }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank));
+  return v;
+}
+
+// A block takes 128 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
+// their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
+// activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.
+constexpr int kManyRows = 16 * kWarps;
+constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
+template <int NT>
+constexpr int kManyAhead = NT == 1 ? 8 : 4;
+template <int NT>
+constexpr int kStepBytes = 4 * NT * (512 + 32);
 
 template <typename T, int NT, int G>
-__global__ void __launch_bounds__(256) k_q4_matmul(const MatmulArgs a) {
-  constexpr int TN = Terms<T>::n;
-  constexpr int kCols = 8 * NT / TN;  // activation rows of a pass
-  constexpr int kOut = 8 * NT + 1;    // floats of a weight row in the joining buffer
+__global__ void __launch_bounds__(32 * kWarps, 2) k_q4_many(const MatmulArgs a, const Planes p) {
+  constexpr int TN = kTerms<T>, kAhead = kManyAhead<NT>;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint4* xs = reinterpret_cast<uint4*>(smem);  // [code block][32-column part][8-column tile][lane]
+  __shared__ uint32_t top[8 * NT];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
   const int blocks = (a.k + kBlock - 1) / kBlock;
   const int ranks = gridDim.y, rank = blockIdx.y;
   const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / ranks);
-  const int b1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / ranks);
-  const int n0 = blockIdx.z * kCols, nn = min(kCols, a.n - n0);
-  const int row0 = blockIdx.x * kRows + warp * 16;
-  const int ra = min(row0 + g, a.m - 1), rb = min(row0 + g + 8, a.m - 1);
-  const uint4* wa = reinterpret_cast<const uint4*>(a.codes) + static_cast<size_t>(ra) * blocks * 4 + c;
-  const uint4* wb = reinterpret_cast<const uint4*>(a.codes) + static_cast<size_t>(rb) * blocks * 4 + c;
-  constexpr int SB = kBlock / G;  // scales of a block
-  const __nv_bfloat16* sa = a.scales + static_cast<size_t>(ra) * blocks * SB;
-  const __nv_bfloat16* sb = a.scales + static_cast<size_t>(rb) * blocks * SB;
-
-  auto fetch = [&](WeightBlock<G>& f, int b) {
-    if (b >= b1) return;
-    f.w[0] = __ldcs(wa + static_cast<size_t>(b) * 4);
-    f.w[1] = __ldcs(wb + static_cast<size_t>(b) * 4);
-    const __nv_bfloat16* p[2] = {sa + b * SB, sb + b * SB};
+  const int count = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / ranks) - b0;
+  uint8_t* xring = smem + kWarps * kAhead * kRing;
+  Codes<G, kAhead> codes(smem + warp * kAhead * kRing, a, blockIdx.x * kManyRows + warp * 16, blocks, b0, count, 1);
+  auto copy_x = [&](int j) {
+    if (j >= count) return;
+    uint8_t* dst = xring + j % kAhead * kStepBytes<NT>;
+    const size_t part = static_cast<size_t>(b0 + j) * 4;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if constexpr (G == 32) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p[r]));
-        f.s[r][0] = v.x, f.s[r][1] = v.y;
-      } else if constexpr (G == 64) {
-        f.s[r][0] = __ldg(reinterpret_cast<const uint32_t*>(p[r]));
-      } else {
-        f.s[r][0] = __ldg(reinterpret_cast<const uint16_t*>(p[r]));
-      }
-    }
+    for (int i = threadIdx.x; i < 4 * NT * 32; i += 32 * kWarps)
+      cp_async16(dst + i * 16, p.b + ((part + i / (NT * 32)) * p.tiles + blockIdx.z * NT) * 32 + i % (NT * 32));
+    if (threadIdx.x < 8 * NT)
+      cp_async16(dst + 4 * NT * 512 + threadIdx.x * 16, p.inits + ((part + threadIdx.x / (2 * NT)) * p.tiles + blockIdx.z * NT) * 8 +
+                                                            threadIdx.x % (2 * NT) * 4);
   };
-  auto scale = [](const WeightBlock<G>& f, int r, int part) {  // of 32-column part 0..3
-    const int i = part * 32 / G;
-    return i % 2 ? bf16hi(f.s[r][i / 2]) : bf16lo(f.s[r][i / 2]);
-  };
-
-  WeightBlock<G> ring[kAhead];
+  // codes do not depend on the kernel in front, which runs after all that came before it
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(ring[i], b0 + i);
-
-  float y[NT][4] = {};
-  for (int base = b0; base < b1; base += kChunk) {
-    const int nb = min(kChunk, b1 - base);
-    if (base > b0) __syncthreads();
-    // stage the activations: one item is eight columns of W of one row
-    const T* x = static_cast<const T*>(a.x);
-    for (int i = threadIdx.x; i < nb * 16 * kCols; i += blockDim.x) {
-      const int col = i / (nb * 16), part = i % (nb * 16);  // part: 4 * (block, 32-column part) + lane c
-      const int k = (base + part / 16) * kBlock + part % 16 * 8;
-      float v[8] = {};
-      if (col < nn && k < a.k) load8(x + (n0 + col) * a.x_stride + k, v);
+  for (int i = 0; i < kAhead - 1; ++i) codes.issue();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        uint32_t h[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = next_term(v[e]);
-        const int j = col * TN + t;
-        xs[((part / 4) * NT + j / 8) * 32 + j % 8 * 4 + part % 4] =
-            make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
-      }
-    }
-    if constexpr (8 * NT % TN != 0) {  // columns that no term fills
-      for (int i = threadIdx.x; i < nb * 16; i += blockDim.x)
-        for (int j = kCols * TN; j < 8 * NT; ++j)
-          xs[((i / 4) * NT + j / 8) * 32 + j % 8 * 4 + i % 4] = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    for (int q = 0; q < nb; q += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (q + u >= nb) break;
-        const WeightBlock<G> f = ring[u];
-        fetch(ring[u], base + q + u + kAhead);
-        const uint32_t wv[2][4] = {{f.w[0].x, f.w[0].y, f.w[0].z, f.w[0].w}, {f.w[1].x, f.w[1].y, f.w[1].z, f.w[1].w}};
-#pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          const uint32_t A0[4] = {expand_q4(wv[0][part], 0), expand_q4(wv[1][part], 0), expand_q4(wv[0][part], 1),
-                                  expand_q4(wv[1][part], 1)};
-          const uint32_t A1[4] = {expand_q4(wv[0][part], 2), expand_q4(wv[1][part], 2), expand_q4(wv[0][part], 3),
-                                  expand_q4(wv[1][part], 3)};
-          const float s0 = scale(f, 0, part), s1 = scale(f, 1, part);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint4 b = xs[(((q + u) * 4 + part) * NT + t) * 32 + lane];
-            float d[4];
-            mma_bf16_zero(d, A0, b.x, b.y);
-            mma_bf16_16816(d, A1[0], A1[1], A1[2], A1[3], b.z, b.w);
-            y[t][0] += s0 * d[0];
-            y[t][1] += s0 * d[1];
-            y[t][2] += s1 * d[2];
-            y[t][3] += s1 * d[3];
-          }
-        }
-      }
-    }
+  for (int i = 0; i < kAhead - 1; ++i) {
+    copy_x(i);
+    cp_async_commit();  // the first group holds the codes of all of them
   }
-  // join: this block's sums, then every block of the cluster adds up a share of the rows
+  if (threadIdx.x < 8 * NT / TN) top[threadIdx.x] = p.top[blockIdx.z * (8 * NT / TN) + threadIdx.x];
+  float z[NT][4] = {};
+  for (int j = 0; j < count; ++j) {
+    cp_async_wait_group<kAhead - 2>();
+    __syncthreads();  // step j is here, and step j - 1 is used up
+    codes.issue();
+    copy_x(j + kAhead - 1);
+    cp_async_commit();
+    const uint8_t* xq = xring + j % kAhead * kStepBytes<NT>;
+    multiply<NT, G>(smem_u32(codes.ring + j % kAhead * kRing), codes.par0 + j, codes.par1 + j,
+                    reinterpret_cast<const uint4*>(xq) + lane, NT * 32,
+                    reinterpret_cast<const float2*>(xq + 4 * NT * 512) + c, z);
+  }
+  cp_async_wait_all();
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[(warp * 16 + g + i / 2 * 8) * kOut + 8 * t + 2 * c + i % 2] = y[t][i];
+    for (int i = 0; i < 4; ++i) out[(8 * t + 2 * c + i % 2) * kJoinRow + warp * 16 + g + i / 2 * 8] = z[t][i];
   if (ranks > 1)
     cluster_sync();
   else
     __syncthreads();
-  const int share = kRows / ranks;
-  for (int i = threadIdx.x; i < share * nn; i += blockDim.x) {
-    const int r = rank * share + i % share, col = i / share, row = blockIdx.x * kRows + r;
-    if (row >= a.m) continue;
-    float v = 0.f;
-    const uint32_t at = smem_u32(out + r * kOut + col * TN);
-    for (int k = 0; k < ranks; ++k)
+  // a thread adds up four rows of one column
+  const int quads = kManyRows / 4 / ranks, n0 = blockIdx.z * 8 * NT / TN, nn = min(8 * NT / TN, a.n - n0);
+  for (int i = threadIdx.x; i < quads * nn; i += 32 * kWarps) {
+    const int r = (rank * quads + i % quads) * 4, col = i / quads, row = blockIdx.x * kManyRows + r;
+    float v[4] = {};
+    const float* at = out + col * TN * kJoinRow + r;
+    float4 u[8][TN];
 #pragma unroll
-      for (int t = TN - 1; t >= 0; --t) v += ranks > 1 ? ld_cluster(at + 4 * t, k) : out[r * kOut + col * TN + t];
-    static_cast<T*>(a.y)[static_cast<size_t>(n0 + col) * a.m + row] = from_f<T>(v);
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+        u[q][t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < ranks)
+          u[q][t] = ranks > 1 ? ld_cluster(smem_u32(at + t * kJoinRow), q)
+                              : *reinterpret_cast<const float4*>(at + t * kJoinRow);
+      }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int t = TN - 1; t >= 0; --t) v[0] += u[q][t].x, v[1] += u[q][t].y, v[2] += u[q][t].z, v[3] += u[q][t].w;
+    T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0 + col) * a.m + row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row + e < a.m) y[e] = from_f<T>(unscale(v[e], top[col]));
   }
   if (ranks > 1) cluster_sync();  // no block leaves while its sums are read
 }
 
 template <typename T, int NT, int G>
-int launch_matmul(const MatmulArgs& a, cudaStream_t st) {
-  constexpr int kCols = 8 * NT / Terms<T>::n;
-  constexpr int kXs = kChunk * 4 * NT * 32 * 16, kJoin = kRows * (8 * NT + 1) * 4;
-  const int blocks = (a.k + kBlock - 1) / kBlock;
-  const int grid = (a.m + kRows - 1) / kRows, passes = (a.n + kCols - 1) / kCols;
+int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
+  const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + kManyRows - 1) / kManyRows, passes = p.tiles / NT;
   if (passes > 65535) return S2_EINVAL;
+  // Up to two blocks an SM in clusters of two, one in larger ones (304 blocks in clusters of four do not all fit
+  // at a time: 9728 x 1024, 32 rows, 12.2 us against 8.8), of two code blocks at least.
   int ranks = 1;
-  while (ranks < 8 && static_cast<long long>(grid) * passes * ranks < 152 * 3 && blocks >= 4 * ranks) ranks *= 2;
-  const int smem = std::max(std::min(blocks, kChunk) * (kXs / kChunk), kJoin);
-  static_assert(kXs <= 200 * 1024 && kJoin <= 200 * 1024, "shared memory");
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k_q4_matmul<T, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, std::max(kXs, kJoin)) !=
-          cudaSuccess)
+  while (ranks < 8 && static_cast<long long>(grid) * passes * ranks * 2 <= (ranks == 1 ? 304 : 152) && blocks >= 4 * ranks)
+    ranks *= 2;
+  constexpr int kRings = kManyAhead<NT> * (kWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
+  constexpr int smem = kRings > kJoin ? kRings : kJoin;
+  if (cudaFuncSetAttribute(k_q4_many<T, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return S2_ECUDA;
+  k_q4_planes<T><<<p.tiles * 8 / kTerms<T>, 512, 0, st>>>(a, p);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, ranks, passes);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 1;
   at[0].val.clusterDim.y = ranks;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_q4_matmul<T, NT, G>, a) == cudaSuccess ? S2_OK : S2_ECUDA;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_q4_many<T, NT, G>, a, p) == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
 template <typename T, int G>
-int launch_columns(const MatmulArgs& a, cudaStream_t st) {
-  const int cols = a.n * Terms<T>::n;  // a pass of the fewest 8-column tiles that hold them, 4 at most
-  if (cols <= 8) return launch_matmul<T, 1, G>(a, st);
-  if (cols <= 16) return launch_matmul<T, 2, G>(a, st);
-  return launch_matmul<T, 4, G>(a, st);
+int launch_matmul(const MatmulArgs& a, void* ws, cudaStream_t st) {
+  if (few<T>(a.n, (a.k + kBlock - 1) / kBlock)) return launch_few<T, G>(a, st);
+  const Planes p = planes(a.n, a.k, kTerms<T>, ws);
+  return p.tiles == 1 ? launch_many<T, 1, G>(a, p, st)
+                      : p.tiles == 2 ? launch_many<T, 2, G>(a, p, st) : launch_many<T, 4, G>(a, p, st);
 }
+
+constexpr int kMatmulMost = 1 << 28;  // of each size
 
 bool bad_group(int group) { return group != 32 && group != 64 && group != 128; }
 
@@ -358,21 +646,32 @@ extern "C" int s2_quantize_q4(const void* w, int dtype, long long rows, int cols
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
+extern "C" size_t s2_q4_matmul_workspace(int n, int k, int dtype) {
+  if (n < 1 || k < 1 || n > kMatmulMost || k > kMatmulMost || !dtype_bytes(dtype)) return 0;
+  return with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    return few<T>(n, (k + kBlock - 1) / kBlock) ? size_t{0} : planes(n, k, kTerms<T>, nullptr).bytes;
+  });
+}
+
 extern "C" int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride, const uint8_t* codes,
-                            const void* scales, int m, int k, int group, void* y, CUstream_st* stream) {
+                            const void* scales, int m, int k, int group, void* y, void* workspace, size_t ws_bytes,
+                            CUstream_st* stream) {
   const int esz = dtype_bytes(dtype);
   if (!x || !codes || !scales || !y || !esz || n < 1 || m < 1 || k < 1 || bad_group(group) || k % group != 0 ||
-      x_stride < k || n > 0x3fffffff || m > 0x3fffffff || k > 0x3fffffff)
+      x_stride < k || n > kMatmulMost || m > kMatmulMost || k > kMatmulMost)
     return S2_EINVAL;
   if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || x_stride * esz % 16 != 0 ||
       reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % 16 != 0 ||
-      reinterpret_cast<uintptr_t>(y) % esz != 0)
+      reinterpret_cast<uintptr_t>(y) % esz != 0 || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return S2_EINVAL;
-  const MatmulArgs a{x, x_stride, n, m, k, codes, static_cast<const __nv_bfloat16*>(scales), y};
+  const size_t need = s2_q4_matmul_workspace(n, k, dtype);
+  if (need > 0 && (!workspace || ws_bytes < need)) return S2_EINVAL;
+  const MatmulArgs a{x, x_stride, n, m, k, codes, static_cast<const __nv_bfloat16*>(scales), y, 0};
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return group == 32 ? launch_columns<T, 32>(a, st)
-                       : group == 64 ? launch_columns<T, 64>(a, st) : launch_columns<T, 128>(a, st);
+    return group == 32 ? launch_matmul<T, 32>(a, workspace, st)
+                       : group == 64 ? launch_matmul<T, 64>(a, workspace, st) : launch_matmul<T, 128>(a, workspace, st);
   });
 }

@@ -353,13 +353,20 @@ int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group
                    struct CUstream_st* stream);
 
 /* y[i][r] = Σ_k x[i][k] · scale[r][k / group] · (code[r][k] - 8) for n activation rows and m weight
- * rows quantised as above.  Activations keep their precision: fp32 rows enter the products in full.
- *   x       device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times the
- *           element size a multiple of 16
+ * rows quantised as above.  Activations keep their precision: bf16 and fp16 rows enter the products
+ * as they are and fp32 rows with 22 bits, but for elements 2^-24 below their row's largest (of an
+ * fp32 row 2^-13), which are taken to 2^-34 of it.  A row with an element that is not finite gives
+ * results that are not.
+ *   x         device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times
+ *             the element size a multiple of 16
  *   codes, scales  as s2_quantize_q4 writes them, both 16-byte aligned; k a multiple of group
- *   y       device [n][m] of dtype, aligned to its element size */
+ *   y         device [n][m] of dtype, aligned to its element size
+ *   workspace device, 16-byte aligned, of at least s2_q4_matmul_workspace bytes for the same sizes
+ *             (NULL where that is 0).  Calls that may run at the same time need one each.
+ * Each size at most 2^28. */
+size_t s2_q4_matmul_workspace(int n, int k, int dtype);
 int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride, const uint8_t* codes, const void* scales,
-                 int m, int k, int group, void* y, struct CUstream_st* stream);
+                 int m, int k, int group, void* y, void* workspace, size_t ws_bytes, struct CUstream_st* stream);
 
 /* The paged 4-bit cache of one layer, and the rows of a call.
  *   pages   device [n_pages][n_kv_head][block], 16-byte aligned.  A page holds S2_KV4_PAGE positions;

@@ -33,9 +33,17 @@ def test_quantize_q4(lib):
 
 
 def test_q4_matmul(lib):
-    good = dict(n=2, x=P, dtype=1, x_stride=128, codes=P, scales=P, m=4, k=128, group=32, y=P, stream=None)
-    _bad(lib.s2_q4_matmul, good, n=[0, -1], x=[None, P + 2], dtype=[3, 9], x_stride=[127, 132, 0], codes=[None, P + 4],
+    good = dict(n=2, x=P, dtype=1, x_stride=128, codes=P, scales=P, m=4, k=128, group=32, y=P, ws=None, nb=0,
+                stream=None)
+    _bad(lib.s2_q4_matmul, good, ws=[P + 8], n=[0, -1], x=[None, P + 2], dtype=[3, 9], x_stride=[127, 132, 0], codes=[None, P + 4],
          scales=[None, P + 2], m=[0, -3], k=[0, 100, -32], group=[0, 31, 256], y=[None, P + 1])
+    for dtype in (0, 1, 2):
+        need = lib.s2_q4_matmul_workspace(40, 2560, dtype)
+        assert need > 0 and lib.s2_q4_matmul_workspace(1, 2560, dtype) == 0
+        _bad(lib.s2_q4_matmul, dict(good, n=40, k=2560, x_stride=2560, dtype=dtype, ws=P, nb=need), nb=[0, need - 1],
+             ws=[None])
+    for bad in ((0, 128, 1), (1, 0, 1), (1, 128, 3), (-1, 128, 0), (1 << 30, 128, 0)):
+        assert lib.s2_q4_matmul_workspace(*bad) == 0
 
 
 def _cache(pkg, **over):
