@@ -10,7 +10,8 @@
 // A column is a (row, query head) pair; with fp32 queries it is two, the high and the low fp16 part of the
 // query, whose scores are added and whose weights are again split so (a weight then carries 22 bits).
 // 16-bit queries are exact in fp16: each row is scaled by a power of two.  Weights are kept as
-// 2^6 exp2(s - m), which puts what fp16 drops 2^-30 below the largest.
+// 2^6 exp2(s - m), m the running maximum or up to 8 (log2) below it: what fp16 drops of them is 2^-30 and
+// less of the largest, and a maximum that rises a little costs no rescaling of the output.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,9 +27,10 @@ namespace s2 {
 namespace {
 
 constexpr int kStep = 16;       // positions of one pair of products
-constexpr int kDepth = 4;       // steps a warp has in flight
+constexpr int kHalfPage = 32;   // positions that a warp copies at a time: two steps
+constexpr int kDepth = 2;       // half pages that a warp holds
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kWeightShift = 6.f;
+constexpr float kWeightShift = 6.f, kSlack = 8.f;
 
 struct AttnArgs {
   s2_kv4 c;
@@ -96,37 +98,40 @@ __device__ __forceinline__ void expand(uint32_t w, const Pair& p, uint32_t (&v)[
   v[3] = h2_bits(__hmul2(p.s, __hfma2(bits_h2((w8 & 0x00f000f0u) | m), sixteenth, p.z64)));
 }
 
-// One step of the cache in shared memory.  Keys are read 16 bytes (a quarter row) a lane, rows packed;
+// Half a page of the cache in shared memory.  Keys are read 16 bytes (a quarter row) a lane, rows packed;
 // values a word or two of four rows a lane, rows padded so that the rows of the four lanes of a group
 // start 32 bytes apart modulo 128: both without bank conflicts.
 template <int HD>
 struct Stage {
   using B = Kv4Block<HD>;
   static constexpr int kVRow = B::kRow + 16;
-  static constexpr int kK = 0, kKPar = kStep * B::kRow, kV = kKPar + kStep * B::kPar, kVPar = kV + kStep * kVRow;
-  static constexpr int kBytes = kVPar + kStep * B::kPar;
+  static constexpr int kK = 0, kKPar = kHalfPage * B::kRow, kV = kKPar + kHalfPage * B::kPar,
+                       kVPar = kV + kHalfPage * kVRow;
+  static constexpr int kBytes = kVPar + kHalfPage * B::kPar;
 };
 
-// a warp's copy of the step at position `slot` of a page block
+// a warp's copy of half `half` of a page block
 template <int HD>
-__device__ __forceinline__ void copy_step(uint8_t* st, const uint8_t* block, int slot, int lane) {
+__device__ __forceinline__ void copy_half(uint8_t* st, const uint8_t* block, int half, int lane) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
-  const uint8_t* k = block + slot * B::kRow;
-  const uint8_t* v = k + B::kHalf;
+  constexpr int per = B::kRow / 16;  // 16-byte units of a row
+  const uint8_t* k = block + half * (kHalfPage * B::kRow) + lane * 16;
+  uint8_t* to = st + lane * 16;
 #pragma unroll
-  for (int i = lane; i < kStep * B::kRow / 16; i += 32) cp_async16(st + S::kK + i * 16, k + i * 16);
+  for (int i = 0; i < per; ++i) cp_async16(to + S::kK + i * 512, k + i * 512);
+  to = st + S::kV + lane / per * S::kVRow + lane % per * 16;
 #pragma unroll
-  for (int i = lane; i < kStep * B::kRow / 16; i += 32) {
-    constexpr int per = B::kRow / 16;
-    cp_async16(st + S::kV + i / per * S::kVRow + i % per * 16, v + i * 16);
-  }
-  constexpr int np = kStep * B::kPar / 16;  // 16 or 8
-  const uint8_t* par = block + kPage * B::kRow + slot * B::kPar;
-  if (lane < np)
+  for (int i = 0; i < per; ++i) cp_async16(to + i * (32 / per) * S::kVRow, k + B::kHalf + i * 512);
+  constexpr int np = kHalfPage * B::kPar / 16;  // 32 or 16
+  const uint8_t* par = block + kPage * B::kRow + half * (kHalfPage * B::kPar);
+  if constexpr (np == 32) {
     cp_async16(st + S::kKPar + lane * 16, par + lane * 16);
-  else if (lane < 2 * np)
-    cp_async16(st + S::kVPar + (lane - np) * 16, par + B::kHalf + (lane - np) * 16);
+    cp_async16(st + S::kVPar + lane * 16, par + B::kHalf + lane * 16);
+  } else {
+    const bool v = lane >= np;
+    cp_async16(st + (v ? S::kVPar : S::kKPar) + lane % np * 16, par + (v ? B::kHalf : 0) + lane % np * 16);
+  }
 }
 
 // The query columns of a warp as B operand: lane (g = lane / 4, c = lane % 4) holds column g of each
@@ -161,12 +166,12 @@ __device__ __forceinline__ float load_q(const T* q, bool live, bool low, int c, 
 
 // S^T of one step: scores of rows g, g + 8 at columns 2c, 2c + 1 of each group of 8
 template <int HD, int NT>
-__device__ __forceinline__ void scores(uint32_t st, int g, int c, const uint32_t (&q)[NT][HD / 8], float (&s)[NT][4]) {
+__device__ __forceinline__ void scores(uint32_t st, int step, int g, int c, const uint32_t (&q)[NT][HD / 8], float (&s)[NT][4]) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
   constexpr int W = HD / 32;  // words of a lane's quarter row
   uint32_t r0[W], r1[W];
-  const uint32_t a = st + S::kK + g * B::kRow + c * (HD / 8);
+  const uint32_t a = st + S::kK + (step * kStep + g) * B::kRow + c * (HD / 8);
   if constexpr (W == 4) {
     const uint4 x = lds128(a), y = lds128(a + 8 * B::kRow);
     r0[0] = x.x, r0[1] = x.y, r0[2] = x.z, r0[3] = x.w;
@@ -176,7 +181,7 @@ __device__ __forceinline__ void scores(uint32_t st, int g, int c, const uint32_t
     r0[0] = x.x, r0[1] = x.y;
     r1[0] = y.x, r1[1] = y.y;
   }
-  const uint32_t par = st + S::kKPar + g * B::kPar + c * (HD / 4) / kKvGroup * 4;
+  const uint32_t par = st + S::kKPar + (step * kStep + g) * B::kPar + c * (HD / 4) / kKvGroup * 4;
   const uint32_t p0 = lds32(par), p1 = lds32(par + 8 * B::kPar);
   const Pair pa(p0, p0), pb(p1, p1);
 #pragma unroll
@@ -196,34 +201,45 @@ __device__ __forceinline__ void scores(uint32_t st, int g, int c, const uint32_t
   }
 }
 
+// Whether parameters of the step's values are no numbers (for the whole warp): each lane looks at its share.
+template <int HD>
+__device__ __forceinline__ bool odd_values(uint32_t st, int step, int lane) {
+  using S = Stage<HD>;
+  const uint32_t a = st + S::kVPar + step * kStep * Kv4Block<HD>::kPar;
+  auto odd = [](uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; };
+  uint32_t bad;
+  if constexpr (HD == 128) {
+    const uint2 w = lds64(a + lane * 8);
+    bad = odd(w.x) | odd(w.y);
+  } else {
+    bad = odd(lds32(a + lane * 4));
+  }
+  return __any_sync(0xffffffffu, bad != 0);
+}
+
 // O^T += V^T P^T of one step.  Lane (g, c) expands elements g * hd/8 .. + hd/8 - 1 of rows 2c, 2c + 1, 2c + 8,
-// 2c + 9; element 2i of those is row g, element 2i + 1 row g + 8 of the i-th tile.  `valid` rows from the
-// step's start are in the sequence; parameters of the others are taken as zero (their weights are zero, but
-// what is there may be no number).  Returns whether a parameter is not finite: such rows count as zero here.
-template <int HD, int NT>
-__device__ __forceinline__ bool values(uint32_t st, int g, int c, int valid, const uint32_t (&p)[NT][2],
+// 2c + 9; element 2i of those is row g, element 2i + 1 row g + 8 of the i-th tile.  Where not kPlain, the
+// parameters of rows from `valid` on (behind the sequence: their weights are zero, but what is there may be no
+// number) and those that are no numbers count as zero.
+template <int HD, int NT, bool kPlain>
+__device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[NT][2],
                                        float (&o)[NT][HD / 16][4]) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
   constexpr int W = HD / 64;  // words of a row that a lane expands
   uint32_t w[4][W], par[4];
-  bool odd = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int row = 2 * c + (k & 1) + (k >> 1) * 8;
-    const uint32_t a = st + S::kV + row * S::kVRow + g * (HD / 16);
+    const uint32_t a = st + S::kV + (step * kStep + row) * S::kVRow + g * (HD / 16);
     if constexpr (W == 2) {
       const uint2 x = lds64(a);
       w[k][0] = x.x, w[k][1] = x.y;
     } else {
       w[k][0] = lds32(a);
     }
-    par[k] = lds32(st + S::kVPar + row * B::kPar + g * (HD / 8) / kKvGroup * 4);
-    if (row >= valid) par[k] = 0;
-    if ((par[k] & 0x7c00u) == 0x7c00u || (par[k] & 0x7c000000u) == 0x7c000000u) {
-      odd = true;
-      par[k] = 0;
-    }
+    par[k] = lds32(st + S::kVPar + (step * kStep + row) * B::kPar + g * (HD / 8) / kKvGroup * 4);
+    if (!kPlain && (row >= valid || (par[k] & 0x7c00u) == 0x7c00u || (par[k] & 0x7c000000u) == 0x7c000000u)) par[k] = 0;
   }
   const Pair lo(par[0], par[1]), hi(par[2], par[3]);
 #pragma unroll
@@ -240,7 +256,6 @@ __device__ __forceinline__ bool values(uint32_t st, int g, int c, int valid, con
         mma_f16_16816(o[n][4 * j + 2 * h + 1], x[2], x[3], y[2], y[3], p[n][0], p[n][1]);
       }
     }
-  return odd;
 }
 
 // The running state of a warp's columns.  A lane's columns are 2c, 2c + 1 of each group of 8 (with fp32
@@ -283,28 +298,37 @@ struct Rows {
             if (t0 + g + 8 * r >= lim[n][j]) x[r][j] = -INFINITY;
         }
       }
+      bool rise = false;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) rise = rise || fmaxf(x[0][j], x[1][j]) > m[n][j] + kSlack;
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          float top = fmaxf(x[0][j], x[1][j]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float mn = fmaxf(m[n][j], top);
+          const float keep = ex2(m[n][j] - (mn == -INFINITY ? 0.f : mn));
+          m[n][j] = mn;
+          l[n][j] *= keep;
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            if constexpr (kTwo) {
+              o[n][i][0] *= keep, o[n][i][1] *= keep, o[n][i][2] *= keep, o[n][i][3] *= keep;
+            } else {
+              o[n][i][j] *= keep, o[n][i][2 + j] *= keep;
+            }
+          }
+        }
+      }
       float w[2][2];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        float top = fmaxf(x[0][j], x[1][j]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float mn = fmaxf(m[n][j], top);
-        const float base = mn == -INFINITY ? 0.f : mn - kWeightShift;
-        const float keep = ex2(m[n][j] - (mn == -INFINITY ? 0.f : mn));
-        m[n][j] = mn;
+        const float base = m[n][j] == -INFINITY ? 0.f : m[n][j] - kWeightShift;
         w[0][j] = ex2(x[0][j] - base);
         w[1][j] = ex2(x[1][j] - base);
-        l[n][j] = l[n][j] * keep + (w[0][j] + w[1][j]);
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          if constexpr (kTwo) {
-            o[n][i][0] *= keep, o[n][i][1] *= keep, o[n][i][2] *= keep, o[n][i][3] *= keep;
-          } else {
-            o[n][i][j] *= keep, o[n][i][2 + j] *= keep;
-          }
-        }
+        l[n][j] += w[0][j] + w[1][j];
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -315,10 +339,10 @@ struct Rows {
   }
 
   // a value row of the step that is no number: every column that sees it is none either, in its group's elements
-  __device__ __forceinline__ void poison(uint32_t st, int t0, int valid, int g) {
+  __device__ __forceinline__ void poison(uint32_t st, int step, int t0, int valid, int g) {
     using S = Stage<HD>;
     for (int r = 0; r < valid; ++r) {
-      const uint32_t par = lds32(st + S::kVPar + r * Kv4Block<HD>::kPar + g * (HD / 8) / kKvGroup * 4);
+      const uint32_t par = lds32(st + S::kVPar + (step * kStep + r) * Kv4Block<HD>::kPar + g * (HD / 8) / kKvGroup * 4);
       if ((par & 0x7c00u) != 0x7c00u && (par & 0x7c000000u) != 0x7c000000u) continue;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -388,19 +412,21 @@ struct Pages {
   }
 };
 
-// Few columns: a block takes one tile of 8 columns of one KV head over a range of pages.  Warp w takes
-// positions 16w .. 16w + 15 of each page with its own copies in flight, so the warps never wait on one
-// another until their states are joined.
+constexpr int kWarps = 4;
+template <int HD>
+constexpr int kDecodeSmem = std::max(kWarps * kDepth * Stage<HD>::kBytes, kWarps * 8 * (HD + 4 + 2) * 4);
+
+// Few columns: a block takes one tile of 8 columns of one KV head over a range of pages, two at a time.  Each of
+// its four warps takes half a page with its own copies in flight, so the warps never wait on one another until
+// their states are joined.
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   constexpr bool kTwo = sizeof(T) == 4;
   constexpr int CT = kTwo ? 4 : 8;  // logical columns
-  constexpr int kWarps = 4;
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
   constexpr int kORow = HD + 4;  // floats of a column's output in the joining buffer
-  constexpr int kRing = kWarps * kDepth * S::kBytes, kJoin = kWarps * CT * (kORow + 2) * 4;
-  __shared__ __align__(16) uint8_t sm[kRing > kJoin ? kRing : kJoin];
+  extern __shared__ __align__(16) uint8_t sm[];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
   const int kh = blockIdx.y, split = blockIdx.z;
   const Tile tile = find_tile(a.c.q_start, a.c.n_seq, a.group, CT, blockIdx.x);
@@ -443,32 +469,47 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   uint8_t* ring = sm + warp * kDepth * S::kBytes;
   Pages pg{a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols, pages, a.c.n_pages};
   const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
-  uint32_t usable = 0;  // by page modulo 32: copied
-  auto issue = [&](int p) {
-    if (p < p1) {
-      const int id = pg.id(p, a.c.status);
-      const bool ok = id >= 0 && p * kPage + warp * kStep < len;
-      usable = ok ? usable | 1u << (p & 31) : usable & ~(1u << (p & 31));
+  uint32_t usable = 0;  // by turn modulo 32: copied
+  const int half = warp & 1, turns = (p1 - p0 + 1) / 2;
+  auto issue = [&](int turn) {
+    const int p = p0 + 2 * turn + warp / 2;
+    if (turn < turns) {
+      const int id = pg.id(p < p1 ? p : p0, a.c.status);
+      const bool ok = p < p1 && id >= 0 && p * kPage + half * kHalfPage < len;
+      usable = ok ? usable | 1u << (turn & 31) : usable & ~(1u << (turn & 31));
       if (ok)
-        copy_step<HD>(ring + p % kDepth * S::kBytes, heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes,
-                      warp * kStep, lane);
+        copy_half<HD>(ring + turn % kDepth * S::kBytes, heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes,
+                      half, lane);
     }
     cp_async_commit();
   };
-  for (int i = 0; i < kDepth - 1; ++i) issue(p0 + i);
-  for (int p = p0; p < p1; ++p) {
-    issue(p + kDepth - 1);
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) issue(i);
+  for (int turn = 0; turn < turns; ++turn) {
+    issue(turn + kDepth - 1);
     cp_async_wait_group<kDepth - 1>();
     __syncwarp();
-    if (usable >> (p & 31) & 1) {
-      const int t0 = p * kPage + warp * kStep;
-      const uint32_t at = smem_u32(ring + p % kDepth * S::kBytes);
-      float s[1][4];
-      uint32_t pf[1][2];
-      scores<HD, 1>(at, g, c, qf, s);
-      st.softmax(s, t0, g, t0 + kStep > first_lim, pf);
-      const int valid = min(len - t0, kStep);
-      if (__any_sync(0xffffffffu, values<HD, 1>(at, g, c, valid, pf, st.o))) st.poison(at, t0, valid, g);
+    if (usable >> (turn & 31) & 1) {
+      const uint32_t at = smem_u32(ring + turn % kDepth * S::kBytes);
+      const int first = (p0 + 2 * turn + warp / 2) * kPage + half * kHalfPage;
+#pragma unroll 1
+      for (int step = 0; step < 2; ++step) {
+        const int t0 = first + step * kStep, valid = min(len - t0, kStep);
+        if (valid <= 0) break;
+        float s[1][4];
+        uint32_t pf[1][2];
+        scores<HD, 1>(at, step, g, c, qf, s);
+        // where every column sees the whole step, a value that is no number reaches all of them anyway
+        const bool cut = t0 + kStep > first_lim;
+        st.softmax(s, t0, g, cut, pf);
+        const bool odd = cut && odd_values<HD>(at, step, lane);
+        if (!odd && valid == kStep) {
+          values<HD, 1, true>(at, step, g, c, valid, pf, st.o);
+        } else {
+          values<HD, 1, false>(at, step, g, c, valid, pf, st.o);
+          if (odd) st.poison(at, step, t0, valid, g);
+        }
+      }
     }
     __syncwarp();
   }
@@ -522,54 +563,335 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   }
 }
 
-// The splits of each (row, query head), one warp each: their maxima decide the weights of their outputs.
+// ---- many columns: a block takes 128 columns (fp32 queries: 64, two each) of one KV head, a warp 32 of them.
+// Every page is expanded once for all of them, into fp16 rows in shared memory (double-buffered; its codes wait in
+// registers while the page before is used), and the products read it with ldmatrix, 32 positions at a time.
+// Within a row the elements of eight codes lie in the order 0 4 1 5 2 6 3 7, queries alike.
+constexpr int kManyCols = 128, kManyTiles = 4;
+template <int HD>
+struct Many {
+  static constexpr int kRow = 2 * HD + 16;  // bytes of an expanded row
+  static constexpr int kHalf = kPage * kRow, kPageBytes = 2 * kHalf;
+  static constexpr int kQ = 0, kKv = kManyCols * kRow, kF = kKv + 2 * kPageBytes, kLim = kF + kManyCols * 4,
+                       kOdd = kLim + kManyCols * 4, kBytes = kOdd + 2 * kPage * 4;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// What a thread holds of a page: half a row of key and value codes with their parameters.
+template <int HD>
+struct HalfRow {
+  static constexpr int kU = HD / 64;  // 16-byte units
+  uint4 k[kU], v[kU];
+  uint32_t kp[kU], vp[kU];
+  __device__ __forceinline__ void load(const uint8_t* block, int row, int half) {
+    using B = Kv4Block<HD>;
+    const uint8_t* p = block + row * B::kRow + half * (kU * 16);
+    const uint8_t* q = block + kPage * B::kRow + row * B::kPar + half * (kU * 4);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      k[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      v[i] = __ldg(reinterpret_cast<const uint4*>(p + B::kHalf) + i);
+      kp[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
+      vp[i] = __ldg(reinterpret_cast<const uint32_t*>(q + B::kHalf) + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) k[i] = v[i] = make_uint4(0, 0, 0, 0), kp[i] = vp[i] = 0;
+  }
+  // Expands into the row of a page buffer; values whose parameters are no numbers become zeros.  Returns the bits
+  // of the groups where they did (within the row).
+  __device__ __forceinline__ uint32_t expand_to(uint8_t* page, int row, int half) const {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int u = kU == 2 ? i ^ half : i;  // the halves write different banks
+      const uint4 kc = kU == 2 && half ? k[i ^ (kU - 1)] : k[i], vc = kU == 2 && half ? v[i ^ (kU - 1)] : v[i];
+      const uint32_t a = kU == 2 && half ? kp[i ^ (kU - 1)] : kp[i];
+      uint32_t b = kU == 2 && half ? vp[i ^ (kU - 1)] : vp[i];
+      if ((b & 0x7c00u) == 0x7c00u || (b & 0x7c000000u) == 0x7c000000u) {
+        odd |= 1u << (half * kU + u);
+        b = 0;
+      }
+      const Pair pk(a, a), pv(b, b);
+      uint8_t* to = page + row * Many<HD>::kRow + (half * kU + u) * 64;
+      const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[4], y[4];
+        expand(kw[j], pk, x);
+        expand(vw[j], pv, y);
+        *reinterpret_cast<uint4*>(to + j * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(to + Many<HD>::kHalf + j * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    return odd;
+  }
+};
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) k_kv4_join(const AttnArgs a) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x % 32;
-  const long long item = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-  const int row = static_cast<int>(item / a.n_head);
-  if (row >= a.c.n_rows) return;
+__global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
+  constexpr bool kTwo = sizeof(T) == 4;
+  constexpr int CT = kTwo ? kManyCols / 2 : kManyCols;
+  constexpr int NT = kManyTiles;
+  using B = Kv4Block<HD>;
+  using M = Many<HD>;
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
+  const int kh = blockIdx.y, split = blockIdx.z;
+  const Tile tile = find_tile(a.c.q_start, a.c.n_seq, a.group, CT, blockIdx.x);
+  if (tile.seq < 0) return;
+  const int q0 = __ldg(a.c.q_start + tile.seq), q1 = __ldg(a.c.q_start + tile.seq + 1);
+  if (q0 < 0 || q1 > a.c.n_rows) {
+    if (threadIdx.x == 0) kv4_bad(a.c.status);
+    return;
+  }
+  const int cols = (q1 - q0) * a.group;
+  int len = __ldg(a.c.lengths + tile.seq);
+  const int over = len - (q1 - q0);  // row i sees over + i + 1 positions
+  if (len > a.c.table_cols * kPage) {
+    if (threadIdx.x == 0) kv4_bad(a.c.status);
+    len = a.c.table_cols * kPage;
+  }
+  len = max(len, 0);
+  const int pages = (len + kPage - 1) / kPage;
+  const int p0 = split * a.split_pages;
+  int p1 = split == a.n_split - 1 ? pages : min(pages, p0 + a.split_pages);
+  if (p0 >= p1 && split > 0) return;
+  // no column of the tile sees more than its last one
+  const int last = min(tile.first + CT, cols) - 1;
+  const int most = min(over + last / a.group + 1, len);
+  p1 = min(p1, (max(most, 0) + kPage - 1) / kPage);
+
+  // queries: a thread a column
+  {
+    const int col = tile.first + (kTwo ? threadIdx.x / 2 : threadIdx.x);
+    const bool live = col < cols;
+    const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
+    const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD;
+    constexpr int kPer = 16 / sizeof(T);
+    float top = 0.f;
+    for (int i = 0; i < HD / kPer; ++i) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
+      const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) top = fmaxf(top, fabsf(to_f(e[k])));
+    }
+    int e = 0;  // as load_q
+    if (live && top > 0.f && isfinite(top)) e = min(13 - ilogbf(top), 126);
+    const float up = live ? ldexpf(1.f, e) : 0.f;
+    uint8_t* to = sm + M::kQ + threadIdx.x * M::kRow;
+    for (int i = 0; i < HD / 8; ++i) {
+      uint4 u[sizeof(T) / 2];
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
+        u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i * (sizeof(T) / 2) + k);
+      const T* v = reinterpret_cast<const T*>(u);
+      uint32_t r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x = live ? to_f(v[k]) * up : 0.f, y = live ? to_f(v[k + 4]) * up : 0.f;
+        if (kTwo && (threadIdx.x & 1)) {
+          x -= round_f16(x);
+          y -= round_f16(y);
+        }
+        r[k] = h2_bits(__floats2half2_rn(x, y));
+      }
+      *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    reinterpret_cast<float*>(sm + M::kF)[threadIdx.x] = ldexpf(1.f, -e) * a.scale * kLog2e;
+    reinterpret_cast<int*>(sm + M::kLim)[threadIdx.x] = live ? min(over + col / a.group + 1, len) : 0;
+  }
+  const int row = threadIdx.x / 2, half = threadIdx.x % 2;
+  const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
+  const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
+  HalfRow<HD> held;
+  // page p into registers (zeros for rows behind the sequence); whether it is there at all
+  auto fetch = [&](int p) {
+    const int id = __ldg(table + p);
+    const bool ok = id >= 0 && id < a.c.n_pages;
+    if (!ok && threadIdx.x == 0) kv4_bad(a.c.status);
+    if (ok && p * kPage + row < len)
+      held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, row, half);
+    else
+      held.zero();
+    return ok;
+  };
+  bool next_ok = p0 < p1 && fetch(p0);
+  __syncthreads();
+  Rows<HD, NT, kTwo> st;
+  st.init();
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < st.NC; ++j) {
+      const int col = warp * 32 + n * 8 + 2 * c + j;
+      st.f[n][j] = reinterpret_cast<float*>(sm + M::kF)[col];
+      st.lim[n][j] = reinterpret_cast<int*>(sm + M::kLim)[col];
+    }
+  // the least and the most that this warp's columns see
+  const int w0 = tile.first + warp * (CT / 4), w1 = min(w0 + CT / 4, cols) - 1;
+  const int least = min(over + w0 / a.group + 1, len), warp_most = w0 < cols ? min(over + w1 / a.group + 1, len) : 0;
+  const uint32_t qa = smem_u32(sm + M::kQ) + (warp * 32 + lane / 16 * 8 + lane % 8) * M::kRow + (lane / 8 % 2) * 16;
+
+  for (int p = p0; p < p1; ++p) {
+    uint8_t* page = sm + M::kKv + (p & 1) * M::kPageBytes;
+    uint32_t* odd_rows = reinterpret_cast<uint32_t*>(sm + M::kOdd) + (p & 1) * kPage;
+    const bool ok = next_ok;
+    const uint32_t mine = held.expand_to(page, row, half);
+    const uint32_t both = mine | __shfl_xor_sync(0xffffffffu, mine, 1);
+    if (half == 0) odd_rows[row] = both;
+    if (p + 1 < p1) next_ok = fetch(p + 1);
+    const bool odd = __syncthreads_or(both != 0);  // also: the page before is used up
+    if (!ok) continue;
+    const uint32_t base = smem_u32(page);
+#pragma unroll 1
+    for (int s0 = 0; s0 < kPage; s0 += 2 * kStep) {
+      const int t0 = p * kPage + s0;
+      if (t0 >= warp_most) break;
+      float s[2][NT][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
+      const uint32_t ka = base + (s0 + lane % 16) * M::kRow + lane / 16 * 16;
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        uint32_t x[2][4], y[2][4];
+        ldmatrix4(ka + k * 32, x[0]);
+        ldmatrix4(ka + kStep * M::kRow + k * 32, x[1]);
+        ldmatrix4(qa + k * 32, y[0]);
+        ldmatrix4(qa + 16 * M::kRow + k * 32, y[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma_f16_16816(s[i][n], x[i][0], x[i][1], x[i][2], x[i][3], y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
+      }
+      const bool cut = t0 + 2 * kStep > least;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t pf[NT][2];
+        st.softmax(s[i], t0 + i * kStep, g, cut, pf);  // may rescale the output: weights are used before the next
+        const uint32_t va =
+            base + M::kHalf + (s0 + i * kStep + lane % 8 + lane / 16 * 8) * M::kRow + lane / 8 % 2 * 16;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          uint32_t x[4];
+          ldmatrix4_trans(va + k * 32, x);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16_16816(st.o[n][k], x[0], x[1], x[2], x[3], pf[n][0], pf[n][1]);
+        }
+      }
+      if (odd) {  // a value row that is no number: neither is any column that sees it, in its group's elements
+        for (int r = s0; r < s0 + 2 * kStep; ++r) {
+          const uint32_t bits = odd_rows[r];
+          if (!bits) continue;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if ((bits >> (i / 2) & 1) && p * kPage + r < st.lim[n][kTwo ? 0 : k % 2]) st.o[n][i][k] = NAN;
+        }
+      }
+    }
+  }
+  st.finish_sums();
+  // element of output tile i, row r: position 16 i + r of an expanded row
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < st.NC; ++j) {
+      const int col = tile.first + (warp * 32 + n * 8 + 2 * c + j) / (kTwo ? 2 : 1);
+      if (col >= cols) continue;
+      const size_t at = static_cast<size_t>(q0 + col / a.group) * a.n_head + kh * a.group + col % a.group;
+      const float l = st.l[n][j], inv = l == 0.f ? 0.f : 1.f / l;
+      const int e0 = (g >> 1) + 4 * (g & 1);  // of positions 16 i + g: element 16 i + e0, and 8 further on
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        float x, y;
+        if constexpr (kTwo)
+          x = st.o[n][i][0] + st.o[n][i][1], y = st.o[n][i][2] + st.o[n][i][3];
+        else
+          x = st.o[n][i][j], y = st.o[n][i][2 + j];
+        if (a.n_split == 1) {
+          T* out = static_cast<T*>(a.out) + at * HD + 16 * i + e0;
+          out[0] = from_f<T>(l == 0.f ? 0.f : x * inv);
+          out[8] = from_f<T>(l == 0.f ? 0.f : y * inv);
+        } else {
+          float* out = a.part_o + (at * a.n_split + split) * HD + 16 * i + e0;
+          out[0] = x;
+          out[8] = y;
+        }
+      }
+      if (a.n_split > 1 && g == 0) a.part_ml[at * a.n_split + split] = make_float2(st.m[n][j], l);
+    }
+}
+
+// The splits of each (row, query head), one block each, a thread an element: their maxima decide the weights of
+// their outputs.
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD) k_kv4_join(const AttnArgs a) {
+  const int item = blockIdx.x, row = item / a.n_head;
   const int seq = seq_of_row(a.c.q_start, a.c.n_seq, row);
-  if (seq >= a.c.n_seq || row < __ldg(a.c.q_start + seq) || __ldg(a.c.q_start + seq + 1) > a.c.n_rows) return;
-  const int len = min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage);
+  const bool live = seq < a.c.n_seq && row >= __ldg(a.c.q_start + seq) && __ldg(a.c.q_start + seq + 1) <= a.c.n_rows;
+  const int len = live ? min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // every thread: no end before the splits'
+  if (!live) return;
   const int pages = (len + kPage - 1) / kPage;
   const int n = min(max((pages + a.split_pages - 1) / a.split_pages, 1), a.n_split);
-  const float2* ml = a.part_ml + item * a.n_split;
-  const float* po = a.part_o + item * a.n_split * HD + lane * E;
+  const float2* ml = a.part_ml + static_cast<size_t>(item) * a.n_split;
+  const float* po = a.part_o + static_cast<size_t>(item) * a.n_split * HD + threadIdx.x;
   float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
+  for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
   m = warp_max(m);
   const float base = m == -INFINITY ? 0.f : m;
-  float o[E] = {}, l = 0.f;
-#pragma unroll 4
+  float o = 0.f, l = 0.f;
+#pragma unroll 8
   for (int s = 0; s < n; ++s) {
     const float2 v = __ldcg(ml + s);
     const float f = ex2(v.x - base);
     l += f * v.y;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] += f * __ldcg(po + s * HD + i);
+    o += f * __ldcg(po + static_cast<size_t>(s) * HD);
   }
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    static_cast<T*>(a.out)[item * HD + lane * E + i] = from_f<T>(l == 0.f ? 0.f : o[i] / l);
+  static_cast<T*>(a.out)[static_cast<size_t>(item) * HD + threadIdx.x] = from_f<T>(l == 0.f ? 0.f : o / l);
 }
 
-// How a call's work is cut.  Splits: enough blocks for twice what the 152 SMs hold at once (4 each), of at
-// least two pages, at most 128.  The workspace is sized for the most splits that any length up to max_len can
-// get, so that it does not shrink with a larger max_len.
+// How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 32 columns on
+// average (rows times query heads of a KV head; fp32 queries count twice).  Splits: blocks for one (many columns) or two rounds of
+// what the 152 SMs hold at once, of at least two pages (an even number: they are taken two at a time), at most
+// 128.  The workspace is sized for the most splits that any length up to max_len can get, so that it does not
+// shrink with a larger max_len.
 struct Plan {
+  bool many;
   int tiles, n_split, split_pages;
   size_t o_bytes, bytes;
 };
 Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len, bool two) {
   Plan p{};
-  const int cols = two ? 4 : 8;
-  const long long group = n_head / n_kv_head;
+  const long long group = n_head / n_kv_head, columns = n_rows * group * (two ? 2 : 1);
+  p.many = columns > 32ll * n_seq;
+  const int cols = (p.many ? kManyCols : 8) / (two ? 2 : 1);
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
-  const int want = static_cast<int>(std::min(std::max(1ll, 152 * 8 / (static_cast<long long>(p.tiles) * n_kv_head)), 128ll));
+  const int room = p.many ? 152 * 2 : 152 * 8;
+  const int want = static_cast<int>(std::min(std::max(1ll, room / (static_cast<long long>(p.tiles) * n_kv_head)), 128ll));
   p.split_pages = std::max(2, (pages + want - 1) / want);
+  p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
   const int most = std::min(want, (pages + 1) / 2);
   if (most > 1) {
@@ -582,10 +904,23 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
 
 template <typename T, int HD>
 int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
-  k_kv4_decode<T, HD><<<dim3(p.tiles, a.c.n_kv_head, p.n_split), 128, 0, st>>>(a);
+  void (*const kernel)(AttnArgs) = p.many ? k_kv4_many<T, HD> : k_kv4_decode<T, HD>;
+  const int smem = p.many ? Many<HD>::kBytes : kDecodeSmem<HD>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return S2_ECUDA;
+  kernel<<<dim3(p.tiles, a.c.n_kv_head, p.n_split), 128, smem, st>>>(a);
   if (p.n_split > 1) {
-    const long long warps = static_cast<long long>(a.c.n_rows) * a.n_head;
-    k_kv4_join<T, HD><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.c.n_rows * a.n_head);
+    cfg.blockDim = dim3(HD);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_kv4_join<T, HD>, a) != cudaSuccess) return S2_ECUDA;
   }
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
