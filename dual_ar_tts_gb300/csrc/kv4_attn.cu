@@ -263,9 +263,11 @@ __device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int 
 template <int HD, int NT, bool kTwo>
 struct Rows {
   static constexpr int NC = kTwo ? 1 : 2;  // a lane's logical columns per group of 8
+  static constexpr float kNone = 3e38f;    // `lift` before a column has seen a position
   float o[NT][HD / 16][4];
-  float m[NT][NC], l[NT][NC], f[NT][NC];   // maximum (log2 units), this lane's part of the sum, score factor
-  int lim[NT][NC];                         // positions seen
+  float lift[NT][NC];  // kWeightShift - m, m the running maximum (log2 units): a weight is exp2(score + lift)
+  float l[NT][NC], f[NT][NC];  // this lane's part of the sum, score factor
+  int lim[NT][NC];             // positions seen
 
   __device__ __forceinline__ void init() {
 #pragma unroll
@@ -275,42 +277,70 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) m[n][j] = -INFINITY, l[n][j] = 0.f;
+      for (int j = 0; j < NC; ++j) lift[n][j] = kNone, l[n][j] = 0.f;
     }
+  }
+  __device__ __forceinline__ float maximum(int n, int j) const {
+    return lift[n][j] == kNone ? -INFINITY : kWeightShift - lift[n][j];
   }
 
   // one step at position t0: s becomes the weights, as B operand
   __device__ __forceinline__ void softmax(float (&s)[NT][4], int t0, int g, bool cut, uint32_t (&p)[NT][2]) {
+    if constexpr (kTwo) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float x[2][NC];  // [row g, row g + 8][column]
+      for (int n = 0; n < NT; ++n) s[n][0] += s[n][1], s[n][2] += s[n][3];
+    }
+    if (cut) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if constexpr (kTwo) {
-          x[r][0] = (s[n][2 * r] + s[n][2 * r + 1]) * f[n][0];
-        } else {
-          x[r][0] = s[n][2 * r] * f[n][0];
-          x[r][1] = s[n][2 * r + 1] * f[n][1];
-        }
-        if (cut) {
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int j = 0; j < NC; ++j)
-            if (t0 + g + 8 * r >= lim[n][j]) x[r][j] = -INFINITY;
-        }
+            if (t0 + g + 8 * r >= lim[n][j]) s[n][2 * r + j] = -INFINITY;
+    }
+    float e[NT][2][NC], top = -INFINITY;  // [row g, row g + 8][column]
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        e[n][0][j] = __fmaf_rn(s[n][j], f[n][j], lift[n][j]);
+        e[n][1][j] = __fmaf_rn(s[n][2 + j], f[n][j], lift[n][j]);
+        top = fmaxf(top, fmaxf(e[n][0][j], e[n][1][j]));
       }
-      bool rise = false;
+    if (__any_sync(0xffffffffu, top > kWeightShift + kSlack)) rise(s, e);
 #pragma unroll
-      for (int j = 0; j < NC; ++j) rise = rise || fmaxf(x[0][j], x[1][j]) > m[n][j] + kSlack;
-      if (__any_sync(0xffffffffu, rise)) {
+    for (int n = 0; n < NT; ++n) {
+      float w[2][2];
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          float top = fmaxf(x[0][j], x[1][j]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float mn = fmaxf(m[n][j], top);
-          const float keep = ex2(m[n][j] - (mn == -INFINITY ? 0.f : mn));
-          m[n][j] = mn;
+      for (int j = 0; j < NC; ++j) {
+        w[0][j] = ex2(e[n][0][j]);
+        w[1][j] = ex2(e[n][1][j]);
+        l[n][j] += w[0][j] + w[1][j];
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (kTwo) w[r][1] = w[r][0] - round_f16(w[r][0]);
+        p[n][r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0], w[r][1])));
+      }
+    }
+  }
+
+  // the maxima raised to the step's, output and sums rescaled
+  __device__ __forceinline__ void rise(const float (&s)[NT][4], float (&e)[NT][2][NC]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const float x0 = s[n][j] * f[n][j], x1 = s[n][2 + j] * f[n][j];
+        float top = fmaxf(x0, x1);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float m = maximum(n, j), mn = fmaxf(m, top);
+        if (mn > -INFINITY) {  // the same in all lanes of the column
+          const float keep = ex2(m - mn);
+          lift[n][j] = kWeightShift - mn;
           l[n][j] *= keep;
 #pragma unroll
           for (int i = 0; i < HD / 16; ++i) {
@@ -321,21 +351,9 @@ struct Rows {
             }
           }
         }
+        e[n][0][j] = __fmaf_rn(s[n][j], f[n][j], lift[n][j]);
+        e[n][1][j] = __fmaf_rn(s[n][2 + j], f[n][j], lift[n][j]);
       }
-      float w[2][2];
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const float base = m[n][j] == -INFINITY ? 0.f : m[n][j] - kWeightShift;
-        w[0][j] = ex2(x[0][j] - base);
-        w[1][j] = ex2(x[1][j] - base);
-        l[n][j] += w[0][j] + w[1][j];
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if constexpr (kTwo) w[r][1] = w[r][0] - round_f16(w[r][0]);
-        p[n][r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0], w[r][1])));
-      }
-    }
   }
 
   // a value row of the step that is no number: every column that sees it is none either, in its group's elements
@@ -366,18 +384,20 @@ struct Rows {
   }
 };
 
-// Where a tile of columns lies: its sequence and the first of its columns there.  Tiles are counted over the
-// sequences in order; -1 where there are fewer.
+// Where a tile of columns lies: its sequence, that one's rows q0 .. q1 - 1 and length, and the first of the tile's
+// columns there.  Tiles are counted over the sequences in order; seq -1 where there are fewer.  Bounds and lengths
+// come in one round of loads.
 struct Tile {
-  int seq, first;
+  int seq, first, q0, q1, len;
 };
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ q_start, int n_seq, int group, int cols, int t) {
+__device__ __forceinline__ Tile find_tile(const s2_kv4& k, int group, int cols, int t) {
   const int lane = threadIdx.x % 32;
   int before = 0;
-  for (int base = 0; base < n_seq; base += 32) {
+  for (int base = 0; base < k.n_seq; base += 32) {
     const int s = base + lane;
-    int tiles = 0;
-    if (s < n_seq) tiles = (max(__ldg(q_start + s + 1) - __ldg(q_start + s), 0) * group + cols - 1) / cols;
+    int q0 = 0, q1 = 0, len = 0;
+    if (s < k.n_seq) q0 = __ldg(k.q_start + s), q1 = __ldg(k.q_start + s + 1), len = __ldg(k.lengths + s);
+    const int tiles = (max(q1 - q0, 0) * group + cols - 1) / cols;
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -387,11 +407,12 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ q_start, i
     const unsigned hit = __ballot_sync(0xffffffffu, before + upto > t);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      return {base + l, (t - before - __shfl_sync(0xffffffffu, upto - tiles, l)) * cols};
+      return {base + l, (t - before - __shfl_sync(0xffffffffu, upto - tiles, l)) * cols,
+              __shfl_sync(0xffffffffu, q0, l), __shfl_sync(0xffffffffu, q1, l), __shfl_sync(0xffffffffu, len, l)};
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  return {-1, 0};
+  return {-1, 0, 0, 0, 0};
 }
 
 // pages of a sequence's table, 32 at a time in the lanes of a warp
@@ -429,15 +450,15 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
   const int kh = blockIdx.y, split = blockIdx.z;
-  const Tile tile = find_tile(a.c.q_start, a.c.n_seq, a.group, CT, blockIdx.x);
+  const Tile tile = find_tile(a.c, a.group, CT, blockIdx.x);
   if (tile.seq < 0) return;
-  const int q0 = __ldg(a.c.q_start + tile.seq), q1 = __ldg(a.c.q_start + tile.seq + 1);
+  const int q0 = tile.q0, q1 = tile.q1;
   if (q0 < 0 || q1 > a.c.n_rows) {
     if (threadIdx.x == 0) kv4_bad(a.c.status);
     return;
   }
   const int cols = (q1 - q0) * a.group;
-  int len = __ldg(a.c.lengths + tile.seq);
+  int len = tile.len;
   const int over = len - (q1 - q0);  // row i sees over + i + 1 positions
   if (len > a.c.table_cols * kPage) {
     if (threadIdx.x == 0) kv4_bad(a.c.status);
@@ -447,24 +468,7 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   const int pages = (len + kPage - 1) / kPage;
   const int p0 = split * a.split_pages, p1 = split == a.n_split - 1 ? pages : min(pages, p0 + a.split_pages);
   if (p0 >= p1 && split > 0) return;
-
-  Rows<HD, 1, kTwo> st;
-  st.init();
-  uint32_t qf[1][HD / 8];
-  {
-    const int col = tile.first + (kTwo ? g / 2 : g);
-    const bool live = col < cols;
-    const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
-    const float down = load_q<T, HD>(static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD, live,
-                                     kTwo && (g & 1), c, qf[0]);
-#pragma unroll
-    for (int j = 0; j < st.NC; ++j) {
-      const int mine = tile.first + (kTwo ? c : 2 * c + j);
-      st.f[0][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * a.scale * kLog2e;
-      st.lim[0][j] = mine < cols ? min(over + mine / a.group + 1, len) : 0;
-    }
-  }
-  const int first_lim = min(over + tile.first / a.group + 1, len);  // the least that a live column sees
+  const bool whole = a.n_split == 1 || pages <= a.split_pages;  // nothing to join
 
   uint8_t* ring = sm + warp * kDepth * S::kBytes;
   Pages pg{a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols, pages, a.c.n_pages};
@@ -485,6 +489,25 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < kDepth - 1; ++i) issue(i);
+
+  Rows<HD, 1, kTwo> st;
+  st.init();
+  uint32_t qf[1][HD / 8];
+  {
+    const int col = tile.first + (kTwo ? g / 2 : g);
+    const bool live = col < cols;
+    const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
+    const float down = load_q<T, HD>(static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD, live,
+                                     kTwo && (g & 1), c, qf[0]);
+#pragma unroll
+    for (int j = 0; j < st.NC; ++j) {
+      const int mine = tile.first + (kTwo ? c : 2 * c + j);
+      st.f[0][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * a.scale * kLog2e;
+      st.lim[0][j] = mine < cols ? min(over + mine / a.group + 1, len) : 0;
+    }
+  }
+  const int first_lim = min(over + tile.first / a.group + 1, len);  // the least that a live column sees
+
   for (int turn = 0; turn < turns; ++turn) {
     issue(turn + kDepth - 1);
     cp_async_wait_group<kDepth - 1>();
@@ -534,7 +557,7 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
       }
     }
     if (g == 0) {
-      jm[(warp * CT + col) * 2] = st.m[0][j];
+      jm[(warp * CT + col) * 2] = st.maximum(0, j);
       jm[(warp * CT + col) * 2 + 1] = st.l[0][j];
     }
   }
@@ -554,7 +577,7 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
       l += f * jm[(w * CT + col) * 2 + 1];
     }
     const size_t at = static_cast<size_t>(q0 + mine / a.group) * a.n_head + kh * a.group + mine % a.group;
-    if (a.n_split == 1) {
+    if (whole) {
       static_cast<T*>(a.out)[at * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
     } else {
       a.part_o[(at * a.n_split + split) * HD + e] = o;
@@ -649,15 +672,15 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
   extern __shared__ __align__(16) uint8_t sm[];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
   const int kh = blockIdx.y, split = blockIdx.z;
-  const Tile tile = find_tile(a.c.q_start, a.c.n_seq, a.group, CT, blockIdx.x);
+  const Tile tile = find_tile(a.c, a.group, CT, blockIdx.x);
   if (tile.seq < 0) return;
-  const int q0 = __ldg(a.c.q_start + tile.seq), q1 = __ldg(a.c.q_start + tile.seq + 1);
+  const int q0 = tile.q0, q1 = tile.q1;
   if (q0 < 0 || q1 > a.c.n_rows) {
     if (threadIdx.x == 0) kv4_bad(a.c.status);
     return;
   }
   const int cols = (q1 - q0) * a.group;
-  int len = __ldg(a.c.lengths + tile.seq);
+  int len = tile.len;
   const int over = len - (q1 - q0);  // row i sees over + i + 1 positions
   if (len > a.c.table_cols * kPage) {
     if (threadIdx.x == 0) kv4_bad(a.c.status);
@@ -668,17 +691,35 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
   const int p0 = split * a.split_pages;
   int p1 = split == a.n_split - 1 ? pages : min(pages, p0 + a.split_pages);
   if (p0 >= p1 && split > 0) return;
+  const bool whole = a.n_split == 1 || pages <= a.split_pages;  // nothing to join
   // no column of the tile sees more than its last one
   const int last = min(tile.first + CT, cols) - 1;
   const int most = min(over + last / a.group + 1, len);
   p1 = min(p1, (max(most, 0) + kPage - 1) / kPage);
 
+  const int row = threadIdx.x / 2, half = threadIdx.x % 2;
+  const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
+  const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
+  HalfRow<HD> held;
+  // page p into registers (zeros for rows behind the sequence); whether it is there at all
+  auto fetch = [&](int p) {
+    const int id = __ldg(table + p);
+    const bool ok = id >= 0 && id < a.c.n_pages;
+    if (!ok && threadIdx.x == 0) kv4_bad(a.c.status);
+    if (ok && p * kPage + row < len)
+      held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, row, half);
+    else
+      held.zero();
+    return ok;
+  };
+  bool next_ok = p0 < p1 && fetch(p0);
+
   // queries: a thread a column
   {
     const int col = tile.first + (kTwo ? threadIdx.x / 2 : threadIdx.x);
     const bool live = col < cols;
-    const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
-    const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD;
+    const int at = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
+    const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(at) * a.n_head + h) * HD;
     constexpr int kPer = 16 / sizeof(T);
     float top = 0.f;
     for (int i = 0; i < HD / kPer; ++i) {
@@ -712,22 +753,6 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
     reinterpret_cast<float*>(sm + M::kF)[threadIdx.x] = ldexpf(1.f, -e) * a.scale * kLog2e;
     reinterpret_cast<int*>(sm + M::kLim)[threadIdx.x] = live ? min(over + col / a.group + 1, len) : 0;
   }
-  const int row = threadIdx.x / 2, half = threadIdx.x % 2;
-  const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
-  const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
-  HalfRow<HD> held;
-  // page p into registers (zeros for rows behind the sequence); whether it is there at all
-  auto fetch = [&](int p) {
-    const int id = __ldg(table + p);
-    const bool ok = id >= 0 && id < a.c.n_pages;
-    if (!ok && threadIdx.x == 0) kv4_bad(a.c.status);
-    if (ok && p * kPage + row < len)
-      held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, row, half);
-    else
-      held.zero();
-    return ok;
-  };
-  bool next_ok = p0 < p1 && fetch(p0);
   __syncthreads();
   Rows<HD, NT, kTwo> st;
   st.init();
@@ -828,7 +853,7 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
           x = st.o[n][i][0] + st.o[n][i][1], y = st.o[n][i][2] + st.o[n][i][3];
         else
           x = st.o[n][i][j], y = st.o[n][i][2 + j];
-        if (a.n_split == 1) {
+        if (whole) {
           T* out = static_cast<T*>(a.out) + at * HD + 16 * i + e0;
           out[0] = from_f<T>(l == 0.f ? 0.f : x * inv);
           out[8] = from_f<T>(l == 0.f ? 0.f : y * inv);
@@ -838,44 +863,56 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
           out[8] = y;
         }
       }
-      if (a.n_split > 1 && g == 0) a.part_ml[at * a.n_split + split] = make_float2(st.m[n][j], l);
+      if (!whole && g == 0) a.part_ml[at * a.n_split + split] = make_float2(st.maximum(n, j), l);
     }
 }
 
-// The splits of each (row, query head), one block each, a thread an element: their maxima decide the weights of
-// their outputs.
-template <typename T, int HD>
-__global__ void __launch_bounds__(HD) k_kv4_join(const AttnArgs a) {
-  const int item = blockIdx.x, row = item / a.n_head;
+// The splits of each (row, query head): one block each, a thread an element of every kJoinParts-th split (4 parts
+// for more than 16 splits: one row over 30000 positions 36 -> 22 us; 1 for fewer, of which there are many rows).
+// The splits' maxima decide the weights of their outputs; parts are added in order.
+template <typename T, int HD, int kJoinParts>
+__global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) {
+  __shared__ float so[kJoinParts][HD], sl[kJoinParts];
+  const int item = blockIdx.x, row = item / a.n_head, e = threadIdx.x % HD, part = threadIdx.x / HD;
   const int seq = seq_of_row(a.c.q_start, a.c.n_seq, row);
   const bool live = seq < a.c.n_seq && row >= __ldg(a.c.q_start + seq) && __ldg(a.c.q_start + seq + 1) <= a.c.n_rows;
   const int len = live ? min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // every thread: no end before the splits'
   if (!live) return;
   const int pages = (len + kPage - 1) / kPage;
-  const int n = min(max((pages + a.split_pages - 1) / a.split_pages, 1), a.n_split);
+  const int n = min((pages + a.split_pages - 1) / a.split_pages, a.n_split);
+  if (n <= 1) return;  // written by its one block
   const float2* ml = a.part_ml + static_cast<size_t>(item) * a.n_split;
-  const float* po = a.part_o + static_cast<size_t>(item) * a.n_split * HD + threadIdx.x;
+  const float* po = a.part_o + static_cast<size_t>(item) * a.n_split * HD + e;
   float m = -INFINITY;
   for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
   m = warp_max(m);
   const float base = m == -INFINITY ? 0.f : m;
   float o = 0.f, l = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) {
+#pragma unroll 4
+  for (int s = part; s < n; s += kJoinParts) {
     const float2 v = __ldcg(ml + s);
     const float f = ex2(v.x - base);
     l += f * v.y;
     o += f * __ldcg(po + static_cast<size_t>(s) * HD);
   }
-  static_cast<T*>(a.out)[static_cast<size_t>(item) * HD + threadIdx.x] = from_f<T>(l == 0.f ? 0.f : o / l);
+  so[part][e] = o;
+  if (e == 0) sl[part] = l;
+  __syncthreads();
+  if (part > 0) return;
+  o = l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinParts; ++i) o += so[i][e], l += sl[i];
+  static_cast<T*>(a.out)[static_cast<size_t>(item) * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
 }
 
 // How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 32 columns on
-// average (rows times query heads of a KV head; fp32 queries count twice).  Splits: blocks for one (many columns) or two rounds of
-// what the 152 SMs hold at once, of at least two pages (an even number: they are taken two at a time), at most
-// 128.  The workspace is sized for the most splits that any length up to max_len can get, so that it does not
-// shrink with a larger max_len.
+// average (rows times query heads of a KV head; fp32 queries count twice): 8 sequences of 4000 positions take 34 us
+// against 55 at 16 columns, 43 against 56 at 32.  Splits: the blocks that the 152 SMs hold at once (4 an SM; of the
+// kernel for many columns 2), twice that where there are many items of what may be different lengths (32 of
+// 512..4096: 32 us against 46), three times for many columns; of at least two pages (an even number: they are taken
+// two at a time), at most 128.  The workspace is sized for the most splits that any length up to max_len can get,
+// so that it does not shrink with a larger max_len.
 struct Plan {
   bool many;
   int tiles, n_split, split_pages;
@@ -888,16 +925,17 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   const int cols = (p.many ? kManyCols : 8) / (two ? 2 : 1);
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
-  const int room = p.many ? 152 * 2 : 152 * 8;
-  const int want = static_cast<int>(std::min(std::max(1ll, room / (static_cast<long long>(p.tiles) * n_kv_head)), 128ll));
+  const long long items = static_cast<long long>(p.tiles) * n_kv_head;
+  const int room = p.many ? 152 * 6 : items < 152 ? 152 * 4 : 152 * 8;
+  const int want = static_cast<int>(std::min(std::max(1ll, room / items), 128ll));
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
   const int most = std::min(want, (pages + 1) / 2);
   if (most > 1) {
-    const size_t items = static_cast<size_t>(n_rows) * n_head * most;
-    p.o_bytes = items * head_dim * 4;
-    p.bytes = p.o_bytes + items * 8;
+    const size_t parts = static_cast<size_t>(n_rows) * n_head * most;
+    p.o_bytes = parts * head_dim * 4;
+    p.bytes = p.o_bytes + parts * 8;
   }
   return p;
 }
@@ -913,14 +951,15 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
   if (p.n_split > 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.c.n_rows * a.n_head);
-    cfg.blockDim = dim3(HD);
+    cfg.blockDim = dim3(p.n_split > 16 ? 4 * HD : HD);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_kv4_join<T, HD>, a) != cudaSuccess) return S2_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, p.n_split > 16 ? k_kv4_join<T, HD, 4> : k_kv4_join<T, HD, 1>, a) != cudaSuccess)
+      return S2_ECUDA;
   }
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
