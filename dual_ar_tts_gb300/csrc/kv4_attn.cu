@@ -22,6 +22,7 @@
 #include "kv4.cuh"
 #include "ptx.cuh"
 #include "s2_internal.h"
+#include "tc05.cuh"
 
 namespace s2 {
 namespace {
@@ -134,10 +135,22 @@ __device__ __forceinline__ void copy_half(uint8_t* st, const uint8_t* block, int
   }
 }
 
+// A row's scores are computed from its query times `up`, and multiplied by `down`: the largest element goes to
+// 2^13 .. 2^14, exact and far from fp16's ends.  `down` is positive (a negative scale turns the query, a scale of 0
+// makes it 0), so that a masked score stays -inf.
+struct QueryScale {
+  float up, down;
+  __device__ __forceinline__ QueryScale(float top, float scale) {
+    const int e = top > 0.f && isfinite(top) ? min(13 - ilogbf(top), 126) : 0;
+    up = scale == 0.f ? 0.f : ldexpf(scale < 0.f ? -1.f : 1.f, e);
+    down = scale == 0.f ? 1.f : fmaxf(ldexpf(1.f, -e) * (fabsf(scale) * kLog2e), 1e-37f);
+  }
+};
+
 // The query columns of a warp as B operand: lane (g = lane / 4, c = lane % 4) holds column g of each
 // group of 8 at the elements that lane c expands of a key row.
 template <typename T, int HD>
-__device__ __forceinline__ float load_q(const T* q, bool live, bool low, int c, uint32_t (&f)[HD / 8]) {
+__device__ __forceinline__ float load_q(const T* q, bool live, bool low, float scale, int c, uint32_t (&f)[HD / 8]) {
   constexpr int E = HD / 4;
   float x[E], top = 0.f;
 #pragma unroll
@@ -147,21 +160,19 @@ __device__ __forceinline__ float load_q(const T* q, bool live, bool low, int c, 
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  int e = 0;  // the largest element to 2^13 .. 2^14: exact, and far from fp16's ends
-  if (top > 0.f && isfinite(top)) e = min(13 - ilogbf(top), 126);
-  const float up = ldexpf(1.f, e);
+  const QueryScale qs(top, scale);
 #pragma unroll
   for (int j = 0; j < E / 8; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float a = x[8 * j + i] * up, b = x[8 * j + i + 4] * up;
+      float a = x[8 * j + i] * qs.up, b = x[8 * j + i + 4] * qs.up;
       if (low) {
         a -= round_f16(a);
         b -= round_f16(b);
       }
       f[4 * j + i] = h2_bits(__floats2half2_rn(a, b));
     }
-  return ldexpf(1.f, -e);
+  return qs.down;
 }
 
 // S^T of one step: scores of rows g, g + 8 at columns 2c, 2c + 1 of each group of 8
@@ -498,11 +509,11 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
     const bool live = col < cols;
     const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
     const float down = load_q<T, HD>(static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD, live,
-                                     kTwo && (g & 1), c, qf[0]);
+                                     kTwo && (g & 1), a.scale, c, qf[0]);
 #pragma unroll
     for (int j = 0; j < st.NC; ++j) {
       const int mine = tile.first + (kTwo ? c : 2 * c + j);
-      st.f[0][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * a.scale * kLog2e;
+      st.f[0][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
       st.lim[0][j] = mine < cols ? min(over + mine / a.group + 1, len) : 0;
     }
   }
@@ -586,93 +597,147 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   }
 }
 
-// ---- many columns: a block takes 128 columns (fp32 queries: 64, two each) of one KV head, a warp 32 of them.
-// Every page is expanded once for all of them, into fp16 rows in shared memory (double-buffered; its codes wait in
-// registers while the page before is used), and the products read it with ldmatrix, 32 positions at a time.
-// Within a row the elements of eight codes lie in the order 0 4 1 5 2 6 3 7, queries alike.
-constexpr int kManyCols = 128, kManyTiles = 4;
-template <int HD>
-struct Many {
-  static constexpr int kRow = 2 * HD + 16;  // bytes of an expanded row
-  static constexpr int kHalf = kPage * kRow, kPageBytes = 2 * kHalf;
-  static constexpr int kQ = 0, kKv = kManyCols * kRow, kF = kKv + 2 * kPageBytes, kLim = kF + kManyCols * 4,
-                       kOdd = kLim + kManyCols * 4, kBytes = kOdd + 2 * kPage * 4;
+// ---- many columns: a block takes 128 columns of one KV head, each a row of tcgen05 products, a page at a time:
+//   S[128][64] = Q[128][hd] K[64][hd]^T      Q and K in shared memory
+//   O[128][hd] += P[128][64] V[64][hd]       P in tensor memory, V^T in shared memory
+// A thread has one column: its scores, its maximum, its sum and its row of the output, all in tensor memory lanes
+// of its own, so the softmax has no shuffles.  Every page is expanded once for all columns (each thread half a key
+// row, and 32 values of two positions); its codes wait in registers while the page before is used.  fp32 queries
+// are two fp16 terms, and so are their weights: the products run twice, into the same sums.
+// Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
+// queries alike.  Two blocks an SM overlap one's expanding and exponentials with the other's products.
+constexpr int kTcCols = 128;
+template <int HD, int TN>
+struct Tc {
+  static constexpr int kAtoms = HD / 64;                // 128-byte columns of Q and K
+  static constexpr int kQAtom = kTcCols * 128, kKAtom = kPage * 128;
+  static constexpr int kQ = 0, kK = kQ + TN * kAtoms * kQAtom, kV = kK + kAtoms * kKAtom, kVBuf = HD * 128,
+                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 4 * kPage, kBytes = kBars + 64 + 1024;
+  // tensor memory columns
+  static constexpr uint32_t kO = 0, kS = HD, kP = kS + kPage, kCols = 256;
+  static_assert(kP + TN * 32 <= kCols, "tensor memory");
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+// A wait that gives up after a second or so (a few hundred ns a try).
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 22); ++i)
+    if (mbar_test(bar, parity)) return true;
+  return false;
 }
 
-// What a thread holds of a page: half a row of key and value codes with their parameters.
+// Warp-wide: 32 consecutive tensor memory columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// fp16 operands, fp32 sums, both K-major (the format fields of fp16 are zero)
+constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// What a thread holds of a page: half a row of keys, and words 32 w / 8 .. of the values of positions 2l, 2l + 1
+// (hd 128: 16 bytes, hd 64: 8), with their parameters.
 template <int HD>
-struct HalfRow {
-  static constexpr int kU = HD / 64;  // 16-byte units
-  uint4 k[kU], v[kU];
-  uint32_t kp[kU], vp[kU];
-  __device__ __forceinline__ void load(const uint8_t* block, int row, int half) {
+struct PageCodes {
+  static constexpr int kU = HD / 64;  // 16-byte units of half a key row; 8-byte units of values
+  uint4 k[kU];
+  uint32_t kp[kU], vp[2];
+  uint2 v[2][kU];
+  // `rows` of the page are in the sequence
+  __device__ __forceinline__ void load(const uint8_t* block, int rows) {
     using B = Kv4Block<HD>;
+    const int row = threadIdx.x / 2, half = threadIdx.x % 2, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint8_t* p = block + row * B::kRow + half * (kU * 16);
     const uint8_t* q = block + kPage * B::kRow + row * B::kPar + half * (kU * 4);
+    const bool live = row < rows;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      k[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      v[i] = __ldg(reinterpret_cast<const uint4*>(p + B::kHalf) + i);
-      kp[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
-      vp[i] = __ldg(reinterpret_cast<const uint32_t*>(q + B::kHalf) + i);
+      k[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+      kp[i] = live ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0;
+    }
+    const uint8_t* vb = block + B::kHalf;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r = 2 * lane + t;
+      const bool in = r < rows;
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        v[t][i] = in ? __ldg(reinterpret_cast<const uint2*>(vb + r * B::kRow + warp * (kU * 8)) + i) : make_uint2(0, 0);
+      vp[t] = in ? __ldg(reinterpret_cast<const uint32_t*>(vb + kPage * B::kRow + r * B::kPar) + warp * HD / 128) : 0;
     }
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kU; ++i) k[i] = v[i] = make_uint4(0, 0, 0, 0), kp[i] = vp[i] = 0;
-  }
-  // Expands into the row of a page buffer; values whose parameters are no numbers become zeros.  Returns the bits
-  // of the groups where they did (within the row).
-  __device__ __forceinline__ uint32_t expand_to(uint8_t* page, int row, int half) const {
-    uint32_t odd = 0;
+  // Into the operands' layouts.  Values whose parameters are no numbers become zeros; returns whether there are.
+  __device__ __forceinline__ bool expand_to(uint8_t* kt, uint8_t* vt, uint16_t* odd_rows) {
+    const int row = threadIdx.x / 2, half = threadIdx.x % 2, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = kU == 2 ? i ^ half : i;  // the halves write different banks
-      const uint4 kc = kU == 2 && half ? k[i ^ (kU - 1)] : k[i], vc = kU == 2 && half ? v[i ^ (kU - 1)] : v[i];
+      const uint4 kc = kU == 2 && half ? k[i ^ (kU - 1)] : k[i];
       const uint32_t a = kU == 2 && half ? kp[i ^ (kU - 1)] : kp[i];
-      uint32_t b = kU == 2 && half ? vp[i ^ (kU - 1)] : vp[i];
-      if ((b & 0x7c00u) == 0x7c00u || (b & 0x7c000000u) == 0x7c000000u) {
-        odd |= 1u << (half * kU + u);
-        b = 0;
-      }
-      const Pair pk(a, a), pv(b, b);
-      uint8_t* to = page + row * Many<HD>::kRow + (half * kU + u) * 64;
-      const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+      const Pair pk(a, a);
+      const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+      // elements 32 (half kU + u) ..: hd 128: atom `half`, chunks 4u ..; hd 64: the one atom, chunks 4 half ..
+      uint8_t* to = kt + (kU == 2 ? half * (kPage * 128) : 0) + row * 128;
+      const int chunk = kU == 2 ? 4 * u : 4 * half;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t x[4], y[4];
+        uint32_t x[4];
         expand(kw[j], pk, x);
-        expand(vw[j], pv, y);
-        *reinterpret_cast<uint4*>(to + j * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(to + Many<HD>::kHalf + j * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + (((chunk + j) ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
-    return odd;
+    uint16_t odd = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if ((vp[t] & 0x7c00u) == 0x7c00u || (vp[t] & 0x7c000000u) == 0x7c000000u) {
+        odd |= 1u << (8 * t);
+        vp[t] = 0;
+      }
+    odd_rows[warp * 32 + lane] = odd;
+    const Pair pv(vp[0], vp[1]);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const uint32_t w0[2] = {v[0][i].x, v[0][i].y}, w1[2] = {v[1][i].x, v[1][i].y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[4];
+          expand(__byte_perm(w0[j], w1[j], h ? 0x7632 : 0x5410), pv, x);
+          const int dim = warp * (kU * 16) + i * 16 + j * 8 + h * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint32_t*>(vt + (dim + e) * 128 + (((lane / 4) ^ ((dim + e) & 7)) * 16) + lane % 4 * 4) = x[e];
+        }
+    }
+    return odd != 0;
   }
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
-  constexpr bool kTwo = sizeof(T) == 4;
-  constexpr int CT = kTwo ? kManyCols / 2 : kManyCols;
-  constexpr int NT = kManyTiles;
+__global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
+  constexpr int TN = sizeof(T) == 4 ? 2 : 1;
   using B = Kv4Block<HD>;
-  using M = Many<HD>;
-  extern __shared__ __align__(16) uint8_t sm[];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
+  using M = Tc<HD, TN>;
+  extern __shared__ __align__(16) uint8_t smraw[];
+  uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::kBars);  // scores, output
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 2);
+  uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [warp][position pair], a byte a position
+  const int warp = threadIdx.x / 32;
   const int kh = blockIdx.y, split = blockIdx.z;
-  const Tile tile = find_tile(a.c, a.group, CT, blockIdx.x);
+  const Tile tile = find_tile(a.c, a.group, kTcCols, blockIdx.x);
   if (tile.seq < 0) return;
   const int q0 = tile.q0, q1 = tile.q1;
   if (q0 < 0 || q1 > a.c.n_rows) {
@@ -692,179 +757,224 @@ __global__ void __launch_bounds__(128, 2) k_kv4_many(const AttnArgs a) {
   int p1 = split == a.n_split - 1 ? pages : min(pages, p0 + a.split_pages);
   if (p0 >= p1 && split > 0) return;
   const bool whole = a.n_split == 1 || pages <= a.split_pages;  // nothing to join
-  // no column of the tile sees more than its last one
-  const int last = min(tile.first + CT, cols) - 1;
-  const int most = min(over + last / a.group + 1, len);
-  p1 = min(p1, (max(most, 0) + kPage - 1) / kPage);
+  // no column of the tile sees more than its last one, nor less than its first
+  const int last = min(tile.first + kTcCols, cols) - 1;
+  p1 = min(p1, (max(min(over + last / a.group + 1, len), 0) + kPage - 1) / kPage);
+  const int least = min(over + tile.first / a.group + 1, len);
 
-  const int row = threadIdx.x / 2, half = threadIdx.x % 2;
   const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
   const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
-  HalfRow<HD> held;
-  // page p into registers (zeros for rows behind the sequence); whether it is there at all
-  auto fetch = [&](int p) {
-    const int id = __ldg(table + p);
-    const bool ok = id >= 0 && id < a.c.n_pages;
-    if (!ok && threadIdx.x == 0) kv4_bad(a.c.status);
-    if (ok && p * kPage + row < len)
-      held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, row, half);
-    else
-      held.zero();
-    return ok;
+  PageCodes<HD> held;
+  int next = p0;
+  // the codes of the next page that is there; `next` ends at p1
+  auto fetch = [&] {
+    for (; next < p1; ++next) {
+      const int id = __ldg(table + next);
+      if (id >= 0 && id < a.c.n_pages) {
+        held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, len - next * kPage);
+        return;
+      }
+      if (threadIdx.x == 0) kv4_bad(a.c.status);
+    }
   };
-  bool next_ok = p0 < p1 && fetch(p0);
-
-  // queries: a thread a column
+  fetch();
+  if (threadIdx.x == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tbase, M::kCols);
+    tmem_relinquish();
+  }
+  // this thread's column
+  const int col = tile.first + threadIdx.x;
+  const bool live = col < cols;
+  const size_t at = static_cast<size_t>(q0 + (live ? col / a.group : 0)) * a.n_head + kh * a.group + (live ? col % a.group : 0);
+  const int lim = live ? min(over + col / a.group + 1, len) : 0;
+  float factor;
   {
-    const int col = tile.first + (kTwo ? threadIdx.x / 2 : threadIdx.x);
-    const bool live = col < cols;
-    const int at = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
-    const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(at) * a.n_head + h) * HD;
+    const T* q = static_cast<const T*>(a.q) + at * HD;
     constexpr int kPer = 16 / sizeof(T);
     float top = 0.f;
+#pragma unroll 4
     for (int i = 0; i < HD / kPer; ++i) {
       const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
       const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) top = fmaxf(top, fabsf(to_f(e[k])));
     }
-    int e = 0;  // as load_q
-    if (live && top > 0.f && isfinite(top)) e = min(13 - ilogbf(top), 126);
-    const float up = live ? ldexpf(1.f, e) : 0.f;
-    uint8_t* to = sm + M::kQ + threadIdx.x * M::kRow;
+    const QueryScale qs(live ? top : 0.f, a.scale);
+    factor = qs.down;
+#pragma unroll 2
     for (int i = 0; i < HD / 8; ++i) {
       uint4 u[sizeof(T) / 2];
 #pragma unroll
       for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
         u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i * (sizeof(T) / 2) + k);
       const T* v = reinterpret_cast<const T*>(u);
-      uint32_t r[4];
+      float x[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float x = live ? to_f(v[k]) * up : 0.f, y = live ? to_f(v[k + 4]) * up : 0.f;
-        if (kTwo && (threadIdx.x & 1)) {
-          x -= round_f16(x);
-          y -= round_f16(y);
+      for (int k = 0; k < 8; ++k) x[k] = live ? to_f(v[k]) * qs.up : 0.f;
+      uint8_t* to = sm + M::kQ + i / 8 * M::kQAtom + threadIdx.x * 128 + (((i % 8) ^ (threadIdx.x & 7)) * 16);
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          r[k] = h2_bits(__floats2half2_rn(x[k], x[k + 4]));
+          x[k] -= round_f16(x[k]);
+          x[k + 4] -= round_f16(x[k + 4]);
         }
-        r[k] = h2_bits(__floats2half2_rn(x, y));
+        *reinterpret_cast<uint4*>(to + t * M::kAtoms * M::kQAtom) = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    reinterpret_cast<float*>(sm + M::kF)[threadIdx.x] = ldexpf(1.f, -e) * a.scale * kLog2e;
-    reinterpret_cast<int*>(sm + M::kLim)[threadIdx.x] = live ? min(over + col / a.group + 1, len) : 0;
   }
+  tc_fence_before();
   __syncthreads();
-  Rows<HD, NT, kTwo> st;
-  st.init();
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < st.NC; ++j) {
-      const int col = warp * 32 + n * 8 + 2 * c + j;
-      st.f[n][j] = reinterpret_cast<float*>(sm + M::kF)[col];
-      st.lim[n][j] = reinterpret_cast<int*>(sm + M::kLim)[col];
-    }
-  // the least and the most that this warp's columns see
-  const int w0 = tile.first + warp * (CT / 4), w1 = min(w0 + CT / 4, cols) - 1;
-  const int least = min(over + w0 / a.group + 1, len), warp_most = w0 < cols ? min(over + w1 / a.group + 1, len) : 0;
-  const uint32_t qa = smem_u32(sm + M::kQ) + (warp * 32 + lane / 16 * 8 + lane % 8) * M::kRow + (lane / 8 % 2) * 16;
+  tc_fence_after();
+  const uint32_t tm = *tbase, tlane = tm + (static_cast<uint32_t>(warp * 32) << 16);
 
-  for (int p = p0; p < p1; ++p) {
-    uint8_t* page = sm + M::kKv + (p & 1) * M::kPageBytes;
-    uint32_t* odd_rows = reinterpret_cast<uint32_t*>(sm + M::kOdd) + (p & 1) * kPage;
-    const bool ok = next_ok;
-    const uint32_t mine = held.expand_to(page, row, half);
-    const uint32_t both = mine | __shfl_xor_sync(0xffffffffu, mine, 1);
-    if (half == 0) odd_rows[row] = both;
-    if (p + 1 < p1) next_ok = fetch(p + 1);
-    const bool odd = __syncthreads_or(both != 0);  // also: the page before is used up
-    if (!ok) continue;
-    const uint32_t base = smem_u32(page);
-#pragma unroll 1
-    for (int s0 = 0; s0 < kPage; s0 += 2 * kStep) {
-      const int t0 = p * kPage + s0;
-      if (t0 >= warp_most) break;
-      float s[2][NT][4];
+  float lift = 3e38f, l = 0.f;  // as Rows
+  uint32_t poison = 0;          // groups of the output that are no numbers
+  bool ok = true;
+  int done = 0;                 // pages used
+  while (next < p1) {
+    const int p = next;
+    uint8_t* vt = sm + M::kV + (done & 1) * M::kVBuf;  // the products of two pages ago are finished
+    const bool mine = held.expand_to(sm + M::kK, vt, odd_rows);
+    fence_proxy_async_smem();
+    const bool odd = __syncthreads_or(mine);
+    if (threadIdx.x == 0) {
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int t = 0; t < TN; ++t)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma(tm + M::kS, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
+                 desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
+                 t > 0 || k > 0);
+      tc_commit(bars);
+    }
+    ++next;
+    fetch();
+    ok = ok && wait_short(bars, done & 1);
+    __syncwarp();
+    tc_fence_after();
+    float s[kPage];
+    tmem_ld32(tlane + M::kS, *reinterpret_cast<float(*)[32]>(s));
+    tmem_ld32(tlane + M::kS + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+    if ((p + 1) * kPage > least) {
+      const int seen = lim - p * kPage;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
-      const uint32_t ka = base + (s0 + lane % 16) * M::kRow + lane / 16 * 16;
+      for (int i = 0; i < kPage; ++i)
+        if (i >= seen) s[i] = -INFINITY;
+    }
+    if (odd)
+      for (int i = 0; i < kPage && p * kPage + i < lim; ++i)
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        uint32_t x[2][4], y[2][4];
-        ldmatrix4(ka + k * 32, x[0]);
-        ldmatrix4(ka + kStep * M::kRow + k * 32, x[1]);
-        ldmatrix4(qa + k * 32, y[0]);
-        ldmatrix4(qa + 16 * M::kRow + k * 32, y[1]);
+        for (int w = 0; w < 4; ++w)
+          if (odd_rows[w * 32 + i / 2] >> (8 * (i & 1)) & 1) poison |= 1u << (w * HD / 128);
+    float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_f16_16816(s[i][n], x[i][0], x[i][1], x[i][2], x[i][3], y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
+    for (int i = 0; i < kPage; ++i) top = fmaxf(top, s[i]);
+    top *= factor;
+    if (done > 0) ok = ok && wait_short(bars + 1, (done - 1) & 1);  // the output so far; weights are used up
+    __syncwarp();
+    tc_fence_after();
+    const bool rise = top + lift > kWeightShift + kSlack;
+    if (__any_sync(0xffffffffu, rise)) {
+      const float m = lift == 3e38f ? -INFINITY : kWeightShift - lift, mn = fmaxf(m, top);
+      float keep = 1.f;
+      if (rise) {
+        keep = ex2(m - mn);
+        lift = kWeightShift - mn;
+        l *= keep;
       }
-      const bool cut = t0 + 2 * kStep > least;
+      __syncwarp();
+      if (done > 0)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t pf[NT][2];
-        st.softmax(s[i], t0 + i * kStep, g, cut, pf);  // may rescale the output: weights are used before the next
-        const uint32_t va =
-            base + M::kHalf + (s0 + i * kStep + lane % 8 + lane / 16 * 8) * M::kRow + lane / 8 % 2 * 16;
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          uint32_t r[32];
+          tmem_ld32(tlane + M::kO + c, o);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          uint32_t x[4];
-          ldmatrix4_trans(va + k * 32, x);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16_16816(st.o[n][k], x[0], x[1], x[2], x[3], pf[n][0], pf[n][1]);
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * keep);
+          tmem_st32(tlane + M::kO + c, r);
         }
+    }
+    float sum = 0.f;
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < kPage; i += 2) {
+      s[i] = ex2(__fmaf_rn(s[i], factor, lift));
+      s[i + 1] = ex2(__fmaf_rn(s[i + 1], factor, lift));
+      sum += s[i] + s[i + 1];
+      w[i / 2] = h2_bits(__floats2half2_rn(s[i], s[i + 1]));
+    }
+    l += sum;
+    tmem_st32(tlane + M::kP, w);
+    if constexpr (TN == 2) {
+#pragma unroll
+      for (int i = 0; i < kPage; i += 2) {
+        const float2 h = __half22float2(bits_h2(w[i / 2]));
+        w[i / 2] = h2_bits(__floats2half2_rn(s[i] - h.x, s[i + 1] - h.y));
       }
-      if (odd) {  // a value row that is no number: neither is any column that sees it, in its group's elements
-        for (int r = s0; r < s0 + 2 * kStep; ++r) {
-          const uint32_t bits = odd_rows[r];
-          if (!bits) continue;
+      tmem_st32(tlane + M::kP + 32, w);
+    }
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) break;
+    if (threadIdx.x == 0) {
+      tc_fence_after();
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < TN; ++t)
 #pragma unroll
-            for (int i = 0; i < HD / 16; ++i)
+        for (int k = 0; k < kPage / 16; ++k)
+          tc_mma_tmem_a(tm + M::kO, tm + M::kP + t * 32 + k * 8, desc_sw128(smem_u32(vt) + k * 32),
+                        idesc_f16(kTcCols, HD), done > 0 || t > 0 || k > 0);
+      tc_commit(bars + 1);
+    }
+    ++done;
+  }
+  if (done > 0) ok = wait_short(bars + 1, (done - 1) & 1) && ok;
+  __syncwarp();
+  tc_fence_after();
+  if (!ok && a.c.status && threadIdx.x == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if ((bits >> (i / 2) & 1) && p * kPage + r < st.lim[n][kTwo ? 0 : k % 2]) st.o[n][i][k] = NAN;
-        }
+  for (int c = 0; c < HD; c += 32) {
+    float o[32];
+    __syncwarp();
+    if (done > 0) {
+      tmem_ld32(tlane + M::kO + c, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0.f;
+    }
+    if (poison >> (c / 32) & 1)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = NAN;
+    if (live && whole) {
+      constexpr int kPer = 16 / sizeof(T);
+      T* out = static_cast<T*>(a.out) + at * HD + c;
+#pragma unroll
+      for (int i = 0; i < 32; i += kPer) {
+        uint4 u;
+        T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) e[k] = from_f<T>(l == 0.f ? 0.f : o[i + k] * inv);
+        *reinterpret_cast<uint4*>(out + i) = u;
       }
+    } else if (live) {
+      float4* out = reinterpret_cast<float4*>(a.part_o + (at * a.n_split + split) * HD + c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
   }
-  st.finish_sums();
-  // element of output tile i, row r: position 16 i + r of an expanded row
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < st.NC; ++j) {
-      const int col = tile.first + (warp * 32 + n * 8 + 2 * c + j) / (kTwo ? 2 : 1);
-      if (col >= cols) continue;
-      const size_t at = static_cast<size_t>(q0 + col / a.group) * a.n_head + kh * a.group + col % a.group;
-      const float l = st.l[n][j], inv = l == 0.f ? 0.f : 1.f / l;
-      const int e0 = (g >> 1) + 4 * (g & 1);  // of positions 16 i + g: element 16 i + e0, and 8 further on
-#pragma unroll
-      for (int i = 0; i < HD / 16; ++i) {
-        float x, y;
-        if constexpr (kTwo)
-          x = st.o[n][i][0] + st.o[n][i][1], y = st.o[n][i][2] + st.o[n][i][3];
-        else
-          x = st.o[n][i][j], y = st.o[n][i][2 + j];
-        if (whole) {
-          T* out = static_cast<T*>(a.out) + at * HD + 16 * i + e0;
-          out[0] = from_f<T>(l == 0.f ? 0.f : x * inv);
-          out[8] = from_f<T>(l == 0.f ? 0.f : y * inv);
-        } else {
-          float* out = a.part_o + (at * a.n_split + split) * HD + 16 * i + e0;
-          out[0] = x;
-          out[8] = y;
-        }
-      }
-      if (!whole && g == 0) a.part_ml[at * a.n_split + split] = make_float2(st.maximum(n, j), l);
-    }
+  if (live && !whole) a.part_ml[at * a.n_split + split] = make_float2(lift == 3e38f ? -INFINITY : kWeightShift - lift, l);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tm, M::kCols);
 }
 
 // The splits of each (row, query head): one block each, a thread an element of every kJoinParts-th split (4 parts
@@ -922,11 +1032,11 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   Plan p{};
   const long long group = n_head / n_kv_head, columns = n_rows * group * (two ? 2 : 1);
   p.many = columns > 32ll * n_seq;
-  const int cols = (p.many ? kManyCols : 8) / (two ? 2 : 1);
+  const int cols = p.many ? kTcCols : two ? 4 : 8;
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
   const long long items = static_cast<long long>(p.tiles) * n_kv_head;
-  const int room = p.many ? 152 * 6 : items < 152 ? 152 * 4 : 152 * 8;
+  const int room = p.many ? 152 * 4 : items < 152 ? 152 * 4 : 152 * 8;
   const int want = static_cast<int>(std::min(std::max(1ll, room / items), 128ll));
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
@@ -942,8 +1052,8 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
 
 template <typename T, int HD>
 int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
-  void (*const kernel)(AttnArgs) = p.many ? k_kv4_many<T, HD> : k_kv4_decode<T, HD>;
-  const int smem = p.many ? Many<HD>::kBytes : kDecodeSmem<HD>;
+  void (*const kernel)(AttnArgs) = p.many ? k_kv4_tc<T, HD> : k_kv4_decode<T, HD>;
+  const int smem = p.many ? Tc<HD, sizeof(T) == 4 ? 2 : 1>::kBytes : kDecodeSmem<HD>;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return S2_ECUDA;

@@ -135,7 +135,7 @@ def attention(q, k, v, seen, scale):
     # sum |q k|, and the same again for the split of q into two fp16 parts (22 bits).  It shifts the row's
     # weights by twice its error; exp and its argument's product with log2(e) add 2^-21 + |s - m| 2^-23;
     # sums over positions L/16 + 64 roundings of 2^-23.
-    ab = (q.abs() @ k.abs().t() * scale).masked_fill(dead, 0)
+    ab = (q.abs() @ k.abs().t() * abs(scale)).masked_fill(dead, 0)
     ds = 2 * (hd / 16 + 32) * 2.0 ** -23 * ab.amax(-1, keepdim=True)
     spread = torch.where(dead, torch.zeros((), dtype=torch.float64), (m - s).clamp(max=60)).amax(-1, keepdim=True)
     rel = 2 * ds + 2 * (2.0 ** -21 + spread * 2.0 ** -23) + (L / 16 + 64) * 2.0 ** -23

@@ -277,6 +277,21 @@ def test_attention_magnitudes(dtype):
     _check_attention(got, q, pages, table, q_start, lengths, 0.125, dt)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, 1.0])
+def test_attention_scales(scale):
+    """A scale of zero (all seen positions alike), a negative one, one that underflows, and none."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(17)
+    for spans in ([(1, 70), (2, 33)], [(50, 100), (3, 3)]):
+        table, q_start, lengths, pool = _layout(spans, rng)
+        pages = torch.zeros((pool, 1, 80 * 64), dtype=torch.uint8)
+        fb.fill_random(pages, rng)
+        for dt in fb.TYPES.values():
+            q = torch.from_numpy(rng.standard_normal((int(q_start[-1]), 4, 64)).astype(np.float32)).to(dt)
+            got = _attend(pkg, q, pages, table, q_start, lengths, scale=scale)
+            _check_attention(got, q, pages, table, q_start, lengths, scale, dt)
+
+
 def test_attention_bad_pages_are_not_attended():
     import dual_ar_tts_gb300 as pkg
     rng = np.random.default_rng(9)
