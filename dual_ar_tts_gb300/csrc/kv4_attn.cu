@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   using S = Stage<HD>;
   constexpr int kORow = HD + 4;  // floats of a column's output in the joining buffer
   extern __shared__ __align__(16) uint8_t sm[];
+  pdl_trigger();  // the joining kernel may find its rows
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
   const int kh = blockIdx.y, split = blockIdx.z;
   const Tile tile = find_tile(a.c, a.group, CT, blockIdx.x);
@@ -731,6 +732,7 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   using B = Kv4Block<HD>;
   using M = Tc<HD, TN>;
   extern __shared__ __align__(16) uint8_t smraw[];
+  pdl_trigger();
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::kBars);  // scores, output
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 2);
@@ -987,7 +989,7 @@ __global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) 
   const int seq = seq_of_row(a.c.q_start, a.c.n_seq, row);
   const bool live = seq < a.c.n_seq && row >= __ldg(a.c.q_start + seq) && __ldg(a.c.q_start + seq + 1) <= a.c.n_rows;
   const int len = live ? min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage) : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // every thread: no end before the splits'
+  pdl_wait();  // every thread: no end before the splits'
   if (!live) return;
   const int pages = (len + kPage - 1) / kPage;
   const int n = min((pages + a.split_pages - 1) / a.split_pages, a.n_split);

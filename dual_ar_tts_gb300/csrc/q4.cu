@@ -13,6 +13,7 @@
 #include "convert.cuh"
 #include "ptx.cuh"
 #include "s2_internal.h"
+#include "tc05.cuh"
 
 namespace s2 {
 namespace {
@@ -432,11 +433,14 @@ Planes planes(int n, int k, int terms, void* ws) {
   return p;
 }
 
-// One block per activation row (and per row of zeros that fills the last tile).
+// One block per activation row (and per row of zeros that fills the last tile).  Rows of up to 4 items a thread are
+// read once.
+constexpr int kPlaneThreads = 512;
 template <typename T>
-__global__ void __launch_bounds__(512) k_q4_planes(const MatmulArgs a, const Planes p) {
-  constexpr int TN = kTerms<T>;
+__global__ void __launch_bounds__(kPlaneThreads) k_q4_planes(const MatmulArgs a, const Planes p) {
+  constexpr int TN = kTerms<T>, kHeld = 4;
   __shared__ uint32_t top;
+  pdl_trigger();  // the products may start on their codes
   const int row = blockIdx.x, lane = threadIdx.x % 32;
   const bool live = row < a.n;
   const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(live ? row : 0) * a.x_stride;
@@ -450,27 +454,33 @@ __global__ void __launch_bounds__(512) k_q4_planes(const MatmulArgs a, const Pla
     return v;
   };
   if (threadIdx.x == 0) top = 0;
-  __syncthreads();
+  Eight<T> held[kHeld];
   uint32_t t = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < items; i += blockDim.x) t = max(t, largest(load(i)));
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) held[u] = load(threadIdx.x + u * kPlaneThreads);
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) t = max(t, largest(held[u]));
+  for (int i = threadIdx.x + kHeld * kPlaneThreads; i < items; i += kPlaneThreads) t = max(t, largest(load(i)));
   t = __reduce_max_sync(0xffffffffu, t);
+  __syncthreads();
   if (lane == 0) atomicMax(&top, t);
   __syncthreads();
   const float up = pow2(scale_exponent(top));
   if (threadIdx.x == 0) p.top[row] = top;
-#pragma unroll 2
-  for (int i0 = 0; i0 < items; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x, part = i / 4;
-    const Staged<T> st(load(i), up);
+  auto store = [&](const Eight<T>& v, int i) {
+    const Staged<T> st(v, up);
     if (i < items)
 #pragma unroll
       for (int u = 0; u < TN; ++u) {
-        const int col = row * TN + u;
+        const int col = row * TN + u, part = i / 4;
         p.b[(static_cast<size_t>(part) * p.tiles + col / 8) * 32 + col % 8 * 4 + i % 4] = st.b[u];
         if (i % 4 == 0) p.inits[static_cast<size_t>(part) * p.tiles * 8 + col] = st.init[u];
       }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (u * kPlaneThreads < items) store(held[u], threadIdx.x + u * kPlaneThreads);
+  for (int i0 = kHeld * kPlaneThreads; i0 < items; i0 += kPlaneThreads) store(load(i0 + threadIdx.x), i0 + threadIdx.x);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -488,7 +498,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 // A block takes 128 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
 // their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
 // activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.
-constexpr int kManyRows = 16 * kWarps;
+constexpr int kManyWarps = 4, kManyRows = 16 * kManyWarps;
 constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
 template <int NT>
 constexpr int kManyAhead = NT == 1 ? 8 : 4;
@@ -496,7 +506,7 @@ template <int NT>
 constexpr int kStepBytes = 4 * NT * (512 + 32);
 
 template <typename T, int NT, int G>
-__global__ void __launch_bounds__(32 * kWarps, 2) k_q4_many(const MatmulArgs a, const Planes p) {
+__global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(const MatmulArgs a, const Planes p) {
   constexpr int TN = kTerms<T>, kAhead = kManyAhead<NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t top[8 * NT];
@@ -505,14 +515,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_many(const MatmulArgs a, 
   const int ranks = gridDim.y, rank = blockIdx.y;
   const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / ranks);
   const int count = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / ranks) - b0;
-  uint8_t* xring = smem + kWarps * kAhead * kRing;
+  uint8_t* xring = smem + kManyWarps * kAhead * kRing;
   Codes<G, kAhead> codes(smem + warp * kAhead * kRing, a, blockIdx.x * kManyRows + warp * 16, blocks, b0, count, 1);
   auto copy_x = [&](int j) {
     if (j >= count) return;
     uint8_t* dst = xring + j % kAhead * kStepBytes<NT>;
     const size_t part = static_cast<size_t>(b0 + j) * 4;
 #pragma unroll
-    for (int i = threadIdx.x; i < 4 * NT * 32; i += 32 * kWarps)
+    for (int i = threadIdx.x; i < 4 * NT * 32; i += 32 * kManyWarps)
       cp_async16(dst + i * 16, p.b + ((part + i / (NT * 32)) * p.tiles + blockIdx.z * NT) * 32 + i % (NT * 32));
     if (threadIdx.x < 8 * NT)
       cp_async16(dst + 4 * NT * 512 + threadIdx.x * 16, p.inits + ((part + threadIdx.x / (2 * NT)) * p.tiles + blockIdx.z * NT) * 8 +
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_many(const MatmulArgs a, 
   // codes do not depend on the kernel in front, which runs after all that came before it
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) codes.issue();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) {
     copy_x(i);
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_many(const MatmulArgs a, 
     __syncthreads();
   // a thread adds up four rows of one column
   const int quads = kManyRows / 4 / ranks, n0 = blockIdx.z * 8 * NT / TN, nn = min(8 * NT / TN, a.n - n0);
-  for (int i = threadIdx.x; i < quads * nn; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < quads * nn; i += 32 * kManyWarps) {
     const int r = (rank * quads + i % quads) * 4, col = i / quads, row = blockIdx.x * kManyRows + r;
     float v[4] = {};
     const float* at = out + col * TN * kJoinRow + r;
@@ -583,19 +593,19 @@ template <typename T, int NT, int G>
 int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + kManyRows - 1) / kManyRows, passes = p.tiles / NT;
   if (passes > 65535) return S2_EINVAL;
-  // Up to two blocks an SM in clusters of two, one in larger ones (304 blocks in clusters of four do not all fit
-  // at a time: 9728 x 1024, 32 rows, 12.2 us against 8.8), of two code blocks at least.
+  // Up to four blocks an SM in clusters of two, about two in larger ones (608 blocks in clusters of four do not all
+  // fit at a time: 9728 x 1024, 32 rows, 13.7 us against 8.5), of two code blocks at least.
   int ranks = 1;
-  while (ranks < 8 && static_cast<long long>(grid) * passes * ranks * 2 <= (ranks == 1 ? 304 : 152) && blocks >= 4 * ranks)
+  while (ranks < 8 && static_cast<long long>(grid) * passes * ranks * 2 <= (ranks == 1 ? 608 : 320) && blocks >= 4 * ranks)
     ranks *= 2;
-  constexpr int kRings = kManyAhead<NT> * (kWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
+  constexpr int kRings = kManyAhead<NT> * (kManyWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
   constexpr int smem = kRings > kJoin ? kRings : kJoin;
   if (cudaFuncSetAttribute(k_q4_many<T, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return S2_ECUDA;
-  k_q4_planes<T><<<p.tiles * 8 / kTerms<T>, 512, 0, st>>>(a, p);
+  k_q4_planes<T><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, ranks, passes);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(32 * kManyWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
