@@ -284,11 +284,6 @@ def _rows16(x):
     s0, s1 = x.stride()
     if s1 == 1 and s0 >= x.shape[1] and s0 * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
         return x
-    pad = -x.shape[1] % 8
-    if pad:
-        import torch
-        y = torch.empty((x.shape[0], x.shape[1] + pad), dtype=x.dtype, device=x.device)[:, :x.shape[1]]
-        return y.copy_(x)
     x = x.contiguous()
     return x.clone() if x.data_ptr() % 16 else x
 

@@ -408,7 +408,7 @@ __device__ __forceinline__ Tile find_tile(const s2_kv4& k, int group, int cols, 
     const int s = base + lane;
     int q0 = 0, q1 = 0, len = 0;
     if (s < k.n_seq) q0 = __ldg(k.q_start + s), q1 = __ldg(k.q_start + s + 1), len = __ldg(k.lengths + s);
-    const int tiles = (max(q1 - q0, 0) * group + cols - 1) / cols;
+    const int tiles = (min(max(q1 - q0, 0), k.n_rows) * group + cols - 1) / cols;
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -252,6 +252,67 @@ def test_attention_ignores_what_is_masked(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_of_many_rows_ignores_what_is_masked(dtype, hd):
+    """As above for sequences of many rows: NaN behind a length and in the future of some rows, in keys or values."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(4)
+    spans = [(70, 100), (130, 130), (40, 20), (64, 0)]
+    table, q_start, lengths, pool = _layout(spans, rng)
+    dt = fb.TYPES[dtype]
+    hq, hkv = 8, 2
+    pages = torch.zeros((pool, hkv, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    for s, (_, L) in enumerate(spans):
+        if L % 64:
+            for part in range(2):
+                codes, par = fb._parts(pages, part)
+                par[int(table[s, L // 64]), :, L % 64:] = torch.tensor([math.nan, -math.inf]).half()
+    q = torch.from_numpy(rng.standard_normal((int(q_start[-1]), hq, hd)).astype(np.float32)).to(dt)
+    got = _attend(pkg, q, pages, table, q_start, lengths)
+    assert torch.isfinite(got).all()
+    assert (got[200:220] == 0).all() and (got[240:] == 0).all()     # rows before their sequence, and of an empty one
+    _check_attention(got, q, pages, table, q_start, lengths, hd ** -0.5, dt)
+    # sequence 0: position 80 is seen by its rows 50 on; sequence 1: position 70 by its rows 70 on
+    codes, par = fb._parts(pages, 1)
+    par[int(table[0, 1]), :, 16, 1] = math.nan                       # one group of the values
+    codes, par = fb._parts(pages, 0)
+    par[int(table[1, 1]), 0, 6] = math.nan                           # a key of KV head 0
+    later = _attend(pkg, q, pages, table, q_start, lengths)
+    assert torch.equal(later[:50], got[:50]) and torch.equal(later[70:140], got[70:140])
+    assert torch.isnan(later[50:70, :, 32:64]).all()
+    assert torch.equal(later[50:70, :, :32], got[50:70, :, :32])
+    assert torch.isnan(later[140:200, :4]).all() and torch.equal(later[140:200, 4:], got[140:200, 4:])
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_many_sequences(dtype):
+    """More sequences than a warp has lanes, empty ones among them, appended, read and attended."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(8)
+    spans = [(int(rng.integers(0, 3)), int(rng.integers(3, 90))) for _ in range(75)] + [(1, 200)]
+    table, q_start, lengths, pool = _layout(spans, rng)
+    rows, dt, hq, hkv, hd = int(q_start[-1]), fb.TYPES[dtype], 6, 2, 64
+    pages = torch.zeros((pool, hkv, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    qkv = torch.from_numpy(rng.standard_normal((rows, (hq + 2 * hkv) * hd)).astype(np.float32)).to(dt)
+    gp = pages.cuda()
+    gt, gs, gl = _gpu(table, q_start, lengths)
+    rope = pkg.rope_table(256, hd)
+    q = pkg.kv4_append(qkv.cuda(), gp, gt, gs, gl, rope, hq)
+    want = pages.clone()
+    f = qkv.float().view(rows, -1, hd)
+    seq = np.repeat(np.arange(len(lengths)), np.diff(q_start))
+    pos = lengths[seq] - (q_start[seq + 1] - np.arange(rows))
+    k = fb.norm_rotate(f[:, hq:hq + hkv], None, 0, rope.cpu()[torch.from_numpy(pos).long()][:, None])
+    for i in range(rows):
+        fb.put(want, int(table[seq[i], pos[i] // 64]), int(pos[i] % 64), k[i], f[i, hq + hkv:])
+    assert torch.equal(gp.cpu(), want)
+    got = pkg.kv4_attention(q, gp, gt, gs, gl)
+    _check_attention(got, q.cpu(), want, table, q_start, lengths, hd ** -0.5, dt)
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
 def test_attention_magnitudes(dtype):
     """Scores far apart (one position takes all; 10 nats below it thousands share the rest), queries of 1e-6 and
     1e4, tiny value scales."""
