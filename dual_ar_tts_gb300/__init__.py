@@ -230,8 +230,8 @@ def quantize_e4m3(w):
 
 # ------------------------------------- 4-bit weights, 4-bit cache, adjusted logits
 
-# A call of a few microseconds is soon outweighed by what Python does around it, so the checks below
-# read each property of a tensor once and compare plain values.
+# A call of a few microseconds is soon outweighed by what Python does around it, so the checks below are few
+# expressions of plain values, each property of a tensor read once.
 
 _kinds = None    # torch element type -> S2_* code
 
@@ -247,11 +247,6 @@ def _code(t):
     return code
 
 
-def _need(ok, msg):
-    if not ok:
-        raise ValueError(msg)
-
-
 def _on(dev, *tensors):
     """All given tensors are on CUDA device number `dev`."""
     for t in tensors:
@@ -261,10 +256,8 @@ def _on(dev, *tensors):
         raise ValueError("tensors must be on one CUDA device")
 
 
-def _launch(name, dev, *args):
+def _launch(torch, fn, dev, *args):
     """Call an entry point on the current stream of device number `dev`, with that device current meanwhile."""
-    import torch
-    fn = getattr(_lib or load(), name)
     stream = torch._C._cuda_getCurrentRawStream(dev)
     if dev == torch._C._cuda_getDevice():
         rc = fn(*args, stream)
@@ -272,7 +265,7 @@ def _launch(name, dev, *args):
         with torch.cuda.device(dev):
             rc = fn(*args, stream)
     if rc != S2_OK:
-        raise S2Error(name, rc, "see include/s2frame.h for what the call takes")
+        raise S2Error(fn.__name__, rc, "see include/s2frame.h for what the call takes")
 
 
 def _ptr(t):
@@ -293,15 +286,17 @@ def quantize_q4(w, group: int = 32):
     [rows][ceil(cols/128)*(128/group)]): 4-bit codes with a scale per `group` (32, 64 or 128) columns; layout in
     s2frame.h."""
     import torch
-    dt = _code(w)
-    _need(w.dim() == 2 and w.is_cuda and w.numel() > 0, "quantize_q4 takes a 2-D CUDA tensor")
-    _need(group in (32, 64, 128) and w.shape[1] % group == 0, "columns must be a multiple of group: 32, 64 or 128")
+    dt, dev = _code(w), w.get_device()
+    _on(dev)
+    if w.dim() != 2 or group not in (32, 64, 128) or w.shape[1] % group or not w.numel():
+        raise ValueError("quantize_q4 takes a 2-D tensor, its columns a multiple of group: 32, 64 or 128")
     w = w.contiguous()
     rows, cols = w.shape
     blocks = -(-cols // 128)
     codes = torch.empty((rows, blocks * 64), dtype=torch.uint8, device=w.device)
     scales = torch.empty((rows, blocks * (128 // group)), dtype=torch.bfloat16, device=w.device)
-    _launch("s2_quantize_q4", w.get_device(), w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
+    _launch(torch, load().s2_quantize_q4, dev, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -310,27 +305,30 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
     workspace, a uint8 tensor of s2_q4_matmul_workspace bytes, is allocated where none is given."""
     import torch
     dt, dev = _code(x), x.get_device()
-    _need(x.dim() == 2 and codes.dim() == 2 and scales.dim() == 2, "q4_matmul takes 2-D tensors")
+    _on(dev, codes, scales, out, workspace)
+    if x.dim() != 2 or codes.dim() != 2 or group not in (32, 64, 128):
+        raise ValueError("q4_matmul takes x [n][k], codes and scales of quantize_q4 and its group: 32, 64 or 128")
     n, k = x.shape
     m, width = codes.shape
-    _on(dev, codes, scales, out, workspace)
-    _need(group in (32, 64, 128) and k % group == 0, "columns must be a multiple of group: 32, 64 or 128")
-    _need(codes.dtype is torch.uint8 and codes.is_contiguous() and width == -(-k // 128) * 64,
-          "codes must be contiguous uint8 [rows][ceil(k/128)*64]")
-    _need(scales.dtype is torch.bfloat16 and scales.is_contiguous() and
-          scales.shape == (m, width * 2 // group), "scales must be contiguous bf16 [rows][ceil(k/128)*(128/group)]")
+    if k % group or width != -(-k // 128) * 64 or scales.shape != (m, width * 2 // group) or \
+            codes.dtype is not torch.uint8 or scales.dtype is not torch.bfloat16 or not codes.is_contiguous() or \
+            not scales.is_contiguous():
+        raise ValueError("codes must be contiguous uint8 [rows][ceil(k/128)*64] and scales contiguous bf16 "
+                         "[rows][ceil(k/128)*(128/group)], k a multiple of group")
     x = _rows16(x)
     if out is None:
         out = torch.empty((n, m), dtype=x.dtype, device=x.device)
+    elif out.dtype is not x.dtype or out.shape != (n, m) or not out.is_contiguous():
+        raise ValueError("out must be contiguous [n][rows] of x's type")
+    lib = _lib or load()
+    if workspace is not None:
+        nbytes = workspace.nbytes
     else:
-        _need(out.dtype is x.dtype and out.shape == (n, m) and out.is_contiguous(),
-              "out must be contiguous [n][rows] of x's type")
-    if workspace is None:
-        nbytes = (_lib or load()).s2_q4_matmul_workspace(n, k, dt)
+        nbytes = lib.s2_q4_matmul_workspace(n, k, dt)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _launch("s2_q4_matmul", dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k, group,
-            out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    _launch(torch, lib.s2_q4_matmul, dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k,
+            group, out.data_ptr(), _ptr(workspace), nbytes)
     return out
 
 
@@ -348,23 +346,25 @@ def kv4_pages(n_pages: int, n_kv_head: int, head_dim: int, device="cuda"):
     """The pages of one layer's 4-bit cache: uint8 [n_pages][n_kv_head][80*head_dim], zeroed."""
     import torch
     nbytes = load().s2_kv4_page_bytes(n_kv_head, head_dim)
-    _need(nbytes > 0 and n_pages > 0, "kv4_pages takes head_dim 64 or 128 and positive counts")
+    if nbytes < 0 or n_pages < 1:
+        raise ValueError("kv4_pages takes head_dim 64 or 128 and positive counts")
     return torch.zeros((n_pages, n_kv_head, nbytes // n_kv_head), dtype=torch.uint8, device=device)
 
 
-def _kv4(dev, pages, table, q_start, lengths, n_rows, status):
-    import torch
+def _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status):
     i32 = torch.int32
+    if pages.dim() != 3 or table.dim() != 2:
+        raise ValueError("pages must be uint8 [n_pages][n_kv_head][80*head_dim], table int32 [n_seq][cols]")
     n_pages, n_kv_head, block = pages.shape
     n_seq, cols = table.shape
     _on(dev, pages, table, q_start, lengths, status)
-    _need(pages.dtype is torch.uint8 and pages.is_contiguous() and block in (80 * 64, 80 * 128),
-          "pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim]")
-    _need(table.dtype is i32 and table.is_contiguous(), "table must be contiguous int32 [n_seq][cols]")
-    _need(q_start.dtype is i32 and q_start.shape == (n_seq + 1,) and q_start.is_contiguous(),
-          "q_start must be int32 [n_seq+1]")
-    _need(lengths.dtype is i32 and lengths.shape == (n_seq,) and lengths.is_contiguous(), "lengths must be int32 [n_seq]")
-    _need(status is None or (status.dtype is i32 and status.numel() == 1), "status must be one int32")
+    if pages.dtype is not torch.uint8 or block not in (80 * 64, 80 * 128) or not pages.is_contiguous() or \
+            table.dtype is not i32 or not table.is_contiguous():
+        raise ValueError("pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim], table contiguous int32")
+    if q_start.dtype is not i32 or lengths.dtype is not i32 or q_start.shape != (n_seq + 1,) or \
+            lengths.shape != (n_seq,) or not q_start.is_contiguous() or not lengths.is_contiguous() or \
+            (status is not None and (status.dtype is not i32 or status.numel() != 1)):
+        raise ValueError("q_start must be int32 [n_seq+1], lengths int32 [n_seq], status one int32")
     return s2_kv4(pages.data_ptr(), n_pages, n_kv_head, block // 80, table.data_ptr(), cols, n_seq, q_start.data_ptr(),
                   lengths.data_ptr(), n_rows, _ptr(status))
 
@@ -378,48 +378,44 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
     Returns the rotated queries [n_rows][n_head][head_dim]; rows behind the last sequence are left as they were."""
     import torch
     dt, dev = _code(qkv), qkv.get_device()
-    _need(qkv.dim() == 2 and pages.dim() == 3 and table.dim() == 2,
-          "qkv and table must be 2-D, pages 3-D")
+    if qkv.dim() != 2:
+        raise ValueError("qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
     n_rows, width = qkv.shape
-    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
-    hd = c.head_dim
+    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
+    hd, f32 = c.head_dim, torch.float32
     _on(dev, rope, q_norm, k_norm, q_out)
-    _need(n_head >= 0 and width == (n_head + 2 * c.n_kv_head) * hd,
-          "qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
-    f32 = torch.float32
-    _need(rope.dtype is f32 and rope.dim() == 3 and rope.shape[1:] == (hd // 2, 2) and rope.is_contiguous(),
-          "rope must be contiguous fp32 [n_pos][head_dim/2][2]")
+    if n_head < 0 or width != (n_head + 2 * c.n_kv_head) * hd:
+        raise ValueError("qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
+    if rope.dtype is not f32 or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2) or not rope.is_contiguous():
+        raise ValueError("rope must be contiguous fp32 [n_pos][head_dim/2][2]")
     for w in (q_norm, k_norm):
-        _need(w is None or (w.dtype is f32 and w.shape == (hd,) and w.is_contiguous()),
-              "norm weights must be fp32 [head_dim]")
+        if w is not None and (w.dtype is not f32 or w.shape != (hd,) or not w.is_contiguous()):
+            raise ValueError("norm weights must be fp32 [head_dim]")
     qkv = _rows16(qkv)
     if q_out is None:
         q_out = torch.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
-    else:
-        _need(q_out.dtype is qkv.dtype and q_out.shape == (n_rows, n_head, hd) and q_out.is_contiguous(),
-              "q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type")
-    _launch("s2_kv4_append", dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
-            rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr())
+    elif q_out.dtype is not qkv.dtype or q_out.shape != (n_rows, n_head, hd) or not q_out.is_contiguous():
+        raise ValueError("q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type")
+    _launch(torch, (_lib or load()).s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head,
+            rope.data_ptr(), rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr())
     return q_out
 
 
 def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None, status=None):
     """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]."""
     import torch
-    _need(pages.dim() == 3 and table.dim() == 2, "pages must be 3-D and table 2-D")
     dev = pages.get_device()
-    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
-    shape = (c.n_kv_head, n_rows, c.head_dim)
-    f16 = torch.float16
+    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
+    shape, f16 = (c.n_kv_head, n_rows, c.head_dim), torch.float16
     if k_out is None:
         k_out = torch.empty(shape, dtype=f16, device=pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=f16, device=pages.device)
-    for t in (k_out, v_out):
-        _need(t.dtype is f16 and t.shape == shape and t.is_contiguous(),
-              "outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim]")
     _on(dev, k_out, v_out)
-    _launch("s2_kv4_read", dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
+    for t in (k_out, v_out):
+        if t.dtype is not f16 or t.shape != shape or not t.is_contiguous():
+            raise ValueError("outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim]")
+    _launch(torch, (_lib or load()).s2_kv4_read, dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
@@ -431,29 +427,30 @@ def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None,
     s2_kv4_attention_workspace bytes, is allocated where none is given."""
     import torch
     dt, dev = _code(q), q.get_device()
-    _need(q.dim() == 3 and pages.dim() == 3 and table.dim() == 2, "q and pages must be 3-D and table 2-D")
+    if q.dim() != 3:
+        raise ValueError("q must be [n_rows][n_head][head_dim]")
     n_rows, n_head, hd = q.shape
-    c = _kv4(dev, pages, table, q_start, lengths, n_rows, status)
+    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
     n_kv = c.n_kv_head
     _on(dev, out, workspace)
-    _need(hd == c.head_dim and n_head % n_kv == 0 and max_len >= 0,
-          "q's heads must be a multiple of the cache's, of the same head_dim")
+    if hd != c.head_dim or n_kv < 1 or n_head % n_kv or max_len < 0:
+        raise ValueError("q's heads must be a multiple of the cache's, of the same head_dim")
     if not q.is_contiguous() or q.data_ptr() % 16:
         q = q.clone(memory_format=torch.contiguous_format)
     if out is None:
         out = torch.empty_like(q)
+    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    lib = _lib or load()
+    if workspace is not None:
+        nbytes = workspace.nbytes
     else:
-        _need(out.dtype is q.dtype and out.shape == q.shape and out.is_contiguous(),
-              "out must be contiguous, of q's shape and type")
-    if workspace is None:
         held = c.table_cols * S2_KV4_PAGE
-        nbytes = (_lib or load()).s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd,
-                                                             min(max_len or held, held))
+        nbytes = lib.s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd, min(max_len or held, held))
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _launch("s2_kv4_attention", dev, ctypes.byref(c), q.data_ptr(), dt, n_head,
-            hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+    _launch(torch, lib.s2_kv4_attention, dev, ctypes.byref(c), q.data_ptr(), dt, n_head,
+            hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _ptr(workspace), nbytes)
     return out
 
 
@@ -464,40 +461,45 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
     presence); bias fp32 [rows or 1][n]; mask int32 or uint32 bits [rows or 1][ceil(n/32)].  Entry ids as in draw."""
     import torch
     dt, dev = _code(logits), logits.get_device()
-    _need(logits.dim() == 2, "logits must be [rows][n]")
+    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows][n]")
     rows, n = logits.shape
     i32, f32 = torch.int32, torch.float32
-    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
     cols = bias_stride = mask_stride = 0
-    _need((history is None) == (penalties is None) and (hist_len is None or history is not None),
-          "history and penalties go together, hist_len with them")
-    if history is not None:
-        _need(history.dtype is i32 and history.dim() == 2 and history.shape[0] == rows and history.is_contiguous(),
-              "history must be contiguous int32 [rows][cols]")
-        _need(penalties.dtype is f32 and penalties.shape == (rows, 3) and penalties.is_contiguous(),
-              "penalties must be contiguous fp32 [rows][3]")
-        _need(hist_len is None or (hist_len.dtype is i32 and hist_len.shape == (rows,) and hist_len.is_contiguous()),
-              "hist_len must be int32 [rows]")
+    if history is None:
+        if penalties is not None or hist_len is not None:
+            raise ValueError("penalties and hist_len go with a history")
+    else:
+        if history.dtype is not i32 or history.dim() != 2 or history.shape[0] != rows or \
+                not history.is_contiguous() or penalties is None or penalties.dtype is not f32 or \
+                penalties.shape != (rows, 3) or not penalties.is_contiguous():
+            raise ValueError("history must be contiguous int32 [rows][cols], with contiguous fp32 penalties [rows][3]")
+        if hist_len is not None and (hist_len.dtype is not i32 or hist_len.shape != (rows,) or
+                                     not hist_len.is_contiguous()):
+            raise ValueError("hist_len must be int32 [rows]")
         cols = history.shape[1]
         if cols == 0:
             history = penalties = hist_len = None
     if bias is not None:
-        _need(bias.dtype is f32 and bias.shape in ((1, n), (rows, n)) and bias.is_contiguous(),
-              "bias must be contiguous fp32 [rows or 1][n]")
+        if bias.dtype is not f32 or bias.shape not in ((1, n), (rows, n)) or not bias.is_contiguous():
+            raise ValueError("bias must be contiguous fp32 [rows or 1][n]")
         bias_stride = n if bias.shape[0] > 1 else 0
     if mask is not None:
         words = -(-n // 32)
-        _need(mask.dtype in (i32, torch.uint32) and mask.shape in ((1, words), (rows, words)) and mask.is_contiguous(),
-              "mask must be contiguous 32-bit [rows or 1][ceil(n/32)]")
+        if mask.dtype not in (i32, torch.uint32) or mask.shape not in ((1, words), (rows, words)) or \
+                not mask.is_contiguous():
+            raise ValueError("mask must be contiguous 32-bit [rows or 1][ceil(n/32)]")
         mask_stride = words if mask.shape[0] > 1 else 0
     if not logits.is_contiguous():
         logits = logits.contiguous()
     if out is None:
         out = torch.empty((rows, n), dtype=f32, device=logits.device)
-    else:
-        _need(out.dtype is f32 and out.shape == (rows, n) and out.is_contiguous(), "out must be contiguous fp32 [rows][n]")
-    _launch("s2_adjust_logits", dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt, _ptr(history), _ptr(hist_len),
-            cols, _ptr(penalties), _ptr(bias), bias_stride, _ptr(mask), mask_stride, out.data_ptr())
+    elif out.dtype is not f32 or out.shape != (rows, n) or not out.is_contiguous():
+        raise ValueError("out must be contiguous fp32 [rows][n]")
+    _launch(torch, (_lib or load()).s2_adjust_logits, dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt,
+            _ptr(history), _ptr(hist_len), cols, _ptr(penalties), _ptr(bias), bias_stride, _ptr(mask), mask_stride,
+            out.data_ptr())
     return out
 
 

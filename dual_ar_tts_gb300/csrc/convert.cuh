@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "../../include/s2frame.h"
 
 namespace s2 {
@@ -29,6 +31,20 @@ inline auto with_dtype(int dtype, F f) {
   if (dtype == S2_F32) return f(float{});
   if (dtype == S2_BF16) return f(__nv_bfloat16{});
   return f(__half{});
+}
+
+// Lets a kernel be launched with up to kMost bytes of dynamic shared memory on the current device.  The limit is set
+// once for a device (setting it again would cost every launch about a microsecond).
+template <auto kKernel, int kMost>
+inline bool allow_smem() {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 }  // namespace s2

@@ -1054,12 +1054,16 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
 
 template <typename T, int HD>
 int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
-  void (*const kernel)(AttnArgs) = p.many ? k_kv4_tc<T, HD> : k_kv4_decode<T, HD>;
-  const int smem = p.many ? Tc<HD, sizeof(T) == 4 ? 2 : 1>::kBytes : kDecodeSmem<HD>;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return S2_ECUDA;
-  kernel<<<dim3(p.tiles, a.c.n_kv_head, p.n_split), 128, smem, st>>>(a);
+  const dim3 grid(p.tiles, a.c.n_kv_head, p.n_split);
+  if (p.many) {
+    constexpr int smem = Tc<HD, sizeof(T) == 4 ? 2 : 1>::kBytes;
+    if (!allow_smem<k_kv4_tc<T, HD>, smem>()) return S2_ECUDA;
+    k_kv4_tc<T, HD><<<grid, kTcCols, smem, st>>>(a);
+  } else {
+    constexpr int smem = kDecodeSmem<HD>;
+    if (!allow_smem<k_kv4_decode<T, HD>, smem>()) return S2_ECUDA;
+    k_kv4_decode<T, HD><<<grid, 32 * kWarps, smem, st>>>(a);
+  }
   if (p.n_split > 1) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.c.n_rows * a.n_head);

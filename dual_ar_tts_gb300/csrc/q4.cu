@@ -396,15 +396,17 @@ bool few(int n, int blocks) {
          static_cast<long long>(n) * blocks * 16 <= kFewItems<T> * 32 * kWarps;
 }
 
+// shared memory: at most kFewItems * 16 (row, block) pairs, of which one row has the most room for sums
+template <typename T>
+constexpr int kFewMost = kWarps * kFewAhead * kRing + kFewItems<T> * 16 * (256 * kTerms<T> + 128);
+
 template <typename T, int G>
 int launch_few(MatmulArgs a, cudaStream_t st) {
   const int all = (a.m + 15) / 16, blocks = (a.k + kBlock - 1) / kBlock;
   a.tiles = kWarps;  // R: the most row tiles in a block that leave two blocks an SM
   while (a.tiles > 1 && (all + a.tiles - 1) / a.tiles < 304) a.tiles /= 2;
   const int smem = kWarps * kFewAhead * kRing + blocks * (256 * a.n * kTerms<T> + 128);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(k_q4_few<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                              cudaSuccess)
-    return S2_ECUDA;
+  if (!allow_smem<k_q4_few<T, G>, kFewMost<T>>()) return S2_ECUDA;
   k_q4_few<T, G><<<(all + a.tiles - 1) / a.tiles, 32 * kWarps, smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
@@ -600,8 +602,7 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
     ranks *= 2;
   constexpr int kRings = kManyAhead<NT> * (kManyWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
   constexpr int smem = kRings > kJoin ? kRings : kJoin;
-  if (cudaFuncSetAttribute(k_q4_many<T, NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return S2_ECUDA;
+  if (!allow_smem<k_q4_many<T, NT, G>, smem>()) return S2_ECUDA;
   k_q4_planes<T><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, ranks, passes);
