@@ -13,7 +13,8 @@ namespace {
 
 constexpr int kSlice = 2048;    // entries of a row that one block takes
 constexpr int kAdjustThreads = 256;
-constexpr int kPer = kSlice / kAdjustThreads;
+constexpr int kPer = kSlice / kAdjustThreads;  // entries of a thread
+static_assert(kPer == 8, "16-byte reads and writes");
 
 struct AdjustArgs {
   int n, sem_begin, im_end;
@@ -29,28 +30,54 @@ struct AdjustArgs {
   float* out;
 };
 
+template <int kBytes>
+struct Words;
+template <>
+struct Words<16> {
+  using type = uint4;
+};
+template <>
+struct Words<32> {
+  struct alignas(16) type {
+    uint4 a, b;
+  };
+};
+
 // One block per (slice, row).  The occurrences of the slice's tokens are counted in shared memory from the row's
 // whole history (whole-number adds: the order does not matter) while the slice's logits, bias and mask are on their
-// way; entry e0 + 256 i + t is thread t's, so rows of any alignment are read and written in whole lines.  Bound by
-// those bytes; the history is read again by every slice, from L2 (four bytes a token against 20 KB and more).
-template <typename T>
+// way.  A thread's kPer entries are consecutive and read 16 bytes at a time where rows are aligned to that (kWide);
+// else they are 256 apart, so that rows of any alignment are read and written in whole lines.  Bound by those bytes;
+// the history is read again by every slice, from L2 (four bytes a token against 20 KB and more).
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kAdjustThreads) k_adjust(const AdjustArgs a) {
-  __shared__ int count[kSlice];
+  __shared__ __align__(16) int count[kSlice];
   const size_t r = blockIdx.y;
   const int e0 = blockIdx.x * kSlice, n = min(a.n - e0, kSlice);
   const bool seen = a.history != nullptr;
   const T* x = static_cast<const T*>(a.logits) + r * a.n + e0;
   const float* bias = a.bias ? a.bias + r * a.bias_stride + e0 : nullptr;
-  const uint32_t* mask = a.mask ? a.mask + r * a.mask_stride : nullptr;
+  const uint32_t* mask = a.mask ? a.mask + r * a.mask_stride + e0 / 32 : nullptr;
+  auto entry = [](int i) { return kWide ? threadIdx.x * kPer + i : i * kAdjustThreads + threadIdx.x; };
+  const bool in = entry(0) < n;  // wide rows are whole groups of kPer
   T v[kPer];
-  float b[kPer];
-  uint32_t m[kPer];
+  float b[kPer] = {};
+  uint32_t m = 0;  // this thread's mask bits
+  if constexpr (kWide) {
+    using W = typename Words<sizeof(T) * kPer>::type;
+    using F = Words<sizeof(float) * kPer>::type;
+    if (in) {
+      *reinterpret_cast<W*>(v) = *reinterpret_cast<const W*>(x + entry(0));
+      if (bias) *reinterpret_cast<F*>(b) = *reinterpret_cast<const F*>(bias + entry(0));
+      if (mask) m = __ldg(mask + entry(0) / 32) >> (entry(0) % 32);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * kAdjustThreads + threadIdx.x;
-    v[i] = e < n ? x[e] : from_f<T>(0.f);
-    b[i] = bias && e < n ? __ldg(bias + e) : 0.f;
-    m[i] = mask && e < n ? __ldg(mask + (e0 + e) / 32) : ~0u;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = entry(i);
+      v[i] = e < n ? x[e] : from_f<T>(0.f);
+      if (bias && e < n) b[i] = __ldg(bias + e);
+      if (mask && e < n) m |= (__ldg(mask + e / 32) >> (e % 32) & 1u) << i;
+    }
   }
   float rep = 1.f, freq = 0.f, pres = 0.f;
   if (seen) {
@@ -65,23 +92,31 @@ __global__ void __launch_bounds__(kAdjustThreads) k_adjust(const AdjustArgs a) {
       const int id = __ldg(h + i);
       // in 64 bits: any 32-bit id may be there
       long long e = id;
-      if (a.sem_begin >= 0)
-        e = id == a.im_end ? a.n - 1 : (static_cast<long long>(id) - a.sem_begin < a.n - 1 ? static_cast<long long>(id) - a.sem_begin : -1);
+      if (a.sem_begin >= 0) {
+        e -= a.sem_begin;
+        if (e >= a.n - 1) e = -1;
+        if (id == a.im_end) e = a.n - 1;
+      }
       if (e >= e0 && e < e0 + n) atomicAdd(count + (e - e0), 1);
     }
     __syncthreads();
   }
   float* out = a.out + r * a.n + e0;
+  float y[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = i * kAdjustThreads + threadIdx.x;
-    if (e >= n) break;
     float l = to_f(v[i]);
-    const int c = seen ? count[e] : 0;
+    const int c = seen ? count[entry(i)] : 0;
     if (c > 0) l = (l > 0.f ? __fdiv_rn(l, rep) : l * rep) - freq * static_cast<float>(c) - pres;
     if (bias) l += b[i];
-    if (!(m[i] >> ((e0 + e) % 32) & 1u)) l = -INFINITY;
-    out[e] = l;
+    if (mask && !(m >> i & 1u)) l = -INFINITY;
+    y[i] = l;
+    if (!kWide && entry(i) < n) out[entry(i)] = l;
+  }
+  if (kWide && in) {
+    float4* o = reinterpret_cast<float4*>(out + entry(0));
+    o[0] = make_float4(y[0], y[1], y[2], y[3]);
+    o[1] = make_float4(y[4], y[5], y[6], y[7]);
   }
 }
 
@@ -107,9 +142,17 @@ extern "C" int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, cons
     if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return S2_EINVAL;
   const AdjustArgs a{n, sem_begin, im_end, logits, history, hist_len, hist_cols, penalties, bias, bias_stride,
                      mask, mask_stride, out};
+  const bool wide = n % kPer == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(out) % 16 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0 &&
+                    bias_stride % 4 == 0;
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    k_adjust<T><<<dim3(n / kSlice + (n % kSlice != 0), rows), kAdjustThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    const dim3 grid(n / kSlice + (n % kSlice != 0), rows);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (wide)
+      k_adjust<T, true><<<grid, kAdjustThreads, 0, st>>>(a);
+    else
+      k_adjust<T, false><<<grid, kAdjustThreads, 0, st>>>(a);
   });
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
