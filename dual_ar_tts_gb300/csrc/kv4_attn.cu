@@ -606,17 +606,18 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // row, and 32 values of two positions); its codes wait in registers while the page before is used.  fp32 queries
 // are two fp16 terms, and so are their weights: the products run twice, into the same sums.
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
-// queries alike.  Two blocks an SM overlap one's expanding and exponentials with the other's products.
+// queries alike.  A page's scores are computed while the softmax of the page before runs, and two blocks an SM
+// overlap one's expanding and exponentials with the other's products.
 constexpr int kTcCols = 128;
 template <int HD, int TN>
 struct Tc {
   static constexpr int kAtoms = HD / 64;                // 128-byte columns of Q and K
   static constexpr int kQAtom = kTcCols * 128, kKAtom = kPage * 128;
   static constexpr int kQ = 0, kK = kQ + TN * kAtoms * kQAtom, kV = kK + kAtoms * kKAtom, kVBuf = HD * 128,
-                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 4 * kPage, kBytes = kBars + 64 + 1024;
-  // tensor memory columns
-  static constexpr uint32_t kO = 0, kS = HD, kP = kS + kPage, kCols = 256;
-  static_assert(kP + TN * 32 <= kCols, "tensor memory");
+                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 2 * 4 * kPage, kBytes = kBars + 64 + 1024;
+  // tensor memory columns: the output, and two pages' scores, whose place their weights take
+  static constexpr uint32_t kO = 0, kS = HD, kCols = 256;
+  static_assert(kS + 2 * kPage <= kCols && TN * 32 <= kPage, "tensor memory");
 };
 
 // A wait that gives up after a second or so (a few hundred ns a try).
@@ -678,9 +679,9 @@ struct PageCodes {
       vp[t] = in ? __ldg(reinterpret_cast<const uint32_t*>(vb + kPage * B::kRow + r * B::kPar) + warp * HD / 128) : 0;
     }
   }
-  // Into the operands' layouts.  Values whose parameters are no numbers become zeros; returns whether there are.
-  __device__ __forceinline__ bool expand_to(uint8_t* kt, uint8_t* vt, uint16_t* odd_rows) {
-    const int row = threadIdx.x / 2, half = threadIdx.x % 2, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  // Into the operands' layouts.
+  __device__ __forceinline__ void expand_keys(uint8_t* kt) const {
+    const int row = threadIdx.x / 2, half = threadIdx.x % 2;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int u = kU == 2 ? i ^ half : i;  // the halves write different banks
@@ -698,6 +699,10 @@ struct PageCodes {
         *reinterpret_cast<uint4*>(to + (((chunk + j) ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
+  }
+  // Values whose parameters are no numbers become zeros; returns whether there are.
+  __device__ __forceinline__ bool expand_values(uint8_t* vt, uint16_t* odd_rows) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     uint16_t odd = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -768,12 +773,14 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
   PageCodes<HD> held;
   int next = p0;
+  int id = next < p1 ? __ldg(table + next) : -1;  // of page `next`, on its way a page ahead
   // the codes of the next page that is there; `next` ends at p1
   auto fetch = [&] {
     for (; next < p1; ++next) {
-      const int id = __ldg(table + next);
-      if (id >= 0 && id < a.c.n_pages) {
-        held.load(heads + static_cast<size_t>(id) * a.c.n_kv_head * B::kBytes, len - next * kPage);
+      const int now = id;
+      id = next + 1 < p1 ? __ldg(table + next + 1) : -1;
+      if (now >= 0 && now < a.c.n_pages) {
+        held.load(heads + static_cast<size_t>(now) * a.c.n_kv_head * B::kBytes, len - next * kPage);
         return;
       }
       if (threadIdx.x == 0) kv4_bad(a.c.status);
@@ -841,31 +848,51 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   uint32_t poison = 0;          // groups of the output that are no numbers
   bool ok = true;
   int done = 0;                 // pages used
-  while (next < p1) {
-    const int p = next;
-    uint8_t* vt = sm + M::kV + (done & 1) * M::kVBuf;  // the products of two pages ago are finished
-    const bool mine = held.expand_to(sm + M::kK, vt, odd_rows);
+  auto issue_scores = [&](int n) {  // of the keys in place, as page n
+    tc_fence_after();
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k)
+        tc_mma(tm + M::kS + (n & 1) * kPage, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
+               desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
+               t > 0 || k > 0);
+    tc_commit(bars);
+  };
+  bool have = next < p1, odd = false;
+  int p = next;  // the page whose scores are under way
+  if (have) {
+    held.expand_keys(sm + M::kK);
+    const bool mine = held.expand_values(sm + M::kV, odd_rows);
     fence_proxy_async_smem();
-    const bool odd = __syncthreads_or(mine);
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-#pragma unroll
-      for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          tc_mma(tm + M::kS, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
-                 desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
-                 t > 0 || k > 0);
-      tc_commit(bars);
-    }
+    odd = __syncthreads_or(mine);
+    if (threadIdx.x == 0) issue_scores(0);
     ++next;
     fetch();
-    ok = ok && wait_short(bars, done & 1);
+  }
+  while (have) {
+    const bool more = next < p1;
+    const int after = next;
+    const uint32_t tscore = tlane + M::kS + (done & 1) * kPage;
+    ok = ok && wait_short(bars, done & 1);  // page `done`: its scores are there, its keys used up
+    if (more) held.expand_keys(sm + M::kK);
+    if (done > 0) ok = ok && wait_short(bars + 1, (done - 1) & 1);  // the output so far; weights and values used up
+    bool mine = false;
+    if (more) {
+      mine = held.expand_values(sm + M::kV + ((done + 1) & 1) * M::kVBuf, odd_rows + ((done + 1) & 1) * 2 * kPage);
+      fence_proxy_async_smem();
+    }
+    const bool odd_after = __syncthreads_or(mine);
+    if (more) {
+      if (threadIdx.x == 0) issue_scores(done + 1);
+      ++next;
+      fetch();
+    }
     __syncwarp();
     tc_fence_after();
     float s[kPage];
-    tmem_ld32(tlane + M::kS, *reinterpret_cast<float(*)[32]>(s));
-    tmem_ld32(tlane + M::kS + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+    tmem_ld32(tscore, *reinterpret_cast<float(*)[32]>(s));
+    tmem_ld32(tscore + 32, *reinterpret_cast<float(*)[32]>(s + 32));
     if ((p + 1) * kPage > least) {
       const int seen = lim - p * kPage;
 #pragma unroll
@@ -876,14 +903,12 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
       for (int i = 0; i < kPage && p * kPage + i < lim; ++i)
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          if (odd_rows[w * 32 + i / 2] >> (8 * (i & 1)) & 1) poison |= 1u << (w * HD / 128);
+          if (odd_rows[(done & 1) * 2 * kPage + w * 32 + i / 2] >> (8 * (i & 1)) & 1) poison |= 1u << (w * HD / 128);
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPage; ++i) top = fmaxf(top, s[i]);
     top *= factor;
-    if (done > 0) ok = ok && wait_short(bars + 1, (done - 1) & 1);  // the output so far; weights are used up
     __syncwarp();
-    tc_fence_after();
     const bool rise = top + lift > kWeightShift + kSlack;
     if (__any_sync(0xffffffffu, rise)) {
       const float m = lift == 3e38f ? -INFINITY : kWeightShift - lift, mn = fmaxf(m, top);
@@ -915,28 +940,36 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
       w[i / 2] = h2_bits(__floats2half2_rn(s[i], s[i + 1]));
     }
     l += sum;
-    tmem_st32(tlane + M::kP, w);
+    tmem_st32(tscore, w);
     if constexpr (TN == 2) {
 #pragma unroll
       for (int i = 0; i < kPage; i += 2) {
         const float2 h = __half22float2(bits_h2(w[i / 2]));
         w[i / 2] = h2_bits(__floats2half2_rn(s[i] - h.x, s[i + 1] - h.y));
       }
-      tmem_st32(tlane + M::kP + 32, w);
+      tmem_st32(tscore + 32, w);
     }
     tc_fence_before();
-    if (!__syncthreads_and(ok)) break;
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      wait_short(bars, (done + 1) & 1);  // what may still be under way, before its memory is given back
+      break;
+    }
     if (threadIdx.x == 0) {
       tc_fence_after();
 #pragma unroll
       for (int t = 0; t < TN; ++t)
 #pragma unroll
         for (int k = 0; k < kPage / 16; ++k)
-          tc_mma_tmem_a(tm + M::kO, tm + M::kP + t * 32 + k * 8, desc_sw128(smem_u32(vt) + k * 32),
-                        idesc_f16(kTcCols, HD), done > 0 || t > 0 || k > 0);
+          tc_mma_tmem_a(tm + M::kO, tm + M::kS + (done & 1) * kPage + t * 32 + k * 8,
+                        desc_sw128(smem_u32(sm + M::kV) + (done & 1) * M::kVBuf + k * 32), idesc_f16(kTcCols, HD),
+                        done > 0 || t > 0 || k > 0);
       tc_commit(bars + 1);
     }
     ++done;
+    have = more;
+    odd = odd_after;
+    p = after;
   }
   if (done > 0) ok = wait_short(bars + 1, (done - 1) & 1) && ok;
   __syncwarp();
