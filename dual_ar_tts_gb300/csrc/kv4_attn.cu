@@ -601,20 +601,21 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // ---- many columns: a block takes 128 columns of one KV head, each a row of tcgen05 products, a page at a time:
 //   S[128][64] = Q[128][hd] K[64][hd]^T      Q and K in shared memory
 //   O[128][hd] += P[128][64] V[64][hd]       P in tensor memory, V^T in shared memory
-// A thread has one column: its scores, its maximum, its sum and its row of the output, all in tensor memory lanes
-// of its own, so the softmax has no shuffles.  Every page is expanded once for all columns (each thread half a key
-// row, and 32 values of two positions); its codes wait in registers while the page before is used.  fp32 queries
-// are two fp16 terms, and so are their weights: the products run twice, into the same sums.
+// Four warps have a column a thread: its scores, its maximum, its sum and its row of the output, all in tensor
+// memory lanes of its own, so the softmax has no shuffles.  Four more expand every page once for all columns (a
+// thread half a key row, and 32 values of two positions; its codes wait in registers while the page before is
+// used) and issue the products; they run a page ahead, so that expanding, exponentials and products overlap.  The
+// two blocks of an SM share its tensor memory.  fp32 queries are two fp16 terms, and so are their weights: the
+// products run twice, into the same sums.
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
-// queries alike.  A page's scores are computed while the softmax of the page before runs, and two blocks an SM
-// overlap one's expanding and exponentials with the other's products.
+// queries alike.
 constexpr int kTcCols = 128;
 template <int HD, int TN>
 struct Tc {
   static constexpr int kAtoms = HD / 64;                // 128-byte columns of Q and K
   static constexpr int kQAtom = kTcCols * 128, kKAtom = kPage * 128;
   static constexpr int kQ = 0, kK = kQ + TN * kAtoms * kQAtom, kV = kK + kAtoms * kKAtom, kVBuf = HD * 128,
-                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 2 * 4 * kPage, kBytes = kBars + 64 + 1024;
+                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 2 * 4 * kPage, kBytes = kBars + 128 + 1024;
   // tensor memory columns: the output, and two pages' scores, whose place their weights take
   static constexpr uint32_t kO = 0, kS = HD, kCols = 256;
   static_assert(kS + 2 * kPage <= kCols && TN * 32 <= kPage, "tensor memory");
@@ -643,66 +644,90 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Barrier `id` of `n` threads: whether `v` holds for all of them.
+__device__ __forceinline__ bool named_and(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
 // fp16 operands, fp32 sums, both K-major (the format fields of fp16 are zero)
 constexpr uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// What a thread holds of a page: half a row of keys, and words 32 w / 8 .. of the values of positions 2l, 2l + 1
-// (hd 128: 16 bytes, hd 64: 8), with their parameters.
+// What a thread holds of a page: hd/64 groups of 32 keys of a row, and 32 (hd 64: 16) values of positions l and
+// l + 32, l its lane, with their parameters.  Neighbouring lanes read neighbouring 16 bytes of keys and, of values,
+// neighbouring rows.  (Positions l and l + 32 share a word of the weights and of V^T: its K index 2l, 2l + 1.)
 template <int HD>
 struct PageCodes {
-  static constexpr int kU = HD / 64;  // 16-byte units of half a key row; 8-byte units of values
+  static constexpr int kU = HD / 64, kGroups = HD / kKvGroup;
   uint4 k[kU];
   uint32_t kp[kU], vp[2];
   uint2 v[2][kU];
   // `rows` of the page are in the sequence
   __device__ __forceinline__ void load(const uint8_t* block, int rows) {
     using B = Kv4Block<HD>;
-    const int row = threadIdx.x / 2, half = threadIdx.x % 2, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint8_t* p = block + row * B::kRow + half * (kU * 16);
-    const uint8_t* q = block + kPage * B::kRow + row * B::kPar + half * (kU * 4);
-    const bool live = row < rows;
+    const int tid = threadIdx.x % kTcCols, lane = tid % 32, warp = tid / 32;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      k[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
-      kp[i] = live ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0;
+      const int unit = tid + i * kTcCols;
+      const bool in = unit / kGroups < rows;
+      k[i] = in ? __ldg(reinterpret_cast<const uint4*>(block) + unit) : make_uint4(0, 0, 0, 0);
+      kp[i] = in ? __ldg(reinterpret_cast<const uint32_t*>(block + kPage * B::kRow) + unit) : 0;
     }
     const uint8_t* vb = block + B::kHalf;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int r = 2 * lane + t;
+      const int r = lane + 32 * t;
       const bool in = r < rows;
-#pragma unroll
-      for (int i = 0; i < kU; ++i)
-        v[t][i] = in ? __ldg(reinterpret_cast<const uint2*>(vb + r * B::kRow + warp * (kU * 8)) + i) : make_uint2(0, 0);
+      const uint8_t* p = vb + r * B::kRow + warp * (kU * 8);
+      if constexpr (kU == 2) {
+        const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+        v[t][0] = make_uint2(u.x, u.y), v[t][1] = make_uint2(u.z, u.w);
+      } else {
+        v[t][0] = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+      }
       vp[t] = in ? __ldg(reinterpret_cast<const uint32_t*>(vb + kPage * B::kRow + r * B::kPar) + warp * HD / 128) : 0;
     }
   }
   // Into the operands' layouts.
   __device__ __forceinline__ void expand_keys(uint8_t* kt) const {
-    const int row = threadIdx.x / 2, half = threadIdx.x % 2;
+    const int tid = threadIdx.x % kTcCols;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const int u = kU == 2 ? i ^ half : i;  // the halves write different banks
-      const uint4 kc = kU == 2 && half ? k[i ^ (kU - 1)] : k[i];
-      const uint32_t a = kU == 2 && half ? kp[i ^ (kU - 1)] : kp[i];
-      const Pair pk(a, a);
-      const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
-      // elements 32 (half kU + u) ..: hd 128: atom `half`, chunks 4u ..; hd 64: the one atom, chunks 4 half ..
-      uint8_t* to = kt + (kU == 2 ? half * (kPage * 128) : 0) + row * 128;
-      const int chunk = kU == 2 ? 4 * u : 4 * half;
+      const int unit = tid + i * kTcCols, row = unit / kGroups, group = unit % kGroups;
+      const Pair pk(kp[i], kp[i]);
+      const bool turn = group / 2;  // the two atoms' chunks share banks: the second's go in another order
+      const uint32_t kw[4] = {turn ? k[i].z : k[i].x, turn ? k[i].w : k[i].y, turn ? k[i].x : k[i].z, turn ? k[i].y : k[i].w};
+      uint8_t* to = kt + group / 2 * (kPage * 128) + row * 128;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t x[4];
         expand(kw[j], pk, x);
-        *reinterpret_cast<uint4*>(to + (((chunk + j) ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
+        const int chunk = group % 2 * 4 + (turn ? j ^ 2 : j);
+        *reinterpret_cast<uint4*>(to + ((chunk ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
   }
   // Values whose parameters are no numbers become zeros; returns whether there are.
   __device__ __forceinline__ bool expand_values(uint8_t* vt, uint16_t* odd_rows) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 4;
     uint16_t odd = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -732,16 +757,22 @@ struct PageCodes {
 };
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
+__global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   constexpr int TN = sizeof(T) == 4 ? 2 : 1;
   using B = Kv4Block<HD>;
   using M = Tc<HD, TN>;
   extern __shared__ __align__(16) uint8_t smraw[];
   pdl_trigger();
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::kBars);  // scores, output
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 2);
-  uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [warp][position pair], a byte a position
+  // Barriers.  Scores of page n: scored[n % 2] (the products' arrival and their issuer's); its weights:
+  // weighed[n % 2]; the output with it: summed.  A barrier completes again only after all have seen it: page
+  // n + 2 is scored after the output of page n, which needs every column's weights.
+  uint64_t* scored = reinterpret_cast<uint64_t*>(sm + M::kBars);
+  uint64_t *weighed = scored + 2, *summed = scored + 4;
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(scored + 5);
+  int* place = reinterpret_cast<int*>(tbase + 1);               // [n % 2]: page n in the sequence, -1 after the last
+  uint32_t* odd_any = reinterpret_cast<uint32_t*>(place + 2);   // [n % 2][warp]: values that are no numbers
+  uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [n % 2][warp][lane], a byte a position
   const int warp = threadIdx.x / 32;
   const int kh = blockIdx.y, split = blockIdx.z;
   const Tile tile = find_tile(a.c, a.group, kTcCols, blockIdx.x);
@@ -769,247 +800,259 @@ __global__ void __launch_bounds__(kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   p1 = min(p1, (max(min(over + last / a.group + 1, len), 0) + kPage - 1) / kPage);
   const int least = min(over + tile.first / a.group + 1, len);
 
-  const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
-  const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
-  PageCodes<HD> held;
-  int next = p0;
-  int id = next < p1 ? __ldg(table + next) : -1;  // of page `next`, on its way a page ahead
-  // the codes of the next page that is there; `next` ends at p1
-  auto fetch = [&] {
-    for (; next < p1; ++next) {
-      const int now = id;
-      id = next + 1 < p1 ? __ldg(table + next + 1) : -1;
-      if (now >= 0 && now < a.c.n_pages) {
-        held.load(heads + static_cast<size_t>(now) * a.c.n_kv_head * B::kBytes, len - next * kPage);
-        return;
-      }
-      if (threadIdx.x == 0) kv4_bad(a.c.status);
-    }
-  };
-  fetch();
   if (threadIdx.x == 0) {
-    mbar_init(bars, 1);
-    mbar_init(bars + 1, 1);
+    mbar_init(scored, 2);
+    mbar_init(scored + 1, 2);
+    mbar_init(weighed, kTcCols);
+    mbar_init(weighed + 1, kTcCols);
+    mbar_init(summed, 1);
     fence_barrier_init();
   }
   if (warp == 0) {
     tmem_alloc(tbase, M::kCols);
     tmem_relinquish();
   }
-  // this thread's column
-  const int col = tile.first + threadIdx.x;
-  const bool live = col < cols;
-  const size_t at = static_cast<size_t>(q0 + (live ? col / a.group : 0)) * a.n_head + kh * a.group + (live ? col % a.group : 0);
-  const int lim = live ? min(over + col / a.group + 1, len) : 0;
-  float factor;
-  {
-    const T* q = static_cast<const T*>(a.q) + at * HD;
-    constexpr int kPer = 16 / sizeof(T);
-    float top = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < HD / kPer; ++i) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
-      const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) top = fmaxf(top, fabsf(to_f(e[k])));
-    }
-    const QueryScale qs(live ? top : 0.f, a.scale);
-    factor = qs.down;
-#pragma unroll 2
-    for (int i = 0; i < HD / 8; ++i) {
-      uint4 u[sizeof(T) / 2];
-#pragma unroll
-      for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
-        u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i * (sizeof(T) / 2) + k);
-      const T* v = reinterpret_cast<const T*>(u);
-      float x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = live ? to_f(v[k]) * qs.up : 0.f;
-      uint8_t* to = sm + M::kQ + i / 8 * M::kQAtom + threadIdx.x * 128 + (((i % 8) ^ (threadIdx.x & 7)) * 16);
-#pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        uint32_t r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          r[k] = h2_bits(__floats2half2_rn(x[k], x[k + 4]));
-          x[k] -= round_f16(x[k]);
-          x[k + 4] -= round_f16(x[k + 4]);
-        }
-        *reinterpret_cast<uint4*>(to + t * M::kAtoms * M::kQAtom) = make_uint4(r[0], r[1], r[2], r[3]);
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tbase, tlane = tm + (static_cast<uint32_t>(warp * 32) << 16);
 
-  float lift = 3e38f, l = 0.f;  // as Rows
-  uint32_t poison = 0;          // groups of the output that are no numbers
-  bool ok = true;
-  int done = 0;                 // pages used
-  auto issue_scores = [&](int n) {  // of the keys in place, as page n
-    tc_fence_after();
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k)
-        tc_mma(tm + M::kS + (n & 1) * kPage, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
-               desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
-               t > 0 || k > 0);
-    tc_commit(bars);
-  };
-  bool have = next < p1, odd = false;
-  int p = next;  // the page whose scores are under way
-  if (have) {
-    held.expand_keys(sm + M::kK);
-    const bool mine = held.expand_values(sm + M::kV, odd_rows);
-    fence_proxy_async_smem();
-    odd = __syncthreads_or(mine);
-    if (threadIdx.x == 0) issue_scores(0);
-    ++next;
-    fetch();
-  }
-  while (have) {
-    const bool more = next < p1;
-    const int after = next;
-    const uint32_t tscore = tlane + M::kS + (done & 1) * kPage;
-    ok = ok && wait_short(bars, done & 1);  // page `done`: its scores are there, its keys used up
-    if (more) held.expand_keys(sm + M::kK);
-    if (done > 0) ok = ok && wait_short(bars + 1, (done - 1) & 1);  // the output so far; weights and values used up
-    bool mine = false;
-    if (more) {
-      mine = held.expand_values(sm + M::kV + ((done + 1) & 1) * M::kVBuf, odd_rows + ((done + 1) & 1) * 2 * kPage);
-      fence_proxy_async_smem();
-    }
-    const bool odd_after = __syncthreads_or(mine);
-    if (more) {
-      if (threadIdx.x == 0) issue_scores(done + 1);
-      ++next;
-      fetch();
-    }
-    __syncwarp();
-    tc_fence_after();
-    float s[kPage];
-    tmem_ld32(tscore, *reinterpret_cast<float(*)[32]>(s));
-    tmem_ld32(tscore + 32, *reinterpret_cast<float(*)[32]>(s + 32));
-    if ((p + 1) * kPage > least) {
-      const int seen = lim - p * kPage;
-#pragma unroll
-      for (int i = 0; i < kPage; ++i)
-        if (i >= seen) s[i] = -INFINITY;
-    }
-    if (odd)
-      for (int i = 0; i < kPage && p * kPage + i < lim; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (odd_rows[(done & 1) * 2 * kPage + w * 32 + i / 2] >> (8 * (i & 1)) & 1) poison |= 1u << (w * HD / 128);
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPage; ++i) top = fmaxf(top, s[i]);
-    top *= factor;
-    __syncwarp();
-    const bool rise = top + lift > kWeightShift + kSlack;
-    if (__any_sync(0xffffffffu, rise)) {
-      const float m = lift == 3e38f ? -INFINITY : kWeightShift - lift, mn = fmaxf(m, top);
-      float keep = 1.f;
-      if (rise) {
-        keep = ex2(m - mn);
-        lift = kWeightShift - mn;
-        l *= keep;
-      }
-      __syncwarp();
-      if (done > 0)
-#pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          uint32_t r[32];
-          tmem_ld32(tlane + M::kO + c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * keep);
-          tmem_st32(tlane + M::kO + c, r);
+  if (warp >= 4) {
+    // ---------------------------------------------------------------- expanding and issuing
+    const bool lead = threadIdx.x == kTcCols;
+    const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
+    const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
+    PageCodes<HD> held;
+    int next = p0;
+    int id = next < p1 ? __ldg(table + next) : -1;  // of page `next`, on its way a page ahead
+    // the codes of the next page that is there; `next` ends at p1
+    auto fetch = [&] {
+      for (; next < p1; ++next) {
+        const int now = id;
+        id = next + 1 < p1 ? __ldg(table + next + 1) : -1;
+        if (now >= 0 && now < a.c.n_pages) {
+          held.load(heads + static_cast<size_t>(now) * a.c.n_kv_head * B::kBytes, len - next * kPage);
+          return;
         }
-    }
-    float sum = 0.f;
-    uint32_t w[32];
-#pragma unroll
-    for (int i = 0; i < kPage; i += 2) {
-      s[i] = ex2(__fmaf_rn(s[i], factor, lift));
-      s[i + 1] = ex2(__fmaf_rn(s[i + 1], factor, lift));
-      sum += s[i] + s[i + 1];
-      w[i / 2] = h2_bits(__floats2half2_rn(s[i], s[i + 1]));
-    }
-    l += sum;
-    tmem_st32(tscore, w);
-    if constexpr (TN == 2) {
-#pragma unroll
-      for (int i = 0; i < kPage; i += 2) {
-        const float2 h = __half22float2(bits_h2(w[i / 2]));
-        w[i / 2] = h2_bits(__floats2half2_rn(s[i] - h.x, s[i + 1] - h.y));
+        if (lead) kv4_bad(a.c.status);
       }
-      tmem_st32(tscore + 32, w);
-    }
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      wait_short(bars, (done + 1) & 1);  // what may still be under way, before its memory is given back
-      break;
-    }
-    if (threadIdx.x == 0) {
+    };
+    fetch();
+    named_bar(2, 2 * kTcCols);  // queries, barriers and tensor memory are there
+    tc_fence_after();
+    const uint32_t tm = *tbase;
+    auto output = [&](int n) {  // the products of page n's weights and values
+      const bool there = wait_short(weighed + (n & 1), n >> 1 & 1);
       tc_fence_after();
+      if (!there) return;
 #pragma unroll
       for (int t = 0; t < TN; ++t)
 #pragma unroll
         for (int k = 0; k < kPage / 16; ++k)
-          tc_mma_tmem_a(tm + M::kO, tm + M::kS + (done & 1) * kPage + t * 32 + k * 8,
-                        desc_sw128(smem_u32(sm + M::kV) + (done & 1) * M::kVBuf + k * 32), idesc_f16(kTcCols, HD),
-                        done > 0 || t > 0 || k > 0);
-      tc_commit(bars + 1);
-    }
-    ++done;
-    have = more;
-    odd = odd_after;
-    p = after;
-  }
-  if (done > 0) ok = wait_short(bars + 1, (done - 1) & 1) && ok;
-  __syncwarp();
-  tc_fence_after();
-  if (!ok && a.c.status && threadIdx.x == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+          tc_mma_tmem_a(tm + M::kO, tm + M::kS + (n & 1) * kPage + t * 32 + k * 8,
+                        desc_sw128(smem_u32(sm + M::kV) + (n & 1) * M::kVBuf + k * 32), idesc_f16(kTcCols, HD),
+                        n > 0 || t > 0 || k > 0);
+      tc_commit(summed);
+    };
+    bool ok = true;
+    int n = 0;
+    for (; next < p1; ++n) {
+      if (n > 0) ok = wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
+      __syncwarp();
+      held.expand_keys(sm + M::kK);
+      if (n > 1) ok = ok && wait_short(summed, n & 1);  // page n - 2: its values, its weights
+      __syncwarp();
+      const bool odd = held.expand_values(sm + M::kV + (n & 1) * M::kVBuf, odd_rows + (n & 1) * 2 * kPage);
+      const bool some = __any_sync(0xffffffffu, odd);
+      if (threadIdx.x % 32 == 0) odd_any[(n & 1) * 4 + warp - 4] = some;
+      if (lead) place[n & 1] = next;
+      fence_proxy_async_smem();
+      ok = named_and(1, kTcCols, ok);
+      if (!ok) break;
+      if (lead) {
+        tc_fence_after();
 #pragma unroll
-  for (int c = 0; c < HD; c += 32) {
-    float o[32];
-    __syncwarp();
-    if (done > 0) {
-      tmem_ld32(tlane + M::kO + c, o);
-    } else {
+        for (int t = 0; t < TN; ++t)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0.f;
-    }
-    if (poison >> (c / 32) & 1)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = NAN;
-    if (live && whole) {
-      constexpr int kPer = 16 / sizeof(T);
-      T* out = static_cast<T*>(a.out) + at * HD + c;
-#pragma unroll
-      for (int i = 0; i < 32; i += kPer) {
-        uint4 u;
-        T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) e[k] = from_f<T>(l == 0.f ? 0.f : o[i + k] * inv);
-        *reinterpret_cast<uint4*>(out + i) = u;
+          for (int k = 0; k < HD / 16; ++k)
+            tc_mma(tm + M::kS + (n & 1) * kPage, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
+                   desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
+                   t > 0 || k > 0);
+        tc_commit(scored + (n & 1));
+        mbar_arrive(scored + (n & 1));
+        if (n > 0) output(n - 1);
       }
-    } else if (live) {
-      float4* out = reinterpret_cast<float4*>(a.part_o + (at * a.n_split + split) * HD + c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      __syncwarp();
+      ++next;
+      fetch();
     }
+    if (lead) {
+      if (ok && n > 0) output(n - 1);
+      place[n & 1] = -1;
+      mbar_arrive(scored + (n & 1));
+      mbar_arrive(scored + (n & 1));
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- a column a thread
+    const int col = tile.first + threadIdx.x;
+    const bool live = col < cols;
+    const size_t at = static_cast<size_t>(q0 + (live ? col / a.group : 0)) * a.n_head + kh * a.group + (live ? col % a.group : 0);
+    const int lim = live ? min(over + col / a.group + 1, len) : 0;
+    float factor;
+    {
+      const T* q = static_cast<const T*>(a.q) + at * HD;
+      constexpr int kPer = 16 / sizeof(T);
+      float top = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < HD / kPer; ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) top = fmaxf(top, fabsf(to_f(e[k])));
+      }
+      const QueryScale qs(live ? top : 0.f, a.scale);
+      factor = qs.down;
+#pragma unroll 2
+      for (int i = 0; i < HD / 8; ++i) {
+        uint4 u[sizeof(T) / 2];
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
+          u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i * (sizeof(T) / 2) + k);
+        const T* v = reinterpret_cast<const T*>(u);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = live ? to_f(v[k]) * qs.up : 0.f;
+        uint8_t* to = sm + M::kQ + i / 8 * M::kQAtom + threadIdx.x * 128 + (((i % 8) ^ (threadIdx.x & 7)) * 16);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+          uint32_t r[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            r[k] = h2_bits(__floats2half2_rn(x[k], x[k + 4]));
+            x[k] -= round_f16(x[k]);
+            x[k + 4] -= round_f16(x[k + 4]);
+          }
+          *reinterpret_cast<uint4*>(to + t * M::kAtoms * M::kQAtom) = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    named_bar(2, 2 * kTcCols);
+    tc_fence_after();
+    const uint32_t tlane = *tbase + (static_cast<uint32_t>(warp * 32) << 16);
+
+    float lift = 3e38f, l = 0.f;  // as Rows
+    uint32_t poison = 0;          // groups of the output that are no numbers
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      ok = __all_sync(0xffffffffu, wait_short(scored + (n & 1), n >> 1 & 1));
+      if (!ok) break;
+      const int p = place[n & 1];
+      if (p < 0) break;
+      tc_fence_after();
+      const uint32_t tscore = tlane + M::kS + (n & 1) * kPage;
+      float s[kPage];
+      tmem_ld32(tscore, *reinterpret_cast<float(*)[32]>(s));
+      tmem_ld32(tscore + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+      if ((p + 1) * kPage > least) {
+        const int seen = lim - p * kPage;
+#pragma unroll
+        for (int i = 0; i < kPage; ++i)
+          if (i >= seen) s[i] = -INFINITY;
+      }
+      const uint32_t* oa = odd_any + (n & 1) * 4;
+      if (oa[0] | oa[1] | oa[2] | oa[3])
+        for (int i = 0; i < kPage && p * kPage + i < lim; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (odd_rows[(n & 1) * 2 * kPage + w * 32 + i % 32] >> (8 * (i / 32)) & 1) poison |= 1u << (w * HD / 128);
+      float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < kPage; ++i) tops[i % 4] = fmaxf(tops[i % 4], s[i]);
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * factor;
+      const bool rise = top + lift > kWeightShift + kSlack;
+      if (__any_sync(0xffffffffu, rise)) {
+        const float m = lift == 3e38f ? -INFINITY : kWeightShift - lift, mn = fmaxf(m, top);
+        float keep = 1.f;
+        if (rise) {
+          keep = ex2(m - mn);
+          lift = kWeightShift - mn;
+          l *= keep;
+        }
+        __syncwarp();
+        if (n > 0) {
+          ok = __all_sync(0xffffffffu, wait_short(summed, (n - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 16) {
+            float o[16];
+            uint32_t r[16];
+            tmem_ld16(tlane + M::kO + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * keep);
+            tmem_st16(tlane + M::kO + c, r);
+          }
+        }
+      }
+      float sum[4] = {};
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        s[i] = ex2(__fmaf_rn(s[i], factor, lift));
+        s[i + 32] = ex2(__fmaf_rn(s[i + 32], factor, lift));
+        sum[i % 4] += s[i] + s[i + 32];
+        w[i] = h2_bits(__floats2half2_rn(s[i], s[i + 32]));
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(tscore, w);
+      if constexpr (TN == 2) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 h = __half22float2(bits_h2(w[i]));
+          w[i] = h2_bits(__floats2half2_rn(s[i] - h.x, s[i + 32] - h.y));
+        }
+        tmem_st32(tscore + 32, w);
+      }
+      tc_fence_before();
+      mbar_arrive(weighed + (n & 1));
+    }
+    if (n > 0) ok = __all_sync(0xffffffffu, wait_short(summed, (n - 1) & 1)) && ok;
+    tc_fence_after();
+    if (!ok && a.c.status && threadIdx.x % 32 == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 16) {
+      float o[16] = {};
+      __syncwarp();
+      if (n > 0) tmem_ld16(tlane + M::kO + c, o);
+      if (poison >> (c / 32) & 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = NAN;
+      if (live && whole) {
+        constexpr int kPer = 16 / sizeof(T);
+        T* out = static_cast<T*>(a.out) + at * HD + c;
+#pragma unroll
+        for (int i = 0; i < 16; i += kPer) {
+          uint4 u;
+          T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) e[k] = from_f<T>(l == 0.f ? 0.f : o[i + k] * inv);
+          *reinterpret_cast<uint4*>(out + i) = u;
+        }
+      } else if (live) {
+        float4* out = reinterpret_cast<float4*>(a.part_o + (at * a.n_split + split) * HD + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+    }
+    if (live && !whole) a.part_ml[at * a.n_split + split] = make_float2(lift == 3e38f ? -INFINITY : kWeightShift - lift, l);
+    tc_fence_before();
   }
-  if (live && !whole) a.part_ml[at * a.n_split + split] = make_float2(lift == 3e38f ? -INFINITY : kWeightShift - lift, l);
-  tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tm, M::kCols);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(*tbase, M::kCols);
+  }
 }
 
 // The splits of each (row, query head): one block each, a thread an element of every kJoinParts-th split (4 parts
@@ -1091,7 +1134,7 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
   if (p.many) {
     constexpr int smem = Tc<HD, sizeof(T) == 4 ? 2 : 1>::kBytes;
     if (!allow_smem<k_kv4_tc<T, HD>, smem>()) return S2_ECUDA;
-    k_kv4_tc<T, HD><<<grid, kTcCols, smem, st>>>(a);
+    k_kv4_tc<T, HD><<<grid, 2 * kTcCols, smem, st>>>(a);
   } else {
     constexpr int smem = kDecodeSmem<HD>;
     if (!allow_smem<k_kv4_decode<T, HD>, smem>()) return S2_ECUDA;
