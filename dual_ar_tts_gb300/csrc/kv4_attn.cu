@@ -40,7 +40,7 @@ struct AttnArgs {
   int group;         // query heads of a KV head
   float scale;
   void* out;
-  int n_split, split_pages;
+  int n_split, split_pages, join_heads;
   float* part_o;     // [row][head][split][hd]
   float2* part_ml;   // [row][head][split]
 };
@@ -603,10 +603,10 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 //   O[128][hd] += P[128][64] V[64][hd]       P in tensor memory, V^T in shared memory
 // Four warps have a column a thread: its scores, its maximum, its sum and its row of the output, all in tensor
 // memory lanes of its own, so the softmax has no shuffles.  Four more expand every page once for all columns (a
-// thread half a key row, and 32 values of two positions; its codes wait in registers while the page before is
-// used) and issue the products; they run a page ahead, so that expanding, exponentials and products overlap.  The
-// two blocks of an SM share its tensor memory.  fp32 queries are two fp16 terms, and so are their weights: the
-// products run twice, into the same sums.
+// thread 64 key codes and 32 values of two positions; its codes wait in registers while the page before is used),
+// and a ninth issues the products, so that expanding, exponentials and products overlap.  The two blocks of an SM
+// share its tensor memory.  fp32 queries are two fp16 terms, and so are their weights: the products run twice,
+// into the same sums.
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
 // queries alike.
 constexpr int kTcCols = 128;
@@ -615,7 +615,7 @@ struct Tc {
   static constexpr int kAtoms = HD / 64;                // 128-byte columns of Q and K
   static constexpr int kQAtom = kTcCols * 128, kKAtom = kPage * 128;
   static constexpr int kQ = 0, kK = kQ + TN * kAtoms * kQAtom, kV = kK + kAtoms * kKAtom, kVBuf = HD * 128,
-                       kOdd = kV + 2 * kVBuf, kBars = kOdd + 2 * 4 * kPage, kBytes = kBars + 128 + 1024;
+                       kOdd = kV + 3 * kVBuf, kBars = kOdd + 4 * 4 * kPage, kBytes = kBars + 128 + 1024;
   // tensor memory columns: the output, and two pages' scores, whose place their weights take
   static constexpr uint32_t kO = 0, kS = HD, kCols = 256;
   static_assert(kS + 2 * kPage <= kCols && TN * 32 <= kPage, "tensor memory");
@@ -652,18 +652,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Barrier `id` of `n` threads: whether `v` holds for all of them.
-__device__ __forceinline__ bool named_and(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(v))
-      : "memory");
-  return r != 0;
 }
 
 // fp16 operands, fp32 sums, both K-major (the format fields of fp16 are zero)
@@ -756,23 +744,24 @@ struct PageCodes {
   }
 };
 
+constexpr int kTcThreads = 2 * kTcCols + 32;  // 96 registers each: two blocks an SM
 template <typename T, int HD>
-__global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
+__global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
   constexpr int TN = sizeof(T) == 4 ? 2 : 1;
   using B = Kv4Block<HD>;
   using M = Tc<HD, TN>;
   extern __shared__ __align__(16) uint8_t smraw[];
   pdl_trigger();
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
-  // Barriers.  Scores of page n: scored[n % 2] (the products' arrival and their issuer's); its weights:
-  // weighed[n % 2]; the output with it: summed.  A barrier completes again only after all have seen it: page
-  // n + 2 is scored after the output of page n, which needs every column's weights.
-  uint64_t* scored = reinterpret_cast<uint64_t*>(sm + M::kBars);
-  uint64_t *weighed = scored + 2, *summed = scored + 4;
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(scored + 5);
-  int* place = reinterpret_cast<int*>(tbase + 1);               // [n % 2]: page n in the sequence, -1 after the last
-  uint32_t* odd_any = reinterpret_cast<uint32_t*>(place + 2);   // [n % 2][warp]: values that are no numbers
-  uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [n % 2][warp][lane], a byte a position
+  // Barriers.  Operands of page n: filled[n % 2]; its scores: scored[n % 2] (the products' arrival and their
+  // issuer's); its weights: weighed[n % 2]; the output with it: summed[n % 2].  A barrier completes again only after
+  // all that wait for it have seen it, since each of them has a part in what comes before its next completion.
+  uint64_t* filled = reinterpret_cast<uint64_t*>(sm + M::kBars);
+  uint64_t *scored = filled + 2, *weighed = filled + 4, *summed = filled + 6;
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(filled + 8);
+  int* place = reinterpret_cast<int*>(tbase + 1);                  // [n % 4]: page n in the sequence, -1 after the last
+  uint8_t* odd_any = reinterpret_cast<uint8_t*>(place + 4);        // [n % 4][warp]: values that are no numbers
+  uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [n % 4][warp][lane], a byte a position
   const int warp = threadIdx.x / 32;
   const int kh = blockIdx.y, split = blockIdx.z;
   const Tile tile = find_tile(a.c, a.group, kTcCols, blockIdx.x);
@@ -801,11 +790,12 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   const int least = min(over + tile.first / a.group + 1, len);
 
   if (threadIdx.x == 0) {
-    mbar_init(scored, 2);
-    mbar_init(scored + 1, 2);
-    mbar_init(weighed, kTcCols);
-    mbar_init(weighed + 1, kTcCols);
-    mbar_init(summed, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(filled + i, 4);
+      mbar_init(scored + i, 2);
+      mbar_init(weighed + i, kTcCols);
+      mbar_init(summed + i, 1);
+    }
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -813,9 +803,53 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
     tmem_relinquish();
   }
 
-  if (warp >= 4) {
-    // ---------------------------------------------------------------- expanding and issuing
-    const bool lead = threadIdx.x == kTcCols;
+  // A wait that gave up is not the last thing that waits: from there on nobody waits, and the call reports it.
+  bool ok = true;
+  if (warp == 8) {
+    // ---------------------------------------------------------------- issuing the products
+    named_bar(2, kTcThreads);  // queries, barriers and tensor memory are there
+    if (threadIdx.x % 32 == 0) {
+      tc_fence_after();
+      const uint32_t tm = *tbase;
+      for (int n = 0;; ++n) {
+        ok = ok && wait_short(filled + (n & 1), n >> 1 & 1);
+        const bool end = !ok || place[n & 3] < 0;
+        if (!end) {
+          if (n > 1) ok = wait_short(summed + (n & 1), (n - 2) >> 1 & 1);  // the weights of page n - 2 lie there
+          tc_fence_after();
+          const uint32_t ts = tm + M::kS + (n & 1) * kPage;
+#pragma unroll
+          for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              tc_mma(ts, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
+                     desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
+                     t > 0 || k > 0);
+          tc_commit(scored + (n & 1));
+        } else {
+          mbar_arrive(scored + (n & 1));
+        }
+        mbar_arrive(scored + (n & 1));
+        if (n > 0) {  // the output with page n - 1
+          const int o = n - 1;
+          ok = ok && wait_short(weighed + (o & 1), o >> 1 & 1);
+          tc_fence_after();
+          const uint32_t tp = tm + M::kS + (o & 1) * kPage;
+#pragma unroll
+          for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int k = 0; k < kPage / 16; ++k)
+              tc_mma_tmem_a(tm + M::kO, tp + t * 32 + k * 8, desc_sw128(smem_u32(sm + M::kV) + o % 3 * M::kVBuf + k * 32),
+                            idesc_f16(kTcCols, HD), o > 0 || t > 0 || k > 0);
+          tc_commit(summed + (o & 1));
+        }
+        if (end) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- expanding
+    const int lane = threadIdx.x % 32;
     const int32_t* table = a.c.table + static_cast<size_t>(tile.seq) * a.c.table_cols;
     const uint8_t* heads = static_cast<const uint8_t*>(a.c.pages) + static_cast<size_t>(kh) * B::kBytes;
     PageCodes<HD> held;
@@ -830,65 +864,33 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
           held.load(heads + static_cast<size_t>(now) * a.c.n_kv_head * B::kBytes, len - next * kPage);
           return;
         }
-        if (lead) kv4_bad(a.c.status);
+        if (lane == 0) kv4_bad(a.c.status);
       }
     };
     fetch();
-    named_bar(2, 2 * kTcCols);  // queries, barriers and tensor memory are there
-    tc_fence_after();
-    const uint32_t tm = *tbase;
-    auto output = [&](int n) {  // the products of page n's weights and values
-      const bool there = wait_short(weighed + (n & 1), n >> 1 & 1);
-      tc_fence_after();
-      if (!there) return;
-#pragma unroll
-      for (int t = 0; t < TN; ++t)
-#pragma unroll
-        for (int k = 0; k < kPage / 16; ++k)
-          tc_mma_tmem_a(tm + M::kO, tm + M::kS + (n & 1) * kPage + t * 32 + k * 8,
-                        desc_sw128(smem_u32(sm + M::kV) + (n & 1) * M::kVBuf + k * 32), idesc_f16(kTcCols, HD),
-                        n > 0 || t > 0 || k > 0);
-      tc_commit(summed);
-    };
-    bool ok = true;
-    int n = 0;
-    for (; next < p1; ++n) {
-      if (n > 0) ok = wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
+    named_bar(2, kTcThreads);
+    for (int n = 0;; ++n) {
+      const bool end = next >= p1;
+      // values first: there are three buffers of them, while the keys wait for the scores of the page before
+      if (n > 2) ok = ok && wait_short(summed + ((n - 3) & 1), (n - 3) >> 1 & 1);  // the values of page n - 3 are used up
       __syncwarp();
-      held.expand_keys(sm + M::kK);
-      if (n > 1) ok = ok && wait_short(summed, n & 1);  // page n - 2: its values, its weights
+      bool odd = false;
+      if (!end) odd = held.expand_values(sm + M::kV + n % 3 * M::kVBuf, odd_rows + (n & 3) * 2 * kPage);
+      if (n > 0) ok = ok && wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
       __syncwarp();
-      const bool odd = held.expand_values(sm + M::kV + (n & 1) * M::kVBuf, odd_rows + (n & 1) * 2 * kPage);
-      const bool some = __any_sync(0xffffffffu, odd);
-      if (threadIdx.x % 32 == 0) odd_any[(n & 1) * 4 + warp - 4] = some;
-      if (lead) place[n & 1] = next;
+      if (!end) held.expand_keys(sm + M::kK);
+      odd = __any_sync(0xffffffffu, odd);
       fence_proxy_async_smem();
-      ok = named_and(1, kTcCols, ok);
-      if (!ok) break;
-      if (lead) {
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < TN; ++t)
-#pragma unroll
-          for (int k = 0; k < HD / 16; ++k)
-            tc_mma(tm + M::kS + (n & 1) * kPage, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
-                   desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
-                   t > 0 || k > 0);
-        tc_commit(scored + (n & 1));
-        mbar_arrive(scored + (n & 1));
-        if (n > 0) output(n - 1);
-      }
       __syncwarp();
+      if (lane == 0) {
+        odd_any[(n & 3) * 4 + warp - 4] = odd;
+        if (warp == 4) place[n & 3] = end ? -1 : next;
+        mbar_arrive(filled + (n & 1));
+      }
+      if (end) break;
       ++next;
       fetch();
     }
-    if (lead) {
-      if (ok && n > 0) output(n - 1);
-      place[n & 1] = -1;
-      mbar_arrive(scored + (n & 1));
-      mbar_arrive(scored + (n & 1));
-    }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- a column a thread
     const int col = tile.first + threadIdx.x;
@@ -897,56 +899,61 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
     const int lim = live ? min(over + col / a.group + 1, len) : 0;
     float factor;
     {
-      const T* q = static_cast<const T*>(a.q) + at * HD;
-      constexpr int kPer = 16 / sizeof(T);
+      // eight loads of a row under way together; rows are read twice
+      constexpr int kPer = 16 / sizeof(T), kUnits = 8;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + at * HD);
+      uint4 u[kUnits];
       float top = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < HD / kPer; ++i) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + i);
-        const T* e = reinterpret_cast<const T*>(&u);
+      constexpr int kTurns = HD / kPer / kUnits > 0 ? HD / kPer / kUnits : 1, kTurn = HD / kPer / kTurns;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) top = fmaxf(top, fabsf(to_f(e[k])));
+      for (int h = 0; h < kTurns; ++h) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) u[i] = __ldg(q + h * kTurn + i);
+        const T* e = reinterpret_cast<const T*>(u);
+#pragma unroll
+        for (int i = 0; i < kTurn * kPer; ++i) top = fmaxf(top, fabsf(to_f(e[i])));
       }
       const QueryScale qs(live ? top : 0.f, a.scale);
       factor = qs.down;
-#pragma unroll 2
-      for (int i = 0; i < HD / 8; ++i) {
-        uint4 u[sizeof(T) / 2];
 #pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
-          u[k] = __ldg(reinterpret_cast<const uint4*>(q) + i * (sizeof(T) / 2) + k);
+      for (int h = 0; h < kTurns; ++h) {
+        if (kTurns > 1)
+#pragma unroll
+          for (int i = 0; i < kTurn; ++i) u[i] = __ldg(q + h * kTurn + i);
         const T* v = reinterpret_cast<const T*>(u);
-        float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = live ? to_f(v[k]) * qs.up : 0.f;
-        uint8_t* to = sm + M::kQ + i / 8 * M::kQAtom + threadIdx.x * 128 + (((i % 8) ^ (threadIdx.x & 7)) * 16);
+        for (int g = 0; g < kTurn * kPer / 8; ++g) {
+          const int i = h * (kTurn * kPer / 8) + g;
+          float x[8];
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          uint32_t r[4];
+          for (int k = 0; k < 8; ++k) x[k] = live ? to_f(v[g * 8 + k]) * qs.up : 0.f;
+          uint8_t* to = sm + M::kQ + i / 8 * M::kQAtom + threadIdx.x * 128 + (((i % 8) ^ (threadIdx.x & 7)) * 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            r[k] = h2_bits(__floats2half2_rn(x[k], x[k + 4]));
-            x[k] -= round_f16(x[k]);
-            x[k + 4] -= round_f16(x[k + 4]);
+          for (int t = 0; t < TN; ++t) {
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              r[k] = h2_bits(__floats2half2_rn(x[k], x[k + 4]));
+              x[k] -= round_f16(x[k]);
+              x[k + 4] -= round_f16(x[k + 4]);
+            }
+            *reinterpret_cast<uint4*>(to + t * M::kAtoms * M::kQAtom) = make_uint4(r[0], r[1], r[2], r[3]);
           }
-          *reinterpret_cast<uint4*>(to + t * M::kAtoms * M::kQAtom) = make_uint4(r[0], r[1], r[2], r[3]);
         }
       }
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    named_bar(2, 2 * kTcCols);
+    named_bar(2, kTcThreads);
     tc_fence_after();
     const uint32_t tlane = *tbase + (static_cast<uint32_t>(warp * 32) << 16);
 
     float lift = 3e38f, l = 0.f;  // as Rows
     uint32_t poison = 0;          // groups of the output that are no numbers
-    bool ok = true;
     int n = 0;
     for (;; ++n) {
       ok = __all_sync(0xffffffffu, wait_short(scored + (n & 1), n >> 1 & 1));
-      if (!ok) break;
-      const int p = place[n & 1];
+      const int p = ok ? place[n & 3] : -1;
       if (p < 0) break;
       tc_fence_after();
       const uint32_t tscore = tlane + M::kS + (n & 1) * kPage;
@@ -959,12 +966,11 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
         for (int i = 0; i < kPage; ++i)
           if (i >= seen) s[i] = -INFINITY;
       }
-      const uint32_t* oa = odd_any + (n & 1) * 4;
-      if (oa[0] | oa[1] | oa[2] | oa[3])
+      if (*reinterpret_cast<const uint32_t*>(odd_any + (n & 3) * 4))
         for (int i = 0; i < kPage && p * kPage + i < lim; ++i)
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            if (odd_rows[(n & 1) * 2 * kPage + w * 32 + i % 32] >> (8 * (i / 32)) & 1) poison |= 1u << (w * HD / 128);
+            if (odd_rows[(n & 3) * 2 * kPage + w * 32 + i % 32] >> (8 * (i / 32)) & 1) poison |= 1u << (w * HD / 128);
       float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
       for (int i = 4; i < kPage; ++i) tops[i % 4] = fmaxf(tops[i % 4], s[i]);
@@ -980,7 +986,7 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
         }
         __syncwarp();
         if (n > 0) {
-          ok = __all_sync(0xffffffffu, wait_short(summed, (n - 1) & 1));
+          ok = __all_sync(0xffffffffu, wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -1016,7 +1022,7 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
       tc_fence_before();
       mbar_arrive(weighed + (n & 1));
     }
-    if (n > 0) ok = __all_sync(0xffffffffu, wait_short(summed, (n - 1) & 1)) && ok;
+    if (n > 0) ok = __all_sync(0xffffffffu, wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1)) && ok;
     tc_fence_after();
     if (!ok && a.c.status && threadIdx.x % 32 == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1055,43 +1061,48 @@ __global__ void __launch_bounds__(2 * kTcCols, 2) k_kv4_tc(const AttnArgs a) {
   }
 }
 
-// The splits of each (row, query head): one block each, a thread an element of every kJoinParts-th split (4 parts
-// for more than 16 splits: one row over 30000 positions 36 -> 22 us; 1 for fewer, of which there are many rows).
-// The splits' maxima decide the weights of their outputs; parts are added in order.
+// The splits of a row's query heads, `a.join_heads` of them a block, a thread an element of every kJoinParts-th split
+// (4 parts for more than 16 splits: one row over 30000 positions 36 -> 22 us; 1 for fewer, of which there are many
+// rows).  The splits' maxima decide the weights of their outputs; parts are added in order.
 template <typename T, int HD, int kJoinParts>
 __global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) {
   __shared__ float so[kJoinParts][HD], sl[kJoinParts];
-  const int item = blockIdx.x, row = item / a.n_head, e = threadIdx.x % HD, part = threadIdx.x / HD;
+  const int row = blockIdx.x, e = threadIdx.x % HD, part = threadIdx.x / HD;
   const int seq = seq_of_row(a.c.q_start, a.c.n_seq, row);
   const bool live = seq < a.c.n_seq && row >= __ldg(a.c.q_start + seq) && __ldg(a.c.q_start + seq + 1) <= a.c.n_rows;
   const int len = live ? min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage) : 0;
   pdl_wait();  // every thread: no end before the splits'
-  if (!live) return;
   const int pages = (len + kPage - 1) / kPage;
   const int n = min((pages + a.split_pages - 1) / a.split_pages, a.n_split);
-  if (n <= 1) return;  // written by its one block
-  const float2* ml = a.part_ml + static_cast<size_t>(item) * a.n_split;
-  const float* po = a.part_o + static_cast<size_t>(item) * a.n_split * HD + e;
-  float m = -INFINITY;
-  for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
-  m = warp_max(m);
-  const float base = m == -INFINITY ? 0.f : m;
-  float o = 0.f, l = 0.f;
+  if (!live || n <= 1) return;  // written by its one block
+  const int h1 = min(a.n_head, static_cast<int>(blockIdx.y + 1) * a.join_heads);
+  for (int h = blockIdx.y * a.join_heads; h < h1; ++h) {
+    const size_t item = static_cast<size_t>(row) * a.n_head + h;
+    const float2* ml = a.part_ml + item * a.n_split;
+    const float* po = a.part_o + item * a.n_split * HD + e;
+    float m = -INFINITY;
+    for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
+    m = warp_max(m);
+    const float base = m == -INFINITY ? 0.f : m;
+    float o = 0.f, l = 0.f;
 #pragma unroll 4
-  for (int s = part; s < n; s += kJoinParts) {
-    const float2 v = __ldcg(ml + s);
-    const float f = ex2(v.x - base);
-    l += f * v.y;
-    o += f * __ldcg(po + static_cast<size_t>(s) * HD);
-  }
-  so[part][e] = o;
-  if (e == 0) sl[part] = l;
-  __syncthreads();
-  if (part > 0) return;
-  o = l = 0.f;
+    for (int s = part; s < n; s += kJoinParts) {
+      const float2 v = __ldcg(ml + s);
+      const float f = ex2(v.x - base);
+      l += f * v.y;
+      o += f * __ldcg(po + static_cast<size_t>(s) * HD);
+    }
+    if constexpr (kJoinParts > 1) {
+      __syncthreads();  // the head before is joined
+      so[part][e] = o;
+      if (e == 0) sl[part] = l;
+      __syncthreads();
+      o = l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kJoinParts; ++i) o += so[i][e], l += sl[i];
-  static_cast<T*>(a.out)[static_cast<size_t>(item) * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
+      for (int i = 0; i < kJoinParts; ++i) o += so[i][e], l += sl[i];
+    }
+    if (part == 0) static_cast<T*>(a.out)[item * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
+  }
 }
 
 // How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 32 columns on
@@ -1103,7 +1114,7 @@ __global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) 
 // so that it does not shrink with a larger max_len.
 struct Plan {
   bool many;
-  int tiles, n_split, split_pages;
+  int tiles, n_split, split_pages, join_heads;
   size_t o_bytes, bytes;
 };
 Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len, bool two) {
@@ -1119,6 +1130,8 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
+  // heads of a joining block: about 2000 blocks (a block a head of 874 rows took 17 us, most of them with nothing to do)
+  p.join_heads = std::max(1, std::min(n_head, static_cast<int>(static_cast<long long>(n_rows) * n_head / 2048)));
   const int most = std::min(want, (pages + 1) / 2);
   if (most > 1) {
     const size_t parts = static_cast<size_t>(n_rows) * n_head * most;
@@ -1134,7 +1147,7 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
   if (p.many) {
     constexpr int smem = Tc<HD, sizeof(T) == 4 ? 2 : 1>::kBytes;
     if (!allow_smem<k_kv4_tc<T, HD>, smem>()) return S2_ECUDA;
-    k_kv4_tc<T, HD><<<grid, 2 * kTcCols, smem, st>>>(a);
+    k_kv4_tc<T, HD><<<grid, kTcThreads, smem, st>>>(a);
   } else {
     constexpr int smem = kDecodeSmem<HD>;
     if (!allow_smem<k_kv4_decode<T, HD>, smem>()) return S2_ECUDA;
@@ -1142,7 +1155,7 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
   }
   if (p.n_split > 1) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.c.n_rows * a.n_head);
+    cfg.gridDim = dim3(a.c.n_rows, (a.n_head + a.join_heads - 1) / a.join_heads);
     cfg.blockDim = dim3(p.n_split > 16 ? 4 * HD : HD);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -1188,7 +1201,7 @@ extern "C" int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, i
   if (max_len == 0 || max_len > cache->table_cols * kPage) max_len = cache->table_cols * kPage;
   const Plan p = plan(cache->n_seq, cache->n_rows, n_head, cache->n_kv_head, cache->head_dim, max_len, dtype == S2_F32);
   if (p.bytes > 0 && (!workspace || ws_bytes < p.bytes)) return S2_EINVAL;
-  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, nullptr, nullptr};
+  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, p.join_heads, nullptr, nullptr};
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
   return with_dtype(dtype, [&](auto t) {
