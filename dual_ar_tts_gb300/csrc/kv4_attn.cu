@@ -40,7 +40,7 @@ struct AttnArgs {
   int group;         // query heads of a KV head
   float scale;
   void* out;
-  int n_split, split_pages, join_heads;
+  int n_split, split_pages;
   float* part_o;     // [row][head][split][hd]
   float2* part_ml;   // [row][head][split]
 };
@@ -1061,48 +1061,74 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
   }
 }
 
-// The splits of a row's query heads, `a.join_heads` of them a block, a thread an element of every kJoinParts-th split
-// (4 parts for more than 16 splits: one row over 30000 positions 36 -> 22 us; 1 for fewer, of which there are many
-// rows).  The splits' maxima decide the weights of their outputs; parts are added in order.
-template <typename T, int HD, int kJoinParts>
-__global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) {
-  __shared__ float so[kJoinParts][HD], sl[kJoinParts];
-  const int row = blockIdx.x, e = threadIdx.x % HD, part = threadIdx.x / HD;
+// What joins a row's splits: how many of them there are (1 or 0: written by its one block).  For every thread of the
+// block, before anything ends.
+__device__ __forceinline__ int row_splits(const AttnArgs& a, int row) {
   const int seq = seq_of_row(a.c.q_start, a.c.n_seq, row);
   const bool live = seq < a.c.n_seq && row >= __ldg(a.c.q_start + seq) && __ldg(a.c.q_start + seq + 1) <= a.c.n_rows;
   const int len = live ? min(max(__ldg(a.c.lengths + seq), 0), a.c.table_cols * kPage) : 0;
-  pdl_wait();  // every thread: no end before the splits'
-  const int pages = (len + kPage - 1) / kPage;
-  const int n = min((pages + a.split_pages - 1) / a.split_pages, a.n_split);
-  if (!live || n <= 1) return;  // written by its one block
-  const int h1 = min(a.n_head, static_cast<int>(blockIdx.y + 1) * a.join_heads);
-  for (int h = blockIdx.y * a.join_heads; h < h1; ++h) {
-    const size_t item = static_cast<size_t>(row) * a.n_head + h;
-    const float2* ml = a.part_ml + item * a.n_split;
-    const float* po = a.part_o + item * a.n_split * HD + e;
-    float m = -INFINITY;
-    for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
-    m = warp_max(m);
-    const float base = m == -INFINITY ? 0.f : m;
-    float o = 0.f, l = 0.f;
+  pdl_wait();  // no end before the splits'
+  return min(((len + kPage - 1) / kPage + a.split_pages - 1) / a.split_pages, a.n_split);
+}
+
+// Many splits (more than 16): a block a (row, query head), a thread an element of every fourth of them; the four
+// parts are added in order.  One row over 30000 positions: 36 -> 22 us against one part.
+constexpr int kJoinParts = 4, kJoinMany = 16;
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join_many(const AttnArgs a) {
+  __shared__ float so[kJoinParts][HD], sl[kJoinParts];
+  const int row = blockIdx.x, e = threadIdx.x % HD, part = threadIdx.x / HD;
+  const int n = row_splits(a, row);
+  if (n <= 1) return;
+  const size_t item = static_cast<size_t>(row) * a.n_head + blockIdx.y;
+  const float2* ml = a.part_ml + item * a.n_split;
+  const float* po = a.part_o + item * a.n_split * HD + e;
+  float m = -INFINITY;
+  for (int s = threadIdx.x % 32; s < n; s += 32) m = fmaxf(m, __ldcg(&ml[s].x));
+  m = warp_max(m);
+  const float base = m == -INFINITY ? 0.f : m;
+  float o = 0.f, l = 0.f;
 #pragma unroll 4
-    for (int s = part; s < n; s += kJoinParts) {
-      const float2 v = __ldcg(ml + s);
-      const float f = ex2(v.x - base);
-      l += f * v.y;
-      o += f * __ldcg(po + static_cast<size_t>(s) * HD);
-    }
-    if constexpr (kJoinParts > 1) {
-      __syncthreads();  // the head before is joined
-      so[part][e] = o;
-      if (e == 0) sl[part] = l;
-      __syncthreads();
-      o = l = 0.f;
-#pragma unroll
-      for (int i = 0; i < kJoinParts; ++i) o += so[i][e], l += sl[i];
-    }
-    if (part == 0) static_cast<T*>(a.out)[item * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
+  for (int s = part; s < n; s += kJoinParts) {
+    const float2 v = __ldcg(ml + s);
+    const float f = ex2(v.x - base);
+    l += f * v.y;
+    o += f * __ldcg(po + static_cast<size_t>(s) * HD);
   }
+  so[part][e] = o;
+  if (e == 0) sl[part] = l;
+  __syncthreads();
+  if (part > 0) return;
+  o = l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinParts; ++i) o += so[i][e], l += sl[i];
+  static_cast<T*>(a.out)[item * HD + e] = from_f<T>(l == 0.f ? 0.f : o / l);
+}
+
+// Up to 16 splits: a warp a query head, eight heads of a row a block, so that a row with nothing to join costs
+// little and one with something has all its heads under way (874 rows, 60 of them split: 23 us -> 6).
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) k_kv4_join_few(const AttnArgs a) {
+  constexpr int E = HD / 32;
+  const int row = blockIdx.x, lane = threadIdx.x % 32, h = blockIdx.y * 8 + threadIdx.x / 32;
+  const int n = row_splits(a, row);
+  if (n <= 1 || h >= a.n_head) return;
+  const size_t item = static_cast<size_t>(row) * a.n_head + h;
+  const float2 ml = lane < n ? __ldcg(a.part_ml + item * a.n_split + lane) : make_float2(-INFINITY, 0.f);
+  const float* po = a.part_o + item * a.n_split * HD + lane;
+  const float m = warp_max(ml.x);
+  const float f = ex2(ml.x - (m == -INFINITY ? 0.f : m));
+  const float l = warp_sum(lane < n ? f * ml.y : 0.f);
+  float o[E] = {};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float w = __shfl_sync(0xffffffffu, f, s);
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] += w * __ldcg(po + static_cast<size_t>(s) * HD + 32 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    static_cast<T*>(a.out)[item * HD + lane + 32 * i] = from_f<T>(l == 0.f ? 0.f : o[i] / l);
 }
 
 // How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 32 columns on
@@ -1114,7 +1140,7 @@ __global__ void __launch_bounds__(HD * kJoinParts) k_kv4_join(const AttnArgs a) 
 // so that it does not shrink with a larger max_len.
 struct Plan {
   bool many;
-  int tiles, n_split, split_pages, join_heads;
+  int tiles, n_split, split_pages;
   size_t o_bytes, bytes;
 };
 Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len, bool two) {
@@ -1130,8 +1156,6 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
-  // heads of a joining block: about 2000 blocks (a block a head of 874 rows took 17 us, most of them with nothing to do)
-  p.join_heads = std::max(1, std::min(n_head, static_cast<int>(static_cast<long long>(n_rows) * n_head / 2048)));
   const int most = std::min(want, (pages + 1) / 2);
   if (most > 1) {
     const size_t parts = static_cast<size_t>(n_rows) * n_head * most;
@@ -1155,15 +1179,16 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
   }
   if (p.n_split > 1) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.c.n_rows, (a.n_head + a.join_heads - 1) / a.join_heads);
-    cfg.blockDim = dim3(p.n_split > 16 ? 4 * HD : HD);
+    const bool many = p.n_split > kJoinMany;
+    cfg.gridDim = dim3(a.c.n_rows, many ? a.n_head : (a.n_head + 7) / 8);
+    cfg.blockDim = dim3(many ? HD * kJoinParts : 256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, p.n_split > 16 ? k_kv4_join<T, HD, 4> : k_kv4_join<T, HD, 1>, a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, many ? k_kv4_join_many<T, HD> : k_kv4_join_few<T, HD>, a) != cudaSuccess)
       return S2_ECUDA;
   }
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
@@ -1201,7 +1226,7 @@ extern "C" int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, i
   if (max_len == 0 || max_len > cache->table_cols * kPage) max_len = cache->table_cols * kPage;
   const Plan p = plan(cache->n_seq, cache->n_rows, n_head, cache->n_kv_head, cache->head_dim, max_len, dtype == S2_F32);
   if (p.bytes > 0 && (!workspace || ws_bytes < p.bytes)) return S2_EINVAL;
-  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, p.join_heads, nullptr, nullptr};
+  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, nullptr, nullptr};
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
   return with_dtype(dtype, [&](auto t) {
