@@ -1131,13 +1131,16 @@ __global__ void __launch_bounds__(256) k_kv4_join_few(const AttnArgs a) {
     static_cast<T*>(a.out)[item * HD + lane + 32 * i] = from_f<T>(l == 0.f ? 0.f : o[i] / l);
 }
 
-// How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 32 columns on
-// average (rows times query heads of a KV head; fp32 queries count twice): 8 sequences of 4000 positions take 34 us
-// against 55 at 16 columns, 43 against 56 at 32.  Splits: the blocks that the 152 SMs hold at once (4 an SM; of the
-// kernel for many columns 2), twice that where there are many items of what may be different lengths (32 of
-// 512..4096: 32 us against 46), three times for many columns; of at least two pages (an even number: they are taken
-// two at a time), at most 128.  The workspace is sized for the most splits that any length up to max_len can get,
-// so that it does not shrink with a larger max_len.
+// How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 12 columns on
+// average (rows times query heads of a KV head; fp32 queries count twice): 8 sequences of 4000 positions take 35 us
+// against 33 at 10 columns on average, 37 against 42 at 18.  Splits, of at least two pages (an even number: they are taken two
+// at a time), at most 128:
+//  - few columns: the blocks that the 152 SMs hold at once (4 an SM), twice that where there are many items of what
+//    may be different lengths (32 of 512..4096: 32 us against 46);
+//  - many columns: the blocks that they hold at once (2 an SM); two where that gives none and there are few rounds,
+//    for the longest sequence (5 pieces, one of 42 pages and four of 20: 52 us against 61).
+// The workspace is sized for the most splits that any length up to max_len can get, so that it does not shrink with
+// a larger max_len.
 struct Plan {
   bool many;
   int tiles, n_split, split_pages;
@@ -1146,13 +1149,14 @@ struct Plan {
 Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len, bool two) {
   Plan p{};
   const long long group = n_head / n_kv_head, columns = n_rows * group * (two ? 2 : 1);
-  p.many = columns > 32ll * n_seq;
+  p.many = columns > 12ll * n_seq;
   const int cols = p.many ? kTcCols : two ? 4 : 8;
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
   const long long items = static_cast<long long>(p.tiles) * n_kv_head;
-  const int room = p.many ? 152 * 4 : items < 152 ? 152 * 4 : 152 * 8;
-  const int want = static_cast<int>(std::min(std::max(1ll, room / items), 128ll));
+  const long long room = p.many ? 152 * 2 : items < 152 ? 152 * 4 : 152 * 8;
+  const long long least = p.many && items < 152 * 4 ? 2 : 1;
+  const int want = static_cast<int>(std::min(std::max(least, room / items), 128ll));
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
