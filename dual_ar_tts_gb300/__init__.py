@@ -230,46 +230,58 @@ def quantize_e4m3(w):
 
 # ------------------------------------- 4-bit weights, 4-bit cache, adjusted logits
 
-# A call of a few microseconds is soon outweighed by what Python does around it, so the checks below are few
-# expressions of plain values, each property of a tensor read once.
+# A call of a few microseconds is soon outweighed by what Python does around it (torch's own x.add_(1) takes 7.5 us
+# on a Grace core), so what these calls use of torch is looked up once, and their checks are few expressions that
+# read each property of a tensor once: 13.3 us a call of a small matmul became 12.7, of which 3 are the launch and 3
+# the output's allocation.
 
-_kinds = None    # torch element type -> S2_* code
+class _Hot:
+    """What the calls below use of torch and of the library."""
+    __slots__ = ("torch", "lib", "kinds", "stream", "device", "empty", "u8", "i32", "f16", "bf16", "f32")
 
-
-def _code(t):
-    global _kinds
-    if _kinds is None:
+    def __init__(self):
         import torch
-        _kinds = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}
-    code = _kinds.get(t.dtype)
-    if code is None:
-        raise ValueError("the element type must be fp32, bf16 or fp16")
-    return code
+        self.torch, self.lib, self.empty = torch, load(), torch.empty
+        self.kinds = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}
+        self.stream = torch._C._cuda_getCurrentRawStream     # of a device number, as an integer
+        self.device = torch._C._cuda_getDevice               # the current one's number
+        self.u8, self.i32 = torch.uint8, torch.int32
+        self.f16, self.bf16, self.f32 = torch.float16, torch.bfloat16, torch.float32
 
 
-def _on(dev, *tensors):
-    """All given tensors are on CUDA device number `dev`."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            dev = -1
-    if dev < 0:
-        raise ValueError("tensors must be on one CUDA device")
+_hot = None
 
 
-def _launch(torch, fn, dev, *args):
+def _bind():
+    global _hot
+    _hot = _Hot()
+    return _hot
+
+
+def _bad(msg):
+    raise ValueError(msg)
+
+
+def _launch(h, fn, dev, *args):
     """Call an entry point on the current stream of device number `dev`, with that device current meanwhile."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
+    if dev == h.device():
+        rc = fn(*args, h.stream(dev))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+        with h.torch.cuda.device(dev):
+            rc = fn(*args, h.stream(dev))
     if rc != S2_OK:
         raise S2Error(fn.__name__, rc, "see include/s2frame.h for what the call takes")
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _off(dev, *tensors):
+    """Whether one of the given tensors is not on CUDA device number `dev`."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            return True
+    return False
+
+
+_DEVICE = "tensors must be on one CUDA device, the operand fp32, bf16 or fp16"
 
 
 def _rows16(x):
@@ -285,51 +297,58 @@ def quantize_q4(w, group: int = 32):
     """Device matrix [rows][cols] (fp32, bf16 or fp16) -> (uint8 codes [rows][ceil(cols/128)*64], bf16 scales
     [rows][ceil(cols/128)*(128/group)]): 4-bit codes with a scale per `group` (32, 64 or 128) columns; layout in
     s2frame.h."""
-    import torch
-    dt, dev = _code(w), w.get_device()
-    _on(dev)
+    h = _hot or _bind()
+    dt, dev = h.kinds.get(w.dtype), w.get_device()
+    if dt is None or dev < 0:
+        _bad(_DEVICE)
     if w.dim() != 2 or group not in (32, 64, 128) or w.shape[1] % group or not w.numel():
-        raise ValueError("quantize_q4 takes a 2-D tensor, its columns a multiple of group: 32, 64 or 128")
+        _bad("quantize_q4 takes a 2-D tensor, its columns a multiple of group: 32, 64 or 128")
     w = w.contiguous()
     rows, cols = w.shape
     blocks = -(-cols // 128)
-    codes = torch.empty((rows, blocks * 64), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((rows, blocks * (128 // group)), dtype=torch.bfloat16, device=w.device)
-    _launch(torch, load().s2_quantize_q4, dev, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(),
-            scales.data_ptr())
+    codes = h.empty((rows, blocks * 64), dtype=h.u8, device=w.device)
+    scales = h.empty((rows, blocks * (128 // group)), dtype=h.bf16, device=w.device)
+    _launch(h, h.lib.s2_quantize_q4, dev, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
     """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type.
     workspace, a uint8 tensor of s2_q4_matmul_workspace bytes, is allocated where none is given."""
-    import torch
-    dt, dev = _code(x), x.get_device()
-    _on(dev, codes, scales, out, workspace)
+    h = _hot or _bind()
+    dt, dev = h.kinds.get(x.dtype), x.get_device()
+    if dt is None or dev < 0 or codes.get_device() != dev or scales.get_device() != dev:
+        _bad(_DEVICE)
     if x.dim() != 2 or codes.dim() != 2 or group not in (32, 64, 128):
-        raise ValueError("q4_matmul takes x [n][k], codes and scales of quantize_q4 and its group: 32, 64 or 128")
+        _bad("q4_matmul takes x [n][k], codes and scales of quantize_q4 and its group: 32, 64 or 128")
     n, k = x.shape
     m, width = codes.shape
     if k % group or width != -(-k // 128) * 64 or scales.shape != (m, width * 2 // group) or \
-            codes.dtype is not torch.uint8 or scales.dtype is not torch.bfloat16 or not codes.is_contiguous() or \
+            codes.dtype is not h.u8 or scales.dtype is not h.bf16 or not codes.is_contiguous() or \
             not scales.is_contiguous():
-        raise ValueError("codes must be contiguous uint8 [rows][ceil(k/128)*64] and scales contiguous bf16 "
-                         "[rows][ceil(k/128)*(128/group)], k a multiple of group")
+        _bad("codes must be contiguous uint8 [rows][ceil(k/128)*64] and scales contiguous bf16 "
+             "[rows][ceil(k/128)*(128/group)], k a multiple of group")
     x = _rows16(x)
     if out is None:
-        out = torch.empty((n, m), dtype=x.dtype, device=x.device)
-    elif out.dtype is not x.dtype or out.shape != (n, m) or not out.is_contiguous():
-        raise ValueError("out must be contiguous [n][rows] of x's type")
-    lib = _lib or load()
-    if workspace is not None:
-        nbytes = workspace.nbytes
+        out = h.empty((n, m), dtype=x.dtype, device=x.device)
+    elif out.dtype is not x.dtype or out.shape != (n, m) or out.get_device() != dev or not out.is_contiguous():
+        _bad("out must be contiguous [n][rows] of x's type, on its device")
+    if workspace is None:
+        nbytes = h.lib.s2_q4_matmul_workspace(n, k, dt)
+        workspace = h.empty(nbytes, dtype=h.u8, device=x.device) if nbytes else None
     else:
-        nbytes = lib.s2_q4_matmul_workspace(n, k, dt)
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _launch(torch, lib.s2_q4_matmul, dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k,
-            group, out.data_ptr(), _ptr(workspace), nbytes)
+        nbytes = _workspace(workspace, dev)
+    ws = None if workspace is None else workspace.data_ptr()
+    _launch(h, h.lib.s2_q4_matmul, dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k,
+            group, out.data_ptr(), ws, nbytes)
     return out
+
+
+def _workspace(workspace, dev):
+    """Bytes of a caller's workspace."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad("workspace must be contiguous, on the operand's device")
+    return workspace.nbytes
 
 
 def rope_table(n_pos: int, head_dim: int, base: float = 1e6, bf16: bool = True, device="cuda"):
@@ -347,26 +366,28 @@ def kv4_pages(n_pages: int, n_kv_head: int, head_dim: int, device="cuda"):
     import torch
     nbytes = load().s2_kv4_page_bytes(n_kv_head, head_dim)
     if nbytes < 0 or n_pages < 1:
-        raise ValueError("kv4_pages takes head_dim 64 or 128 and positive counts")
+        _bad("kv4_pages takes head_dim 64 or 128 and positive counts")
     return torch.zeros((n_pages, n_kv_head, nbytes // n_kv_head), dtype=torch.uint8, device=device)
 
 
-def _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status):
-    i32 = torch.int32
-    if pages.dim() != 3 or table.dim() != 2:
-        raise ValueError("pages must be uint8 [n_pages][n_kv_head][80*head_dim], table int32 [n_seq][cols]")
+def _kv4(h, dev, pages, table, q_start, lengths, n_rows, status):
+    if dev < 0 or pages.get_device() != dev or table.get_device() != dev or q_start.get_device() != dev or \
+            lengths.get_device() != dev or (status is not None and status.get_device() != dev):
+        _bad(_DEVICE)
+    i32 = h.i32
+    if pages.dim() != 3 or table.dim() != 2 or pages.dtype is not h.u8 or table.dtype is not i32 or \
+            not pages.is_contiguous() or not table.is_contiguous():
+        _bad("pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim], table contiguous int32 [n_seq][cols]")
     n_pages, n_kv_head, block = pages.shape
     n_seq, cols = table.shape
-    _on(dev, pages, table, q_start, lengths, status)
-    if pages.dtype is not torch.uint8 or block not in (80 * 64, 80 * 128) or not pages.is_contiguous() or \
-            table.dtype is not i32 or not table.is_contiguous():
-        raise ValueError("pages must be contiguous uint8 [n_pages][n_kv_head][80*head_dim], table contiguous int32")
+    if block not in (80 * 64, 80 * 128):
+        _bad("pages must be uint8 [n_pages][n_kv_head][80*head_dim], head_dim 64 or 128")
     if q_start.dtype is not i32 or lengths.dtype is not i32 or q_start.shape != (n_seq + 1,) or \
             lengths.shape != (n_seq,) or not q_start.is_contiguous() or not lengths.is_contiguous() or \
             (status is not None and (status.dtype is not i32 or status.numel() != 1)):
-        raise ValueError("q_start must be int32 [n_seq+1], lengths int32 [n_seq], status one int32")
+        _bad("q_start must be int32 [n_seq+1], lengths int32 [n_seq], status one int32")
     return s2_kv4(pages.data_ptr(), n_pages, n_kv_head, block // 80, table.data_ptr(), cols, n_seq, q_start.data_ptr(),
-                  lengths.data_ptr(), n_rows, _ptr(status))
+                  lengths.data_ptr(), n_rows, None if status is None else status.data_ptr())
 
 
 def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=None, k_norm=None, eps: float = 1e-6,
@@ -376,46 +397,49 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
     given and rotated by rope's (rope_table) row of their position; keys and values are quantised.  table int32
     [n_seq][cols], q_start int32 [n_seq + 1] and lengths int32 [n_seq] place the rows (see s2_kv4 in s2frame.h).
     Returns the rotated queries [n_rows][n_head][head_dim]; rows behind the last sequence are left as they were."""
-    import torch
-    dt, dev = _code(qkv), qkv.get_device()
-    if qkv.dim() != 2:
-        raise ValueError("qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
+    h = _hot or _bind()
+    dt, dev = h.kinds.get(qkv.dtype), qkv.get_device()
+    if dt is None or qkv.dim() != 2:
+        _bad("qkv must be fp32, bf16 or fp16 [n_rows][(n_head + 2 n_kv_head)*head_dim]")
     n_rows, width = qkv.shape
-    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
-    hd, f32 = c.head_dim, torch.float32
-    _on(dev, rope, q_norm, k_norm, q_out)
+    c = _kv4(h, dev, pages, table, q_start, lengths, n_rows, status)
+    hd, f32 = c.head_dim, h.f32
     if n_head < 0 or width != (n_head + 2 * c.n_kv_head) * hd:
-        raise ValueError("qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
-    if rope.dtype is not f32 or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2) or not rope.is_contiguous():
-        raise ValueError("rope must be contiguous fp32 [n_pos][head_dim/2][2]")
+        _bad("qkv must be [n_rows][(n_head + 2 n_kv_head)*head_dim]")
+    if rope.dtype is not f32 or rope.dim() != 3 or rope.shape[1:] != (hd // 2, 2) or not rope.is_contiguous() or \
+            rope.get_device() != dev:
+        _bad("rope must be contiguous fp32 [n_pos][head_dim/2][2] on qkv's device")
     for w in (q_norm, k_norm):
-        if w is not None and (w.dtype is not f32 or w.shape != (hd,) or not w.is_contiguous()):
-            raise ValueError("norm weights must be fp32 [head_dim]")
+        if w is not None and (w.dtype is not f32 or w.shape != (hd,) or not w.is_contiguous() or
+                              w.get_device() != dev):
+            _bad("norm weights must be fp32 [head_dim] on qkv's device")
     qkv = _rows16(qkv)
     if q_out is None:
-        q_out = torch.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
-    elif q_out.dtype is not qkv.dtype or q_out.shape != (n_rows, n_head, hd) or not q_out.is_contiguous():
-        raise ValueError("q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type")
-    _launch(torch, (_lib or load()).s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head,
-            rope.data_ptr(), rope.shape[0], _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr())
+        q_out = h.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
+    elif q_out.dtype is not qkv.dtype or q_out.shape != (n_rows, n_head, hd) or q_out.get_device() != dev or \
+            not q_out.is_contiguous():
+        _bad("q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type, on its device")
+    _launch(h, h.lib.s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
+            rope.shape[0], None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+            eps, q_out.data_ptr())
     return q_out
 
 
 def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None, status=None):
     """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]."""
-    import torch
+    h = _hot or _bind()
     dev = pages.get_device()
-    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
-    shape, f16 = (c.n_kv_head, n_rows, c.head_dim), torch.float16
+    c = _kv4(h, dev, pages, table, q_start, lengths, n_rows, status)
+    shape, f16 = (c.n_kv_head, n_rows, c.head_dim), h.f16
     if k_out is None:
-        k_out = torch.empty(shape, dtype=f16, device=pages.device)
+        k_out = h.empty(shape, dtype=f16, device=pages.device)
+    elif k_out.dtype is not f16 or k_out.shape != shape or k_out.get_device() != dev or not k_out.is_contiguous():
+        _bad("outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim] on the pages' device")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=f16, device=pages.device)
-    _on(dev, k_out, v_out)
-    for t in (k_out, v_out):
-        if t.dtype is not f16 or t.shape != shape or not t.is_contiguous():
-            raise ValueError("outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim]")
-    _launch(torch, (_lib or load()).s2_kv4_read, dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
+        v_out = h.empty(shape, dtype=f16, device=pages.device)
+    elif v_out.dtype is not f16 or v_out.shape != shape or v_out.get_device() != dev or not v_out.is_contiguous():
+        _bad("outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim] on the pages' device")
+    _launch(h, h.lib.s2_kv4_read, dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
@@ -425,32 +449,30 @@ def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None,
     the rows' own keys and values already (kv4_append).  scale defaults to 1/sqrt(head_dim); max_len (the largest
     length expected, 0: what the table can hold) only sets how the work is split; workspace, a uint8 tensor of
     s2_kv4_attention_workspace bytes, is allocated where none is given."""
-    import torch
-    dt, dev = _code(q), q.get_device()
-    if q.dim() != 3:
-        raise ValueError("q must be [n_rows][n_head][head_dim]")
+    h = _hot or _bind()
+    dt, dev = h.kinds.get(q.dtype), q.get_device()
+    if dt is None or q.dim() != 3:
+        _bad("q must be fp32, bf16 or fp16 [n_rows][n_head][head_dim]")
     n_rows, n_head, hd = q.shape
-    c = _kv4(torch, dev, pages, table, q_start, lengths, n_rows, status)
+    c = _kv4(h, dev, pages, table, q_start, lengths, n_rows, status)
     n_kv = c.n_kv_head
-    _on(dev, out, workspace)
     if hd != c.head_dim or n_kv < 1 or n_head % n_kv or max_len < 0:
-        raise ValueError("q's heads must be a multiple of the cache's, of the same head_dim")
+        _bad("q's heads must be a multiple of the cache's, of the same head_dim")
     if not q.is_contiguous() or q.data_ptr() % 16:
-        q = q.clone(memory_format=torch.contiguous_format)
+        q = q.clone(memory_format=h.torch.contiguous_format)
     if out is None:
-        out = torch.empty_like(q)
-    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous, of q's shape and type")
-    lib = _lib or load()
-    if workspace is not None:
-        nbytes = workspace.nbytes
-    else:
+        out = h.empty((n_rows, n_head, hd), dtype=q.dtype, device=q.device)
+    elif out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != dev or not out.is_contiguous():
+        _bad("out must be contiguous, of q's shape and type, on its device")
+    if workspace is None:
         held = c.table_cols * S2_KV4_PAGE
-        nbytes = lib.s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd, min(max_len or held, held))
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _launch(torch, lib.s2_kv4_attention, dev, ctypes.byref(c), q.data_ptr(), dt, n_head,
-            hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(), _ptr(workspace), nbytes)
+        nbytes = h.lib.s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd, min(max_len or held, held))
+        workspace = h.empty(nbytes, dtype=h.u8, device=q.device) if nbytes else None
+    else:
+        nbytes = _workspace(workspace, dev)
+    _launch(h, h.lib.s2_kv4_attention, dev, ctypes.byref(c), q.data_ptr(), dt, n_head,
+            hd ** -0.5 if scale is None else scale, max_len, out.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), nbytes)
     return out
 
 
@@ -459,47 +481,48 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
     """Logits [rows][n] (fp32, bf16 or fp16) adjusted for a draw -> fp32 [rows][n] (see s2_adjust_logits).
     history int32 [rows][cols] with hist_len int32 [rows] and penalties fp32 [rows][3] of (repetition, frequency,
     presence); bias fp32 [rows or 1][n]; mask int32 or uint32 bits [rows or 1][ceil(n/32)].  Entry ids as in draw."""
-    import torch
-    dt, dev = _code(logits), logits.get_device()
-    _on(dev, logits, history, hist_len, penalties, bias, mask, out)
+    h = _hot or _bind()
+    dt, dev = h.kinds.get(logits.dtype), logits.get_device()
+    if dt is None or dev < 0 or _off(dev, history, hist_len, penalties, bias, mask, out):
+        _bad(_DEVICE)
     if logits.dim() != 2:
-        raise ValueError("logits must be [rows][n]")
+        _bad("logits must be [rows][n]")
     rows, n = logits.shape
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = h.i32, h.f32
     cols = bias_stride = mask_stride = 0
-    if history is None:
-        if penalties is not None or hist_len is not None:
-            raise ValueError("penalties and hist_len go with a history")
-    else:
+    hp = lp = pp = bp = mp = None       # device pointers of what is given
+    if history is not None:
         if history.dtype is not i32 or history.dim() != 2 or history.shape[0] != rows or \
                 not history.is_contiguous() or penalties is None or penalties.dtype is not f32 or \
                 penalties.shape != (rows, 3) or not penalties.is_contiguous():
-            raise ValueError("history must be contiguous int32 [rows][cols], with contiguous fp32 penalties [rows][3]")
+            _bad("history must be contiguous int32 [rows][cols], with contiguous fp32 penalties [rows][3]")
         if hist_len is not None and (hist_len.dtype is not i32 or hist_len.shape != (rows,) or
                                      not hist_len.is_contiguous()):
-            raise ValueError("hist_len must be int32 [rows]")
+            _bad("hist_len must be int32 [rows]")
         cols = history.shape[1]
-        if cols == 0:
-            history = penalties = hist_len = None
+        if cols:
+            hp, pp = history.data_ptr(), penalties.data_ptr()
+            lp = None if hist_len is None else hist_len.data_ptr()
+    elif penalties is not None or hist_len is not None:
+        _bad("penalties and hist_len go with a history")
     if bias is not None:
         if bias.dtype is not f32 or bias.shape not in ((1, n), (rows, n)) or not bias.is_contiguous():
-            raise ValueError("bias must be contiguous fp32 [rows or 1][n]")
-        bias_stride = n if bias.shape[0] > 1 else 0
+            _bad("bias must be contiguous fp32 [rows or 1][n]")
+        bp, bias_stride = bias.data_ptr(), n if bias.shape[0] > 1 else 0
     if mask is not None:
         words = -(-n // 32)
-        if mask.dtype not in (i32, torch.uint32) or mask.shape not in ((1, words), (rows, words)) or \
+        if mask.dtype not in (i32, h.torch.uint32) or mask.shape not in ((1, words), (rows, words)) or \
                 not mask.is_contiguous():
-            raise ValueError("mask must be contiguous 32-bit [rows or 1][ceil(n/32)]")
-        mask_stride = words if mask.shape[0] > 1 else 0
+            _bad("mask must be contiguous 32-bit [rows or 1][ceil(n/32)]")
+        mp, mask_stride = mask.data_ptr(), words if mask.shape[0] > 1 else 0
     if not logits.is_contiguous():
         logits = logits.contiguous()
     if out is None:
-        out = torch.empty((rows, n), dtype=f32, device=logits.device)
+        out = h.empty((rows, n), dtype=f32, device=logits.device)
     elif out.dtype is not f32 or out.shape != (rows, n) or not out.is_contiguous():
-        raise ValueError("out must be contiguous fp32 [rows][n]")
-    _launch(torch, (_lib or load()).s2_adjust_logits, dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt,
-            _ptr(history), _ptr(hist_len), cols, _ptr(penalties), _ptr(bias), bias_stride, _ptr(mask), mask_stride,
-            out.data_ptr())
+        _bad("out must be contiguous fp32 [rows][n]")
+    _launch(h, h.lib.s2_adjust_logits, dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt, hp, lp, cols, pp, bp,
+            bias_stride, mp, mask_stride, out.data_ptr())
     return out
 
 
