@@ -175,9 +175,10 @@ __device__ __forceinline__ float load_q(const T* q, bool live, bool low, float s
   return qs.down;
 }
 
-// S^T of one step: scores of rows g, g + 8 at columns 2c, 2c + 1 of each group of 8
-template <int HD, int NT>
-__device__ __forceinline__ void scores(uint32_t st, int step, int g, int c, const uint32_t (&q)[NT][HD / 8], float (&s)[NT][4]) {
+// S^T of one step: scores of rows g, g + 8 at columns 2c, 2c + 1
+template <int HD>
+__device__ __forceinline__ void scores(uint32_t st, int step, int g, int c, const uint32_t (&q)[HD / 8],
+                                       float (&s)[4]) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
   constexpr int W = HD / 32;  // words of a lane's quarter row
@@ -196,19 +197,14 @@ __device__ __forceinline__ void scores(uint32_t st, int step, int g, int c, cons
   const uint32_t p0 = lds32(par), p1 = lds32(par + 8 * B::kPar);
   const Pair pa(p0, p0), pb(p1, p1);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+  for (int i = 0; i < 4; ++i) s[i] = 0.f;
 #pragma unroll
   for (int j = 0; j < W; ++j) {
     uint32_t x[4], y[4];
     expand(r0[j], pa, x);
     expand(r1[j], pb, y);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mma_f16_16816(s[n], x[0], y[0], x[1], y[1], q[n][4 * j], q[n][4 * j + 1]);
-      mma_f16_16816(s[n], x[2], y[2], x[3], y[3], q[n][4 * j + 2], q[n][4 * j + 3]);
-    }
+    mma_f16_16816(s, x[0], y[0], x[1], y[1], q[4 * j], q[4 * j + 1]);
+    mma_f16_16816(s, x[2], y[2], x[3], y[3], q[4 * j + 2], q[4 * j + 3]);
   }
 }
 
@@ -232,9 +228,9 @@ __device__ __forceinline__ bool odd_values(uint32_t st, int step, int lane) {
 // 2c + 9; element 2i of those is row g, element 2i + 1 row g + 8 of the i-th tile.  Where not kPlain, the
 // parameters of rows from `valid` on (behind the sequence: their weights are zero, but what is there may be no
 // number) and those that are no numbers count as zero.
-template <int HD, int NT, bool kPlain>
-__device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[NT][2],
-                                       float (&o)[NT][HD / 16][4]) {
+template <int HD, bool kPlain>
+__device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[2],
+                                       float (&o)[HD / 16][4]) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
   constexpr int W = HD / 64;  // words of a row that a lane expands
@@ -261,110 +257,92 @@ __device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int 
       const uint32_t sel = h ? 0x7632 : 0x5410;
       expand(__byte_perm(w[0][j], w[1][j], sel), lo, x);
       expand(__byte_perm(w[2][j], w[3][j], sel), hi, y);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_f16_16816(o[n][4 * j + 2 * h], x[0], x[1], y[0], y[1], p[n][0], p[n][1]);
-        mma_f16_16816(o[n][4 * j + 2 * h + 1], x[2], x[3], y[2], y[3], p[n][0], p[n][1]);
-      }
+      mma_f16_16816(o[4 * j + 2 * h], x[0], x[1], y[0], y[1], p[0], p[1]);
+      mma_f16_16816(o[4 * j + 2 * h + 1], x[2], x[3], y[2], y[3], p[0], p[1]);
     }
 }
 
-// The running state of a warp's columns.  A lane's columns are 2c, 2c + 1 of each group of 8 (with fp32
-// queries the two parts of one), the same in the scores and in the output tiles.
-template <int HD, int NT, bool kTwo>
+// The running state of a warp's columns.  A lane's columns are 2c, 2c + 1 (with fp32 queries the
+// two parts of one), the same in the scores and in the output tiles.
+template <int HD, bool kTwo>
 struct Rows {
-  static constexpr int NC = kTwo ? 1 : 2;  // a lane's logical columns per group of 8
+  static constexpr int NC = kTwo ? 1 : 2;  // a lane's logical columns
   static constexpr float kNone = 3e38f;    // `lift` before a column has seen a position
-  float o[NT][HD / 16][4];
-  float lift[NT][NC];  // kWeightShift - m, m the running maximum (log2 units): a weight is exp2(score + lift)
-  float l[NT][NC], f[NT][NC];  // this lane's part of the sum, score factor
-  int lim[NT][NC];             // positions seen
+  float o[HD / 16][4];
+  float lift[NC];  // kWeightShift - m, m the running maximum (log2 units): a weight is exp2(score + lift)
+  float l[NC], f[NC];  // this lane's part of the sum, score factor
+  int lim[NC];             // positions seen
 
   __device__ __forceinline__ void init() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < HD / 16; ++i)
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) lift[n][j] = kNone, l[n][j] = 0.f;
-    }
+    for (int j = 0; j < NC; ++j) lift[j] = kNone, l[j] = 0.f;
   }
-  __device__ __forceinline__ float maximum(int n, int j) const {
-    return lift[n][j] == kNone ? -INFINITY : kWeightShift - lift[n][j];
+  __device__ __forceinline__ float maximum(int j) const {
+    return lift[j] == kNone ? -INFINITY : kWeightShift - lift[j];
   }
 
   // one step at position t0: s becomes the weights, as B operand
-  __device__ __forceinline__ void softmax(float (&s)[NT][4], int t0, int g, bool cut, uint32_t (&p)[NT][2]) {
-    if constexpr (kTwo) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] += s[n][1], s[n][2] += s[n][3];
-    }
+  __device__ __forceinline__ void softmax(float (&s)[4], int t0, int g, bool cut, uint32_t (&p)[2]) {
+    if constexpr (kTwo) s[0] += s[1], s[2] += s[3];
     if (cut) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (t0 + g + 8 * r >= lim[n][j]) s[n][2 * r + j] = -INFINITY;
+        for (int j = 0; j < NC; ++j)
+          if (t0 + g + 8 * r >= lim[j]) s[2 * r + j] = -INFINITY;
     }
-    float e[NT][2][NC], top = -INFINITY;  // [row g, row g + 8][column]
+    float e[2][NC], top = -INFINITY;  // [row g, row g + 8][column]
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        e[n][0][j] = __fmaf_rn(s[n][j], f[n][j], lift[n][j]);
-        e[n][1][j] = __fmaf_rn(s[n][2 + j], f[n][j], lift[n][j]);
-        top = fmaxf(top, fmaxf(e[n][0][j], e[n][1][j]));
-      }
+    for (int j = 0; j < NC; ++j) {
+      e[0][j] = __fmaf_rn(s[j], f[j], lift[j]);
+      e[1][j] = __fmaf_rn(s[2 + j], f[j], lift[j]);
+      top = fmaxf(top, fmaxf(e[0][j], e[1][j]));
+    }
     if (__any_sync(0xffffffffu, top > kWeightShift + kSlack)) rise(s, e);
+    float w[2][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float w[2][2];
+    for (int j = 0; j < NC; ++j) {
+      w[0][j] = ex2(e[0][j]);
+      w[1][j] = ex2(e[1][j]);
+      l[j] += w[0][j] + w[1][j];
+    }
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        w[0][j] = ex2(e[n][0][j]);
-        w[1][j] = ex2(e[n][1][j]);
-        l[n][j] += w[0][j] + w[1][j];
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if constexpr (kTwo) w[r][1] = w[r][0] - round_f16(w[r][0]);
-        p[n][r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0], w[r][1])));
-      }
+    for (int r = 0; r < 2; ++r) {
+      if constexpr (kTwo) w[r][1] = w[r][0] - round_f16(w[r][0]);
+      p[r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0], w[r][1])));
     }
   }
 
   // the maxima raised to the step's, output and sums rescaled
-  __device__ __forceinline__ void rise(const float (&s)[NT][4], float (&e)[NT][2][NC]) {
+  __device__ __forceinline__ void rise(const float (&s)[4], float (&e)[2][NC]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < NC; ++j) {
+      const float x0 = s[j] * f[j], x1 = s[2 + j] * f[j];
+      float top = fmaxf(x0, x1);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float m = maximum(j), mn = fmaxf(m, top);
+      if (mn > -INFINITY) {  // the same in all lanes of the column
+        const float keep = ex2(m - mn);
+        lift[j] = kWeightShift - mn;
+        l[j] *= keep;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const float x0 = s[n][j] * f[n][j], x1 = s[n][2 + j] * f[n][j];
-        float top = fmaxf(x0, x1);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float m = maximum(n, j), mn = fmaxf(m, top);
-        if (mn > -INFINITY) {  // the same in all lanes of the column
-          const float keep = ex2(m - mn);
-          lift[n][j] = kWeightShift - mn;
-          l[n][j] *= keep;
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i) {
-            if constexpr (kTwo) {
-              o[n][i][0] *= keep, o[n][i][1] *= keep, o[n][i][2] *= keep, o[n][i][3] *= keep;
-            } else {
-              o[n][i][j] *= keep, o[n][i][2 + j] *= keep;
-            }
+        for (int i = 0; i < HD / 16; ++i) {
+          if constexpr (kTwo) {
+            o[i][0] *= keep, o[i][1] *= keep, o[i][2] *= keep, o[i][3] *= keep;
+          } else {
+            o[i][j] *= keep, o[i][2 + j] *= keep;
           }
         }
-        e[n][0][j] = __fmaf_rn(s[n][j], f[n][j], lift[n][j]);
-        e[n][1][j] = __fmaf_rn(s[n][2 + j], f[n][j], lift[n][j]);
       }
+      e[0][j] = __fmaf_rn(s[j], f[j], lift[j]);
+      e[1][j] = __fmaf_rn(s[2 + j], f[j], lift[j]);
+    }
   }
 
   // a value row of the step that is no number: every column that sees it is none either, in its group's elements
@@ -374,24 +352,20 @@ struct Rows {
       const uint32_t par = lds32(st + S::kVPar + (step * kStep + r) * Kv4Block<HD>::kPar + g * (HD / 8) / kKvGroup * 4);
       if ((par & 0x7c00u) != 0x7c00u && (par & 0x7c000000u) != 0x7c000000u) continue;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (t0 + r < lim[n][kTwo ? 0 : j % 2]) o[n][i][j] = NAN;
+        for (int j = 0; j < 4; ++j)
+          if (t0 + r < lim[kTwo ? 0 : j % 2]) o[i][j] = NAN;
     }
   }
 
   __device__ __forceinline__ void finish_sums() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
-        l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
-        l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
-      }
+    for (int j = 0; j < NC; ++j) {
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+    }
   }
 };
 
@@ -502,20 +476,20 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 #pragma unroll
   for (int i = 0; i < kDepth - 1; ++i) issue(i);
 
-  Rows<HD, 1, kTwo> st;
+  Rows<HD, kTwo> st;
   st.init();
-  uint32_t qf[1][HD / 8];
+  uint32_t qf[HD / 8];
   {
     const int col = tile.first + (kTwo ? g / 2 : g);
     const bool live = col < cols;
     const int row = q0 + (live ? col / a.group : 0), h = kh * a.group + (live ? col % a.group : 0);
     const float down = load_q<T, HD>(static_cast<const T*>(a.q) + (static_cast<size_t>(row) * a.n_head + h) * HD, live,
-                                     kTwo && (g & 1), a.scale, c, qf[0]);
+                                     kTwo && (g & 1), a.scale, c, qf);
 #pragma unroll
     for (int j = 0; j < st.NC; ++j) {
       const int mine = tile.first + (kTwo ? c : 2 * c + j);
-      st.f[0][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
-      st.lim[0][j] = mine < cols ? min(over + mine / a.group + 1, len) : 0;
+      st.f[j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
+      st.lim[j] = mine < cols ? min(over + mine / a.group + 1, len) : 0;
     }
   }
   const int first_lim = min(over + tile.first / a.group + 1, len);  // the least that a live column sees
@@ -531,17 +505,17 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
       for (int step = 0; step < 2; ++step) {
         const int t0 = first + step * kStep, valid = min(len - t0, kStep);
         if (valid <= 0) break;
-        float s[1][4];
-        uint32_t pf[1][2];
-        scores<HD, 1>(at, step, g, c, qf, s);
+        float s[4];
+        uint32_t pf[2];
+        scores<HD>(at, step, g, c, qf, s);
         // where every column sees the whole step, a value that is no number reaches all of them anyway
         const bool cut = t0 + kStep > first_lim;
         st.softmax(s, t0, g, cut, pf);
         const bool odd = cut && odd_values<HD>(at, step, lane);
         if (!odd && valid == kStep) {
-          values<HD, 1, true>(at, step, g, c, valid, pf, st.o);
+          values<HD, true>(at, step, g, c, valid, pf, st.o);
         } else {
-          values<HD, 1, false>(at, step, g, c, valid, pf, st.o);
+          values<HD, false>(at, step, g, c, valid, pf, st.o);
           if (odd) st.poison(at, step, t0, valid, g);
         }
       }
@@ -561,16 +535,16 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < HD / 16; ++i) {
       if constexpr (kTwo) {
-        dst[2 * i] = st.o[0][i][0] + st.o[0][i][1];
-        dst[2 * i + 1] = st.o[0][i][2] + st.o[0][i][3];
+        dst[2 * i] = st.o[i][0] + st.o[i][1];
+        dst[2 * i + 1] = st.o[i][2] + st.o[i][3];
       } else {
-        dst[2 * i] = st.o[0][i][j];
-        dst[2 * i + 1] = st.o[0][i][2 + j];
+        dst[2 * i] = st.o[i][j];
+        dst[2 * i + 1] = st.o[i][2 + j];
       }
     }
     if (g == 0) {
-      jm[(warp * CT + col) * 2] = st.maximum(0, j);
-      jm[(warp * CT + col) * 2 + 1] = st.l[0][j];
+      jm[(warp * CT + col) * 2] = st.maximum(j);
+      jm[(warp * CT + col) * 2 + 1] = st.l[j];
     }
   }
   __syncthreads();
