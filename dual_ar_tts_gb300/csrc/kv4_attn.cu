@@ -595,13 +595,6 @@ struct Tc {
   static_assert(kS + 2 * kPage <= kCols && TN * 32 <= kPage, "tensor memory");
 };
 
-// A wait that gives up after a second or so (a few hundred ns a try).
-__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 22); ++i)
-    if (mbar_test(bar, parity)) return true;
-  return false;
-}
-
 // Warp-wide: 32 consecutive tensor memory columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -626,11 +619,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// fp16 operands, fp32 sums, both K-major (the format fields of fp16 are zero)
-constexpr uint32_t idesc_f16(int m, int n) {
-  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // What a thread holds of a page: hd/64 groups of 32 keys of a row, and 32 (hd 64: 16) values of positions l and
@@ -786,10 +774,10 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
       tc_fence_after();
       const uint32_t tm = *tbase;
       for (int n = 0;; ++n) {
-        ok = ok && wait_short(filled + (n & 1), n >> 1 & 1);
+        ok = ok && mbar_wait_short(filled + (n & 1), n >> 1 & 1);
         const bool end = !ok || place[n & 3] < 0;
         if (!end) {
-          if (n > 1) ok = wait_short(summed + (n & 1), (n - 2) >> 1 & 1);  // the weights of page n - 2 lie there
+          if (n > 1) ok = mbar_wait_short(summed + (n & 1), (n - 2) >> 1 & 1);  // the weights of page n - 2 lie there
           tc_fence_after();
           const uint32_t ts = tm + M::kS + (n & 1) * kPage;
 #pragma unroll
@@ -806,7 +794,7 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
         mbar_arrive(scored + (n & 1));
         if (n > 0) {  // the output with page n - 1
           const int o = n - 1;
-          ok = ok && wait_short(weighed + (o & 1), o >> 1 & 1);
+          ok = ok && mbar_wait_short(weighed + (o & 1), o >> 1 & 1);
           tc_fence_after();
           const uint32_t tp = tm + M::kS + (o & 1) * kPage;
 #pragma unroll
@@ -846,11 +834,11 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
     for (int n = 0;; ++n) {
       const bool end = next >= p1;
       // values first: there are three buffers of them, while the keys wait for the scores of the page before
-      if (n > 2) ok = ok && wait_short(summed + ((n - 3) & 1), (n - 3) >> 1 & 1);  // the values of page n - 3 are used up
+      if (n > 2) ok = ok && mbar_wait_short(summed + ((n - 3) & 1), (n - 3) >> 1 & 1);  // the values of page n - 3 are used up
       __syncwarp();
       bool odd = false;
       if (!end) odd = held.expand_values(sm + M::kV + n % 3 * M::kVBuf, odd_rows + (n & 3) * 2 * kPage);
-      if (n > 0) ok = ok && wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
+      if (n > 0) ok = ok && mbar_wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
       __syncwarp();
       if (!end) held.expand_keys(sm + M::kK);
       odd = __any_sync(0xffffffffu, odd);
@@ -926,7 +914,7 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
     uint32_t poison = 0;          // groups of the output that are no numbers
     int n = 0;
     for (;; ++n) {
-      ok = __all_sync(0xffffffffu, wait_short(scored + (n & 1), n >> 1 & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait_short(scored + (n & 1), n >> 1 & 1));
       const int p = ok ? place[n & 3] : -1;
       if (p < 0) break;
       tc_fence_after();
@@ -960,7 +948,7 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
         }
         __syncwarp();
         if (n > 0) {
-          ok = __all_sync(0xffffffffu, wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -996,7 +984,7 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
       tc_fence_before();
       mbar_arrive(weighed + (n & 1));
     }
-    if (n > 0) ok = __all_sync(0xffffffffu, wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1)) && ok;
+    if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1)) && ok;
     tc_fence_after();
     if (!ok && a.c.status && threadIdx.x % 32 == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
     const float inv = l == 0.f ? 0.f : 1.f / l;

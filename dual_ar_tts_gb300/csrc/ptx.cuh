@@ -65,6 +65,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A wait that gives up after a second or so (a few hundred ns a try).
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 22); ++i)
+    if (mbar_test(bar, parity)) return true;
+  return false;
+}
+
 // 1-D bulk copy global -> shared, completion signalled on `bar` (complete_tx).
 // dst/src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar,

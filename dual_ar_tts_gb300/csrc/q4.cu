@@ -288,11 +288,10 @@ __device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t pa
   }
 }
 
-// a row's sum with its scaling taken back (the power itself may be out of fp32's range)
-__device__ __forceinline__ float unscale(float z, uint32_t top) {
-  const int e = 24 - scale_exponent(top);
-  return z * pow2(e / 2) * pow2(e - e / 2);
-}
+// z * 2^e, the power itself perhaps out of fp32's range (e from -252 to 252)
+__device__ __forceinline__ float by_pow2(float z, int e) { return z * pow2(e / 2) * pow2(e - e / 2); }
+// a row's sum with its scaling taken back
+__device__ __forceinline__ float unscale(float z, uint32_t top) { return by_pow2(z, 24 - scale_exponent(top)); }
 
 // ---- few activations: one tile of columns, staged whole by every block.  A block is 8 warps: R tiles of 16 rows
 // times 8 / R parts of W's columns (blocks of 128, taken in turn), whose sums are added in order at the end.
@@ -413,32 +412,44 @@ int launch_few(MatmulArgs a, cudaStream_t st) {
 
 // ---- more activations: staged once, as planes in the workspace that every block then copies.
 
-// What the workspace holds for `tiles` tiles of 8 columns.
+// tcgen05 takes over behind 32 columns (rows; fp32 rows are two): 19456 x 2560 takes 35 us on mma.sync and 23 here at
+// 64 columns, 18.8 and 19.3 at 32; 2560 x 9728 at 32 16.7 and 16.9.
+constexpr int kMmaMost = 32;
+// What the workspace holds: for mma.sync `tiles` tiles of 8 columns; for tcgen05 `tiles` tiles of `width` columns, as
+// its B operand (two 128-byte-swizzled tiles of 64 positions a code block).
 struct Planes {
-  uint4* b;       // [block, part][tile][lane]
-  float* inits;   // [block, part][8 tiles]
+  uint4* b;       // [block, part][tile][lane], or [block][tile][half][column][chunk]
+  float* inits;   // [block, part][8 tiles] (mma.sync)
   uint32_t* top;  // [row]
-  int tiles;
+  int tiles, width;
   size_t bytes;
 };
 Planes planes(int n, int k, int terms, void* ws) {
   Planes p{};
   const long long cols = static_cast<long long>(n) * terms;
-  // passes of one, two or four tiles
-  p.tiles = static_cast<int>(cols <= 8 ? 1 : cols <= 16 ? 2 : (cols + 31) / 32 * 4);
-  const size_t parts = (static_cast<size_t>(k) + kBlock - 1) / kBlock * 4;
+  const size_t blocks = (static_cast<size_t>(k) + kBlock - 1) / kBlock, parts = blocks * 4;
   uint8_t* at = static_cast<uint8_t*>(ws);
   p.b = reinterpret_cast<uint4*>(at);
+  if (cols > kMmaMost) {
+    p.width = cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
+    p.tiles = static_cast<int>((cols + p.width - 1) / p.width);
+    const size_t b = blocks * p.tiles * p.width * 256;
+    p.top = reinterpret_cast<uint32_t*>(at + b);
+    p.bytes = b + static_cast<size_t>(n) * 4;
+    return p;
+  }
+  p.width = 8;
+  p.tiles = static_cast<int>(cols <= 8 ? 1 : cols <= 16 ? 2 : (cols + 31) / 32 * 4);  // passes of one, two or four
   p.inits = reinterpret_cast<float*>(at + parts * p.tiles * 512);
   p.top = reinterpret_cast<uint32_t*>(at + parts * p.tiles * (512 + 32));
   p.bytes = parts * p.tiles * (512 + 32) + static_cast<size_t>(p.tiles) * 8 * 4;
   return p;
 }
 
-// One block per activation row (and per row of zeros that fills the last tile).  Rows of up to 4 items a thread are
-// read once.
+// One block per activation row (for mma.sync also per row of zeros that fills the last tile; columns behind the last
+// row of tcgen05's tiles are never looked at).  Rows of up to 4 items a thread are read once.
 constexpr int kPlaneThreads = 512;
-template <typename T>
+template <typename T, bool kTc>
 __global__ void __launch_bounds__(kPlaneThreads) k_q4_planes(const MatmulArgs a, const Planes p) {
   constexpr int TN = kTerms<T>, kHeld = 4;
   __shared__ uint32_t top;
@@ -470,6 +481,29 @@ __global__ void __launch_bounds__(kPlaneThreads) k_q4_planes(const MatmulArgs a,
   const float up = pow2(scale_exponent(top));
   if (threadIdx.x == 0) p.top[row] = top;
   auto store = [&](const Eight<T>& v, int i) {
+    if constexpr (kTc) {
+      if (i >= items) return;
+      float rest[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rest[e] = v[e] * up;
+      const int q = i % 4 * 4 + i / 4 % 4;  // the word of the code block that holds these columns
+#pragma unroll
+      for (int u = 0; u < TN; ++u) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 two = __floats2half2_rn(rest[e], rest[e + 4]);
+          const float2 r = __half22float2(two);
+          h[e] = *reinterpret_cast<const uint32_t*>(&two);
+          rest[e] -= r.x;
+          rest[e + 4] -= r.y;
+        }
+        const int col = row * TN + u, at = col % p.width;
+        p.b[((static_cast<size_t>(i / 16) * p.tiles + col / p.width) * 2 + q / 8) * p.width * 8 + at * 8 +
+            ((q % 8) ^ (at & 7))] = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      return;
+    }
     const Staged<T> st(v, up);
     if (i < items)
 #pragma unroll
@@ -495,6 +529,27 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
       : "r"(addr), "r"(rank));
   return v;
+}
+
+__device__ __forceinline__ float ld_cluster1(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank));
+  return v;
+}
+
+// The eight codes of a word as fp16 scale * (code - 8), in the order 0 4 1 5 2 6 3 7.  0x6400 | code is 1024 + code in
+// fp16 and 0x6400 | code << 4 is 1024 + 16 code: code - 8 comes out of one exact subtraction or FMA.
+__device__ __forceinline__ void expand(uint32_t w, __half2 s, uint32_t* v) {
+  const uint32_t m = 0x64006400u, w8 = w >> 8;
+  const __half2 z = __float2half2_rn(1032.f), z16 = __float2half2_rn(-72.f), sixteenth = __float2half2_rn(0.0625f);
+  auto h2 = [](uint32_t u) { return *reinterpret_cast<__half2*>(&u); };
+  auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t*>(&h); };
+  v[0] = bits(__hmul2(s, __hsub2(h2((w & 0x000f000fu) | m), z)));
+  v[1] = bits(__hmul2(s, __hfma2(h2((w & 0x00f000f0u) | m), sixteenth, z16)));
+  v[2] = bits(__hmul2(s, __hsub2(h2((w8 & 0x000f000fu) | m), z)));
+  v[3] = bits(__hmul2(s, __hfma2(h2((w8 & 0x00f000f0u) | m), sixteenth, z16)));
 }
 
 // A block takes 128 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
@@ -591,6 +646,26 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
   if (ranks > 1) cluster_sync();  // no block leaves while its sums are read
 }
 
+// a grid of clusters of `ranks` blocks, which may start before the kernel in front ends
+int launch_joined(void (*kernel)(MatmulArgs, Planes), dim3 grid, int threads, int smem, int ranks, const MatmulArgs& a,
+                  const Planes& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1;
+  at[0].val.clusterDim.y = ranks;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a, p) == cudaSuccess ? S2_OK : S2_ECUDA;
+}
+
 template <typename T, int NT, int G>
 int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + kManyRows - 1) / kManyRows, passes = p.tiles / NT;
@@ -603,28 +678,282 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   constexpr int kRings = kManyAhead<NT> * (kManyWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
   constexpr int smem = kRings > kJoin ? kRings : kJoin;
   if (!allow_smem<k_q4_many<T, NT, G>, smem>()) return S2_ECUDA;
-  k_q4_planes<T><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, ranks, passes);
-  cfg.blockDim = dim3(32 * kManyWarps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = ranks;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_q4_many<T, NT, G>, a, p) == cudaSuccess ? S2_OK : S2_ECUDA;
+  k_q4_planes<T, false><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
+  return launch_joined(k_q4_many<T, NT, G>, dim3(grid, ranks, passes), 32 * kManyWarps, smem, ranks, a, p, st);
+}
+
+// ---- many activations: tcgen05, its A operand the weights.  A block takes 128 rows and N columns; four warps expand
+// codes, a thread its row's, to fp16 in tensor memory, a fifth copies activations (one bulk copy a code block) and
+// issues the products.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
+// taken times the power of two that brings the largest of those used here to 2^11 .. 2^12 (scales 2^-28 of it and
+// less lose bits).  The blocks of a cluster split W's columns and add their sums in rank order.
+template <int N>
+struct Tc {
+  static constexpr int kA = N == 128 ? 2 : 3;                      // expanded code blocks, 64 tensor memory columns each
+  static constexpr int kB = N == 32 ? 4 : N == 64 ? 3 : 2;         // code blocks' activations
+  static constexpr int kAhead = N == 32 ? 8 : N == 64 ? 6 : 4;     // code blocks in flight
+  static constexpr int kBBytes = N * 256, kRow = 32 * 64 + 32 * 8;  // of a code block: activations; a warp's codes and scales
+  static constexpr int kCodes = kB * kBBytes, kBars = kCodes + 4 * kAhead * kRow, kBytes = kBars + 128 + 1024;
+  static constexpr uint32_t kCols = 256;
+  static_assert(N + 64 * kA <= 256 && (N + 1) * 512 <= kBars, "room");
+};
+
+template <typename T, int N, int G>
+__global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Planes p) {
+  using M = Tc<N>;
+  constexpr int TN = kTerms<T>, SB = kBlock / G;
+  extern __shared__ __align__(16) uint8_t smraw[];
+  __shared__ int ex[N / TN];  // the activations' powers of two
+  uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
+  uint64_t* arrived = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [j % kB]: activations of code block j
+  uint64_t *expanded = arrived + M::kB, *used = expanded + M::kA;  // [j % kA]: its weights; both used up
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(used + M::kA);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int blocks = (a.k + kBlock - 1) / kBlock;
+  const int ranks = gridDim.y, rank = blockIdx.y;
+  const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / ranks);
+  const int count = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / ranks) - b0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < M::kB; ++i) mbar_init(arrived + i, 1);
+    for (int i = 0; i < M::kA; ++i) {
+      mbar_init(expanded + i, 4);
+      mbar_init(used + i, 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(tbase, M::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tbase;
+
+  bool ok = true;
+  int ew = 0;
+  const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0);
+  if (warp == 4) {
+    pdl_wait();
+    for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
+    if (lane == 0) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<size_t>(b0) * p.tiles + blockIdx.z) * M::kBBytes;
+      auto copy = [&](int j) {
+        mbar_arrive_expect_tx(arrived + j % M::kB, M::kBBytes);
+        bulk_g2s_plain(sm + j % M::kB * M::kBBytes, src + static_cast<size_t>(j) * p.tiles * M::kBBytes, M::kBBytes,
+                       arrived + j % M::kB);
+      };
+      for (int j = 0; j < min(count, M::kB); ++j) copy(j);
+      int j = 0;
+      for (; j < count; ++j) {
+        ok = ok && mbar_wait_short(arrived + j % M::kB, j / M::kB & 1);
+        ok = ok && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t b = smem_u32(sm + j % M::kB * M::kBBytes), ta = tm + N + j % M::kA * 64;
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)
+          tc_mma_tmem_a(tm, ta + k * 8, desc_sw128(b + k / 4 * (N * 128) + k % 4 * 32), idesc_f16(128, N), j > 0 || k > 0);
+        tc_commit(used + j % M::kA);
+        if (j > 0 && j - 1 + M::kB < count) {  // the place of block j - 1
+          ok = mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
+          if (ok) copy(j - 1 + M::kB);
+        }
+      }
+      if (!ok) {  // what is in flight still comes
+        if (j > 0) mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
+        for (int i = j; i < min(count, j + M::kB - 1); ++i) mbar_wait_short(arrived + i % M::kB, i / M::kB & 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    uint8_t* ring = sm + M::kCodes + warp * M::kAhead * M::kRow;
+    const int row0 = blockIdx.x * 128 + warp * 32;
+    const uint8_t* from[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      from[i] = a.codes + (static_cast<size_t>(min(row0 + i * 8 + lane / 4, a.m - 1)) * blocks + b0) * 64 + lane % 4 * 16;
+    const size_t first = (static_cast<size_t>(min(row0 + lane, a.m - 1)) * blocks + b0) * SB;
+    const size_t send = static_cast<size_t>(a.m) * blocks * SB;
+    auto issue = [&](int j) {
+      if (j < count) {
+        uint8_t* dst = ring + j % M::kAhead * M::kRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + lane / 4;
+          cp_async16(dst + r * 64 + ((lane % 4) ^ (r / 2 & 3)) * 16, from[i] + static_cast<size_t>(j) * 64);
+        }
+        const size_t at = first + static_cast<size_t>(j) * SB;
+        if constexpr (G == 128)  // two bytes wanted: the aligned four around them, less what lies past the last scale
+          cp_async_small<4>(dst + 2048 + lane * 8, a.scales + (at & ~size_t{1}), (at | 1) < send ? 4 : 2);
+        else
+          cp_async_small<2 * SB>(dst + 2048 + lane * 8, a.scales + at, 2 * SB);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < M::kAhead - 1; ++i) issue(i);
+    // the largest finite scale of each of the warp's rows here: a code block a lane, 16 rows under way together
+    uint32_t most = 0;
+    using Unit = std::conditional_t<SB == 4, uint2, std::conditional_t<SB == 2, uint32_t, uint16_t>>;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16)
+#pragma unroll 1
+      for (int b = 0; b < count; b += 32) {
+        Unit v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          v[r] = Unit{};
+          if (b + lane < count)
+            v[r] = __ldg(reinterpret_cast<const Unit*>(
+                             a.scales + (static_cast<size_t>(min(row0 + r0 + r, a.m - 1)) * blocks + b0) * SB) + b + lane);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          uint32_t t = 0;
+          auto look = [&](uint32_t bits) { t = max(t, (bits & 0x7fffu) < 0x7f80u ? bits & 0x7fffu : 0u); };
+          if constexpr (SB == 4)
+            look(v[r].x), look(v[r].x >> 16), look(v[r].y), look(v[r].y >> 16);
+          else
+            look(v[r]), look(static_cast<uint32_t>(v[r]) >> 16);
+          t = __reduce_max_sync(0xffffffffu, t);
+          if (lane == r0 + r) most = max(most, t);
+        }
+      }
+    ew = most == 0 ? 0 : min(11 + 127 - static_cast<int>(most >> 7), 126);
+    const float up = pow2(ew);
+    const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int j = 0; j < count; ++j) {
+      issue(j + M::kAhead - 1);
+      cp_async_wait_group<M::kAhead - 1>();
+      __syncwarp();
+      const uint32_t at = smem_u32(ring + j % M::kAhead * M::kRow);
+      uint4 w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[c] = lds128(at + lane * 64 + ((c ^ (lane / 2 & 3)) * 16));
+      __half2 s[4];
+      {
+        const uint32_t u = lds32(at + 2048 + lane * 8);
+        uint32_t v = u;
+        if constexpr (G == 32) v = lds32(at + 2048 + lane * 8 + 4);
+        auto h = [&](float f) { return __float2half2_rn(f * up); };
+        if constexpr (G == 32) {
+          s[0] = h(bf16lo(u)), s[1] = h(bf16hi(u)), s[2] = h(bf16lo(v)), s[3] = h(bf16hi(v));
+        } else if constexpr (G == 64) {
+          s[0] = s[1] = h(bf16lo(u)), s[2] = s[3] = h(bf16hi(u));
+        } else {
+          s[0] = s[1] = s[2] = s[3] = h((first + j) & 1 ? bf16hi(u) : bf16lo(u));
+        }
+      }
+      __syncwarp();  // the ring's place may be filled again
+      if (j >= M::kA) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_short(used + j % M::kA, (j / M::kA - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 x = w[half * 2 + c];
+          const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) expand(word[i], s[i], r + c * 16 + i * 4);
+        }
+        tmem_st32(tlane + j % M::kA * 64 + half * 32, r);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(expanded + j % M::kA);
+    }
+    cp_async_wait_all();
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(used + (count - 1) % M::kA, (count - 1) / M::kA & 1));
+    tc_fence_after();
+  }
+  // a wait that gave up leaves no numbers
+  const int row = blockIdx.x * 128 + warp * 32 + lane;
+  T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
+  __syncthreads();
+  if (ranks == 1) {
+    if (warp < 4)
+#pragma unroll 1
+      for (int c = 0; c < N && c < nn * TN; c += 16) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tm + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+        if (row < a.m)
+#pragma unroll
+          for (int i = 0; i < 16 / TN; ++i) {
+            const int col = c / TN + i;
+            if (col < nn)
+              y[static_cast<size_t>(col) * a.m] =
+                  from_f<T>(ok ? by_pow2(TN == 2 ? v[2 * i] + v[2 * i + 1] : v[i], -ew - ex[col]) : NAN);
+          }
+      }
+  } else {
+    // sums as [column][row] where the operands were, behind them the rows' powers of two
+    float* out = reinterpret_cast<float*>(sm);
+    if (warp < 4) {
+#pragma unroll 1
+      for (int c = 0; c < N && c < nn * TN; c += 16) {
+        float v[16];
+        tmem_ld16(tm + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[(c + i) * 128 + threadIdx.x] = ok ? v[i] : NAN;
+      }
+      out[N * 128 + threadIdx.x] = __int_as_float(ew);
+    }
+    cluster_sync();
+    if (warp < 4) {
+      int e[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < ranks) e[q] = __float_as_int(ld_cluster1(smem_u32(out + N * 128 + threadIdx.x), q));
+      for (int col = rank; col < nn; col += ranks) {
+        float v[8][TN], sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int t = 0; t < TN; ++t)
+            if (q < ranks) v[q][t] = ld_cluster1(smem_u32(out + (col * TN + t) * 128 + threadIdx.x), q);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < ranks) sum += by_pow2(TN == 2 ? v[q][0] + v[q][TN - 1] : v[q][0], -e[q] - ex[col]);
+        if (row < a.m) y[static_cast<size_t>(col) * a.m] = from_f<T>(sum);
+      }
+    }
+    cluster_sync();  // no block leaves while its sums are read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tm, M::kCols);
+  }
+}
+
+template <typename T, int N, int G>
+int launch_tc(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
+  const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + 127) / 128;
+  if (p.tiles > 65535) return S2_EINVAL;
+  // Clusters up to what the SMs hold (two blocks each): 256 columns, 2560 x 9728, 34 us against 57 with one block an
+  // SM; 19456 x 2560 at 64 columns 23 against 41 with four, which take two rounds.
+  int ranks = 1;
+  while (ranks < 8 && static_cast<long long>(grid) * p.tiles * ranks * 2 <= 304 && blocks >= 4 * ranks) ranks *= 2;
+  constexpr int smem = Tc<N>::kBytes;
+  if (!allow_smem<k_q4_tc<T, N, G>, smem>()) return S2_ECUDA;
+  k_q4_planes<T, true><<<a.n, kPlaneThreads, 0, st>>>(a, p);
+  return launch_joined(k_q4_tc<T, N, G>, dim3(grid, ranks, p.tiles), 160, smem, ranks, a, p, st);
 }
 
 template <typename T, int G>
 int launch_matmul(const MatmulArgs& a, void* ws, cudaStream_t st) {
   if (few<T>(a.n, (a.k + kBlock - 1) / kBlock)) return launch_few<T, G>(a, st);
   const Planes p = planes(a.n, a.k, kTerms<T>, ws);
+  if (p.width > 8)
+    return p.width == 32 ? launch_tc<T, 32, G>(a, p, st)
+                         : p.width == 64 ? launch_tc<T, 64, G>(a, p, st) : launch_tc<T, 128, G>(a, p, st);
   return p.tiles == 1 ? launch_many<T, 1, G>(a, p, st)
                       : p.tiles == 2 ? launch_many<T, 2, G>(a, p, st) : launch_many<T, 4, G>(a, p, st);
 }

@@ -137,3 +137,77 @@ def test_matmul_on_another_stream_and_in_a_graph():
     x.copy_(torch.randn((3, 512), device="cuda"))
     graph.replay()
     assert torch.equal(out, pkg.q4_matmul(x, codes, scales, 32))
+
+
+MANY = [  # n, m, k, group: tiles of 32, 64 and 128 columns, their ends, split and whole sums, one code block and many
+    (33, 129, 32, 32), (47, 1, 128, 128), (63, 257, 1920, 64), (127, 300, 1056, 32), (128, 128, 640, 128),
+    (129, 40, 9728, 64), (200, 1000, 2688, 128), (257, 2500, 224, 32), (600, 640, 512, 64)]
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("n,m,k,group", MANY)
+def test_matmul_of_many_rows(dtype, n, m, k, group):
+    test_matmul(dtype, n, m, k, group)
+
+
+def test_matmul_of_many_rows_takes_rows_as_they_are():
+    """Every row's result does not depend on the rows beside it: not on their magnitudes, nor on what is no number."""
+    import dual_ar_tts_gb300 as pkg
+    codes, scales = pkg.quantize_q4(_weights(300, 1600, torch.bfloat16, 9).cuda(), 32)
+    for dtype in fb.TYPES.values():
+        x = torch.randn((150, 1600), generator=torch.Generator().manual_seed(4)).to(dtype).cuda()
+        clean = pkg.q4_matmul(x, codes, scales, 32)
+        x[7] *= 1000
+        x[20, 5], x[140, 1000], x[149] = math.nan, -math.inf, 0
+        y = pkg.q4_matmul(x, codes, scales, 32)
+        assert torch.isnan(y[20]).all() and not torch.isfinite(y[140]).all() and (y[149] == 0).all()
+        keep = [r for r in range(149) if r not in (7, 20, 140)]
+        assert torch.equal(y[keep], clean[keep])
+        _check(y[7:8], x[7:8], codes, scales, 1600, 32)
+
+
+def test_matmul_of_many_rows_of_weights_of_many_sizes():
+    """Weight rows of magnitudes from 1e-30 to 1e30, groups a millionfold apart in a row, groups of zeros, a row of
+    zeros, and a group that is no number: only its row is none."""
+    import dual_ar_tts_gb300 as pkg
+    m, k = 140, 1280
+    w = _weights(m, k, torch.float32, 12)
+    for r in range(m):
+        w[r] *= 10.0 ** (r % 61 - 30)
+    w[3, 32:64], w[5, :640], w[9] = 0, w[5, :640] * 1e-6, 0
+    w[11, 70] = math.inf
+    codes, scales = pkg.quantize_q4(w.cuda(), 32)
+    x = torch.randn((70, k), generator=torch.Generator().manual_seed(8)).cuda()
+    y = pkg.q4_matmul(x, codes, scales, 32)
+    assert torch.isnan(y[:, 11]).all() and (y[:, 9] == 0).all()
+    keep = torch.tensor([r for r in range(m) if r != 11])
+    _check(y[:, keep.cuda()], x, codes[keep.cuda()], scales[keep.cuda()], k, 32)
+    tail = x.clone()
+    tail[:, 640:] = 0                                                   # only the small groups of row 5 count
+    y = pkg.q4_matmul(tail, codes, scales, 32)
+    _check(y[:, 5:6], tail, codes[5:6], scales[5:6], k, 32)
+
+
+def test_matmul_of_many_rows_in_a_graph_beside_another():
+    """Two captured calls on two streams, replayed at once with new inputs; a workspace of the caller's."""
+    import dual_ar_tts_gb300 as pkg
+    codes, scales = pkg.quantize_q4(_weights(700, 1024, torch.bfloat16, 1).cuda(), 64)
+    runs = []
+    for n in (100, 260):
+        x, out = torch.randn((n, 1024), device="cuda"), torch.empty((n, 700), device="cuda")
+        ws = torch.empty(pkg.load().s2_q4_matmul_workspace(n, 1024, pkg.S2_F32), dtype=torch.uint8, device="cuda")
+        pkg.q4_matmul(x, codes, scales, 64, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkg.q4_matmul(x, codes, scales, 64, out=out, workspace=ws)
+        x.copy_(torch.randn((n, 1024), device="cuda"))
+        runs.append((graph, x, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, _, _, stream in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, x, out, _ in runs:
+        assert torch.equal(out, pkg.q4_matmul(x, codes, scales, 64))
