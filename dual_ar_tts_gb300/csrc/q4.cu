@@ -414,7 +414,10 @@ int launch_few(MatmulArgs a, cudaStream_t st) {
 
 // tcgen05 takes over behind 32 columns (rows; fp32 rows are two): 19456 x 2560 takes 35 us on mma.sync and 23 here at
 // 64 columns, 18.8 and 19.3 at 32; 2560 x 9728 at 32 16.7 and 16.9.
-constexpr int kMmaMost = 32;
+#ifndef S2_MMA_MOST
+#define S2_MMA_MOST 32
+#endif
+constexpr int kMmaMost = S2_MMA_MOST;
 // What the workspace holds: for mma.sync `tiles` tiles of 8 columns; for tcgen05 `tiles` tiles of `width` columns, as
 // its B operand (two 128-byte-swizzled tiles of 64 positions a code block).
 struct Planes {
@@ -682,32 +685,34 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   return launch_joined(k_q4_many<T, NT, G>, dim3(grid, ranks, passes), 32 * kManyWarps, smem, ranks, a, p, st);
 }
 
-// ---- many activations: tcgen05, its A operand the weights.  A block takes 128 rows and N columns; four warps expand
-// codes, a thread its row's, to fp16 in tensor memory, a fifth copies activations (one bulk copy a code block) and
-// issues the products.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
+// ---- many activations: tcgen05, its A operand the weights.  A block takes 128 rows and N columns; twice four warps
+// expand code blocks in turn, a thread its row's, to fp16 in tensor memory, a ninth copies activations (one bulk copy a
+// code block) and issues the products.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
 // taken times the power of two that brings the largest of those used here to 2^11 .. 2^12 (scales 2^-28 of it and
 // less lose bits).  The blocks of a cluster split W's columns and add their sums in rank order.
 template <int N>
 struct Tc {
   static constexpr int kA = N == 128 ? 2 : 3;                      // expanded code blocks, 64 tensor memory columns each
   static constexpr int kB = N == 32 ? 4 : N == 64 ? 3 : 2;         // code blocks' activations
-  static constexpr int kAhead = N == 32 ? 8 : N == 64 ? 6 : 4;     // code blocks in flight
+  static constexpr int kAhead = N == 32 ? 4 : N == 64 ? 3 : 2;     // code blocks of a warp in flight
   static constexpr int kBBytes = N * 256, kRow = 32 * 64 + 32 * 8;  // of a code block: activations; a warp's codes and scales
-  static constexpr int kCodes = kB * kBBytes, kBars = kCodes + 4 * kAhead * kRow, kBytes = kBars + 128 + 1024;
+  static constexpr int kCodes = kB * kBBytes, kBars = kCodes + 8 * kAhead * kRow, kBytes = kBars + 128 + 1024;
   static constexpr uint32_t kCols = 256;
   static_assert(N + 64 * kA <= 256 && (N + 1) * 512 <= kBars, "room");
 };
 
+constexpr int kTcThreads = 288;
 template <typename T, int N, int G>
-__global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Planes p) {
+__global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, const Planes p) {
   using M = Tc<N>;
   constexpr int TN = kTerms<T>, SB = kBlock / G;
   extern __shared__ __align__(16) uint8_t smraw[];
-  __shared__ int ex[N / TN];  // the activations' powers of two
+  __shared__ int ex[N / TN], ew[128];  // powers of two of the activations' and the weights' rows
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
   uint64_t* arrived = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [j % kB]: activations of code block j
   uint64_t *expanded = arrived + M::kB, *used = expanded + M::kA;  // [j % kA]: its weights; both used up
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(used + M::kA);
+  uint64_t* done = used + M::kA;                                     // all of them
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int blocks = (a.k + kBlock - 1) / kBlock;
   const int ranks = gridDim.y, rank = blockIdx.y;
@@ -719,9 +724,10 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
       mbar_init(expanded + i, 4);
       mbar_init(used + i, 1);
     }
+    mbar_init(done, 1);
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(tbase, M::kCols);
     tmem_relinquish();
   }
@@ -731,9 +737,8 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
   const uint32_t tm = *tbase;
 
   bool ok = true;
-  int ew = 0;
   const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0);
-  if (warp == 4) {
+  if (warp == 8) {
     pdl_wait();
     for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
     if (lane == 0) {
@@ -755,6 +760,7 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
         for (int k = 0; k < kBlock / 16; ++k)
           tc_mma_tmem_a(tm, ta + k * 8, desc_sw128(b + k / 4 * (N * 128) + k % 4 * 32), idesc_f16(128, N), j > 0 || k > 0);
         tc_commit(used + j % M::kA);
+        if (j == count - 1) tc_commit(done);
         if (j > 0 && j - 1 + M::kB < count) {  // the place of block j - 1
           ok = mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
           if (ok) copy(j - 1 + M::kB);
@@ -767,23 +773,24 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
     }
     __syncwarp();
   } else {
+    const int wg = warp / 4, mine = (count - wg + 1) / 2;  // the code blocks 2 t + wg
     uint8_t* ring = sm + M::kCodes + warp * M::kAhead * M::kRow;
-    const int row0 = blockIdx.x * 128 + warp * 32;
+    const int row0 = blockIdx.x * 128 + warp % 4 * 32;
     const uint8_t* from[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      from[i] = a.codes + (static_cast<size_t>(min(row0 + i * 8 + lane / 4, a.m - 1)) * blocks + b0) * 64 + lane % 4 * 16;
-    const size_t first = (static_cast<size_t>(min(row0 + lane, a.m - 1)) * blocks + b0) * SB;
+      from[i] = a.codes + (static_cast<size_t>(min(row0 + i * 8 + lane / 4, a.m - 1)) * blocks + b0 + wg) * 64 + lane % 4 * 16;
+    const size_t first = (static_cast<size_t>(min(row0 + lane, a.m - 1)) * blocks + b0 + wg) * SB;
     const size_t send = static_cast<size_t>(a.m) * blocks * SB;
-    auto issue = [&](int j) {
-      if (j < count) {
-        uint8_t* dst = ring + j % M::kAhead * M::kRow;
+    auto issue = [&](int t) {
+      if (t < mine) {
+        uint8_t* dst = ring + t % M::kAhead * M::kRow;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 8 + lane / 4;
-          cp_async16(dst + r * 64 + ((lane % 4) ^ (r / 2 & 3)) * 16, from[i] + static_cast<size_t>(j) * 64);
+          cp_async16(dst + r * 64 + ((lane % 4) ^ (r / 2 & 3)) * 16, from[i] + static_cast<size_t>(t) * 128);
         }
-        const size_t at = first + static_cast<size_t>(j) * SB;
+        const size_t at = first + static_cast<size_t>(t) * 2 * SB;
         if constexpr (G == 128)  // two bytes wanted: the aligned four around them, less what lies past the last scale
           cp_async_small<4>(dst + 2048 + lane * 8, a.scales + (at & ~size_t{1}), (at | 1) < send ? 4 : 2);
         else
@@ -793,56 +800,55 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
     };
 #pragma unroll
     for (int i = 0; i < M::kAhead - 1; ++i) issue(i);
-    // the largest finite scale of each of the warp's rows here: a code block a lane, 16 rows under way together
+    // the largest finite scale here of each of 16 rows: a code block a lane, the rows under way together
     uint32_t most = 0;
     using Unit = std::conditional_t<SB == 4, uint2, std::conditional_t<SB == 2, uint32_t, uint16_t>>;
 #pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += 16)
-#pragma unroll 1
-      for (int b = 0; b < count; b += 32) {
-        Unit v[16];
+    for (int b = 0; b < count; b += 32) {
+      Unit v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          v[r] = Unit{};
-          if (b + lane < count)
-            v[r] = __ldg(reinterpret_cast<const Unit*>(
-                             a.scales + (static_cast<size_t>(min(row0 + r0 + r, a.m - 1)) * blocks + b0) * SB) + b + lane);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          uint32_t t = 0;
-          auto look = [&](uint32_t bits) { t = max(t, (bits & 0x7fffu) < 0x7f80u ? bits & 0x7fffu : 0u); };
-          if constexpr (SB == 4)
-            look(v[r].x), look(v[r].x >> 16), look(v[r].y), look(v[r].y >> 16);
-          else
-            look(v[r]), look(static_cast<uint32_t>(v[r]) >> 16);
-          t = __reduce_max_sync(0xffffffffu, t);
-          if (lane == r0 + r) most = max(most, t);
-        }
+      for (int r = 0; r < 16; ++r) {
+        v[r] = Unit{};
+        if (b + lane < count)
+          v[r] = __ldg(reinterpret_cast<const Unit*>(
+                           a.scales + (static_cast<size_t>(min(row0 + wg * 16 + r, a.m - 1)) * blocks + b0) * SB) + b + lane);
       }
-    ew = most == 0 ? 0 : min(11 + 127 - static_cast<int>(most >> 7), 126);
-    const float up = pow2(ew);
-    const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp * 32) << 16);
-    for (int j = 0; j < count; ++j) {
-      issue(j + M::kAhead - 1);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        uint32_t t = 0;
+        auto look = [&](uint32_t bits) { t = max(t, (bits & 0x7fffu) < 0x7f80u ? bits & 0x7fffu : 0u); };
+        if constexpr (SB == 4)
+          look(v[r].x), look(v[r].x >> 16), look(v[r].y), look(v[r].y >> 16);
+        else
+          look(v[r]), look(static_cast<uint32_t>(v[r]) >> 16);
+        t = __reduce_max_sync(0xffffffffu, t);
+        if (lane == r) most = max(most, t);
+      }
+    }
+    if (lane < 16) ew[warp % 4 * 32 + wg * 16 + lane] = most == 0 ? 0 : min(11 + 127 - static_cast<int>(most >> 7), 126);
+    named_bar(1, 256);
+    const float up = pow2(ew[warp % 4 * 32 + lane]);
+    const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+    for (int t = 0; t < mine; ++t) {
+      const int j = 2 * t + wg;
+      issue(t + M::kAhead - 1);
       cp_async_wait_group<M::kAhead - 1>();
       __syncwarp();
-      const uint32_t at = smem_u32(ring + j % M::kAhead * M::kRow);
+      const uint32_t at = smem_u32(ring + t % M::kAhead * M::kRow);
       uint4 w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) w[c] = lds128(at + lane * 64 + ((c ^ (lane / 2 & 3)) * 16));
       __half2 s[4];
       {
         const uint32_t u = lds32(at + 2048 + lane * 8);
-        uint32_t v = u;
-        if constexpr (G == 32) v = lds32(at + 2048 + lane * 8 + 4);
         auto h = [&](float f) { return __float2half2_rn(f * up); };
         if constexpr (G == 32) {
+          const uint32_t v = lds32(at + 2048 + lane * 8 + 4);
           s[0] = h(bf16lo(u)), s[1] = h(bf16hi(u)), s[2] = h(bf16lo(v)), s[3] = h(bf16hi(v));
         } else if constexpr (G == 64) {
           s[0] = s[1] = h(bf16lo(u)), s[2] = s[3] = h(bf16hi(u));
         } else {
-          s[0] = s[1] = s[2] = s[3] = h((first + j) & 1 ? bf16hi(u) : bf16lo(u));
+          s[0] = s[1] = s[2] = s[3] = h(first & 1 ? bf16hi(u) : bf16lo(u));
         }
       }
       __syncwarp();  // the ring's place may be filled again
@@ -868,55 +874,56 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
       if (lane == 0) mbar_arrive(expanded + j % M::kA);
     }
     cp_async_wait_all();
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(used + (count - 1) % M::kA, (count - 1) / M::kA & 1));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(done, 0));
     tc_fence_after();
   }
-  // a wait that gave up leaves no numbers
-  const int row = blockIdx.x * 128 + warp * 32 + lane;
+  // two threads a row, each half of the columns; a wait that gave up leaves no numbers
+  const int r = threadIdx.x % 128, row = blockIdx.x * 128 + r, wg = warp / 4;
+  const uint32_t tsum = tm + (static_cast<uint32_t>(warp % 4 * 32) << 16);
   T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
   __syncthreads();
   if (ranks == 1) {
-    if (warp < 4)
+    if (warp < 8)
 #pragma unroll 1
-      for (int c = 0; c < N && c < nn * TN; c += 16) {
+      for (int c = wg * 16; c < nn * TN; c += 32) {
         float v[16];
         __syncwarp();
-        tmem_ld16(tm + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+        tmem_ld16(tsum + c, v);
         if (row < a.m)
 #pragma unroll
           for (int i = 0; i < 16 / TN; ++i) {
             const int col = c / TN + i;
             if (col < nn)
               y[static_cast<size_t>(col) * a.m] =
-                  from_f<T>(ok ? by_pow2(TN == 2 ? v[2 * i] + v[2 * i + 1] : v[i], -ew - ex[col]) : NAN);
+                  from_f<T>(ok ? by_pow2(TN == 2 ? v[2 * i] + v[2 * i + 1] : v[i], -ew[r] - ex[col]) : NAN);
           }
       }
   } else {
-    // sums as [column][row] where the operands were, behind them the rows' powers of two
+    // sums as [column][row] where the operands were, behind them the weights' powers of two
     float* out = reinterpret_cast<float*>(sm);
-    if (warp < 4) {
+    if (warp < 8) {
 #pragma unroll 1
-      for (int c = 0; c < N && c < nn * TN; c += 16) {
+      for (int c = wg * 16; c < nn * TN; c += 32) {
         float v[16];
-        tmem_ld16(tm + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+        tmem_ld16(tsum + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) out[(c + i) * 128 + threadIdx.x] = ok ? v[i] : NAN;
+        for (int i = 0; i < 16; ++i) out[(c + i) * 128 + r] = ok ? v[i] : NAN;
       }
-      out[N * 128 + threadIdx.x] = __int_as_float(ew);
+      if (wg == 0) out[N * 128 + r] = __int_as_float(ew[r]);
     }
     cluster_sync();
-    if (warp < 4) {
+    if (warp < 8) {
       int e[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (q < ranks) e[q] = __float_as_int(ld_cluster1(smem_u32(out + N * 128 + threadIdx.x), q));
-      for (int col = rank; col < nn; col += ranks) {
+        if (q < ranks) e[q] = __float_as_int(ld_cluster1(smem_u32(out + N * 128 + r), q));
+      for (int col = wg * ranks + rank; col < nn; col += 2 * ranks) {
         float v[8][TN], sum = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
 #pragma unroll
           for (int t = 0; t < TN; ++t)
-            if (q < ranks) v[q][t] = ld_cluster1(smem_u32(out + (col * TN + t) * 128 + threadIdx.x), q);
+            if (q < ranks) v[q][t] = ld_cluster1(smem_u32(out + (col * TN + t) * 128 + r), q);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (q < ranks) sum += by_pow2(TN == 2 ? v[q][0] + v[q][TN - 1] : v[q][0], -e[q] - ex[col]);
@@ -927,7 +934,7 @@ __global__ void __launch_bounds__(160, 2) k_q4_tc(const MatmulArgs a, const Plan
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tm, M::kCols);
   }
@@ -944,7 +951,7 @@ int launch_tc(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   constexpr int smem = Tc<N>::kBytes;
   if (!allow_smem<k_q4_tc<T, N, G>, smem>()) return S2_ECUDA;
   k_q4_planes<T, true><<<a.n, kPlaneThreads, 0, st>>>(a, p);
-  return launch_joined(k_q4_tc<T, N, G>, dim3(grid, ranks, p.tiles), 160, smem, ranks, a, p, st);
+  return launch_joined(k_q4_tc<T, N, G>, dim3(grid, ranks, p.tiles), kTcThreads, smem, ranks, a, p, st);
 }
 
 template <typename T, int G>
