@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kBlock = 128;  // columns of a code block
 
-// One warp per block of 128 columns; lane l holds columns 4l .. 4l + 3.  A group's scale is its entry
+// One warp per block of 128 columns; lane l holds columns 4l .. 4l + 3 (19456 x 2560: 116 us, bound by its divisions;
+// weights are quantised once).  A group's scale is its entry
 // of the largest magnitude (the first of equals) divided by -8, rounded to bf16, so that entry takes
 // code 0 and the range -8..7 is used whole; the codes are taken against the rounded scale.
 template <typename T>
@@ -70,10 +71,9 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 
 // ---------------------------------------------------------------- products
 //
-// y = x W^T on mma.sync.m16n8k16 (fp16 operands, fp32 sums): 16 weight rows are the A operand, expanded from
-// their codes in registers, 8 activation columns the B operand.  tcgen05 would want the expanded weights in
-// tensor or shared memory first and their group sums read back for every scale; a decode step has 1 to 32
-// columns, and what bounds it is the reading and expanding of the codes.
+// y = x W^T.  Up to 32 columns (activation rows; an fp32 row is two) on mma.sync.m16n8k16 (fp16 operands, fp32 sums):
+// 16 weight rows are the A operand, expanded from their codes in registers, 8 columns the B operand.  tcgen05 wants
+// the expanded weights in tensor memory first; behind 32 columns that pays (k_q4_tc, below).
 //
 // Expanding is masking: a nibble in the low bits of an fp16 is the subnormal code * 2^-24, and four bits up it
 // is 16 times that.  The activations of those positions are staged as x / 16, the products are exact, and the
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 // which keep 2^-34 of it; an fp32 value is two fp16 terms (22 bits), each a column of its own, added at the end.
 //
 // A warp copies its codes ahead of their use (cp.async, its own ring).  Few activations are staged by each
-// block itself (k_q4_few); more of them once, by a kernel in front (k_q4_planes, k_q4_many).
+// block itself (k_q4_few); more of them once, by a kernel in front (k_q4_planes, then k_q4_many or k_q4_tc).
 
 constexpr int kWarps = 8;
 
@@ -295,6 +295,7 @@ __device__ __forceinline__ float unscale(float z, uint32_t top) { return by_pow2
 
 // ---- few activations: one tile of columns, staged whole by every block.  A block is 8 warps: R tiles of 16 rows
 // times 8 / R parts of W's columns (blocks of 128, taken in turn), whose sums are added in order at the end.
+// 19456 x 2560, one fp32 row: 8.8 us, 3.2 TB/s of codes and scales; the launch and the staging are 3 of them.
 constexpr int kFewAhead = 8;
 template <typename T>
 constexpr int kFewItems = sizeof(T) == 4 ? 4 : 8;  // loads of 8 activations that a thread has in flight
@@ -412,12 +413,10 @@ int launch_few(MatmulArgs a, cudaStream_t st) {
 
 // ---- more activations: staged once, as planes in the workspace that every block then copies.
 
-// tcgen05 takes over behind 32 columns (rows; fp32 rows are two): 19456 x 2560 takes 35 us on mma.sync and 23 here at
-// 64 columns, 18.8 and 19.3 at 32; 2560 x 9728 at 32 16.7 and 16.9.
-#ifndef S2_MMA_MOST
-#define S2_MMA_MOST 32
-#endif
-constexpr int kMmaMost = S2_MMA_MOST;
+// tcgen05 takes over behind 32 columns: 19456 x 2560 takes 35 us on mma.sync and 21 there at 64 columns, 18.8 and 18.4
+// at 32; smaller matrices keep mma.sync ahead at 32 (1024 x 1024: 5.8 us and 8.2).
+constexpr int kMmaMost = 32;
+
 // What the workspace holds: for mma.sync `tiles` tiles of 8 columns; for tcgen05 `tiles` tiles of `width` columns, as
 // its B operand (two 128-byte-swizzled tiles of 64 positions a code block).
 struct Planes {
@@ -442,7 +441,7 @@ Planes planes(int n, int k, int terms, void* ws) {
     return p;
   }
   p.width = 8;
-  p.tiles = static_cast<int>(cols <= 8 ? 1 : cols <= 16 ? 2 : (cols + 31) / 32 * 4);  // passes of one, two or four
+  p.tiles = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
   p.inits = reinterpret_cast<float*>(at + parts * p.tiles * 512);
   p.top = reinterpret_cast<uint32_t*>(at + parts * p.tiles * (512 + 32));
   p.bytes = parts * p.tiles * (512 + 32) + static_cast<size_t>(p.tiles) * 8 * 4;
@@ -555,9 +554,11 @@ __device__ __forceinline__ void expand(uint32_t w, __half2 s, uint32_t* v) {
   v[3] = bits(__hmul2(s, __hfma2(h2((w8 & 0x00f000f0u) | m), sixteenth, z16)));
 }
 
-// A block takes 128 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
+// A block takes 64 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
 // their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
-// activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.
+// activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.  32 bf16 rows,
+// 2560 x 9728: 16.7 us, 4 of them until the planes are there and 4 for the join; the steps between take 0.9 us each,
+// bound by what a warp reads of shared memory: all activations for its 16 rows.
 constexpr int kManyWarps = 4, kManyRows = 16 * kManyWarps;
 constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
 template <int NT>
@@ -583,10 +584,9 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
     const size_t part = static_cast<size_t>(b0 + j) * 4;
 #pragma unroll
     for (int i = threadIdx.x; i < 4 * NT * 32; i += 32 * kManyWarps)
-      cp_async16(dst + i * 16, p.b + ((part + i / (NT * 32)) * p.tiles + blockIdx.z * NT) * 32 + i % (NT * 32));
+      cp_async16(dst + i * 16, p.b + part * NT * 32 + i);
     if (threadIdx.x < 8 * NT)
-      cp_async16(dst + 4 * NT * 512 + threadIdx.x * 16, p.inits + ((part + threadIdx.x / (2 * NT)) * p.tiles + blockIdx.z * NT) * 8 +
-                                                            threadIdx.x % (2 * NT) * 4);
+      cp_async16(dst + 4 * NT * 512 + threadIdx.x * 16, p.inits + part * NT * 8 + threadIdx.x * 4);
   };
   // codes do not depend on the kernel in front, which runs after all that came before it
 #pragma unroll
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
     copy_x(i);
     cp_async_commit();  // the first group holds the codes of all of them
   }
-  if (threadIdx.x < 8 * NT / TN) top[threadIdx.x] = p.top[blockIdx.z * (8 * NT / TN) + threadIdx.x];
+  if (threadIdx.x < 8 * NT / TN) top[threadIdx.x] = p.top[threadIdx.x];
   float z[NT][4] = {};
   for (int j = 0; j < count; ++j) {
     cp_async_wait_group<kAhead - 2>();
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
   else
     __syncthreads();
   // a thread adds up four rows of one column
-  const int quads = kManyRows / 4 / ranks, n0 = blockIdx.z * 8 * NT / TN, nn = min(8 * NT / TN, a.n - n0);
-  for (int i = threadIdx.x; i < quads * nn; i += 32 * kManyWarps) {
+  const int quads = kManyRows / 4 / ranks;
+  for (int i = threadIdx.x; i < quads * a.n; i += 32 * kManyWarps) {
     const int r = (rank * quads + i % quads) * 4, col = i / quads, row = blockIdx.x * kManyRows + r;
     float v[4] = {};
     const float* at = out + col * TN * kJoinRow + r;
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
     for (int q = 0; q < 8; ++q)
 #pragma unroll
       for (int t = TN - 1; t >= 0; --t) v[0] += u[q][t].x, v[1] += u[q][t].y, v[2] += u[q][t].z, v[3] += u[q][t].w;
-    T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0 + col) * a.m + row;
+    T* y = static_cast<T*>(a.y) + static_cast<size_t>(col) * a.m + row;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (row + e < a.m) y[e] = from_f<T>(unscale(v[e], top[col]));
@@ -671,37 +671,38 @@ int launch_joined(void (*kernel)(MatmulArgs, Planes), dim3 grid, int threads, in
 
 template <typename T, int NT, int G>
 int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
-  const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + kManyRows - 1) / kManyRows, passes = p.tiles / NT;
-  if (passes > 65535) return S2_EINVAL;
+  const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + kManyRows - 1) / kManyRows;
   // Up to four blocks an SM in clusters of two, about two in larger ones (608 blocks in clusters of four do not all
   // fit at a time: 9728 x 1024, 32 rows, 13.7 us against 8.5), of two code blocks at least.
   int ranks = 1;
-  while (ranks < 8 && static_cast<long long>(grid) * passes * ranks * 2 <= (ranks == 1 ? 608 : 320) && blocks >= 4 * ranks)
+  while (ranks < 8 && static_cast<long long>(grid) * ranks * 2 <= (ranks == 1 ? 608 : 320) && blocks >= 4 * ranks)
     ranks *= 2;
   constexpr int kRings = kManyAhead<NT> * (kManyWarps * kRing + kStepBytes<NT>), kJoin = 8 * NT * kJoinRow * 4;
   constexpr int smem = kRings > kJoin ? kRings : kJoin;
   if (!allow_smem<k_q4_many<T, NT, G>, smem>()) return S2_ECUDA;
   k_q4_planes<T, false><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
-  return launch_joined(k_q4_many<T, NT, G>, dim3(grid, ranks, passes), 32 * kManyWarps, smem, ranks, a, p, st);
+  return launch_joined(k_q4_many<T, NT, G>, dim3(grid, ranks), 32 * kManyWarps, smem, ranks, a, p, st);
 }
 
 // ---- many activations: tcgen05, its A operand the weights.  A block takes 128 rows and N columns; twice four warps
-// expand code blocks in turn, a thread its row's, to fp16 in tensor memory, a ninth copies activations (one bulk copy a
-// code block) and issues the products.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
+// expand code blocks in turn, a thread its row's, to fp16 in tensor memory; a ninth issues the products, a tenth copies
+// activations, one bulk copy a code block.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
 // taken times the power of two that brings the largest of those used here to 2^11 .. 2^12 (scales 2^-28 of it and
 // less lose bits).  The blocks of a cluster split W's columns and add their sums in rank order.
+// 19456 x 2560, 2048 bf16 rows: 227 us, 900 TFLOP/s; 512 rows 60 us; bound by the two blocks' waits for activations
+// (their 32 KB a code block leave room for two).  A block of 256 rows, one an SM with five of those, took 287 us.
 template <int N>
 struct Tc {
   static constexpr int kA = N == 128 ? 2 : 3;                      // expanded code blocks, 64 tensor memory columns each
   static constexpr int kB = N == 32 ? 4 : N == 64 ? 3 : 2;         // code blocks' activations
   static constexpr int kAhead = N == 32 ? 4 : N == 64 ? 3 : 2;     // code blocks of a warp in flight
   static constexpr int kBBytes = N * 256, kRow = 32 * 64 + 32 * 8;  // of a code block: activations; a warp's codes and scales
-  static constexpr int kCodes = kB * kBBytes, kBars = kCodes + 8 * kAhead * kRow, kBytes = kBars + 128 + 1024;
+  static constexpr int kCodes = kB * kBBytes, kBars = kCodes + 8 * kAhead * kRow, kBytes = kBars + 192 + 1024;
   static constexpr uint32_t kCols = 256;
-  static_assert(N + 64 * kA <= 256 && (N + 1) * 512 <= kBars, "room");
+  static_assert(N + 64 * kA <= kCols && (N + 1) * 512 <= kBars, "room");
 };
 
-constexpr int kTcThreads = 288;
+constexpr int kTcThreads = 320;
 template <typename T, int N, int G>
 __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, const Planes p) {
   using M = Tc<N>;
@@ -710,8 +711,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   __shared__ int ex[N / TN], ew[128];  // powers of two of the activations' and the weights' rows
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
   uint64_t* arrived = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [j % kB]: activations of code block j
-  uint64_t *expanded = arrived + M::kB, *used = expanded + M::kA;  // [j % kA]: its weights; both used up
-  uint64_t* done = used + M::kA;                                     // all of them
+  uint64_t* freed = arrived + M::kB;                               // [j % kB]: used up
+  uint64_t *expanded = freed + M::kB, *used = expanded + M::kA;    // [j % kA]: its weights; used up
+  uint64_t* done = used + M::kA;                                   // all of them
   uint32_t* tbase = reinterpret_cast<uint32_t*>(done + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int blocks = (a.k + kBlock - 1) / kBlock;
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / ranks);
   const int count = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / ranks) - b0;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < M::kB; ++i) mbar_init(arrived + i, 1);
+    for (int i = 0; i < 2 * M::kB; ++i) mbar_init(arrived + i, 1);
     for (int i = 0; i < M::kA; ++i) {
       mbar_init(expanded + i, 4);
       mbar_init(used + i, 1);
@@ -739,43 +741,49 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   bool ok = true;
   const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0);
   if (warp == 8) {
-    pdl_wait();
-    for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
+    // ---------------------------------------------------------------- issuing the products
     if (lane == 0) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<size_t>(b0) * p.tiles + blockIdx.z) * M::kBBytes;
-      auto copy = [&](int j) {
-        mbar_arrive_expect_tx(arrived + j % M::kB, M::kBBytes);
-        bulk_g2s_plain(sm + j % M::kB * M::kBBytes, src + static_cast<size_t>(j) * p.tiles * M::kBBytes, M::kBBytes,
-                       arrived + j % M::kB);
-      };
-      for (int j = 0; j < min(count, M::kB); ++j) copy(j);
-      int j = 0;
-      for (; j < count; ++j) {
-        ok = ok && mbar_wait_short(arrived + j % M::kB, j / M::kB & 1);
-        ok = ok && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1);
-        if (!ok) break;
+      for (int j = 0; j < count && ok; ++j) {
+        ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1) && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1);
+        if (!ok) {  // what is under way still ends
+          if (j > 0) mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
+          break;
+        }
         tc_fence_after();
-        const uint32_t b = smem_u32(sm + j % M::kB * M::kBBytes), ta = tm + N + j % M::kA * 64;
+        const uint32_t ta = tm + N + j % M::kA * 64;
+        const uint64_t b = desc_sw128(smem_u32(sm + j % M::kB * M::kBBytes));
 #pragma unroll
         for (int k = 0; k < kBlock / 16; ++k)
-          tc_mma_tmem_a(tm, ta + k * 8, desc_sw128(b + k / 4 * (N * 128) + k % 4 * 32), idesc_f16(128, N), j > 0 || k > 0);
+          tc_mma_tmem_a(tm, ta + k * 8, b + ((k / 4 * (N * 128) + k % 4 * 32) >> 4), idesc_f16(128, N), j > 0 || k > 0);
+        tc_commit(freed + j % M::kB);
         tc_commit(used + j % M::kA);
         if (j == count - 1) tc_commit(done);
-        if (j > 0 && j - 1 + M::kB < count) {  // the place of block j - 1
-          ok = mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
-          if (ok) copy(j - 1 + M::kB);
-        }
-      }
-      if (!ok) {  // what is in flight still comes
-        if (j > 0) mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
-        for (int i = j; i < min(count, j + M::kB - 1); ++i) mbar_wait_short(arrived + i % M::kB, i / M::kB & 1);
       }
     }
     __syncwarp();
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- copying activations
+    pdl_wait();
+    if (lane == 0) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<size_t>(b0) * p.tiles + blockIdx.z) * M::kBBytes;
+      int j = 0;
+      for (; j < count; ++j) {
+        if (j >= M::kB) ok = mbar_wait_short(freed + j % M::kB, (j / M::kB - 1) & 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(arrived + j % M::kB, M::kBBytes);
+        bulk_g2s_plain(sm + j % M::kB * M::kBBytes, src + static_cast<size_t>(j) * p.tiles * M::kBBytes, M::kBBytes,
+                       arrived + j % M::kB);
+      }
+      if (!ok)  // what is in flight still comes
+        for (int i = j - M::kB; i < j; ++i) mbar_wait_short(arrived + i % M::kB, i / M::kB & 1);
+    }
+    __syncwarp();
+    for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
   } else {
+    // ---------------------------------------------------------------- expanding
     const int wg = warp / 4, mine = (count - wg + 1) / 2;  // the code blocks 2 t + wg
     uint8_t* ring = sm + M::kCodes + warp * M::kAhead * M::kRow;
-    const int row0 = blockIdx.x * 128 + warp % 4 * 32;
+    const int in = warp % 4 * 32, row0 = blockIdx.x * 128 + in;
     const uint8_t* from[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -825,9 +833,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
         if (lane == r) most = max(most, t);
       }
     }
-    if (lane < 16) ew[warp % 4 * 32 + wg * 16 + lane] = most == 0 ? 0 : min(11 + 127 - static_cast<int>(most >> 7), 126);
+    if (lane < 16) ew[in + wg * 16 + lane] = most == 0 ? 0 : min(11 + 127 - static_cast<int>(most >> 7), 126);
     named_bar(1, 256);
-    const float up = pow2(ew[warp % 4 * 32 + lane]);
+    const float up = pow2(ew[in + lane]);
     const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp % 4 * 32) << 16);
     for (int t = 0; t < mine; ++t) {
       const int j = 2 * t + wg;
