@@ -951,7 +951,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
 template <typename T, int N, int G>
 int launch_tc(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   const int blocks = (a.k + kBlock - 1) / kBlock, grid = (a.m + 127) / 128;
-  if (p.tiles > 65535) return S2_EINVAL;
   // Clusters up to what the SMs hold (two blocks each): 256 columns, 2560 x 9728, 34 us against 57 with one block an
   // SM; 19456 x 2560 at 64 columns 23 against 41 with four, which take two rounds.
   int ranks = 1;
@@ -973,7 +972,7 @@ int launch_matmul(const MatmulArgs& a, void* ws, cudaStream_t st) {
                       : p.tiles == 2 ? launch_many<T, 2, G>(a, p, st) : launch_many<T, 4, G>(a, p, st);
 }
 
-constexpr int kMatmulMost = 1 << 28;  // of each size
+constexpr int kRowsMost = 1 << 21, kMatmulMost = 1 << 28;  // activation rows, the other sizes
 
 bool bad_group(int group) { return group != 32 && group != 64 && group != 128; }
 
@@ -1002,7 +1001,7 @@ extern "C" int s2_quantize_q4(const void* w, int dtype, long long rows, int cols
 }
 
 extern "C" size_t s2_q4_matmul_workspace(int n, int k, int dtype) {
-  if (n < 1 || k < 1 || n > kMatmulMost || k > kMatmulMost || !dtype_bytes(dtype)) return 0;
+  if (n < 1 || k < 1 || n > kRowsMost || k > kMatmulMost || !dtype_bytes(dtype)) return 0;
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     return few<T>(n, (k + kBlock - 1) / kBlock) ? size_t{0} : planes(n, k, kTerms<T>, nullptr).bytes;
@@ -1014,7 +1013,7 @@ extern "C" int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride,
                             CUstream_st* stream) {
   const int esz = dtype_bytes(dtype);
   if (!x || !codes || !scales || !y || !esz || n < 1 || m < 1 || k < 1 || bad_group(group) || k % group != 0 ||
-      x_stride < k || n > kMatmulMost || m > kMatmulMost || k > kMatmulMost)
+      x_stride < k || n > kRowsMost || m > kMatmulMost || k > kMatmulMost)
     return S2_EINVAL;
   if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || x_stride * esz % 16 != 0 ||
       reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % 16 != 0 ||

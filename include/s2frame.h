@@ -356,14 +356,15 @@ int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group
  * rows quantised as above.  Activations keep their precision: bf16 and fp16 rows enter the products
  * as they are and fp32 rows with 22 bits, but for elements 2^-24 below their row's largest (of an
  * fp32 row 2^-13), which are taken to 2^-34 of it.  A row with an element that is not finite gives
- * results that are not.
+ * results that are not.  With more than 32 of them (fp32: 16) a row's scales below 2^-28 of its
+ * largest lose bits.  A wait on the device that gives up (after a second or so) leaves NaN.
  *   x         device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times
  *             the element size a multiple of 16
  *   codes, scales  as s2_quantize_q4 writes them, both 16-byte aligned; k a multiple of group
  *   y         device [n][m] of dtype, aligned to its element size
  *   workspace device, 16-byte aligned, of at least s2_q4_matmul_workspace bytes for the same sizes
  *             (NULL where that is 0).  Calls that may run at the same time need one each.
- * Each size at most 2^28. */
+ * n at most 2^21, the other sizes 2^28. */
 size_t s2_q4_matmul_workspace(int n, int k, int dtype);
 int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride, const uint8_t* codes, const void* scales,
                  int m, int k, int group, void* y, void* workspace, size_t ws_bytes, struct CUstream_st* stream);
@@ -428,7 +429,8 @@ int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* strea
  * h / (n_head / n_kv_head) at positions 0 .. its own, scores scaled by `scale`.  A row that sees no
  * position (lengths[s] short of the sequence's rows) gets zeros; what a page holds past a
  * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
- * are not attended.
+ * are not attended.  A wait on the device that gives up (after a second or so) writes S2_ETIMEOUT
+ * to `status`; the results are then not to be used.
  *   q, out    device [n_rows][n_head][head_dim] of dtype, 16-byte aligned
  *   max_len   the largest length expected, by which the work is split (0, or more than table_cols
  *             pages hold: those); a longer sequence is still right

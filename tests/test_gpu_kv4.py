@@ -438,3 +438,33 @@ def test_attention_captured_and_replayed_with_other_lengths():
         torch.cuda.synchronize()
         assert torch.equal(graphs[0][2], graphs[1][2])
         _check_attention(graphs[0][2], q.cpu(), pages, table, q_start, np.asarray(new), 128 ** -0.5, torch.float16)
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("fp32", 128)])
+def test_attention_of_many_rows_beside_products_on_other_streams(dtype, hd):
+    """Calls of both operators that use tensor memory, on three streams at once: each gives its own bits."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(17)
+    spans = [(60, 700), (200, 1300), (33, 64)]
+    table, q_start, lengths, pool = _layout(spans, rng, cols=24)
+    dt = fb.TYPES[dtype]
+    pages = torch.zeros((pool, 8, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((293, 32, hd)).astype(np.float32)).to(dt).cuda()
+    args = (q, pages.cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(q_start).cuda(),
+            torch.from_numpy(lengths).cuda())
+    w = torch.randn((2500, 1280), generator=torch.Generator().manual_seed(2)).cuda()
+    codes, scales = pkg.quantize_q4(w, 64)
+    xs = [torch.randn((n, 1280), generator=torch.Generator().manual_seed(n)).to(dt).cuda() for n in (40, 300)]
+    calls = [lambda: pkg.kv4_attention(*args)] + [lambda x=x: pkg.q4_matmul(x, codes, scales, 64) for x in xs]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for f, s, g in zip(calls, streams, got):
+            with torch.cuda.stream(s):
+                g.append(f())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, y) for y in g)
