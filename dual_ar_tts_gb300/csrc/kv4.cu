@@ -136,7 +136,7 @@ struct Quotients {
 // where any of them needs it.
 template <typename T, int HD>
 __device__ __forceinline__ void append_item(const AppendArgs& a, int row, const Place& at, int h, int sub, bool live,
-                                            float (&x)[8]) {
+                                            const float4 (&cs)[2], float (&x)[8]) {
   using B = Kv4Block<HD>;
   const bool is_q = h < a.n_head, is_v = h >= a.n_head + a.c.n_kv_head, is_k = !is_q && !is_v;
   const float* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
@@ -157,11 +157,9 @@ __device__ __forceinline__ void append_item(const AppendArgs& a, int row, const 
     for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), ww[i]);
   }
   if (!is_v) {
-    const float4* cs = reinterpret_cast<const float4*>(a.rope) + (static_cast<size_t>(at.pos) * (HD / 2) + sub * 4) / 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 t = __ldg(cs + i);
-      const float t4[4] = {t.x, t.y, t.z, t.w};
+      const float t4[4] = {cs[i].x, cs[i].y, cs[i].z, cs[i].w};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float u = x[4 * i + 2 * k], v = x[4 * i + 2 * k + 1];
@@ -215,7 +213,7 @@ __device__ __forceinline__ void append_item(const AppendArgs& a, int row, const 
 
 // A block takes one row of the call and some of its heads; its warps take heads in turn.  The first load of a head
 // does not wait for the row's place.  One pass: a head is read once, and its sums and extremes are shuffles in a
-// quarter or half of a warp.  5916 fp16 rows of 32 + 2 x 8 heads: 47 us, 2.7 TB/s; bound by instructions (the norm of
+// quarter or half of a warp.  5916 fp16 rows of 32 + 2 x 8 heads: 46.6 us, 2.7 TB/s; bound by instructions (the norm of
 // keys to the last bit, the quotients and codes), not by the bytes, which would take 19.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) k_kv4_append(const AppendArgs a) {
@@ -242,10 +240,12 @@ __global__ void __launch_bounds__(256) k_kv4_append(const AppendArgs a) {
     if (lane == 0) kv4_bad(a.c.status);
     return;
   }
+  const float4* rope = reinterpret_cast<const float4*>(a.rope) + (static_cast<size_t>(at.pos) * (HD / 2) + sub * 4) / 2;
+  const float4 cs[2] = {__ldg(rope), __ldg(rope + 1)};  // the same for all heads
   for (; h0 < heads; h0 += step) {
     const int h = h0 + lane / kLanes<HD>;
     if (h0 + step < heads) load(h + step, y);
-    append_item<T, HD>(a, row, at, h, sub, h < heads, x);
+    append_item<T, HD>(a, row, at, h, sub, h < heads, cs, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = y[i];
   }
@@ -316,14 +316,17 @@ extern "C" int s2_kv4_append(const s2_kv4* cache, const void* qkv, int dtype, lo
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // Few rows: a warp for every 2 (hd 128) or 4 heads.  Many: one block a row, whose warps load a head ahead
-    // (4700 rows of 48 heads: 65 us against 74, with the reading back).
+    // Few rows: a warp for every 2 (hd 128) or 4 heads.  Many: one block of four warps a row, each of which finds the
+    // row's place and its rotation once and loads a head ahead (5916 rows of 48 heads: 46.6 us; with two warps 49.3,
+    // with eight 50.5; before, with a warp for every 2 heads, 4700 rows took 74 us with the reading back, not 65).
     const int turns = static_cast<int>((heads * cache->head_dim / 8 + 255) / 256);
-    const dim3 grid(cache->n_rows, cache->n_rows >= 512 ? 1 : turns);
+    const bool many = cache->n_rows >= 512;
+    const dim3 grid(cache->n_rows, many ? 1 : turns);
+    const int threads = many ? 128 : 256;
     if (cache->head_dim == 64)
-      k_kv4_append<T, 64><<<grid, 256, 0, st>>>(a);
+      k_kv4_append<T, 64><<<grid, threads, 0, st>>>(a);
     else
-      k_kv4_append<T, 128><<<grid, 256, 0, st>>>(a);
+      k_kv4_append<T, 128><<<grid, threads, 0, st>>>(a);
   });
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
