@@ -71,9 +71,9 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 
 // ---------------------------------------------------------------- products
 //
-// y = x W^T.  Up to 32 columns (activation rows; an fp32 row is two) on mma.sync.m16n8k16 (fp16 operands, fp32 sums):
+// y = x W^T.  Up to 16 or 32 columns (activation rows; an fp32 row is two) on mma.sync.m16n8k16 (fp16 operands, fp32 sums):
 // 16 weight rows are the A operand, expanded from their codes in registers, 8 columns the B operand.  tcgen05 wants
-// the expanded weights in tensor memory first; behind 32 columns that pays (k_q4_tc, below).
+// the expanded weights in tensor memory first; with more columns that pays (k_q4_tc, below).
 //
 // Expanding is masking: a nibble in the low bits of an fp16 is the subnormal code * 2^-24, and four bits up it
 // is 16 times that.  The activations of those positions are staged as x / 16, the products are exact, and the
@@ -413,9 +413,12 @@ int launch_few(MatmulArgs a, cudaStream_t st) {
 
 // ---- more activations: staged once, as planes in the workspace that every block then copies.
 
-// tcgen05 takes over behind 32 columns: 19456 x 2560 takes 35 us on mma.sync and 21 there at 64 columns, 18.8 and 18.4
-// at 32; smaller matrices keep mma.sync ahead at 32 (1024 x 1024: 5.8 us and 8.2).
-constexpr int kMmaMost = 32;
+// tcgen05 takes over behind 32 columns (19456 x 2560 at 64: 35 us on mma.sync, 20 there), and behind 16 for matrices
+// of 12 Mi weights on: 2560 x 9728 at 32 columns 16.3 us and 14.2, at 17 15.3 and 13.8, 6144 x 2560 at 24 12.7 and 12.0;
+// but 2560 x 2560 at 17 8.4 and 10.3, 1024 x 1024 at 32 5.6 and 7.7.
+bool on_tcgen05(long long cols, int m, int k) {
+  return cols > 32 || (cols > 16 && static_cast<long long>(m) * k >= 12ll << 20);
+}
 
 // What the workspace holds: for mma.sync `tiles` tiles of 8 columns; for tcgen05 `tiles` tiles of `width` columns, as
 // its B operand (two 128-byte-swizzled tiles of 64 positions a code block).
@@ -426,13 +429,13 @@ struct Planes {
   int tiles, width;
   size_t bytes;
 };
-Planes planes(int n, int k, int terms, void* ws) {
+Planes planes(int n, int k, int terms, bool tc, void* ws) {
   Planes p{};
   const long long cols = static_cast<long long>(n) * terms;
   const size_t blocks = (static_cast<size_t>(k) + kBlock - 1) / kBlock, parts = blocks * 4;
   uint8_t* at = static_cast<uint8_t*>(ws);
   p.b = reinterpret_cast<uint4*>(at);
-  if (cols > kMmaMost) {
+  if (tc) {
     p.width = cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
     p.tiles = static_cast<int>((cols + p.width - 1) / p.width);
     const size_t b = blocks * p.tiles * p.width * 256;
@@ -556,9 +559,8 @@ __device__ __forceinline__ void expand(uint32_t w, __half2 s, uint32_t* v) {
 
 // A block takes 64 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
 // their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
-// activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.  32 bf16 rows,
-// 2560 x 9728: 16.7 us, 4 of them until the planes are there and 4 for the join; the steps between take 0.9 us each,
-// bound by what a warp reads of shared memory: all activations for its 16 rows.
+// activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.  16 bf16 rows,
+// 19456 x 2560: 14.5 us; 17 rows, 2560 x 2560: 8.4.  At 32 columns a step of 128 takes 0.9 us, bound by mma.sync.
 constexpr int kManyWarps = 4, kManyRows = 16 * kManyWarps;
 constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
 template <int NT>
@@ -689,8 +691,9 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
 // activations, one bulk copy a code block.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
 // taken times the power of two that brings the largest of those used here to 2^11 .. 2^12 (scales 2^-28 of it and
 // less lose bits).  The blocks of a cluster split W's columns and add their sums in rank order.
-// 19456 x 2560, 2048 bf16 rows: 227 us, 900 TFLOP/s; 512 rows 60 us; bound by the two blocks' waits for activations
-// (their 32 KB a code block leave room for two).  A block of 256 rows, one an SM with five of those, took 287 us.
+// 19456 x 2560, 2048 bf16 rows: 207 us, 990 TFLOP/s; 512 rows 53 us; bound by the activations that every block reads
+// again from L2 (9 TB/s).  2560 x 9728, 32 rows: 14.2 us, 4 of them until the planes are there and scales looked
+// through, 4 for the join.
 template <int N>
 struct Tc {
   static constexpr int kA = N == 128 ? 2 : 3;                      // expanded code blocks, 64 tensor memory columns each
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   uint64_t *expanded = freed + M::kB, *used = expanded + M::kA;    // [j % kA]: its weights; used up
   uint64_t* done = used + M::kA;                                   // all of them
   uint32_t* tbase = reinterpret_cast<uint32_t*>(done + 1);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int blocks = (a.k + kBlock - 1) / kBlock;
   const int ranks = gridDim.y, rank = blockIdx.y;
   const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / ranks);
@@ -736,13 +739,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *tbase;
+  const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
 
   bool ok = true;
   const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0);
   if (warp == 8) {
     // ---------------------------------------------------------------- issuing the products
-    if (lane == 0) {
+    if (elect_one()) {
       for (int j = 0; j < count && ok; ++j) {
         ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1) && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1);
         if (!ok) {  // what is under way still ends
@@ -964,8 +967,9 @@ int launch_tc(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
 template <typename T, int G>
 int launch_matmul(const MatmulArgs& a, void* ws, cudaStream_t st) {
   if (few<T>(a.n, (a.k + kBlock - 1) / kBlock)) return launch_few<T, G>(a, st);
-  const Planes p = planes(a.n, a.k, kTerms<T>, ws);
-  if (p.width > 8)
+  const bool tc = on_tcgen05(static_cast<long long>(a.n) * kTerms<T>, a.m, a.k);
+  const Planes p = planes(a.n, a.k, kTerms<T>, tc, ws);
+  if (tc)
     return p.width == 32 ? launch_tc<T, 32, G>(a, p, st)
                          : p.width == 64 ? launch_tc<T, 64, G>(a, p, st) : launch_tc<T, 128, G>(a, p, st);
   return p.tiles == 1 ? launch_many<T, 1, G>(a, p, st)
@@ -1004,7 +1008,11 @@ extern "C" size_t s2_q4_matmul_workspace(int n, int k, int dtype) {
   if (n < 1 || k < 1 || n > kRowsMost || k > kMatmulMost || !dtype_bytes(dtype)) return 0;
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return few<T>(n, (k + kBlock - 1) / kBlock) ? size_t{0} : planes(n, k, kTerms<T>, nullptr).bytes;
+    if (few<T>(n, (k + kBlock - 1) / kBlock)) return size_t{0};
+    // whatever the matrix
+    const size_t tc = planes(n, k, kTerms<T>, true, nullptr).bytes;
+    return on_tcgen05(static_cast<long long>(n) * kTerms<T>, 1, 1) ? tc
+                                                                   : std::max(tc, planes(n, k, kTerms<T>, false, nullptr).bytes);
   });
 }
 

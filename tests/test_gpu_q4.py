@@ -211,3 +211,11 @@ def test_matmul_of_many_rows_in_a_graph_beside_another():
     torch.cuda.synchronize()
     for _, x, out, _ in runs:
         assert torch.equal(out, pkg.q4_matmul(x, codes, scales, 64))
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 17), ("fp16", 32), ("fp32", 9), ("fp32", 16)])
+@pytest.mark.parametrize("m,k,group", [(1300, 9728, 128), (5000, 2560, 64), (4930, 2560, 32)])
+def test_matmul_of_large_matrices(dtype, n, m, k, group):
+    """17 to 32 columns (an fp32 row is two) of matrices on both sides of 12 Mi weights."""
+    test_matmul(dtype, n, m, k, group)
+    test_matmul(dtype, n, (12 << 20) // k - 1, k, group)
