@@ -425,8 +425,8 @@ constexpr int kDecodeSmem = std::max(kWarps * kDepth * Stage<HD>::kBytes, kWarps
 
 // Few columns: a block takes one tile of 8 columns of one KV head over a range of pages, two at a time.  Each of
 // its four warps takes half a page with its own copies in flight, so the warps never wait on one another until
-// their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 79.5 us, 3.9 TB/s of the
-// cache; 32 of 512 .. 4096: 31 us.  Bound by the instructions that expand codes (about 60 million a call of the first,
+// their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 78 us, 3.9 TB/s of the
+// cache; 32 of 512 .. 4096: 30 us.  Bound by the instructions that expand codes (55 million a call of the first,
 // 2.7 of 4 issued a cycle; the copies alone take 55 us), each of which serves four query heads here.
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
     if (usable >> (turn & 31) & 1) {
       const uint32_t at = smem_u32(ring + turn % kDepth * S::kBytes);
       const int first = (p0 + 2 * turn + warp / 2) * kPage + half * kHalfPage;
-#pragma unroll 1
+#pragma unroll
       for (int step = 0; step < 2; ++step) {
         const int t0 = first + step * kStep, valid = min(len - t0, kStep);
         if (valid <= 0) break;
