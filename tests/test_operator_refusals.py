@@ -109,3 +109,13 @@ def test_python_checks():
                  lambda: pkg.kv4_pages(1, 1, 96)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_q4_matmul_sizes(lib):
+    """The largest counts are taken, one more is not; a workspace serves whatever matrix follows."""
+    import dual_ar_tts_gb300 as pkg
+    assert lib.s2_q4_matmul_workspace(1 << 21, 128, pkg.S2_F32) > 0
+    assert lib.s2_q4_matmul_workspace((1 << 21) + 1, 128, pkg.S2_F32) == 0
+    assert lib.s2_q4_matmul_workspace(40, (1 << 28) + 1, pkg.S2_BF16) == 0
+    sizes = [lib.s2_q4_matmul_workspace(n, 2560, pkg.S2_BF16) for n in (1, 8, 9, 16, 17, 32, 33, 64, 65, 500)]
+    assert sizes[0] == 0 and all(a <= b for a, b in zip(sizes[2:], sizes[3:]))
