@@ -75,15 +75,16 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 // 16 weight rows are the A operand, expanded from their codes in registers, 8 columns the B operand.  tcgen05 wants
 // the expanded weights in tensor memory first; with more columns that pays (k_q4_tc, below).
 //
-// Expanding is masking: a nibble in the low bits of an fp16 is the subnormal code * 2^-24, and four bits up it
-// is 16 times that.  The activations of those positions are staged as x / 16, the products are exact, and the
-// 8 that each code is off by goes into the sum's start, -8 * 2^-24 * sum x.  A 32-bit word of codes feeds the
-// k positions of two instructions in the order (0,4)(1,5) | (2,6)(3,7) of its nibbles; activations are staged
-// in that order.  A group's scale multiplies its fp32 sum.
+// A code is expanded to the whole number code - 8.  (Masked alone it would be the fp16 subnormal code * 2^-24, and the
+// sum would have to start with -8 * sum x.  That costs two instructions a word less, 10.5 us against 11.3 for one row
+// of 19456 x 2560, but the tensor cores line products up by their operands' exponents and cut off what is below a
+// sum's last bit, and the rest cancels: fp32 products were 1e-6 to 2e-6 off, where they now are 1e-7.)  A 32-bit word of codes feeds the k positions of two instructions in the
+// order (0,4)(1,5) | (2,6)(3,7) of its nibbles; activations are staged in that order.  A group's scale multiplies its
+// fp32 sum.
 //
 // Activations are scaled by a power of two so that the largest of a row (of a staged chunk of it) lies in
-// 2^13 .. 2^14.  fp16 and bf16 values are then exact in fp16, but for elements 2^-24 below the largest and less,
-// which keep 2^-34 of it; an fp32 value is two fp16 terms (22 bits), each a column of its own, added at the end.
+// 2^13 .. 2^14.  fp16 and bf16 values are then exact in fp16, but for elements 2^-27 below the largest and less,
+// which keep 2^-38 of it; an fp32 value is two fp16 terms (22 bits), each a column of its own, added at the end.
 //
 // A warp copies its codes ahead of their use (cp.async, its own ring).  Few activations are staged by each
 // block itself (k_q4_few); more of them once, by a kernel in front (k_q4_planes, then k_q4_many or k_q4_tc).
@@ -121,13 +122,13 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// d = A b + init, and d += A b
+// d = A b, and d += A b
 __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1, float2 init) {
+                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %10, %11};"
+      "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(init.x), "f"(init.y));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_more(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -153,38 +154,43 @@ struct MatmulArgs {
   int tiles;  // R
 };
 
-// One 8-element item of an activation row (columns 8c .. 8c + 7 of a 32-column part, the four lanes c of a part
-// side by side in the warp), scaled by `up`: the B operand's 16 bytes of each term, and what the part's sum of
-// codes starts with (for all four lanes).
+// One 8-element item of an activation row, scaled by `up`: the B operand's 16 bytes of each term, as the pairs
+// (0,4) (1,5) (2,6) (3,7).
 template <typename T>
 struct Staged {
   uint4 b[kTerms<T>];
-  float init[kTerms<T>];
   __device__ __forceinline__ Staged(const Eight<T>& v, float up) {
     float rest[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) rest[e] = v[e] * up;
 #pragma unroll
     for (int t = 0; t < kTerms<T>; ++t) {
-      uint32_t h[4];  // pairs (0,4) (1,5) (2,6) (3,7), the odd ones sixteen times too small
-      float sum = 0.f;
+      uint32_t h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = e % 2 ? 0.0625f : 1.f, back = e % 2 ? 16.f : 1.f;
-        const __half2 p = __floats2half2_rn(rest[e] * f, rest[e + 4] * f);
-        const float2 r = __half22float2(p);
-        h[e] = *reinterpret_cast<const uint32_t*>(&p);
-        sum += (r.x + r.y) * back;
-        rest[e] -= r.x * back;
-        rest[e + 4] -= r.y * back;
+        const __half2 two = __floats2half2_rn(rest[e], rest[e + 4]);
+        const float2 r = __half22float2(two);
+        h[e] = *reinterpret_cast<const uint32_t*>(&two);
+        rest[e] -= r.x;
+        rest[e + 4] -= r.y;
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       b[t] = make_uint4(h[0], h[1], h[2], h[3]);
-      init[t] = sum * (-8.f / 16777216.f);
     }
   }
 };
+
+// The eight codes of a word as fp16 code - 8, in the order 0 4 1 5 2 6 3 7.  0x6400 | code is 1024 + code in fp16 and
+// 0x6400 | code << 4 is 1024 + 16 code: code - 8 comes out of one exact subtraction or FMA.
+__device__ __forceinline__ void expand(uint32_t w, __half2 (&v)[4]) {
+  const uint32_t m = 0x64006400u, w8 = w >> 8;
+  const __half2 z = __float2half2_rn(1032.f), z16 = __float2half2_rn(-72.f), sixteenth = __float2half2_rn(0.0625f);
+  auto h2 = [](uint32_t u) { return *reinterpret_cast<__half2*>(&u); };
+  v[0] = __hsub2(h2((w & 0x000f000fu) | m), z);
+  v[1] = __hfma2(h2((w & 0x00f000f0u) | m), sixteenth, z16);
+  v[2] = __hsub2(h2((w8 & 0x000f000fu) | m), z);
+  v[3] = __hfma2(h2((w8 & 0x00f000f0u) | m), sixteenth, z16);
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
 template <typename T>
 __device__ __forceinline__ uint32_t largest(const Eight<T>& v) {  // bits of the magnitude; NaN counts as the largest
@@ -239,11 +245,11 @@ struct Codes {
   }
 };
 
-// One code block (entry j of a ring) times the staged activations: z += W x, in units of 2^-24.  xq: this lane's
-// B operands, part p of tile t at xq[p * part_stride + t * 32]; iq: its sums' starts, at iq[(p * NT + t) * 4].
+// One code block (entry j of a ring) times the staged activations: z += W x.  xq: this lane's B operands, part p of
+// tile t at xq[p * part_stride + t * 32].
 template <int NT, int G>
 __device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t par1, const uint4* xq, int part_stride,
-                                         const float2* iq, float (&z)[NT][4]) {
+                                         float (&z)[NT][4]) {
   const int lane = threadIdx.x % 32, g = lane / 4;
   const uint4 w0 = lds128(at + lane * 16), w1 = lds128(at + 512 + lane * 16);
   float s0[4], s1[4];
@@ -264,20 +270,18 @@ __device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t pa
   float d[NT][4];
 #pragma unroll
   for (int part = 0; part < 4; ++part) {
-    const uint32_t p = wv[0][part], q = wv[1][part], p8 = p >> 8, q8 = q >> 8;
-    constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+    __half2 p[4], q[4];
+    expand(wv[0][part], p);
+    expand(wv[1][part], q);
     const bool first = part * 32 % G == 0, last = (part + 1) * 32 % G == 0;  // of a group
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const uint4 x = xq[part * part_stride + t * 32];
-      const float2 i0 = iq[(part * NT + t) * 4];
-      if (first) {
-        mma_first(d[t], p & lo, q & lo, p & hi, q & hi, x.x, x.y, i0);
-      } else {
-        d[t][0] += i0.x, d[t][1] += i0.y, d[t][2] += i0.x, d[t][3] += i0.y;
-        mma_more(d[t], p & lo, q & lo, p & hi, q & hi, x.x, x.y);
-      }
-      mma_more(d[t], p8 & lo, q8 & lo, p8 & hi, q8 & hi, x.z, x.w);
+      if (first)
+        mma_first(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
+      else
+        mma_more(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
+      mma_more(d[t], h2_bits(p[2]), h2_bits(q[2]), h2_bits(p[3]), h2_bits(q[3]), x.z, x.w);
       if (last) {
         z[t][0] += s0[part] * d[t][0];
         z[t][1] += s0[part] * d[t][1];
@@ -291,11 +295,12 @@ __device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t pa
 // z * 2^e, the power itself perhaps out of fp32's range (e from -252 to 252)
 __device__ __forceinline__ float by_pow2(float z, int e) { return z * pow2(e / 2) * pow2(e - e / 2); }
 // a row's sum with its scaling taken back
-__device__ __forceinline__ float unscale(float z, uint32_t top) { return by_pow2(z, 24 - scale_exponent(top)); }
+__device__ __forceinline__ float unscale(float z, uint32_t top) { return by_pow2(z, -scale_exponent(top)); }
 
 // ---- few activations: one tile of columns, staged whole by every block.  A block is 8 warps: R tiles of 16 rows
 // times 8 / R parts of W's columns (blocks of 128, taken in turn), whose sums are added in order at the end.
-// 19456 x 2560, one fp32 row: 8.8 us, 3.2 TB/s of codes and scales; the launch and the staging are 3 of them.
+// 19456 x 2560, one fp32 row, weights not in L2: 11.3 us, 2.5 TB/s of codes and scales; the launch and the staging are
+// 3 of them.
 constexpr int kFewAhead = 8;
 template <typename T>
 constexpr int kFewItems = sizeof(T) == 4 ? 4 : 8;  // loads of 8 activations that a thread has in flight
@@ -309,7 +314,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_few(const MatmulArgs a) {
   const int parts = kWarps / a.tiles, tile = warp % a.tiles, part_k = warp / a.tiles;
   const int blocks = (a.k + kBlock - 1) / kBlock, nn = a.n, live = nn * TN;
   uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kFewAhead * kRing);  // [block, part][live column][lane c]
-  float* inits = reinterpret_cast<float*>(xs + blocks * 16 * live);         // [block, part][8]
   const int row0 = (blockIdx.x * a.tiles + tile) * 16;
 
   Codes<G, kFewAhead> codes(smem + warp * kFewAhead * kRing, a, row0, blocks, part_k,
@@ -353,10 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_few(const MatmulArgs a) {
     const Staged<T> st(held[u], pow2(scale_exponent(top[row])));
     if (i < items)
 #pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        xs[(p * live + row * TN + t) * 4 + c] = st.b[t];
-        if (c == 0) inits[p * 8 + row * TN + t] = st.init[t];
-      }
+      for (int t = 0; t < TN; ++t) xs[(p * live + row * TN + t) * 4 + c] = st.b[t];
   }
   __syncthreads();
 
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_q4_few(const MatmulArgs a) {
     cp_async_wait_group<kFewAhead - 1>();
     __syncwarp();
     multiply<1, G>(smem_u32(codes.ring + j % kFewAhead * kRing), codes.par0 + j * parts, codes.par1 + j * parts,
-                   xl + b * 16 * live, 4 * live, reinterpret_cast<const float2*>(inits + b * 32) + c, z);
+                   xl + b * 16 * live, 4 * live, z);
     __syncwarp();
   }
   cp_async_wait_all();
@@ -396,16 +397,16 @@ bool few(int n, int blocks) {
          static_cast<long long>(n) * blocks * 16 <= kFewItems<T> * 32 * kWarps;
 }
 
-// shared memory: at most kFewItems * 16 (row, block) pairs, of which one row has the most room for sums
+// shared memory: at most kFewItems * 16 (row, block) pairs
 template <typename T>
-constexpr int kFewMost = kWarps * kFewAhead * kRing + kFewItems<T> * 16 * (256 * kTerms<T> + 128);
+constexpr int kFewMost = kWarps * kFewAhead * kRing + kFewItems<T> * 16 * 256 * kTerms<T>;
 
 template <typename T, int G>
 int launch_few(MatmulArgs a, cudaStream_t st) {
   const int all = (a.m + 15) / 16, blocks = (a.k + kBlock - 1) / kBlock;
   a.tiles = kWarps;  // R: the most row tiles in a block that leave two blocks an SM
   while (a.tiles > 1 && (all + a.tiles - 1) / a.tiles < 304) a.tiles /= 2;
-  const int smem = kWarps * kFewAhead * kRing + blocks * (256 * a.n * kTerms<T> + 128);
+  const int smem = kWarps * kFewAhead * kRing + blocks * 256 * a.n * kTerms<T>;
   if (!allow_smem<k_q4_few<T, G>, kFewMost<T>>()) return S2_ECUDA;
   k_q4_few<T, G><<<(all + a.tiles - 1) / a.tiles, 32 * kWarps, smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
@@ -424,7 +425,6 @@ bool on_tcgen05(long long cols, int m, int k) {
 // its B operand (two 128-byte-swizzled tiles of 64 positions a code block).
 struct Planes {
   uint4* b;       // [block, part][tile][lane], or [block][tile][half][column][chunk]
-  float* inits;   // [block, part][8 tiles] (mma.sync)
   uint32_t* top;  // [row]
   int tiles, width;
   size_t bytes;
@@ -445,9 +445,8 @@ Planes planes(int n, int k, int terms, bool tc, void* ws) {
   }
   p.width = 8;
   p.tiles = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  p.inits = reinterpret_cast<float*>(at + parts * p.tiles * 512);
-  p.top = reinterpret_cast<uint32_t*>(at + parts * p.tiles * (512 + 32));
-  p.bytes = parts * p.tiles * (512 + 32) + static_cast<size_t>(p.tiles) * 8 * 4;
+  p.top = reinterpret_cast<uint32_t*>(at + parts * p.tiles * 512);
+  p.bytes = parts * p.tiles * 512 + static_cast<size_t>(p.tiles) * 8 * 4;
   return p;
 }
 
@@ -486,37 +485,19 @@ __global__ void __launch_bounds__(kPlaneThreads) k_q4_planes(const MatmulArgs a,
   const float up = pow2(scale_exponent(top));
   if (threadIdx.x == 0) p.top[row] = top;
   auto store = [&](const Eight<T>& v, int i) {
-    if constexpr (kTc) {
-      if (i >= items) return;
-      float rest[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) rest[e] = v[e] * up;
-      const int q = i % 4 * 4 + i / 4 % 4;  // the word of the code block that holds these columns
-#pragma unroll
-      for (int u = 0; u < TN; ++u) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 two = __floats2half2_rn(rest[e], rest[e + 4]);
-          const float2 r = __half22float2(two);
-          h[e] = *reinterpret_cast<const uint32_t*>(&two);
-          rest[e] -= r.x;
-          rest[e + 4] -= r.y;
-        }
-        const int col = row * TN + u, at = col % p.width;
-        p.b[((static_cast<size_t>(i / 16) * p.tiles + col / p.width) * 2 + q / 8) * p.width * 8 + at * 8 +
-            ((q % 8) ^ (at & 7))] = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      return;
-    }
+    if (i >= items) return;
     const Staged<T> st(v, up);
-    if (i < items)
 #pragma unroll
-      for (int u = 0; u < TN; ++u) {
-        const int col = row * TN + u, part = i / 4;
-        p.b[(static_cast<size_t>(part) * p.tiles + col / 8) * 32 + col % 8 * 4 + i % 4] = st.b[u];
-        if (i % 4 == 0) p.inits[static_cast<size_t>(part) * p.tiles * 8 + col] = st.init[u];
+    for (int u = 0; u < TN; ++u) {
+      const int col = row * TN + u;
+      if constexpr (kTc) {
+        const int q = i % 4 * 4 + i / 4 % 4, at = col % p.width;  // q: the word of the code block that holds these columns
+        p.b[((static_cast<size_t>(i / 16) * p.tiles + col / p.width) * 2 + q / 8) * p.width * 8 + at * 8 +
+            ((q % 8) ^ (at & 7))] = st.b[u];
+      } else {
+        p.b[(static_cast<size_t>(i / 4) * p.tiles + col / 8) * 32 + col % 8 * 4 + i % 4] = st.b[u];
       }
+    }
   };
 #pragma unroll
   for (int u = 0; u < kHeld; ++u)
@@ -544,29 +525,16 @@ __device__ __forceinline__ float ld_cluster1(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// The eight codes of a word as fp16 scale * (code - 8), in the order 0 4 1 5 2 6 3 7.  0x6400 | code is 1024 + code in
-// fp16 and 0x6400 | code << 4 is 1024 + 16 code: code - 8 comes out of one exact subtraction or FMA.
-__device__ __forceinline__ void expand(uint32_t w, __half2 s, uint32_t* v) {
-  const uint32_t m = 0x64006400u, w8 = w >> 8;
-  const __half2 z = __float2half2_rn(1032.f), z16 = __float2half2_rn(-72.f), sixteenth = __float2half2_rn(0.0625f);
-  auto h2 = [](uint32_t u) { return *reinterpret_cast<__half2*>(&u); };
-  auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t*>(&h); };
-  v[0] = bits(__hmul2(s, __hsub2(h2((w & 0x000f000fu) | m), z)));
-  v[1] = bits(__hmul2(s, __hfma2(h2((w & 0x00f000f0u) | m), sixteenth, z16)));
-  v[2] = bits(__hmul2(s, __hsub2(h2((w8 & 0x000f000fu) | m), z)));
-  v[3] = bits(__hmul2(s, __hfma2(h2((w8 & 0x00f000f0u) | m), sixteenth, z16)));
-}
-
 // A block takes 64 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
 // their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
 // activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.  16 bf16 rows,
-// 19456 x 2560: 14.5 us; 17 rows, 2560 x 2560: 8.4.  At 32 columns a step of 128 takes 0.9 us, bound by mma.sync.
+// 19456 x 2560, weights not in L2: 16.2 us; 17 rows, 2560 x 2560: 8.2.  At 32 columns a step of 128 takes 0.9 us, bound by mma.sync.
 constexpr int kManyWarps = 4, kManyRows = 16 * kManyWarps;
 constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
 template <int NT>
 constexpr int kManyAhead = NT == 1 ? 8 : 4;
 template <int NT>
-constexpr int kStepBytes = 4 * NT * (512 + 32);
+constexpr int kStepBytes = 4 * NT * 512;
 
 template <typename T, int NT, int G>
 __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(const MatmulArgs a, const Planes p) {
@@ -587,8 +555,6 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
 #pragma unroll
     for (int i = threadIdx.x; i < 4 * NT * 32; i += 32 * kManyWarps)
       cp_async16(dst + i * 16, p.b + part * NT * 32 + i);
-    if (threadIdx.x < 8 * NT)
-      cp_async16(dst + 4 * NT * 512 + threadIdx.x * 16, p.inits + part * NT * 8 + threadIdx.x * 4);
   };
   // codes do not depend on the kernel in front, which runs after all that came before it
 #pragma unroll
@@ -609,8 +575,7 @@ __global__ void __launch_bounds__(32 * kManyWarps, 16 / kManyWarps) k_q4_many(co
     cp_async_commit();
     const uint8_t* xq = xring + j % kAhead * kStepBytes<NT>;
     multiply<NT, G>(smem_u32(codes.ring + j % kAhead * kRing), codes.par0 + j, codes.par1 + j,
-                    reinterpret_cast<const uint4*>(xq) + lane, NT * 32,
-                    reinterpret_cast<const float2*>(xq + 4 * NT * 512) + c, z);
+                    reinterpret_cast<const uint4*>(xq) + lane, NT * 32, z);
   }
   cp_async_wait_all();
   __syncthreads();
@@ -876,7 +841,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
           const uint4 x = w[half * 2 + c];
           const uint32_t word[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) expand(word[i], s[i], r + c * 16 + i * 4);
+          for (int i = 0; i < 4; ++i) {
+            __half2 v[4];
+            expand(word[i], v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[c * 16 + i * 4 + e] = h2_bits(__hmul2(s[i], v[e]));
+          }
         }
         tmem_st32(tlane + j % M::kA * 64 + half * 32, r);
       }

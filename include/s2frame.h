@@ -354,8 +354,8 @@ int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group
 
 /* y[i][r] = Σ_k x[i][k] · scale[r][k / group] · (code[r][k] - 8) for n activation rows and m weight
  * rows quantised as above.  Activations keep their precision: bf16 and fp16 rows enter the products
- * as they are and fp32 rows with 22 bits, but for elements 2^-24 below their row's largest (of an
- * fp32 row 2^-13), which are taken to 2^-34 of it.  A row with an element that is not finite gives
+ * as they are and fp32 rows with 22 bits, but for elements 2^-27 below their row's largest (of an
+ * fp32 row 2^-16), which are taken to 2^-38 of it.  A row with an element that is not finite gives
  * results that are not.  With more than 16 of them (fp32: 8) a row's scales below 2^-28 of its
  * largest may lose bits.  A wait on the device that gives up (after a second or so) leaves NaN.
  *   x         device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times

@@ -219,3 +219,20 @@ def test_matmul_of_large_matrices(dtype, n, m, k, group):
     """17 to 32 columns (an fp32 row is two) of matrices on both sides of 12 Mi weights."""
     test_matmul(dtype, n, m, k, group)
     test_matmul(dtype, n, (12 << 20) // k - 1, k, group)
+
+
+@pytest.mark.parametrize("n,m,k,group", [(1, 3000, 128, 32), (1, 5000, 1536, 32), (3, 2000, 1536, 32), (13, 700, 1536, 32),
+                                         (1, 2000, 64, 64), (2, 2000, 2560, 32), (14, 1000, 160, 32)])
+def test_matmul_keeps_fp32(n, m, k, group):
+    """The error of fp32 products of few rows, 2-norm over 2-norm.  A tensor core cuts a sum off at its last bit, half of
+    it on average: a group of 32 (64) columns is 2 (4) such additions of 2^-24 of a partial sum.  Splitting an
+    activation into two fp16 terms leaves 2^-23 / sqrt(3) of it.  At most 2560 / 32 / 2 group sums are added one by
+    one, each rounding 2^-25 and independent.  4 * 2^-24 + 0.7e-7 + sqrt(40) * 2^-25 = 5e-7; 6e-7 asked."""
+    import dual_ar_tts_gb300 as pkg
+    for seed in range(4):
+        codes, scales = pkg.quantize_q4(_weights(m, k, torch.float32, seed).cuda(), group)
+        w = fb.q4_values(codes, scales, k, group)
+        x = torch.randn((n, k), generator=torch.Generator().manual_seed(100 + seed))
+        want = x.double() @ w.t()
+        off = (pkg.q4_matmul(x.cuda(), codes, scales, group).cpu().double() - want).norm(dim=1) / want.norm(dim=1)
+        assert off.max() <= 6e-7, (seed, off.max())
