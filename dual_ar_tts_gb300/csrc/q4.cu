@@ -656,6 +656,9 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
 // activations, one bulk copy a code block.  scale * (code - 8) has 8 + 3 significant bits, so it is exact in fp16: each row's scales are
 // taken times the power of two that brings the largest of those used here to 2^11 .. 2^12 (scales 2^-28 of it and
 // less lose bits).  The blocks of a cluster split W's columns and add their sums in rank order.
+// The tensor core cuts every product's sum off at its last bit: a few 1e-8 each, in one direction.  16-bit results do not
+// show it (6e-6 over 9728 columns).  Of fp32 rows the sums of two code blocks at a time (chunks) are added up in
+// registers: 3e-7 at any k where they were up to 6e-6 off; 1024 rows of 19456 x 2560 take 201 us, 187 without.
 // 19456 x 2560, 2048 bf16 rows: 207 us, 990 TFLOP/s; 512 rows 53 us; bound by the activations that every block reads
 // again from L2 (9 TB/s).  2560 x 9728, 32 rows: 14.2 us, 4 of them until the planes are there and scales looked
 // through, 4 for the join.
@@ -675,14 +678,15 @@ template <typename T, int N, int G>
 __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, const Planes p) {
   using M = Tc<N>;
   constexpr int TN = kTerms<T>, SB = kBlock / G;
+  constexpr bool kChunks = TN == 2;
   extern __shared__ __align__(16) uint8_t smraw[];
   __shared__ int ex[N / TN], ew[128];  // powers of two of the activations' and the weights' rows
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
   uint64_t* arrived = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [j % kB]: activations of code block j
   uint64_t* freed = arrived + M::kB;                               // [j % kB]: used up
   uint64_t *expanded = freed + M::kB, *used = expanded + M::kA;    // [j % kA]: its weights; used up
-  uint64_t* done = used + M::kA;                                   // all of them
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t *done = used + M::kA, *taken = done + 1;                // a chunk's products (or all); its sums read
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(taken + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int blocks = (a.k + kBlock - 1) / kBlock;
   const int ranks = gridDim.y, rank = blockIdx.y;
@@ -695,6 +699,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
       mbar_init(used + i, 1);
     }
     mbar_init(done, 1);
+    mbar_init(taken, 8);
     fence_barrier_init();
   }
   if (warp == 8) {
@@ -707,12 +712,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
 
   bool ok = true;
-  const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0);
+  const int n0 = blockIdx.z * (N / TN), nn = min(N / TN, a.n - n0), wg = warp / 4;
+  const uint32_t tsum = tm + (static_cast<uint32_t>(warp % 4 * 32) << 16) + wg * 16;
+  float acc[kChunks ? N / 4 : 1] = {};  // of this thread's row, half of the columns
   if (warp == 8) {
     // ---------------------------------------------------------------- issuing the products
     if (elect_one()) {
       for (int j = 0; j < count && ok; ++j) {
-        ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1) && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1);
+        ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1) && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1) &&
+             (!kChunks || j < 2 || j % 2 || mbar_wait_short(taken, (j / 2 - 1) & 1));
         if (!ok) {  // what is under way still ends
           if (j > 0) mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
           break;
@@ -722,10 +730,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
         const uint64_t b = desc_sw128(smem_u32(sm + j % M::kB * M::kBBytes));
 #pragma unroll
         for (int k = 0; k < kBlock / 16; ++k)
-          tc_mma_tmem_a(tm, ta + k * 8, b + ((k / 4 * (N * 128) + k % 4 * 32) >> 4), idesc_f16(128, N), j > 0 || k > 0);
+          tc_mma_tmem_a(tm, ta + k * 8, b + ((k / 4 * (N * 128) + k % 4 * 32) >> 4), idesc_f16(128, N),
+                        (kChunks ? j % 2 : j) > 0 || k > 0);
         tc_commit(freed + j % M::kB);
         tc_commit(used + j % M::kA);
-        if (j == count - 1) tc_commit(done);
+        if (j == count - 1 || (kChunks && j % 2)) tc_commit(done);
       }
     }
     __syncwarp();
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
   } else {
     // ---------------------------------------------------------------- expanding
-    const int wg = warp / 4, mine = (count - wg + 1) / 2;  // the code blocks 2 t + wg
+    const int mine = (count - wg + 1) / 2;  // the code blocks 2 t + wg
     uint8_t* ring = sm + M::kCodes + warp * M::kAhead * M::kRow;
     const int in = warp % 4 * 32, row0 = blockIdx.x * 128 + in;
     const uint8_t* from[4];
@@ -805,6 +814,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     named_bar(1, 256);
     const float up = pow2(ew[in + lane]);
     const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+    // a chunk's sums, which make room for the next chunk's
+    auto take = [&](int chunk) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_short(done, chunk & 1));
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i) {
+        float v[16];
+        tmem_ld16(tsum + i * 32, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i * 8 + e] += v[2 * e] + v[2 * e + 1];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(taken);
+    };
     for (int t = 0; t < mine; ++t) {
       const int j = 2 * t + wg;
       issue(t + M::kAhead - 1);
@@ -853,61 +878,73 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(expanded + j % M::kA);
+      if constexpr (kChunks) {
+        if (t > 0) take(t - 1);
+        if (!ok) break;
+      }
     }
     cp_async_wait_all();
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(done, 0));
-    tc_fence_after();
+    if constexpr (kChunks) {
+      for (int i = max(mine - 1, 0); i < (count + 1) / 2 && ok; ++i) take(i);
+    } else {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(done, 0));
+      tc_fence_after();
+    }
   }
   // two threads a row, each half of the columns; a wait that gave up leaves no numbers
-  const int r = threadIdx.x % 128, row = blockIdx.x * 128 + r, wg = warp / 4;
-  const uint32_t tsum = tm + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+  const int r = threadIdx.x % 128, row = blockIdx.x * 128 + r;
   T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
+  constexpr int kAt = 16 / TN;  // columns of x that 16 columns of sums are
+  auto sums = [&](auto use) {   // use(first column, kAt sums)
+    if constexpr (kChunks) {
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i)
+        if (wg * kAt + i * 2 * kAt < nn) use(wg * kAt + i * 2 * kAt, acc + i * kAt);
+    } else {
+#pragma unroll 1
+      for (int c = wg * 16; c < nn; c += 32) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tsum + c - wg * 16, v);
+        use(c, v);
+      }
+    }
+  };
   __syncthreads();
   if (ranks == 1) {
     if (warp < 8)
-#pragma unroll 1
-      for (int c = wg * 16; c < nn * TN; c += 32) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(tsum + c, v);
-        if (row < a.m)
+      sums([&](int c, const float* v) {
+        if (row >= a.m) return;
 #pragma unroll
-          for (int i = 0; i < 16 / TN; ++i) {
-            const int col = c / TN + i;
-            if (col < nn)
-              y[static_cast<size_t>(col) * a.m] =
-                  from_f<T>(ok ? by_pow2(TN == 2 ? v[2 * i] + v[2 * i + 1] : v[i], -ew[r] - ex[col]) : NAN);
-          }
-      }
+        for (int i = 0; i < kAt; ++i)
+          if (c + i < nn)
+            y[static_cast<size_t>(c + i) * a.m] = from_f<T>(ok ? by_pow2(v[i], -ew[r] - ex[c + i]) : NAN);
+      });
   } else {
     // sums as [column][row] where the operands were, behind them the weights' powers of two
     float* out = reinterpret_cast<float*>(sm);
+    constexpr int kEnd = N / TN * 128;
     if (warp < 8) {
-#pragma unroll 1
-      for (int c = wg * 16; c < nn * TN; c += 32) {
-        float v[16];
-        tmem_ld16(tsum + c, v);
+      sums([&](int c, const float* v) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) out[(c + i) * 128 + r] = ok ? v[i] : NAN;
-      }
-      if (wg == 0) out[N * 128 + r] = __int_as_float(ew[r]);
+        for (int i = 0; i < kAt; ++i) out[(c + i) * 128 + r] = ok ? v[i] : NAN;
+      });
+      if (wg == 0) out[kEnd + r] = __int_as_float(ew[r]);
     }
     cluster_sync();
     if (warp < 8) {
       int e[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (q < ranks) e[q] = __float_as_int(ld_cluster1(smem_u32(out + N * 128 + r), q));
+        if (q < ranks) e[q] = __float_as_int(ld_cluster1(smem_u32(out + kEnd + r), q));
       for (int col = wg * ranks + rank; col < nn; col += 2 * ranks) {
-        float v[8][TN], sum = 0.f;
+        float v[8], sum = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-#pragma unroll
-          for (int t = 0; t < TN; ++t)
-            if (q < ranks) v[q][t] = ld_cluster1(smem_u32(out + (col * TN + t) * 128 + r), q);
+          if (q < ranks) v[q] = ld_cluster1(smem_u32(out + col * 128 + r), q);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (q < ranks) sum += by_pow2(TN == 2 ? v[q][0] + v[q][TN - 1] : v[q][0], -e[q] - ex[col]);
+          if (q < ranks) sum += by_pow2(v[q], -e[q] - ex[col]);
         if (row < a.m) y[static_cast<size_t>(col) * a.m] = from_f<T>(sum);
       }
     }

@@ -236,3 +236,20 @@ def test_matmul_keeps_fp32(n, m, k, group):
         want = x.double() @ w.t()
         off = (pkg.q4_matmul(x.cuda(), codes, scales, group).cpu().double() - want).norm(dim=1) / want.norm(dim=1)
         assert off.max() <= 6e-7, (seed, off.max())
+
+
+@pytest.mark.parametrize("n,m,k,group", [(9, 2560, 9728, 128), (40, 1300, 9728, 32), (200, 640, 9728, 32), (150, 500, 2560, 64),
+                                         (17, 300, 384, 32), (70, 257, 128, 128)])
+def test_matmul_of_many_rows_keeps_fp32(n, m, k, group):
+    """As above for more rows.  Sums of two code blocks are 16 additions on the tensor core, each of which cuts off half of
+    the last bit (2^-24 to 2^-23 of a partial sum, 0.72 * 2^-23 on average; the partial sums' sizes average 0.7 of
+    the whole): 16 * 0.5 * 0.72 * 0.7 * 2^-23 = 4.8e-7, in one direction.  These are added one by one, 38 of them at
+    most, and over up to eight blocks: sqrt(38 + 8) * 2^-25 = 2e-7, independent; 0.7e-7 for the split: 7.5e-7 in all, 8e-7 asked."""
+    import dual_ar_tts_gb300 as pkg
+    for seed in range(2):
+        codes, scales = pkg.quantize_q4(_weights(m, k, torch.float32, seed).cuda(), group)
+        w = fb.q4_values(codes, scales, k, group)
+        x = torch.randn((n, k), generator=torch.Generator().manual_seed(100 + seed))
+        want = x.double() @ w.t()
+        off = (pkg.q4_matmul(x.cuda(), codes, scales, group).cpu().double() - want).norm(dim=1) / want.norm(dim=1)
+        assert off.max() <= 8e-7, (seed, off.max())
