@@ -46,14 +46,6 @@ struct AttnArgs {
   float2* part_ml;   // [row][head][split]
 };
 
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -228,8 +220,9 @@ __device__ __forceinline__ bool odd_values(uint32_t st, int step, int lane) {
 // O^T += V^T P^T of one step.  Lane (g, c) expands elements g * hd/8 .. + hd/8 - 1 of rows 2c, 2c + 1, 2c + 8,
 // 2c + 9; element 2i of those is row g, element 2i + 1 row g + 8 of the i-th tile.  Where not kPlain, the
 // parameters of rows from `valid` on (behind the sequence: their weights are zero, but what is there may be no
-// number) and those that are no numbers count as zero.
-template <int HD, bool kPlain>
+// number) and those that are no numbers count as zero.  kApart: the step's products start at zero and are added to O
+// outside the tensor core, which cuts a sum off at its last bit at every addition (as k_kv4_tc's).
+template <int HD, bool kPlain, bool kApart>
 __device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[2],
                                        float (&o)[HD / 16][4]) {
   using B = Kv4Block<HD>;
@@ -258,8 +251,18 @@ __device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int 
       const uint32_t sel = h ? 0x7632 : 0x5410;
       expand(__byte_perm(w[0][j], w[1][j], sel), lo, x);
       expand(__byte_perm(w[2][j], w[3][j], sel), hi, y);
-      mma_f16_16816(o[4 * j + 2 * h], x[0], x[1], y[0], y[1], p[0], p[1]);
-      mma_f16_16816(o[4 * j + 2 * h + 1], x[2], x[3], y[2], y[3], p[0], p[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float(&to)[4] = o[4 * j + 2 * h + i];
+        if constexpr (kApart) {
+          float d[4];
+          mma_f16_16816_first(d, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0], p[1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[k] += d[k];
+        } else {
+          mma_f16_16816(to, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0], p[1]);
+        }
+      }
     }
 }
 
@@ -516,9 +519,9 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
         st.softmax(s, t0, g, cut, pf);
         const bool odd = cut && odd_values<HD>(at, step, lane);
         if (!odd && valid == kStep) {
-          values<HD, true>(at, step, g, c, valid, pf, st.o);
+          values<HD, true, kTwo>(at, step, g, c, valid, pf, st.o);
         } else {
-          values<HD, false>(at, step, g, c, valid, pf, st.o);
+          values<HD, false, kTwo>(at, step, g, c, valid, pf, st.o);
           if (odd) st.poison(at, step, t0, valid, g);
         }
       }
@@ -583,7 +586,10 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // thread 64 key codes and 32 values of two positions; its codes wait in registers while the page before is used),
 // and a ninth issues the products, so that expanding, exponentials and products overlap.  The two blocks of an SM
 // share its tensor memory.  fp32 queries are two fp16 terms, and so are their weights: the products run twice,
-// into the same sums.
+// into the same sums, the small terms first.  The tensor core cuts every sum off at its last bit, a few 1e-8 each, in
+// one direction; so with fp32 queries a page's output starts at zero, and the threads of its rows add it to the one so
+// far, which has tensor memory of its own (pieces of prompts over up to 3000 positions: 2.7e-6 off 64 bits
+// without, 2.7e-7 with, 83 us and 84 at head size 128, 56 and 61 at 64).
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
 // queries alike.
 // 512 bf16 rows over 30000 positions: 370 us, 680 TFLOP/s; five pieces of prompts (874 rows over up to 42 pages): 52 us,
@@ -595,9 +601,11 @@ struct Tc {
   static constexpr int kQAtom = kTcCols * 128, kKAtom = kPage * 128;
   static constexpr int kQ = 0, kK = kQ + TN * kAtoms * kQAtom, kV = kK + kAtoms * kKAtom, kVBuf = HD * 128,
                        kOdd = kV + 3 * kVBuf, kBars = kOdd + 4 * 4 * kPage, kBytes = kBars + 128 + 1024;
-  // tensor memory columns: the output, and two pages' scores, whose place their weights take
-  static constexpr uint32_t kO = 0, kS = HD, kCols = 256;
-  static_assert(kS + 2 * kPage <= kCols && TN * 32 <= kPage, "tensor memory");
+  // tensor memory columns: the output, two pages' scores, whose place their weights take, and (fp32 queries) the
+  // output of the pages before the last one
+  static constexpr uint32_t kO = 0, kS = HD, kBefore = kS + 2 * kPage, kUsed = kBefore + (TN == 2 ? HD : 0),
+                            kCols = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= kCols && TN * 32 <= kPage, "tensor memory");
 };
 
 // Warp-wide: 32 consecutive tensor memory columns of this thread's lane.
@@ -711,10 +719,12 @@ struct PageCodes {
   }
 };
 
-constexpr int kTcThreads = 2 * kTcCols + 32;  // 96 registers each: two blocks an SM
+// 96 registers a thread: two blocks an SM.  fp32 queries at head size 128 have tensor memory and shared memory for one.
+constexpr int kTcThreads = 2 * kTcCols + 32;
 template <typename T, int HD>
-__global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
+__global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(const AttnArgs a) {
   constexpr int TN = sizeof(T) == 4 ? 2 : 1;
+  constexpr bool kApart = TN == 2;
   using B = Kv4Block<HD>;
   using M = Tc<HD, TN>;
   extern __shared__ __align__(16) uint8_t smraw[];
@@ -786,12 +796,12 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
           tc_fence_after();
           const uint32_t ts = tm + M::kS + (n & 1) * kPage;
 #pragma unroll
-          for (int t = 0; t < TN; ++t)
+          for (int t = TN - 1; t >= 0; --t)
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
               tc_mma(ts, desc_sw128(smem_u32(sm + M::kQ) + (t * M::kAtoms + k / 4) * M::kQAtom + k % 4 * 32),
                      desc_sw128(smem_u32(sm + M::kK) + k / 4 * M::kKAtom + k % 4 * 32), idesc_f16(kTcCols, kPage),
-                     t > 0 || k > 0);
+                     t < TN - 1 || k > 0);
           tc_commit(scored + (n & 1));
         } else {
           mbar_arrive(scored + (n & 1));
@@ -803,11 +813,11 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
           tc_fence_after();
           const uint32_t tp = tm + M::kS + (o & 1) * kPage;
 #pragma unroll
-          for (int t = 0; t < TN; ++t)
+          for (int t = TN - 1; t >= 0; --t)
 #pragma unroll
             for (int k = 0; k < kPage / 16; ++k)
               tc_mma_tmem_a(tm + M::kO, tp + t * 32 + k * 8, desc_sw128(smem_u32(sm + M::kV) + o % 3 * M::kVBuf + k * 32),
-                            idesc_f16(kTcCols, HD), o > 0 || t > 0 || k > 0);
+                            idesc_f16(kTcCols, HD), (!kApart && o > 0) || t < TN - 1 || k > 0);
           tc_commit(summed + (o & 1));
         }
         if (end) break;
@@ -943,28 +953,39 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
       for (int i = 4; i < kPage; ++i) tops[i % 4] = fmaxf(tops[i % 4], s[i]);
       const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * factor;
       const bool rise = top + lift > kWeightShift + kSlack;
+      float keep = 1.f;
+      // the output so far times `keep`; where it is apart, with the last page's
+      auto carry = [&] {
+        ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 16) {
+          float o[16];
+          uint32_t r[16];
+          tmem_ld16(tlane + M::kO + c, o);
+          if (kApart && n > 1) {
+            float before[16];
+            tmem_ld16(tlane + M::kBefore + c, before);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] += before[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * keep);
+          tmem_st16(tlane + (kApart ? M::kBefore : M::kO) + c, r);
+        }
+      };
       if (__any_sync(0xffffffffu, rise)) {
         const float m = lift == 3e38f ? -INFINITY : kWeightShift - lift, mn = fmaxf(m, top);
-        float keep = 1.f;
         if (rise) {
           keep = ex2(m - mn);
           lift = kWeightShift - mn;
           l *= keep;
         }
         __syncwarp();
-        if (n > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
+        if (!kApart && n > 0) {
+          carry();
           if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 16) {
-            float o[16];
-            uint32_t r[16];
-            tmem_ld16(tlane + M::kO + c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(o[i] * keep);
-            tmem_st16(tlane + M::kO + c, r);
-          }
         }
       }
       float sum[4] = {};
@@ -986,6 +1007,10 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
         }
         tmem_st32(tscore + 32, w);
       }
+      if (kApart && n > 0) {
+        carry();
+        if (!ok) break;
+      }
       tc_fence_before();
       mbar_arrive(weighed + (n & 1));
     }
@@ -998,6 +1023,12 @@ __global__ void __maxnreg__(96) k_kv4_tc(const AttnArgs a) {
       float o[16] = {};
       __syncwarp();
       if (n > 0) tmem_ld16(tlane + M::kO + c, o);
+      if (kApart && n > 1) {
+        float before[16];
+        tmem_ld16(tlane + M::kBefore + c, before);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] += before[i];
+      }
       if (poison >> (c / 32) & 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = NAN;

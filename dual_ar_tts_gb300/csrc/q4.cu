@@ -122,22 +122,6 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// d = A b, and d += A b
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_more(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 template <int kSize>
 __device__ __forceinline__ void cp_async_small(void* smem, const void* gmem, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(kSize), "r"(bytes)
@@ -278,10 +262,10 @@ __device__ __forceinline__ void multiply(uint32_t at, uint32_t par0, uint32_t pa
     for (int t = 0; t < NT; ++t) {
       const uint4 x = xq[part * part_stride + t * 32];
       if (first)
-        mma_first(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
+        mma_f16_16816_first(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
       else
-        mma_more(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
-      mma_more(d[t], h2_bits(p[2]), h2_bits(q[2]), h2_bits(p[3]), h2_bits(q[3]), x.z, x.w);
+        mma_f16_16816(d[t], h2_bits(p[0]), h2_bits(q[0]), h2_bits(p[1]), h2_bits(q[1]), x.x, x.y);
+      mma_f16_16816(d[t], h2_bits(p[2]), h2_bits(q[2]), h2_bits(p[3]), h2_bits(q[3]), x.z, x.w);
       if (last) {
         z[t][0] += s0[part] * d[t][0];
         z[t][1] += s0[part] * d[t][1];

@@ -357,7 +357,9 @@ int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group
  * as they are and fp32 rows with 22 bits, but for elements 2^-27 below their row's largest (of an
  * fp32 row 2^-16), which are taken to 2^-38 of it.  A row with an element that is not finite gives
  * results that are not.  With more than 16 of them (fp32: 8) a row's scales below 2^-28 of its
- * largest may lose bits.  fp32 results are within 1e-6 of 64-bit ones (2-norm over 2-norm), whatever k.  A wait on the device that gives up (after a second or so) leaves NaN.
+ * largest may lose bits.  Sums are fp32; the tensor cores add up no more than 256 columns of an fp32
+ * row (they cut off at a sum's last bit).  A wait on the device that gives up (after a second or so)
+ * leaves NaN.
  *   x         device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times
  *             the element size a multiple of 16
  *   codes, scales  as s2_quantize_q4 writes them, both 16-byte aligned; k a multiple of group

@@ -468,3 +468,30 @@ def test_attention_of_many_rows_beside_products_on_other_streams(dtype, hd):
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(w, y) for y in g)
+
+
+@pytest.mark.parametrize("hd,hq,hkv", [(64, 4, 1), (128, 8, 2)])
+@pytest.mark.parametrize("spans,hint", [([(1, 20000)], 64), ([(1, 3000), (2, 700)], 0), ([(200, 3000), (60, 60)], 0),
+                                        ([(40, 20000)], 64), ([(130, 1000)], 0)])
+def test_attention_keeps_fp32(spans, hint, hd, hq, hkv):
+    """The error of fp32 attention, 2-norm over 2-norm of a sequence, for queries and keys of unit size.  A score: the split
+    of the query leaves 2^-23 / sqrt(3) of its terms (1e-7 of their size), hd / 16 = 8 additions on the tensor core cut
+    off half of the last bit each, 0.72 * 2^-23 on average, of sums 0.7 as large: 2.4e-7 of the score, whose size is
+    about 1.5: 3.6e-7 of a weight.  ex2 and its argument: 2^-22.  Output: a page's (a step's) 4 additions: 1.2e-7; its sums,
+    added one by one: 2^-25 sqrt(470) / 2 = 3e-7 at 20000 positions (of a size that grows as its root).  Independent but for
+    the two cuts: sqrt(1^2 + 2.4^2 + 3^2) + 3.6 + 1.2 = 8.8e-7; 1e-6 asked."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(hd + len(spans))
+    table, q_start, lengths, pool = _layout(spans, rng)
+    pages = torch.zeros((pool, hkv, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((int(q_start[-1]), hq, hd)).astype(np.float32))
+    got = _attend(pkg, q, pages, table, q_start, lengths, max_len=hint).cpu().double()
+    for s, (n, length) in enumerate(spans):
+        ids, rows = [int(p) for p in table[s, :-(-length // 64)]], slice(int(q_start[s]), int(q_start[s + 1]))
+        want = torch.empty((n, hq, hd), dtype=torch.float64)
+        for h in range(hq):
+            k, v = [fb.get(pages[:, h // (hq // hkv)][:, None], part, ids)[0, :length] for part in range(2)]
+            want[:, h] = fb.attention(q[rows, h], k, v, range(length - n + 1, length + 1), hd ** -0.5)[0]
+        off = float((got[rows] - want).norm() / want.norm())
+        assert off <= 1e-6, off
