@@ -11,8 +11,12 @@
 //  - many (pieces of prompts): tcgen05, the cache expanded once for 128 columns (k_kv4_tc, below).
 // With fp32 queries a column is two, the high and the low fp16 part of the query, whose scores are added and whose
 // weights are again split so (a weight then carries 22 bits).  16-bit queries are exact in fp16: each row is scaled by
-// a power of two.  Weights are kept as 2^6 exp2(s - m), m the running maximum or up to 8 (log2) below it: what fp16
-// drops of them is 2^-30 and less of the largest, and a maximum that rises a little costs no rescaling of the output.
+// a power of two.  Weights are kept as 2^6 exp2(s - m), m the running maximum or up to 8 (log2) below it: what falls off
+// fp16's end is 2^-30 and less of the largest, and a maximum that rises a little costs no rescaling of the output.
+// Of 16-bit queries a weight is rounded to fp16, 2^-11 of it; the sum that divides the output is of the weights before
+// that.  bf16 results do not show it (1.7e-3 off 64 bits either way), fp16 ones are 2.4e-4 off where their own rounding
+// is 2.1e-4.  A second term was measured: it leaves 2.1e-4, and 8 x 30000 positions take 85 us instead of 80, 512
+// rows over 30000 578 us instead of 374.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -428,7 +428,9 @@ int s2_kv4_append(const s2_kv4* cache, const void* qkv, int dtype, long long qkv
 int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* stream);
 
 /* Causal attention of the rows' queries over their sequences: query head h reads KV head
- * h / (n_head / n_kv_head) at positions 0 .. its own, scores scaled by `scale`.  A row that sees no
+ * h / (n_head / n_kv_head) at positions 0 .. its own, scores scaled by `scale`.  Queries enter the
+ * products as rows of s2_q4_matmul do; scores, softmax statistics and sums are fp32; a softmax weight
+ * meets the values rounded to fp16 (2^-11 of it), with fp32 queries to 22 bits.  A row that sees no
  * position (lengths[s] short of the sequence's rows) gets zeros; what a page holds past a
  * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
  * are not attended.  A wait on the device that gives up (after a second or so) writes S2_ETIMEOUT
