@@ -24,7 +24,7 @@ EXPORTS = ("s2_weight_count", "s2_weight_info", "s2_frame_workspace_bytes", "s2_
            "s2_stop_stream", "s2_stream_progress", "s2_codec_latent", "s2_quantize_e4m3", "s2_set_barrier_base",
            "s2_draw", "s2_quantize_q4", "s2_q4_matmul_workspace", "s2_q4_matmul",
            "s2_kv4_page_bytes", "s2_kv4_append", "s2_kv4_read",
-           "s2_kv4_attention_workspace", "s2_kv4_attention", "s2_adjust_logits")
+           "s2_kv4_attention_workspace", "s2_kv4_attention", "s2_adjust_logits", "s2_set_wait_limit")
 
 S2_KV4_PAGE = 64
 
@@ -105,6 +105,7 @@ def load(path: str = LIB_PATH):
         "s2_kv4_read": (i32, [P(s2_kv4), vp, vp, vp]),
         "s2_kv4_attention_workspace": (sz, [i32, i32, i32, i32, i32, i32]),
         "s2_kv4_attention": (i32, [P(s2_kv4), vp, i32, i32, ctypes.c_float, i32, vp, vp, sz, vp]),
+        "s2_set_wait_limit": (i32, [i32]),
         "s2_adjust_logits": (i32, [i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, vp, i64, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -546,6 +547,10 @@ def s2_sync_status(ctx, stream: int = 0) -> int:
 
 def s2_set_spin_limit(ctx, limit: int):
     return _check("s2_set_spin_limit", load().s2_set_spin_limit(ctx, limit), ctx)
+
+
+def s2_set_wait_limit(tries: int):
+    return _check("s2_set_wait_limit", load().s2_set_wait_limit(tries))
 
 
 def s2_set_barrier_base(ctx, base: int):

@@ -7,8 +7,11 @@
 #include <atomic>
 
 #include "../../include/s2frame.h"
+#include "ptx.cuh"
 
 namespace s2 {
+
+inline std::atomic<int> wait_tries{kWaitTries};  // of the device waits of calls launched from here on
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }

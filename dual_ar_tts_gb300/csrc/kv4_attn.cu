@@ -48,6 +48,7 @@ struct AttnArgs {
   int n_split, split_pages;
   float* part_o;     // [row][head][split][hd]
   float2* part_ml;   // [row][head][split]
+  int tries;         // of a wait
 };
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
@@ -738,10 +739,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
   // issuer's); its weights: weighed[n % 2]; the output with it: summed[n % 2].  A barrier completes again only after
   // all that wait for it have seen it, since each of them has a part in what comes before its next completion.
   uint64_t* filled = reinterpret_cast<uint64_t*>(sm + M::kBars);
-  uint64_t *scored = filled + 2, *weighed = filled + 4, *summed = filled + 6;
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(filled + 8);
+  uint64_t *scored = filled + 2, *weighed = filled + 4, *summed = filled + 6, *drained = filled + 8;
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(filled + 9);
   int* place = reinterpret_cast<int*>(tbase + 1);                  // [n % 4]: page n in the sequence, -1 after the last
   uint8_t* odd_any = reinterpret_cast<uint8_t*>(place + 4);        // [n % 4][warp]: values that are no numbers
+  volatile int* failed = place + 8;                                // a wait gave up
   uint16_t* odd_rows = reinterpret_cast<uint16_t*>(sm + M::kOdd);  // [n % 4][warp][lane], a byte a position
   const int warp = threadIdx.x / 32;
   const int kh = blockIdx.y, split = blockIdx.z;
@@ -777,6 +779,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
       mbar_init(weighed + i, kTcCols);
       mbar_init(summed + i, 1);
     }
+    mbar_init(drained, 1);
+    *failed = 0;
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -784,8 +788,10 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
     tmem_relinquish();
   }
 
-  // A wait that gave up is not the last thing that waits: from there on nobody waits, and the call reports it.
+  // Where a wait gives up its warp goes on without waiting (all it touches is its block's own) and says so in `failed`,
+  // which the block's results go by: they are NaN then, and the call reports it.
   bool ok = true;
+  auto wait = [&](uint64_t* bar, int n) { return mbar_wait_short(bar + (n & 1), n >> 1 & 1, a.tries); };
   if (warp == 8) {
     // ---------------------------------------------------------------- issuing the products
     named_bar(2, kTcThreads);  // queries, barriers and tensor memory are there
@@ -793,10 +799,10 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
       tc_fence_after();
       const uint32_t tm = *tbase;
       for (int n = 0;; ++n) {
-        ok = ok && mbar_wait_short(filled + (n & 1), n >> 1 & 1);
+        ok = ok && wait(filled, n);
         const bool end = !ok || place[n & 3] < 0;
         if (!end) {
-          if (n > 1) ok = mbar_wait_short(summed + (n & 1), (n - 2) >> 1 & 1);  // the weights of page n - 2 lie there
+          if (n > 1) ok = wait(summed, n - 2);  // the weights of page n - 2 lie there
           tc_fence_after();
           const uint32_t ts = tm + M::kS + (n & 1) * kPage;
 #pragma unroll
@@ -813,7 +819,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
         mbar_arrive(scored + (n & 1));
         if (n > 0) {  // the output with page n - 1
           const int o = n - 1;
-          ok = ok && mbar_wait_short(weighed + (o & 1), o >> 1 & 1);
+          ok = ok && wait(weighed, o);
           tc_fence_after();
           const uint32_t tp = tm + M::kS + (o & 1) * kPage;
 #pragma unroll
@@ -826,8 +832,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
         }
         if (end) break;
       }
+      tc_commit(drained);  // no end before that of the products
+      if (!mbar_wait_short(drained, 0) || !ok) *failed = 1;
     }
     __syncwarp();
+    named_bar(3, kTcThreads);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- expanding
     const int lane = threadIdx.x % 32;
@@ -853,11 +862,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
     for (int n = 0;; ++n) {
       const bool end = next >= p1;
       // values first: there are three buffers of them, while the keys wait for the scores of the page before
-      if (n > 2) ok = ok && mbar_wait_short(summed + ((n - 3) & 1), (n - 3) >> 1 & 1);  // the values of page n - 3 are used up
+      if (n > 2) ok = ok && wait(summed, n - 3);  // the values of page n - 3 are used up
       __syncwarp();
       bool odd = false;
       if (!end) odd = held.expand_values(sm + M::kV + n % 3 * M::kVBuf, odd_rows + (n & 3) * 2 * kPage);
-      if (n > 0) ok = ok && mbar_wait_short(scored + ((n - 1) & 1), (n - 1) >> 1 & 1);  // the keys before are used up
+      if (n > 0) ok = ok && wait(scored, n - 1);  // the keys before are used up
       __syncwarp();
       if (!end) held.expand_keys(sm + M::kK);
       odd = __any_sync(0xffffffffu, odd);
@@ -872,6 +881,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
       ++next;
       fetch();
     }
+    if (!ok) *failed = 1;
+    named_bar(3, kTcThreads);
   } else {
     // ---------------------------------------------------------------- a column a thread
     const int col = tile.first + threadIdx.x;
@@ -933,7 +944,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
     uint32_t poison = 0;          // groups of the output that are no numbers
     int n = 0;
     for (;; ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(scored + (n & 1), n >> 1 & 1));
+      ok = __all_sync(0xffffffffu, wait(scored, n));
       const int p = ok ? place[n & 3] : -1;
       if (p < 0) break;
       tc_fence_after();
@@ -960,7 +971,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
       float keep = 1.f;
       // the output so far times `keep`; where it is apart, with the last page's
       auto carry = [&] {
-        ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1));
+        ok = __all_sync(0xffffffffu, wait(summed, n - 1));
         if (!ok) return;
         tc_fence_after();
 #pragma unroll 1
@@ -1018,9 +1029,14 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
       tc_fence_before();
       mbar_arrive(weighed + (n & 1));
     }
-    if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait_short(summed + ((n - 1) & 1), (n - 1) >> 1 & 1)) && ok;
+    if (!ok) *failed = 1;
+    named_bar(3, kTcThreads);  // all products have ended, and all waits
     tc_fence_after();
-    if (!ok && a.c.status && threadIdx.x % 32 == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
+    if (*failed) {
+      ok = false;
+      l = NAN;
+      if (a.c.status && threadIdx.x == 0) atomicCAS(a.c.status, 0, static_cast<int>(S2_ETIMEOUT));
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
     for (int c = 0; c < HD; c += 16) {
@@ -1053,7 +1069,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
         for (int i = 0; i < 4; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
     }
-    if (live && !whole) a.part_ml[at * a.n_split + split] = make_float2(lift == 3e38f ? -INFINITY : kWeightShift - lift, l);
+    if (live && !whole)
+      a.part_ml[at * a.n_split + split] = make_float2(lift == 3e38f || !ok ? -INFINITY : kWeightShift - lift, l);
     tc_fence_before();
   }
   __syncthreads();
@@ -1212,6 +1229,11 @@ bool bad_sizes(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, i
 
 using namespace s2;
 
+extern "C" int s2_set_wait_limit(int tries) {
+  wait_tries.store(tries < 0 ? kWaitTries : tries, std::memory_order_relaxed);
+  return S2_OK;
+}
+
 extern "C" size_t s2_kv4_attention_workspace(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim,
                                              int max_len) {
   if (bad_sizes(n_seq, n_rows, n_head, n_kv_head, head_dim, max_len)) return 0;
@@ -1232,9 +1254,10 @@ extern "C" int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, i
   if (max_len == 0 || max_len > cache->table_cols * kPage) max_len = cache->table_cols * kPage;
   const Plan p = plan(cache->n_seq, cache->n_rows, n_head, cache->n_kv_head, cache->head_dim, max_len, dtype == S2_F32);
   if (p.bytes > 0 && (!workspace || ws_bytes < p.bytes)) return S2_EINVAL;
-  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, nullptr, nullptr};
+  AttnArgs a{*cache, q, n_head, n_head / cache->n_kv_head, scale, out, p.n_split, p.split_pages, nullptr, nullptr, 0};
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
+  a.tries = wait_tries.load(std::memory_order_relaxed);
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

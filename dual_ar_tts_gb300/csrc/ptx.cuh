@@ -65,9 +65,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A wait that gives up after a second or so (a few hundred ns a try).
-__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 22); ++i)
+// A wait that gives up, by default after a second or so (a few hundred ns a try).
+constexpr int kWaitTries = 1 << 22;
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, int tries = kWaitTries) {
+  for (int i = 0; i < tries; ++i)
     if (mbar_test(bar, parity)) return true;
   return false;
 }

@@ -433,8 +433,8 @@ int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* strea
  * meets the values rounded to fp16 (2^-11 of it), with fp32 queries to 22 bits.  A row that sees no
  * position (lengths[s] short of the sequence's rows) gets zeros; what a page holds past a
  * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
- * are not attended.  A wait on the device that gives up (after a second or so) writes S2_ETIMEOUT
- * to `status`; the results are then not to be used.
+ * are not attended.  Where a wait on the device gives up (after a second or so) the results that it
+ * concerns are NaN, and S2_ETIMEOUT is written to `status`.
  *   q, out    device [n_rows][n_head][head_dim] of dtype, 16-byte aligned
  *   max_len   the largest length expected, by which the work is split (0, or more than table_cols
  *             pages hold: those); a longer sequence is still right
@@ -443,6 +443,11 @@ int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* strea
 size_t s2_kv4_attention_workspace(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len);
 int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, int n_head, float scale, int max_len, void* out,
                      void* workspace, size_t ws_bytes, struct CUstream_st* stream);
+
+/* Testing hook: tries (each of a few hundred ns) that the device waits of s2_q4_matmul and
+ * s2_kv4_attention make in calls launched from here on, in this process; 0: each gives up at once.
+ * Negative: the default, 2^22.  A captured call keeps the limit that it was captured with. */
+int s2_set_wait_limit(int tries);
 
 /* Logits adjusted for a draw (s2_draw takes the result).  For entry e of row r, c the number of
  * times its token is in the row's history:

@@ -495,3 +495,31 @@ def test_attention_keeps_fp32(spans, hint, hd, hq, hkv):
             want[:, h] = fb.attention(q[rows, h], k, v, range(length - n + 1, length + 1), hd ** -0.5)[0]
         off = float((got[rows] - want).norm() / want.norm())
         assert off <= 1e-6, off
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("spans", [[(70, 100), (130, 130)], [(300, 4000), (20, 64)]])
+def test_attention_of_many_rows_whose_waits_give_up(spans, hd, dtype):
+    """No tries: every wait gives up at once.  No number comes out, the status says so, and the next call is as ever."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(4)
+    table, q_start, lengths, pool = _layout(spans, rng)
+    rows = int(q_start[-1])
+    pages = torch.zeros((pool, 2, 80 * hd), dtype=torch.uint8)
+    fb.fill_random(pages, rng)
+    q = torch.from_numpy(rng.standard_normal((rows + 1, 8, hd)).astype(np.float32)).to(fb.TYPES[dtype])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((rows + 1, 8, hd), 9.0, dtype=q.dtype, device="cuda")
+    want = _attend(pkg, q, pages, table, q_start, lengths, out=out.clone(), status=status)
+    assert int(status) == 0 and torch.isfinite(want).all()
+    pkg.s2_set_wait_limit(0)
+    try:
+        got = _attend(pkg, q, pages, table, q_start, lengths, out=out, status=status)
+        torch.cuda.synchronize()
+    finally:
+        pkg.s2_set_wait_limit(-1)
+    assert int(status) == pkg.S2_ETIMEOUT
+    assert torch.isnan(got[:rows]).all() and (got[rows:] == 9).all()
+    status.zero_()
+    assert torch.equal(_attend(pkg, q, pages, table, q_start, lengths, out=out, status=status), want) and int(status) == 0
