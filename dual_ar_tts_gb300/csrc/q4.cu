@@ -136,6 +136,7 @@ struct MatmulArgs {
   const __nv_bfloat16* scales;
   void* y;
   int tiles;  // R
+  int tries;  // of a wait
 };
 
 // One 8-element item of an activation row, scaled by `up`: the B operand's 16 bytes of each term, as the pairs
@@ -670,7 +671,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
   uint64_t* freed = arrived + M::kB;                               // [j % kB]: used up
   uint64_t *expanded = freed + M::kB, *used = expanded + M::kA;    // [j % kA]: its weights; used up
   uint64_t *done = used + M::kA, *taken = done + 1;                // a chunk's products (or all); its sums read
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(taken + 1);
+  uint64_t* drained = taken + 1;                                   // nothing under way
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(drained + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int blocks = (a.k + kBlock - 1) / kBlock;
   const int ranks = gridDim.y, rank = blockIdx.y;
@@ -684,6 +686,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     }
     mbar_init(done, 1);
     mbar_init(taken, 8);
+    mbar_init(drained, 1);
     fence_barrier_init();
   }
   if (warp == 8) {
@@ -703,12 +706,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     // ---------------------------------------------------------------- issuing the products
     if (elect_one()) {
       for (int j = 0; j < count && ok; ++j) {
-        ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1) && mbar_wait_short(expanded + j % M::kA, j / M::kA & 1) &&
-             (!kChunks || j < 2 || j % 2 || mbar_wait_short(taken, (j / 2 - 1) & 1));
-        if (!ok) {  // what is under way still ends
-          if (j > 0) mbar_wait_short(used + (j - 1) % M::kA, (j - 1) / M::kA & 1);
-          break;
-        }
+        ok = mbar_wait_short(arrived + j % M::kB, j / M::kB & 1, a.tries) &&
+             mbar_wait_short(expanded + j % M::kA, j / M::kA & 1, a.tries) &&
+             (!kChunks || j < 2 || j % 2 || mbar_wait_short(taken, (j / 2 - 1) & 1, a.tries));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t ta = tm + N + j % M::kA * 64;
         const uint64_t b = desc_sw128(smem_u32(sm + j % M::kB * M::kBBytes));
@@ -720,6 +721,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
         tc_commit(used + j % M::kA);
         if (j == count - 1 || (kChunks && j % 2)) tc_commit(done);
       }
+      tc_commit(drained);  // no end before that of the products, whoever gave up
+      mbar_wait_short(drained, 0);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -729,14 +732,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
       const uint8_t* src = reinterpret_cast<const uint8_t*>(p.b) + (static_cast<size_t>(b0) * p.tiles + blockIdx.z) * M::kBBytes;
       int j = 0;
       for (; j < count; ++j) {
-        if (j >= M::kB) ok = mbar_wait_short(freed + j % M::kB, (j / M::kB - 1) & 1);
+        if (j >= M::kB) ok = mbar_wait_short(freed + j % M::kB, (j / M::kB - 1) & 1, a.tries);
         if (!ok) break;
         mbar_arrive_expect_tx(arrived + j % M::kB, M::kBBytes);
         bulk_g2s_plain(sm + j % M::kB * M::kBBytes, src + static_cast<size_t>(j) * p.tiles * M::kBBytes, M::kBBytes,
                        arrived + j % M::kB);
       }
-      if (!ok)  // what is in flight still comes
-        for (int i = j - M::kB; i < j; ++i) mbar_wait_short(arrived + i % M::kB, i / M::kB & 1);
+      for (int i = max(j - M::kB, 0); i < j; ++i)  // no end before that of the copies
+        mbar_wait_short(arrived + i % M::kB, i / M::kB & 1);
     }
     __syncwarp();
     for (int i = lane; i < nn; i += 32) ex[i] = scale_exponent(__ldcg(p.top + n0 + i));
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     const uint32_t tlane = tm + N + (static_cast<uint32_t>(warp % 4 * 32) << 16);
     // a chunk's sums, which make room for the next chunk's
     auto take = [&](int chunk) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_short(done, chunk & 1));
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_short(done, chunk & 1, a.tries));
       if (!ok) return;
       tc_fence_after();
 #pragma unroll
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
       }
       __syncwarp();  // the ring's place may be filled again
       if (j >= M::kA) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_short(used + j % M::kA, (j / M::kA - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_short(used + j % M::kA, (j / M::kA - 1) & 1, a.tries));
         if (!ok) break;
         tc_fence_after();
       }
@@ -871,7 +874,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_q4_tc(const MatmulArgs a, con
     if constexpr (kChunks) {
       for (int i = max(mine - 1, 0); i < (count + 1) / 2 && ok; ++i) take(i);
     } else {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(done, 0));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_short(done, 0, a.tries));
       tc_fence_after();
     }
   }
@@ -1020,7 +1023,8 @@ extern "C" int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride,
     return S2_EINVAL;
   const size_t need = s2_q4_matmul_workspace(n, k, dtype);
   if (need > 0 && (!workspace || ws_bytes < need)) return S2_EINVAL;
-  const MatmulArgs a{x, x_stride, n, m, k, codes, static_cast<const __nv_bfloat16*>(scales), y, 0};
+  const MatmulArgs a{x, x_stride, n, m, k, codes, static_cast<const __nv_bfloat16*>(scales), y, 0,
+                     wait_tries.load(std::memory_order_relaxed)};
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

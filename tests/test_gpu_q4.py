@@ -253,3 +253,22 @@ def test_matmul_of_many_rows_keeps_fp32(n, m, k, group):
         want = x.double() @ w.t()
         off = (pkg.q4_matmul(x.cuda(), codes, scales, group).cpu().double() - want).norm(dim=1) / want.norm(dim=1)
         assert off.max() <= 8e-7, (seed, off.max())
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 40), ("fp16", 64), ("bf16", 300), ("fp32", 17), ("fp32", 100)])
+@pytest.mark.parametrize("m,k", [(300, 2560), (300, 256), (20000, 640)])
+def test_matmul_of_many_rows_whose_waits_give_up(dtype, n, m, k):
+    """No tries: every wait gives up at once.  No number comes out, and the next call is as ever."""
+    import dual_ar_tts_gb300 as pkg
+    codes, scales = pkg.quantize_q4(_weights(m, k, torch.bfloat16, 1).cuda(), 32)
+    x = torch.randn((n, k), generator=torch.Generator().manual_seed(2)).to(fb.TYPES[dtype]).cuda()
+    want = pkg.q4_matmul(x, codes, scales, 32)
+    out = torch.full((n + 1, m), 7.0, dtype=x.dtype, device="cuda")
+    pkg.s2_set_wait_limit(0)
+    try:
+        pkg.q4_matmul(x, codes, scales, 32, out=out[:n])
+        torch.cuda.synchronize()
+    finally:
+        pkg.s2_set_wait_limit(-1)
+    assert torch.isnan(out[:n]).all() and (out[n] == 7).all()
+    assert torch.equal(pkg.q4_matmul(x, codes, scales, 32), want) and torch.isfinite(want).all()
