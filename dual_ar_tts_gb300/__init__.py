@@ -286,12 +286,16 @@ _DEVICE = "tensors must be on one CUDA device, the operand fp32, bf16 or fp16"
 
 
 def _rows16(x):
-    """x [n][k], as rows that start on 16 bytes (a copy where they do not)."""
+    """x [n][k], k elements a multiple of 16 bytes, as rows that start on 16 bytes (a copy where they do not), and
+    their stride."""
+    k = x.shape[1]
     s0, s1 = x.stride()
-    if s1 == 1 and s0 >= x.shape[1] and s0 * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
-        return x
+    if x.shape[0] == 1:  # one row: its stride may be anything, for torch too
+        s0 = k
+    if s1 == 1 and s0 >= k and s0 * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
+        return x, s0
     x = x.contiguous()
-    return x.clone() if x.data_ptr() % 16 else x
+    return x.clone() if x.data_ptr() % 16 else x, k
 
 
 def quantize_q4(w, group: int = 32):
@@ -329,7 +333,7 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
             not scales.is_contiguous():
         _bad("codes must be contiguous uint8 [rows][ceil(k/128)*64] and scales contiguous bf16 "
              "[rows][ceil(k/128)*(128/group)], k a multiple of group")
-    x = _rows16(x)
+    x, stride = _rows16(x)
     if out is None:
         out = h.empty((n, m), dtype=x.dtype, device=x.device)
     elif out.dtype is not x.dtype or out.shape != (n, m) or out.get_device() != dev or not out.is_contiguous():
@@ -340,7 +344,7 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
     else:
         nbytes = _workspace(workspace, dev)
     ws = None if workspace is None else workspace.data_ptr()
-    _launch(h, h.lib.s2_q4_matmul, dev, n, x.data_ptr(), dt, x.stride(0), codes.data_ptr(), scales.data_ptr(), m, k,
+    _launch(h, h.lib.s2_q4_matmul, dev, n, x.data_ptr(), dt, stride, codes.data_ptr(), scales.data_ptr(), m, k,
             group, out.data_ptr(), ws, nbytes)
     return out
 
@@ -414,13 +418,13 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
         if w is not None and (w.dtype is not f32 or w.shape != (hd,) or not w.is_contiguous() or
                               w.get_device() != dev):
             _bad("norm weights must be fp32 [head_dim] on qkv's device")
-    qkv = _rows16(qkv)
+    qkv, stride = _rows16(qkv)
     if q_out is None:
         q_out = h.empty((n_rows, n_head, hd), dtype=qkv.dtype, device=qkv.device)
     elif q_out.dtype is not qkv.dtype or q_out.shape != (n_rows, n_head, hd) or q_out.get_device() != dev or \
             not q_out.is_contiguous():
         _bad("q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type, on its device")
-    _launch(h, h.lib.s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, qkv.stride(0), n_head, rope.data_ptr(),
+    _launch(h, h.lib.s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, stride, n_head, rope.data_ptr(),
             rope.shape[0], None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
             eps, q_out.data_ptr())
     return q_out

@@ -523,3 +523,18 @@ def test_attention_of_many_rows_whose_waits_give_up(spans, hd, dtype):
     assert torch.isnan(got[:rows]).all() and (got[rows:] == 9).all()
     status.zero_()
     assert torch.equal(_attend(pkg, q, pages, table, q_start, lengths, out=out, status=status), want) and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_append_of_one_row_of_any_stride(dtype):
+    import dual_ar_tts_gb300 as pkg
+    hq, hkv, hd = 2, 1, 64
+    width = (hq + 2 * hkv) * hd
+    wide = torch.randn((3, width + 3), generator=torch.Generator().manual_seed(1)).to(fb.TYPES[dtype]).cuda()
+    one = _gpu(np.zeros((1, 1), np.int32), np.asarray([0, 1], np.int32), np.asarray([9], np.int32))
+    rope = pkg.rope_table(16, hd)
+    for x in (wide[1:2, :width], wide[2:, 3:], wide[:1, 1:1 + width], wide[:1, :width].t().contiguous().t()):
+        pages, want = [pkg.kv4_pages(1, hkv, hd) for _ in range(2)]
+        q = pkg.kv4_append(x, pages, *one, rope, hq)
+        same = torch.empty((1, width), dtype=x.dtype, device="cuda").copy_(x)
+        assert torch.equal(q, pkg.kv4_append(same, want, *one, rope, hq)) and torch.equal(pages, want)

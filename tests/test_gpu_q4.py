@@ -272,3 +272,14 @@ def test_matmul_of_many_rows_whose_waits_give_up(dtype, n, m, k):
         pkg.s2_set_wait_limit(-1)
     assert torch.isnan(out[:n]).all() and (out[n] == 7).all()
     assert torch.equal(pkg.q4_matmul(x, codes, scales, 32), want) and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_matmul_of_one_row_of_any_stride(dtype):
+    import dual_ar_tts_gb300 as pkg
+    k, m = 256, 75
+    codes, scales = pkg.quantize_q4(_weights(m, k, torch.float32, 3).cuda(), 32)
+    wide = torch.randn((4, 260), generator=torch.Generator().manual_seed(1)).to(fb.TYPES[dtype]).cuda()
+    column = wide[:2].flatten()[:2 * k].view(k, 2)
+    for x in (wide[:1, :k], wide[1:2, 1:1 + k], wide[3:, 4:], column[:, :1].t(), column[:, 1:].t(), column[:, :1].clone().t()):
+        _check(pkg.q4_matmul(x, codes, scales, 32), x, codes, scales, k, 32)

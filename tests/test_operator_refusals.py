@@ -119,3 +119,21 @@ def test_q4_matmul_sizes(lib):
     assert lib.s2_q4_matmul_workspace(40, (1 << 28) + 1, pkg.S2_BF16) == 0
     sizes = [lib.s2_q4_matmul_workspace(n, 2560, pkg.S2_BF16) for n in (1, 8, 9, 16, 17, 32, 33, 64, 65, 500)]
     assert sizes[0] == 0 and all(a <= b for a, b in zip(sizes[2:], sizes[3:]))
+
+
+def test_rows_of_any_stride_are_taken():
+    """What q4_matmul and kv4_append do with their rows: a start and a stride that the library takes, the values as
+    they were.  torch lets a single row have any stride."""
+    torch = pytest.importorskip("torch")
+    import dual_ar_tts_gb300 as pkg
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        wide, k = torch.randn((4, 260)).to(dt), 256
+        rows = [wide[:, :k], wide[0:1, :k], wide[1:2, 1:1 + k], wide[:1, 2:2 + k], wide[3:, 4:], wide[::2, :k],
+                torch.randn((k, 1)).to(dt).t(), torch.randn((k, 3)).to(dt).t(), torch.randn((k, 3)).to(dt).t()[1:2],
+                wide[:1, :k].expand(3, k), torch.randn(k).to(dt).as_strided((1, k), (0, 1)),
+                torch.randn(2 * k).to(dt)[::2][None], torch.randn(k + 1).to(dt)[1:][None]]
+        for x in rows:
+            y, stride = pkg._rows16(x)
+            assert y.shape == x.shape and torch.equal(y, x)
+            assert y.data_ptr() % 16 == 0 and stride >= k and stride * y.element_size() % 16 == 0
+            assert y.stride(1) == 1 and (y.shape[0] == 1 or y.stride(0) == stride)
