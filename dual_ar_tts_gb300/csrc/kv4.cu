@@ -42,7 +42,34 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8]) {
     hi = h;
     lo = lo + ol + l;
   }
-  return hi + lo;
+  return isfinite(hi) ? hi + lo : hi;  // where hi is infinite, lo is none
+}
+
+// The same to a few fp32 roundings, for queries.
+template <int HD>
+__device__ __forceinline__ float sum_squares_fp32(const float (&x)[8]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum = __fmaf_rn(x[i], x[i], sum);
+#pragma unroll
+  for (int o = HD / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Mean square of a head, for the whole warp.  Where the sum is past fp32's range the mean may not be: it is then taken of
+// x / 2^64 (of which what underflows does not count).
+template <int HD, bool kKey>
+__device__ __forceinline__ float mean_square(const float (&x)[8]) {
+  auto mean = [](const float(&v)[8]) { return (kKey ? sum_squares<HD>(v) : sum_squares_fp32<HD>(v)) * (1.f / HD); };
+  float m = mean(x);
+  if (__any_sync(0xffffffffu, isinf(m))) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * 0x1p-64f;
+    const float small = mean(y);
+    if (isinf(m)) m = small * 0x1p64f * 0x1p64f;
+  }
+  return m;
 }
 
 struct AppendArgs {
@@ -140,17 +167,14 @@ __device__ __forceinline__ void append_item(const AppendArgs& a, int row, const 
   using B = Kv4Block<HD>;
   const bool is_q = h < a.n_head, is_v = h >= a.n_head + a.c.n_kv_head, is_k = !is_q && !is_v;
   const float* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
-  float sum = 0.f;
-  if (a.k_norm && __any_sync(0xffffffffu, is_k)) {
-    sum = sum_squares<HD>(x);
-  } else if (a.q_norm && __any_sync(0xffffffffu, is_q)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
-#pragma unroll
-    for (int o = HD / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float mean = 0.f;
+  if (a.k_norm && __any_sync(0xffffffffu, is_k)) mean = mean_square<HD, true>(x);
+  if (a.q_norm && __any_sync(0xffffffffu, is_q)) {
+    const float m = mean_square<HD, false>(x);
+    if (is_q) mean = m;  // whatever heads share the warp
   }
   if (w) {
-    const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum * (1.f / HD), a.eps)));
+    const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(mean, a.eps)));
     const float4 w0 = __ldg(reinterpret_cast<const float4*>(w) + sub * 2), w1 = __ldg(reinterpret_cast<const float4*>(w) + sub * 2 + 1);
     const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll

@@ -409,7 +409,8 @@ long long s2_kv4_page_bytes(int n_kv_head, int head_dim);
  *          scale = fp16(max((hi - lo) / 15, max|x| / 127)), zero = clamp(rint(-lo / scale), -127, 127),
  *          code = clamp(rint(x / scale) + zero, 0, 15); elements beyond ±57344 count as that, a
  *          group with a NaN gets scale NaN, and where the scale rounds to 0 so are zero and codes
- * all in fp32, each operation rounded by itself.
+ * all in fp32, each operation rounded by itself; the mean of a key's squares is rounded once or twice,
+ * of a query's some 12 times.
  *   qkv     device [n_rows][n_head + 2 n_kv_head][head_dim] of dtype, rows qkv_stride elements apart
  *           (16-byte aligned, as is the stride)
  *   n_head  query heads (0: keys and values alone; q_out may then be NULL)

@@ -538,3 +538,51 @@ def test_append_of_one_row_of_any_stride(dtype):
         q = pkg.kv4_append(x, pages, *one, rope, hq)
         same = torch.empty((1, width), dtype=x.dtype, device="cuda").copy_(x)
         assert torch.equal(q, pkg.kv4_append(same, want, *one, rope, hq)) and torch.equal(pages, want)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,hd", [(9, 3, 64), (32, 8, 128), (3, 2, 128)])
+def test_append_norm_of_large_rows(hq, hkv, hd, dtype):
+    """Rows whose sum of squares, or mean square too, is past fp32's range: the definition gives numbers where the
+    mean fits (rounded from 64 bits), and zeros where it does not (1 / sqrt(inf)).  A query: 12 roundings of 2^-24 in its
+    mean, half of that after the root, 6 more of the norm and 3 of the rotation: 15; and 9 of the plain form's."""
+    import dual_ar_tts_gb300 as pkg
+    rng = np.random.default_rng(3)
+    dt, heads, sizes = fb.TYPES[dtype], hq + 2 * hkv, (1.0, 2e17, 1.5e18, 1e19, 1.7e19, 3e19, 1e25, 1e37)
+    rows = len(sizes)
+    x = rng.standard_normal((rows, heads, hd)).clip(-3, 3) * np.asarray(sizes)[:, None, None]
+    x[4, :, 1:] *= 1e-8                                                # one element has it all
+    f = torch.from_numpy(x.astype(np.float32)).to(dt)
+    qw, kw = [torch.from_numpy((1 + 0.1 * rng.standard_normal(hd)).astype(np.float32)) for _ in "qk"]
+    one = _gpu(np.zeros((1, 1), np.int32), np.asarray([0, rows], np.int32), np.asarray([rows], np.int32))
+    rope = pkg.rope_table(rows, hd)
+    pages = pkg.kv4_pages(1, hkv, hd)
+    q = pkg.kv4_append(f.flatten(1).cuda(), pages, *one, rope, hq, q_norm=qw.cuda(), k_norm=kw.cuda()).cpu().double()
+    cs = rope.cpu()[:, None]
+    f = f.float()
+    want = fb.norm_rotate(f[:, :hq], qw, 1e-6, cs).double()
+    a, b = want[..., 0::2].abs(), want[..., 1::2].abs()
+    mag = (a + b).repeat_interleave(2, -1) * 1.5                       # of what was rotated: at most sqrt(2) of this
+    assert ((q - want).abs() <= 24 * 2.0 ** -24 * mag + fb.rounding(want, dt)).all()
+    assert (q[6:] == 0).all() and (q[:5].abs().amax((1, 2)) > 0.5).all()
+    want = torch.zeros((1, hkv, 80 * hd), dtype=torch.uint8)
+    k = fb.norm_rotate(f[:, hq:hq + hkv], kw, 1e-6, cs)
+    assert torch.isfinite(k).all()
+    for i in range(rows):
+        fb.put(want, 0, i, k[i], f[i, hq + hkv:])
+    assert (pages.cpu() != want).sum() <= 2                            # a mean on a rounding border may move a code
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+def test_append_query_bits_do_not_depend_on_the_heads_beside_it(dtype):
+    import dual_ar_tts_gb300 as pkg
+    rows, hd = 300, 64
+    x = torch.randn((rows, 6, hd), generator=torch.Generator().manual_seed(1)).to(fb.TYPES[dtype]).cuda()
+    w = torch.ones(hd, device="cuda")
+    place = _gpu(np.arange(5, dtype=np.int32)[None], np.asarray([0, rows], np.int32), np.asarray([rows], np.int32))
+    rope = pkg.rope_table(rows, hd)
+    got = []
+    for heads, hq in (([0, 1, 2, 3, 4, 5], 4), ([0, 4, 5], 1), ([1, 0, 4, 5], 2)):
+        qkv = x[:, heads].flatten(1).contiguous()
+        got.append(pkg.kv4_append(qkv, pkg.kv4_pages(5, 1, hd), *place, rope, hq, q_norm=w, k_norm=w)[:, heads.index(0)])
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
