@@ -633,6 +633,7 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   constexpr int smem = kRings > kJoin ? kRings : kJoin;
   if (!allow_smem<k_q4_many<T, NT, G>, smem>()) return S2_ECUDA;
   k_q4_planes<T, false><<<p.tiles * 8 / kTerms<T>, kPlaneThreads, 0, st>>>(a, p);
+  if (cudaGetLastError() != cudaSuccess) return S2_ECUDA;  // else the products would be of an old workspace
   return launch_joined(k_q4_many<T, NT, G>, dim3(grid, ranks), 32 * kManyWarps, smem, ranks, a, p, st);
 }
 
@@ -955,6 +956,7 @@ int launch_tc(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
   constexpr int smem = Tc<N>::kBytes;
   if (!allow_smem<k_q4_tc<T, N, G>, smem>()) return S2_ECUDA;
   k_q4_planes<T, true><<<a.n, kPlaneThreads, 0, st>>>(a, p);
+  if (cudaGetLastError() != cudaSuccess) return S2_ECUDA;
   return launch_joined(k_q4_tc<T, N, G>, dim3(grid, ranks, p.tiles), kTcThreads, smem, ranks, a, p, st);
 }
 
