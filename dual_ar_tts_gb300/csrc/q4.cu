@@ -399,11 +399,12 @@ int launch_few(MatmulArgs a, cudaStream_t st) {
 
 // ---- more activations: staged once, as planes in the workspace that every block then copies.
 
-// tcgen05 takes over behind 32 columns (19456 x 2560 at 64: 35 us on mma.sync, 20 there), and behind 16 for matrices
-// of 12 Mi weights on: 2560 x 9728 at 32 columns 16.3 us and 14.2, at 17 15.3 and 13.8, 6144 x 2560 at 24 12.7 and 12.0;
-// but 2560 x 2560 at 17 8.4 and 10.3, 1024 x 1024 at 32 5.6 and 7.7.
+// tcgen05 takes over behind 32 columns (19456 x 2560 at 64: 35 us on mma.sync, 21 there), and behind 16 for matrices
+// of 32 Mi weights on.  With weights not in L2, groups of 32, at 17 and 32 columns on mma.sync and on tcgen05:
+// 19456 x 2560 19.2 and 19.5 us, 17.5 and 18.8; 12288 x 2560 16.0 and 16.8, 16.5 and 17.7; 2560 x 9728 16.1 and 16.8,
+// 17.1 and 17.4; 9728 x 2560 14.2 and 14.6, 18.2 and 19.3; 2560 x 2560 7.9 and 9.1, 10.4 and 10.8.
 bool on_tcgen05(long long cols, int m, int k) {
-  return cols > 32 || (cols > 16 && static_cast<long long>(m) * k >= 12ll << 20);
+  return cols > 32 || (cols > 16 && static_cast<long long>(m) * k >= 32ll << 20);
 }
 
 // What the workspace holds: for mma.sync `tiles` tiles of 8 columns; for tcgen05 `tiles` tiles of `width` columns, as

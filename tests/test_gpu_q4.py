@@ -283,3 +283,11 @@ def test_matmul_of_one_row_of_any_stride(dtype):
     column = wide[:2].flatten()[:2 * k].view(k, 2)
     for x in (wide[:1, :k], wide[1:2, 1:1 + k], wide[3:, 4:], column[:, :1].t(), column[:, 1:].t(), column[:, :1].clone().t()):
         _check(pkg.q4_matmul(x, codes, scales, 32), x, codes, scales, k, 32)
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 17), ("fp16", 32), ("fp32", 9)])
+def test_matmul_of_larger_matrices(dtype, n):
+    """The same on both sides of 32 Mi weights."""
+    k = 2560
+    for m in ((32 << 20) // k + 1, (32 << 20) // k - 1):
+        test_matmul(dtype, n, m, k, 64)
