@@ -318,7 +318,8 @@ def quantize_q4(w, group: int = 32):
 
 
 def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
-    """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4 -> [n][rows] in x's type.
+    """x [n][k] (fp32, bf16 or fp16) times the transposed 4-bit matrix of quantize_q4, or consecutive rows of it
+    (codes[a:b], scales[a:b]) -> [n][rows] in x's type.
     workspace, a uint8 tensor of s2_q4_matmul_workspace bytes, is allocated where none is given."""
     h = _hot or _bind()
     dt, dev = h.kinds.get(x.dtype), x.get_device()
@@ -333,6 +334,10 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
             not scales.is_contiguous():
         _bad("codes must be contiguous uint8 [rows][ceil(k/128)*64] and scales contiguous bf16 "
              "[rows][ceil(k/128)*(128/group)], k a multiple of group")
+    if codes.data_ptr() % 16:
+        codes = codes.clone()
+    if scales.data_ptr() % (8 if group == 32 else 4):  # rows of a quantised matrix, from an odd number of scales on
+        scales = scales.clone()
     x, stride = _rows16(x)
     if out is None:
         out = h.empty((n, m), dtype=x.dtype, device=x.device)

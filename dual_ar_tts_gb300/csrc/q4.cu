@@ -1021,7 +1021,7 @@ extern "C" int s2_q4_matmul(int n, const void* x, int dtype, long long x_stride,
       x_stride < k || n > kRowsMost || m > kMatmulMost || k > kMatmulMost)
     return S2_EINVAL;
   if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || x_stride * esz % 16 != 0 ||
-      reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(codes) % 16 != 0 || reinterpret_cast<uintptr_t>(scales) % (group == 32 ? 8 : 4) != 0 ||
       reinterpret_cast<uintptr_t>(y) % esz != 0 || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return S2_EINVAL;
   const size_t need = s2_q4_matmul_workspace(n, k, dtype);

@@ -362,7 +362,8 @@ int s2_quantize_q4(const void* w, int dtype, long long rows, int cols, int group
  * leaves NaN.
  *   x         device [n][k] of dtype, rows x_stride elements apart; 16-byte aligned, x_stride times
  *             the element size a multiple of 16
- *   codes, scales  as s2_quantize_q4 writes them, both 16-byte aligned; k a multiple of group
+ *   codes, scales  as s2_quantize_q4 writes them, or from one of their rows on; codes 16-byte aligned,
+ *             scales 8 (group 32) or 4; k a multiple of group
  *   y         device [n][m] of dtype, aligned to its element size
  *   workspace device, 16-byte aligned, of at least s2_q4_matmul_workspace bytes for the same sizes
  *             (NULL where that is 0).  Calls that may run at the same time need one each.

@@ -291,3 +291,16 @@ def test_matmul_of_larger_matrices(dtype, n):
     k = 2560
     for m in ((32 << 20) // k + 1, (32 << 20) // k - 1):
         test_matmul(dtype, n, m, k, 64)
+
+
+@pytest.mark.parametrize("dtype,n", [("fp32", 1), ("bf16", 3), ("fp16", 14), ("bf16", 50), ("fp32", 70)])
+@pytest.mark.parametrize("k,group", [(128, 128), (1408, 128), (2560, 128), (640, 64), (160, 32)])
+def test_matmul_of_a_part_of_the_rows(k, group, dtype, n):
+    """Rows of a quantised matrix, from the second, the third and the last on: their scales start on 2, 4 or 8 bytes."""
+    import dual_ar_tts_gb300 as pkg
+    codes, scales = pkg.quantize_q4(_weights(90, k, torch.bfloat16, 1).cuda(), group)
+    x = torch.randn((n, k), generator=torch.Generator().manual_seed(2)).to(fb.TYPES[dtype]).cuda()
+    for a, b in ((1, 90), (2, 33), (7, 8), (89, 90)):
+        _check(pkg.q4_matmul(x, codes[a:b], scales[a:b], group), x, codes[a:b], scales[a:b], k, group)
+    held = torch.empty(codes.numel() + 4, dtype=torch.uint8, device="cuda")[4:].view(codes.shape).copy_(codes)
+    _check(pkg.q4_matmul(x, held, scales, group), x, codes, scales, k, group)

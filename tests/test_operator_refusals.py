@@ -137,3 +137,11 @@ def test_rows_of_any_stride_are_taken():
             assert y.shape == x.shape and torch.equal(y, x)
             assert y.data_ptr() % 16 == 0 and stride >= k and stride * y.element_size() % 16 == 0
             assert y.stride(1) == 1 and (y.shape[0] == 1 or y.stride(0) == stride)
+
+
+def test_q4_matmul_alignment_of_scales(lib):
+    good = dict(n=2, x=P, dtype=1, x_stride=128, codes=P, scales=P, m=4, k=128, group=32, y=P, ws=None, nb=0,
+                stream=None)
+    _bad(lib.s2_q4_matmul, good, scales=[P + 1, P + 2, P + 4, P + 12])
+    for group in (64, 128):
+        _bad(lib.s2_q4_matmul, dict(good, group=group), scales=[P + 1, P + 2, P + 6])
