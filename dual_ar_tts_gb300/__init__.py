@@ -306,14 +306,16 @@ def quantize_q4(w, group: int = 32):
     dt, dev = h.kinds.get(w.dtype), w.get_device()
     if dt is None or dev < 0:
         _bad(_DEVICE)
-    if w.dim() != 2 or group not in (32, 64, 128) or w.shape[1] % group or not w.numel():
+    if w.dim() != 2 or group not in (32, 64, 128) or w.shape[1] % group or not w.shape[1]:
         _bad("quantize_q4 takes a 2-D tensor, its columns a multiple of group: 32, 64 or 128")
     w = w.contiguous()
     rows, cols = w.shape
     blocks = -(-cols // 128)
     codes = h.empty((rows, blocks * 64), dtype=h.u8, device=w.device)
     scales = h.empty((rows, blocks * (128 // group)), dtype=h.bf16, device=w.device)
-    _launch(h, h.lib.s2_quantize_q4, dev, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(), scales.data_ptr())
+    if rows:
+        _launch(h, h.lib.s2_quantize_q4, dev, w.data_ptr(), dt, rows, cols, group, codes.data_ptr(),
+                scales.data_ptr())
     return codes, scales
 
 
@@ -343,6 +345,8 @@ def q4_matmul(x, codes, scales, group: int = 32, out=None, workspace=None):
         out = h.empty((n, m), dtype=x.dtype, device=x.device)
     elif out.dtype is not x.dtype or out.shape != (n, m) or out.get_device() != dev or not out.is_contiguous():
         _bad("out must be contiguous [n][rows] of x's type, on its device")
+    if not n or not m:
+        return out
     if workspace is None:
         nbytes = h.lib.s2_q4_matmul_workspace(n, k, dt)
         workspace = h.empty(nbytes, dtype=h.u8, device=x.device) if nbytes else None
@@ -429,6 +433,8 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
     elif q_out.dtype is not qkv.dtype or q_out.shape != (n_rows, n_head, hd) or q_out.get_device() != dev or \
             not q_out.is_contiguous():
         _bad("q_out must be contiguous [n_rows][n_head][head_dim] of qkv's type, on its device")
+    if not n_rows:
+        return q_out
     _launch(h, h.lib.s2_kv4_append, dev, ctypes.byref(c), qkv.data_ptr(), dt, stride, n_head, rope.data_ptr(),
             rope.shape[0], None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
             eps, q_out.data_ptr())
@@ -449,7 +455,8 @@ def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None
         v_out = h.empty(shape, dtype=f16, device=pages.device)
     elif v_out.dtype is not f16 or v_out.shape != shape or v_out.get_device() != dev or not v_out.is_contiguous():
         _bad("outputs must be contiguous fp16 [n_kv_head][n_rows][head_dim] on the pages' device")
-    _launch(h, h.lib.s2_kv4_read, dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
+    if n_rows:
+        _launch(h, h.lib.s2_kv4_read, dev, ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr())
     return k_out, v_out
 
 
@@ -474,6 +481,8 @@ def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None,
         out = h.empty((n_rows, n_head, hd), dtype=q.dtype, device=q.device)
     elif out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != dev or not out.is_contiguous():
         _bad("out must be contiguous, of q's shape and type, on its device")
+    if not n_rows or not n_head:
+        return out
     if workspace is None:
         held = c.table_cols * S2_KV4_PAGE
         nbytes = h.lib.s2_kv4_attention_workspace(c.n_seq, n_rows, n_head, n_kv, hd, min(max_len or held, held))
@@ -531,6 +540,8 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
         out = h.empty((rows, n), dtype=f32, device=logits.device)
     elif out.dtype is not f32 or out.shape != (rows, n) or not out.is_contiguous():
         _bad("out must be contiguous fp32 [rows][n]")
+    if not rows or not n:
+        return out
     _launch(h, h.lib.s2_adjust_logits, dev, rows, n, sem_begin, im_end, logits.data_ptr(), dt, hp, lp, cols, pp, bp,
             bias_stride, mp, mask_stride, out.data_ptr())
     return out
