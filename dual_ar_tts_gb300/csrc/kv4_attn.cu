@@ -1150,10 +1150,19 @@ __global__ void __launch_bounds__(256) k_kv4_join_few(const AttnArgs a) {
     static_cast<T*>(a.out)[item * HD + lane + 32 * i] = from_f<T>(l == 0.f ? 0.f : o[i] / l);
 }
 
-// How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 12 columns on
-// average (rows times query heads of a KV head; fp32 queries count twice): 8 sequences of 4000 positions take 35 us
-// against 33 at 10 columns on average, 37 against 42 at 18.  Splits, of at least two pages (an even number: they are taken two
-// at a time), at most 128:
+// How a call's work is cut.  The kernel for many columns takes over where a sequence has more than 16 columns on
+// average (rows times query heads of a KV head; fp32 queries count twice, and there it is 40).  32 query heads on 8, us
+// of the kernel for few and of that for many:
+//   sequences x positions      8 x 4000    1 x 30000   32 x 1000   8 x 200
+//   bf16 hd 128, 16 columns    36.5 33.7   38.1 32.5   30.4 39.1   12.7 11.1
+//                24            45.4 34.3   45.9 32.8   43.5 39.8   14.8 11.1
+//   bf16 hd 64,  16            23.4 25.9   25.0 25.8   22.1 30.3    8.6  9.0
+//                24            27.5 26.3   29.9 26.2   25.8 30.5    9.4  9.0
+//   fp32 hd 128, 32            50.2 62.0   45.1 58.5   48.4 73.5   13.5 12.7
+//                48            69.0 63.1   63.1 59.4   71.7 75.4   19.0 13.5
+//   fp32 hd 64,  32            30.8 40.1   29.1 37.8   29.1 44.9    8.6 11.1
+//                48            42.2 40.4   40.2 38.9   41.8 45.9   10.2 11.1
+// Splits, of at least two pages (an even number: they are taken two at a time), at most 128:
 //  - few columns: the blocks that the 152 SMs hold at once (4 an SM), twice that where there are many items of what
 //    may be different lengths (32 of 512..4096: 32 us against 46);
 //  - many columns: the blocks that they hold at once (2 an SM); two where that gives none and there are few rounds,
@@ -1168,7 +1177,7 @@ struct Plan {
 Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int max_len, bool two) {
   Plan p{};
   const long long group = n_head / n_kv_head, columns = n_rows * group * (two ? 2 : 1);
-  p.many = columns > 12ll * n_seq;
+  p.many = columns > (two ? 40ll : 16ll) * n_seq;
   const int cols = p.many ? kTcCols : two ? 4 : 8;
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
