@@ -341,8 +341,9 @@ extern "C" int s2_kv4_append(const s2_kv4* cache, const void* qkv, int dtype, lo
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // Few rows: a warp for every 2 (hd 128) or 4 heads.  Many: one block of four warps a row, each of which finds the
-    // row's place and its rotation once and loads a head ahead (5916 rows of 48 heads: 46.6 us; with two warps 49.3,
-    // with eight 50.5; before, with a warp for every 2 heads, 4700 rows took 74 us with the reading back, not 65).
+    // row's place and its rotation once and loads a head ahead.  Few and many, us, fp16: 48 heads of 128, 256 rows 5.3
+    // and 6.6, 512 7.4 and 7.4, 1024 11.9 and 9.7, 4096 42.4 and 31.7; 15 heads of 64, 512 rows 3.7 and 3.7, 4096 13.5 and
+    // 10.3.  (With two warps a row 5916 rows took 49.3 us, with four 46.6, with eight 50.5.)
     const int turns = static_cast<int>((heads * cache->head_dim / 8 + 255) / 256);
     const bool many = cache->n_rows >= 512;
     const dim3 grid(cache->n_rows, many ? 1 : turns);
