@@ -1166,10 +1166,12 @@ __global__ void __launch_bounds__(256) k_kv4_join_few(const AttnArgs a) {
 //  - few columns: the blocks that the 152 SMs hold at once (4 an SM), twice that where there are many items of what
 //    may be different lengths (32 of 512..4096: 32 us against 46);
 //  - many columns: the blocks that they hold at once (2 an SM; fp32 queries at head size 128 have one, and two rounds).
-//    Two splits where that gives one would help a sequence much longer than the others (five pieces, 60 rows over 42
-//    pages and four over 20: 55 us against 63), but lengths are not known here, and where they are alike it costs more
-//    than that (5 x 200 rows over 2000: 79 against 57; 4 x 512 over 512: 81 against 37; 23 calls of 2 to 12 sequences
-//    of random rows and lengths: 15 % more).
+//    Two where that gives one, there are few rounds and max_len is 32 pages or more: a sequence much longer than the
+//    others is a chain of pages by itself (five pieces, 60 rows over 42 pages and four over 20: 55 us, unsplit 63; 30 rows
+//    over 59 and four of 160 over 20: 56, 77).  Lengths are not known here, and where they are alike two splits cost more
+//    than they give, the more the shorter (8 x 100 rows over 47 pages: 96 us, unsplit 79; 5 x 200 over 32: 79, 57; 4 x 512
+//    over 8: 81, 37).  42 calls of 1 to 16 sequences, geometric means: split from 32 pages on 44.7 us, never 45.4,
+//    always 51.6.
 // The workspace is sized for the most splits that any length up to max_len can get, so that it does not shrink with
 // a larger max_len.
 struct Plan {
@@ -1186,7 +1188,8 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
   const long long items = static_cast<long long>(p.tiles) * n_kv_head;
   const long long room = p.many ? 152 * 2 : items < 152 ? 152 * 4 : 152 * 8;
-  const int want = static_cast<int>(std::min(std::max(1ll, room / items), 128ll));
+  const long long least = p.many && items < 152 * 4 && pages >= 32 ? 2 : 1;
+  const int want = static_cast<int>(std::min(std::max(least, room / items), 128ll));
   p.split_pages = std::max(2, (pages + want - 1) / want);
   p.split_pages += p.split_pages & 1;
   p.n_split = std::max(1, (pages + p.split_pages - 1) / p.split_pages);
