@@ -410,7 +410,9 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
     fp16; q | k | v, head-major).  Queries and keys are normed per head where q_norm / k_norm (fp32 [head_dim]) are
     given and rotated by rope's (rope_table) row of their position; keys and values are quantised.  table int32
     [n_seq][cols], q_start int32 [n_seq + 1] and lengths int32 [n_seq] place the rows (see s2_kv4 in s2frame.h).
-    Returns the rotated queries [n_rows][n_head][head_dim]; rows behind the last sequence are left as they were."""
+    Returns the rotated queries [n_rows][n_head][head_dim].  Rows behind the last sequence are left as they were, and so
+    are rows whose position or page is out of range, of which status (one int32, zeroed by the caller) tells; in a q_out
+    that the call allocates they hold nothing in particular."""
     h = _hot or _bind()
     dt, dev = h.kinds.get(qkv.dtype), qkv.get_device()
     if dt is None or qkv.dim() != 2:
@@ -442,7 +444,9 @@ def kv4_append(qkv, pages, table, q_start, lengths, rope, n_head: int, q_norm=No
 
 
 def kv4_read(pages, table, q_start, lengths, n_rows: int, k_out=None, v_out=None, status=None):
-    """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]."""
+    """What the rows' positions of a paged 4-bit cache stand for: (k, v) fp16 [n_kv_head][n_rows][head_dim]; zeros where a
+    position or page is out of range (status, as kv4_append's, then tells).  Rows behind the last sequence are left as
+    they were."""
     h = _hot or _bind()
     dev = pages.get_device()
     c = _kv4(h, dev, pages, table, q_start, lengths, n_rows, status)
@@ -465,7 +469,8 @@ def kv4_attention(q, pages, table, q_start, lengths, scale: float | None = None,
     """Causal attention of q [n_rows][n_head][head_dim] (fp32, bf16 or fp16) over a paged 4-bit cache that holds
     the rows' own keys and values already (kv4_append).  scale defaults to 1/sqrt(head_dim); max_len (the largest
     length expected, 0: what the table can hold) only sets how the work is split; workspace, a uint8 tensor of
-    s2_kv4_attention_workspace bytes, is allocated where none is given."""
+    s2_kv4_attention_workspace bytes, is allocated where none is given.  Pages out of range are not attended; status, as
+    kv4_append's, tells of them.  Rows behind the last sequence are left as they were."""
     h = _hot or _bind()
     dt, dev = h.kinds.get(q.dtype), q.get_device()
     if dt is None or q.dim() != 3:

@@ -48,8 +48,8 @@ struct Words<32> {
 // way.  A thread's kPer entries are consecutive and read 16 bytes at a time where rows are aligned to that (kWide);
 // else they are 256 apart, so that rows of any alignment are read and written in whole lines.  Bound by those bytes;
 // the history is read again by every slice, from L2 (four bytes a token against 20 KB and more).  32 bf16 rows of
-// 155776, each with its bias, mask and 2048 tokens: 14.2 us, 3.6 TB/s; slices of 1024 entries took 15.4, of 4096 14.5,
-// of 8192 19.8.
+// 155776, each with its bias, mask and 2048 tokens: 15.7 us, 3.2 TB/s; 14.2 with part of that in L2, where slices of 1024
+// entries took 15.4, of 4096 14.5, of 8192 19.8.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kAdjustThreads) k_adjust(const AdjustArgs a) {
   __shared__ __align__(16) int count[kSlice];

@@ -237,7 +237,7 @@ __device__ __forceinline__ void append_item(const AppendArgs& a, int row, const 
 
 // A block takes one row of the call and some of its heads; its warps take heads in turn.  The first load of a head
 // does not wait for the row's place.  One pass: a head is read once, and its sums and extremes are shuffles in a
-// quarter or half of a warp.  5916 fp16 rows of 32 + 2 x 8 heads: 46.6 us, 2.7 TB/s; bound by instructions (the norm of
+// quarter or half of a warp.  5916 fp16 rows of 32 + 2 x 8 heads: 47.8 us, 2.6 TB/s; bound by instructions (the norm of
 // keys to the last bit, the quotients and codes), not by the bytes, which would take 19.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) k_kv4_append(const AppendArgs a) {
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(256) k_kv4_append(const AppendArgs a) {
   }
 }
 
-// A warp takes a row's keys and values of 32 / kLanes heads.  5916 rows of 8 heads: 7.6 us, 4.2 TB/s of what it reads
-// and writes.
+// A warp takes a row's keys and values of 32 / kLanes heads.  5916 rows of 8 heads: 8.3 us, 3.9 TB/s of what it reads
+// and writes; a warp's loads are three in a chain (bounds, page, codes) before its only stores.
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv4_read(const s2_kv4 c, __half* __restrict__ k_out,
                                                   __half* __restrict__ v_out) {

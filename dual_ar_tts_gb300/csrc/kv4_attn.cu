@@ -434,8 +434,9 @@ constexpr int kDecodeSmem = std::max(kWarps * kDepth * Stage<HD>::kBytes, kWarps
 // Few columns: a block takes one tile of 8 columns of one KV head over a range of pages, two at a time.  Each of
 // its four warps takes half a page with its own copies in flight, so the warps never wait on one another until
 // their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 78 us, 3.9 TB/s of the
-// cache; 32 of 512 .. 4096: 30 us.  Bound by the instructions that expand codes (55 million a call of the first,
-// 2.7 of 4 issued a cycle; the copies alone take 55 us), each of which serves four query heads here.
+// cache (fp32 queries 82); 32 of 512 .. 4096: 31 us.  Bound by a step's chain (scores, exponential, turned weights,
+// output) on the instructions that expand codes, 54 million a call of the first, each of which serves four query heads
+// here: sixteen warps an SM fill 67 % of the issue slots with them; the copies alone take 55 us.
 template <typename T, int HD>
 __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   constexpr bool kTwo = sizeof(T) == 4;
@@ -597,8 +598,8 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // without, 2.7e-7 with, 83 us and 84 at head size 128, 56 and 61 at 64).
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
 // queries alike.
-// 512 bf16 rows over 30000 positions: 370 us, 680 TFLOP/s; five pieces of prompts (874 rows over up to 42 pages): 52 us,
-// with the joining.  Bound by a page's chain of scores, exponentials (one thread a column) and output.
+// 512 bf16 rows over 30000 positions: 377 us, 670 TFLOP/s (fp32 724); five pieces of prompts (874 rows over up to 42
+// pages): 54 us, with the joining, 63 where the cache is not in L2.  Bound by a page's chain of scores, exponentials (one thread a column) and output.
 constexpr int kTcCols = 128;
 template <int HD, int TN>
 struct Tc {

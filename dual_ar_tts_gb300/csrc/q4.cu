@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kBlock = 128;  // columns of a code block
 
-// One warp per block of 128 columns; lane l holds columns 4l .. 4l + 3 (19456 x 2560: 116 us, bound by its divisions;
+// One warp per block of 128 columns; lane l holds columns 4l .. 4l + 3 (19456 x 2560: 118 us, bound by its divisions;
 // weights are quantised once).  A group's scale is its entry
 // of the largest magnitude (the first of equals) divided by -8, rounded to bf16, so that entry takes
 // code 0 and the range -8..7 is used whole; the codes are taken against the rounded scale.
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) k_quant_q4(const T* __restrict__ w, long 
 // the expanded weights in tensor memory first; with more columns that pays (k_q4_tc, below).
 //
 // A code is expanded to the whole number code - 8.  (Masked alone it would be the fp16 subnormal code * 2^-24, and the
-// sum would have to start with -8 * sum x.  That costs two instructions a word less, 10.5 us against 11.3 for one row
+// sum would have to start with -8 * sum x.  That is four instructions a word less, 10.5 us against 11.3 for one row
 // of 19456 x 2560, but the tensor cores line products up by their operands' exponents and cut off what is below a
 // sum's last bit, and the rest cancels: fp32 products were 1e-6 to 2e-6 off, where they now are 1e-7.)  A 32-bit word of codes feeds the k positions of two instructions in the
 // order (0,4)(1,5) | (2,6)(3,7) of its nibbles; activations are staged in that order.  A group's scale multiplies its
@@ -284,7 +284,7 @@ __device__ __forceinline__ float unscale(float z, uint32_t top) { return by_pow2
 
 // ---- few activations: one tile of columns, staged whole by every block.  A block is 8 warps: R tiles of 16 rows
 // times 8 / R parts of W's columns (blocks of 128, taken in turn), whose sums are added in order at the end.
-// 19456 x 2560, one fp32 row, weights not in L2: 11.3 us, 2.5 TB/s of codes and scales; the launch and the staging are
+// 19456 x 2560, one fp32 row, weights not in L2: 11.0 us, 2.6 TB/s of codes and scales; the launch and the staging are
 // 3 of them.
 constexpr int kFewAhead = 8;
 template <typename T>
@@ -514,7 +514,7 @@ __device__ __forceinline__ float ld_cluster1(uint32_t addr, uint32_t rank) {
 // A block takes 64 rows (a warp 16) and a range of W's columns; the blocks of a cluster split W's columns and add
 // their sums through distributed shared memory in rank order.  Every step is one block of 128 columns: its
 // activations are copied for all warps, kAhead steps ahead, and one barrier a step passes them on.  16 bf16 rows,
-// 19456 x 2560, weights not in L2: 16.2 us; 17 rows, 2560 x 2560: 8.2.  At 32 columns a step of 128 takes 0.9 us, bound by mma.sync.
+// 19456 x 2560, weights not in L2: 15.8 us; 17 rows, 2560 x 2560: 8.3; 32 rows, 2560 x 9728: 15.1.  At 32 columns a step of 128 takes 0.9 us, bound by mma.sync.
 constexpr int kManyWarps = 4, kManyRows = 16 * kManyWarps;
 constexpr int kJoinRow = kManyRows + 4;  // floats of a column in the joining buffer: 4-row groups, no bank conflicts
 template <int NT>
@@ -647,8 +647,7 @@ int launch_many(const MatmulArgs& a, const Planes& p, cudaStream_t st) {
 // show it (6e-6 over 9728 columns).  Of fp32 rows the sums of two code blocks at a time (chunks) are added up in
 // registers: 3e-7 at any k where they were up to 6e-6 off; 1024 rows of 19456 x 2560 take 201 us, 187 without.
 // 19456 x 2560, 2048 bf16 rows: 207 us, 990 TFLOP/s; 512 rows 53 us; bound by the activations that every block reads
-// again from L2 (9 TB/s).  2560 x 9728, 32 rows: 14.2 us, 4 of them until the planes are there and scales looked
-// through, 4 for the join.
+// again from L2 (9 TB/s).  64 rows 20.5 us.
 template <int N>
 struct Tc {
   static constexpr int kA = N == 128 ? 2 : 3;                      // expanded code blocks, 64 tensor memory columns each

@@ -329,10 +329,11 @@ int s2_draw(int rows, const float* logits, int n, int sem_begin, int im_end, int
  * 4-bit weights, a 4-bit paged key/value cache and adjusted logits: stateless calls on caller
  * buffers, for a decode step whose projections and cache are held in 4 bits.  (The precedent on
  * the pages is s2.cpp's K-quantised GGUF tensors, s2.cpp analysis ch.02 §5 and ch.04 §4; the
- * formats are this library's choice.)  One such step is: s2_q4_matmul (wqkv), s2_kv4_append,
- * s2_kv4_attention, s2_q4_matmul (wo, then the feed-forward and the logits), s2_adjust_logits,
- * s2_draw.  All of them allocate nothing, keep nothing between calls, are asynchronous on
- * `stream`, may be captured into a CUDA graph, and give the same bits for the same inputs.
+ * formats are this library's choice.)  Of such a step they are: s2_q4_matmul (wqkv), s2_kv4_append,
+ * s2_kv4_attention, s2_q4_matmul (wo, the feed-forward's three, the logits), s2_adjust_logits,
+ * s2_draw; the RMSNorm of the hidden state, the feed-forward's gate and the residual sums between
+ * them are the caller's.  All of them allocate nothing, keep nothing between calls, are asynchronous
+ * on `stream`, may be captured into a CUDA graph, and give the same bits for the same inputs.
  * dtype is S2_F32, S2_BF16 or S2_F16; sums are held in fp32 whatever the type, and a result is
  * rounded to it once.  Outputs may not overlap inputs unless a call says so.
  * Errors (nothing launched): S2_EINVAL bad count, size, type, pointer or alignment; S2_ECUDA
