@@ -1032,6 +1032,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
     }
     if (!ok) *failed = 1;
     named_bar(3, kTcThreads);  // all products have ended, and all waits
+    mbar_wait_short(drained, 0);  // for this thread's order with the products; it does not wait any more
     tc_fence_after();
     if (*failed) {
       ok = false;

@@ -34,3 +34,22 @@ def test_no_rows(dtype):
         pkg.q4_matmul(none(0, 128), codes, scales, 64)
     with pytest.raises(ValueError):
         pkg.kv4_append(none(0, 5 * 64), pages, *place, pkg.rope_table(8, 64), 2)
+
+
+@pytest.mark.parametrize("dtype", list(fb.TYPES))
+@pytest.mark.parametrize("rows", [3, 600])
+def test_append_of_rows_of_a_wider_tensor(rows, dtype):
+    """Rows that start on 16 bytes are read where they lie, others are copied: the same bytes and queries."""
+    import dual_ar_tts_gb300 as pkg
+    hq, hkv, hd = 3, 2, 64
+    width, dt = (hq + 2 * hkv) * hd, fb.TYPES[dtype]
+    wide = torch.randn((rows, width + 24), generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    place = (torch.randperm(10, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()[None].contiguous(),
+             ints(0, rows), ints(rows + 5))
+    rope = pkg.rope_table(rows + 5, hd)
+    for x in (wide[:, :width], wide[:, 16:16 + width], wide[:, 3:3 + width], wide[:, :width].t().contiguous().t()):
+        got, want = pkg.kv4_pages(10, hkv, hd), pkg.kv4_pages(10, hkv, hd)
+        q = pkg.kv4_append(x, got, *place, rope, hq)
+        same = torch.empty((rows, width), dtype=dt, device="cuda").copy_(x)
+        assert torch.equal(q, pkg.kv4_append(same, want, *place, rope, hq)) and torch.equal(got, want)
