@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
 // queries alike.
 // 512 bf16 rows over 30000 positions: 377 us, 670 TFLOP/s (fp32 724); five pieces of prompts (874 rows over up to 42
-// pages): 54 us, with the joining, 63 where the cache is not in L2.  Bound by a page's chain of scores, exponentials (one thread a column) and output.
+// pages): 54 us, with the joining, 63 where the cache is not in L2.  Bound by a page's chain of scores, exponentials (one
+// thread a column) and output.
 constexpr int kTcCols = 128;
 template <int HD, int TN>
 struct Tc {
