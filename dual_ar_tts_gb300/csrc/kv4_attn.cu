@@ -9,19 +9,22 @@
 //      S^T[16 positions][8 columns] = K[16][hd] Q^T[hd][8]
 //      O^T[hd][8] += V^T[hd][16] P^T[16][8]
 //  - many (pieces of prompts): tcgen05, the cache expanded once for 128 columns (k_kv4_tc, below).
-// With fp32 queries a column is two, the high and the low fp16 part of the query, whose scores are added and whose
-// weights are again split so (a weight then carries 22 bits).  16-bit queries are exact in fp16: each row is scaled by
-// a power of two.  Weights are kept as 2^6 exp2(s - m), m the running maximum or up to 8 (log2) below it: what falls off
-// fp16's end is 2^-30 and less of the largest, and a maximum that rises a little costs no rescaling of the output.
-// Of 16-bit queries a weight is rounded to fp16, 2^-11 of it; the sum that divides the output is of the weights before
-// that.  bf16 results do not show it (1.7e-3 off 64 bits either way), fp16 ones are 2.4e-4 off where their own rounding
-// is 2.1e-4.  A second term was measured: it leaves 2.1e-4, and 8 x 30000 positions take 85 us instead of 80, 512
-// rows over 30000 578 us instead of 374.
+// A weight of the softmax is two fp16 terms (22 bits), whose products with the values are added: rounded to one, 2^-11 of
+// it, weights made fp16 results 2.4e-4 off 64 bits, where their own rounding is 2.1e-4, and took 15 % of them (2 % of bf16
+// ones) to the neighbour of the rounded 64-bit result.  In the kernel for few a lane's two columns are then a weight's
+// terms, four columns a tile, which costs nothing where a sequence has no more than four; with more, eight columns a
+// tile and twice the products.  (8 x 30000 positions, four query heads a KV head: 79 us so, 85 with eight columns, 78
+// with one term; pieces of prompts 57 us, 54 with one term; 512 rows over 30000 397 and 378.)
+// fp32 queries are two fp16 terms as well, a column each in the kernel for few, whose scores are added.  16-bit queries
+// are exact in fp16: each row is scaled by a power of two.  Weights are kept as 2^6 exp2(s - m), m the running maximum or
+// up to 8 (log2) below it: what falls off fp16's end is 2^-30 and less of the largest, and a maximum that rises a little
+// costs no rescaling of the output.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "convert.cuh"
 #include "kv4.cuh"
@@ -225,10 +228,11 @@ __device__ __forceinline__ bool odd_values(uint32_t st, int step, int lane) {
 // O^T += V^T P^T of one step.  Lane (g, c) expands elements g * hd/8 .. + hd/8 - 1 of rows 2c, 2c + 1, 2c + 8,
 // 2c + 9; element 2i of those is row g, element 2i + 1 row g + 8 of the i-th tile.  Where not kPlain, the
 // parameters of rows from `valid` on (behind the sequence: their weights are zero, but what is there may be no
-// number) and those that are no numbers count as zero.  kApart: the step's products start at zero and are added to O
-// outside the tensor core, which cuts a sum off at its last bit at every addition (as k_kv4_tc's).
-template <int HD, bool kPlain, bool kApart>
-__device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[2],
+// number) and those that are no numbers count as zero.  p: the terms of the weights (kTwo: one, of columns in pairs).
+// kApart: the step's products start at zero and are added to O outside the tensor core, which cuts a sum off at its
+// last bit at every addition (as k_kv4_tc's).
+template <int HD, bool kPlain, bool kApart, bool kTwo>
+__device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int valid, const uint32_t (&p)[2][2],
                                        float (&o)[HD / 16][4]) {
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
@@ -261,18 +265,19 @@ __device__ __forceinline__ void values(uint32_t st, int step, int g, int c, int 
         float(&to)[4] = o[4 * j + 2 * h + i];
         if constexpr (kApart) {
           float d[4];
-          mma_f16_16816_first(d, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0], p[1]);
+          mma_f16_16816_first(d, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0][0], p[0][1]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) to[k] += d[k];
         } else {
-          mma_f16_16816(to, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0], p[1]);
+          if constexpr (!kTwo) mma_f16_16816(to, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[1][0], p[1][1]);
+          mma_f16_16816(to, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1], p[0][0], p[0][1]);
         }
       }
     }
 }
 
-// The running state of a warp's columns.  A lane's columns are 2c, 2c + 1 (with fp32 queries the
-// two parts of one), the same in the scores and in the output tiles.
+// The running state of a warp's columns.  A lane's columns are 2c, 2c + 1 (kTwo: the two terms of one), the same in the
+// scores and in the output tiles.
 template <int HD, bool kTwo>
 struct Rows {
   static constexpr int NC = kTwo ? 1 : 2;  // a lane's logical columns
@@ -294,8 +299,8 @@ struct Rows {
     return lift[j] == kNone ? -INFINITY : kWeightShift - lift[j];
   }
 
-  // one step at position t0: s becomes the weights, as B operand
-  __device__ __forceinline__ void softmax(float (&s)[4], int t0, int g, bool cut, uint32_t (&p)[2]) {
+  // one step at position t0: s becomes the weights, as B operand, in two terms (kTwo: a column each)
+  __device__ __forceinline__ void softmax(float (&s)[4], int t0, int g, bool cut, uint32_t (&p)[2][2]) {
     if constexpr (kTwo) s[0] += s[1], s[2] += s[3];
     if (cut) {
 #pragma unroll
@@ -322,7 +327,12 @@ struct Rows {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if constexpr (kTwo) w[r][1] = w[r][0] - round_f16(w[r][0]);
-      p[r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0], w[r][1])));
+      const __half2 h = __floats2half2_rn(w[r][0], w[r][1]);
+      p[0][r] = movmatrix_trans(h2_bits(h));
+      if constexpr (!kTwo) {
+        const float2 f = __half22float2(h);
+        p[1][r] = movmatrix_trans(h2_bits(__floats2half2_rn(w[r][0] - f.x, w[r][1] - f.y)));
+      }
     }
   }
 
@@ -431,15 +441,15 @@ constexpr int kWarps = 4;
 template <int HD>
 constexpr int kDecodeSmem = std::max(kWarps * kDepth * Stage<HD>::kBytes, kWarps * 8 * (HD + 4 + 2) * 4);
 
-// Few columns: a block takes one tile of 8 columns of one KV head over a range of pages, two at a time.  Each of
-// its four warps takes half a page with its own copies in flight, so the warps never wait on one another until
-// their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 78 us, 3.9 TB/s of the
-// cache (fp32 queries 82); 32 of 512 .. 4096: 31 us.  Bound by a step's chain (scores, exponential, turned weights,
-// output) on the instructions that expand codes, 54 million a call of the first, each of which serves four query heads
-// here: sixteen warps an SM fill 67 % of the issue slots with them; the copies alone take 55 us.
-template <typename T, int HD>
+// Few columns: a block takes one tile of 8 columns (kTwo: 4 of two terms each, see above) of one KV head over a range of
+// pages, two at a time.  Each of its four warps takes half a page with its own copies in flight, so the warps never wait
+// on one another until their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 79 us, 3.9
+// TB/s of the cache (fp32 queries 82); 32 of 512 .. 4096: 31 us.  Bound by a step's chain (scores, exponential, turned
+// weights, output) on the instructions that expand codes, 54 million a call of the first, each of which serves four query
+// heads here: sixteen warps an SM fill 67 % of the issue slots with them; the copies alone take 55 us.
+template <typename T, int HD, bool kTwo>
 __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
-  constexpr bool kTwo = sizeof(T) == 4;
+  constexpr bool kApart = sizeof(T) == 4;
   constexpr int CT = kTwo ? 4 : 8;  // logical columns
   using B = Kv4Block<HD>;
   using S = Stage<HD>;
@@ -518,16 +528,16 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
         const int t0 = first + step * kStep, valid = min(len - t0, kStep);
         if (valid <= 0) break;
         float s[4];
-        uint32_t pf[2];
+        uint32_t pf[2][2];
         scores<HD>(at, step, g, c, qf, s);
         // where every column sees the whole step, a value that is no number reaches all of them anyway
         const bool cut = t0 + kStep > first_lim;
         st.softmax(s, t0, g, cut, pf);
         const bool odd = cut && odd_values<HD>(at, step, lane);
         if (!odd && valid == kStep) {
-          values<HD, true, kTwo>(at, step, g, c, valid, pf, st.o);
+          values<HD, true, kApart, kTwo>(at, step, g, c, valid, pf, st.o);
         } else {
-          values<HD, false, kTwo>(at, step, g, c, valid, pf, st.o);
+          values<HD, false, kApart, kTwo>(at, step, g, c, valid, pf, st.o);
           if (odd) st.poison(at, step, t0, valid, g);
         }
       }
@@ -591,15 +601,15 @@ __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
 // memory lanes of its own, so the softmax has no shuffles.  Four more expand every page once for all columns (a
 // thread 64 key codes and 32 values of two positions; its codes wait in registers while the page before is used),
 // and a ninth issues the products, so that expanding, exponentials and products overlap.  The two blocks of an SM
-// share its tensor memory.  fp32 queries are two fp16 terms, and so are their weights: the products run twice,
-// into the same sums, the small terms first.  The tensor core cuts every sum off at its last bit, a few 1e-8 each, in
+// share its tensor memory.  Weights are two fp16 terms, and so are fp32 queries: their products run twice, into the same
+// sums, the small terms first.  The tensor core cuts every sum off at its last bit, a few 1e-8 each, in
 // one direction; so with fp32 queries a page's output starts at zero, and the threads of its rows add it to the one so
-// far, which has tensor memory of its own (pieces of prompts over up to 3000 positions: 2.7e-6 off 64 bits
-// without, 2.7e-7 with, 83 us and 84 at head size 128, 56 and 61 at 64).
+// far, which has tensor memory of its own (pieces of prompts over up to 3000 positions: 2.7e-6 off 64 bits without,
+// 2.7e-7 with, for 1 to 10 % of the time).
 // Operands lie in the 128-byte-swizzled layout; the elements of eight key codes in the order 0 4 1 5 2 6 3 7,
 // queries alike.
-// 512 bf16 rows over 30000 positions: 377 us, 670 TFLOP/s (fp32 724); five pieces of prompts (874 rows over up to 42
-// pages): 54 us, with the joining, 63 where the cache is not in L2.  Bound by a page's chain of scores, exponentials (one
+// 512 bf16 rows over 30000 positions: 397 us, 640 TFLOP/s (fp32 705); five pieces of prompts (874 rows over up to 42
+// pages): 57 us, with the joining, 66 where the cache is not in L2.  Bound by a page's chain of scores, exponentials (one
 // thread a column) and output.
 constexpr int kTcCols = 128;
 template <int HD, int TN>
@@ -630,6 +640,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+// (complete after tmem_st_wait)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -825,11 +843,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
           tc_fence_after();
           const uint32_t tp = tm + M::kS + (o & 1) * kPage;
 #pragma unroll
-          for (int t = TN - 1; t >= 0; --t)
+          for (int t = 1; t >= 0; --t)
 #pragma unroll
             for (int k = 0; k < kPage / 16; ++k)
               tc_mma_tmem_a(tm + M::kO, tp + t * 32 + k * 8, desc_sw128(smem_u32(sm + M::kV) + o % 3 * M::kVBuf + k * 32),
-                            idesc_f16(kTcCols, HD), (!kApart && o > 0) || t < TN - 1 || k > 0);
+                            idesc_f16(kTcCols, HD), (!kApart && o > 0) || t < 1 || k > 0);
           tc_commit(summed + (o & 1));
         }
         if (end) break;
@@ -1005,25 +1023,28 @@ __global__ void __maxnreg__(sizeof(T) == 4 && HD == 128 ? 168 : 96) k_kv4_tc(con
           if (!ok) break;
         }
       }
-      float sum[4] = {};
-      uint32_t w[32];
+      float2 sum[2] = {};
+      const float2 f2 = make_float2(factor, factor), lift2 = make_float2(lift, lift), minus = make_float2(-1.f, -1.f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        s[i] = ex2(__fmaf_rn(s[i], factor, lift));
-        s[i + 32] = ex2(__fmaf_rn(s[i + 32], factor, lift));
-        sum[i % 4] += s[i] + s[i + 32];
-        w[i] = h2_bits(__floats2half2_rn(s[i], s[i + 32]));
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32(tscore, w);
-      if constexpr (TN == 2) {
+      for (int c = 0; c < 32; c += 8) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 h = __half22float2(bits_h2(w[i]));
-          w[i] = h2_bits(__floats2half2_rn(s[i] - h.x, s[i + 32] - h.y));
+        for (int i = 0; i < 8; i += 2) {
+          float2 e0 = __ffma2_rn(make_float2(s[c + i], s[c + i + 1]), f2, lift2);
+          float2 e1 = __ffma2_rn(make_float2(s[c + i + 32], s[c + i + 33]), f2, lift2);
+          e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
+          sum[i / 2 % 2] = __fadd2_rn(sum[i / 2 % 2], __fadd2_rn(e0, e1));
+          const __half2 h0 = __floats2half2_rn(e0.x, e1.x), h1 = __floats2half2_rn(e0.y, e1.y);
+          const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
+          hi[i] = h2_bits(h0), hi[i + 1] = h2_bits(h1);
+          const float2 r0 = __ffma2_rn(make_float2(g0.x, g1.x), minus, e0), r1 = __ffma2_rn(make_float2(g0.y, g1.y), minus, e1);
+          lo[i] = h2_bits(__floats2half2_rn(r0.x, r1.x)), lo[i + 1] = h2_bits(__floats2half2_rn(r0.y, r1.y));
         }
-        tmem_st32(tscore + 32, w);
+        tmem_st8(tscore + c, hi);
+        tmem_st8(tscore + 32 + c, lo);
       }
+      l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+      tmem_st_wait();
       if (kApart && n > 0) {
         carry();
         if (!ok) break;
@@ -1157,28 +1178,28 @@ __global__ void __launch_bounds__(256) k_kv4_join_few(const AttnArgs a) {
 // average (rows times query heads of a KV head; fp32 queries count twice, and there it is 40).  32 query heads on 8, us
 // of the kernel for few and of that for many:
 //   sequences x positions      8 x 4000    1 x 30000   32 x 1000   8 x 200
-//   bf16 hd 128, 16 columns    36.5 33.7   38.1 32.5   30.4 39.1   12.7 11.1
-//                24            45.4 34.3   45.9 32.8   43.5 39.8   14.8 11.1
-//   bf16 hd 64,  16            23.4 25.9   25.0 25.8   22.1 30.3    8.6  9.0
-//                24            27.5 26.3   29.9 26.2   25.8 30.5    9.4  9.0
-//   fp32 hd 128, 32            50.2 62.0   45.1 58.5   48.4 73.5   13.5 12.7
-//                48            69.0 63.1   63.1 59.4   71.7 75.4   19.0 13.5
-//   fp32 hd 64,  32            30.8 40.1   29.1 37.8   29.1 44.9    8.6 11.1
-//                48            42.2 40.4   40.2 38.9   41.8 45.9   10.2 11.1
+//   bf16 hd 128, 16 columns    38.5 35.9   40.6 34.4   32.4 33.4   13.1 11.5
+//                24            48.3 36.5   49.2 34.8   46.6 33.6   15.0 11.9
+//   bf16 hd 64,  16            22.2 29.1   26.2 28.4   20.1 27.1    8.6  9.5
+//                24            30.3 29.5   31.5 28.8   28.7 27.5    9.7  9.9
+//   fp32 hd 128, 32            50.2 60.2   45.1 57.0   48.4 59.0   13.5 12.3
+//                48            69.0 61.1   63.2 57.8   71.7 59.8   19.1 13.5
+//   fp32 hd 64,  32            30.8 35.0   29.1 33.2   29.1 33.2    8.6 10.3
+//                48            42.2 35.3   40.2 34.0   41.8 33.3   10.2 10.6
 // Splits, of at least two pages (an even number: they are taken two at a time), at most 128:
 //  - few columns: the blocks that the 152 SMs hold at once (4 an SM), twice that where there are many items of what
 //    may be different lengths (32 of 512..4096: 32 us against 46);
 //  - many columns: the blocks that they hold at once (2 an SM; fp32 queries at head size 128 have one, and two rounds).
 //    Two where that gives one, there are few rounds and max_len is 32 pages or more: a sequence much longer than the
-//    others is a chain of pages by itself (five pieces, 60 rows over 42 pages and four over 20: 55 us, unsplit 63; 30 rows
-//    over 59 and four of 160 over 20: 56, 77).  Lengths are not known here, and where they are alike two splits cost more
-//    than they give, the more the shorter (8 x 100 rows over 47 pages: 96 us, unsplit 79; 5 x 200 over 32: 79, 57; 4 x 512
-//    over 8: 81, 37).  42 calls of 1 to 16 sequences, geometric means: split from 32 pages on 44.7 us, never 45.4,
-//    always 51.6.
+//    others is a chain of pages by itself (five pieces, 60 rows over 42 pages and four over 20: 56 us, unsplit 67; 30 rows
+//    over 59 and four of 160 over 20: 59, 82).  Lengths are not known here, and where they are alike two splits cost more
+//    than they give, the more the shorter (8 x 100 rows over 47 pages: 102 us, unsplit 84; 5 x 200 over 32: 82, 60; 4 x
+//    512 over 8: 82, 39).  42 calls of 1 to 16 sequences, geometric means (with one term a weight): split from 32 pages
+//    on 44.7 us, never 45.4, always 51.6.
 // The workspace is sized for the most splits that any length up to max_len can get, so that it does not shrink with
 // a larger max_len.
 struct Plan {
-  bool many;
+  bool many, pairs;
   int tiles, n_split, split_pages;
   size_t o_bytes, bytes;
 };
@@ -1186,7 +1207,8 @@ Plan plan(int n_seq, int n_rows, int n_head, int n_kv_head, int head_dim, int ma
   Plan p{};
   const long long group = n_head / n_kv_head, columns = n_rows * group * (two ? 2 : 1);
   p.many = columns > (two ? 40ll : 16ll) * n_seq;
-  const int cols = p.many ? kTcCols : two ? 4 : 8;
+  p.pairs = two || columns <= 4ll * n_seq;
+  const int cols = p.many ? kTcCols : p.pairs ? 4 : 8;
   p.tiles = static_cast<int>(std::min(n_rows * group / cols + n_seq, n_rows * ((group + cols - 1) / cols)));
   const int pages = static_cast<int>((static_cast<long long>(max_len) + kPage - 1) / kPage);
   const long long items = static_cast<long long>(p.tiles) * n_kv_head;
@@ -1214,8 +1236,17 @@ int launch(const AttnArgs& a, const Plan& p, cudaStream_t st) {
     k_kv4_tc<T, HD><<<grid, kTcThreads, smem, st>>>(a);
   } else {
     constexpr int smem = kDecodeSmem<HD>;
-    if (!allow_smem<k_kv4_decode<T, HD>, smem>()) return S2_ECUDA;
-    k_kv4_decode<T, HD><<<grid, 32 * kWarps, smem, st>>>(a);
+    auto go = [&](auto pairs) {
+      if (!allow_smem<k_kv4_decode<T, HD, decltype(pairs)::value>, smem>()) return false;
+      k_kv4_decode<T, HD, decltype(pairs)::value><<<grid, 32 * kWarps, smem, st>>>(a);
+      return true;
+    };
+    bool ok;
+    if constexpr (sizeof(T) == 4)
+      ok = go(std::true_type{});
+    else
+      ok = p.pairs ? go(std::true_type{}) : go(std::false_type{});
+    if (!ok) return S2_ECUDA;
   }
   if (p.n_split > 1) {
     cudaLaunchConfig_t cfg{};

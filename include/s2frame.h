@@ -432,8 +432,8 @@ int s2_kv4_read(const s2_kv4* cache, void* k, void* v, struct CUstream_st* strea
 
 /* Causal attention of the rows' queries over their sequences: query head h reads KV head
  * h / (n_head / n_kv_head) at positions 0 .. its own, scores scaled by `scale`.  Queries enter the
- * products as rows of s2_q4_matmul do; scores, softmax statistics and sums are fp32; a softmax weight
- * meets the values rounded to fp16 (2^-11 of it), with fp32 queries to 22 bits.  A row that sees no
+ * products as rows of s2_q4_matmul do; scores, softmax statistics and sums are fp32, and a softmax
+ * weight keeps 22 bits when it meets the values.  A row that sees no
  * position (lengths[s] short of the sequence's rows) gets zeros; what a page holds past a
  * sequence's length does not matter.  Positions on a page out of range, or past table_cols pages,
  * are not attended.  Where a wait on the device gives up (after a second or so) the results that it

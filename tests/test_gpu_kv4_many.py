@@ -186,3 +186,30 @@ def test_append_alike_on_both_sides_of_512_rows(rows):
         at = kv._gpu(table, np.asarray([0, b - a], np.int32), np.asarray([b], np.int32))
         got.append(pkg.kv4_append(qkv[a:b], two, *at, rope, hq, *w))
     assert torch.equal(one, two) and torch.equal(q, torch.cat(got))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("spans,hq,hkv,hd", [([(1, 2500), (1, 700)], 32, 8, 128), ([(1, 2500), (2, 900)], 16, 2, 64),
+                                             ([(3, 2000)], 12, 3, 128), ([(40, 2500), (100, 300)], 8, 2, 128),
+                                             ([(130, 1500)], 8, 2, 64)])
+def test_16_bit_results_are_the_rounded_ones(spans, hq, hkv, hd, dtype):
+    """Of 16-bit queries too a weight has two terms, so that a result before its rounding is some 3e-6 off at most (fp32 sums
+    on the tensor core, cut off at their last bit at each of up to 160 additions).  A result then takes the neighbour of the
+    rounded 64-bit one where that lies as near to a border between two: 0.8 * 3e-6 over steps of 2^-10.5 (fp16, in the
+    mean) or 2^-7.5, three times that since some results are small beside what they are sums of: 1 % and 0.13 %; 3 % and
+    0.5 % asked.  Weights rounded to fp16, 1.2e-4 off, gave 15 % and 2 %, and 2.4e-4 for the error of fp16 results, whose
+    rounding alone is 2^-11 / sqrt(3) * 0.735 (its mean over a binade) = 2.07e-4; 2.15e-4 asked."""
+    import dual_ar_tts_gb300 as pkg
+    q, pages, table, q_start, lengths = _made(spans, hq, hkv, hd, dtype, 31)
+    got = kv._attend(pkg, q, pages, table, q_start, lengths).cpu()
+    want = torch.empty(q.shape, dtype=torch.float64)
+    for s, (n, length) in enumerate(spans):
+        ids, rows = [int(p) for p in table[s, :-(-length // 64)]], slice(int(q_start[s]), int(q_start[s + 1]))
+        for h in range(hq):
+            k, v = [fb.get(pages[:, h // (hq // hkv)][:, None], part, ids)[0, :length] for part in range(2)]
+            want[rows, h] = fb.attention(q[rows, h], k, v, range(length - n + 1, length + 1), hd ** -0.5)[0]
+    differ = float((got != want.to(got.dtype)).float().mean())
+    assert differ <= (0.03 if dtype == "fp16" else 0.005), differ
+    if dtype == "fp16":
+        off = float((got.double() - want).norm() / want.norm())
+        assert off <= 2.15e-4, off
