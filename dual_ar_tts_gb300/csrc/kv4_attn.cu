@@ -10,8 +10,8 @@
 //      O^T[hd][8] += V^T[hd][16] P^T[16][8]
 //  - many (pieces of prompts): tcgen05, the cache expanded once for 128 columns (k_kv4_tc, below).
 // A weight of the softmax is two fp16 terms (22 bits), whose products with the values are added: rounded to one, 2^-11 of
-// it, weights made fp16 results 2.4e-4 off 64 bits, where their own rounding is 2.1e-4, and took 15 % of them (2 % of bf16
-// ones) to the neighbour of the rounded 64-bit result.  In the kernel for few a lane's two columns are then a weight's
+// it, weights made fp16 results 2.4e-4 off 64 bits, where their own rounding is 2.1e-4, and took 20 % of them (4 % of bf16
+// ones) to a neighbour of the rounded 64-bit result; now 0.3 % (0.03 %).  In the kernel for few a lane's two columns are then a weight's
 // terms, four columns a tile, which costs nothing where a sequence has no more than four; with more, eight columns a
 // tile and twice the products.  (8 x 30000 positions, four query heads a KV head: 79 us so, 85 with eight columns, 78
 // with one term; pieces of prompts 57 us, 54 with one term; 512 rows over 30000 397 and 378.)
@@ -445,8 +445,8 @@ constexpr int kDecodeSmem = std::max(kWarps * kDepth * Stage<HD>::kBytes, kWarps
 // pages, two at a time.  Each of its four warps takes half a page with its own copies in flight, so the warps never wait
 // on one another until their states are joined.  8 sequences of 30000 positions, 32 query heads on 8, hd 128: 79 us, 3.9
 // TB/s of the cache (fp32 queries 82); 32 of 512 .. 4096: 31 us.  Bound by a step's chain (scores, exponential, turned
-// weights, output) on the instructions that expand codes, 54 million a call of the first, each of which serves four query
-// heads here: sixteen warps an SM fill 67 % of the issue slots with them; the copies alone take 55 us.
+// weights, output) on the instructions that expand codes, 53 million a call of the first, each of which serves four query
+// heads here: sixteen warps an SM fill 66 % of the issue slots with them; the copies alone take 55 us.
 template <typename T, int HD, bool kTwo>
 __global__ void __launch_bounds__(128) k_kv4_decode(const AttnArgs a) {
   constexpr bool kApart = sizeof(T) == 4;
