@@ -11,10 +11,10 @@
 //  - many (pieces of prompts): tcgen05, the cache expanded once for 128 columns (k_kv4_tc, below).
 // A weight of the softmax is two fp16 terms (22 bits), whose products with the values are added: rounded to one, 2^-11 of
 // it, weights made fp16 results 2.4e-4 off 64 bits, where their own rounding is 2.1e-4, and took 20 % of them (4 % of bf16
-// ones) to a neighbour of the rounded 64-bit result; now 0.3 % (0.03 %).  In the kernel for few a lane's two columns are then a weight's
-// terms, four columns a tile, which costs nothing where a sequence has no more than four; with more, eight columns a
-// tile and twice the products.  (8 x 30000 positions, four query heads a KV head: 79 us so, 85 with eight columns, 78
-// with one term; pieces of prompts 57 us, 54 with one term; 512 rows over 30000 397 and 378.)
+// ones) to a neighbour of the rounded 64-bit result; now 0.3 % (0.03 %).  In the kernel for few a lane's two columns are
+// then a weight's terms, four columns a tile, which costs nothing where a sequence has no more than four; with more,
+// eight columns a tile and twice the products.  (8 x 30000 positions, four query heads a KV head: 79 us so, 85 with eight
+// columns, 78 with one term; pieces of prompts 57 us, 54 with one term; 512 rows over 30000 397 and 378.)
 // fp32 queries are two fp16 terms as well, a column each in the kernel for few, whose scores are added.  16-bit queries
 // are exact in fp16: each row is scaled by a power of two.  Weights are kept as 2^6 exp2(s - m), m the running maximum or
 // up to 8 (log2) below it: what falls off fp16's end is 2^-30 and less of the largest, and a maximum that rises a little
