@@ -471,6 +471,58 @@ int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* log
                      const float* bias, long long bias_stride, const uint32_t* mask, long long mask_stride,
                      float* out, struct CUstream_st* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Projections in 8-bit integers, activations and weights with a scale a row: stateless calls on caller
+ * buffers, beside those on 4-bit weights and under the same rules (nothing allocated, nothing kept,
+ * asynchronous on `stream`, capturable, the same bits for the same inputs; no workspace).  Of a layer
+ * they are: s2_rms_norm_q8, s2_q8_matmul (wqkv), s2_quantize_q8 of attention's output, s2_q8_matmul (wo),
+ * s2_rms_norm_q8 with the residual's sum, s2_q8_matmul (gate and up), s2_swiglu_q8, s2_q8_matmul (down).
+ *
+ * A row v of values becomes
+ *   step = max(max|v| / 127, 2^-126),  scale = step rounded to fp32,  code[i] = v[i] / step rounded to the
+ *   nearest whole number, ties to even: -127..127
+ * and stands for scale * code (the scale is no more than the largest number that is finite 127 times).  Codes are those of the exact quotients (of a norm and a gate, of v to
+ * 2^-44 or so), scales of norms and gates are good to a few roundings of fp32.  A row that holds
+ * something not finite, or whose values or norm come to that in fp32, gets scale NaN and codes 0, so that
+ * products with it are NaN.
+ *   codes   device int8 [rows][pitch], 16-byte aligned; pitch = cols rounded up to 16, the columns behind
+ *           cols are written as zeros
+ *   scales  device fp32 [rows]
+ * Inputs are rows of neighbouring elements, a stride (in elements, no less than their width) apart, aligned to
+ * their element size; rows that start on 16 bytes are read faster.  rows at most 2^31 - 1, cols 2^24. */
+
+/* v = x [rows][cols] of dtype: weights once, activations at each step. */
+int s2_quantize_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes, float* scales,
+                   struct CUstream_st* stream);
+
+/* out [rows][cols] of dtype, contiguous: scale * code, the product in fp32. */
+int s2_dequantize_q8(const int8_t* codes, const float* scales, long long rows, int cols, void* out, int dtype,
+                     struct CUstream_st* stream);
+
+/* v = h * weight / sqrt(mean(h^2) + eps) with h = x, or with a residual h = residual + x rounded to dtype, which is
+ * written to total.
+ *   residual  [rows][cols] of dtype, or NULL
+ *   weight    device fp32 [cols]
+ *   total     device [rows][cols] of dtype, contiguous; given with a residual and only then.  It may be x or
+ *             residual itself (where that is contiguous), but not overlap them otherwise */
+int s2_rms_norm_q8(const void* x, int dtype, long long x_stride, const void* residual, long long residual_stride,
+                   const float* weight, float eps, long long rows, int cols, void* total, int8_t* codes, float* scales,
+                   struct CUstream_st* stream);
+
+/* v[i] = silu(x[i]) * x[cols + i], silu(g) = g / (1 + exp(-g)): x [rows][2 * cols] of dtype, gate | up. */
+int s2_swiglu_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes, float* scales,
+                 struct CUstream_st* stream);
+
+/* y[i][r] = x_scales[i] * scales[r] * Σ_k x_codes[i][k] * codes[r][k] for n activation rows and m weight rows.
+ * The sum is the exact integer; it is rounded to fp32, and so is each product with a scale (x_scales first), and the
+ * result to dtype.  Codes may be -128.  A wait on the device that gives up (after a second or so) leaves NaN.
+ *   x_codes [n][k], codes [m][k]  device int8, contiguous, 16-byte aligned; k a multiple of 16, at most 2^17 - 16
+ *   x_scales [n], scales [m]      device fp32
+ *   y         device [n][m] of dtype, aligned to its element size
+ * n at most 2^21 - 32, m 2^28. */
+int s2_q8_matmul(int n, const int8_t* x_codes, const float* x_scales, const int8_t* codes, const float* scales, int m,
+                 int k, void* y, int dtype, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
