@@ -1,6 +1,6 @@
 // Rows as 8-bit integers with a scale each: the quantiser, RMSNorm with the residual's sum and the
 // feed-forward's gate with such an output, and reading back.
-//   step = max(max|v| / 127, 2^-126),   scale = fp32(step),   code_i = rint(v_i / step), ties to even
+//   step = max(max|v| / 127, 2^-126),   scale = fp32(step),   code_i = rint(v_i / step), ties (to 2^-42) to even
 //   v = x                                          (quantiser)
 //   v = h w / sqrt(mean(h^2) + eps), h = x + residual rounded to its type
 //   v = silu(x_i) x_{f+i}, silu(g) = g / (1 + exp(-g))
@@ -230,8 +230,11 @@ __device__ __forceinline__ float decide(Two v, Two most, float t) {
     most = {most.hi * s, most.lo * s};
   }
   const Two p = two_prod(254.f, v.hi), q = two_prod(b, most.hi);
-  const float d = __fadd_rn(__fsub_rn(p.hi, q.hi), __fadd_rn(__fsub_rn(p.lo, q.lo), __fmaf_rn(254.f, v.lo, -b * most.lo)));
-  if (d == 0.f) return 2.f * rintf(0.5f * (l + 0.5f));  // the even one
+  const float d = __fadd_rn(__fsub_rn(p.hi, q.hi),
+                            __fadd_rn(__fsub_rn(p.lo, q.lo), __fsub_rn(__fmul_rn(254.f, v.lo), __fmul_rn(b, most.lo))));
+  // A half, to what these sums are good to: halves are met in earnest (elements of 16 bits with the gate, or the norm's
+  // weight, of their row's largest), and a quotient of 24-bit numbers is 2^-31 away from one if it is none.
+  if (fabsf(d) <= p.hi * 0x1p-42f) return 2.f * rintf(0.5f * (l + 0.5f));  // the even one
   return d > 0.f ? l + 1.f : l;
 }
 

@@ -63,6 +63,24 @@ def test_quantise_halves(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(eb.TYPES))
+def test_halves_of_norm_and_gate(dtype):
+    """Elements that share their row's largest one's weight or gate: quotients that are exact halves go to the even code."""
+    import dual_ar_tts_gb300 as pkg
+    dt = eb.TYPES[dtype]
+    half = torch.arange(-126.5, 127.0, 1.0, dtype=torch.float64)
+    x = (torch.cat([half, torch.tensor([127.0])]) / 16).to(dt)
+    x = torch.stack([x, -x, x.flip(0)])                  # bf16 rounds the larger halves
+    want = torch.round(x.double() * 16).long()
+    for weight in (1.0, 1.1, 0.3, 7e-3):
+        w = torch.full((255,), weight, device="cuda")
+        assert torch.equal(pkg.rms_norm_q8(x.cuda(), w)[0].cpu()[:, :255].long(), want)
+    for gate in (2.296875, -1.3, 0.1, 11.0, -20.5, 61.0):
+        g = torch.full((3, 255), gate).to(dt)
+        codes = pkg.swiglu_q8(torch.cat([g, x], 1).cuda())[0]
+        assert torch.equal(codes.cpu()[:, :255].long(), want * (1 if gate > 0 else -1)), gate
+
+
+@pytest.mark.parametrize("dtype", list(eb.TYPES))
 @pytest.mark.parametrize("cols", [40, 1300])
 def test_quantise_extremes(cols, dtype):
     """The type's largest and smallest numbers; rows with an infinity or a NaN stand for NaN and leave others alone."""
