@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "convert.cuh"
 #include "ptx.cuh"
@@ -119,39 +120,87 @@ __device__ __noinline__ Two gate_exactly(float g, float u) {
 
 // ------------------------------------------------------------------- the rows' values
 
-// eight elements of a row from column c on, zeros past the last
+// eight elements as they lie in memory
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int cols, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    uint4 raw[sizeof(T) / 2];
+struct Eight {
+  uint32_t w[2 * sizeof(T)];
+  // of columns c .. c + 7, zeros past the last
+  __device__ __forceinline__ void load(const T* row, int c, int cols, bool vec) {
+    if (vec && c + 8 <= cols) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) raw[i] = *(reinterpret_cast<const uint4*>(row + c) + i);
-    const T* e = reinterpret_cast<const T*>(raw);
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+        const uint4 u = *(reinterpret_cast<const uint4*>(row + c) + i);
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f(e[i]);
-  } else {
+      for (int i = 0; i < 8; ++i) w[i] = c + i < cols ? __float_as_uint(row[c + i]) : 0u;
+    } else {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f(row[c + i]) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = c + 2 * i < cols ? e[c + 2 * i] : 0u, hi = c + 2 * i + 1 < cols ? e[c + 2 * i + 1] : 0u;
+        w[i] = lo | hi << 16;
+      }
+    }
   }
-}
-template <typename T>
-__device__ __forceinline__ void save8(T* row, int c, int cols, bool vec, const float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    uint4 raw[sizeof(T) / 2];
-    T* e = reinterpret_cast<T*>(raw);
+  __device__ __forceinline__ void store(T* row, int c, int cols, bool vec) const {
+    if (vec && c + 8 <= cols) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        *(reinterpret_cast<uint4*>(row + c) + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) *(reinterpret_cast<uint4*>(row + c) + i) = raw[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) row[c + i] = from_f<T>(v[i]);
+      for (int i = 0; i < 8; ++i) {
+        if (c + i >= cols) break;
+        if constexpr (sizeof(T) == 4)
+          row[c + i] = __uint_as_float(w[i]);
+        else
+          reinterpret_cast<uint16_t*>(row)[c + i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+      }
+    }
   }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+        v[i] = i % 2 ? f.y : f.x;
+      } else {
+        v[i] = i % 2 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {  // rounded to T
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+        }
+      }
+    }
+  }
+};
+
+// maximum of which a NaN is one
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 template <typename T, Op kOp>
 struct Row {
+  static constexpr bool kTwo = kOp == kGate || kOp == kNormResidual, kNorms = kOp == kNorm || kOp == kNormResidual;
   const T* x;
   const T* residual;
   T* total;
@@ -164,40 +213,70 @@ struct Row {
         total(static_cast<T*>(a.total) + (kOp == kNormResidual ? row * a.cols : 0)),
         weight(a.weight), cols(a.cols), vec(a.vec) {}
 
-  // Values of columns c .. c + 7 (of a norm h f w g, without its row's factor), and the sum of the squares of h f.  The first
-  // time the residual's sum is made and written; after that it is read, so it may have overwritten what it came from.
-  template <bool kFirst>
-  __device__ __forceinline__ void values(int c, float f, float g, float (&v)[8], float& squares) const {
+  // What eight values are made of: loaded first, for all that a thread holds.
+  struct In {
+    Eight<T> x;
+    std::conditional_t<kTwo, Eight<T>, uint32_t> other;
+    std::conditional_t<kNorms, Eight<float>, uint32_t> weight;
+  };
+  __device__ __forceinline__ void load(int c, In& in) const {
+    in.x.load(x, c, cols, vec);
+    if constexpr (kOp == kGate) in.other.load(x + cols, c, cols, vec);
+    if constexpr (kOp == kNormResidual) in.other.load(residual, c, cols, vec);
+    if constexpr (kNorms) in.weight.load(weight, c, cols, vec);
+  }
+  // Values of columns c .. c + 7 (of a norm h w, without its row's factor), and the sum of the squares of h.  The residual's
+  // sum is written, and read from there when values are made again: it may have overwritten what it came from.
+  __device__ __forceinline__ void values(int c, In& in, float (&v)[8], float& squares) const {
+    in.x.get(v);
     if constexpr (kOp == kGate) {
       float u[8];
-      load8(x, c, cols, vec, v);
-      load8(x + cols, c, cols, vec, u);
+      in.other.get(u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float e = expf(-fabsf(v[i])), s = __fdividef(v[i], 1.f + e);
         v[i] = (v[i] >= 0.f ? s : s * e) * u[i];
       }
-    } else if constexpr (kOp == kQuantize) {
-      load8(x, c, cols, vec, v);
-    } else {
-      if constexpr (kOp == kNormResidual && kFirst) {
-        float d[8];
-        load8(x, c, cols, vec, d);
-        load8(residual, c, cols, vec, v);
+    }
+    if constexpr (kOp == kNormResidual) {
+      float r[8];
+      in.other.get(r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f(from_f<T>(v[i] + d[i]));
-        save8(total, c, cols, vec, v);
-      } else {
-        load8(kOp == kNormResidual ? total : x, c, cols, vec, v);
-      }
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
+      in.x.set(v);
+      in.x.store(total, c, cols, vec);
+      in.x.get(v);
+    }
+    if constexpr (kNorms) {
       float w[8];
-      load8(weight, c, cols, vec, w);
+      in.weight.get(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = v[i] * f;
-        squares = __fmaf_rn(h, h, squares);
-        v[i] = __fmul_rn(h, w[i] * g);
+        squares = __fmaf_rn(v[i], v[i], squares);
+        v[i] = __fmul_rn(v[i], w[i]);
       }
+    }
+  }
+  // The same once more, of h f and w g.
+  __device__ __forceinline__ void again(int c, float f, float g, float (&v)[8], float& squares) const {
+    if constexpr (kNorms) {
+      Eight<T> h;
+      Eight<float> weights;
+      h.load(kOp == kNormResidual ? total : x, c, cols, vec);
+      weights.load(weight, c, cols, vec);
+      float w[8];
+      h.get(v);
+      weights.get(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * f;
+        squares = __fmaf_rn(t, t, squares);
+        v[i] = __fmul_rn(t, w[i] * g);
+      }
+    } else {
+      In in;
+      load(c, in);
+      values(c, in, v, squares);
     }
   }
 
@@ -215,11 +294,12 @@ struct Row {
   }
 };
 
-// Elements nearer to a border than this are decided exactly.  t = v * (127 / peak) is off by at most 127 times the
-// roundings in it, 2^-24 each: two (quantiser), four (norm), sixteen (gate, where expf and the division are good to two last
-// places, four of them, and exp(-|g|) enters twice): 1.5e-5, 3.1e-5, 1.22e-4.
-template <Op kOp>
-constexpr float kMargin = kOp == kQuantize ? 0x1p-15f : kOp == kGate ? 0x1.2p-13f : 0x1p-14f;
+// Elements nearer to a border than this are decided exactly.  v * (127 / most) is off by at most 127 times the roundings in
+// v, most and their quotient, 2^-24 each: one (quantiser; 7.6e-6), three (norm; 2.3e-5), and, expf and the division good to
+// two last places, four roundings, and exp(-|g|) there twice, thirteen each in v and most (gate; 2.1e-4) or, where most is known
+// better, fourteen (1.1e-4).
+template <Op kOp, bool kPeakFirst>
+constexpr float kMargin = kOp == kQuantize ? 0x1p-16f : kOp == kGate ? (kPeakFirst ? 0x1p-13f : 0x1p-12f) : 0x1p-15f;
 
 // The magnitude's code where t, its quotient in fp32, lies next to a border: 254 v against (2 l + 1) most.
 __device__ __forceinline__ float decide(Two v, Two most, float t) {
@@ -238,29 +318,6 @@ __device__ __forceinline__ float decide(Two v, Two most, float t) {
   return d > 0.f ? l + 1.f : l;
 }
 
-// For one-warp rows and one-block rows
-template <bool kBlock>
-__device__ __forceinline__ uint32_t most_of(uint32_t v, uint32_t* shared) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if constexpr (kBlock) {
-    if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-    __syncthreads();
-    const int lane = threadIdx.x % 32;
-    v = __reduce_max_sync(0xffffffffu, lane < static_cast<int>(blockDim.x / 32) ? shared[lane] : 0u);
-  }
-  return v;
-}
-template <bool kBlock>
-__device__ __forceinline__ float sum_of(float v, float* shared) {  // in a fixed order
-  v = warp_sum(v);
-  if constexpr (kBlock) {
-    if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-    __syncthreads();
-    const int lane = threadIdx.x % 32;
-    v = warp_sum(lane < static_cast<int>(blockDim.x / 32) ? shared[lane] : 0.f);
-  }
-  return v;
-}
 // hi + lo in the order of their sizes (hi >= 0)
 __device__ __forceinline__ unsigned long long ordered(Two v) {
   const uint32_t l = __float_as_uint(v.lo);
@@ -271,69 +328,105 @@ __device__ __forceinline__ Two from_ordered(unsigned long long k) {
   return {__uint_as_float(static_cast<uint32_t>(k >> 32)), __uint_as_float(l & 0x80000000u ? l & 0x7fffffffu : ~l)};
 }
 
-// A row is a warp's (up to kHeld * 256 columns) or a block's.  A thread holds kHeld times eight elements; what lies
-// past them is computed again for its codes.
-template <typename T, Op kOp, int kHeld, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) k_q8_rows(const RowArgs a) {
-  __shared__ uint32_t shared_most[32];
-  __shared__ float shared_sum[32];
-  __shared__ unsigned long long shared_exact[kBlock ? 1 : 8];
-  constexpr bool kNorms = kOp == kNorm || kOp == kNormResidual;
-  const int team = kBlock ? blockDim.x : 32, me = kBlock ? threadIdx.x : threadIdx.x % 32;
-  const long long row = kBlock ? blockIdx.x : static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (!kBlock && row >= a.rows) return;
-  unsigned long long* exact = shared_exact + (kBlock ? 0 : threadIdx.x / 32);
-  if (me == 0) *exact = 0;
-  if constexpr (!kBlock) __syncwarp();
-  const Row<T, kOp> in(a, row);
+// A row is a team's: 8 or 32 lanes of a warp, or a block.  Reductions are in a fixed order.
+template <int kTeam>  // 0: the block
+struct Team {
+  __device__ static __forceinline__ unsigned mask() {
+    return kTeam == 8 ? 0xffu << (threadIdx.x & 24u) : 0xffffffffu;
+  }
+  // the largest of a magnitude (infinities and NaN are the largest) and the sum of s
+  template <bool kSum>
+  __device__ static __forceinline__ void reduce(float& most, float& s, float2* shared) {
+    constexpr int kLanes = kTeam == 8 ? 8 : 32;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      if constexpr (kTeam == 8) most = max_nan(most, __shfl_xor_sync(mask(), most, o));
+      if constexpr (kSum) s += __shfl_xor_sync(mask(), s, o);
+    }
+    if constexpr (kTeam != 8) most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if constexpr (kTeam == 0) {
+      const int lane = threadIdx.x % 32;
+      if (lane == 0) shared[threadIdx.x / 32] = make_float2(most, s);
+      __syncthreads();
+      const float2 t = lane < static_cast<int>(blockDim.x / 32) ? shared[lane] : make_float2(0.f, 0.f);
+      most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t.x)));
+      if constexpr (kSum) s = warp_sum(t.y);
+    }
+  }
+};
+
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
+
+template <typename T, Op kOp, int kHeld, int kTeam, int kThreads>
+__global__ void __launch_bounds__(kThreads) k_q8_rows(const RowArgs a) {
+  __shared__ float2 shared[2][kTeam == 0 ? 32 : 1];
+  __shared__ unsigned long long exact[kTeam == 0 ? 1 : kThreads / kTeam];
+  using R = Row<T, kOp>;
+  constexpr bool kNorms = R::kNorms;
+  // Whether the largest magnitude is made exact before any code: a block's rows are long, and an element next to a border is
+  // then a common thing; a short row has none more often than not.
+  constexpr bool kPeakFirst = kTeam == 0 && kOp != kQuantize;
+  const int team = kTeam == 0 ? blockDim.x : kTeam, me = kTeam == 0 ? threadIdx.x : threadIdx.x % kTeam;
+  const long long row = kTeam == 0 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTeam;
+  if (kTeam != 0 && row >= a.rows) return;
+  unsigned long long* const largest_key = exact + (kTeam == 0 ? 0 : threadIdx.x / kTeam);
+  if (kPeakFirst && me == 0) *largest_key = 0;
+  const R in(a, row);
 
   float held[kHeld][8];
-  float f = 1.f, g = 1.f, squares = 0.f;
-  uint32_t top = 0;  // bits of the largest magnitude; infinities and NaN are the largest
+  float f = 1.f, g = 1.f, squares = 0.f, most = 0.f;
   auto look = [&](const float(&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(v[i]));
   };
+  {
+    typename R::In raw[kHeld];
 #pragma unroll
-  for (int h = 0; h < kHeld; ++h) {
-    const int c = (h * team + me) * 8;
+    for (int h = 0; h < kHeld; ++h) {
+      const int c = (h * team + me) * 8;
+      if (c < a.cols) in.load(c, raw[h]);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) held[h][i] = 0.f;
-    if (c < a.cols) in.template values<true>(c, f, g, held[h], squares);
-    look(held[h]);
+    for (int h = 0; h < kHeld; ++h) {
+      const int c = (h * team + me) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) held[h][i] = 0.f;
+      if (c < a.cols) in.values(c, raw[h], held[h], squares);
+      look(held[h]);
+    }
   }
-  for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {
+#pragma unroll 1
+  for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {  // what a thread does not hold is made again for its codes
     float v[8];
-    in.template values<true>(c, f, g, v, squares);
+    typename R::In raw;
+    in.load(c, raw);
+    in.values(c, raw, v, squares);
     look(v);
   }
-  top = most_of<kBlock>(top, shared_most);
+  Team<kTeam>::template reduce<kNorms>(most, squares, shared[0]);
   float r = 1.f;
   if constexpr (kNorms) {
-    float sum = sum_of<kBlock>(squares, shared_sum);
-    if (top == 0x7f800000u || isinf(sum)) {  // perhaps only past fp32's range: once more with what is too large times 2^-80
-      if (isinf(sum)) f = 0x1p-80f;
-      if (top == 0x7f800000u) g = 0x1p-80f;
-      squares = 0.f, top = 0;
+    if (isinf(most) || isinf(squares)) {  // perhaps only past fp32's range: once more with what is too large times 2^-80
+      if (isinf(squares)) f = 0x1p-80f;
+      if (isinf(most)) g = 0x1p-80f;
+      squares = most = 0.f;
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
         const int c = (h * team + me) * 8;
-        if (c < a.cols) in.template values<false>(c, f, g, held[h], squares);
+        if (c < a.cols) in.again(c, f, g, held[h], squares);
         look(held[h]);
       }
+#pragma unroll 1
       for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {
         float v[8];
-        in.template values<false>(c, f, g, v, squares);
+        in.again(c, f, g, v, squares);
         look(v);
       }
-      if constexpr (kBlock) __syncthreads();
-      top = most_of<kBlock>(top, shared_most);
-      sum = sum_of<kBlock>(squares, shared_sum);
+      Team<kTeam>::template reduce<kNorms>(most, squares, shared[1]);
     }
     // 1 / f times the row's factor
-    r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.cols)), a.eps * f * f)));
+    r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), a.eps * f * f)));
   }
-  const float most = __uint_as_float(top);
   const float largest = most * r * (g == 1.f ? 1.f : 0x1p80f);
   int8_t* codes = a.codes + row * a.pitch;
   if (!(largest <= 3.4028234663852886e38f)) {  // not finite
@@ -345,93 +438,134 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_q8_rows(const RowArgs a
   const bool tiny = step < 0x1p-126f;  // the quotient is v 2^126 then
   if (tiny) step = 0x1p-126f;
   if (me == 0) a.scales[row] = step;
+  if (kNorms && tiny) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) held[h][i] *= r;
+  }
 
-  // the largest magnitude to more than fp32
+  // The largest magnitude to more than fp32: of what comes near to it, the largest.
   Two peak{most, 0.f};
-  if constexpr (kOp != kQuantize) {
-    if (!tiny) {
+  auto find_peak = [&] {
+    if constexpr (kOp != kQuantize) {
       const float near = most * (1.f - 0x1p-18f);
+      unsigned long long key = 0;
       auto candidates = [&](const float(&v)[8], int c) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+        if (m < near) return;
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           float one = v[0];
 #pragma unroll
           for (int j = 1; j < 8; ++j) one = i == j ? v[j] : one;
-          if (fabsf(one) >= near) atomicMax(exact, ordered(in.exactly(c + i, f, g)));
+          if (fabsf(one) >= near) key = max(key, ordered(in.exactly(c + i, f, g)));
         }
       };
-      auto any = [&](const float(&v)[8]) {
-        float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-        return m >= near;
-      };
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h)
-        if (any(held[h])) candidates(held[h], (h * team + me) * 8);
+      for (int h = 0; h < kHeld; ++h) candidates(held[h], (h * team + me) * 8);
+#pragma unroll 1
       for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {
         float v[8], unused = 0.f;
-        in.template values<false>(c, f, g, v, unused);
-        if (any(v)) candidates(v, c);
+        in.again(c, f, g, v, unused);
+        candidates(v, c);
       }
+      if constexpr (kTeam == 0) {
+        if (key) atomicMax(largest_key, key);
+        __syncthreads();
+        key = *reinterpret_cast<volatile unsigned long long*>(largest_key);
+      } else {
+#pragma unroll
+        for (int o = kTeam / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(Team<kTeam>::mask(), key, o));
+      }
+      peak = from_ordered(key);
     }
-    if constexpr (kBlock)
-      __syncthreads();
-    else
-      __syncwarp();
-    if (!tiny) peak = from_ordered(*reinterpret_cast<volatile unsigned long long*>(exact));
+  };
+  if constexpr (kPeakFirst) {
+    if (!tiny) find_peak();  // the block's threads agree on that
   }
-
   const float inverse = tiny ? 0x1p126f : __fdiv_rn(127.f, peak.hi);
+  constexpr float kNear = 0.5f - kMargin<kOp, kPeakFirst>;
+  // how far eight quotients are from whole numbers, at most
+  auto distance = [&](const float(&v)[8]) {
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d = fmaxf(d, fabsf(__fmaf_rn(v[i], inverse, -(__fmaf_rn(v[i], inverse, kMagic) - kMagic))));
+    return d;
+  };
+  if constexpr (kTeam != 0 && kOp != kQuantize) {
+    float d = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) d = fmaxf(d, distance(held[h]));
+    if (__any_sync(Team<kTeam>::mask(), d > kNear && !tiny)) find_peak();
+  }
   auto encode = [&](const float(&v)[8], int c) {
     if (c >= a.pitch) return;
-    float t[8], k[8];
-    uint32_t near = 0;
+    uint32_t k[8];  // the low byte is the code
+    float d = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      t[i] = kNorms && tiny ? v[i] * r * inverse : v[i] * inverse;
-      k[i] = rintf(t[i]);
-      near |= (fabsf(t[i] - k[i]) > 0.5f - kMargin<kOp> ? 1u : 0u) << i;
+      const float s = __fmaf_rn(v[i], inverse, kMagic);
+      k[i] = __float_as_uint(s);
+      d = fmaxf(d, fabsf(__fmaf_rn(v[i], inverse, -(s - kMagic))));
     }
-    if (near && !tiny) {
+    if (d > kNear && !tiny) {
 #pragma unroll 1
       for (int i = 0; i < 8; ++i) {
-        if (!(near >> i & 1)) continue;
-        float one = t[0];
+        float one = v[0];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) one = i == j ? t[j] : one;
-        const float code = copysignf(decide(in.exactly(c + i, f, g), peak, fabsf(one)), one);
+        for (int j = 1; j < 8; ++j) one = i == j ? v[j] : one;
+        if (fabsf(__fmaf_rn(one, inverse, -(__fmaf_rn(one, inverse, kMagic) - kMagic))) <= kNear) continue;
+        const float code = copysignf(decide(in.exactly(c + i, f, g), peak, fabsf(one * inverse)), one);
+        const uint32_t bits = __float_as_uint(code + kMagic);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) k[j] = i == j ? code : k[j];
+        for (int j = 0; j < 8; ++j) k[j] = i == j ? bits : k[j];
       }
     }
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i / 4] |= (static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(k[i], -127.f), 127.f))) & 255u) << (i % 4 * 8);
-    *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+    auto pack = [](uint32_t p, uint32_t q, uint32_t r, uint32_t t) {
+      return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(r, t, 0x0040), 0x5410);
+    };
+    *reinterpret_cast<uint2*>(codes + c) = make_uint2(pack(k[0], k[1], k[2], k[3]), pack(k[4], k[5], k[6], k[7]));
   };
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) encode(held[h], (h * team + me) * 8);
+#pragma unroll 1
   for (int c = (kHeld * team + me) * 8; c < a.pitch; c += team * 8) {
     float v[8], unused = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (c < a.cols) in.template values<false>(c, f, g, v, unused);
+    if (c < a.cols) {
+      in.again(c, f, g, v, unused);
+      if (kNorms && tiny) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= r;
+      }
+    }
     encode(v, c);
   }
 }
 
-// Rows of up to 1024 columns by a warp each, longer ones by a block whose threads hold 16 elements.
+template <typename T, Op kOp, int kHeld, int kTeam, int kThreads>
+void launch_teams(const RowArgs& a, cudaStream_t st) {
+  constexpr int per = kThreads / kTeam;
+  k_q8_rows<T, kOp, kHeld, kTeam, kThreads><<<static_cast<unsigned>((a.rows + per - 1) / per), kThreads, 0, st>>>(a);
+}
+
 template <Op kOp>
 int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.cols <= 1024) {
-      k_q8_rows<T, kOp, 4, false><<<static_cast<unsigned>((a.rows + 7) / 8), 256, 0, st>>>(a);
+    const int eights = a.pitch / 8;
+    if (a.cols <= 256 && (kOp == kQuantize || kOp == kGate)) {
+      if constexpr (kOp == kQuantize || kOp == kGate) launch_teams<T, kOp, 4, 8, 128>(a, st);
+    } else if (a.cols <= 1024) {
+      launch_teams<T, kOp, 4, 32, 128>(a, st);
+    } else if (a.cols <= 4096) {
+      k_q8_rows<T, kOp, 2, 0, 256><<<static_cast<unsigned>(a.rows), (eights + 63) / 64 * 32, 0, st>>>(a);
     } else {
-      const int threads = min(1024, (a.pitch / 8 + 63) / 64 * 32);
-      k_q8_rows<T, kOp, 2, true><<<static_cast<unsigned>(a.rows), threads, 0, st>>>(a);
+      k_q8_rows<T, kOp, 4, 0, 512><<<static_cast<unsigned>(a.rows), min(512, (eights + 127) / 128 * 32), 0, st>>>(a);
     }
   });
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
@@ -454,7 +588,9 @@ __global__ void __launch_bounds__(256) k_q8_read(const int8_t* __restrict__ code
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = s * static_cast<float>(static_cast<int8_t>(w[2 * h + e / 4] >> (e % 4 * 8)));
-    if (c + 8 * h < cols) save8(out + row * cols, c + 8 * h, cols, vec, v);
+    Eight<T> o;
+    o.set(v);
+    if (c + 8 * h < cols) o.store(out + row * cols, c + 8 * h, cols, vec);
   }
 }
 
