@@ -14,6 +14,7 @@
 // (gate) to 2^14.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -36,8 +37,7 @@ struct RowArgs {
   float* scales;
   long long x_stride, residual_stride, rows;
   int cols, pitch;  // pitch: cols rounded up to 16
-  float eps;
-  bool vec;         // rows may be read 16 bytes at a time
+  float eps, per_col;  // per_col: 1 / cols
 };
 
 // ------------------------------------------------------------- two-term numbers
@@ -123,15 +123,32 @@ __device__ __noinline__ Two gate_exactly(float g, float u) {
 // eight elements as they lie in memory
 template <typename T>
 struct Eight {
-  uint32_t w[2 * sizeof(T)];
-  // of columns c .. c + 7, zeros past the last
-  __device__ __forceinline__ void load(const T* row, int c, int cols, bool vec) {
-    if (vec && c + 8 <= cols) {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+  // Of columns c .. c + 7 of a row, zeros past the last.  Rows start anywhere: the aligned 16-byte blocks around an eight are
+  // loaded and shifted by `skew`, the bytes of the row's start past a block's (the same for all eights of a row).  The row's first
+  // and last eights, whose blocks may reach out of it, are loaded by elements.  (By elements alone: 20000 x 700 bf16 gate 60 us.)
+  __device__ __forceinline__ void load(const T* row, int c, int cols, int skew) {
+    const uint4* block = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(row + c) - skew);
+    if (skew == 0 && c + 8 <= cols) {
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
-        const uint4 u = *(reinterpret_cast<const uint4*>(row + c) + i);
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 u = block[i];
         w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
       }
+    } else if (c > 0 && c + 16 <= cols) {
+      uint32_t b[kWords + 4];
+#pragma unroll
+      for (int i = 0; i <= kWords / 4; ++i) {
+        const uint4 u = block[i];
+        b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
+      }
+#pragma unroll
+      for (int i = 0; i < kWords + 3; ++i) b[i] = skew & 4 ? b[i + 1] : b[i];
+#pragma unroll
+      for (int i = 0; i < kWords + 1; ++i) b[i] = skew & 8 ? b[i + 2] : b[i];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], skew % 4 * 8);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = c + i < cols ? __float_as_uint(row[c + i]) : 0u;
@@ -144,11 +161,16 @@ struct Eight {
       }
     }
   }
-  __device__ __forceinline__ void store(T* row, int c, int cols, bool vec) const {
-    if (vec && c + 8 <= cols) {
+  __device__ static __forceinline__ int skew_of(const T* row) { return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15); }
+  // in pieces of 16, 4 or 2 bytes
+  __device__ __forceinline__ void store(T* row, int c, int cols, int skew) const {
+    if (skew == 0 && c + 8 <= cols) {
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-        *(reinterpret_cast<uint4*>(row + c) + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(row + c)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if (skew % 4 == 0 && c + 8 <= cols) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t*>(row + c)[i] = w[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -202,16 +224,16 @@ template <typename T, Op kOp>
 struct Row {
   static constexpr bool kTwo = kOp == kGate || kOp == kNormResidual, kNorms = kOp == kNorm || kOp == kNormResidual;
   const T* x;
-  const T* residual;
+  const T* other;  // the residual, or the gate's second half
   T* total;
   const float* weight;
-  int cols;
-  bool vec;
+  int cols, skew, other_skew, total_skew, weight_skew;
   __device__ __forceinline__ Row(const RowArgs& a, long long row)
       : x(static_cast<const T*>(a.x) + row * a.x_stride),
-        residual(static_cast<const T*>(a.residual) + (kOp == kNormResidual ? row * a.residual_stride : 0)),
+        other(kOp == kGate ? x + a.cols : static_cast<const T*>(a.residual) + (kTwo ? row * a.residual_stride : 0)),
         total(static_cast<T*>(a.total) + (kOp == kNormResidual ? row * a.cols : 0)),
-        weight(a.weight), cols(a.cols), vec(a.vec) {}
+        weight(a.weight), cols(a.cols), skew(Eight<T>::skew_of(x)), other_skew(Eight<T>::skew_of(other)),
+        total_skew(Eight<T>::skew_of(total)), weight_skew(Eight<float>::skew_of(weight)) {}
 
   // What eight values are made of: loaded first, for all that a thread holds.
   struct In {
@@ -220,10 +242,9 @@ struct Row {
     std::conditional_t<kNorms, Eight<float>, uint32_t> weight;
   };
   __device__ __forceinline__ void load(int c, In& in) const {
-    in.x.load(x, c, cols, vec);
-    if constexpr (kOp == kGate) in.other.load(x + cols, c, cols, vec);
-    if constexpr (kOp == kNormResidual) in.other.load(residual, c, cols, vec);
-    if constexpr (kNorms) in.weight.load(weight, c, cols, vec);
+    in.x.load(x, c, cols, skew);
+    if constexpr (kTwo) in.other.load(other, c, cols, other_skew);
+    if constexpr (kNorms) in.weight.load(weight, c, cols, weight_skew);
   }
   // Values of columns c .. c + 7 (of a norm h w, without its row's factor), and the sum of the squares of h.  The residual's
   // sum is written, and read from there when values are made again: it may have overwritten what it came from.
@@ -244,7 +265,7 @@ struct Row {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += r[i];
       in.x.set(v);
-      in.x.store(total, c, cols, vec);
+      in.x.store(total, c, cols, total_skew);
       in.x.get(v);
     }
     if constexpr (kNorms) {
@@ -262,8 +283,11 @@ struct Row {
     if constexpr (kNorms) {
       Eight<T> h;
       Eight<float> weights;
-      h.load(kOp == kNormResidual ? total : x, c, cols, vec);
-      weights.load(weight, c, cols, vec);
+      if constexpr (kOp == kNormResidual)
+        h.load(total, c, cols, total_skew);
+      else
+        h.load(x, c, cols, skew);
+      weights.load(weight, c, cols, weight_skew);
       float w[8];
       h.get(v);
       weights.get(w);
@@ -280,24 +304,23 @@ struct Row {
     }
   }
 
-  // One column's value to 2^-44 or exactly, as its magnitude
+  // One column's value to 2^-44 or exactly
   __device__ __forceinline__ Two exactly(int c, float f, float g) const {
-    Two v;
-    if constexpr (kOp == kGate) {
-      v = gate_exactly(to_f(x[c]), to_f(x[cols + c]));
-    } else if constexpr (kOp == kQuantize) {
-      v = {to_f(x[c]), 0.f};
-    } else {
-      v = two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, __ldg(weight + c) * g);
-    }
-    return v.hi < 0.f ? Two{-v.hi, -v.lo} : v;
+    if constexpr (kOp == kGate)
+      return gate_exactly(to_f(x[c]), to_f(other[c]));
+    else if constexpr (kOp == kQuantize)
+      return {to_f(x[c]), 0.f};
+    else
+      return two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, __ldg(weight + c) * g);
   }
 };
+
+__device__ __forceinline__ Two magnitude(Two v) { return v.hi < 0.f ? Two{-v.hi, -v.lo} : v; }
 
 // Elements nearer to a border than this are decided exactly.  v * (127 / most) is off by at most 127 times the roundings in
 // v, most and their quotient, 2^-24 each: one (quantiser; 7.6e-6), three (norm; 2.3e-5), and, expf and the division good to
 // two last places, four roundings, and exp(-|g|) there twice, thirteen each in v and most (gate; 2.1e-4) or, where most is known
-// better, fourteen (1.1e-4).
+// better, fifteen (1.14e-4).
 template <Op kOp, bool kPeakFirst>
 constexpr float kMargin = kOp == kQuantize ? 0x1p-16f : kOp == kGate ? (kPeakFirst ? 0x1p-13f : 0x1p-12f) : 0x1p-15f;
 
@@ -357,22 +380,22 @@ struct Team {
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
 
-template <typename T, Op kOp, int kHeld, int kTeam, int kThreads>
-__global__ void __launch_bounds__(kThreads) k_q8_rows(const RowArgs a) {
+// A thread holds kHeld times eight elements; what lies past them is made again for its codes.
+template <typename T, Op kOp, int kHeld, int kTeam, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) {
   __shared__ float2 shared[2][kTeam == 0 ? 32 : 1];
-  __shared__ unsigned long long exact[kTeam == 0 ? 1 : kThreads / kTeam];
+  __shared__ unsigned long long exact;
   using R = Row<T, kOp>;
   constexpr bool kNorms = R::kNorms;
-  // Whether the largest magnitude is made exact before any code: a block's rows are long, and an element next to a border is
-  // then a common thing; a short row has none more often than not.
-  constexpr bool kPeakFirst = kTeam == 0 && kOp != kQuantize;
+  // Whether the largest magnitude is made exact before any code: a gate's long row has an element next to a border more often
+  // than not, others have none.
+  constexpr bool kPeakFirst = kTeam == 0 && kOp == kGate;
   const int team = kTeam == 0 ? blockDim.x : kTeam, me = kTeam == 0 ? threadIdx.x : threadIdx.x % kTeam;
   const long long row = kTeam == 0 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTeam;
   if (kTeam != 0 && row >= a.rows) return;
-  unsigned long long* const largest_key = exact + (kTeam == 0 ? 0 : threadIdx.x / kTeam);
-  if (kPeakFirst && me == 0) *largest_key = 0;
+  if (kTeam == 0 && me == 0) exact = 0;
   const R in(a, row);
-
+  auto column = [&](int h) { return (h * team + me) * 8; };
   float held[kHeld][8];
   float f = 1.f, g = 1.f, squares = 0.f, most = 0.f;
   auto look = [&](const float(&v)[8]) {
@@ -382,21 +405,20 @@ __global__ void __launch_bounds__(kThreads) k_q8_rows(const RowArgs a) {
   {
     typename R::In raw[kHeld];
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-      const int c = (h * team + me) * 8;
-      if (c < a.cols) in.load(c, raw[h]);
-    }
+    for (int h = 0; h < kHeld; ++h)
+      if (column(h) < a.cols) in.load(column(h), raw[h]);
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-      const int c = (h * team + me) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) held[h][i] = 0.f;
-      if (c < a.cols) in.values(c, raw[h], held[h], squares);
-      look(held[h]);
+      if (column(h) < a.cols) {
+        in.values(column(h), raw[h], held[h], squares);
+        look(held[h]);
+      }
     }
   }
 #pragma unroll 1
-  for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {  // what a thread does not hold is made again for its codes
+  for (int c = column(kHeld); c < a.cols; c += team * 8) {
     float v[8];
     typename R::In raw;
     in.load(c, raw);
@@ -404,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) k_q8_rows(const RowArgs a) {
     look(v);
   }
   Team<kTeam>::template reduce<kNorms>(most, squares, shared[0]);
-  float r = 1.f;
+  float r = 1.f;  // of a norm, 1 / f times the row's factor, to a few last places
   if constexpr (kNorms) {
     if (isinf(most) || isinf(squares)) {  // perhaps only past fp32's range: once more with what is too large times 2^-80
       if (isinf(squares)) f = 0x1p-80f;
@@ -412,186 +434,194 @@ __global__ void __launch_bounds__(kThreads) k_q8_rows(const RowArgs a) {
       squares = most = 0.f;
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
-        const int c = (h * team + me) * 8;
-        if (c < a.cols) in.again(c, f, g, held[h], squares);
+        if (column(h) < a.cols) in.again(column(h), f, g, held[h], squares);
         look(held[h]);
       }
 #pragma unroll 1
-      for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {
+      for (int c = column(kHeld); c < a.cols; c += team * 8) {
         float v[8];
         in.again(c, f, g, v, squares);
         look(v);
       }
       Team<kTeam>::template reduce<kNorms>(most, squares, shared[1]);
     }
-    // 1 / f times the row's factor
-    r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), a.eps * f * f)));
+    r = rsqrtf(__fmaf_rn(squares, a.per_col, a.eps * f * f));
   }
-  const float largest = most * r * (g == 1.f ? 1.f : 0x1p80f);
+  const float back = g == 1.f ? 1.f : 0x1p80f;
   int8_t* codes = a.codes + row * a.pitch;
-  if (!(largest <= 3.4028234663852886e38f)) {  // not finite
+  if (!(most * r * back <= 3.4028234663852886e38f)) {  // not finite
     for (int c = me * 8; c < a.pitch; c += team * 8) *reinterpret_cast<uint2*>(codes + c) = make_uint2(0, 0);
     if (me == 0) a.scales[row] = __uint_as_float(0x7fc00000u);
     return;
   }
-  float step = fminf(__fdiv_rn(largest, 127.f), 0x1.020406p+121f);  // what 127 times is finite
-  const bool tiny = step < 0x1p-126f;  // the quotient is v 2^126 then
-  if (tiny) step = 0x1p-126f;
-  if (me == 0) a.scales[row] = step;
+  const bool tiny = most * r * back < 127 * 0x1p-126f;  // the step is its least, the quotient is v 2^126
+  const float early = r;
+  if (me == 0) {
+    if (kNorms) r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), a.eps * f * f)));
+    // at most what 127 times is finite
+    a.scales[row] = fminf(fmaxf(__fdiv_rn(most * r * back, 127.f), 0x1p-126f), 0x1.020406p+121f);
+  }
   if (kNorms && tiny) {
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) held[h][i] *= r;
+      for (int i = 0; i < 8; ++i) held[h][i] *= early;
   }
 
   // The largest magnitude to more than fp32: of what comes near to it, the largest.
   Two peak{most, 0.f};
   auto find_peak = [&] {
-    if constexpr (kOp != kQuantize) {
-      const float near = most * (1.f - 0x1p-18f);
-      unsigned long long key = 0;
-      auto candidates = [&](const float(&v)[8], int c) {
-        float m = 0.f;
+    const float near = most * (1.f - 0x1p-18f);
+    unsigned long long key = 0;
+    uint32_t mask = 0;  // bit 8 h + i
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-        if (m < near) return;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          float one = v[0];
+    for (int h = 0; h < kHeld; ++h)
 #pragma unroll
-          for (int j = 1; j < 8; ++j) one = i == j ? v[j] : one;
-          if (fabsf(one) >= near) key = max(key, ordered(in.exactly(c + i, f, g)));
-        }
-      };
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h) candidates(held[h], (h * team + me) * 8);
-#pragma unroll 1
-      for (int c = (kHeld * team + me) * 8; c < a.cols; c += team * 8) {
-        float v[8], unused = 0.f;
-        in.again(c, f, g, v, unused);
-        candidates(v, c);
-      }
-      if constexpr (kTeam == 0) {
-        if (key) atomicMax(largest_key, key);
-        __syncthreads();
-        key = *reinterpret_cast<volatile unsigned long long*>(largest_key);
-      } else {
-#pragma unroll
-        for (int o = kTeam / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(Team<kTeam>::mask(), key, o));
-      }
-      peak = from_ordered(key);
+      for (int i = 0; i < 8; ++i) mask |= (fabsf(held[h][i]) >= near ? 1u : 0u) << (8 * h + i);
+    for (; mask; mask &= mask - 1) {
+      const int i = __ffs(mask) - 1;
+      key = max(key, ordered(magnitude(in.exactly(column(i / 8) + i % 8, f, g))));
     }
+#pragma unroll 1
+    for (int c = column(kHeld); c < a.cols; c += team * 8) {
+      float v[8], unused = 0.f;
+      in.again(c, f, g, v, unused);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mask |= (fabsf(v[i]) >= near ? 1u : 0u) << i;
+      for (; mask; mask &= mask - 1) key = max(key, ordered(magnitude(in.exactly(c + __ffs(mask) - 1, f, g))));
+    }
+    if constexpr (kTeam == 0) {
+      if (key) atomicMax(&exact, key);
+      __syncthreads();
+      key = *reinterpret_cast<volatile unsigned long long*>(&exact);
+    } else {
+#pragma unroll
+      for (int o = kTeam / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(Team<kTeam>::mask(), key, o));
+    }
+    peak = from_ordered(key);
   };
   if constexpr (kPeakFirst) {
     if (!tiny) find_peak();  // the block's threads agree on that
   }
   const float inverse = tiny ? 0x1p126f : __fdiv_rn(127.f, peak.hi);
-  constexpr float kNear = 0.5f - kMargin<kOp, kPeakFirst>;
-  // how far eight quotients are from whole numbers, at most
-  auto distance = [&](const float(&v)[8]) {
-    float d = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d = fmaxf(d, fabsf(__fmaf_rn(v[i], inverse, -(__fmaf_rn(v[i], inverse, kMagic) - kMagic))));
-    return d;
-  };
-  if constexpr (kTeam != 0 && kOp != kQuantize) {
-    float d = 0.f;
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) d = fmaxf(d, distance(held[h]));
-    if (__any_sync(Team<kTeam>::mask(), d > kNear && !tiny)) find_peak();
-  }
-  auto encode = [&](const float(&v)[8], int c) {
-    if (c >= a.pitch) return;
-    uint32_t k[8];  // the low byte is the code
-    float d = 0.f;
+  const float border = tiny ? 1.f : 0.5f - kMargin<kOp, kPeakFirst>;
+  // eight codes; the mask of those next to a border
+  auto encode = [&](int c, const float(&v)[8]) {
+    float k[8], d[8], far = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = __fmaf_rn(v[i], inverse, kMagic);
-      k[i] = __float_as_uint(s);
-      d = fmaxf(d, fabsf(__fmaf_rn(v[i], inverse, -(s - kMagic))));
+      k[i] = __fmaf_rn(v[i], inverse, kMagic);
+      d[i] = fabsf(__fmaf_rn(v[i], inverse, -(k[i] - kMagic)));
+      far = fmaxf(far, d[i]);
     }
-    if (d > kNear && !tiny) {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        float one = v[0];
+    uint32_t w[2];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) one = i == j ? v[j] : one;
-        if (fabsf(__fmaf_rn(one, inverse, -(__fmaf_rn(one, inverse, kMagic) - kMagic))) <= kNear) continue;
-        const float code = copysignf(decide(in.exactly(c + i, f, g), peak, fabsf(one * inverse)), one);
-        const uint32_t bits = __float_as_uint(code + kMagic);
+    for (int i = 0; i < 2; ++i)
+      w[i] = __byte_perm(__byte_perm(__float_as_uint(k[4 * i]), __float_as_uint(k[4 * i + 1]), 0x0040),
+                         __byte_perm(__float_as_uint(k[4 * i + 2]), __float_as_uint(k[4 * i + 3]), 0x0040), 0x5410);
+    *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+    uint32_t mask = 0;
+    if (far > border) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) k[j] = i == j ? bits : k[j];
-      }
+      for (int i = 0; i < 8; ++i) mask |= (d[i] > border ? 1u : 0u) << i;
     }
-    auto pack = [](uint32_t p, uint32_t q, uint32_t r, uint32_t t) {
-      return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(r, t, 0x0040), 0x5410);
-    };
-    *reinterpret_cast<uint2*>(codes + c) = make_uint2(pack(k[0], k[1], k[2], k[3]), pack(k[4], k[5], k[6], k[7]));
+    return mask;
   };
+  auto correct = [&](int c) {
+    const Two v = in.exactly(c, f, g), m = magnitude(v);
+    codes[c] = static_cast<int8_t>(copysignf(decide(m, peak, m.hi * inverse), v.hi));
+  };
+  uint32_t mask = 0;
 #pragma unroll
-  for (int h = 0; h < kHeld; ++h) encode(held[h], (h * team + me) * 8);
+  for (int h = 0; h < kHeld; ++h)
+    if (column(h) < a.pitch) mask |= encode(column(h), held[h]) << (8 * h);
+  if constexpr (kOp != kQuantize && !kPeakFirst) {
+    // (a thread with columns that it does not hold does not know of them yet)
+    bool some = mask != 0 || column(kHeld) < a.cols;
+    if constexpr (kTeam == 0)
+      some = __syncthreads_or(some);
+    else
+      some = __any_sync(Team<kTeam>::mask(), some);
+    if (some && !tiny) find_peak();
+  }
+  for (; mask; mask &= mask - 1) {
+    const int i = __ffs(mask) - 1;
+    correct(column(i / 8) + i % 8);
+  }
 #pragma unroll 1
-  for (int c = (kHeld * team + me) * 8; c < a.pitch; c += team * 8) {
+  for (int c = column(kHeld); c < a.pitch; c += team * 8) {
     float v[8], unused = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (c < a.cols) {
-      in.again(c, f, g, v, unused);
-      if (kNorms && tiny) {
+    if (c < a.cols) in.again(c, f, g, v, unused);
+    if (kNorms && tiny) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= r;
-      }
+      for (int i = 0; i < 8; ++i) v[i] *= early;
     }
-    encode(v, c);
+    for (mask = encode(c, v); mask; mask &= mask - 1) correct(c + __ffs(mask) - 1);
   }
 }
 
-template <typename T, Op kOp, int kHeld, int kTeam, int kThreads>
-void launch_teams(const RowArgs& a, cudaStream_t st) {
-  constexpr int per = kThreads / kTeam;
-  k_q8_rows<T, kOp, kHeld, kTeam, kThreads><<<static_cast<unsigned>((a.rows + per - 1) / per), kThreads, 0, st>>>(a);
+// threads: a block's, kThreads at most
+template <typename T, Op kOp, int kHeld, int kTeam, int kThreads, int kBlocks>
+int launch_teams(const RowArgs& a, int threads, cudaStream_t st) {
+  static_assert(kHeld <= 4, "masks of 32 bits");
+  const int rows_per = kTeam == 0 ? 1 : threads / (kTeam == 0 ? 1 : kTeam);
+  k_q8_rows<T, kOp, kHeld, kTeam, kThreads, kBlocks>
+      <<<static_cast<unsigned>((a.rows + rows_per - 1) / rows_per), threads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
 template <Op kOp>
 int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
-  with_dtype(dtype, [&](auto t) {
+  return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const int eights = a.pitch / 8;
-    if (a.cols <= 256 && (kOp == kQuantize || kOp == kGate)) {
-      if constexpr (kOp == kQuantize || kOp == kGate) launch_teams<T, kOp, 4, 8, 128>(a, st);
-    } else if (a.cols <= 1024) {
-      launch_teams<T, kOp, 4, 32, 128>(a, st);
-    } else if (a.cols <= 4096) {
-      k_q8_rows<T, kOp, 2, 0, 256><<<static_cast<unsigned>(a.rows), (eights + 63) / 64 * 32, 0, st>>>(a);
-    } else {
-      k_q8_rows<T, kOp, 4, 0, 512><<<static_cast<unsigned>(a.rows), min(512, (eights + 127) / 128 * 32), 0, st>>>(a);
+    auto threads = [&](int each) { return (eights + 32 * each - 1) / (32 * each) * 32; };
+    if constexpr (kOp == kQuantize || kOp == kGate) {
+      if (a.cols <= 128) return launch_teams<T, kOp, 2, 8, 128, 8>(a, 128, st);
+      if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 8>(a, 128, st);
+      if (a.cols <= 4096 && kOp == kQuantize) return launch_teams<T, kOp, 4, 0, 128, 6>(a, threads(4), st);
+      if (a.cols > 4096 && sizeof(T) == 2) return launch_teams<T, kOp, 4, 0, 320, 3>(a, std::min(320, threads(4)), st);
     }
+    if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 6>(a, 128, st);
+    if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, 4>(a, threads(2), st);
+    return launch_teams<T, kOp, 2, 0, 640, kOp == kGate ? 2 : 1>(a, std::min(640, threads(2)), st);
   });
-  return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
-// A thread reads 16 codes.
+// A thread writes eight values of the output, taken as one row of rows * cols, from up to two 8-byte words of codes.
 template <typename T>
 __global__ void __launch_bounds__(256) k_q8_read(const int8_t* __restrict__ codes, const float* __restrict__ scales,
-                                                 long long items, int per, int cols, bool vec, T* __restrict__ out) {
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= items) return;
-  const long long row = i / per;
-  const int c = static_cast<int>(i - row * per) * 16;
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-  const float s = __ldg(scales + row);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+                                                 long long all, int cols, int pitch, bool wide, T* __restrict__ out) {
+  const long long at = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
+  if (at >= all) return;
+  // (32-bit division where it does)
+  long long row = at >> 32 ? at / cols : static_cast<uint32_t>(at) / static_cast<uint32_t>(cols);
+  int c = static_cast<int>(at - row * cols);
+  float v[8];
+  if (c + 8 <= cols) {
+    const uint2* w = reinterpret_cast<const uint2*>(codes + row * pitch + (c & ~7));
+    uint2 lo = __ldg(w), hi = c & 7 ? __ldg(w + 1) : make_uint2(0, 0);
+    const uint32_t b[4] = {lo.x, lo.y, hi.x, hi.y};
+    const float s = __ldg(scales + row);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float v[8];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t p = c & 4 ? b[i + 1] : b[i], q = c & 4 ? b[i + 2 < 4 ? i + 2 : 3] : b[i + 1];
+      const uint32_t u = __funnelshift_r(p, q, c % 4 * 8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = s * static_cast<float>(static_cast<int8_t>(w[2 * h + e / 4] >> (e % 4 * 8)));
-    Eight<T> o;
-    o.set(v);
-    if (c + 8 * h < cols) o.store(out + row * cols, c + 8 * h, cols, vec);
+      for (int e = 0; e < 4; ++e) v[4 * i + e] = s * static_cast<float>(static_cast<int8_t>(u >> (8 * e)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = at + i < all ? __ldg(scales + row) * static_cast<float>(__ldg(codes + row * pitch + c)) : 0.f;
+      if (++c == cols) c = 0, ++row;
+    }
   }
+  Eight<T> o;
+  o.set(v);
+  o.store(out + at, 0, static_cast<int>(min(all - at, 8ll)), wide ? 0 : 1);
 }
 
 constexpr int kColsMost = 1 << 24;
@@ -603,7 +633,6 @@ bool bad_rows(const void* x, int dtype, long long stride, long long rows, long l
   return !x || !esz || !codes || !scales || rows < 1 || rows > 0x7fffffffll || cols < 1 || cols > kColsMost ||
          stride < width || !aligned(x, esz) || !aligned(codes, 16) || !aligned(scales, 4);
 }
-bool wide(const void* p, long long stride, int esz) { return aligned(p, 16) && stride * esz % 16 == 0; }
 int pitch_of(int cols) { return (cols + 15) / 16 * 16; }
 
 }  // namespace
@@ -614,9 +643,7 @@ using namespace s2;
 extern "C" int s2_quantize_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes,
                               float* scales, CUstream_st* stream) {
   if (bad_rows(x, dtype, x_stride, rows, cols, cols, codes, scales)) return S2_EINVAL;
-  const int esz = dtype_bytes(dtype);
-  const RowArgs a{x, nullptr, nullptr, nullptr, codes, scales, x_stride, 0, rows, cols, pitch_of(cols), 0.f,
-                  wide(x, x_stride, esz)};
+  const RowArgs a{x, nullptr, nullptr, nullptr, codes, scales, x_stride, 0, rows, cols, pitch_of(cols), 0.f, 0.f};
   return launch_rows<kQuantize>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -631,32 +658,27 @@ extern "C" int s2_rms_norm_q8(const void* x, int dtype, long long x_stride, cons
       (residual && (residual_stride < cols || !aligned(residual, esz) || !aligned(total, esz))))
     return S2_EINVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  RowArgs a{x, residual, weight, total, codes, scales, x_stride, residual_stride, rows, cols, pitch_of(cols), eps,
-            wide(x, x_stride, esz) && aligned(weight, 16)};
-  if (!residual) return launch_rows<kNorm>(a, dtype, st);
-  a.vec = a.vec && wide(residual, residual_stride, esz) && wide(total, cols, esz);
-  return launch_rows<kNormResidual>(a, dtype, st);
+  const RowArgs a{x, residual, weight, total, codes, scales, x_stride, residual_stride, rows, cols, pitch_of(cols), eps,
+                  1.f / cols};
+  return residual ? launch_rows<kNormResidual>(a, dtype, st) : launch_rows<kNorm>(a, dtype, st);
 }
 
 extern "C" int s2_swiglu_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes,
                             float* scales, CUstream_st* stream) {
   if (bad_rows(x, dtype, x_stride, rows, 2ll * cols, cols, codes, scales)) return S2_EINVAL;
-  const int esz = dtype_bytes(dtype);
-  const RowArgs a{x, nullptr, nullptr, nullptr, codes, scales, x_stride, 0, rows, cols, pitch_of(cols), 0.f,
-                  wide(x, x_stride, esz) && static_cast<long long>(cols) * esz % 16 == 0};
+  const RowArgs a{x, nullptr, nullptr, nullptr, codes, scales, x_stride, 0, rows, cols, pitch_of(cols), 0.f, 0.f};
   return launch_rows<kGate>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int s2_dequantize_q8(const int8_t* codes, const float* scales, long long rows, int cols, void* out, int dtype,
                                 CUstream_st* stream) {
   if (bad_rows(out, dtype, cols, rows, cols, cols, codes, scales)) return S2_EINVAL;
-  const int per = pitch_of(cols) / 16;
-  const long long items = rows * per, grid = (items + 255) / 256;
+  const long long all = rows * cols, grid = (all + 2047) / 2048;
   if (grid > 0x7fffffffll) return S2_EINVAL;
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     k_q8_read<T><<<static_cast<unsigned>(grid), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        codes, scales, items, per, cols, wide(out, cols, sizeof(T)), static_cast<T*>(out));
+        codes, scales, all, cols, pitch_of(cols), aligned(out, 16), static_cast<T*>(out));
   });
   return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }
