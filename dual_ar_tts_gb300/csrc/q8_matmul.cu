@@ -192,162 +192,343 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
 
 // ---- more activation rows: tcgen05, its A operand the weights, B the activations.
 //
-// A block takes 128 weight rows and N activation rows.  Twice four warps expand steps in turn: a thread a weight row to fp16
-// in tensor memory, and a share of the activations into the swizzled tiles that the tensor core reads.  A ninth warp issues
-// the products.  Sums of a chunk are exact; two places in tensor memory take chunks in turn, and the expanding warps add
-// the one that is done to their integers while the other is filled.  The blocks of a cluster split W's columns.
-template <int N>
+// A tile is 128 weight rows a block times N activation rows.  Twice four warps take steps of 128 columns in turn: a thread
+// expands a weight row to fp16 in tensor memory.  Four warps expand every step's activations into the swizzled tiles that the
+// tensor core reads.  One warp issues the products, in two halves of the columns.  The first eight warps also own the sums, a
+// thread half a row's: when a chunk's products are done they are added to integers, and the next chunk starts in their place;
+// the halves end one after the other, and the operands of the next steps lie ready meanwhile.
+// kPair: the blocks of a pair work on one tile of 256 weight rows (cta_group::2), each holds half of the activations, which
+// halves what a block reads and stores of them.  Blocks take tiles in turn (there is no end of a pipeline between them), or
+// the blocks of a cluster split W's columns of one tile.
+template <int N, bool kPair>
 struct Tc {
-  static constexpr int kStages = N == 128 ? 3 : 4;                  // expanded steps: 64 tensor memory columns and B each
-  static constexpr int kAhead = 3;                                  // steps of a warp's weights
-  static constexpr int kBBytes = N * 256, kWarpRow = 32 * kStep;
-  static constexpr int kRing = kStages * kBBytes, kBars = kRing + 8 * kAhead * kWarpRow, kBytes = kBars + 128 + 1024;
-  static constexpr uint32_t kCols = 512, kA = 2 * N;                // tensor memory: two places for sums, then A
-  static_assert(kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars, "room");
+  static constexpr int kRows = kPair ? N / 2 : N;                   // of activations in a block
+  static constexpr int kStages = 4;                                 // expanded steps: 64 tensor memory columns and B each
+  static constexpr int kAhead = kRows == 128 ? 2 : 4;               // steps of a warp's weights under way
+  static constexpr int kXAhead = 2;                                 // steps of activations under way
+  static constexpr int kBBytes = kRows * 256, kWarpRow = 32 * kStep, kXBytes = kRows * kStep;
+  static constexpr int kRing = kStages * kBBytes, kXRing = kRing + 8 * kAhead * kWarpRow;
+  static constexpr int kBars = kXRing + kXAhead * kXBytes, kBytes = kBars + 128 + 1024;
+  static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
+  static_assert(N <= 256 && kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars && kBytes <= 232448, "room");
 };
 
-constexpr int kTcThreads = 288;
-template <typename T, int N>
+// Arrival at the same barrier of the pair's first block.
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int tries) {
+  for (int i = 0; i < tries; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+template <bool kPair>
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  if constexpr (!kPair) {
+    tc_mma_tmem_a(d, a, b, idesc, accum);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+  }
+}
+// An arrival at `bar` (in both blocks of a pair) when the products issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (!kPair)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// The same at this block's alone.
+template <bool kPair>
+__device__ __forceinline__ void commit_here(uint64_t* bar) {
+  if constexpr (!kPair)
+    tc_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_get(uint32_t* dst, uint32_t cols) {
+  if constexpr (!kPair) {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  if constexpr (!kPair)
+    tmem_dealloc(at, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+// Threads: eight warps for weights, four for activations, four of which one issues.  A pair's sums take 128 registers a thread:
+// of the launch's 512 x 128 registers the first eight warps' threads take 200, the next four's 80, the last four's 24
+// (504 x 128 in all).
+constexpr int kTcThreads = 512;
+template <typename T, int N, bool kPair>
 __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
-  using M = Tc<N>;
+  using M = Tc<N, kPair>;
+  constexpr int S = M::kStages, kHalf = N / 2;  // columns of a half
   extern __shared__ __align__(16) uint8_t smraw[];
   __shared__ int failed;
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [j % kStages]: step j is expanded
-  uint64_t* empty = full + M::kStages;                          // and used up
-  uint64_t *done = empty + M::kStages, *taken = done + 2;       // [chunk % 2]: its products; its sums read
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [step % S]: expanded
+  uint64_t* empty = full + S;                                   // and used up
+  uint64_t *done = empty + S, *taken = done + 2;                // [half]: a chunk's products; its sums read
   uint64_t* drained = taken + 2;                                // nothing under way
   uint32_t* tbase = reinterpret_cast<uint32_t*>(drained + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int steps = (a.k + kStep - 1) / kStep;
-  const int ranks = gridDim.y, rank = blockIdx.y;
+  const int ranks = kPair ? 1 : gridDim.y, rank = kPair ? 0 : blockIdx.y, side = kPair ? blockIdx.x % 2 : 0;
   const int s0 = static_cast<int>(static_cast<long long>(steps) * rank / ranks);
   const int count = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / ranks) - s0;
-  const int chunks = (count + kChunk - 1) / kChunk;
+  const int chunks = (count + kChunk - 1) / kChunk;  // of a tile
+  // tiles: weight rows first, so that blocks at work together share activations
+  constexpr int kTile = kPair ? 256 : 128;
+  const int row_tiles = (a.m + kTile - 1) / kTile, tiles = row_tiles * ((a.n + N - 1) / N);
+  const int first = kPair ? blockIdx.x / 2 : blockIdx.x, apart = kPair ? gridDim.x / 2 : gridDim.x;
+  const int mine = first < tiles ? (tiles - first + apart - 1) / apart : 0;
   if (threadIdx.x == 0) {
     failed = 0;
-    for (int i = 0; i < M::kStages; ++i) {
-      mbar_init(full + i, 4);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + i, kPair ? 16 : 8);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done + i, 1);
-      mbar_init(taken + i, 8);
+      mbar_init(taken + i, kPair ? 8 : 4);
     }
     mbar_init(drained, 1);
     fence_barrier_init();
   }
-  if (warp == 8) {
-    tmem_alloc(tbase, M::kCols);
-    tmem_relinquish();
-  }
+  if (warp == 12) tmem_get<kPair>(tbase, M::kCols);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair)
+    cluster_sync();  // the barriers that the other block arrives at
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
+  auto arrive = [&](uint64_t* bar) {
+    if constexpr (kPair)
+      mbar_arrive_first(bar);
+    else
+      mbar_arrive(bar);
+  };
 
   bool ok = true;
-  const int n0 = blockIdx.z * N, nn = min(N, a.n - n0), wg = warp / 4;
-  int sum[N / 2] = {};  // of this thread's row, half of the columns
-  if (warp == 8) {
+  if (warp >= 12) {
     // ---------------------------------------------------------------- issuing the products
-    if (elect_one()) {
-      for (int j = 0; j < count; ++j) {
-        const int s = j % M::kStages, chunk = j / kChunk;
-        ok = mbar_wait_short(full + s, j / M::kStages & 1, a.tries) &&
-             (j % kChunk || chunk < 2 || mbar_wait_short(taken + chunk % 2, (chunk / 2 - 1) & 1, a.tries));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t ta = tm + M::kA + s * 64, td = tm + chunk % 2 * N;
-        const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
+    if constexpr (N >= 128) fewer_registers<24>();
+    if (warp == 12 && side == 0) {
+      if (elect_one()) {
+        int g = 0, chunk = 0;  // over all tiles
+        for (int i = 0; i < mine && ok; ++i)
+          for (int j = 0; j < count && ok; ++j, ++g) {
+            const int s = g % S;
+            const bool starts = j % kChunk == 0, ends = j % kChunk == kChunk - 1 || j == count - 1;
+            ok = kPair ? mbar_wait_cluster(full + s, g / S & 1, a.tries) : mbar_wait_short(full + s, g / S & 1, a.tries);
+            if (!ok) break;
+            const uint32_t ta = tm + M::kA + s * 64;
+            const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
-          tc_mma_tmem_a(td, ta + k * 8, b + ((k / 4 * (N * 128) + k % 4 * 32) >> 4), idesc_f16(128, N), j % kChunk > 0 || k > 0);
-        tc_commit(empty + s);
-        if (j == count - 1 || j % kChunk == kChunk - 1) tc_commit(done + chunk % 2);
+            for (int h = 0; h < 2; ++h) {
+              if (starts && chunk > 0)
+                ok = kPair ? mbar_wait_cluster(taken + h, (chunk - 1) & 1, a.tries)
+                           : mbar_wait_short(taken + h, (chunk - 1) & 1, a.tries);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < kStep / 16; ++k)
+                mma_tmem_a<kPair>(tm + h * kHalf, ta + k * 8,
+                                  b + ((h * (M::kRows / 2) * 128 + k / 4 * (M::kRows * 128) + k % 4 * 32) >> 4),
+                                  idesc_f16(kTile, kHalf), !starts || k > 0);
+              if (h == 1) commit<kPair>(empty + s);
+              if (ends) commit<kPair>(done + h);
+            }
+            if (ends) ++chunk;
+          }
+        commit_here<kPair>(drained);  // no end before that of the products, whoever gave up
+        mbar_wait_short(drained, 0);
       }
-      tc_commit(drained);  // no end before that of the products, whoever gave up
-      mbar_wait_short(drained, 0);
+      __syncwarp();
     }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- expanding
-    const int mine = (count - wg + 1) / 2;  // the steps 2 t + wg
-    const int in = warp % 4 * 32, row0 = blockIdx.x * 128 + in, tid = threadIdx.x % 128;
-    // weights: eight lanes a row of 128 bytes, its 16-byte pieces swizzled by the row
-    const uint32_t ring = smem_u32(sm + M::kRing + warp * M::kAhead * M::kWarpRow);
-    const int8_t* from[8];
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- expanding activations
+    if constexpr (N >= 128) fewer_registers<80>();
+    // four lanes 64 bytes of a row; a thread copies what it expands itself
+    constexpr int kLoads = M::kRows / 16;
+    const int tid = threadIdx.x % 128;
+    uint8_t* ring = sm + M::kXRing + tid * 16;
+    const int all = mine * count;
+    int at_tile = 0, at_step = 0;  // of the next copy
+    auto issue = [&](int slot) {
+      if (at_tile < mine) {
+        const int n0 = (first + at_tile * apart) / row_tiles * N;
+        const int col = (s0 + at_step) * kStep + tid % 4 * 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) from[i] = a.w + static_cast<size_t>(min(row0 + i * 4 + lane / 8, a.m - 1)) * a.k;
-    auto issue = [&](int t) {
-      if (t < mine) {
-        const uint32_t dst = ring + t % M::kAhead * M::kWarpRow;
-        const int col = (s0 + 2 * t + wg) * kStep + lane % 8 * 16;
-        const bool live = col < a.k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + lane / 8;
-          cp_async16_or_zero(dst + r * kStep + ((lane % 8) ^ (r & 7)) * 16, from[i] + (live ? col : 0), live);
+        for (int i = 0; i < kLoads; ++i) {
+          const int l = i / 2 * 32 + tid / 4, at = col + i % 2 * 64;
+          const int r = n0 + (kPair ? l / (kHalf / 2) * kHalf + side * (kHalf / 2) + l % (kHalf / 2) : l);
+          const bool live = r < a.n && at < a.k;
+          cp_async16_or_zero(smem_u32(ring + slot * M::kXBytes + i * 2048), a.x + (live ? static_cast<size_t>(r) * a.k + at : 0),
+                             live);
         }
+        if (++at_step == count) at_step = 0, ++at_tile;
       }
       cp_async_commit();
     };
-    // activations: four lanes 64 bytes of a row
-    constexpr int kLoads = N / 16;
-    uint4 held[kLoads];
-    auto load = [&](int t) {
-      const int col = (s0 + 2 * t + wg) * kStep + tid % 4 * 16;
+    for (int i = 0; i < M::kXAhead; ++i) issue(i);
+    for (int g = 0; g < all; ++g) {
+      const int s = g % S;
+      cp_async_wait_group<M::kXAhead - 1>();
+      if (g >= S) {
+        ok = __all_sync(0xffffffffu, mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries));
+        if (!ok) break;
+      }
+      uint8_t* b = sm + s * M::kBBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = i / 2 * 32 + tid / 4, at = col + i % 2 * 64;
-        held[i] = make_uint4(0, 0, 0, 0);
-        if (t < mine && r < nn && at < a.k)
-          held[i] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(n0 + r) * a.k + at));
+        const int r = i / 2 * 32 + tid / 4, c = tid % 4 * 2;
+        const uint4 v = lds128(smem_u32(ring + g % M::kXAhead * M::kXBytes + i * 2048));
+        uint4 p, q;
+        expand(v.x, p.x, p.y);
+        expand(v.y, p.z, p.w);
+        expand(v.z, q.x, q.y);
+        expand(v.w, q.z, q.w);
+        uint8_t* dst = b + i % 2 * (M::kRows * 128) + r * 128;
+        *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) * 16)) = p;
+        *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) * 16)) = q;
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(full + s);
+      issue(g % M::kXAhead);
+    }
+    cp_async_wait_all();
+    // the last arrivals of the pair's first block, which the second may not leave before
+    for (int g = max(all - S, 0); kPair && ok && g < all; ++g)
+      ok = __all_sync(0xffffffffu, mbar_wait_short(empty + g % S, g / S & 1, a.tries));
+  } else {
+    // ---------------------------------------------------------------- expanding weights, adding up
+    if constexpr (N >= 128) more_registers<200>();
+    const int wg = warp / 4, in = warp % 4 * 32;
+    const uint32_t ring = smem_u32(sm + M::kRing + warp * M::kAhead * M::kWarpRow);
+    const int all = mine * count;
+    // weights: eight lanes a row of 128 bytes, its 16-byte pieces swizzled by the row
+    int at_tile = 0, at_step = wg;  // of the next copy
+    while (at_tile < mine && at_step >= count) at_step -= count, ++at_tile;
+    auto issue = [&](int slot) {
+      if (at_tile < mine) {
+        const int row0 = (first + at_tile * apart) % row_tiles * kTile + side * 128 + in + lane / 8;
+        const int col = (s0 + at_step) * kStep + lane % 8 * 16;
+        const bool live = col < a.k;
+        const int8_t* from = a.w + (live ? col : 0);
+        const uint32_t dst = ring + slot * M::kWarpRow + lane / 8 * kStep;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cp_async16_or_zero(dst + i * 4 * kStep + ((lane % 8) ^ (i * 4 + lane / 8 & 7)) * 16,
+                             from + static_cast<size_t>(min(row0 + i * 4, a.m - 1)) * a.k, live);
+        at_step += 2;
+        while (at_tile < mine && at_step >= count) at_step -= count, ++at_tile;
+      }
+      cp_async_commit();
     };
-    // adds a chunk's sums, which makes room for the chunk after the next
-    auto take = [&](int chunk) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_short(done + chunk % 2, chunk / 2 & 1, a.tries));
+    for (int i = 0; i < M::kAhead; ++i) issue(i);
+    const uint32_t lanes = static_cast<uint32_t>(in) << 16, tlane = tm + M::kA + lanes;
+    int sum[kHalf];  // of this thread's row, half of the columns
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) sum[i] = 0;
+    int chunk = 0, tile = 0, in_tile = 0, last = min(kChunk, count) - 1;  // the chunk to take: its tile, place there, last step
+    auto take = [&] {
+      ok = __all_sync(0xffffffffu, mbar_wait_short(done + wg, chunk & 1, a.tries));
       if (!ok) return;
       tc_fence_after();
-      const uint32_t at = tm + (static_cast<uint32_t>(in) << 16) + chunk % 2 * N + wg * (N / 2);
 #pragma unroll
-      for (int i = 0; i < N / 32; ++i) {
+      for (int i = 0; i < kHalf / 16; ++i) {
         float v[16];
-        tmem_ld16(at + i * 16, v);
+        tmem_ld16(tm + lanes + wg * kHalf + i * 16, v);
 #pragma unroll
         for (int e = 0; e < 16; ++e) sum[i * 16 + e] += __float2int_rn(v[e]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(taken + chunk % 2);
+      if (lane == 0) arrive(taken + wg);
+      ++chunk;
     };
+    // a tile's results, two threads a row; a wait that gave up leaves no numbers
+    auto write = [&](bool good) {
+      const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
+      const int row = t % row_tiles * kTile + side * 128 + in + lane;
+      if (row < a.m) {
+        T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
+        const float ws = good ? __ldg(a.ws + row) : __uint_as_float(0x7fc00000u);
 #pragma unroll
-    for (int i = 0; i < M::kAhead - 1; ++i) issue(i);
-    load(0);
-    const uint32_t tlane = tm + M::kA + (static_cast<uint32_t>(in) << 16);
-    int next = 0;  // chunk to take
-    for (int t = 0; t < mine; ++t) {
-      const int j = 2 * t + wg, s = j % M::kStages;
-      issue(t + M::kAhead - 1);
+        for (int i = 0; i < kHalf; ++i)
+          if (n0 + i < a.n) y[static_cast<size_t>(i) * a.m] = scaled<T>(sum[i], __ldg(a.xs + n0 + i), ws);
+      }
+    };
+    // takes the chunk, and writes the tile that ends with it
+    auto step_on = [&] {
+      take();
+      if (!ok) return;
+      if (++in_tile == chunks) {
+        if (ranks == 1) {
+          write(true);
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) sum[i] = 0;
+        }
+        in_tile = 0, ++tile;
+      }
+      last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
+    };
+    int slot = 0;
+    for (int g = wg; g < all && ok; g += 2) {
+      const int s = g % S;
+      // a chunk whose last step has to leave its stage before this one can come is done at once, and waited for
+      while (tile < mine && last <= g - S && ok) step_on();
+      if (!ok) break;
       cp_async_wait_group<M::kAhead - 1>();
       __syncwarp();
-      const uint32_t at = ring + t % M::kAhead * M::kWarpRow + lane * kStep;
-      uint4 w[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = lds128(at + ((c ^ (lane & 7)) * 16));
-      __syncwarp();  // the ring's place may be filled again
-      if (j >= M::kStages) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_short(empty + s, (j / M::kStages - 1) & 1, a.tries));
+      if (g >= S) {
+        ok = __all_sync(0xffffffffu, mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries));
         if (!ok) break;
         tc_fence_after();
       }
+      const uint32_t at = ring + slot * M::kWarpRow + lane * kStep;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t r[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 x = w[half * 4 + c];
+          const uint4 x = lds128(at + (((half * 4 + c) ^ (lane & 7)) * 16));
           expand(x.x, r[c * 8], r[c * 8 + 1]);
           expand(x.y, r[c * 8 + 2], r[c * 8 + 3]);
           expand(x.z, r[c * 8 + 4], r[c * 8 + 5]);
@@ -355,80 +536,61 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
         }
         tmem_st32(tlane + s * 64 + half * 32, r);
       }
-      uint8_t* b = sm + s * M::kBBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = i / 2 * 32 + tid / 4, c = tid % 4 * 2;
-        uint4 p, q;
-        expand(held[i].x, p.x, p.y);
-        expand(held[i].y, p.z, p.w);
-        expand(held[i].z, q.x, q.y);
-        expand(held[i].w, q.z, q.w);
-        uint8_t* dst = b + i % 2 * (N * 128) + r * 128;
-        *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) * 16)) = p;
-        *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) * 16)) = q;
-      }
-      fence_proxy_async_smem();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + s);
-      load(t + 1);
-      // by now the chunk before is done, since the stage that this step took was its
-      if (j % kChunk >= M::kStages && j / kChunk > next) {
-        take(next++);
-        if (!ok) break;
-      }
+      __syncwarp();  // the ring's place may be filled again
+      if (lane == 0) arrive(full + s);
+      issue(slot);
+      slot = slot + 1 == M::kAhead ? 0 : slot + 1;
     }
     cp_async_wait_all();
-    while (ok && next < chunks) take(next++);
-    if (!ok && lane == 0) failed = 1;
+    while (tile < mine && ok) step_on();
+    if (!ok) {
+      if (lane == 0) failed = 1;
+      if (ranks == 1)
+        for (; tile < mine; ++tile) write(false);
+    }
+    if (ranks > 1) {
+      named_bar(1, 256);  // every operand is used up
+      int* out = reinterpret_cast<int*>(sm);  // [column][row], where the operands were
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) out[(wg * kHalf + i) * 128 + in + lane] = sum[i];
+    }
   }
-  // two threads a row, each half of the columns; a wait that gave up leaves no numbers
-  const int r = threadIdx.x % 128, row = blockIdx.x * 128 + r;
-  T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
-  __syncthreads();
-  if (ranks == 1) {
-    if (warp < 8 && row < a.m) {
-      const float ws = failed ? __uint_as_float(0x7fc00000u) : __ldg(a.ws + row);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const int col = wg * (N / 2) + i;
-        if (col < nn) y[static_cast<size_t>(col) * a.m] = scaled<T>(sum[i], __ldg(a.xs + n0 + col), ws);
-      }
-    }
-  } else {
-    int* out = reinterpret_cast<int*>(sm);  // [column][row], where the operands were
-    if (warp < 8) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) out[(wg * (N / 2) + i) * 128 + r] = sum[i];
-    }
-    cluster_sync();
-    if (warp < 8) {
+  if constexpr (!kPair) {
+    if (ranks > 1) {
+      const int r = threadIdx.x % 128, part = threadIdx.x / 128;
+      const int row = first % row_tiles * 128 + r, n0 = first / row_tiles * N, nn = min(N, a.n - n0);
+      const int* out = reinterpret_cast<const int*>(sm);
+      cluster_sync();
       int bad = 0;
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         if (q < ranks) bad |= ld_cluster_int(smem_u32(&failed), q);
       const float ws = bad ? __uint_as_float(0x7fc00000u) : __ldg(a.ws + min(row, a.m - 1));
-      for (int col = wg * ranks + rank; col < nn; col += 2 * ranks) {
+      for (int col = part * ranks + rank; col < nn; col += 4 * ranks) {
         int v[8], total = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = q < ranks ? ld_cluster_int(smem_u32(out + col * 128 + r), q) : 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) total += v[q];
-        if (row < a.m) y[static_cast<size_t>(col) * a.m] = scaled<T>(total, __ldg(a.xs + n0 + col), ws);
+        if (row < a.m)
+          static_cast<T*>(a.y)[static_cast<size_t>(n0 + col) * a.m + row] = scaled<T>(total, __ldg(a.xs + n0 + col), ws);
       }
+      cluster_sync();  // no block leaves while its sums are read
     }
-    cluster_sync();  // no block leaves while its sums are read
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == 8) {
+  if constexpr (kPair)
+    cluster_sync();  // no block leaves while its operands are read, or its barriers arrived at
+  else
+    __syncthreads();
+  if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tm, M::kCols);
+    tmem_free<kPair>(tm, M::kCols);
   }
 }
 
-int launch_clusters(void (*kernel)(Q8Args), dim3 grid, int threads, int smem, int ranks, const Q8Args& a, cudaStream_t st) {
+int launch_clusters(void (*kernel)(Q8Args), dim3 grid, dim3 cluster, int threads, int smem, const Q8Args& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -436,11 +598,11 @@ int launch_clusters(void (*kernel)(Q8Args), dim3 grid, int threads, int smem, in
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = ranks;
-  at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = cluster.x;
+  at[0].val.clusterDim.y = cluster.y;
+  at[0].val.clusterDim.z = cluster.z;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
@@ -451,16 +613,25 @@ int launch_few(const Q8Args& a, cudaStream_t st) {
   const long long groups = static_cast<long long>(rows) * cols;
   const int ranks = std::max(1, std::min({8, static_cast<int>((NT == 4 ? 152 : 304) / groups), steps / 2}));
   if (!allow_smem<k_q8_few<T, NT>, kFewBytes<NT>>()) return S2_ECUDA;
-  return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), 32 * kFewWarps, kFewBytes<NT>, ranks, a, st);
+  return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, a, st);
 }
 
 template <typename T, int N>
 int launch_tc(const Q8Args& a, cudaStream_t st) {
   const int rows = (a.m + 127) / 128, cols = (a.n + N - 1) / N, steps = (a.k + kStep - 1) / kStep;
-  const long long groups = static_cast<long long>(rows) * cols;
-  const int ranks = std::max(1, std::min({8, static_cast<int>(152 / groups), steps / 4}));
-  if (!allow_smem<k_q8_tc<T, N>, Tc<N>::kBytes>()) return S2_ECUDA;
-  return launch_clusters(k_q8_tc<T, N>, dim3(rows, ranks, cols), kTcThreads, Tc<N>::kBytes, ranks, a, st);
+  const long long tiles = static_cast<long long>(rows) * cols;
+  const int ranks = std::max(1, std::min({8, static_cast<int>(152 / tiles), steps / 4}));
+  const int blocks = static_cast<int>(ranks > 1 ? tiles : std::min(tiles, 152ll));
+  if (!allow_smem<k_q8_tc<T, N, false>, Tc<N, false>::kBytes>()) return S2_ECUDA;
+  return launch_clusters(k_q8_tc<T, N, false>, dim3(blocks, ranks), dim3(1, ranks), kTcThreads, Tc<N, false>::kBytes, a, st);
+}
+template <typename T>
+int launch_pairs(const Q8Args& a, cudaStream_t st) {
+  constexpr int N = 256;
+  const long long tiles = static_cast<long long>((a.m + 255) / 256) * ((a.n + N - 1) / N);
+  const int blocks = 2 * static_cast<int>(std::min(tiles, 76ll));
+  if (!allow_smem<k_q8_tc<T, N, true>, Tc<N, true>::kBytes>()) return S2_ECUDA;
+  return launch_clusters(k_q8_tc<T, N, true>, dim3(blocks), dim3(2), kTcThreads, Tc<N, true>::kBytes, a, st);
 }
 
 constexpr int kRowsMost = (1 << 21) - 32, kOutMost = 1 << 28, kColsMost = (1 << 17) - 16;  // activation and weight rows; columns
@@ -485,6 +656,7 @@ extern "C" int s2_q8_matmul(int n, const int8_t* x_codes, const float* x_scales,
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (n <= 32) return n <= 8 ? launch_few<T, 1>(a, st) : n <= 16 ? launch_few<T, 2>(a, st) : launch_few<T, 4>(a, st);
+    if (static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= 76) return launch_pairs<T>(a, st);
     return n <= 64 ? launch_tc<T, 64>(a, st) : launch_tc<T, 128>(a, st);
   });
 }
