@@ -4,10 +4,13 @@
 // both measured 256 products a clock and SM; fp16 has 1024 on mma.sync and 4096 on tcgen05), so codes are expanded to fp16,
 // which holds them exactly; a product has 14 bits, and fp32 holds the sum of 1024 of them exactly (2^24).  Every 1024
 // columns (a chunk) the sums go over to 32-bit integers.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "convert.cuh"
 #include "ptx.cuh"
@@ -204,14 +207,25 @@ template <int N, bool kPair>
 struct Tc {
   static constexpr int kRows = kPair ? N / 2 : N;                   // of activations in a block
   static constexpr int kStages = 4;                                 // expanded steps: 64 tensor memory columns and B each
-  static constexpr int kAhead = kRows == 128 ? 2 : 4;               // steps of a warp's weights under way
-  static constexpr int kXAhead = 2;                                 // steps of activations under way
-  static constexpr int kBBytes = kRows * 256, kWarpRow = 32 * kStep, kXBytes = kRows * kStep;
-  static constexpr int kRing = kStages * kBBytes, kXRing = kRing + 8 * kAhead * kWarpRow;
-  static constexpr int kBars = kXRing + kXAhead * kXBytes, kBytes = kBars + 128 + 1024;
+  static constexpr int kW = kRows == 128 ? 4 : 8, kX = kRows == 128 ? 2 : 4;  // steps of codes
+  static constexpr int kBBytes = kRows * 256, kWBytes = 128 * kStep, kXBytes = kRows * kStep;
+  static constexpr int kWRing = kStages * kBBytes, kXRing = kWRing + kW * kWBytes;
+  static constexpr int kBars = kXRing + kX * kXBytes, kBytes = kBars + 512 + 1024;
   static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
-  static_assert(N <= 256 && kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars && kBytes <= 232448, "room");
+  static_assert(N <= 256 && kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars && kBytes <= 232000, "room");
 };
+
+struct Maps {
+  CUtensorMap w, x;  // codes as [rows][k]: boxes of 128 columns, swizzled
+};
+
+// Box at (column, row) of a tensor map into shared memory.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                   smem_u32(dst)),
+               "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+               : "memory");
+}
 
 // Arrival at the same barrier of the pair's first block.
 __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
@@ -293,7 +307,7 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // (504 x 128 in all).
 constexpr int kTcThreads = 512;
 template <typename T, int N, bool kPair>
-__global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const __grid_constant__ Maps maps) {
   using M = Tc<N, kPair>;
   constexpr int S = M::kStages, kHalf = N / 2;  // columns of a half
   extern __shared__ __align__(16) uint8_t smraw[];
@@ -303,7 +317,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
   uint64_t* empty = full + S;                                   // and used up
   uint64_t *done = empty + S, *taken = done + 2;                // [half]: a chunk's products; its sums read
   uint64_t* drained = taken + 2;                                // nothing under way
-  uint32_t* tbase = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t *w_here = drained + 1, *w_free = w_here + M::kW;     // [step % kW]: codes of weights
+  uint64_t *x_here = w_free + M::kW, *x_free = x_here + M::kX;  // [step % kX]: codes of activations
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(x_free + M::kX);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int steps = (a.k + kStep - 1) / kStep;
   const int ranks = kPair ? 1 : gridDim.y, rank = kPair ? 0 : blockIdx.y, side = kPair ? blockIdx.x % 2 : 0;
@@ -326,6 +342,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
       mbar_init(taken + i, kPair ? 8 : 4);
     }
     mbar_init(drained, 1);
+    for (int i = 0; i < M::kW; ++i) {
+      mbar_init(w_here + i, 1);
+      mbar_init(w_free + i, 4);
+    }
+    for (int i = 0; i < M::kX; ++i) {
+      mbar_init(x_here + i, 1);
+      mbar_init(x_free + i, 4);
+    }
     fence_barrier_init();
   }
   if (warp == 12) tmem_get<kPair>(tbase, M::kCols);
@@ -379,60 +403,74 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
         mbar_wait_short(drained, 0);
       }
       __syncwarp();
+    } else if (warp == 13 || warp == 14) {
+      // -------------------------------------------------------------- copying codes
+      // Blocks start at different steps of K: all of them reading the same lines of activations at a time, L2 serves a
+      // line once in 12 clocks or so.  (The sums do not depend on the order.)
+      if (elect_one()) {
+        const bool w = warp == 13;
+        const int ring = w ? M::kW : M::kX;
+        uint64_t *here = w ? w_here : x_here, *freed = w ? w_free : x_free;
+        uint8_t* to = sm + (w ? M::kWRing : M::kXRing);
+        int g = 0;
+        for (int i = 0; i < mine && ok; ++i) {
+          const int t = first + i * apart, row = t % row_tiles * kTile + side * 128, n0 = t / row_tiles * N;
+          int j = t % count;
+          for (int q = 0; q < count; ++q, ++g) {
+            const int s = g % ring, col = (s0 + j) * kStep;
+            if (g >= ring) ok = mbar_wait_short(freed + s, (g / ring - 1) & 1, a.tries);
+            if (!ok) break;
+            mbar_arrive_expect_tx(here + s, w ? M::kWBytes : M::kXBytes);
+            if (w) {
+              tma_box(to + s * M::kWBytes, &maps.w, col, row, here + s);
+            } else if constexpr (kPair) {
+              tma_box(to + s * M::kXBytes, &maps.x, col, n0 + side * 64, here + s);
+              tma_box(to + s * M::kXBytes + M::kXBytes / 2, &maps.x, col, n0 + kHalf + side * 64, here + s);
+            } else {
+              tma_box(to + s * M::kXBytes, &maps.x, col, n0, here + s);
+            }
+            if (++j == count) j = 0;
+          }
+        }
+        for (int q = max(g - ring, 0); q < g; ++q) mbar_wait_short(here + q % ring, q / ring & 1);  // no end before that of the copies
+      }
+      __syncwarp();
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- expanding activations
     if constexpr (N >= 128) fewer_registers<80>();
-    // four lanes 64 bytes of a row; a thread copies what it expands itself
+    // Eight lanes take the low half of a row's 128 codes and the high half of its neighbour's, then the other two: neither
+    // reading the swizzled codes nor writing the swizzled tiles, in which the halves are apart, meets a bank twice.
     constexpr int kLoads = M::kRows / 16;
-    const int tid = threadIdx.x % 128;
-    uint8_t* ring = sm + M::kXRing + tid * 16;
-    const int all = mine * count;
-    int at_tile = 0, at_step = 0;  // of the next copy
-    auto issue = [&](int slot) {
-      if (at_tile < mine) {
-        const int n0 = (first + at_tile * apart) / row_tiles * N;
-        const int col = (s0 + at_step) * kStep + tid % 4 * 16;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int l = i / 2 * 32 + tid / 4, at = col + i % 2 * 64;
-          const int r = n0 + (kPair ? l / (kHalf / 2) * kHalf + side * (kHalf / 2) + l % (kHalf / 2) : l);
-          const bool live = r < a.n && at < a.k;
-          cp_async16_or_zero(smem_u32(ring + slot * M::kXBytes + i * 2048), a.x + (live ? static_cast<size_t>(r) * a.k + at : 0),
-                             live);
-        }
-        if (++at_step == count) at_step = 0, ++at_tile;
-      }
-      cp_async_commit();
-    };
-    for (int i = 0; i < M::kXAhead; ++i) issue(i);
+    const int tid = threadIdx.x % 128, all = mine * count, high = tid / 4 % 2, c = tid % 4;
     for (int g = 0; g < all; ++g) {
-      const int s = g % S;
-      cp_async_wait_group<M::kXAhead - 1>();
-      if (g >= S) {
-        ok = __all_sync(0xffffffffu, mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries));
-        if (!ok) break;
-      }
-      uint8_t* b = sm + s * M::kBBytes;
+      const int s = g % S, slot = g % M::kX;
+      ok = mbar_wait_short(x_here + slot, g / M::kX & 1, a.tries);
+      if (g >= S) ok = ok && mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t from = smem_u32(sm + M::kXRing + slot * M::kXBytes);
+      uint8_t* b = sm + s * M::kBBytes + high * (M::kRows * 128);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = i / 2 * 32 + tid / 4, c = tid % 4 * 2;
-        const uint4 v = lds128(smem_u32(ring + g % M::kXAhead * M::kXBytes + i * 2048));
+        const int r = i / 2 * 32 + tid / 8 * 2 + (high ^ (i & 1));
+        const uint4 v = lds128(from + r * kStep + (((high * 4 + c) ^ (r & 7)) * 16));
         uint4 p, q;
         expand(v.x, p.x, p.y);
         expand(v.y, p.z, p.w);
         expand(v.z, q.x, q.y);
         expand(v.w, q.z, q.w);
-        uint8_t* dst = b + i % 2 * (M::kRows * 128) + r * 128;
-        *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) * 16)) = p;
-        *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) * 16)) = q;
+        uint8_t* dst = b + r * 128;
+        *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) * 16)) = p;
+        *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) * 16)) = q;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive(full + s);
-      issue(g % M::kXAhead);
+      if (lane == 0) {
+        arrive(full + s);
+        mbar_arrive(x_free + slot);
+      }
     }
-    cp_async_wait_all();
     // the last arrivals of the pair's first block, which the second may not leave before
     for (int g = max(all - S, 0); kPair && ok && g < all; ++g)
       ok = __all_sync(0xffffffffu, mbar_wait_short(empty + g % S, g / S & 1, a.tries));
@@ -440,28 +478,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
     // ---------------------------------------------------------------- expanding weights, adding up
     if constexpr (N >= 128) more_registers<200>();
     const int wg = warp / 4, in = warp % 4 * 32;
-    const uint32_t ring = smem_u32(sm + M::kRing + warp * M::kAhead * M::kWarpRow);
     const int all = mine * count;
-    // weights: eight lanes a row of 128 bytes, its 16-byte pieces swizzled by the row
-    int at_tile = 0, at_step = wg;  // of the next copy
-    while (at_tile < mine && at_step >= count) at_step -= count, ++at_tile;
-    auto issue = [&](int slot) {
-      if (at_tile < mine) {
-        const int row0 = (first + at_tile * apart) % row_tiles * kTile + side * 128 + in + lane / 8;
-        const int col = (s0 + at_step) * kStep + lane % 8 * 16;
-        const bool live = col < a.k;
-        const int8_t* from = a.w + (live ? col : 0);
-        const uint32_t dst = ring + slot * M::kWarpRow + lane / 8 * kStep;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          cp_async16_or_zero(dst + i * 4 * kStep + ((lane % 8) ^ (i * 4 + lane / 8 & 7)) * 16,
-                             from + static_cast<size_t>(min(row0 + i * 4, a.m - 1)) * a.k, live);
-        at_step += 2;
-        while (at_tile < mine && at_step >= count) at_step -= count, ++at_tile;
-      }
-      cp_async_commit();
-    };
-    for (int i = 0; i < M::kAhead; ++i) issue(i);
     const uint32_t lanes = static_cast<uint32_t>(in) << 16, tlane = tm + M::kA + lanes;
     int sum[kHalf];  // of this thread's row, half of the columns
 #pragma unroll
@@ -487,12 +504,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
     auto write = [&](bool good) {
       const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
       const int row = t % row_tiles * kTile + side * 128 + in + lane;
-      if (row < a.m) {
-        T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
-        const float ws = good ? __ldg(a.ws + row) : __uint_as_float(0x7fc00000u);
+      T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
+      const float ws = good ? __ldg(a.ws + min(row, a.m - 1)) : __uint_as_float(0x7fc00000u);
+      float xs[(kHalf + 31) / 32];  // a lane holds every 32nd of the columns' scales
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i)
-          if (n0 + i < a.n) y[static_cast<size_t>(i) * a.m] = scaled<T>(sum[i], __ldg(a.xs + n0 + i), ws);
+      for (int i = 0; i < kHalf; i += 32) xs[i / 32] = __ldg(a.xs + min(n0 + i + lane, a.n - 1));
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const T v = scaled<T>(sum[i], __shfl_sync(0xffffffffu, xs[i / 32], i % 32), ws);
+        if (row < a.m && n0 + i < a.n) *y = v;
+        y += a.m;
       }
     };
     // takes the chunk, and writes the tile that ends with it
@@ -509,20 +530,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
       }
       last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
     };
-    int slot = 0;
     for (int g = wg; g < all && ok; g += 2) {
-      const int s = g % S;
+      const int s = g % S, slot = g % M::kW;
       // a chunk whose last step has to leave its stage before this one can come is done at once, and waited for
       while (tile < mine && last <= g - S && ok) step_on();
       if (!ok) break;
-      cp_async_wait_group<M::kAhead - 1>();
-      __syncwarp();
-      if (g >= S) {
-        ok = __all_sync(0xffffffffu, mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t at = ring + slot * M::kWarpRow + lane * kStep;
+      ok = mbar_wait_short(w_here + slot, g / M::kW & 1, a.tries);
+      if (g >= S) ok = ok && mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t at = smem_u32(sm + M::kWRing + slot * M::kWBytes) + (in + lane) * kStep;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t r[32];
@@ -537,12 +555,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
         tmem_st32(tlane + s * 64 + half * 32, r);
       }
       tc_fence_before();
-      __syncwarp();  // the ring's place may be filled again
-      if (lane == 0) arrive(full + s);
-      issue(slot);
-      slot = slot + 1 == M::kAhead ? 0 : slot + 1;
+      __syncwarp();
+      if (lane == 0) {
+        arrive(full + s);
+        mbar_arrive(w_free + slot);
+      }
     }
-    cp_async_wait_all();
     while (tile < mine && ok) step_on();
     if (!ok) {
       if (lane == 0) failed = 1;
@@ -590,7 +608,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a) {
   }
 }
 
-int launch_clusters(void (*kernel)(Q8Args), dim3 grid, dim3 cluster, int threads, int smem, const Q8Args& a, cudaStream_t st) {
+template <typename... Args>
+int launch_clusters(void (*kernel)(Args...), dim3 grid, dim3 cluster, int threads, int smem, cudaStream_t st,
+                    const std::decay_t<Args>&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -603,7 +623,7 @@ int launch_clusters(void (*kernel)(Q8Args), dim3 grid, dim3 cluster, int threads
   at[0].val.clusterDim.z = cluster.z;
   cfg.attrs = at;
   cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? S2_OK : S2_ECUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
 template <typename T, int NT>
@@ -613,25 +633,42 @@ int launch_few(const Q8Args& a, cudaStream_t st) {
   const long long groups = static_cast<long long>(rows) * cols;
   const int ranks = std::max(1, std::min({8, static_cast<int>((NT == 4 ? 152 : 304) / groups), steps / 2}));
   if (!allow_smem<k_q8_few<T, NT>, kFewBytes<NT>>()) return S2_ECUDA;
-  return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, a, st);
+  return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, st, a);
 }
 
-template <typename T, int N>
-int launch_tc(const Q8Args& a, cudaStream_t st) {
-  const int rows = (a.m + 127) / 128, cols = (a.n + N - 1) / N, steps = (a.k + kStep - 1) / kStep;
-  const long long tiles = static_cast<long long>(rows) * cols;
-  const int ranks = std::max(1, std::min({8, static_cast<int>(152 / tiles), steps / 4}));
-  const int blocks = static_cast<int>(ranks > 1 ? tiles : std::min(tiles, 152ll));
-  if (!allow_smem<k_q8_tc<T, N, false>, Tc<N, false>::kBytes>()) return S2_ECUDA;
-  return launch_clusters(k_q8_tc<T, N, false>, dim3(blocks, ranks), dim3(1, ranks), kTcThreads, Tc<N, false>::kBytes, a, st);
+// Boxes of `box` rows by 128 columns of codes [rows][k], swizzled in 128 bytes; zeros outside.
+bool code_map(CUtensorMap* map, const int8_t* codes, long long rows, int k, int box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+               : nullptr;
+  }();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)}, stride[1] = {static_cast<cuuint64_t>(k)};
+  const cuuint32_t boxes[2] = {kStep, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, stride, boxes, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <typename T>
-int launch_pairs(const Q8Args& a, cudaStream_t st) {
-  constexpr int N = 256;
-  const long long tiles = static_cast<long long>((a.m + 255) / 256) * ((a.n + N - 1) / N);
-  const int blocks = 2 * static_cast<int>(std::min(tiles, 76ll));
-  if (!allow_smem<k_q8_tc<T, N, true>, Tc<N, true>::kBytes>()) return S2_ECUDA;
-  return launch_clusters(k_q8_tc<T, N, true>, dim3(blocks), dim3(2), kTcThreads, Tc<N, true>::kBytes, a, st);
+
+template <typename T, int N, bool kPair>
+int launch_tc(const Q8Args& a, cudaStream_t st) {
+  using M = Tc<N, kPair>;
+  constexpr int kTile = kPair ? 256 : 128;
+  const int rows = (a.m + kTile - 1) / kTile, cols = (a.n + N - 1) / N, steps = (a.k + kStep - 1) / kStep;
+  const long long tiles = static_cast<long long>(rows) * cols;
+  Maps maps;
+  if (!allow_smem<k_q8_tc<T, N, kPair>, M::kBytes>() || !code_map(&maps.w, a.w, a.m, a.k, 128) ||
+      !code_map(&maps.x, a.x, a.n, a.k, kPair ? 64 : N))
+    return S2_ECUDA;
+  if (kPair)
+    return launch_clusters(k_q8_tc<T, N, kPair>, dim3(2 * static_cast<unsigned>(std::min(tiles, 76ll))), dim3(2), kTcThreads,
+                           M::kBytes, st, a, maps);
+  const int ranks = std::max(1, std::min({8, static_cast<int>(152 / tiles), steps / 4}));
+  return launch_clusters(k_q8_tc<T, N, kPair>, dim3(static_cast<unsigned>(ranks > 1 ? tiles : std::min(tiles, 152ll)), ranks),
+                         dim3(1, ranks), kTcThreads, M::kBytes, st, a, maps);
 }
 
 constexpr int kRowsMost = (1 << 21) - 32, kOutMost = 1 << 28, kColsMost = (1 << 17) - 16;  // activation and weight rows; columns
@@ -656,7 +693,7 @@ extern "C" int s2_q8_matmul(int n, const int8_t* x_codes, const float* x_scales,
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (n <= 32) return n <= 8 ? launch_few<T, 1>(a, st) : n <= 16 ? launch_few<T, 2>(a, st) : launch_few<T, 4>(a, st);
-    if (static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= 76) return launch_pairs<T>(a, st);
-    return n <= 64 ? launch_tc<T, 64>(a, st) : launch_tc<T, 128>(a, st);
+    if (static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= 76) return launch_tc<T, 256, true>(a, st);
+    return n <= 64 ? launch_tc<T, 64, false>(a, st) : launch_tc<T, 128, false>(a, st);
   });
 }
