@@ -227,26 +227,30 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x
                : "memory");
 }
 
-// Arrival at the same barrier of the pair's first block.
+// Arrival at the same barrier of the pair's first block.  What it tells of lies in the arriving block's own shared and tensor
+// memory, and is complete: fence.proxy.async and tcgen05.wait::st come first.  So the release is the block's; one at cluster
+// scope cost 1200 clocks each, and 2048 rows of 19456 x 2560 193 us.
 __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int tries) {
-  for (int i = 0; i < tries; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
+// 32 columns of tensor memory; their values are there after tmem_loaded().
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // not used before
 }
 template <bool kPair>
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
@@ -378,15 +382,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
           for (int j = 0; j < count && ok; ++j, ++g) {
             const int s = g % S;
             const bool starts = j % kChunk == 0, ends = j % kChunk == kChunk - 1 || j == count - 1;
-            ok = kPair ? mbar_wait_cluster(full + s, g / S & 1, a.tries) : mbar_wait_short(full + s, g / S & 1, a.tries);
+            ok = mbar_wait_short(full + s, g / S & 1, a.tries);
             if (!ok) break;
             const uint32_t ta = tm + M::kA + s * 64;
             const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (starts && chunk > 0)
-                ok = kPair ? mbar_wait_cluster(taken + h, (chunk - 1) & 1, a.tries)
-                           : mbar_wait_short(taken + h, (chunk - 1) & 1, a.tries);
+              if (starts && chunk > 0) ok = mbar_wait_short(taken + h, (chunk - 1) & 1, a.tries);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -405,8 +407,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       __syncwarp();
     } else if (warp == 13 || warp == 14) {
       // -------------------------------------------------------------- copying codes
-      // Blocks start at different steps of K: all of them reading the same lines of activations at a time, L2 serves a
-      // line once in 12 clocks or so.  (The sums do not depend on the order.)
       if (elect_one()) {
         const bool w = warp == 13;
         const int ring = w ? M::kW : M::kX;
@@ -415,8 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
         int g = 0;
         for (int i = 0; i < mine && ok; ++i) {
           const int t = first + i * apart, row = t % row_tiles * kTile + side * 128, n0 = t / row_tiles * N;
-          int j = t % count;
-          for (int q = 0; q < count; ++q, ++g) {
+          for (int j = 0; j < count; ++j, ++g) {
             const int s = g % ring, col = (s0 + j) * kStep;
             if (g >= ring) ok = mbar_wait_short(freed + s, (g / ring - 1) & 1, a.tries);
             if (!ok) break;
@@ -429,7 +428,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
             } else {
               tma_box(to + s * M::kXBytes, &maps.x, col, n0, here + s);
             }
-            if (++j == count) j = 0;
           }
         }
         for (int q = max(g - ring, 0); q < g; ++q) mbar_wait_short(here + q % ring, q / ring & 1);  // no end before that of the copies
@@ -451,10 +449,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       if (!ok) break;
       const uint32_t from = smem_u32(sm + M::kXRing + slot * M::kXBytes);
       uint8_t* b = sm + s * M::kBBytes + high * (M::kRows * 128);
+      uint4 held[kLoads];
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = i / 2 * 32 + tid / 8 * 2 + (high ^ (i & 1));
-        const uint4 v = lds128(from + r * kStep + (((high * 4 + c) ^ (r & 7)) * 16));
+        held[i] = lds128(from + r * kStep + (((high * 4 + c) ^ (r & 7)) * 16));
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i / 2 * 32 + tid / 8 * 2 + (high ^ (i & 1));
+        const uint4 v = held[i];
         uint4 p, q;
         expand(v.x, p.x, p.y);
         expand(v.y, p.z, p.w);
@@ -489,11 +493,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       if (!ok) return;
       tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < kHalf / 16; ++i) {
-        float v[16];
-        tmem_ld16(tm + lanes + wg * kHalf + i * 16, v);
+      for (int i = 0; i < kHalf / 32; ++i) {
+        uint32_t v[32];
+        tmem_load32(tm + lanes + wg * kHalf + i * 32, v);
+        tmem_loaded(v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[i * 16 + e] += __float2int_rn(v[e]);
+        for (int e = 0; e < 32; ++e) sum[i * 32 + e] += __float2int_rn(__uint_as_float(v[e]));
       }
       tc_fence_before();
       __syncwarp();
@@ -509,10 +514,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       float xs[(kHalf + 31) / 32];  // a lane holds every 32nd of the columns' scales
 #pragma unroll
       for (int i = 0; i < kHalf; i += 32) xs[i / 32] = __ldg(a.xs + min(n0 + i + lane, a.n - 1));
+      const int live = row < a.m ? a.n - n0 : 0;
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) {
         const T v = scaled<T>(sum[i], __shfl_sync(0xffffffffu, xs[i / 32], i % 32), ws);
-        if (row < a.m && n0 + i < a.n) *y = v;
+        if (i < live) *y = v;
         y += a.m;
       }
     };
