@@ -210,6 +210,7 @@ struct Tc {
   static constexpr int kW = kRows == 128 ? 4 : 8, kX = kRows == 128 ? 2 : 4;  // steps of codes
   static constexpr int kBBytes = kRows * 256, kWBytes = 128 * kStep, kXBytes = kRows * kStep;
   static constexpr int kWRing = kStages * kBBytes, kXRing = kWRing + kW * kWBytes;
+  static constexpr int kParts = kPair ? 4 : 2, kPart = N / kParts;   // of the columns, each with its products and its sums
   static constexpr int kBars = kXRing + kX * kXBytes, kBytes = kBars + 512 + 1024;
   static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
   static_assert(N <= 256 && kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars && kBytes <= 232000, "room");
@@ -306,6 +307,26 @@ __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
+// sum += v, a whole number of up to 2^24, and a sum in fp32, rounded once.  The machine's conversions pass one lane in eight
+// a clock; done by a conversion and by arithmetic in turn, the two keep pace.
+__device__ __forceinline__ void add_whole(int& sum, float v, bool arithmetic) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
+  constexpr uint32_t kBits = 0x4b400000;
+  if (arithmetic) {
+    const float t = __fmaf_rn(v, 0x1p-12f, kMagic), low = __fmaf_rn(t - kMagic, -4096.f, v) + kMagic;  // v = 4096 t + low
+    sum = static_cast<int>(static_cast<uint32_t>(sum) + __float_as_uint(t) * 4096u + __float_as_uint(low) - (kBits * 4096u + kBits));
+  } else {
+    sum += __float2int_rn(v);
+  }
+}
+__device__ __forceinline__ float to_float(int v, bool arithmetic) {
+  if (!arithmetic) return __int2float_rn(v);
+  // v = 65536 high + low, both exact by 2^23 and their bits
+  const float low = __uint_as_float(__byte_perm(v, 0x4b000000, 0x7610)) - 8388608.f;
+  const float high = __uint_as_float(__byte_perm(v ^ 0x80000000, 0x4b000000, 0x7632)) - (8388608.f + 32768.f);
+  return __fmaf_rn(high, 65536.f, low);
+}
+
 // Threads: eight warps for weights, four for activations, four of which one issues.  A pair's sums take 128 registers a thread:
 // of the launch's 512 x 128 registers the first eight warps' threads take 200, the next four's 80, the last four's 24
 // (504 x 128 in all).
@@ -313,14 +334,14 @@ constexpr int kTcThreads = 512;
 template <typename T, int N, bool kPair>
 __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const __grid_constant__ Maps maps) {
   using M = Tc<N, kPair>;
-  constexpr int S = M::kStages, kHalf = N / 2;  // columns of a half
+  constexpr int S = M::kStages, kHalf = N / 2, P = M::kParts, kPart = M::kPart;  // columns of four warps, of a part
   extern __shared__ __align__(16) uint8_t smraw[];
   __shared__ int failed;
   uint8_t* sm = smraw + (-smem_u32(smraw) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + M::kBars);  // [step % S]: expanded
   uint64_t* empty = full + S;                                   // and used up
-  uint64_t *done = empty + S, *taken = done + 2;                // [half]: a chunk's products; its sums read
-  uint64_t* drained = taken + 2;                                // nothing under way
+  uint64_t *done = empty + S, *taken = done + P;                // [part]: a chunk's products; its sums read
+  uint64_t* drained = taken + P;                                // nothing under way
   uint64_t *w_here = drained + 1, *w_free = w_here + M::kW;     // [step % kW]: codes of weights
   uint64_t *x_here = w_free + M::kW, *x_free = x_here + M::kX;  // [step % kX]: codes of activations
   uint32_t* tbase = reinterpret_cast<uint32_t*>(x_free + M::kX);
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       mbar_init(full + i, kPair ? 16 : 8);
       mbar_init(empty + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < P; ++i) {
       mbar_init(done + i, 1);
       mbar_init(taken + i, kPair ? 8 : 4);
     }
@@ -387,17 +408,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
             const uint32_t ta = tm + M::kA + s * 64;
             const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (starts && chunk > 0) ok = mbar_wait_short(taken + h, (chunk - 1) & 1, a.tries);
+            for (int p = 0; p < P; ++p) {
+              if (starts && chunk > 0) ok = mbar_wait_short(taken + p, (chunk - 1) & 1, a.tries);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < kStep / 16; ++k)
-                mma_tmem_a<kPair>(tm + h * kHalf, ta + k * 8,
-                                  b + ((h * (M::kRows / 2) * 128 + k / 4 * (M::kRows * 128) + k % 4 * 32) >> 4),
-                                  idesc_f16(kTile, kHalf), !starts || k > 0);
-              if (h == 1) commit<kPair>(empty + s);
-              if (ends) commit<kPair>(done + h);
+                mma_tmem_a<kPair>(tm + p * kPart, ta + k * 8,
+                                  b + ((p * (M::kRows / P) * 128 + k / 4 * (M::kRows * 128) + k % 4 * 32) >> 4),
+                                  idesc_f16(kTile, kPart), !starts || k > 0);
+              if (p == P - 1) commit<kPair>(empty + s);
+              if (ends) commit<kPair>(done + p);
             }
             if (ends) ++chunk;
           }
@@ -423,8 +444,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
             if (w) {
               tma_box(to + s * M::kWBytes, &maps.w, col, row, here + s);
             } else if constexpr (kPair) {
-              tma_box(to + s * M::kXBytes, &maps.x, col, n0 + side * 64, here + s);
-              tma_box(to + s * M::kXBytes + M::kXBytes / 2, &maps.x, col, n0 + kHalf + side * 64, here + s);
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+                tma_box(to + s * M::kXBytes + p * (M::kXBytes / P), &maps.x, col, n0 + p * kPart + side * (kPart / 2), here + s);
             } else {
               tma_box(to + s * M::kXBytes, &maps.x, col, n0, here + s);
             }
@@ -489,58 +511,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     for (int i = 0; i < kHalf; ++i) sum[i] = 0;
     int chunk = 0, tile = 0, in_tile = 0, last = min(kChunk, count) - 1;  // the chunk to take: its tile, place there, last step
     auto take = [&] {
-      ok = __all_sync(0xffffffffu, mbar_wait_short(done + wg, chunk & 1, a.tries));
-      if (!ok) return;
-      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < kHalf / 32; ++i) {
-        uint32_t v[32];
-        tmem_load32(tm + lanes + wg * kHalf + i * 32, v);
-        tmem_loaded(v);
+      for (int p = 0; p < P / 2; ++p) {
+        const int part = wg * (P / 2) + p;
+        ok = __all_sync(0xffffffffu, mbar_wait_short(done + part, chunk & 1, a.tries));
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[i * 32 + e] += __float2int_rn(__uint_as_float(v[e]));
+        for (int i = 0; i < kPart; i += 32) {
+          uint32_t v[32];
+          tmem_load32(tm + lanes + part * kPart + i, v);
+          tmem_loaded(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) add_whole(sum[p * kPart + i + e], __uint_as_float(v[e]), e % 2);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(taken + part);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(taken + wg);
       ++chunk;
     };
-    // a tile's results, two threads a row; a wait that gave up leaves no numbers
-    auto write = [&](bool good) {
+    // a tile's results, two threads a row
+    auto write = [&] {
       const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
       const int row = t % row_tiles * kTile + side * 128 + in + lane;
       T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
-      const float ws = good ? __ldg(a.ws + min(row, a.m - 1)) : __uint_as_float(0x7fc00000u);
+      const float ws = __ldg(a.ws + min(row, a.m - 1));
       float xs[(kHalf + 31) / 32];  // a lane holds every 32nd of the columns' scales
 #pragma unroll
       for (int i = 0; i < kHalf; i += 32) xs[i / 32] = __ldg(a.xs + min(n0 + i + lane, a.n - 1));
       const int live = row < a.m ? a.n - n0 : 0;
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) {
-        const T v = scaled<T>(sum[i], __shfl_sync(0xffffffffu, xs[i / 32], i % 32), ws);
+        const T v = from_f<T>(to_float(sum[i], i % 2) * __shfl_sync(0xffffffffu, xs[i / 32], i % 32) * ws);
         if (i < live) *y = v;
         y += a.m;
+        sum[i] = 0;
       }
     };
-    // takes the chunk, and writes the tile that ends with it
-    auto step_on = [&] {
-      take();
-      if (!ok) return;
-      if (++in_tile == chunks) {
-        if (ranks == 1) {
-          write(true);
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) sum[i] = 0;
-        }
-        in_tile = 0, ++tile;
-      }
-      last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
-    };
-    for (int g = wg; g < all && ok; g += 2) {
+    for (int g = wg; ok && tile < mine; g += 2) {
       const int s = g % S, slot = g % M::kW;
-      // a chunk whose last step has to leave its stage before this one can come is done at once, and waited for
-      while (tile < mine && last <= g - S && ok) step_on();
-      if (!ok) break;
+      // A chunk whose last step has to leave its stage before this one can come is done at once, and waited for.  Behind the
+      // last step, those that are left.
+      while (ok && tile < mine && (last <= g - S || g >= all)) {
+        take();
+        if (ok && ++in_tile == chunks) {
+          if (ranks == 1) write();
+          in_tile = 0, ++tile;
+        }
+        last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
+      }
+      if (!ok || g >= all) continue;
       ok = mbar_wait_short(w_here + slot, g / M::kW & 1, a.tries);
       if (g >= S) ok = ok && mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries);
       ok = __all_sync(0xffffffffu, ok);
@@ -567,11 +588,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
         mbar_arrive(w_free + slot);
       }
     }
-    while (tile < mine && ok) step_on();
     if (!ok) {
       if (lane == 0) failed = 1;
-      if (ranks == 1)
-        for (; tile < mine; ++tile) write(false);
+      // a wait that gave up leaves no numbers
+      for (; ranks == 1 && tile < mine; ++tile) {
+        const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
+        const int row = t % row_tiles * kTile + side * 128 + in + lane;
+#pragma unroll 1
+        for (int i = n0; row < a.m && i < min(n0 + kHalf, a.n); ++i)
+          static_cast<T*>(a.y)[static_cast<size_t>(i) * a.m + row] = from_f<T>(__uint_as_float(0x7fc00000u));
+      }
     }
     if (ranks > 1) {
       named_bar(1, 256);  // every operand is used up
@@ -667,7 +693,7 @@ int launch_tc(const Q8Args& a, cudaStream_t st) {
   const long long tiles = static_cast<long long>(rows) * cols;
   Maps maps;
   if (!allow_smem<k_q8_tc<T, N, kPair>, M::kBytes>() || !code_map(&maps.w, a.w, a.m, a.k, 128) ||
-      !code_map(&maps.x, a.x, a.n, a.k, kPair ? 64 : N))
+      !code_map(&maps.x, a.x, a.n, a.k, kPair ? M::kPart / 2 : N))
     return S2_ECUDA;
   if (kPair)
     return launch_clusters(k_q8_tc<T, N, kPair>, dim3(2 * static_cast<unsigned>(std::min(tiles, 76ll))), dim3(2), kTcThreads,
