@@ -49,7 +49,10 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gm
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(live ? 16 : 0) : "memory");
 }
 
+// (.aligned: a warp arrives as one.  What comes before may have been done by some of its lanes alone, and a warp that is still
+// apart would count more than once, so that the other block could leave early.)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ int ld_cluster_int(uint32_t addr, uint32_t rank) {
@@ -206,18 +209,24 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
 template <int N, bool kPair>
 struct Tc {
   static constexpr int kRows = kPair ? N / 2 : N;                   // of activations in a block
-  static constexpr int kStages = 4;                                 // expanded steps: 64 tensor memory columns and B each
-  static constexpr int kW = kRows == 128 ? 4 : 8, kX = kRows == 128 ? 2 : 4;  // steps of codes
+  static constexpr int kStages = kRows == 128 ? 3 : 4;              // expanded steps: 64 tensor memory columns and B each
+  // Steps of codes.  A place of the weights' is always the same four warps': copies may land out of order, and a warp that had
+  // not waited for a place's former step could take that step's phase, still open, for its own (waits know a phase's parity).
+  static constexpr int kW = kRows == 128 ? 4 : 6, kX = kRows == 128 ? 3 : 4;
+  static_assert(kW % 2 == 0, "a place's steps are of one parity");
   static constexpr int kBBytes = kRows * 256, kWBytes = 128 * kStep, kXBytes = kRows * kStep;
   static constexpr int kWRing = kStages * kBBytes, kXRing = kWRing + kW * kWBytes;
   static constexpr int kParts = kPair ? 4 : 2, kPart = N / kParts;   // of the columns, each with its products and its sums
-  static constexpr int kBars = kXRing + kX * kXBytes, kBytes = kBars + 512 + 1024;
+  static constexpr int kOut = kXRing + kX * kXBytes, kOutWarp = 2048;  // results on their way, of a warp
+  static constexpr int kBars = kOut + 8 * kOutWarp, kBytes = kBars + 512 + 1024;
   static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
   static_assert(N <= 256 && kA + 64 * kStages <= kCols && N * 128 * 4 <= kBars && kBytes <= 232000, "room");
 };
 
 struct Maps {
   CUtensorMap w, x;  // codes as [rows][k]: boxes of 128 columns, swizzled
+  CUtensorMap y;     // results, where `bulk`: boxes of 32 weight rows
+  bool bulk;
 };
 
 // Box at (column, row) of a tensor map into shared memory.
@@ -253,18 +262,33 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // not used before
 }
-template <bool kPair>
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  if constexpr (!kPair) {
-    tc_mma_tmem_a(d, a, b, idesc, accum);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accum)
-        : "memory");
-  }
+// A step's products with one part of the columns: eight of 16 columns of K.  b: the low word of the part's descriptor, whose
+// address is the only thing that moves (bits 0 - 13, in 16 bytes); kFar: from K's first 64 columns to the second.
+template <bool kPair, int kFar>
+__device__ __forceinline__ void mma_part(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t idesc, bool add) {
+#define S2_MMA(group)                                                                                         \
+  asm volatile(                                                                                               \
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 d0, d1, d2, d3, d4, d5, d6, d7;\n\t"                                \
+      "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, %4, %4;\n\t"                                                  \
+      "mov.b64 d0, {%5, %3};\n\tmov.b64 d1, {%6, %3};\n\tmov.b64 d2, {%7, %3};\n\tmov.b64 d3, {%8, %3};\n\t" \
+      "mov.b64 d4, {%9, %3};\n\tmov.b64 d5, {%10, %3};\n\tmov.b64 d6, {%11, %3};\n\tmov.b64 d7, {%12, %3};\n\t" \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%1], d0, %2, p;\n\t"                                 \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%13], d1, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%14], d2, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%15], d3, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%16], d4, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%17], d5, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%18], d6, %2, q;\n\t"                                \
+      "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [%19], d7, %2, q;\n\t}"                               \
+      ::"r"(d), "r"(a), "r"(idesc), "r"(b_high), "r"(static_cast<uint32_t>(add)), "r"(b), "r"(b + 2), "r"(b + 4), "r"(b + 6), \
+      "r"(b + kFar), "r"(b + kFar + 2), "r"(b + kFar + 4), "r"(b + kFar + 6), "r"(a + 8), "r"(a + 16), "r"(a + 24),           \
+      "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56)                                                      \
+      : "memory")
+  if constexpr (kPair)
+    S2_MMA("2");
+  else
+    S2_MMA("1");
+#undef S2_MMA
 }
 // An arrival at `bar` (in both blocks of a pair) when the products issued so far are done.
 template <bool kPair>
@@ -307,29 +331,8 @@ __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// sum += v, a whole number of up to 2^24, and a sum in fp32, rounded once.  The machine's conversions pass one lane in eight
-// a clock; done by a conversion and by arithmetic in turn, the two keep pace.
-__device__ __forceinline__ void add_whole(int& sum, float v, bool arithmetic) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
-  constexpr uint32_t kBits = 0x4b400000;
-  if (arithmetic) {
-    const float t = __fmaf_rn(v, 0x1p-12f, kMagic), low = __fmaf_rn(t - kMagic, -4096.f, v) + kMagic;  // v = 4096 t + low
-    sum = static_cast<int>(static_cast<uint32_t>(sum) + __float_as_uint(t) * 4096u + __float_as_uint(low) - (kBits * 4096u + kBits));
-  } else {
-    sum += __float2int_rn(v);
-  }
-}
-__device__ __forceinline__ float to_float(int v, bool arithmetic) {
-  if (!arithmetic) return __int2float_rn(v);
-  // v = 65536 high + low, both exact by 2^23 and their bits
-  const float low = __uint_as_float(__byte_perm(v, 0x4b000000, 0x7610)) - 8388608.f;
-  const float high = __uint_as_float(__byte_perm(v ^ 0x80000000, 0x4b000000, 0x7632)) - (8388608.f + 32768.f);
-  return __fmaf_rn(high, 65536.f, low);
-}
-
 // Threads: eight warps for weights, four for activations, four of which one issues.  A pair's sums take 128 registers a thread:
-// of the launch's 512 x 128 registers the first eight warps' threads take 200, the next four's 80, the last four's 24
-// (504 x 128 in all).
+// of the launch's 512 x 128 registers the first eight warps' threads take 208, the next four's 72, the last four's 24.
 constexpr int kTcThreads = 512;
 template <typename T, int N, bool kPair>
 __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const __grid_constant__ Maps maps) {
@@ -412,11 +415,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
               if (starts && chunk > 0) ok = mbar_wait_short(taken + p, (chunk - 1) & 1, a.tries);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kStep / 16; ++k)
-                mma_tmem_a<kPair>(tm + p * kPart, ta + k * 8,
-                                  b + ((p * (M::kRows / P) * 128 + k / 4 * (M::kRows * 128) + k % 4 * 32) >> 4),
-                                  idesc_f16(kTile, kPart), !starts || k > 0);
+              mma_part<kPair, M::kRows * 8>(tm + p * kPart, ta, static_cast<uint32_t>(b) + p * (M::kRows / P) * 8,
+                                            static_cast<uint32_t>(b >> 32), idesc_f16(kTile, kPart), !starts);
               if (p == P - 1) commit<kPair>(empty + s);
               if (ends) commit<kPair>(done + p);
             }
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- expanding activations
-    if constexpr (N >= 128) fewer_registers<80>();
+    if constexpr (N >= 128) fewer_registers<72>();
     // Eight lanes take the low half of a row's 128 codes and the high half of its neighbour's, then the other two: neither
     // reading the swizzled codes nor writing the swizzled tiles, in which the halves are apart, meets a bank twice.
     constexpr int kLoads = M::kRows / 16;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
       ok = __all_sync(0xffffffffu, mbar_wait_short(empty + g % S, g / S & 1, a.tries));
   } else {
     // ---------------------------------------------------------------- expanding weights, adding up
-    if constexpr (N >= 128) more_registers<200>();
+    if constexpr (N >= 128) more_registers<208>();
     const int wg = warp / 4, in = warp % 4 * 32;
     const int all = mine * count;
     const uint32_t lanes = static_cast<uint32_t>(in) << 16, tlane = tm + M::kA + lanes;
@@ -517,50 +517,94 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
         ok = __all_sync(0xffffffffu, mbar_wait_short(done + part, chunk & 1, a.tries));
         if (!ok) return;
         tc_fence_after();
+        uint32_t v[kPart / 32][32];
 #pragma unroll
-        for (int i = 0; i < kPart; i += 32) {
-          uint32_t v[32];
-          tmem_load32(tm + lanes + part * kPart + i, v);
-          tmem_loaded(v);
+        for (int i = 0; i < kPart / 32; ++i) tmem_load32(tm + lanes + part * kPart + i * 32, v[i]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) add_whole(sum[p * kPart + i + e], __uint_as_float(v[e]), e % 2);
-        }
+        for (int i = 0; i < kPart / 32; ++i) tmem_loaded(v[i]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive(taken + part);
+        if (lane == 0) arrive(taken + part);  // the next chunk's products may start
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) sum[p * kPart + i] += __float2int_rn(__uint_as_float(v[i / 32][i % 32]));
       }
       ++chunk;
     };
-    // a tile's results, two threads a row
-    auto write = [&] {
-      const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
-      const int row = t % row_tiles * kTile + side * 128 + in + lane;
-      T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row;
-      const float ws = __ldg(a.ws + min(row, a.m - 1));
-      float xs[(kHalf + 31) / 32];  // a lane holds every 32nd of the columns' scales
+    // A tile's results, two threads a row; a quarter of a thread's columns after each of the next tile's first steps, by TMA, so
+    // that the tensor core does not wait for them (all at once and by plain stores: 5000 to 7000 clocks).
+    int left = 0, written = 0;  // quarters to write, and their tile
+    float ws = 0.f, xs[4] = {};  // its scales: the thread's row's, and every 32nd (kQ-th) of the columns'
+    constexpr int kQ = kHalf / 4, kC = std::min(kQ, static_cast<int>(M::kOutWarp / 32 / sizeof(T)));  // columns of a quarter, of a box
+    T* const out = reinterpret_cast<T*>(sm + M::kOut + warp * M::kOutWarp);
+    auto row_of = [&](int t) { return t % row_tiles * kTile + side * 128 + in; };
+    auto column_of = [&](int t) { return t / row_tiles * N + wg * kHalf; };
+    auto load_scales = [&] {
+      const int t = first + tile * apart;
+      ws = __ldg(a.ws + min(row_of(t) + lane, a.m - 1));
 #pragma unroll
-      for (int i = 0; i < kHalf; i += 32) xs[i / 32] = __ldg(a.xs + min(n0 + i + lane, a.n - 1));
-      const int live = row < a.m ? a.n - n0 : 0;
+      for (int i = 0; i < 4; ++i) xs[i] = __ldg(a.xs + min(column_of(t) + i * kQ + lane % kQ, a.n - 1));
+    };
+    auto write = [&](auto quarter) {
+      constexpr int q = decltype(quarter)::value;
+      const int t = first + written * apart, row = row_of(t), n0 = column_of(t) + q * kQ;
+      if (maps.bulk) {
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        const T v = from_f<T>(to_float(sum[i], i % 2) * __shfl_sync(0xffffffffu, xs[i / 32], i % 32) * ws);
-        if (i < live) *y = v;
-        y += a.m;
-        sum[i] = 0;
+        for (int c = 0; c < kQ; c += kC) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the box before is read
+          __syncwarp();
+#pragma unroll
+          for (int i = c; i < c + kC; ++i) {
+            out[(i - c) * 32 + lane] = scaled<T>(sum[q * kQ + i], __shfl_sync(0xffffffffu, xs[q], i), ws);
+            sum[q * kQ + i] = 0;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row < a.m && n0 + c < a.n)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(&maps.y),
+                "r"(row), "r"(n0 + c), "r"(smem_u32(out))
+                : "memory");
+          __syncwarp();
+        }
+      } else {
+        T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0) * a.m + row + lane;
+        const int live = row + lane < a.m ? a.n - n0 : 0;
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const T v = scaled<T>(sum[q * kQ + i], __shfl_sync(0xffffffffu, xs[q], i), ws);
+          if (i < live) *y = v;
+          y += a.m;
+          sum[q * kQ + i] = 0;
+        }
       }
     };
-    for (int g = wg; ok && tile < mine; g += 2) {
+    auto write_some = [&] {
+      if (left == 4) write(std::integral_constant<int, 0>{});
+      if (left == 3) write(std::integral_constant<int, 1>{});
+      if (left == 2) write(std::integral_constant<int, 2>{});
+      if (left == 1) write(std::integral_constant<int, 3>{});
+      --left;
+    };
+    for (int g = wg; ok && (tile < mine || left > 0); g += 2) {
       const int s = g % S, slot = g % M::kW;
       // A chunk whose last step has to leave its stage before this one can come is done at once, and waited for.  Behind the
       // last step, those that are left.
-      while (ok && tile < mine && (last <= g - S || g >= all)) {
-        take();
-        if (ok && ++in_tile == chunks) {
-          if (ranks == 1) write();
-          in_tile = 0, ++tile;
+      bool due;
+      do {
+        due = tile < mine && (last <= g - S || g >= all);
+        if (left > 0) {
+          write_some();
+        } else if (due) {
+          if (in_tile == chunks - 1) load_scales();
+          take();
+          if (ok && ++in_tile == chunks) {
+            if (ranks == 1) left = 4, written = tile;
+            in_tile = 0, ++tile;
+          }
+          last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
         }
-        last = tile * count + min((in_tile + 1) * kChunk, count) - 1;
-      }
+      } while (ok && due);
       if (!ok || g >= all) continue;
       ok = mbar_wait_short(w_here + slot, g / M::kW & 1, a.tries);
       if (g >= S) ok = ok && mbar_wait_short(empty + s, (g / S - 1) & 1, a.tries);
@@ -591,14 +635,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     if (!ok) {
       if (lane == 0) failed = 1;
       // a wait that gave up leaves no numbers
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // none of its results come later
+      __syncwarp();
+      if (left > 0) tile = written;
       for (; ranks == 1 && tile < mine; ++tile) {
-        const int t = first + tile * apart, n0 = t / row_tiles * N + wg * kHalf;
-        const int row = t % row_tiles * kTile + side * 128 + in + lane;
+        const int t = first + tile * apart, n0 = column_of(t), row = row_of(t) + lane;
 #pragma unroll 1
         for (int i = n0; row < a.m && i < min(n0 + kHalf, a.n); ++i)
           static_cast<T*>(a.y)[static_cast<size_t>(i) * a.m + row] = from_f<T>(__uint_as_float(0x7fc00000u));
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
     if (ranks > 1) {
       named_bar(1, 256);  // every operand is used up
       int* out = reinterpret_cast<int*>(sm);  // [column][row], where the operands were
@@ -668,8 +716,7 @@ int launch_few(const Q8Args& a, cudaStream_t st) {
   return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, st, a);
 }
 
-// Boxes of `box` rows by 128 columns of codes [rows][k], swizzled in 128 bytes; zeros outside.
-bool code_map(CUtensorMap* map, const int8_t* codes, long long rows, int k, int box) {
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -678,11 +725,30 @@ bool code_map(CUtensorMap* map, const int8_t* codes, long long rows, int k, int 
                ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
                : nullptr;
   }();
+  return encode;
+}
+// Boxes of `box` rows by 128 columns of codes [rows][k], swizzled in 128 bytes; zeros outside.
+bool code_map(CUtensorMap* map, const int8_t* codes, long long rows, int k, int box) {
+  const auto encode = encoder();
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)}, stride[1] = {static_cast<cuuint64_t>(k)};
   const cuuint32_t boxes[2] = {kStep, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
   return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, stride, boxes, ones,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Boxes of 32 weight rows by `box` activation rows of results [n][m], where their rows start on 16 bytes.
+template <typename T>
+bool result_map(CUtensorMap* map, void* y, int n, int m, int box) {
+  const long long stride = static_cast<long long>(m) * sizeof(T);
+  const auto encode = encoder();
+  if (reinterpret_cast<uintptr_t>(y) % 16 != 0 || stride % 16 != 0 || !encode) return false;
+  const CUtensorMapDataType type = std::is_same<T, float>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m), static_cast<cuuint64_t>(n)}, strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t boxes[2] = {32, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return encode(map, type, 2, y, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int N, bool kPair>
@@ -695,6 +761,7 @@ int launch_tc(const Q8Args& a, cudaStream_t st) {
   if (!allow_smem<k_q8_tc<T, N, kPair>, M::kBytes>() || !code_map(&maps.w, a.w, a.m, a.k, 128) ||
       !code_map(&maps.x, a.x, a.n, a.k, kPair ? M::kPart / 2 : N))
     return S2_ECUDA;
+  maps.bulk = result_map<T>(&maps.y, a.y, a.n, a.m, std::min(N / 8, static_cast<int>(M::kOutWarp / 32 / sizeof(T))));
   if (kPair)
     return launch_clusters(k_q8_tc<T, N, kPair>, dim3(2 * static_cast<unsigned>(std::min(tiles, 76ll))), dim3(2), kTcThreads,
                            M::kBytes, st, a, maps);
