@@ -216,7 +216,7 @@ struct Tc {
   static_assert(kW % 2 == 0, "a place's steps are of one parity");
   static constexpr int kBBytes = kRows * 256, kWBytes = 128 * kStep, kXBytes = kRows * kStep;
   static constexpr int kWRing = kStages * kBBytes, kXRing = kWRing + kW * kWBytes;
-  static constexpr int kParts = kPair ? 4 : 2, kPart = N / kParts;   // of the columns, each with its products and its sums
+  static constexpr int kParts = 2, kPart = N / kParts;   // of the columns, each with its products and its sums
   static constexpr int kOut = kXRing + kX * kXBytes, kOutWarp = 2048;  // results on their way, of a warp
   static constexpr int kBars = kOut + 8 * kOutWarp, kBytes = kBars + 512 + 1024;
   static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
@@ -245,6 +245,16 @@ __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
       "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
+}
+// Whether a phase is done, without waiting.
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // 32 columns of tensor memory; their values are there after tmem_loaded().
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
@@ -331,6 +341,19 @@ __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
+// sum += v, a whole number of up to 2^24.  The machine's conversion passes one lane in eight a clock; by arithmetic it takes
+// six instructions.  Where the next part's products wait, half of them go each way.
+__device__ __forceinline__ void add_whole(int& sum, float v, bool arithmetic) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
+  constexpr uint32_t kBits = 0x4b400000;
+  if (arithmetic) {
+    const float t = __fmaf_rn(v, 0x1p-12f, kMagic), low = __fmaf_rn(t - kMagic, -4096.f, v) + kMagic;  // v = 4096 t + low
+    sum = static_cast<int>(static_cast<uint32_t>(sum) + __float_as_uint(t) * 4096u + __float_as_uint(low) - (kBits * 4096u + kBits));
+  } else {
+    sum += __float2int_rn(v);
+  }
+}
+
 // Threads: eight warps for weights, four for activations, four of which one issues.  A pair's sums take 128 registers a thread:
 // of the launch's 512 x 128 registers the first eight warps' threads take 208, the next four's 72, the last four's 24.
 constexpr int kTcThreads = 512;
@@ -367,7 +390,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     }
     for (int i = 0; i < P; ++i) {
       mbar_init(done + i, 1);
-      mbar_init(taken + i, kPair ? 8 : 4);
+      mbar_init(taken + i, (kPair ? 8 : 4) * 2 / P);
     }
     mbar_init(drained, 1);
     for (int i = 0; i < M::kW; ++i) {
@@ -401,27 +424,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     if constexpr (N >= 128) fewer_registers<24>();
     if (warp == 12 && side == 0) {
       if (elect_one()) {
-        int g = 0, chunk = 0;  // over all tiles
-        for (int i = 0; i < mine && ok; ++i)
-          for (int j = 0; j < count && ok; ++j, ++g) {
-            const int s = g % S;
-            const bool starts = j % kChunk == 0, ends = j % kChunk == kChunk - 1 || j == count - 1;
-            ok = mbar_wait_short(full + s, g / S & 1, a.tries);
-            if (!ok) break;
-            const uint32_t ta = tm + M::kA + s * 64;
-            const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
+        int chunk = 0, j = 0, s = 0;  // chunks so far; the step's place in its tile, its stage
+        bool here = false;            // whether the step is known to be expanded
+        for (int g = 0, all = mine * count; g < all; ++g) {
+          const bool starts = j % kChunk == 0, ends = j % kChunk == kChunk - 1 || j == count - 1;
+          ok = here || mbar_wait_short(full + s, g / S & 1, a.tries);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = tm + M::kA + s * 64;
+          const uint64_t b = desc_sw128(smem_u32(sm + s * M::kBBytes));
+          const int next = s + 1 == S ? 0 : s + 1;
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-              if (starts && chunk > 0) ok = mbar_wait_short(taken + p, (chunk - 1) & 1, a.tries);
+          for (int p = 0; p < P; ++p) {
+            if (starts && chunk > 0) {
+              ok = mbar_wait_short(taken + p, (chunk - 1) & 1, a.tries);
               if (!ok) break;
               tc_fence_after();
-              mma_part<kPair, M::kRows * 8>(tm + p * kPart, ta, static_cast<uint32_t>(b) + p * (M::kRows / P) * 8,
-                                            static_cast<uint32_t>(b >> 32), idesc_f16(kTile, kPart), !starts);
-              if (p == P - 1) commit<kPair>(empty + s);
-              if (ends) commit<kPair>(done + p);
             }
-            if (ends) ++chunk;
+            // the next step is looked for while products are left to do
+            if (p == P - 1) here = g + 1 < all && mbar_done(full + next, (g + 1) / S & 1);
+            mma_part<kPair, M::kRows * 8>(tm + p * kPart, ta, static_cast<uint32_t>(b) + p * (M::kRows / P) * 8,
+                                          static_cast<uint32_t>(b >> 32), idesc_f16(kTile, kPart), !starts);
+            if (p == P - 1) commit<kPair>(empty + s);
+            if (ends) commit<kPair>(done + p);
           }
+          if (!ok) break;
+          if (ends) ++chunk;
+          if (++j == count) j = 0;
+          s = next;
+        }
         commit_here<kPair>(drained);  // no end before that of the products, whoever gave up
         mbar_wait_short(drained, 0);
       }
@@ -510,23 +541,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) sum[i] = 0;
     int chunk = 0, tile = 0, in_tile = 0, last = min(kChunk, count) - 1;  // the chunk to take: its tile, place there, last step
+    const int part = wg * P / 2;
     auto take = [&] {
+      ok = __all_sync(0xffffffffu, mbar_wait_short(done + part, chunk & 1, a.tries));
+      if (!ok) return;
+      tc_fence_after();
+      constexpr int kPass = std::min(kHalf, 64);
 #pragma unroll
-      for (int p = 0; p < P / 2; ++p) {
-        const int part = wg * (P / 2) + p;
-        ok = __all_sync(0xffffffffu, mbar_wait_short(done + part, chunk & 1, a.tries));
-        if (!ok) return;
-        tc_fence_after();
-        uint32_t v[kPart / 32][32];
+      for (int c = 0; c < kHalf; c += kPass) {
+        uint32_t v[kPass / 32][32];
 #pragma unroll
-        for (int i = 0; i < kPart / 32; ++i) tmem_load32(tm + lanes + part * kPart + i * 32, v[i]);
+        for (int i = 0; i < kPass / 32; ++i) tmem_load32(tm + lanes + wg * kHalf + c + i * 32, v[i]);
 #pragma unroll
-        for (int i = 0; i < kPart / 32; ++i) tmem_loaded(v[i]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(taken + part);  // the next chunk's products may start
+        for (int i = 0; i < kPass / 32; ++i) tmem_loaded(v[i]);
+        if (c + kPass == kHalf) {  // the next chunk's products may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(taken + part);
+        }
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) sum[p * kPart + i] += __float2int_rn(__uint_as_float(v[i / 32][i % 32]));
+        for (int i = 0; i < kPass; ++i) add_whole(sum[c + i], __uint_as_float(v[i / 32][i % 32]), c + kPass < kHalf && i % 2);
       }
       ++chunk;
     };
@@ -588,11 +622,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     };
     for (int g = wg; ok && (tile < mine || left > 0); g += 2) {
       const int s = g % S, slot = g % M::kW;
-      // A chunk whose last step has to leave its stage before this one can come is done at once, and waited for.  Behind the
-      // last step, those that are left.
+      // A chunk is taken when it is done.  One whose last step has to leave its stage before this one can come is waited for, and
+      // behind the last step those that are left.
       bool due;
       do {
-        due = tile < mine && (last <= g - S || g >= all);
+        due = tile < mine &&
+              (last <= g - S || g >= all || (last < g && __all_sync(0xffffffffu, mbar_done(done + part, chunk & 1))));
         if (left > 0) {
           write_some();
         } else if (due) {
