@@ -63,6 +63,15 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr, uint32_t rank) {
+  int4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(addr), "r"(rank));
+  return v;
+}
+
 template <typename T>
 __device__ __forceinline__ T scaled(int sum, float xs, float ws) {
   return from_f<T>(__int2float_rn(sum) * xs * ws);
@@ -691,23 +700,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
   }
   if constexpr (!kPair) {
     if (ranks > 1) {
-      const int r = threadIdx.x % 128, part = threadIdx.x / 128;
-      const int row = first % row_tiles * 128 + r, n0 = first / row_tiles * N, nn = min(N, a.n - n0);
-      const int* out = reinterpret_cast<const int*>(sm);
       cluster_sync();
-      int bad = 0;
+      if (warp < 8) {  // the others have few registers left; four rows of a column a thread
+        const int r = lane * 4, row = first % row_tiles * 128 + r, n0 = first / row_tiles * N, nn = min(N, a.n - n0);
+        const int* out = reinterpret_cast<const int*>(sm);
+        int bad = 0;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < ranks) bad |= ld_cluster_int(smem_u32(&failed), q);
-      const float ws = bad ? __uint_as_float(0x7fc00000u) : __ldg(a.ws + min(row, a.m - 1));
-      for (int col = part * ranks + rank; col < nn; col += 4 * ranks) {
-        int v[8], total = 0;
+        for (int q = 0; q < 8; ++q)
+          if (q < ranks) bad |= ld_cluster_int(smem_u32(&failed), q);
+        float ws[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = q < ranks ? ld_cluster_int(smem_u32(out + col * 128 + r), q) : 0;
+        for (int e = 0; e < 4; ++e) ws[e] = bad ? __uint_as_float(0x7fc00000u) : __ldg(a.ws + min(row + e, a.m - 1));
+#pragma unroll 2
+        for (int col = warp * ranks + rank; col < nn; col += 8 * ranks) {
+          int4 v[8];
+          int total[4] = {};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) total += v[q];
-        if (row < a.m)
-          static_cast<T*>(a.y)[static_cast<size_t>(n0 + col) * a.m + row] = scaled<T>(total, __ldg(a.xs + n0 + col), ws);
+          for (int q = 0; q < 8; ++q) v[q] = q < ranks ? ld_cluster_int4(smem_u32(out + col * 128 + r), q) : make_int4(0, 0, 0, 0);
+          const float xs = __ldg(a.xs + n0 + col);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) total[0] += v[q].x, total[1] += v[q].y, total[2] += v[q].z, total[3] += v[q].w;
+          T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0 + col) * a.m + row;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (row + e < a.m) y[e] = scaled<T>(total[e], xs, ws[e]);
+        }
       }
       cluster_sync();  // no block leaves while its sums are read
     }
@@ -741,13 +758,44 @@ int launch_clusters(void (*kernel)(Args...), dim3 grid, dim3 cluster, int thread
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
+// Blocks that split W's columns for each of `groups` tiles: the most, up to eight and `most`, whose clusters the device
+// holds at a time.  (It takes whole clusters in whole groups of its SMs, so many sizes leave SMs over: 20 clusters of seven
+// blocks of k_q8_tc take two rounds, 22 us for 64 rows of 2560 x 9728 against 15 with six.)  What it holds is asked once.
+template <auto kKernel>
+int split(long long groups, int most, int threads, int smem) {
+  static std::atomic<int> held[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  for (int ranks = std::min(8, most); ranks > 1; --ranks) {
+    int n = dev < 64 ? held[dev][ranks].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(1, ranks);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 1;
+      at[0].val.clusterDim.y = ranks;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // not a failure of the call's
+        n = -1;
+      }
+      if (dev < 64) held[dev][ranks].store(n, std::memory_order_relaxed);
+    }
+    if (groups <= n) return ranks;
+  }
+  return 1;
+}
+
 template <typename T, int NT>
 int launch_few(const Q8Args& a, cudaStream_t st) {
   const int rows = (a.m + kFewRows - 1) / kFewRows, cols = (a.n + NT * 8 - 1) / (NT * 8), steps = (a.k + kStep - 1) / kStep;
-  // two blocks an SM (one, where it holds no more), of two steps at least
-  const long long groups = static_cast<long long>(rows) * cols;
-  const int ranks = std::max(1, std::min({8, static_cast<int>((NT == 4 ? 152 : 304) / groups), steps / 2}));
   if (!allow_smem<k_q8_few<T, NT>, kFewBytes<NT>>()) return S2_ECUDA;
+  const int ranks = split<k_q8_few<T, NT>>(static_cast<long long>(rows) * cols, steps / 2, 32 * kFewWarps, kFewBytes<NT>);
   return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, st, a);
 }
 
@@ -786,23 +834,53 @@ bool result_map(CUtensorMap* map, void* y, int n, int m, int box) {
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch of k_q8_tc: what it splits, and what it takes, in ns.
+struct Plan {
+  int blocks, ranks;
+  double time;
+};
+// A block has 5.5 to 7.5 us of launch, filling and draining, and a time a step; blocks at work together are a round.  A join
+// costs by its columns.  Measured, us, at (rows) for one column tile of 64 and 128 and a pair's 256, weights not in L2:
+// 19456 x 2560 (64) 16.2, 18.7, 22.3; (128) 27.1, 19.1, 22.5; (256) 48.8, 32.1, 23.2; (1024) -, 112, 70; 6144 x 2560 (64) 12.0,
+// 15.3, 20.9; (256) 25.7, 17.7, 21.1; (512) -, 30.8, 21.4; 2560 x 9728 (64) 13.2, 16.0, 55.6; (512) -, 47.5, 56.0.
 template <typename T, int N, bool kPair>
-int launch_tc(const Q8Args& a, cudaStream_t st) {
+Plan plan_tc(const Q8Args& a) {
   using M = Tc<N, kPair>;
-  constexpr int kTile = kPair ? 256 : 128;
-  const int rows = (a.m + kTile - 1) / kTile, cols = (a.n + N - 1) / N, steps = (a.k + kStep - 1) / kStep;
-  const long long tiles = static_cast<long long>(rows) * cols;
+  constexpr int kTile = kPair ? 256 : 128, kAtOnce = kPair ? 76 : 152;
+  constexpr double kFixed = kPair ? 7500 : N == 128 ? 6000 : 5500, kPerStep = kPair ? 720 : N == 128 ? 600 : 500;
+  constexpr double kPerColumn = N == 128 ? 45 : 20;
+  const int steps = (a.k + kStep - 1) / kStep;
+  const long long tiles = static_cast<long long>((a.m + kTile - 1) / kTile) * ((a.n + N - 1) / N);
+  Plan p{};
+  p.ranks = kPair ? 1 : split<k_q8_tc<T, N, kPair>>(tiles, steps / 4, kTcThreads, M::kBytes);
+  p.blocks = static_cast<int>(p.ranks > 1 ? tiles : std::min<long long>(tiles, kAtOnce));
+  const long long rounds = p.ranks > 1 ? 1 : (tiles + kAtOnce - 1) / kAtOnce;
+  p.time = kFixed + rounds * kPerStep * ((steps + p.ranks - 1) / p.ranks) + (p.ranks > 1 ? 1500 + kPerColumn * std::min(N, a.n) : 0);
+  return p;
+}
+
+template <typename T, int N, bool kPair>
+int launch_tc(const Q8Args& a, const Plan& plan, cudaStream_t st) {
+  using M = Tc<N, kPair>;
   Maps maps;
-  if (!allow_smem<k_q8_tc<T, N, kPair>, M::kBytes>() || !code_map(&maps.w, a.w, a.m, a.k, 128) ||
-      !code_map(&maps.x, a.x, a.n, a.k, kPair ? M::kPart / 2 : N))
-    return S2_ECUDA;
+  if (!code_map(&maps.w, a.w, a.m, a.k, 128) || !code_map(&maps.x, a.x, a.n, a.k, kPair ? M::kPart / 2 : N)) return S2_ECUDA;
   maps.bulk = result_map<T>(&maps.y, a.y, a.n, a.m, std::min(N / 8, static_cast<int>(M::kOutWarp / 32 / sizeof(T))));
-  if (kPair)
-    return launch_clusters(k_q8_tc<T, N, kPair>, dim3(2 * static_cast<unsigned>(std::min(tiles, 76ll))), dim3(2), kTcThreads,
-                           M::kBytes, st, a, maps);
-  const int ranks = std::max(1, std::min({8, static_cast<int>(152 / tiles), steps / 4}));
-  return launch_clusters(k_q8_tc<T, N, kPair>, dim3(static_cast<unsigned>(ranks > 1 ? tiles : std::min(tiles, 152ll)), ranks),
-                         dim3(1, ranks), kTcThreads, M::kBytes, st, a, maps);
+  return launch_clusters(k_q8_tc<T, N, kPair>, dim3(plan.blocks * (kPair ? 2 : 1), plan.ranks),
+                         kPair ? dim3(2) : dim3(1, plan.ranks), kTcThreads, M::kBytes, st, a, maps);
+}
+
+template <typename T>
+int launch_matmul(const Q8Args& a, cudaStream_t st) {
+  // mma.sync up to 16 rows, and up to 64 of a matrix of less than 4 Mi weights (1024 x 1024 6.2 us against 7.2 and 7.9 at 32 and
+  // 64 rows; 2560 x 4096 10.3 against 9.2 at 32).
+  if (a.n <= 16) return a.n <= 8 ? launch_few<T, 1>(a, st) : launch_few<T, 2>(a, st);
+  if (a.n <= 64 && static_cast<long long>(a.m) * a.k < 4ll << 20) return launch_few<T, 4>(a, st);
+  if (!allow_smem<k_q8_tc<T, 64, false>, Tc<64, false>::kBytes>() || !allow_smem<k_q8_tc<T, 128, false>, Tc<128, false>::kBytes>() ||
+      !allow_smem<k_q8_tc<T, 256, true>, Tc<256, true>::kBytes>())
+    return S2_ECUDA;
+  const Plan one = plan_tc<T, 64, false>(a), two = plan_tc<T, 128, false>(a), pair = plan_tc<T, 256, true>(a);
+  if (one.time <= two.time && one.time <= pair.time) return launch_tc<T, 64, false>(a, one, st);
+  return two.time <= pair.time ? launch_tc<T, 128, false>(a, two, st) : launch_tc<T, 256, true>(a, pair, st);
 }
 
 constexpr int kRowsMost = (1 << 21) - 32, kOutMost = 1 << 28, kColsMost = (1 << 17) - 16;  // activation and weight rows; columns
@@ -825,9 +903,6 @@ extern "C" int s2_q8_matmul(int n, const int8_t* x_codes, const float* x_scales,
   const Q8Args a{x_codes, x_scales, codes, scales, y, n, m, k, wait_tries.load(std::memory_order_relaxed)};
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (n <= 32) return n <= 8 ? launch_few<T, 1>(a, st) : n <= 16 ? launch_few<T, 2>(a, st) : launch_few<T, 4>(a, st);
-    if (static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= 76) return launch_tc<T, 256, true>(a, st);
-    return n <= 64 ? launch_tc<T, 64, false>(a, st) : launch_tc<T, 128, false>(a, st);
+    return launch_matmul<T>(a, reinterpret_cast<cudaStream_t>(stream));
   });
 }
