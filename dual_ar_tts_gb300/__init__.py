@@ -244,7 +244,7 @@ def quantize_e4m3(w):
 
 class _Hot:
     """What the calls below use of torch and of the library."""
-    __slots__ = ("torch", "lib", "kinds", "stream", "device", "empty", "u8", "i8", "i32", "f16", "bf16", "f32")
+    __slots__ = ("torch", "lib", "kinds", "stream", "device", "empty", "u8", "i32", "f16", "bf16", "f32")
 
     def __init__(self):
         import torch
@@ -252,7 +252,7 @@ class _Hot:
         self.kinds = {torch.float32: S2_F32, torch.bfloat16: S2_BF16, torch.float16: S2_F16}
         self.stream = torch._C._cuda_getCurrentRawStream     # of a device number, as an integer
         self.device = torch._C._cuda_getDevice               # the current one's number
-        self.u8, self.i8, self.i32 = torch.uint8, torch.int8, torch.int32
+        self.u8, self.i32 = torch.uint8, torch.int32
         self.f16, self.bf16, self.f32 = torch.float16, torch.bfloat16, torch.float32
 
 
@@ -560,171 +560,55 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
 
 # ------------------------------------------- projections in 8-bit integers
 
-def _rows(x):
-    """x [n][k] as rows of neighbouring elements (a copy where they are not), and their stride."""
-    s0, s1 = x.stride()
-    n, k = x.shape
-    if n == 1:  # its stride may be anything
-        s0 = k
-    if (s1 == 1 or k == 1) and s0 >= k:
-        return x, s0
-    return x.contiguous(), k
+# The checks, outputs and launches of these are in csrc/calls.cpp: on a Grace core a call of one row takes 4.4 us there and 13
+# from Python.
+
+_q8 = None
 
 
-def _coded(h, x, cols, codes, scales):
-    """The outputs of a row quantiser: codes and scales given by the caller, or new ones."""
-    rows, pitch = x.shape[0], (cols + 15) & -16
-    if codes is None:
-        codes = h.empty((rows, pitch), dtype=h.i8, device=x.device)
-    elif codes.dtype is not h.i8 or codes.shape != (rows, pitch) or codes.get_device() != x.get_device() or \
-            not codes.is_contiguous() or codes.data_ptr() % 16:
-        _bad("codes must be contiguous int8 [rows][columns rounded up to 16] on the operand's device, from 16 bytes on")
-    if scales is None:
-        scales = h.empty((rows,), dtype=h.f32, device=x.device)
-    elif scales.dtype is not h.f32 or scales.shape != (rows,) or scales.get_device() != x.get_device() or \
-            not scales.is_contiguous():
-        _bad("scales must be contiguous fp32 [rows] on the operand's device")
-    return codes, scales
+def _bind_q8():
+    global _q8
+    import torch  # noqa: F401  (its libraries, which the module is linked against)
+    load()
+    try:
+        from . import _calls as module
+    except ImportError as e:
+        raise ImportError(f"{e}: run `python -c 'import __graft_entry__ as g; g.build()'`") from e
+    module.set_error(S2Error)
+    _q8 = module
+    return module
 
 
 def quantize_q8(x, codes=None, scales=None):
     """Rows [rows][cols] (fp32, bf16 or fp16; weights, or activations) -> (int8 codes [rows][cols rounded up to 16], fp32
-    scales [rows]): scale = max|x| / 127 of the row, code = x / scale rounded (see s2_quantize_q8 in s2frame.h)."""
-    h = _hot or _bind()
-    dt, dev = h.kinds.get(x.dtype), x.get_device()
-    if dt is None or dev < 0:
-        _bad(_DEVICE)
-    if x.dim() != 2 or not x.shape[1]:
-        _bad("quantize_q8 takes [rows][cols]")
-    rows, cols = x.shape
-    codes, scales = _coded(h, x, cols, codes, scales)
-    if rows:
-        x, stride = _rows(x)
-        _launch(h, h.lib.s2_quantize_q8, dev, x.data_ptr(), dt, stride, rows, cols, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    scales [rows]): scale = max|x| / 127 of the row, code = x / scale rounded (see s2_quantize_q8 in s2frame.h).  Outputs
+    may be given."""
+    return (_q8 or _bind_q8()).quantize_q8(x, codes, scales)
 
 
 def dequantize_q8(codes, scales, cols: int | None = None, dtype=None, out=None):
     """The values that rows of codes stand for, scale * code -> [rows][cols] of dtype (fp32 where none is given); cols
     defaults to all that the codes hold."""
-    h = _hot or _bind()
-    dev = codes.get_device()
-    if dev < 0 or scales.get_device() != dev:
-        _bad(_DEVICE)
-    if codes.dim() != 2 or codes.dtype is not h.i8 or not codes.is_contiguous() or scales.dtype is not h.f32 or \
-            scales.shape != (codes.shape[0],) or not scales.is_contiguous():
-        _bad("dequantize_q8 takes contiguous int8 codes [rows][columns rounded up to 16] and fp32 scales [rows]")
-    rows, pitch = codes.shape
-    cols = pitch if cols is None else cols
-    if cols < 1 or (cols + 15) & -16 != pitch:
-        _bad("codes must hold cols columns, rounded up to 16")
-    dtype = h.f32 if dtype is None else dtype
-    dt = h.kinds.get(dtype)
-    if dt is None:
-        _bad("dtype must be fp32, bf16 or fp16")
-    if out is None:
-        out = h.empty((rows, cols), dtype=dtype, device=codes.device)
-    elif out.dtype is not dtype or out.shape != (rows, cols) or out.get_device() != dev or not out.is_contiguous():
-        _bad("out must be contiguous [rows][cols] of dtype on the codes' device")
-    if rows:
-        if codes.data_ptr() % 16:
-            codes = codes.clone()
-        _launch(h, h.lib.s2_dequantize_q8, dev, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt)
-    return out
+    return (_q8 or _bind_q8()).dequantize_q8(codes, scales, cols, dtype, out)
 
 
 def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, total=None, codes=None, scales=None):
     """RMSNorm of rows [rows][cols] (fp32, bf16 or fp16) with fp32 weight [cols], as codes and scales of quantize_q8.  With a
     residual (x's shape and type) the norm is of total = residual + x, rounded to their type, which is returned third;
     total may be given, and be x or residual itself."""
-    h = _hot or _bind()
-    dt, dev = h.kinds.get(x.dtype), x.get_device()
-    if dt is None or dev < 0 or weight.get_device() != dev:
-        _bad(_DEVICE)
-    if x.dim() != 2 or not x.shape[1]:
-        _bad("rms_norm_q8 takes [rows][cols]")
-    rows, cols = x.shape
-    if weight.dtype is not h.f32 or weight.shape != (cols,) or not weight.is_contiguous():
-        _bad("weight must be contiguous fp32 [cols]")
-    if residual is None:
-        if total is not None:
-            _bad("total goes with a residual")
-        codes, scales = _coded(h, x, cols, codes, scales)
-        if rows:
-            x, stride = _rows(x)
-            _launch(h, h.lib.s2_rms_norm_q8, dev, x.data_ptr(), dt, stride, None, 0, weight.data_ptr(), eps, rows, cols,
-                    None, codes.data_ptr(), scales.data_ptr())
-        return codes, scales
-    if residual.dtype is not x.dtype or residual.shape != x.shape or residual.get_device() != dev:
-        _bad("residual must have x's shape and type, on its device")
-    if total is None:
-        total = h.empty((rows, cols), dtype=x.dtype, device=x.device)
-    elif total.dtype is not x.dtype or total.shape != x.shape or total.get_device() != dev or not total.is_contiguous():
-        _bad("total must be contiguous, of x's shape and type, on its device")
-    codes, scales = _coded(h, x, cols, codes, scales)
-    if rows:
-        x, stride = _rows(x)
-        residual, rstride = _rows(residual)
-        _launch(h, h.lib.s2_rms_norm_q8, dev, x.data_ptr(), dt, stride, residual.data_ptr(), rstride, weight.data_ptr(),
-                eps, rows, cols, total.data_ptr(), codes.data_ptr(), scales.data_ptr())
-    return codes, scales, total
+    return (_q8 or _bind_q8()).rms_norm_q8(x, weight, eps, residual, total, codes, scales)
 
 
 def swiglu_q8(x, codes=None, scales=None):
     """The feed-forward's gate: rows [rows][2 f] (fp32, bf16 or fp16; gate | up) -> silu(gate) * up as codes and scales of
     quantize_q8, codes [rows][f rounded up to 16]."""
-    h = _hot or _bind()
-    dt, dev = h.kinds.get(x.dtype), x.get_device()
-    if dt is None or dev < 0:
-        _bad(_DEVICE)
-    if x.dim() != 2 or not x.shape[1] or x.shape[1] % 2:
-        _bad("swiglu_q8 takes [rows][2 f]")
-    rows, cols = x.shape[0], x.shape[1] // 2
-    codes, scales = _coded(h, x, cols, codes, scales)
-    if rows:
-        x, stride = _rows(x)
-        _launch(h, h.lib.s2_swiglu_q8, dev, x.data_ptr(), dt, stride, rows, cols, codes.data_ptr(), scales.data_ptr())
-    return codes, scales
+    return (_q8 or _bind_q8()).swiglu_q8(x, codes, scales)
 
 
 def q8_matmul(x_codes, x_scales, codes, scales, dtype=None, out=None):
     """Activation rows [n][k] times the transposed weight rows [m][k], both as codes and scales of quantize_q8 (or rows of
     them; k a multiple of 16) -> [n][m] of dtype (bf16 where none is given).  The sums are exact integers."""
-    h = _hot or _bind()
-    dev = x_codes.get_device()
-    if dev < 0 or x_scales.get_device() != dev or codes.get_device() != dev or scales.get_device() != dev:
-        _bad(_DEVICE)
-    i8, f32 = h.i8, h.f32
-    if x_codes.dim() != 2 or codes.dim() != 2 or x_codes.dtype is not i8 or codes.dtype is not i8 or \
-            not x_codes.is_contiguous() or not codes.is_contiguous():
-        _bad("q8_matmul takes contiguous int8 codes [n][k] and [m][k]")
-    n, k = x_codes.shape
-    m = codes.shape[0]
-    if codes.shape[1] != k or not k or k % 16:
-        _bad("both operands' codes must have the same columns, a multiple of 16")
-    if x_scales.dtype is not f32 or scales.dtype is not f32 or x_scales.shape != (n,) or scales.shape != (m,) or \
-            not x_scales.is_contiguous() or not scales.is_contiguous():
-        _bad("scales must be contiguous fp32 [n] and [m]")
-    if dtype is None:
-        dtype = h.bf16
-    dt = h.kinds.get(dtype)
-    if dt is None:
-        _bad("dtype must be fp32, bf16 or fp16")
-    if out is None:
-        out = h.empty((n, m), dtype=dtype, device=codes.device)
-    elif out.dtype is not dtype or out.shape != (n, m) or out.get_device() != dev or not out.is_contiguous():
-        _bad("out must be contiguous [n][m] of dtype, on the operands' device")
-    if not n or not m:
-        return out
-    xp, wp = x_codes.data_ptr(), codes.data_ptr()
-    if (xp | wp) & 15:
-        if xp & 15:
-            x_codes = x_codes.clone()
-        if wp & 15:
-            codes = codes.clone()
-        xp, wp = x_codes.data_ptr(), codes.data_ptr()
-    _launch(h, h.lib.s2_q8_matmul, dev, n, xp, x_scales.data_ptr(), wp, scales.data_ptr(), m, k, out.data_ptr(), dt)
-    return out
+    return (_q8 or _bind_q8()).q8_matmul(x_codes, x_scales, codes, scales, dtype, out)
 
 
 def s2_decode_frames(ctx, stream_ids, n_frames: int, params, expo_ptr: int, forced_ptr: int | None, codes_ptr: int,

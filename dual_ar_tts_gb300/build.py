@@ -1,4 +1,5 @@
-"""Build ``libs2frame.so`` in-tree with nvcc for sm_103a (one -gencode, TUs compiled in parallel)."""
+"""Build ``libs2frame.so`` in-tree with nvcc for sm_103a (one -gencode, TUs compiled in parallel), and ``_calls.so``, the
+8-bit operators' calls on torch tensors, with g++ against the installed torch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,10 +7,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libs2frame.so")
+CALLS = os.path.join(HERE, "_calls.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["fk_bf16_h128.cu", "fk_bf16_h64.cu", "fk_f32_h128.cu", "fk_f32_h64.cu", "frame_launch.cu", "prefill.cu",
            "engine.cu", "batch.cu", "codec.cu", "draw.cu", "q4.cu", "kv4.cu", "kv4_attn.cu", "adjust.cu", "q8.cu",
@@ -29,11 +32,23 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(OUT):
+    if not os.path.exists(OUT) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(OUT)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
+    t = min(os.path.getmtime(OUT), os.path.getmtime(CALLS))
+    deps = [os.path.join(CSRC, s) for s in SOURCES + ["calls.cpp"]] + [os.path.join(CSRC, h) for h in HEADERS]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _torch_flags() -> tuple[list[str], list[str]]:
+    """What compiling and linking against the installed torch takes."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    dirs = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    lib = os.path.join(t, "lib")
+    return ["-O2", "-std=c++17", "-fPIC", *["-isystem" + d for d in dirs]], \
+        ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -53,13 +68,30 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    flags, libs = _torch_flags()
+
+    def compile_calls():
+        obj = os.path.join(BUILD, "calls.o")
+        r = subprocess.run(["g++", *flags, "-c", os.path.join(CSRC, "calls.cpp"), "-o", obj], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls = calls.result()
     tmp = OUT + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, calls, "-L" + HERE, "-l:libs2frame.so", "-Wl,-rpath,$ORIGIN", *libs],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return OUT
 
 
