@@ -18,7 +18,7 @@ SOURCES = ["fk_bf16_h128.cu", "fk_bf16_h64.cu", "fk_f32_h128.cu", "fk_f32_h64.cu
            "engine.cu", "batch.cu", "codec.cu", "draw.cu", "q4.cu", "kv4.cu", "kv4_attn.cu", "adjust.cu", "q8.cu",
            "q8_matmul.cu"]
 HEADERS = ["s2_internal.h", "ptx.cuh", "frame_kernel.cuh", "sampler.cuh", "tc05.cuh",
-           "convert.cuh", "kv4.cuh", os.path.join("..", "..", "include", "s2frame.h")]
+           "convert.cuh", "kv4.cuh", "q8.cuh", os.path.join("..", "..", "include", "s2frame.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

@@ -21,7 +21,9 @@
 
 #include "convert.cuh"
 #include "ptx.cuh"
+#include "q8.cuh"
 #include "s2_internal.h"
+#include "tc05.cuh"
 
 namespace s2 {
 namespace {
@@ -133,14 +135,14 @@ struct Eight {
     if (skew == 0 && c + 8 <= cols) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 u = block[i];
+        const uint4 u = __ldcg(block + i);
         w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
       }
     } else if (c > 0 && c + 16 <= cols) {
       uint32_t b[kWords + 4];
 #pragma unroll
       for (int i = 0; i <= kWords / 4; ++i) {
-        const uint4 u = block[i];
+        const uint4 u = __ldcg(block + i);
         b[4 * i] = u.x, b[4 * i + 1] = u.y, b[4 * i + 2] = u.z, b[4 * i + 3] = u.w;
       }
 #pragma unroll
@@ -151,12 +153,12 @@ struct Eight {
       for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? b[i] : __funnelshift_r(b[i], b[i + 1], skew % 4 * 8);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = c + i < cols ? __float_as_uint(row[c + i]) : 0u;
+      for (int i = 0; i < 8; ++i) w[i] = c + i < cols ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(row) + c + i)) : 0u;
     } else {
       const uint16_t* e = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = c + 2 * i < cols ? e[c + 2 * i] : 0u, hi = c + 2 * i + 1 < cols ? e[c + 2 * i + 1] : 0u;
+        const uint32_t lo = c + 2 * i < cols ? __ldcg(e + c + 2 * i) : 0u, hi = c + 2 * i + 1 < cols ? __ldcg(e + c + 2 * i + 1) : 0u;
         w[i] = lo | hi << 16;
       }
     }
@@ -318,11 +320,11 @@ struct Row {
   // One column's value to 2^-44 or exactly
   __device__ __forceinline__ Two exactly(int c, float f, float g) const {
     if constexpr (kOp == kGate)
-      return gate_exactly(to_f(x[c]), to_f(other[c]));
+      return gate_exactly(to_f(__ldcg(x + c)), to_f(__ldcg(other + c)));
     else if constexpr (kOp == kQuantize)
-      return {to_f(x[c]), 0.f};
+      return {to_f(__ldcg(x + c)), 0.f};
     else
-      return two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, __ldg(weight + c) * g);
+      return two_prod(to_f(__ldcg((kOp == kNormResidual ? total : x) + c)) * f, __ldcg(weight + c) * g);
   }
 };
 
@@ -400,6 +402,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   // Whether the largest magnitude is made exact before any code: a gate's long row has an element next to a border more often
   // than not, others have none.
   constexpr bool kPeakFirst = kTeam == 0 && kOp == kGate;
+  pdl_trigger();
+  pdl_wait();
   const int team = kTeam == 0 ? blockDim.x : kTeam, me = kTeam == 0 ? threadIdx.x : threadIdx.x % kTeam;
   const long long row = kTeam == 0 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / kTeam;
   if (kTeam != 0 && row >= a.rows) return;
@@ -581,9 +585,8 @@ template <typename T, Op kOp, int kHeld, int kTeam, int kThreads, int kBlocks>
 int launch_teams(const RowArgs& a, int threads, cudaStream_t st) {
   static_assert(kHeld <= 4, "masks of 32 bits");
   const int rows_per = kTeam == 0 ? 1 : threads / (kTeam == 0 ? 1 : kTeam);
-  k_q8_rows<T, kOp, kHeld, kTeam, kThreads, kBlocks>
-      <<<static_cast<unsigned>((a.rows + rows_per - 1) / rows_per), threads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
+  return launch_ahead(k_q8_rows<T, kOp, kHeld, kTeam, kThreads, kBlocks>, dim3(static_cast<unsigned>((a.rows + rows_per - 1) / rows_per)),
+                      dim3(1), threads, 0, st, a);
 }
 
 template <Op kOp>
@@ -615,9 +618,9 @@ __device__ __forceinline__ void read_eight(const int8_t* __restrict__ codes, con
   float v[8];
   if (c + 8 <= cols) {
     const uint2* w = reinterpret_cast<const uint2*>(codes + row * pitch + (c & ~7));
-    uint2 lo = __ldg(w), hi = c & 7 ? __ldg(w + 1) : make_uint2(0, 0);
+    uint2 lo = __ldcg(w), hi = c & 7 ? __ldcg(w + 1) : make_uint2(0, 0);
     const uint32_t b[4] = {lo.x, lo.y, hi.x, hi.y};
-    const float s = __ldg(scales + row);
+    const float s = __ldcg(scales + row);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t p = c & 4 ? b[i + 1] : b[i], q = c & 4 ? b[i + 2 < 4 ? i + 2 : 3] : b[i + 1];
@@ -628,7 +631,7 @@ __device__ __forceinline__ void read_eight(const int8_t* __restrict__ codes, con
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] = at + i < all ? __ldg(scales + row) * static_cast<float>(__ldg(codes + row * pitch + c)) : 0.f;
+      v[i] = at + i < all ? __ldcg(scales + row) * static_cast<float>(__ldcg(reinterpret_cast<const signed char*>(codes) + row * pitch + c)) : 0.f;
       if (++c == cols) c = 0, ++row;
     }
   }
@@ -639,6 +642,8 @@ __device__ __forceinline__ void read_eight(const int8_t* __restrict__ codes, con
 template <typename T>
 __global__ void __launch_bounds__(256) k_q8_read(const int8_t* __restrict__ codes, const float* __restrict__ scales,
                                                  long long all, int cols, int pitch, bool wide, T* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
   read_eight(codes, scales, (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8, all, cols, pitch, wide, out);
 }
 // Rows of whole 16 columns, and an output that starts on 16 bytes: 16 codes a thread (19456 x 2560 bf16 24.3 us, 6.1 TB/s; by
@@ -646,11 +651,13 @@ __global__ void __launch_bounds__(256) k_q8_read(const int8_t* __restrict__ code
 template <typename T>
 __global__ void __launch_bounds__(256) k_q8_read16(const int8_t* __restrict__ codes, const float* __restrict__ scales,
                                                    long long items, int per, T* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= items) return;
   const long long row = i >> 32 ? i / per : static_cast<uint32_t>(i) / static_cast<uint32_t>(per);
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-  const float s = __ldg(scales + row);
+  const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(codes) + i);
+  const float s = __ldcg(scales + row);
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -716,14 +723,13 @@ extern "C" int s2_dequantize_q8(const int8_t* codes, const float* scales, long l
   const bool sixteens = cols % 16 == 0 && aligned(out, 16);
   const long long items = sixteens ? all / 16 : (all + 7) / 8, grid = (items + 255) / 256;
   if (grid > 0x7fffffffll) return S2_EINVAL;
-  with_dtype(dtype, [&](auto t) {
+  return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (sixteens)
-      k_q8_read16<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(codes, scales, items, cols / 16, static_cast<T*>(out));
-    else
-      k_q8_read<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(codes, scales, all, cols, pitch_of(cols), aligned(out, 16),
-                                                              static_cast<T*>(out));
+    T* const to = static_cast<T*>(out);
+    const dim3 blocks(static_cast<unsigned>(grid));
+    return sixteens ? launch_ahead(k_q8_read16<T>, blocks, dim3(1), 256, 0, st, codes, scales, items, cols / 16, to)
+                    : launch_ahead(k_q8_read<T>, blocks, dim3(1), 256, 0, st, codes, scales, all, cols, pitch_of(cols),
+                                   aligned(out, 16), to);
   });
-  return cudaGetLastError() == cudaSuccess ? S2_OK : S2_ECUDA;
 }

@@ -14,6 +14,7 @@
 
 #include "convert.cuh"
 #include "ptx.cuh"
+#include "q8.cuh"
 #include "s2_internal.h"
 #include "tc05.cuh"
 
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
     }
     cp_async_commit();
   };
+  pdl_trigger();
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < kFewAhead - 1; ++i) issue(i);
 
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
       const int half = i / NT, col = i % NT * 8 + g, k = (s0 + j0) * kStep + half * 64 + c * 16;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (col < nn && k < a.k)
-        v = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(n0 + col) * a.k + k));
+        v = __ldcg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(n0 + col) * a.k + k));
       uint4 p, q;
       expand(v.x, p.x, p.y);
       expand(v.y, p.z, p.w);
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
       v = out[col * kJoinRow + r];
     }
     if (row < a.m)
-      static_cast<T*>(a.y)[static_cast<size_t>(n0 + col) * a.m + row] = scaled<T>(v, __ldg(a.xs + n0 + col), __ldg(a.ws + row));
+      static_cast<T*>(a.y)[static_cast<size_t>(n0 + col) * a.m + row] = scaled<T>(v, __ldcg(a.xs + n0 + col), __ldcg(a.ws + row));
   }
   if (ranks > 1) cluster_sync();  // no block leaves while its sums are read
 }
@@ -412,6 +415,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     }
     fence_barrier_init();
   }
+  if (warp == 13 && lane == 0) {
+    prefetch_tmap(&maps.w);
+    prefetch_tmap(&maps.x);
+  }
+  // All of an SM's tensor memory is taken when the kernel in front has ended, and the next is let on when it is: two kernels that
+  // wait for each other's memory and end would never do either.
+  pdl_wait();
   if (warp == 12) tmem_get<kPair>(tbase, M::kCols);
   tc_fence_before();
   if constexpr (kPair)
@@ -420,6 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
+  pdl_trigger();
   auto arrive = [&](uint64_t* bar) {
     if constexpr (kPair)
       mbar_arrive_first(bar);
@@ -583,9 +594,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     auto column_of = [&](int t) { return t / row_tiles * N + wg * kHalf; };
     auto load_scales = [&] {
       const int t = first + tile * apart;
-      ws = __ldg(a.ws + min(row_of(t) + lane, a.m - 1));
+      ws = __ldcg(a.ws + min(row_of(t) + lane, a.m - 1));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = __ldg(a.xs + min(column_of(t) + i * kQ + lane % kQ, a.n - 1));
+      for (int i = 0; i < 4; ++i) xs[i] = __ldcg(a.xs + min(column_of(t) + i * kQ + lane % kQ, a.n - 1));
     };
     auto write = [&](auto quarter) {
       constexpr int q = decltype(quarter)::value;
@@ -710,14 +721,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
           if (q < ranks) bad |= ld_cluster_int(smem_u32(&failed), q);
         float ws[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ws[e] = bad ? __uint_as_float(0x7fc00000u) : __ldg(a.ws + min(row + e, a.m - 1));
+        for (int e = 0; e < 4; ++e) ws[e] = bad ? __uint_as_float(0x7fc00000u) : __ldcg(a.ws + min(row + e, a.m - 1));
 #pragma unroll 2
         for (int col = warp * ranks + rank; col < nn; col += 8 * ranks) {
           int4 v[8];
           int total[4] = {};
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[q] = q < ranks ? ld_cluster_int4(smem_u32(out + col * 128 + r), q) : make_int4(0, 0, 0, 0);
-          const float xs = __ldg(a.xs + n0 + col);
+          const float xs = __ldcg(a.xs + n0 + col);
 #pragma unroll
           for (int q = 0; q < 8; ++q) total[0] += v[q].x, total[1] += v[q].y, total[2] += v[q].z, total[3] += v[q].w;
           T* y = static_cast<T*>(a.y) + static_cast<size_t>(n0 + col) * a.m + row;
@@ -738,24 +749,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
     tc_fence_after();
     tmem_free<kPair>(tm, M::kCols);
   }
-}
-
-template <typename... Args>
-int launch_clusters(void (*kernel)(Args...), dim3 grid, dim3 cluster, int threads, int smem, cudaStream_t st,
-                    const std::decay_t<Args>&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster.x;
-  at[0].val.clusterDim.y = cluster.y;
-  at[0].val.clusterDim.z = cluster.z;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? S2_OK : S2_ECUDA;
 }
 
 // Blocks that split W's columns for each of `groups` tiles: the most, up to eight and `most`, whose clusters the device
@@ -796,7 +789,7 @@ int launch_few(const Q8Args& a, cudaStream_t st) {
   const int rows = (a.m + kFewRows - 1) / kFewRows, cols = (a.n + NT * 8 - 1) / (NT * 8), steps = (a.k + kStep - 1) / kStep;
   if (!allow_smem<k_q8_few<T, NT>, kFewBytes<NT>>()) return S2_ECUDA;
   const int ranks = split<k_q8_few<T, NT>>(static_cast<long long>(rows) * cols, steps / 2, 32 * kFewWarps, kFewBytes<NT>);
-  return launch_clusters(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, st, a);
+  return launch_ahead(k_q8_few<T, NT>, dim3(rows, ranks, cols), dim3(1, ranks), 32 * kFewWarps, kFewBytes<NT>, st, a);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -865,7 +858,7 @@ int launch_tc(const Q8Args& a, const Plan& plan, cudaStream_t st) {
   Maps maps;
   if (!code_map(&maps.w, a.w, a.m, a.k, 128) || !code_map(&maps.x, a.x, a.n, a.k, kPair ? M::kPart / 2 : N)) return S2_ECUDA;
   maps.bulk = result_map<T>(&maps.y, a.y, a.n, a.m, std::min(N / 8, static_cast<int>(M::kOutWarp / 32 / sizeof(T))));
-  return launch_clusters(k_q8_tc<T, N, kPair>, dim3(plan.blocks * (kPair ? 2 : 1), plan.ranks),
+  return launch_ahead(k_q8_tc<T, N, kPair>, dim3(plan.blocks * (kPair ? 2 : 1), plan.ranks),
                          kPair ? dim3(2) : dim3(1, plan.ranks), kTcThreads, M::kBytes, st, a, maps);
 }
 
