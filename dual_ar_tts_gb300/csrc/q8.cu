@@ -679,6 +679,14 @@ bool bad_rows(const void* x, int dtype, long long stride, long long rows, long l
   return !x || !esz || !codes || !scales || rows < 1 || rows > 0x7fffffffll || cols < 1 || cols > kColsMost ||
          stride < width || !aligned(x, esz) || !aligned(codes, 16) || !aligned(scales, 4);
 }
+// Whether `total`, contiguous, meets rows of which it is not the whole.
+bool meets(const void* total, const void* x, long long stride, long long rows, int cols, int esz) {
+  if (total == x && (stride == cols || rows == 1)) return false;
+  const long long begin = static_cast<long long>(reinterpret_cast<uintptr_t>(total) - reinterpret_cast<uintptr_t>(x));  // past x
+  const long long end = begin + rows * cols * esz, row = static_cast<long long>(cols) * esz, step = stride * esz;
+  const long long first = begin < row ? 0 : (begin - row) / step + 1;  // the first row that ends behind its begin
+  return first < rows && first * step < end;
+}
 int pitch_of(int cols) { return (cols + 15) / 16 * 16; }
 
 }  // namespace
@@ -701,7 +709,8 @@ extern "C" int s2_rms_norm_q8(const void* x, int dtype, long long x_stride, cons
     return S2_EINVAL;
   const int esz = dtype_bytes(dtype);
   if ((residual != nullptr) != (total != nullptr) ||
-      (residual && (residual_stride < cols || !aligned(residual, esz) || !aligned(total, esz))))
+      (residual && (residual_stride < cols || !aligned(residual, esz) || !aligned(total, esz) ||
+                    meets(total, x, x_stride, rows, cols, esz) || meets(total, residual, residual_stride, rows, cols, esz))))
     return S2_EINVAL;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const RowArgs a{x, residual, weight, total, codes, scales, x_stride, residual_stride, rows, cols, pitch_of(cols), eps,

@@ -447,7 +447,7 @@ size_t s2_kv4_attention_workspace(int n_seq, int n_rows, int n_head, int n_kv_he
 int s2_kv4_attention(const s2_kv4* cache, const void* q, int dtype, int n_head, float scale, int max_len, void* out,
                      void* workspace, size_t ws_bytes, struct CUstream_st* stream);
 
-/* Testing hook: tries (each of a few hundred ns) that the device waits of s2_q4_matmul and
+/* Testing hook: tries (each of a few hundred ns) that the device waits of s2_q4_matmul, s2_q8_matmul and
  * s2_kv4_attention make in calls launched from here on, in this process; 0: each gives up at once.
  * Negative: the default, 2^22.  A captured call keeps the limit that it was captured with. */
 int s2_set_wait_limit(int tries);
@@ -474,17 +474,19 @@ int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* log
 /* ---------------------------------------------------------------------------------------------
  * Projections in 8-bit integers, activations and weights with a scale a row: stateless calls on caller
  * buffers, beside those on 4-bit weights and under the same rules (nothing allocated, nothing kept,
- * asynchronous on `stream`, capturable, the same bits for the same inputs; no workspace).  Of a layer
+ * asynchronous on `stream`, capturable, the same bits for the same inputs; no workspace).  Each may be scheduled before
+ * what is in front of it on the stream has ended, and waits for that on the device before it reads or writes.  Of a layer
  * they are: s2_rms_norm_q8, s2_q8_matmul (wqkv), s2_quantize_q8 of attention's output, s2_q8_matmul (wo),
  * s2_rms_norm_q8 with the residual's sum, s2_q8_matmul (gate and up), s2_swiglu_q8, s2_q8_matmul (down).
  *
  * A row v of values becomes
  *   step = max(max|v| / 127, 2^-126),  scale = step rounded to fp32,  code[i] = v[i] / step rounded to the
  *   nearest whole number, ties (within 2^-42) to even: -127..127
- * and stands for scale * code (the scale is no more than the largest number that is finite 127 times).  Codes are those of the exact quotients (of a norm and a gate, of v to
- * 2^-44 or so), scales of norms and gates are good to a few roundings of fp32.  A row that holds
- * something not finite, or whose values or norm come to that in fp32, gets scale NaN and codes 0, so that
- * products with it are NaN.
+ * and stands for scale * code (the scale is no more than the largest number that is finite 127 times).  Codes
+ * are those of the exact quotients (of a norm and a gate, of v to 2^-44 or so), scales of norms and gates are good to
+ * a few roundings of fp32 (norms of rows past some 2^16 columns: to those of a sum of so many squares).  A row that holds
+ * something not finite, or whose values or norm come to that in fp32, gets scale NaN and codes 0, so that products with
+ * it are NaN.
  *   codes   device int8 [rows][pitch], 16-byte aligned; pitch = cols rounded up to 16, the columns behind
  *           cols are written as zeros
  *   scales  device fp32 [rows]
@@ -504,12 +506,13 @@ int s2_dequantize_q8(const int8_t* codes, const float* scales, long long rows, i
  *   residual  [rows][cols] of dtype, or NULL
  *   weight    device fp32 [cols]
  *   total     device [rows][cols] of dtype, contiguous; given with a residual and only then.  It may be x or
- *             residual itself (where that is contiguous), but not overlap them otherwise */
+ *             residual itself (where that is contiguous), but not overlap them otherwise (S2_EINVAL) */
 int s2_rms_norm_q8(const void* x, int dtype, long long x_stride, const void* residual, long long residual_stride,
                    const float* weight, float eps, long long rows, int cols, void* total, int8_t* codes, float* scales,
                    struct CUstream_st* stream);
 
-/* v[i] = silu(x[i]) * x[cols + i], silu(g) = g / (1 + exp(-g)): x [rows][2 * cols] of dtype, gate | up. */
+/* v[i] = silu(x[i]) * x[cols + i], silu(g) = g / (1 + exp(-g)): x [rows][2 * cols] of dtype, gate | up.  An exp(-|g|) below
+ * 2^-126 (|g| past 87.3) counts as 0. */
 int s2_swiglu_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes, float* scales,
                  struct CUstream_st* stream);
 

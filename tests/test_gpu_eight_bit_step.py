@@ -106,3 +106,57 @@ def test_quality_of_a_layer():
     y = pkg.q8_matmul(*pkg.quantize_q8(x), *pkg.quantize_q8(w), dtype=torch.float32)
     want = x.double() @ w.double().t()
     assert ((y.double() - want).norm() / want.norm()) < 0.02
+
+
+@pytest.mark.parametrize("n,m,k", [(1, 512, 2560), (12, 2560, 512), (40, 2560, 1024), (300, 4864, 512)])
+def test_run_on_the_same_buffers(n, m, k):
+    """Calls may begin before the one in front of them has ended: a run of them in which each writes what the one in front reads,
+    and reads what it writes, eager and captured, gives what calls with buffers of their own give."""
+    import dual_ar_tts_gb300 as pkg
+    g = torch.Generator(device="cuda").manual_seed(n)
+    ws = [pkg.quantize_q8(torch.randn((m, k), generator=g, device="cuda") * 0.05) for _ in range(3)]
+    raw = [pkg.dequantize_q8(*w) for w in ws]
+    xs = [torch.randn((n, k), generator=g, device="cuda") for _ in range(3)]
+    norm = 1 + 0.1 * torch.randn(k, generator=g, device="cuda")
+    want = []
+    for i in range(12):
+        c, s, total = pkg.rms_norm_q8(xs[i % 3], norm, residual=xs[(i + 1) % 3])
+        torch.cuda.synchronize()
+        y = pkg.q8_matmul(c, s, *ws[i % 3], dtype=torch.float32)
+        torch.cuda.synchronize()
+        want.append((c, s, total, y, *pkg.swiglu_q8(y)))
+        torch.cuda.synchronize()
+    i8 = dict(dtype=torch.int8, device="cuda")
+    f32 = dict(device="cuda")
+    codes, scales, total = torch.empty((n, k), **i8), torch.empty(n, **f32), torch.empty((n, k), **f32)
+    wc, wsc, y = torch.empty((m, k), **i8), torch.empty(m, **f32), torch.empty((n, m), **f32)
+    act = torch.empty((n, (m // 2 + 15) // 16 * 16), **i8), torch.empty(n, **f32)
+    got = [[torch.empty_like(t) for t in w] for w in want]
+
+    def run():
+        for i in range(12):
+            pkg.quantize_q8(raw[i % 3], wc, wsc)                        # the weights that the product before this reads
+            pkg.rms_norm_q8(xs[i % 3], norm, 1e-6, xs[(i + 1) % 3], total, codes, scales)
+            pkg.q8_matmul(codes, scales, wc, wsc, out=y, dtype=torch.float32)
+            pkg.swiglu_q8(y, *act)
+            if i % 4 == 3:                                              # (a kernel of another kind now and then)
+                for a, b in zip(got[i], (codes, scales, total, y, *act)):
+                    a.copy_(b)
+
+    def check():
+        for i in range(3, 12, 4):
+            for j, (a, b) in enumerate(zip(got[i], want[i])):
+                assert torch.equal(a, b), (i, j)
+
+    for _ in range(20):
+        run()
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(20):
+        for o in got:
+            for t in o:
+                t.zero_()
+        graph.replay()
+        check()

@@ -285,3 +285,21 @@ def test_many_short_rows():
     eb.check_codes(codes.cpu(), want, distance, 127 * 2.0 ** -51)
     assert torch.equal(scales.cpu(), scale.float())
     assert torch.equal(pkg.dequantize_q8(codes, scales, 3), codes[:, :3].float() * scales[:, None])
+
+
+def test_norm_sum_between_rows():
+    """A sum that lies between the operand's rows, and in the operand of a single row, is taken."""
+    import dual_ar_tts_gb300 as pkg
+    x, r, w = _rand((3, 700), 1), _rand((3, 100), 2).cuda(), torch.ones(100, device="cuda")
+    want = pkg.rms_norm_q8(x[:, :100].cuda(), w, residual=r)
+    held = x.cuda()
+    total = held.view(-1)[100:400].view(3, 100)       # behind the first row, before the second
+    got = pkg.rms_norm_q8(held[:, :100], w, residual=r, total=total)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(held.cpu()[:, :100], x[:, :100]) and torch.equal(total, want[2])
+    one = x.cuda()[:1, :100]
+    got = pkg.rms_norm_q8(one, w, residual=r[:1], total=one)
+    assert torch.equal(one, want[2][:1]) and torch.equal(got[0], want[0][:1])
+    with pytest.raises(pkg.S2Error):
+        pkg.rms_norm_q8(held[:, :100], w, residual=r, total=held.view(-1)[600:900].view(3, 100))

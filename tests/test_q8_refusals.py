@@ -43,6 +43,19 @@ def test_norm(lib):
     _bad(lib.s2_rms_norm_q8, dict(good, res=P, rstride=100, total=P), res=[None, P + 1], rstride=[99, 0], total=[None, P + 2])
 
 
+def test_norm_sum_in_place(lib):
+    """The residual's sum may be one of the operands, not part of one, or of its rows."""
+    fn, size = lib.s2_rms_norm_q8, 3 * 100 * 4
+    good = dict(x=P, dtype=0, stride=100, res=4 * P, rstride=100, weight=P, eps=1e-6, rows=3, cols=100, total=8 * P, codes=P,
+                scales=P, stream=None)
+    assert 4 * P - P > size
+    _bad(fn, good, total=[P + 4, P + 400, P + size - 4, P - size + 4, 4 * P - 4, 4 * P + size - 4])
+    # rows apart: a sum over them, and over the last one's end
+    apart = dict(good, stride=1000)
+    _bad(fn, apart, total=[P, P + 396, P + 4000, P + 8396, P + 4000 - size + 4, P - 4])
+    _bad(fn, dict(good, rstride=101), total=[4 * P])
+
+
 def test_matmul(lib):
     good = dict(n=2, x=P, xs=P, w=P, ws=P, m=3, k=32, y=P, dtype=1, stream=None)
     _bad(lib.s2_q8_matmul, good, n=[0, -1, (1 << 21) - 31], x=[None, P + 8], xs=[None, P + 2], w=[None, P + 4], ws=[None, P + 1],
