@@ -228,7 +228,9 @@ struct Tc {
   static_assert(kW % 2 == 0, "a place's steps are of one parity");
   static constexpr int kBBytes = kRows * 256, kWBytes = 128 * kStep, kXBytes = kRows * kStep;
   static constexpr int kWRing = kStages * kBBytes, kXRing = kWRing + kW * kWBytes;
-  static constexpr int kParts = 2, kPart = N / kParts;   // of the columns, each with its products and its sums
+  // Parts of the columns, each with its products and its sums.  A pair's are two (all at once: 138 us for 2048 rows of
+  // 19456 x 2560, 134 so); a block's one (in two: 11.4 us for 32 rows of 2560 x 9728, 10.9 so).
+  static constexpr int kParts = kPair ? 2 : 1, kPart = N / kParts;
   static constexpr int kOut = kXRing + kX * kXBytes, kOutWarp = 2048;  // results on their way, of a warp
   static constexpr int kBars = kOut + 8 * kOutWarp, kBytes = kBars + 512 + 1024;
   static constexpr uint32_t kCols = 512, kA = 256;                  // tensor memory: sums, then A
