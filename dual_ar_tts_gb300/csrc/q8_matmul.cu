@@ -84,6 +84,9 @@ __device__ __forceinline__ T scaled(int sum, float xs, float ws) {
 // add up through distributed shared memory.  Weights come through a warp's own ring of cp.async, kAhead steps deep.  The
 // activations of a chunk are expanded once a block, laid out as the lanes' B operands.  K is permuted alike in both
 // operands: lane c of a row's four holds 16 consecutive columns of 64, and a word of them is its part of one product.
+// It is bound by latency: of 11.7 us for one row of 19456 x 2560 (4.3 TB/s; 8.3 us with the weights in L2), 4 are there at any
+// size: the launch, the first copies, the join.  7 rows of 6144 x 2560 6.8 us, 16 of 19456 x 2560 14.4.  (Results stored behind the
+// last meeting of the cluster instead of before: 11.7, 6.4 .. 6.9 us, no gain.)
 constexpr int kFewWarps = 8, kFewRows = 16 * kFewWarps, kFewAhead = 4;
 constexpr int kFewRing = kFewWarps * kFewAhead * 16 * kStep;
 constexpr int kJoinRow = kFewRows + 4;
@@ -218,6 +221,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_q8_few(const Q8Args a) {
 // kPair: the blocks of a pair work on one tile of 256 weight rows (cta_group::2), each holds half of the activations, which
 // halves what a block reads and stores of them.  Blocks take tiles in turn (there is no end of a pipeline between them), or
 // the blocks of a cluster split W's columns of one tile.
+// Bound by the hand-overs of a step with few rows (some 800 clocks a step, the slowest of copying, expanding either operand and
+// issuing; the weights in L2 or not), and with many by the tensor core beside the expansion (2048 rows of 19456 x 2560 132 us,
+// 1.55 PFLOP/s, 0.81 of what the library's bf16 products reach; 32 rows of 2560 x 9728 11.0 us, 512 rows of 19456 x 2560 38).
+// Waits know a phase's parity only, so none may be two phases behind: a stage's `empty` comes in the order of its steps, since
+// products are done in order, and who fills it has waited for the step before; copies land in any order, see kW.
 template <int N, bool kPair>
 struct Tc {
   static constexpr int kRows = kPair ? N / 2 : N;                   // of activations in a block
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_q8_tc(const Q8Args a, const _
 
 // Blocks that split W's columns for each of `groups` tiles: the most, up to eight and `most`, whose clusters the device
 // holds at a time.  (It takes whole clusters in whole groups of its SMs, so many sizes leave SMs over: 20 clusters of seven
-// blocks of k_q8_tc take two rounds, 22 us for 64 rows of 2560 x 9728 against 15 with six.)  What it holds is asked once.
+// blocks of k_q8_tc took two rounds, 22 us for 64 rows of 2560 x 9728 against 15 with six, which are 11.5 now.)  What it holds is asked once.
 template <auto kKernel>
 int split(long long groups, int most, int threads, int smem) {
   static std::atomic<int> held[64][9];
@@ -835,7 +843,7 @@ struct Plan {
   double time;
 };
 // A block has 5.5 to 7.5 us of launch, filling and draining, and a time a step; blocks at work together are a round.  A join
-// costs by its columns.  Measured, us, at (rows) for one column tile of 64 and 128 and a pair's 256, weights not in L2:
+// costs by its columns.  Measured (each 1 to 2 us less since launches are ahead of the kernel in front), us, at (rows) for one column tile of 64 and 128 and a pair's 256, weights not in L2:
 // 19456 x 2560 (64) 16.2, 18.7, 22.3; (128) 27.1, 19.1, 22.5; (256) 48.8, 32.1, 23.2; (1024) -, 112, 70; 6144 x 2560 (64) 12.0,
 // 15.3, 20.9; (256) 25.7, 17.7, 21.1; (512) -, 30.8, 21.4; 2560 x 9728 (64) 13.2, 16.0, 55.6; (512) -, 47.5, 56.0.
 template <typename T, int N, bool kPair>
