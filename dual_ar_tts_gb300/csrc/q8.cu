@@ -613,7 +613,7 @@ int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
     using T = decltype(t);
     const int eights = a.pitch / 8;
     auto threads = [&](int each) { return (eights + 32 * each - 1) / (32 * each) * 32; };
-    // Short rows: eight lanes a row up to 128 columns (300000 x 64 24 us; a warp a row 88), a warp up to 1024 (gate of 20000 x 700
+    // us.  Short rows: eight lanes a row up to 128 columns (300000 x 64 24 us; a warp a row 88), a warp up to 1024 (gate of 20000 x 700
     // bf16 33; a block 43).  A quantiser's rows up to 4096 columns, and long ones of 16 bits: 32 elements a thread (19456 x 2560
     // bf16 33.2, with 16 35.2; gate of 2048 x 9728 29.5, 34.2).  Others 16: an fp32 thread would hold too much (gate of 1024 x 9728
     // 22.1, with 32 28.5), and so would a norm's.
@@ -625,7 +625,16 @@ int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
     }
     if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 6>(a, 128, st);
     if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, 4>(a, threads(2), st);
-    return launch_teams<T, kOp, 2, 0, 640, kOp == kGate ? 2 : 1>(a, std::min(640, threads(2)), st);
+    // Norms past 4096 columns: two blocks an SM (2048 x 9728 bf16 without a residual 25.7, with one block 40.8); with a residual
+    // smaller ones (bf16 36.8, 42.5; 2000 x 5000 fp32 26.0, 29.2; of one row 3.5 and 4.1, where 640 threads take 3.1).  Nothing here
+    // goes by the rows: a row's sums, and so its scale's last place, are the same in any batch.
+    if constexpr (kOp == kNormResidual) {
+      if constexpr (sizeof(T) == 2)
+        return launch_teams<T, kOp, 3, 0, 416, 2>(a, std::min(416, threads(3)), st);
+      else
+        return launch_teams<T, kOp, 2, 0, 512, 2>(a, std::min(512, threads(2)), st);
+    }
+    return launch_teams<T, kOp, 2, 0, 640, 2>(a, std::min(640, threads(2)), st);
   });
 }
 

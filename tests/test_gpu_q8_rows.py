@@ -303,3 +303,27 @@ def test_norm_sum_between_rows():
     assert torch.equal(one, want[2][:1]) and torch.equal(got[0], want[0][:1])
     with pytest.raises(pkg.S2Error):
         pkg.rms_norm_q8(held[:, :100], w, residual=r, total=held.view(-1)[600:900].view(3, 100))
+
+
+@pytest.mark.parametrize("dtype", list(eb.TYPES))
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("cols", [4097, 5000, 9985, 17003])
+def test_wide_norms(cols, residual, dtype):
+    """More rows than SMs, wider than a block holds, or than it is by one; a row has the same bits in any batch."""
+    import dual_ar_tts_gb300 as pkg
+    rows, dt = 160, eb.TYPES[dtype]
+    x, w = _rand((rows, cols), cols).to(dt), torch.exp(0.3 * _rand(cols, 7))
+    res = _rand((rows, cols), 6, 2.0).to(dt) if residual else None
+    call = lambda a, b: pkg.rms_norm_q8(a.cuda(), w.cuda(), 1e-6, residual=None if b is None else b.cuda())    # noqa: E731
+    out = call(x, res)
+    v, r, total = eb.norm(x, w, 1e-6, res)
+    want, scale, distance = eb.coded(v, r)
+    eb.check_codes(out[0].cpu(), want, distance, SURE)
+    # a thread adds eight elements of every 3328 at least, the others as above
+    tol = ((8 * math.ceil(cols / 3328) + 12) / 2 + 7) * eb.STEP
+    assert ((out[1].cpu().double() - scale).abs() <= tol * scale).all()
+    if residual:
+        assert torch.equal(out[2].cpu(), total)
+    for at in (slice(0, 1), slice(3, 10)):
+        for a, b in zip(call(x[at], None if res is None else res[at]), out):
+            assert torch.equal(a, b[at])
