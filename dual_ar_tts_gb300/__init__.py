@@ -595,7 +595,7 @@ def dequantize_q8(codes, scales, cols: int | None = None, dtype=None, out=None):
 def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, total=None, codes=None, scales=None):
     """RMSNorm of rows [rows][cols] (fp32, bf16 or fp16) with fp32 weight [cols], as codes and scales of quantize_q8.  With a
     residual (x's shape and type) the norm is of total = residual + x, rounded to their type, which is returned third;
-    total may be given, and be x or residual itself."""
+    total may be given, and be x or residual itself, but lie over neither otherwise."""
     return (_q8 or _bind_q8()).rms_norm_q8(x, weight, eps, residual, total, codes, scales)
 
 
