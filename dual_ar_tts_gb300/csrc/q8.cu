@@ -74,6 +74,23 @@ __device__ __forceinline__ Two div(Two a, Two b) {
   return fast_sum(q, __fdiv_rn(rest, b.hi));
 }
 
+// x = m 2^e, 1 <= |m| < 2
+struct Split {
+  float m;
+  int e;
+};
+__device__ __forceinline__ Split split(float x) {
+  const bool small = fabsf(x) < 0x1p-126f;
+  const uint32_t b = __float_as_uint(small ? x * 0x1p64f : x);
+  return {__uint_as_float((b & 0x807fffffu) | 0x3f800000u), static_cast<int>(b >> 23 & 255u) - (small ? 191 : 127)};
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126..127
+// v 2^e, kept within what can be compared with numbers of about 1
+__device__ __forceinline__ Two scaled(Two v, int e) {
+  const float s = power_of_two(min(max(e, -100), 100));
+  return {v.hi * s, v.lo * s};
+}
+
 // 1 / n! and ln 2 in terms
 struct Factorial {
   static constexpr double at(int n) { return n < 2 ? 1.0 : at(n - 1) * n; }
@@ -85,14 +102,17 @@ __device__ __forceinline__ Two inverse_factorial() {
   return {hi, lo};
 }
 
-// silu(g) * u to about 2^-44.  exp(-|g|) = 2^n exp(r), |r| <= ln 2 / 2, exp(r) by its Taylor series: the terms from
-// r^7 on, 2^-23 of the sum, in fp32, the others in two terms.
-__device__ __noinline__ Two gate_exactly(float g, float u) {
+// silu(g) * u * 2^unit to about 2^-44, from the factors' significands: neither g u, which passes fp32's range where silu(g) u does
+// not, nor the last places of a small product are lost.  exp(-|g|) = 2^-n exp(r), |r| <= ln 2 / 2, exp(r) by its Taylor series:
+// the terms from r^7 on, 2^-23 of the sum, in fp32, the others in two terms.
+__device__ __noinline__ Two gate_exactly(float g, float u, int unit) {
   constexpr double kLn2 = 0.693147180559945309417232121458;
   constexpr float kA = static_cast<float>(static_cast<int>(kLn2 * 32768) / 32768.0);  // 15 bits: n times it is exact
   constexpr float kB = static_cast<float>(kLn2 - kA), kC = static_cast<float>(kLn2 - kA - kB);
   const float a = fabsf(g), n = rintf(a * static_cast<float>(1.0 / kLn2));
-  if (g >= 0.f && a > 60.f) return two_prod(g, u);  // 1 + exp(-g) is 1 to 2^-86
+  const Split gs = split(g), us = split(u);
+  unit += gs.e + us.e;
+  if (g >= 0.f && a > 60.f) return scaled(two_prod(gs.m, us.m), unit);  // 1 + exp(-g) is 1 to 2^-86
   const Two nb = two_prod(n, kB);
   // r = n ln 2 - |g|; n A - |g| is exact
   Two r = two_sum(__fsub_rn(__fmul_rn(n, kA), a), nb.hi);
@@ -110,14 +130,11 @@ __device__ __noinline__ Two gate_exactly(float g, float u) {
   e = add(inverse_factorial<2>(), mul(e, r));
   e = add(Two{1.f, 0.f}, mul(e, r));
   e = add(Two{1.f, 0.f}, mul(e, r));
-  const float half = -n * 0.5f, up = exp2f(floorf(half)), up2 = exp2f(-n - floorf(half));  // 2^-n, perhaps below 2^-126
-  const Two small{e.hi * up * up2, e.lo * up * up2};
-  const Two below = add(Two{1.f, 0.f}, small);
-  Two v = two_prod(g, u);
+  const int down = -static_cast<int>(fminf(n, 200.f));
+  const Two below = add(Two{1.f, 0.f}, scaled(e, down));
+  Two v = two_prod(gs.m, us.m);
   if (g < 0.f) v = mul(v, e);
-  v = div(v, below);
-  if (g < 0.f) v = {v.hi * up * up2, v.lo * up * up2};
-  return v;
+  return scaled(div(v, below), unit + (g < 0.f ? down : 0));
 }
 
 // ------------------------------------------------------------------- the rows' values
@@ -330,14 +347,16 @@ struct Row {
     }
   }
 
-  // One column's value to 2^-44 or exactly
-  __device__ __forceinline__ Two exactly(int c, float f, float g) const {
-    if constexpr (kOp == kGate)
-      return gate_exactly(to_f(x[c]), to_f(other[c]));
-    else if constexpr (kOp == kQuantize)
-      return {to_f(x[c]), 0.f};
-    else
-      return two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, weight[c] * g);
+  // One column's value times 2^unit, to 2^-44 or exactly
+  __device__ __forceinline__ Two exactly(int c, float f, float g, int unit) const {
+    if constexpr (kOp == kGate) {
+      return gate_exactly(to_f(x[c]), to_f(other[c]), unit);
+    } else if constexpr (kOp == kQuantize) {
+      return {to_f(x[c]) * power_of_two(unit), 0.f};
+    } else {
+      const Two v = two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, weight[c] * g);
+      return {v.hi * power_of_two(unit), v.lo * power_of_two(unit)};
+    }
   }
 };
 
@@ -349,14 +368,9 @@ __device__ __forceinline__ Two magnitude(Two v) { return v.hi < 0.f ? Two{-v.hi,
 template <Op kOp, bool kPeakFirst>
 constexpr float kMargin = kOp == kQuantize ? 0x1p-16f : kOp == kGate ? (kPeakFirst ? 0x1p-13f : 0x1p-12f) : 0x1p-15f;
 
-// The magnitude's code where t, its quotient in fp32, lies next to a border: 254 v against (2 l + 1) most.
-__device__ __forceinline__ float decide(Two v, Two most, float t) {
-  const float l = floorf(t), b = 2.f * l + 1.f;
-  if (most.hi > 0x1p100f || most.hi < 0x1p-60f) {  // keep the products' last places within fp32's range
-    const float s = most.hi > 1.f ? 0x1p-64f : 0x1p64f;
-    v = {v.hi * s, v.lo * s};
-    most = {most.hi * s, most.lo * s};
-  }
+// The magnitude's code where v per, its quotient in fp32, lies next to a border: 254 v against (2 l + 1) most.
+__device__ __forceinline__ float decide(Two v, Two most, float per) {
+  const float l = floorf(v.hi * per), b = 2.f * l + 1.f;
   const Two p = two_prod(254.f, v.hi), q = two_prod(b, most.hi);
   const float d = __fadd_rn(__fsub_rn(p.hi, q.hi),
                             __fadd_rn(__fsub_rn(p.lo, q.lo), __fsub_rn(__fmul_rn(254.f, v.lo), __fmul_rn(b, most.lo))));
@@ -502,8 +516,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
       for (int i = 0; i < 8; ++i) held[h][i] *= early;
   }
 
-  // The largest magnitude to more than fp32: of what comes near to it, the largest.
-  Two peak{most, 0.f};
+  // The largest magnitude to more than fp32: of what comes near to it, the largest.  What is taken exactly is held times 2^unit, which
+  // brings the largest to 1 .. 4.
+  const int unit = 127 - min(static_cast<int>(__float_as_uint(most) >> 23), 253);
+  Two peak{most * power_of_two(unit), 0.f};
   auto find_peak = [&] {
     const float near = most * (1.f - 0x1p-18f);
     unsigned long long key = 0;
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
     }
     for (; mask; mask &= mask - 1) {
       const int i = __ffs(mask) - 1;
-      key = max(key, ordered(magnitude(in.exactly(column(i / 8) + i % 8, f, g))));
+      key = max(key, ordered(magnitude(in.exactly(column(i / 8) + i % 8, f, g, unit))));
     }
 #pragma unroll 1
     for (int c = column(kHeld); c < a.cols; c += team * 8) {
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
       in.again(c, f, g, v, unused);
 #pragma unroll
       for (int i = 0; i < 8; ++i) mask |= (fabsf(v[i]) >= near ? 1u : 0u) << i;
-      for (; mask; mask &= mask - 1) key = max(key, ordered(magnitude(in.exactly(c + __ffs(mask) - 1, f, g))));
+      for (; mask; mask &= mask - 1) key = max(key, ordered(magnitude(in.exactly(c + __ffs(mask) - 1, f, g, unit))));
     }
     if constexpr (kTeam == 0) {
       if (key) atomicMax(&exact, key);
@@ -539,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   if constexpr (kPeakFirst) {
     if (!tiny) find_peak();  // the block's threads agree on that
   }
-  const float inverse = tiny ? 0x1p126f : __fdiv_rn(127.f, peak.hi);
+  const float per = __fdiv_rn(127.f, peak.hi), inverse = tiny ? 0x1p126f : per * power_of_two(unit);
   const float border = tiny ? 1.f : 0.5f - kMargin<kOp, kPeakFirst>;
   // eight codes; the mask of those next to a border
   auto encode = [&](int c, const float(&v)[8]) {
@@ -564,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
     return mask;
   };
   auto correct = [&](int c) {
-    const Two v = in.exactly(c, f, g), m = magnitude(v);
-    codes[c] = static_cast<int8_t>(copysignf(decide(m, peak, m.hi * inverse), v.hi));
+    const Two v = in.exactly(c, f, g, unit), m = magnitude(v);
+    codes[c] = static_cast<int8_t>(copysignf(decide(m, peak, per), v.hi));
   };
   uint32_t mask = 0;
 #pragma unroll
