@@ -66,3 +66,27 @@ def test_gate_halves_at_the_ends(gate, power, cols, dtype):
     assert torch.equal(x[0, cols:].double(), up * 2.0 ** power) and x[0, 0] == gate
     codes, scales = pkg.swiglu_q8(x.cuda())
     assert scales.item() > 2.0 ** -126 and torch.equal(codes.cpu()[0, :cols].double(), torch.round(up) * math.copysign(1, gate))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", COLS)
+def test_gates_as_large_as_their_type(cols, dtype):
+    """A finite gate of any size is one: past 87.3 its exponential counts as nothing."""
+    import dual_ar_tts_gb300 as pkg
+    dt = eb.TYPES[dtype]
+    most = torch.finfo(dt).max
+    g, u = _rand((6, cols), 12), _rand((6, cols), 13).clamp(-4, 4)
+    g[0, 3], u[0, 3] = 3e38, 0.5
+    g[1, cols - 1], u[1, cols - 1] = -3e38, 2.0
+    g[2], u[2] = g[2].sign() * most, u[2] / 5
+    g[3], u[3] = -most, u[3] * 1e30
+    g[4, 7], u[4, 7] = 2.4e38, 1e-38
+    g[5] *= 1e37
+    x = torch.cat([g, u], 1)
+    _check_gate(x, dt)
+    x = x.to(dt)
+    for at, v in ((3, math.inf), (3, -math.inf), (3, math.nan), (cols + 3, math.inf), (cols + 3, math.nan)):
+        y = x.clone()
+        y[:, at] = v
+        codes, scales = pkg.swiglu_q8(y.cuda())
+        assert torch.isnan(scales).all() and (codes == 0).all(), (at, v)
