@@ -325,41 +325,42 @@ struct Row {
       }
     }
   }
-  // The same once more, of h f and w g.
-  __device__ __forceinline__ void again(int c, float f, float g, float (&v)[8], float& squares) const {
+  // A norm's h and weights of columns c .. c + 7, once more
+  __device__ __forceinline__ void operands(int c, float (&h)[8], float (&w)[8]) const {
+    Eight<T> hs;
+    Eight<float> ws;
+    if constexpr (kOp == kNormResidual)
+      hs.template load<false>(total, c, cols, total_skew);
+    else
+      hs.template load<kKeep>(x, c, cols, skew);
+    ws.template load<true>(weight, c, cols, weight_skew);
+    hs.get(h);
+    ws.get(w);
+  }
+  // Values once more
+  __device__ __forceinline__ void again(int c, float (&v)[8]) const {
     if constexpr (kNorms) {
-      Eight<T> h;
-      Eight<float> weights;
-      if constexpr (kOp == kNormResidual)
-        h.template load<false>(total, c, cols, total_skew);
-      else
-        h.template load<kKeep>(x, c, cols, skew);
-      weights.template load<true>(weight, c, cols, weight_skew);
       float w[8];
-      h.get(v);
-      weights.get(w);
+      operands(c, v, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = v[i] * f;
-        squares = __fmaf_rn(t, t, squares);
-        v[i] = __fmul_rn(t, w[i] * g);
-      }
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], w[i]);
     } else {
       In in;
+      float unused;
       load(c, in);
-      values(c, in, v, squares);
+      values(c, in, v, unused);
     }
   }
 
-  // One column's value times 2^unit, to 2^-44 or exactly
-  __device__ __forceinline__ Two exactly(int c, float f, float g, int unit) const {
+  // One column's value (of a norm h w) times 2^unit, to 2^-44 or exactly
+  __device__ __forceinline__ Two exactly(int c, int unit) const {
     if constexpr (kOp == kGate) {
       return gate_exactly(to_f(x[c]), to_f(other[c]), unit);
     } else if constexpr (kOp == kQuantize) {
       return {to_f(x[c]) * power_of_two(unit), 0.f};
     } else {
-      const Two v = two_prod(to_f((kOp == kNormResidual ? total : x)[c]) * f, weight[c] * g);
-      return {v.hi * power_of_two(unit), v.lo * power_of_two(unit)};
+      const Split h = split(to_f((kOp == kNormResidual ? total : x)[c])), w = split(weight[c]);
+      return scaled(two_prod(h.m, w.m), h.e + w.e + unit);
     }
   }
 };
@@ -419,7 +420,106 @@ struct Team {
       if constexpr (kSum) s = warp_sum(t.y);
     }
   }
+  // of a block in *shared, which was zero
+  __device__ static __forceinline__ unsigned long long largest(unsigned long long key, unsigned long long* shared) {
+    if constexpr (kTeam == 0) {
+      if (key) atomicMax(shared, key);
+      __syncthreads();
+      key = *reinterpret_cast<volatile unsigned long long*>(shared);
+    } else {
+#pragma unroll
+      for (int o = kTeam / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(mask(), key, o));
+    }
+    return key;
+  }
 };
+
+constexpr float kMost = 3.4028234663852886e38f;
+// at most what 127 times is finite
+__device__ __forceinline__ float scale_of(float largest) { return fminf(fmaxf(__fdiv_rn(largest, 127.f), 0x1p-126f), 0x1.020406p+121f); }
+
+// A norm's row whose squares or products leave fp32's range, or the places that it has near its lower end: h is taken times 2^h_up, h w
+// times 2^product_up, which bring the largest to 1 .. 4, from their significands and exponents.  Sums are in the order of k_q8_rows.
+// Such rows are rare (and rows of zeros end after the first pass), so nothing is held; they have a function of their own so that the
+// others keep their registers (as a second round of k_q8_rows itself: norm of 5916 x 2560 with a residual, bf16 26.2 us, so 24.0; fp32 42.8
+// and 34.4).
+template <typename T, Op kOp, int kTeam>
+__device__ __noinline__ void norm_by_exponents(const RowArgs a, long long row, float2* shared, float2* shared_too,
+                                               unsigned long long* exact) {
+  using R = Row<T, kOp>;
+  const R in(a, row);
+  const T* const from = kOp == kNormResidual ? in.total : in.x;
+  const int team = kTeam == 0 ? blockDim.x : kTeam, me = kTeam == 0 ? threadIdx.x : threadIdx.x % kTeam;
+  int8_t* codes = a.codes + row * a.pitch;
+  constexpr int kZero = 400;  // all exponents are above -400
+  float h_most = 0.f, product_most = 0.f, unused = 0.f;
+#pragma unroll 1
+  for (int c = me * 8; c < a.cols; c += team * 8) {
+    float h[8], w[8];
+    in.operands(c, h, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = split(h[i]).e + kZero, p = split(w[i]).e + e;
+      if (h[i] != 0.f) h_most = fmaxf(h_most, static_cast<float>(e));
+      if (h[i] != 0.f && w[i] != 0.f) product_most = fmaxf(product_most, static_cast<float>(p));
+    }
+  }
+  Team<kTeam>::template reduce<false>(h_most, unused, shared_too);
+  Team<kTeam>::template reduce<false>(product_most, unused, shared);
+  int h_up = h_most > 0.f ? kZero - static_cast<int>(h_most) : 0;
+  if (a.eps > 0.f) h_up = min(h_up, -(split(a.eps).e >> 1));  // beside eps, what is lower than half of its exponent does not count
+  const int product_up = kZero - static_cast<int>(product_most), back = h_up - product_up;
+  const float eps = ldexpf(a.eps, 2 * h_up);
+  // h w 2^product_up in fp32; not a number where one of them is not finite
+  auto product = [&](float h, float w) {
+    const Split p = split(h), q = split(w);
+    const float bad = __fadd_rn(__fsub_rn(h, h), __fsub_rn(w, w));
+    return h == 0.f || w == 0.f ? bad : __fmul_rn(p.m, q.m) * power_of_two(min(max(p.e + q.e + product_up, -126), 1)) + bad;
+  };
+  float squares = 0.f, most = 0.f;
+#pragma unroll 1
+  for (int c = me * 8; c < a.cols && h_most > 0.f; c += team * 8)
+#pragma unroll 1
+    for (int i = c; i < min(c + 8, a.cols); ++i) {
+      const float h = to_f(from[i]);
+      const Split p = split(h);
+      const float t = h == 0.f ? 0.f : p.m * power_of_two(min(max(p.e + h_up, -126), 1));
+      squares = __fmaf_rn(t, t, squares);
+      most = max_nan(most, fabsf(product(h, a.weight[i])));
+    }
+  Team<kTeam>::template reduce<true>(most, squares, shared_too);
+  const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), eps)));
+  const float largest = ldexpf(most * r, back);
+  const bool finite = largest <= kMost;
+  if (me == 0) a.scales[row] = finite ? scale_of(largest) : __uint_as_float(0x7fc00000u);
+  if (!finite || most == 0.f) {
+    for (int c = me * 8; c < a.pitch; c += team * 8) *reinterpret_cast<uint2*>(codes + c) = make_uint2(0, 0);
+    return;
+  }
+  const bool tiny = largest < 127 * 0x1p-126f;
+  unsigned long long key = 0;
+#pragma unroll 1
+  for (int c = me * 8; c < a.cols && !tiny; c += team * 8)
+#pragma unroll 1
+    for (int i = c; i < min(c + 8, a.cols); ++i)
+      if (fabsf(product(to_f(from[i]), a.weight[i])) >= most * (1.f - 0x1p-18f))
+        key = max(key, ordered(magnitude(in.exactly(i, product_up))));
+  key = Team<kTeam>::largest(key, exact);
+  const Two peak = tiny ? Two{127.f, 0.f} : from_ordered(key);
+  const float per = tiny ? r * power_of_two(max(126 + back, -126)) : __fdiv_rn(127.f, peak.hi);
+#pragma unroll 1
+  for (int c = me * 8; c < a.pitch; c += team * 8) {
+    unsigned long long word = 0;
+#pragma unroll 1
+    for (int i = c; i < min(c + 8, a.cols); ++i) {
+      const float v = product(to_f(from[i]), a.weight[i]), t = fabsf(v) * per;
+      float k = rintf(t);
+      if (!tiny && fabsf(t - k) > 0.5f - kMargin<kOp, false>) k = decide(magnitude(in.exactly(i, product_up)), peak, per);
+      word |= static_cast<unsigned long long>(static_cast<uint8_t>(static_cast<int>(copysignf(k, v)))) << 8 * (i - c);
+    }
+    *reinterpret_cast<unsigned long long*>(codes + c) = word;
+  }
+}
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole number, which the sum's low bits then hold
 
@@ -447,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   const R in(a, row);
   auto column = [&](int h) { return (h * team + me) * 8; };
   float held[kHeld][8];
-  float f = 1.f, g = 1.f, squares = 0.f, most = 0.f;
+  float squares = 0.f, most = 0.f;
   auto look = [&](const float(&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(v[i]));
@@ -477,41 +577,28 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   }
   float mine = most;
   Team<kTeam>::template reduce<kNorms>(most, squares, shared[0]);
-  float r = 1.f;  // of a norm, 1 / f times the row's factor, to a few last places
+  float r = 1.f;  // of a norm the row's factor, to a few last places
   if constexpr (kNorms) {
-    if (isinf(most) || isinf(squares)) {  // perhaps only past fp32's range: once more with what is too large times 2^-80
-      if (isinf(squares)) f = 0x1p-80f;
-      if (isinf(most)) g = 0x1p-80f;
-      squares = most = 0.f;
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h) {
-        if (column(h) < a.cols) in.again(column(h), f, g, held[h], squares);
-        look(held[h]);
-      }
-#pragma unroll 1
-      for (int c = column(kHeld); c < a.cols; c += team * 8) {
-        float v[8];
-        in.again(c, f, g, v, squares);
-        look(v);
-      }
-      mine = most;
-      Team<kTeam>::template reduce<kNorms>(most, squares, shared[1]);
+    // Sums and products in fp32 are good while nothing that counts leaves its range: squares past it or so small that what falls below
+    // it counts beside eps, products past it or so small that their last places are lost.
+    const float mean = __fmaf_rn(squares, a.per_col, a.eps);
+    if (isinf(most) || isinf(squares) || most < 0x1p-64f || mean < 0x1p-100f) {
+      norm_by_exponents<T, kOp, kTeam>(a, row, shared[0], shared[1], &exact);
+      return;
     }
-    r = rsqrtf(__fmaf_rn(squares, a.per_col, a.eps * f * f));
+    r = rsqrtf(mean);
   }
-  const float back = g == 1.f ? 1.f : 0x1p80f;
   int8_t* codes = a.codes + row * a.pitch;
-  if (!(most * r * back <= 3.4028234663852886e38f)) {  // not finite
+  if (!(most * r <= kMost)) {  // not finite
     for (int c = me * 8; c < a.pitch; c += team * 8) *reinterpret_cast<uint2*>(codes + c) = make_uint2(0, 0);
     if (me == 0) a.scales[row] = __uint_as_float(0x7fc00000u);
     return;
   }
-  const bool tiny = most * r * back < 127 * 0x1p-126f;  // the step is its least, the quotient is v 2^126
+  const bool tiny = most * r < 127 * 0x1p-126f;  // the step is its least, the quotient is v 2^126
   const float early = r;
   if (me == 0) {
-    if (kNorms) r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), a.eps * f * f)));
-    // at most what 127 times is finite
-    a.scales[row] = fminf(fmaxf(__fdiv_rn(most * r * back, 127.f), 0x1p-126f), 0x1.020406p+121f);
+    if (kNorms) r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), a.eps)));
+    a.scales[row] = scale_of(most * r);
   }
   if (kNorms && tiny) {
 #pragma unroll
@@ -536,25 +623,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
     }
     for (; mask; mask &= mask - 1) {
       const int i = __ffs(mask) - 1;
-      key = max(key, ordered(magnitude(in.exactly(column(i / 8) + i % 8, f, g, unit))));
+      key = max(key, ordered(magnitude(in.exactly(column(i / 8) + i % 8, unit))));
     }
 #pragma unroll 1
     for (int c = column(kHeld); c < a.cols; c += team * 8) {
-      float v[8], unused = 0.f;
-      in.again(c, f, g, v, unused);
+      float v[8];
+      in.again(c, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) mask |= (fabsf(v[i]) >= near ? 1u : 0u) << i;
-      for (; mask; mask &= mask - 1) key = max(key, ordered(magnitude(in.exactly(c + __ffs(mask) - 1, f, g, unit))));
+      for (; mask; mask &= mask - 1) key = max(key, ordered(magnitude(in.exactly(c + __ffs(mask) - 1, unit))));
     }
-    if constexpr (kTeam == 0) {
-      if (key) atomicMax(&exact, key);
-      __syncthreads();
-      key = *reinterpret_cast<volatile unsigned long long*>(&exact);
-    } else {
-#pragma unroll
-      for (int o = kTeam / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(Team<kTeam>::mask(), key, o));
-    }
-    peak = from_ordered(key);
+    peak = from_ordered(Team<kTeam>::largest(key, &exact));
   };
   if constexpr (kPeakFirst) {
     if (!tiny) find_peak();  // the block's threads agree on that
@@ -584,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
     return mask;
   };
   auto correct = [&](int c) {
-    const Two v = in.exactly(c, f, g, unit), m = magnitude(v);
+    const Two v = in.exactly(c, unit), m = magnitude(v);
     codes[c] = static_cast<int8_t>(copysignf(decide(m, peak, per), v.hi));
   };
   uint32_t mask = 0;
@@ -606,10 +685,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   }
 #pragma unroll 1
   for (int c = column(kHeld); c < a.pitch; c += team * 8) {
-    float v[8], unused = 0.f;
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (c < a.cols) in.again(c, f, g, v, unused);
+    if (c < a.cols) in.again(c, v);
     if (kNorms && tiny) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= early;
@@ -644,7 +723,9 @@ int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
       if (a.cols > 4096 && sizeof(T) == 2) return launch_teams<T, kOp, 4, 0, 320, 3>(a, std::min(320, threads(4)), st);
     }
     if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 6>(a, 128, st);
-    if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, 4>(a, threads(2), st);
+    // (64 registers are too few for fp32 rows with a residual: 5916 x 2560 36.6, with up to 80 34.4.)
+    constexpr int kBlocks = sizeof(T) == 4 && kOp == kNormResidual ? 3 : 4;
+    if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, kBlocks>(a, threads(2), st);
     // Norms past 4096 columns: two blocks an SM (2048 x 9728 bf16 without a residual 25.7, with one block 40.8); with a residual
     // smaller ones (bf16 36.8, 42.5; 2000 x 5000 fp32 26.0, 29.2; of one row 3.5 and 4.1, where 640 threads take 3.1).  Nothing here
     // goes by the rows: a row's sums, and so its scale's last place, are the same in any batch.

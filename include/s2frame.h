@@ -483,7 +483,8 @@ int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* log
  *   step = max(max|v| / 127, 2^-126),  scale = step rounded to fp32,  code[i] = v[i] / step rounded to the
  *   nearest whole number, ties (within 2^-42) to even: -127..127
  * and stands for scale * code (the scale is no more than the largest number that is finite 127 times).  Codes
- * are those of the exact quotients (of a norm and a gate, of v to 2^-44 or so), scales of norms and gates are good to
+ * are those of the exact quotients (of a norm and a gate, of v to 2^-44 or so; where a norm's step is 2^-126, of v as
+ * fp32 has it), scales of norms and gates are good to
  * a few roundings of fp32 (norms of rows past some 2^16 columns: to those of a sum of so many squares).  A row that holds
  * something not finite, or whose values or norm come to that in fp32, gets scale NaN and codes 0, so that products with
  * it are NaN.

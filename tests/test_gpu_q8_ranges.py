@@ -90,3 +90,82 @@ def test_gates_as_large_as_their_type(cols, dtype):
         y[:, at] = v
         codes, scales = pkg.swiglu_q8(y.cuda())
         assert torch.isnan(scales).all() and (codes == 0).all(), (at, v)
+
+
+def _check_norm(x, w, eps, dt, residual=False):
+    import dual_ar_tts_gb300 as pkg
+    x, w = x.to(dt), w.float()
+    assert torch.isfinite(x).all() and torch.isfinite(w).all()
+    res = (x.double() / 2).to(dt) if residual else None
+    out = pkg.rms_norm_q8(x.cuda(), w.cuda(), eps, residual=None if res is None else res.cuda())
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    v, r, total = eb.norm(x, w, eps, res)
+    assert ((v * r).abs() <= torch.finfo(torch.float32).max).all()
+    want, scale, distance = eb.coded(v, r)
+    if residual:
+        assert torch.equal(out[2].cpu(), total)
+    # as many additions as a thread's elements (32 of up to 1024 columns; 16, or eight of every 3328 at least), then as there
+    cols = x.shape[1]
+    adds = 32 if cols <= 1024 else max(16, 8 * math.ceil(cols / 3328))
+    got = out[1].cpu().double()
+    assert ((got - scale).abs() <= ((adds + 12) / 2 + 7) * eb.STEP * scale).all(), (got / scale)
+    least = scale <= 2.0 ** -126
+    eb.check_codes(out[0].cpu()[~least], want[~least], distance[~least], SURE)
+    # at the least step a code is the value's, as fp32 has it: off by the factor's roundings
+    tol = ((adds + 12) / 2 + 7) * eb.STEP * 127
+    eb.check_codes(out[0].cpu()[least], want[least], distance[least], tol)
+
+
+# (of x, of the weight, eps): all below are what a finite norm is made of
+SMALL = [(1e-12, 1e-25, 1e-6), (1e-13, 1e-25, 1e-6), (1e-21, 1.0, 0.0), (1e-30, 1e-5, 0.0), (1e-37, 1.0, 0.0), (3e-39, 1e20, 1e-38), (1e-19, 1e-12, 1e-40),
+         (1e-20, 1e-15, 1e-6), (1e-30, 1e20, 1e-20), (1.0, 1e-36, 1e-6), (1e30, 1e-30, 1e-6), (1e36, 1e-37, 0.0), (1e37, 1e3, 1e-6),
+         (1e20, 1e-38, 1e-6), (1e-25, 1e-25, 1e-6)]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", [300, 1300, 5000, 20001])
+@pytest.mark.parametrize("size,weight,eps", SMALL)
+def test_norm_of_factors_out_of_range(size, weight, eps, cols, dtype):
+    """Squares or products with the weight that leave fp32's range while the norm does not."""
+    x, w = _rand((9, cols), 14) * size, torch.exp(0.3 * _rand(cols, 15)) * weight
+    _check_norm(x, w, eps, eb.TYPES[dtype], residual=cols in (300, 5000))
+
+
+@pytest.mark.parametrize("cols", [300, 5000])
+def test_norm_of_small_fp16_rows(cols):
+    for weight, eps in ((1e-25, 1e-6), (1e-30, 0.0), (1e30, 0.0)):
+        _check_norm(_rand((5, cols), 16) * 3e-7, torch.exp(0.3 * _rand(cols, 15)) * weight, eps, torch.float16, residual=True)
+
+
+@pytest.mark.parametrize("cols", [300, 5000])
+def test_norm_of_uneven_factors(cols):
+    """Large weights meet elements that are small or nothing."""
+    w = torch.full((cols,), 1e-30, dtype=torch.float64)
+    x = _rand((4, cols), 17) * 1e-12
+    w[0], w[1], w[2] = 3e38, 1e38, 1e20
+    x[:, 0], x[1, 1], x[2, 1] = 0.0, 1e-44, 0.0
+    x[[0, 3], 1] = 0.0
+    x[:3, 2] = 0.0
+    _check_norm(x, w, 1e-6, torch.float32)
+    _check_norm(x * 2.0 ** -90, w, 0.0, torch.float32)
+    for at, v in ((0, math.inf), (cols - 1, math.nan)):
+        import dual_ar_tts_gb300 as pkg
+        y = x.clone().float()
+        y[1, at] = v
+        codes, scales = pkg.rms_norm_q8(y.cuda(), w.float().cuda(), 1e-6)
+        assert torch.equal(torch.isnan(scales).cpu(), torch.tensor([False, True, False, False])) and (codes[1] == 0).all()
+
+
+@pytest.mark.parametrize("cols", [255, 1500, 5000])
+@pytest.mark.parametrize("weight,power", [(1.1, -113), (1.1e-20, -60), (1.1e-30, -30), (1.1e-37, 20), (1.1e37, 20), (1.1, 100)])
+def test_norm_halves_at_the_ends(weight, power, cols):
+    """Elements under one weight: exact halves go to the even code, whatever range the products are in."""
+    import dual_ar_tts_gb300 as pkg
+    half = torch.arange(0.5, 127.0, 1.0, dtype=torch.float64)
+    x = torch.cat([half, torch.tensor([127.0]), -half]).repeat(cols // 255 + 1)[:cols]
+    codes, scales = pkg.rms_norm_q8((x * 2.0 ** power)[None].float().cuda(), torch.full((cols,), weight, device="cuda"), 0.0)
+    if 1.7 * weight >= 127 * 2.0 ** -126:         # the largest of the norm: 127 / rms
+        assert torch.equal(codes.cpu()[0, :cols].double(), torch.round(x))
+    rms = x.square().mean().sqrt().item()
+    want = float(torch.tensor(weight)) / rms
+    assert abs(scales.item() / max(want, 2.0 ** -126) - 1) <= ((32 + 12) / 2 + 7) * eb.STEP
