@@ -607,10 +607,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
       for (int i = 0; i < 8; ++i) held[h][i] *= early;
   }
 
-  // The largest magnitude to more than fp32: of what comes near to it, the largest.  What is taken exactly is held times 2^unit, which
-  // brings the largest to 1 .. 4.
-  const int unit = 127 - min(static_cast<int>(__float_as_uint(most) >> 23), 253);
-  Two peak{most * power_of_two(unit), 0.f};
+  // What codes go by, the largest magnitude or what has the least step, to more than fp32: of what comes near to it, the largest.  What
+  // is taken exactly is held times 2^unit, which brings that to 1 .. 4.
+  const float top = tiny ? 127 * 0x1p-126f : most;
+  const int unit = 127 - min(static_cast<int>(__float_as_uint(top) >> 23), 253);
+  Two peak{top * power_of_two(unit), 0.f};
   auto find_peak = [&] {
     const float near = most * (1.f - 0x1p-18f);
     unsigned long long key = 0;
@@ -638,8 +639,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   if constexpr (kPeakFirst) {
     if (!tiny) find_peak();  // the block's threads agree on that
   }
-  const float per = __fdiv_rn(127.f, peak.hi), inverse = tiny ? 0x1p126f : per * power_of_two(unit);
-  const float border = tiny ? 1.f : 0.5f - kMargin<kOp, kPeakFirst>;
+  const float per = __fdiv_rn(127.f, peak.hi), inverse = per * power_of_two(unit);
+  // (of a tiny row the quantiser's quotients are exact, and a norm's are what fp32 has)
+  const float border = tiny && kOp != kGate ? 1.f : 0.5f - kMargin<kOp, kPeakFirst>;
   // eight codes; the mask of those next to a border
   auto encode = [&](int c, const float(&v)[8]) {
     float k[8], d[8], far = 0.f;

@@ -70,6 +70,26 @@ def test_gate_halves_at_the_ends(gate, power, cols, dtype):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("cols", COLS)
+def test_gate_of_small_rows(cols, dtype):
+    """Values about the least step and below, ordinary gates: codes are still the exact quotients'."""
+    rows = max(4, 1_000_000 // cols)
+    g, u = _rand((rows, cols), 6), _uniform((rows, cols), 7)
+    u *= 2.0 ** _uniform((rows, 1), 8, -122, -117)
+    _check_gate(torch.cat([g, u], 1), eb.TYPES[dtype])
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_gate_borders_at_the_least_step(cols):
+    """Values as near as fp32 operands bring them to borders between multiples of the least step: fp32's own roundings would put many of
+    them on the wrong side."""
+    g = _rand((20, cols), 18).float().double()
+    g = torch.where(g.abs() < 0.1, torch.full_like(g, 0.7), g)
+    v = (torch.floor(_uniform((20, cols), 19, -126, 126)) + 0.5) * 2.0 ** -126
+    _check_gate(torch.cat([g, v * (1 + torch.exp(-g)) / g], 1), torch.float32)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", COLS)
 def test_gates_as_large_as_their_type(cols, dtype):
     """A finite gate of any size is one: past 87.3 its exponential counts as nothing."""
     import dual_ar_tts_gb300 as pkg
