@@ -90,6 +90,16 @@ def test_gate_borders_at_the_least_step(cols):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("cols", COLS)
+def test_gate_below_the_range(cols, dtype):
+    """Gates (and their silu) below fp32's normal range times numbers that bring the values back into it."""
+    rows = max(4, 300_000 // cols)
+    g, u = _rand((rows, cols), 9), _uniform((rows, cols), 10)
+    g, u = g * 2.0 ** _uniform((rows, 1), 8, -140, -126), u * 2.0 ** _uniform((rows, 1), 11, 20, 127)
+    _check_gate(torch.cat([g, u], 1), eb.TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", COLS)
 def test_gates_as_large_as_their_type(cols, dtype):
     """A finite gate of any size is one: past 87.3 its exponential counts as nothing."""
     import dual_ar_tts_gb300 as pkg
