@@ -244,17 +244,15 @@ struct Eight {
 
 // silu(g) u = (u / (1 + e)) g, times e for negative g, e = exp(-|g|) = 2^(-|g| log2 e) with the product's rounding taken back.  Off by
 // up to: e, four last places' halves from ex2 and 1.5 more; the sum one, its reciprocal two, three products.  An e below 2^-126
-// (g beyond 87.3) is zero.  Past 2.36e38 (which fp16 does not reach) |g| log2 e would be infinite and its rounding not a number, so
-// |g| is taken as 128 at most: 2048 x 9728 bf16 30.1 us, 29.6 without; only in rows that come out not finite, done once more, 30.4.
+// (g beyond 87.3) is zero.  The product with log2 e is rounded towards zero, which of gates past 2.36e38 leaves
+// fp32's largest number instead of an infinity, whose rounding is not a number (|g| taken as 128 at most: 2048 x 9728 bf16 30.0 us, so 29.6).
 // The gate comes last: u g may pass fp32's range where the value does not, silu(g) of a small g lose places below it that a large u brings
 // back; u sigmoid(g) loses at most 88 2^-150 of the value, 2^-17 of the least step.
 // (expf and __fdividef: 12 instructions more, 33.0 us against 29.8 for 2048 x 9728 bf16.)
-template <typename T>
 __device__ __forceinline__ float gate_fast(float g, float u) {
   constexpr double kLog2 = 1.44269504088896340735992468100;
   constexpr float kHi = static_cast<float>(kLog2), kLo = static_cast<float>(kLog2 - kHi), kLn2 = 0.69314718f;
-  const float a = std::is_same<T, __half>::value ? -fabsf(g) : fmaxf(-fabsf(g), -128.f);
-  const float y = __fmul_rn(a, kHi), rest = __fmaf_rn(a, kLo, __fmaf_rn(a, kHi, -y));
+  const float a = -fabsf(g), y = __fmul_rz(a, kHi), rest = __fmaf_rn(a, kLo, __fmaf_rn(a, kHi, -y));
   float e, d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
   e = __fmaf_rn(e, __fmul_rn(rest, kLn2), e);
@@ -306,7 +304,7 @@ struct Row {
       float u[8];
       in.other.get(u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = gate_fast<T>(v[i], u[i]);
+      for (int i = 0; i < 8; ++i) v[i] = gate_fast(v[i], u[i]);
     }
     if constexpr (kOp == kNormResidual) {
       float r[8];
