@@ -573,7 +573,8 @@ def _bind_q8():
     try:
         from . import _calls as module
     except ImportError as e:
-        raise ImportError(f"{e}: run `python -c 'import __graft_entry__ as g; g.build()'`") from e
+        raise ImportError(f"{e}: run `python -c 'import __graft_entry__ as g; g.build()'` where torch and Python's headers "
+                          "are installed") from e
     module.set_error(S2Error)
     _q8 = module
     return module
