@@ -721,23 +721,31 @@ int launch_rows(const RowArgs& a, int dtype, cudaStream_t st) {
     if constexpr (kOp == kQuantize || kOp == kGate) {
       if (a.cols <= 128) return launch_teams<T, kOp, 2, 8, 128, 8>(a, 128, st);
       if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 8>(a, 128, st);
-      if (a.cols <= 4096 && kOp == kQuantize) return launch_teams<T, kOp, 4, 0, 128, 6>(a, threads(4), st);
-      if (a.cols > 4096 && sizeof(T) == 2) return launch_teams<T, kOp, 4, 0, 320, 3>(a, std::min(320, threads(4)), st);
-    }
-    if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 6>(a, 128, st);
-    // (64 registers are too few for fp32 rows with a residual: 5916 x 2560 36.6, with up to 80 34.4.)
-    constexpr int kBlocks = sizeof(T) == 4 && kOp == kNormResidual ? 3 : 4;
-    if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, kBlocks>(a, threads(2), st);
-    // Norms past 4096 columns: two blocks an SM (2048 x 9728 bf16 without a residual 25.7, with one block 40.8); with a residual
-    // smaller ones (bf16 36.8, 42.5; 2000 x 5000 fp32 26.0, 29.2; of one row 3.5 and 4.1, where 640 threads take 3.1).  Nothing here
-    // goes by the rows: a row's sums, and so its scale's last place, are the same in any batch.
-    if constexpr (kOp == kNormResidual) {
+      if (a.cols <= 4096) {
+        if constexpr (kOp == kQuantize)
+          return launch_teams<T, kOp, 4, 0, 128, 6>(a, threads(4), st);
+        else
+          return launch_teams<T, kOp, 2, 0, 256, 4>(a, threads(2), st);
+      }
       if constexpr (sizeof(T) == 2)
+        return launch_teams<T, kOp, 4, 0, 320, 3>(a, std::min(320, threads(4)), st);
+      else
+        return launch_teams<T, kOp, 2, 0, 640, 2>(a, std::min(640, threads(2)), st);
+    } else {
+      if (a.cols <= 1024) return launch_teams<T, kOp, 4, 32, 128, 6>(a, 128, st);
+      // (64 registers are too few for fp32 rows with a residual: 5916 x 2560 36.6, with up to 80 34.4.)
+      constexpr int kBlocks = sizeof(T) == 4 && kOp == kNormResidual ? 3 : 4;
+      if (a.cols <= 4096) return launch_teams<T, kOp, 2, 0, 256, kBlocks>(a, threads(2), st);
+      // Norms past 4096 columns: two blocks an SM (2048 x 9728 bf16 without a residual 25.7, with one block 40.8); with a residual
+      // smaller ones (bf16 36.8, 42.5; 2000 x 5000 fp32 26.0, 29.2; of one row 3.5 and 4.1, where 640 threads take 3.1).  Nothing here
+      // goes by the rows: a row's sums, and so its scale's last place, are the same in any batch.
+      if constexpr (kOp == kNorm)
+        return launch_teams<T, kOp, 2, 0, 640, 2>(a, std::min(640, threads(2)), st);
+      else if constexpr (sizeof(T) == 2)
         return launch_teams<T, kOp, 3, 0, 416, 2>(a, std::min(416, threads(3)), st);
       else
         return launch_teams<T, kOp, 2, 0, 512, 2>(a, std::min(512, threads(2)), st);
     }
-    return launch_teams<T, kOp, 2, 0, 640, 2>(a, std::min(640, threads(2)), st);
   });
 }
 
