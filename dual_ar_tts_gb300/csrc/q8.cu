@@ -244,8 +244,8 @@ struct Eight {
 
 // silu(g) u = (u / (1 + e)) g, times e for negative g, e = exp(-|g|) = 2^(-|g| log2 e) with the product's rounding taken back.  Off by
 // up to: e, four last places' halves from ex2 and 1.5 more; the sum one, its reciprocal two, three products.  An e below 2^-126
-// (g beyond 87.3) is zero.  The product with log2 e is rounded towards zero, which of gates past 2.36e38 leaves
-// fp32's largest number instead of an infinity, whose rounding is not a number (|g| taken as 128 at most: 2048 x 9728 bf16 30.0 us, so 29.6).
+// (g beyond 87.3) is zero.  The product with log2 e is rounded towards zero, which of gates past 2.36e38 leaves fp32's largest
+// number instead of an infinity, whose rounding is not a number (|g| taken as 128 at most: 2048 x 9728 bf16 30.0 us, so 29.7).
 // The gate comes last: u g may pass fp32's range where the value does not, silu(g) of a small g lose places below it that a large u brings
 // back; u sigmoid(g) loses at most 88 2^-150 of the value, 2^-17 of the least step.
 // (expf and __fdividef: 12 instructions more, 33.0 us against 29.8 for 2048 x 9728 bf16.)
@@ -440,55 +440,51 @@ __device__ __forceinline__ float scale_of(float largest) { return fminf(fmaxf(__
 
 // A norm's row whose squares or products leave fp32's range, or the places that it has near its lower end: h is taken times 2^h_up, h w
 // times 2^product_up, which bring the largest to 1 .. 4, from their significands and exponents.  Sums are in the order of k_q8_rows.
-// Such rows are rare (and rows of zeros end after the first pass), so nothing is held; they have a function of their own so that the
-// others keep their registers (as a second round of k_q8_rows itself: norm of 5916 x 2560 with a residual, bf16 26.2 us, so 24.0; fp32 42.8
-// and 34.4).
+// Such rows are rare, so nothing is held; they have a function of their own, and it takes its columns one by one, so that the others
+// keep their registers (as a second round of k_q8_rows itself: norm of 5916 x 2560 with a residual, bf16 26.2 us, so 24.1; fp32 42.8
+// and 34.5; by eights 26.3 and 38.2.  Of such rows alone bf16 103, by eights 91).
 template <typename T, Op kOp, int kTeam>
 __device__ __noinline__ void norm_by_exponents(const RowArgs a, long long row, float2* shared, float2* shared_too,
                                                unsigned long long* exact) {
   using R = Row<T, kOp>;
   const R in(a, row);
-  const T* const from = kOp == kNormResidual ? in.total : in.x;
   const int team = kTeam == 0 ? blockDim.x : kTeam, me = kTeam == 0 ? threadIdx.x : threadIdx.x % kTeam;
   int8_t* codes = a.codes + row * a.pitch;
   constexpr int kZero = 400;  // all exponents are above -400
-  float h_most = 0.f, product_most = 0.f, unused = 0.f;
+  const T* const from = kOp == kNormResidual ? in.total : in.x;
+  auto each = [&](auto f) {  // of this thread's columns
 #pragma unroll 1
-  for (int c = me * 8; c < a.cols; c += team * 8) {
-    float h[8], w[8];
-    in.operands(c, h, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = split(h[i]).e + kZero, p = split(w[i]).e + e;
-      if (h[i] != 0.f) h_most = fmaxf(h_most, static_cast<float>(e));
-      if (h[i] != 0.f && w[i] != 0.f) product_most = fmaxf(product_most, static_cast<float>(p));
-    }
-  }
+    for (int c = me * 8; c < a.cols; c += team * 8)
+#pragma unroll 1
+      for (int i = c; i < min(c + 8, a.cols); ++i) f(to_f(from[i]), a.weight[i]);
+  };
+  float h_most = 0.f, product_most = 0.f, unused = 0.f;
+  each([&](float h, float w) {
+    const int e = split(h).e + kZero, p = split(w).e + e;
+    if (h != 0.f) h_most = fmaxf(h_most, static_cast<float>(e));
+    if (h != 0.f && w != 0.f) product_most = fmaxf(product_most, static_cast<float>(p));
+  });
   Team<kTeam>::template reduce<false>(h_most, unused, shared_too);
   Team<kTeam>::template reduce<false>(product_most, unused, shared);
   int h_up = h_most > 0.f ? kZero - static_cast<int>(h_most) : 0;
   if (a.eps > 0.f) h_up = min(h_up, -(split(a.eps).e >> 1));  // beside eps, what is lower than half of its exponent does not count
   const int product_up = kZero - static_cast<int>(product_most), back = h_up - product_up;
-  const float eps = ldexpf(a.eps, 2 * h_up);
-  // h w 2^product_up in fp32; not a number where one of them is not finite
   auto product = [&](float h, float w) {
     const Split p = split(h), q = split(w);
-    const float bad = __fadd_rn(__fsub_rn(h, h), __fsub_rn(w, w));
-    return h == 0.f || w == 0.f ? bad : __fmul_rn(p.m, q.m) * power_of_two(min(max(p.e + q.e + product_up, -126), 1)) + bad;
+    return h == 0.f || w == 0.f ? Two{0.f, 0.f} : scaled(two_prod(p.m, q.m), p.e + q.e + product_up);
   };
   float squares = 0.f, most = 0.f;
-#pragma unroll 1
-  for (int c = me * 8; c < a.cols && h_most > 0.f; c += team * 8)
-#pragma unroll 1
-    for (int i = c; i < min(c + 8, a.cols); ++i) {
-      const float h = to_f(from[i]);
-      const Split p = split(h);
-      const float t = h == 0.f ? 0.f : p.m * power_of_two(min(max(p.e + h_up, -126), 1));
-      squares = __fmaf_rn(t, t, squares);
-      most = max_nan(most, fabsf(product(h, a.weight[i])));
-    }
+  unsigned long long key = 0;
+  each([&](float h, float w) {
+    const Split p = split(h);
+    const float t = h == 0.f ? 0.f : p.m * power_of_two(min(max(p.e + h_up, -126), 1));
+    squares = __fmaf_rn(t, t, squares);
+    key = max(key, ordered(magnitude(product(h, w))));
+    most += __fadd_rn(__fsub_rn(h, h), __fsub_rn(w, w));  // not a number where one of them is not finite
+  });
+  most = fabsf(most + __uint_as_float(static_cast<uint32_t>(key >> 32)));
   Team<kTeam>::template reduce<true>(most, squares, shared_too);
-  const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), eps)));
+  const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, static_cast<float>(a.cols)), ldexpf(a.eps, 2 * h_up))));
   const float largest = ldexpf(most * r, back);
   const bool finite = largest <= kMost;
   if (me == 0) a.scales[row] = finite ? scale_of(largest) : __uint_as_float(0x7fc00000u);
@@ -497,25 +493,18 @@ __device__ __noinline__ void norm_by_exponents(const RowArgs a, long long row, f
     return;
   }
   const bool tiny = largest < 127 * 0x1p-126f;
-  unsigned long long key = 0;
-#pragma unroll 1
-  for (int c = me * 8; c < a.cols && !tiny; c += team * 8)
-#pragma unroll 1
-    for (int i = c; i < min(c + 8, a.cols); ++i)
-      if (fabsf(product(to_f(from[i]), a.weight[i])) >= most * (1.f - 0x1p-18f))
-        key = max(key, ordered(magnitude(in.exactly(i, product_up))));
-  key = Team<kTeam>::largest(key, exact);
-  const Two peak = tiny ? Two{127.f, 0.f} : from_ordered(key);
+  const Two peak = from_ordered(Team<kTeam>::largest(key, exact));
   const float per = tiny ? r * power_of_two(max(126 + back, -126)) : __fdiv_rn(127.f, peak.hi);
 #pragma unroll 1
   for (int c = me * 8; c < a.pitch; c += team * 8) {
     unsigned long long word = 0;
 #pragma unroll 1
     for (int i = c; i < min(c + 8, a.cols); ++i) {
-      const float v = product(to_f(from[i]), a.weight[i]), t = fabsf(v) * per;
+      const Two v = product(to_f(from[i]), a.weight[i]);
+      const float t = fabsf(v.hi * per);
       float k = rintf(t);
-      if (!tiny && fabsf(t - k) > 0.5f - kMargin<kOp, false>) k = decide(magnitude(in.exactly(i, product_up)), peak, per);
-      word |= static_cast<unsigned long long>(static_cast<uint8_t>(static_cast<int>(copysignf(k, v)))) << 8 * (i - c);
+      if (!tiny && fabsf(t - k) > 0.5f - kMargin<kOp, false>) k = decide(magnitude(v), peak, per);
+      word |= static_cast<unsigned long long>(static_cast<uint8_t>(static_cast<int>(copysignf(k, v.hi)))) << 8 * (i - c);
     }
     *reinterpret_cast<unsigned long long*>(codes + c) = word;
   }
@@ -579,14 +568,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_q8_rows(const RowArgs a) 
   Team<kTeam>::template reduce<kNorms>(most, squares, shared[0]);
   float r = 1.f;  // of a norm the row's factor, to a few last places
   if constexpr (kNorms) {
-    // Sums and products in fp32 are good while nothing that counts leaves its range: squares past it or so small that what falls below
-    // it counts beside eps, products past it or so small that their last places are lost.
+    // Sums and products in fp32 are good while nothing that counts leaves its range: squares past it, or so small that what falls below
+    // it counts beside eps; products past it, or so small that codes would not have fp32's places.  (Where the step is its least, products
+    // are off by up to 2^-24 r of it; rows of zeros are such, and any product that is 0 here is one of them while r is up to 2^22.)
     const float mean = __fmaf_rn(squares, a.per_col, a.eps);
-    if (isinf(most) || isinf(squares) || most < 0x1p-64f || mean < 0x1p-100f) {
+    r = rsqrtf(mean);
+    const bool small = most < 0x1p-110f && (r > (most == 0.f ? 0x1p22f : 0x1p10f) || most * r >= 0x1p-120f);
+    if (isinf(most) || isinf(squares) || mean < 0x1p-100f || small) {
       norm_by_exponents<T, kOp, kTeam>(a, row, shared[0], shared[1], &exact);
       return;
     }
-    r = rsqrtf(mean);
   }
   int8_t* codes = a.codes + row * a.pitch;
   if (!(most * r <= kMost)) {  // not finite

@@ -147,9 +147,11 @@ def _check_norm(x, w, eps, dt, residual=False):
 
 
 # (of x, of the weight, eps): all below are what a finite norm is made of
-SMALL = [(1e-12, 1e-25, 1e-6), (1e-13, 1e-25, 1e-6), (1e-21, 1.0, 0.0), (1e-30, 1e-5, 0.0), (1e-37, 1.0, 0.0), (3e-39, 1e20, 1e-38), (1e-19, 1e-12, 1e-40),
+SMALL = [(1e-12, 1e-25, 1e-6), (1e-13, 1e-25, 1e-6), (1e-21, 1.0, 0.0), (1e-30, 1e-5, 0.0), (1e-37, 1.0, 0.0), (3e-39, 1e20, 1e-38),
+         (1e-19, 1e-12, 1e-40),
          (1e-20, 1e-15, 1e-6), (1e-30, 1e20, 1e-20), (1.0, 1e-36, 1e-6), (1e30, 1e-30, 1e-6), (1e36, 1e-37, 0.0), (1e37, 1e3, 1e-6),
-         (1e20, 1e-38, 1e-6), (1e-25, 1e-25, 1e-6)]
+         (1e20, 1e-38, 1e-6), (1e-25, 1e-25, 1e-6),
+         (1e-33, 1.0, 1e-6), (1e-36, 1.0, 1e-9), (1e-42, 1e3, 1e-12), (1e-24, 1e-24, 1e-14)]
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
