@@ -560,8 +560,8 @@ def adjust_logits(logits, history=None, hist_len=None, penalties=None, bias=None
 
 # ------------------------------------------- projections in 8-bit integers
 
-# The checks, outputs and launches of these are in csrc/calls.cpp: on a Grace core a call of one row takes 4.4 us there and 13
-# from Python.
+# The checks, outputs and launches of these are in csrc/calls.cpp: on a Grace core a call of one row takes 4.6 us there, 2.1
+# with outputs given, and 13 from Python.
 
 _q8 = None
 

@@ -1,6 +1,6 @@
 // The 8-bit operators' calls from Python on torch tensors: checks, outputs, launch.  The calls themselves are those of
 // include/s2frame.h; this is what a Python function would do around them, in C++, because these calls are short: on a Grace
-// core quantize_q8 of one row takes 4.4 us here, 13 through Python and ctypes, where each of its two outputs alone is 2.3.
+// core quantize_q8 of one row takes 4.6 us here, 2.1 where its outputs are given (13 through Python and ctypes).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

@@ -2,7 +2,7 @@
 //
 // Each may be scheduled before the kernel in front of it on its stream has ended (programmatic stream serialisation) and waits
 // for that on the device, before it reads or writes anything but its own shared memory: a run of these short kernels does
-// not pay a launch's latency each time (7 rows of 6144 x 2560 7.7 -> 6.8 us, one row's norm 2.8 -> 2.3).  What the kernel in
+// not pay a launch's latency each time (7 rows of 6144 x 2560 7.7 -> 6.8 us, one row's norm 2.8 -> 2.4).  What the kernel in
 // front may have written is not read through the read-only path: it was not constant while this kernel ran.
 #pragma once
 

@@ -842,10 +842,12 @@ struct Plan {
   int blocks, ranks;
   double time;
 };
-// A block has 5.5 to 7.5 us of launch, filling and draining, and a time a step; blocks at work together are a round.  A join
-// costs by its columns.  Measured (each 1 to 2 us less since launches are ahead of the kernel in front), us, at (rows) for one column tile of 64 and 128 and a pair's 256, weights not in L2:
-// 19456 x 2560 (64) 16.2, 18.7, 22.3; (128) 27.1, 19.1, 22.5; (256) 48.8, 32.1, 23.2; (1024) -, 112, 70; 6144 x 2560 (64) 12.0,
-// 15.3, 20.9; (256) 25.7, 17.7, 21.1; (512) -, 30.8, 21.4; 2560 x 9728 (64) 13.2, 16.0, 55.6; (512) -, 47.5, 56.0.
+// A block has 5.5 to 7.5 us of launch, filling and draining, and a time a step; blocks at work together are a round (152 SMs, 76 pairs).
+// A join costs by its columns.  Measured, us, at (rows) for one column tile of 64 and 128 and a pair's 256, weights not in L2:
+// 19456 x 2560 (64) 14.8, 17.4, 21.7; (128) 25.3, 17.9, 21.8; (256) 45.7, 30.5, 22.5; (1024) -, 108, 69; 6144 x 2560 (64) 10.9,
+// 14.4, 20.0; (128) 13.6, 17.8, 20.0; (256) 23.8, 16.8, 20.3; (512) -, 29.6, 21.2; 2560 x 9728 (64) 11.6, 15.0, 54.6; (128) 16.9, 16.4,
+// 54.7; (512) -, 45.9, 55.0; (2048) -, 129, 107.  The constants were fitted before launches came to begin ahead of the kernel
+// in front: times are off by up to 5 us, or a seventh, but the fastest is the shortest at each of these.
 template <typename T, int N, bool kPair>
 Plan plan_tc(const Q8Args& a) {
   using M = Tc<N, kPair>;
@@ -874,8 +876,8 @@ int launch_tc(const Q8Args& a, const Plan& plan, cudaStream_t st) {
 
 template <typename T>
 int launch_matmul(const Q8Args& a, cudaStream_t st) {
-  // mma.sync up to 16 rows, and up to 64 of a matrix of less than 4 Mi weights (1024 x 1024 6.2 us against 7.2 and 7.9 at 32 and
-  // 64 rows; 2560 x 4096 10.3 against 9.2 at 32).
+  // mma.sync up to 16 rows, and up to 64 of a matrix of less than 4 Mi weights (1024 x 1024 5.7 us against 6.1 at 32 rows,
+  // 5.8 against 6.7 at 64; 2560 x 4096 9.8 against 7.9 at 32).
   if (a.n <= 16) return a.n <= 8 ? launch_few<T, 1>(a, st) : launch_few<T, 2>(a, st);
   if (a.n <= 64 && static_cast<long long>(a.m) * a.k < 4ll << 20) return launch_few<T, 4>(a, st);
   if (!allow_smem<k_q8_tc<T, 64, false>, Tc<64, false>::kBytes>() || !allow_smem<k_q8_tc<T, 128, false>, Tc<128, false>::kBytes>() ||

@@ -484,8 +484,8 @@ int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* log
  *   nearest whole number, ties (within 2^-42) to even: -127..127
  * and stands for scale * code (the scale is no more than the largest number that is finite 127 times).  Codes
  * are those of the exact quotients (of a norm and a gate, of v to 2^-44 or so; where a norm's step is 2^-126, of v as
- * fp32 has it), scales of norms and gates are good to
- * a few roundings of fp32 (norms of rows past some 2^16 columns: to those of a sum of so many squares).  A row that holds
+ * fp32 has it), whatever of v is made of leaves fp32's range on the way; scales of norms and gates are good to a few
+ * roundings of fp32 (norms of rows past some 2^16 columns: to those of a sum of so many squares).  A row that holds
  * something not finite, or whose values or norm come to that in fp32, gets scale NaN and codes 0, so that products with
  * it are NaN.
  *   codes   device int8 [rows][pitch], 16-byte aligned; pitch = cols rounded up to 16, the columns behind
@@ -513,7 +513,7 @@ int s2_rms_norm_q8(const void* x, int dtype, long long x_stride, const void* res
                    struct CUstream_st* stream);
 
 /* v[i] = silu(x[i]) * x[cols + i], silu(g) = g / (1 + exp(-g)): x [rows][2 * cols] of dtype, gate | up.  An exp(-|g|) below
- * 2^-126 (|g| past 87.3) counts as 0. */
+ * 2^-126 (|g| past 87.3, as large as dtype has it) counts as 0. */
 int s2_swiglu_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes, float* scales,
                  struct CUstream_st* stream);
 
