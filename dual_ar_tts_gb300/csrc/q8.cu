@@ -514,8 +514,8 @@ constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it rounds to a whole
 
 // One pass over memory: a row's threads hold its values while they agree on the largest (and a norm's sum of squares), and then
 // encode them.  A thread holds kHeld times eight elements; what lies past them is made again for its codes.
-// Rows of fp32 run near the copy's rate.  Those of 16 bits are bound by latency that nothing hides: a row's loads, meetings and codes
-// do not overlap with another's in its block, and 40 to 48 % of the warps that an SM holds are there.  (Profiled: 16 warp
+// Quantised and normed rows of fp32 run near the copy's rate.  Others are bound by latency that nothing hides: a row's loads, meetings and
+// codes do not overlap with another's in its block, and 40 to 49 % of the warps that an SM holds are there.  (Profiled: 16 warp
 // instructions for 32 values of the quantiser, 39 of a norm with a residual, 33 of the gate, that is 20, 15 and 17 us of issue slots, of
 // which 60 to 70 % are taken; 22, 16 and 15 us of bytes; no pipe is full.)  Measured, operands not in L2 (GB300, copies run at
 // 6.7 TB/s): quantising 19456 x 2560 bf16 33.4 us (4.5 TB/s), 9728 x 2560 fp32 19.6 (6.4); norm with a residual of 5916 x 2560 bf16 24.2

@@ -492,7 +492,8 @@ int s2_adjust_logits(int rows, int n, int sem_begin, int im_end, const void* log
  *           cols are written as zeros
  *   scales  device fp32 [rows]
  * Inputs are rows of neighbouring elements, a stride (in elements, no less than their width) apart, aligned to
- * their element size; rows that start on 16 bytes are read faster.  rows at most 2^31 - 1, cols 2^24. */
+ * their element size; rows that start on 16 bytes are read faster.  No output may overlap an input or another output, but
+ * for total as said below.  rows at most 2^31 - 1, cols 2^24. */
 
 /* v = x [rows][cols] of dtype: weights once, activations at each step. */
 int s2_quantize_q8(const void* x, int dtype, long long x_stride, long long rows, int cols, int8_t* codes, float* scales,
