@@ -201,3 +201,29 @@ def test_norm_halves_at_the_ends(weight, power, cols):
     rms = x.square().mean().sqrt().item()
     want = float(torch.tensor(weight)) / rms
     assert abs(scales.item() / max(want, 2.0 ** -126) - 1) <= ((32 + 12) / 2 + 7) * eb.STEP
+
+
+@pytest.mark.parametrize("which", ["x", "residual"])
+@pytest.mark.parametrize("cols", [300, 2560, 17000])
+def test_norm_rows_out_of_range_in_place(cols, which):
+    """Rows past the range, whose sum lies over an operand, beside ordinary ones, whose bits are those of any other batch."""
+    import dual_ar_tts_gb300 as pkg
+    scale = torch.tensor([1.0, 1e30, 1e-36, 1.0, 0.0, 1e36, 1e-40, 1.0], dtype=torch.float64)[:, None]
+    x, res = [(_rand((8, cols), s) * scale).float().cuda() for s in (20, 21)]
+    w = torch.exp(0.3 * _rand(cols, 22)).float().cuda()
+    for eps in (0.0, 1e-6):
+        want = pkg.rms_norm_q8(x, w, eps, residual=res)
+        v, r, total = eb.norm(x.cpu(), w.cpu(), eps, res.cpu())
+        live = (total != 0).any(1) if eps == 0.0 else torch.ones(8, dtype=torch.bool)
+        codes, step, distance = eb.coded(v[live], r[live])
+        usual = step > 2.0 ** -126
+        eb.check_codes(want[0].cpu()[live][usual], codes[usual], distance[usual], SURE)
+        assert torch.equal(torch.isnan(want[1]).cpu(), ~live) and torch.equal(want[2].cpu(), total)
+        a, b = x.clone(), res.clone()
+        got = pkg.rms_norm_q8(a, w, eps, residual=b, total=a if which == "x" else b)
+        for p, q in zip(got, want):
+            assert torch.equal(p.nan_to_num(7.0) if p.is_floating_point() else p, q.nan_to_num(7.0) if q.is_floating_point() else q)
+        rest = torch.tensor([0, 3, 7], device="cuda")
+        alone = pkg.rms_norm_q8(x[rest], w, eps, residual=res[rest])
+        for p, q in zip(alone, want):
+            assert torch.equal(p, q[rest])
